@@ -70,7 +70,9 @@ int nvfp4_version(void);
  *   bit 1 (2)  reset_sample called with a state built for a smaller window;
  *   bit 2 (4)  a GEMV CTA's wait for another CTA's partial sum.  After this
  *              error the GEMV workspace may hold a partial sum published after
- *              the wait gave up: zero the workspace again before its next use.
+ *              the wait gave up: zero the workspace again before its next use;
+ *   bit 3 (8)  a KV cache kernel met a slot or a page outside the cache, or a
+ *              length or row range outside its table, and skipped it.
  * Synchronous (it copies a few bytes from the device); not for use inside
  * stream capture.
  */
@@ -370,6 +372,187 @@ nvfp4_status nvfp4_rms_norm_quantize(const float* x, int rows, int K, int ld, fl
 
 /* FP32 -> BF16 (RNE) elementwise cast of n values; x, y 16-byte aligned, n a multiple of 8. */
 nvfp4_status nvfp4_f32_to_bf16(const float* x, size_t n, uint16_t* y, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Paged KV cache in NVFP4                                                     */
+/* ------------------------------------------------------------------------ */
+/*
+ * K and V rows of D = head_dim elements (64 or 128) quantized to NVFP4 along D
+ * (one E4M3 scale per 16 elements, one FP32 global scale for all of K and one
+ * for all of V: x = e2m1(code) * e4m3(scale) * global), 9/16 byte an element.
+ * The ReSET pages keep the KV cache in BF16 (reading note §6.1) and describe
+ * no cache kernel; this part has no counterpart there.
+ *
+ * The cache is num_pages pages of page_size tokens (a multiple of 16).  Slot
+ * s is token s % page_size of page s / page_size.  Memory: page, then kv
+ * head, then groups of 16 tokens of 18 D bytes each:
+ *   K codes  [pos][D/2 bytes]           pos = 8 (t/2 % 2) + 2 (t/4) + t % 2 for token t of the group
+ *   K scales [r 8][c 4][i 2][D/64]      pos = 8 i + r, block of 16 elements = c D/64 + last index
+ *   V codes  D = 128: [4][i 2][2][c 4][t0 2][8 bytes]  t = 4 c + 2 i + t0, elements 16 r .. 16 r + 15
+ *                                       with r = 2 (first index) + (third index)
+ *            D = 64:  [r 8][t 16][4 bytes]             elements 8 r .. 8 r + 7
+ *   V scales [block][t]
+ * of 8 D, D, 8 D and D bytes.  The even element of a pair sits in the low
+ * nibble.  The order is that of the attention kernel's matrix fragments: each
+ * of its threads finds what it multiplies in a few 16-byte pieces.
+ */
+typedef struct nvfp4_kv_cache {
+  uint8_t* pages;         /* device, num_pages * nvfp4_kv_page_bytes bytes, 16-byte aligned */
+  const float* k_global;  /* device, one float > 0                                         */
+  const float* v_global;  /* device, one float > 0                                         */
+  int num_pages;          /* >= 1; num_pages * page_size < 2^31                            */
+  int page_size;          /* a multiple of 16, 16 .. 1024                                  */
+  int kv_heads;           /* 1 .. 1024                                                     */
+  int head_dim;           /* 64 or 128                                                     */
+} nvfp4_kv_cache;
+
+/* Element types of the rows that the functions below read. */
+enum { NVFP4_DTYPE_F32 = 0, NVFP4_DTYPE_BF16 = 1 };
+
+/* Bytes of one page (all kv heads), or 0 for an invalid shape. */
+size_t nvfp4_kv_page_bytes(int page_size, int kv_heads, int head_dim);
+
+/*
+ * Gives the pages of ended requests back to the stack of free pages: for each
+ * request b with ended[b] != 0, in order, its first ceil(lens[b] / page_size)
+ * table entries are pushed, and free_count_out = free_count + their number.
+ * The table is left as it is: the caller sets the request's length to 0.
+ *   lens         device, [batch] int32, tokens held (negative counts as 0)
+ *   ended        device, [batch] uint8
+ *   batch        >= 0;  page_size a multiple of 16, 16 .. 1024
+ *   block_table  device, [batch, table_width] int32 page ids
+ *   free_pages   device, [free_capacity] int32, entries [0, free_count) are free pages (written behind them);
+ *                pages beyond free_capacity are dropped
+ *   free_count, free_count_out   device, one int32 each; may be the same address
+ */
+nvfp4_status nvfp4_kv_release(const int32_t* lens, const uint8_t* ended, int batch, int page_size,
+                              const int32_t* block_table, int table_width, int32_t* free_pages, int free_capacity,
+                              const int32_t* free_count, int32_t* free_count_out, cudaStream_t stream);
+
+/*
+ * Page table and slot map of a step from the requests' lengths.  Request b
+ * holds ctx_lens[b] tokens and gets new_lens[b] more; the new tokens of all
+ * requests are packed one request after the other.  With pages(n) =
+ * ceil(n / page_size), it needs pages(ctx + new) - pages(ctx) new pages, taken
+ * from the top of the free stack in request order, and
+ *   block_table[b, pages(ctx) ..]  the new pages (other entries are kept);
+ *   slots[i]      slot of new token i = block_table[b, pos / page_size] * page_size + pos % page_size;
+ *   positions[i]  pos, its place in its request (ctx[b] for the first new token);
+ *   cu_q[b]       first new token of request b; cu_q[batch] = their number;
+ *   kv_lens[b]    ctx + new;
+ *   free_count_out  pages left on the stack.
+ * A request is refused when it needs pages and the needs of the requests up
+ * to and including it exceed free_count, when pages(ctx + new) > table_width
+ * or when a length is negative: it takes no page, its tokens' slots are -1 and
+ * its kv_lens is its ctx (0 if negative).  A request that is invalid by its
+ * lengths or its table counts as needing nothing; a negative new length counts
+ * as no token.  Entries of slots and positions past the last token are -1 and 0.
+ *   batch >= 1; max_tokens >= 0: entries of slots and positions; tokens beyond are not written
+ *   info  device, two int32: requests refused, tokens planned (cu_q[batch])
+ *   free_count, free_count_out may be the same address; all other outputs are distinct
+ */
+nvfp4_status nvfp4_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int batch, int page_size,
+                           int32_t* block_table, int table_width, const int32_t* free_pages, int free_capacity,
+                           const int32_t* free_count, int32_t* free_count_out, int32_t* kv_lens, int32_t* cu_q,
+                           int32_t* slots, int32_t* positions, int max_tokens, int32_t* info, cudaStream_t stream);
+
+/*
+ * Quantizes K and V rows into the cache: row i, head h at k + i * k_token_stride
+ * + h * k_head_stride (strides in elements, the D elements of a row adjacent)
+ * goes to slot slots[i] by the recipe of nvfp4_quantize_act with the cache's
+ * global scales: s = E4M3(max|x_block| / (6 * global)), code = E2M1(x /
+ * (e4m3(s) * global)).  FP32 rows are first rounded to BF16 (RNE).
+ * A slot of -1 skips its row (padding); a slot outside the cache skips it and
+ * records device error bit 3.  Two rows of one call with the same slot give
+ * either row's bytes (per 16 elements).
+ *   k, v     device, 16-byte aligned, strides multiples of 16 bytes
+ *   dtype    NVFP4_DTYPE_*;  tokens >= 0
+ */
+nvfp4_status nvfp4_kv_append(const void* k, const void* v, int dtype, int tokens, int64_t k_token_stride,
+                             int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                             const int32_t* slots, const nvfp4_kv_cache* cache, cudaStream_t stream);
+
+/*
+ * Reads rows back: k_out, v_out [tokens, kv_heads, head_dim] BF16 (16-byte
+ * aligned) receive BF16(e2m1(code) * (e4m3(scale) * global)) of the slots'
+ * rows, products in FP32; a slot of -1 gives zeros, one outside the cache gives zeros and
+ * records device error bit 3.
+ */
+nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int32_t* slots, int tokens, uint16_t* k_out,
+                           uint16_t* v_out, cudaStream_t stream);
+
+/*
+ * Attention of the packed query rows over the cache, causal from the bottom
+ * right: query row i of request b (rows cu_q[b] .. cu_q[b+1]) stands at
+ * position p = kv_lens[b] - (cu_q[b+1] - cu_q[b]) + i and sees the keys
+ * j <= p, with window > 0 only those with j > p - window.  Query head h reads
+ * kv head h / (heads / kv_heads):
+ *   out[r, h, :] = sum_j softmax_j(scale * q[r, h] . K[j]) V[j]      (BF16)
+ *   lse[r, h]    = log sum_j exp(scale * q[r, h] . K[j])             (FP32, natural log)
+ * A row that sees no key gives out = 0, lse = -inf.  The keys' dequantized
+ * values are exact; scores, their maxima and sums and the accumulators are FP32;
+ * FP32 queries are first rounded to BF16 (RNE).
+ *   q            device, [tokens, heads, head_dim] at q + r * q_token_stride + h * q_head_stride
+ *                (elements; 16-byte aligned, strides multiples of 16 bytes)
+ *   heads        a multiple of kv_heads, at most 64 times it
+ *   block_table  device, [batch, table_width] int32: page of tokens j * page_size ..
+ *                Only entries of pages that some row sees are read; a page outside the cache is
+ *                skipped (its keys count as unseen) and records device error bit 3, and so does a
+ *                kv_lens beyond table_width * page_size (cut there) or a row range outside [0, tokens).
+ *   kv_lens      device, [batch] int32
+ *   cu_q         device, [batch + 1] int32, or NULL: one row a request (tokens == batch)
+ *   max_q        >= 1: most rows of a request, as far as the caller knows (it chooses the kernel,
+ *                not the result)
+ *   out          device, [tokens, heads, head_dim] BF16, 16-byte aligned (written; rows of no request are left)
+ *   lse          device, [tokens, heads] FP32, or NULL
+ *   workspace    device scratch of nvfp4_kv_attention_workspace_bytes bytes, 256-byte aligned,
+ *                ZEROED ONCE before its first use; every call leaves it ready for the next one of any
+ *                shape that fits.  Calls that overlap on the GPU need different workspaces.
+ */
+size_t nvfp4_kv_attention_workspace_bytes(int batch, int tokens, int heads, int kv_heads, int head_dim);
+
+nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens, int64_t q_token_stride, int64_t q_head_stride,
+                                int heads, const nvfp4_kv_cache* cache, const int32_t* block_table, int table_width,
+                                const int32_t* kv_lens, const int32_t* cu_q, int batch, int max_q, float scale,
+                                int window, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rules on the logits                                                        */
+/* ------------------------------------------------------------------------ */
+/*
+ * Penalties, biases and grammar masks on logits, in front of the sampler (the
+ * ReSET pages run their sampler as a logits processor inside a serving engine,
+ * reading note §4.3; these rules are the engine's).  For row r, token v, in
+ * this order, each step FP32 with IEEE rounding:
+ *   x = logits[r, v]
+ *   if v stands in the row's tokens:       x = x > 0 ? x / repetition[r] : x * repetition[r]
+ *   c = its count behind the prompt:       x = x - frequency[r] * c;  if c > 0: x = x - presence[r]
+ *   if v stands in the row's bias list:    x = x + its value
+ *   if the row's grammar forbids v:        x = fill
+ * -inf and NaN logits pass through the arithmetic as they are.
+ *   logits    device, [rows, V] of dtype NVFP4_DTYPE_*, row r at logits + r * ld (elements)
+ *   rows      >= 0;  V 1 .. 2^24;  ld >= V
+ *   tokens    device, [rows, history] int32: prompt then output of each row; ids outside [0, V) count nothing.
+ *             NULL with history 0: no penalties
+ *   n_tokens  device, [rows] int32: how many of them are there (cut to [0, history])
+ *   n_prompt  device, [rows] int32: how many of those are the prompt, or NULL: none
+ *   repetition, presence, frequency   device, [rows] FP32, each may be NULL (1, 0, 0)
+ *   bias_ids, bias_values   device, [rows, n_bias] int32 / FP32 (NULL with n_bias 0); an id outside [0, V) is
+ *             an unused entry; of equal ids in a row the last one holds
+ *   mask      device, bit v % 32 of word v / 32 set: v is allowed; [mask_count, ceil(V/32)] uint32, or NULL
+ *   mask_rows device, [rows] int32: the mask row of each row, -1 (or any outside [0, mask_count)): none;
+ *             NULL: row r has mask row r (mask_count >= rows)
+ *   fill      what forbidden logits become, e.g. -inf (a row whose mask allows nothing is all fill)
+ *   out       device, [rows, V] FP32, 16-byte aligned when V % 4 == 0 is to be fast (written); for FP32 logits with
+ *             ld == V it may be the logits themselves
+ */
+nvfp4_status nvfp4_process_logits(const void* logits, int dtype, int rows, int V, int64_t ld, const int32_t* tokens,
+                                  int history, const int32_t* n_tokens, const int32_t* n_prompt,
+                                  const float* repetition, const float* presence, const float* frequency,
+                                  const int32_t* bias_ids, const float* bias_values, int n_bias, const uint32_t* mask,
+                                  int mask_count, const int32_t* mask_rows, float fill, float* out,
+                                  cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* ReSET sampler                                                              */

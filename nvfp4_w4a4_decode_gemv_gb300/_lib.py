@@ -21,6 +21,8 @@ STATUS = {
 _c_p = ctypes.c_void_p
 _c_i = ctypes.c_int
 _c_sz = ctypes.c_size_t
+_c_i64 = ctypes.c_int64
+_c_f = ctypes.c_float
 
 
 # reset_params.threshold values (RESET_THRESHOLD_* in nvfp4.h)
@@ -31,6 +33,17 @@ class ResetParams(ctypes.Structure):
     """reset_params; fields left out default to 0 (ReSET threshold, no top-p)."""
     _fields_ = [("tau0", ctypes.c_float), ("t_low", ctypes.c_float), ("t_high", ctypes.c_float), ("w", ctypes.c_int),
                 ("threshold", ctypes.c_int), ("top_p", ctypes.c_float)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    """nvfp4_kv_cache."""
+    _fields_ = [("pages", ctypes.c_void_p), ("k_global", ctypes.c_void_p), ("v_global", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int)]
+
+
+# NVFP4_DTYPE_* of nvfp4.h
+DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
 # name -> (restype, argtypes); mirrors include/nvfp4.h
@@ -61,6 +74,17 @@ SIGNATURES = {
     "nvfp4_rms_norm_bf16": (_c_i, [_c_p, _c_i, _c_i, _c_i, ctypes.c_float, _c_p, _c_p]),
     "nvfp4_rms_norm_quantize": (_c_i, [_c_p, _c_i, _c_i, _c_i, ctypes.c_float, _c_p, _c_p, _c_p, _c_p, _c_p]),
     "nvfp4_f32_to_bf16": (_c_i, [_c_p, _c_sz, _c_p, _c_p]),
+    "nvfp4_kv_page_bytes": (_c_sz, [_c_i, _c_i, _c_i]),
+    "nvfp4_kv_release": (_c_i, [_c_p, _c_p, _c_i, _c_i, _c_p, _c_i, _c_p, _c_i, _c_p, _c_p, _c_p]),
+    "nvfp4_kv_plan": (_c_i, [_c_p, _c_p, _c_i, _c_i, _c_p, _c_i, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i,
+                             _c_p, _c_p]),
+    "nvfp4_kv_append": (_c_i, [_c_p, _c_p, _c_i, _c_i, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p]),
+    "nvfp4_kv_read": (_c_i, [_c_p, _c_p, _c_i, _c_p, _c_p, _c_p]),
+    "nvfp4_kv_attention_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i, _c_i]),
+    "nvfp4_kv_attention": (_c_i, [_c_p, _c_i, _c_i, _c_i64, _c_i64, _c_i, _c_p, _c_p, _c_i, _c_p, _c_p, _c_i, _c_i,
+                                  _c_f, _c_i, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "nvfp4_process_logits": (_c_i, [_c_p, _c_i, _c_i, _c_i, _c_i64, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
+                                    _c_p, _c_i, _c_p, _c_i, _c_p, _c_f, _c_p, _c_p]),
     "reset_state_bytes": (_c_sz, [_c_i, _c_i]),
     "reset_state_init": (_c_i, [_c_p, _c_i, _c_i, _c_p]),
     "reset_workspace_bytes": (_c_sz, [_c_i, _c_i]),

@@ -8,7 +8,8 @@ import weakref
 
 import torch
 
-from ._lib import THRESHOLD_FIXED, THRESHOLD_RESET, THRESHOLD_WINDOW, ResetParams, check, lib, ptr, stream_handle
+from ._lib import (DTYPES, THRESHOLD_FIXED, THRESHOLD_RESET, THRESHOLD_WINDOW, KVCacheDesc, ResetParams, check, lib,
+                   ptr, stream_handle)
 
 __all__ = [
     "nvfp4_quantize_act", "nvfp4_quantize_f32", "nvfp4_silu_mul_quantize", "nvfp4_gemv_smallm",
@@ -20,6 +21,9 @@ __all__ = [
     "reset_state_bytes",
     "reset_state_init", "reset_workspace_bytes", "reset_sample", "reset_sample_noalloc", "device_status", "GemvWorkspace",
     "NVFP4Tensor", "ResetSampler",
+    "NVFP4KVCache", "KVPlan", "nvfp4_kv_page_bytes", "nvfp4_kv_release", "nvfp4_kv_plan", "nvfp4_kv_append",
+    "nvfp4_kv_read", "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_bytes", "nvfp4_process_logits",
+    "DEVERR_KV_RANGE",
 ]
 
 
@@ -325,6 +329,251 @@ def nvfp4_f32_to_bf16(x: torch.Tensor, y: torch.Tensor | None = None, stream=Non
     y = y if y is not None else torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
     check(lib().nvfp4_f32_to_bf16(ptr(x), x.numel(), ptr(y), stream_handle(stream)), "nvfp4_f32_to_bf16")
     return y
+
+
+# Device error bit of a KV cache kernel that met a slot, page, length or row range outside its cache or
+# tables and skipped it (nvfp4_device_status).
+DEVERR_KV_RANGE = 8
+
+
+def _need(t, dtype, name, dim=None):
+    """A contiguous CUDA tensor of one type (and rank), or ValueError."""
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or (dim is not None and t.dim() != dim):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}" + (f" with {dim} dimensions" if dim else ""))
+
+
+def nvfp4_kv_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().nvfp4_kv_page_bytes(page_size, kv_heads, head_dim))
+
+
+class NVFP4KVCache:
+    """A paged KV cache in NVFP4: pages uint8 [num_pages, kv_heads, page_size / 16, 18 * head_dim] (layout:
+    nvfp4_kv_cache in nvfp4.h) and one FP32 global scale [1] each for K and V, all on the device."""
+
+    def __init__(self, pages: torch.Tensor, k_global: torch.Tensor, v_global: torch.Tensor):
+        _need(pages, torch.uint8, "pages", 4)
+        _need(k_global, torch.float32, "k_global")
+        _need(v_global, torch.float32, "v_global")
+        self.pages, self.k_global, self.v_global = pages, k_global, v_global
+        self.num_pages, self.kv_heads, groups, group_bytes = pages.shape
+        self.page_size, self.head_dim = 16 * groups, group_bytes // 18
+        if (k_global.numel() != 1 or v_global.numel() != 1 or group_bytes != 18 * self.head_dim
+                or nvfp4_kv_page_bytes(self.page_size, self.kv_heads, self.head_dim) == 0):
+            raise ValueError(f"unsupported cache shape {tuple(pages.shape)}")
+        self.desc = KVCacheDesc(pages.data_ptr(), k_global.data_ptr(), v_global.data_ptr(), self.num_pages,
+                                self.page_size, self.kv_heads, self.head_dim)
+        self.desc_ptr = ctypes.addressof(self.desc)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, k_global: float = 1.0,
+              v_global: float = 1.0, device="cuda"):
+        if nvfp4_kv_page_bytes(page_size, kv_heads, head_dim) == 0:
+            raise ValueError(f"unsupported cache shape: page_size {page_size}, kv_heads {kv_heads}, head_dim {head_dim}")
+        return cls(torch.empty((num_pages, kv_heads, page_size // 16, 18 * head_dim), dtype=torch.uint8, device=device),
+                   torch.tensor([k_global], dtype=torch.float32, device=device),
+                   torch.tensor([v_global], dtype=torch.float32, device=device))
+
+
+class KVPlan:
+    """Outputs of nvfp4_kv_plan, int32 on the device: slots and positions [max_tokens] of the packed new tokens,
+    cu_q [batch + 1], kv_lens [batch], free_count [1] (pages left), info [2] (requests refused, tokens planned)."""
+
+    __slots__ = ("slots", "positions", "cu_q", "kv_lens", "free_count", "info")
+
+    def __init__(self, slots, positions, cu_q, kv_lens, free_count, info):
+        self.slots, self.positions, self.cu_q = slots, positions, cu_q
+        self.kv_lens, self.free_count, self.info = kv_lens, free_count, info
+
+    @classmethod
+    def empty(cls, batch: int, max_tokens: int, device="cuda", free_count: torch.Tensor | None = None):
+        i32 = lambda n: torch.empty(n, dtype=torch.int32, device=device)
+        return cls(i32(max_tokens), i32(max_tokens), i32(batch + 1), i32(batch),
+                   i32(1) if free_count is None else free_count, i32(2))
+
+
+def nvfp4_kv_release(lens: torch.Tensor, ended: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                     free_count: torch.Tensor, page_size: int, free_count_out: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Pushes the pages of the requests with ended[b] != 0 (lens[b] tokens each) onto the free stack; returns the
+    new count (in place unless free_count_out is given)."""
+    for t, n, d in ((lens, "lens", 1), (block_table, "block_table", 2), (free_pages, "free_pages", 1),
+                    (free_count, "free_count", 1)):
+        _need(t, torch.int32, n, d)
+    _need(ended, torch.uint8, "ended", 1)
+    out = free_count if free_count_out is None else free_count_out
+    _need(out, torch.int32, "free_count_out", 1)
+    batch, width = block_table.shape
+    if lens.numel() != batch or ended.numel() != batch or free_count.numel() != 1 or out.numel() != 1:
+        raise ValueError("lens and ended need one entry a row of block_table, the counts one entry")
+    check(lib().nvfp4_kv_release(ptr(lens), ptr(ended), batch, page_size, ptr(block_table), width, ptr(free_pages),
+                                 free_pages.numel(), ptr(free_count), ptr(out), stream_handle(stream)),
+          "nvfp4_kv_release")
+    return out
+
+
+def nvfp4_kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                  free_count: torch.Tensor, page_size: int, max_tokens: int | None = None,
+                  out: KVPlan | None = None, stream=None) -> KVPlan:
+    """Takes pages for new_lens[b] tokens behind ctx_lens[b] (block_table updated in place) and maps every new token
+    to its slot.  Without `out`, the outputs are new tensors for max_tokens tokens and free_count is updated in
+    place; out.free_count may be free_count."""
+    for t, n, d in ((ctx_lens, "ctx_lens", 1), (new_lens, "new_lens", 1), (block_table, "block_table", 2),
+                    (free_pages, "free_pages", 1), (free_count, "free_count", 1)):
+        _need(t, torch.int32, n, d)
+    batch, width = block_table.shape
+    if out is None:
+        if max_tokens is None:
+            raise ValueError("max_tokens is needed to allocate the outputs")
+        out = KVPlan.empty(batch, max_tokens, ctx_lens.device, free_count)
+    for n in KVPlan.__slots__:
+        _need(getattr(out, n), torch.int32, n, 1)
+    if (ctx_lens.numel() != batch or new_lens.numel() != batch or out.kv_lens.numel() != batch
+            or out.cu_q.numel() != batch + 1 or out.positions.numel() != out.slots.numel()
+            or free_count.numel() != 1 or out.free_count.numel() != 1 or out.info.numel() != 2):
+        raise ValueError("the lengths and outputs do not fit a batch of the block_table's rows")
+    check(lib().nvfp4_kv_plan(ptr(ctx_lens), ptr(new_lens), batch, page_size, ptr(block_table), width, ptr(free_pages),
+                              free_pages.numel(), ptr(free_count), ptr(out.free_count), ptr(out.kv_lens), ptr(out.cu_q),
+                              ptr(out.slots), ptr(out.positions), out.slots.numel(), ptr(out.info),
+                              stream_handle(stream)), "nvfp4_kv_plan")
+    return out
+
+
+def _need_rows(t, name, heads, dim):
+    """CUDA rows [tokens, heads, dim] with adjacent elements in a row: their NVFP4_DTYPE_* code."""
+    code = DTYPES.get(t.dtype)
+    if code is None or not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.stride(2) != 1:
+        raise ValueError(f"{name} must be a CUDA tensor [tokens, {heads}, {dim}] of float32 or bfloat16 with adjacent "
+                         "elements")
+    return code
+
+
+def nvfp4_kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: NVFP4KVCache, stream=None) -> None:
+    """Quantizes rows k, v [tokens, kv_heads, head_dim] (any token and head strides) into the cache's slots (-1: skip)."""
+    code = _need_rows(k, "k", cache.kv_heads, cache.head_dim)
+    if _need_rows(v, "v", cache.kv_heads, cache.head_dim) != code or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have the same type and number of tokens")
+    _need(slots, torch.int32, "slots", 1)
+    tokens = k.shape[0]
+    if slots.numel() != tokens:
+        raise ValueError("slots needs one entry a token")
+    ks, vs = k.stride(), v.stride()
+    check(lib().nvfp4_kv_append(ptr(k), ptr(v), code, tokens, ks[0], ks[1], vs[0], vs[1], ptr(slots), cache.desc_ptr,
+                                stream_handle(stream)), "nvfp4_kv_append")
+
+
+def nvfp4_kv_read(cache: NVFP4KVCache, slots: torch.Tensor, k_out: torch.Tensor | None = None,
+                  v_out: torch.Tensor | None = None, stream=None):
+    """The cached rows of the slots as BF16 [tokens, kv_heads, head_dim] (k, v); zeros where a slot is -1."""
+    _need(slots, torch.int32, "slots", 1)
+    shape = (slots.numel(), cache.kv_heads, cache.head_dim)
+    k_out = k_out if k_out is not None else torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    v_out = v_out if v_out is not None else torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        _need(t, torch.bfloat16, n)
+        if t.shape != shape:
+            raise ValueError(f"{n} must have shape {shape}")
+    check(lib().nvfp4_kv_read(cache.desc_ptr, ptr(slots), shape[0], ptr(k_out), ptr(v_out), stream_handle(stream)),
+          "nvfp4_kv_read")
+    return k_out, v_out
+
+
+def nvfp4_kv_attention_workspace_bytes(batch: int, tokens: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().nvfp4_kv_attention_workspace_bytes(batch, tokens, heads, kv_heads, head_dim))
+
+
+_attention_ws: dict = {}
+
+
+def nvfp4_kv_attention(q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                       cu_q: torch.Tensor | None = None, max_q: int | None = None, scale: float | None = None,
+                       window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """softmax(scale q K^T) V of packed query rows q [tokens, heads, head_dim] over the cache, causal from the
+    bottom right (BF16).  kv_lens [batch]: keys of each request, its new tokens among them; cu_q [batch + 1]: first
+    row of each request, None: one row each; max_q: most rows of a request; scale: 1 / sqrt(head_dim) by default;
+    window: a row sees its last `window` keys only (0: all); lse [tokens, heads] FP32 receives log sum exp."""
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    tokens, heads = q.shape[0], q.shape[1]
+    code = _need_rows(q, "q", heads, cache.head_dim)
+    _need(block_table, torch.int32, "block_table", 2)
+    _need(kv_lens, torch.int32, "kv_lens", 1)
+    batch, width = block_table.shape
+    if kv_lens.numel() != batch:
+        raise ValueError("kv_lens needs one entry a row of block_table")
+    if cu_q is not None:
+        _need(cu_q, torch.int32, "cu_q", 1)
+        if cu_q.numel() != batch + 1:
+            raise ValueError("cu_q needs batch + 1 entries")
+    shape = (tokens, heads, cache.head_dim)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    else:
+        _need(out, torch.bfloat16, "out")
+        if out.shape != shape:
+            raise ValueError(f"out must have shape {shape}")
+    if lse is not None:
+        _need(lse, torch.float32, "lse", 2)
+        if lse.shape != shape[:2]:
+            raise ValueError(f"lse must have shape {shape[:2]}")
+    if workspace is None:
+        need = nvfp4_kv_attention_workspace_bytes(batch, tokens, heads, cache.kv_heads, cache.head_dim)
+        workspace = _attention_ws.get(q.device)
+        if workspace is None or workspace.numel() < need:
+            workspace = _attention_ws[q.device] = torch.zeros(need, dtype=torch.uint8, device=q.device)
+    qs = q.stride()
+    check(lib().nvfp4_kv_attention(ptr(q), code, tokens, qs[0], qs[1], heads, cache.desc_ptr, ptr(block_table), width,
+                                   ptr(kv_lens), ptr(cu_q), batch,
+                                   max_q if max_q is not None else 1 if cu_q is None else max(1, tokens),
+                                   scale if scale is not None else cache.head_dim ** -0.5, window, ptr(out), ptr(lse),
+                                   ptr(workspace), workspace.numel(), stream_handle(stream)), "nvfp4_kv_attention")
+    return out
+
+
+def nvfp4_process_logits(logits: torch.Tensor, tokens: torch.Tensor | None = None, n_tokens: torch.Tensor | None = None,
+                         n_prompt: torch.Tensor | None = None, repetition: torch.Tensor | None = None,
+                         presence: torch.Tensor | None = None, frequency: torch.Tensor | None = None,
+                         bias_ids: torch.Tensor | None = None, bias_values: torch.Tensor | None = None,
+                         mask: torch.Tensor | None = None, mask_rows: torch.Tensor | None = None,
+                         fill: float = float("-inf"), out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Penalties, biases and grammar masks on logits [rows, V] (float32 or bfloat16, adjacent elements in a row);
+    FP32 result.  tokens [rows, history] int32 with n_tokens, n_prompt [rows] int32; repetition, presence, frequency
+    [rows] float32; bias_ids [rows, n] int32 (-1: unused) with bias_values float32; mask [masks, ceil(V / 32)] int32,
+    bit v % 32 of word v / 32 set where token v is allowed, mask_rows [rows] int32 (-1: no mask)."""
+    code = DTYPES.get(logits.dtype)
+    if code is None or not logits.is_cuda or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a CUDA tensor [rows, V] of float32 or bfloat16 with adjacent elements")
+    rows, V = logits.shape
+    for t, n, dt, d in ((tokens, "tokens", torch.int32, 2), (n_tokens, "n_tokens", torch.int32, 1),
+                        (n_prompt, "n_prompt", torch.int32, 1), (repetition, "repetition", torch.float32, 1),
+                        (presence, "presence", torch.float32, 1), (frequency, "frequency", torch.float32, 1),
+                        (bias_ids, "bias_ids", torch.int32, 2), (bias_values, "bias_values", torch.float32, 2),
+                        (mask_rows, "mask_rows", torch.int32, 1)):
+        if t is not None:
+            _need(t, dt, n, d)
+            if t.shape[0] != rows:
+                raise ValueError(f"{n} needs one entry a row of logits")
+    if (tokens is None) != (n_tokens is None) or (bias_ids is None) != (bias_values is None):
+        raise ValueError("tokens and n_tokens, bias_ids and bias_values go together")
+    if bias_ids is not None and bias_ids.shape != bias_values.shape:
+        raise ValueError("bias_ids and bias_values must have the same shape")
+    if mask is not None:
+        _need(mask, torch.int32, "mask", 2)
+        if mask.shape[1] != (V + 31) // 32 or (mask_rows is None and mask.shape[0] < rows):
+            raise ValueError("mask needs ceil(V / 32) words a row, and a row for each row of logits without mask_rows")
+    if out is None:
+        out = torch.empty((rows, V), dtype=torch.float32, device=logits.device)
+    else:
+        _need(out, torch.float32, "out", 2)
+        if out.shape != logits.shape:
+            raise ValueError("out must have the shape of logits")
+    check(lib().nvfp4_process_logits(
+        ptr(logits), code, rows, V, logits.stride(0) if rows > 1 else V, ptr(tokens),
+        tokens.shape[1] if tokens is not None else 0, ptr(n_tokens), ptr(n_prompt), ptr(repetition), ptr(presence),
+        ptr(frequency), ptr(bias_ids), ptr(bias_values), bias_ids.shape[1] if bias_ids is not None else 0, ptr(mask),
+        mask.shape[0] if mask is not None else 0, ptr(mask_rows), fill, ptr(out), stream_handle(stream)),
+        "nvfp4_process_logits")
+    return out
 
 
 def reset_state_bytes(M: int, w: int) -> int:

@@ -64,6 +64,7 @@ enum : unsigned int {
   NVFP4_DEVERR_MBAR_TIMEOUT = 1,   // an mbarrier wait exceeded its iteration limit
   NVFP4_DEVERR_STATE_W = 2,        // reset_sample called with a window larger than the state's
   NVFP4_DEVERR_FLAG_TIMEOUT = 4,   // a wait for another CTA's partial sum exceeded its iteration limit
+  NVFP4_DEVERR_KV_RANGE = 8,       // a slot, page, length or row range outside a KV cache or its tables
 };
 
 // Relaxed GPU-scope word store / load: single-copy atomic, no ordering.
