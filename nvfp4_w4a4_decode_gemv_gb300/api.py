@@ -517,10 +517,15 @@ def nvfp4_kv_attention(q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.
         if lse.shape != shape[:2]:
             raise ValueError(f"lse must have shape {shape[:2]}")
     if workspace is None:
+        key = (q.device, stream_handle(stream))          # calls on different streams may overlap
+        workspace = _attention_ws.get(key)
         need = nvfp4_kv_attention_workspace_bytes(batch, tokens, heads, cache.kv_heads, cache.head_dim)
-        workspace = _attention_ws.get(q.device)
         if workspace is None or workspace.numel() < need:
-            workspace = _attention_ws[q.device] = torch.zeros(need, dtype=torch.uint8, device=q.device)
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("nvfp4_kv_attention: pass a workspace to a call that is captured first")
+            workspace = _attention_ws[key] = torch.zeros(need, dtype=torch.uint8, device=q.device)
+            if stream is not None:                       # zeroed on the current stream
+                stream.wait_stream(torch.cuda.current_stream())
     qs = q.stride()
     check(lib().nvfp4_kv_attention(ptr(q), code, tokens, qs[0], qs[1], heads, cache.desc_ptr, ptr(block_table), width,
                                    ptr(kv_lens), ptr(cu_q), batch,

@@ -1,14 +1,48 @@
-// Attention over the NVFP4 KV cache:
-//   out[r, h] = sum_j p_j V[j] / sum_j p_j,  p_j = exp(scale * q[r, h] . K[j] - m),  m the running maximum,
-// over the keys j that row r sees (causal from the bottom right, optionally a
-// window), in one pass with the running maximum and sum.
+// Attention over the NVFP4 KV cache, for few query rows a request (decode,
+// drafted tokens):
+//   out[r, h] = sum_j p_j V[j] / sum_j p_j,  p_j = 2^(f q[r, h] . K[j] - m),  m a running maximum,
+// over the keys j that row r sees, f = scale * log2 e, in one pass over the cache.
+//
+// Bound by HBM: 18 D / 16 bytes a token and kv head, each read once for all the
+// query heads (and rows) that share it.  What could stop it from getting there
+// is the instruction rate: a token of one kv head (D = 128) is 256 elements, and
+// at the copy rate an SM has about 6 cycles (24 issue slots) for it.  So:
+//  - the matrix instructions (mma.m16n8k16, FP16 in, FP32 out) have the tokens or
+//    the elements of V on their 16-row side and the query rows on the 8-column
+//    side: no half-empty tiles at 8 query heads a kv head;
+//  - a code and its scale multiply exactly in FP16 (2 + 4 significant bits, 2^-10
+//    .. 2688), so dequantization is one conversion and one multiply for two
+//    elements; V's two tokens of an operand register are put together on the 4-bit
+//    codes (half an instruction an operand) instead of on the FP16 values;
+//  - the cache's own layout is that of the operands, so a lane's loads are whole
+//    16-byte pieces without bank conflicts.
+// Queries enter as FP16 of q / 2^e, 2^e the power of two at the row's maximum:
+// exact for BF16 queries down to 2^-14 of it.  Weights are rounded to FP16 for
+// the product with V (2^-11 of each); their sum is FP32.
+//
+// Work split: units of kUnitTokens tokens of one (request, kv head, row tile),
+// Stream-K over all of them, so that any mix of lengths fills the GPU; the split
+// is made on the GPU from the lengths (a captured call follows them).  A CTA of
+// four warps takes a contiguous range; its warps take every fourth unit of a
+// segment, each with its own ring of bulk copies (no CTA barrier while it
+// streams) and its own running maximum, and are merged in shared memory at the
+// segment's end.  Segments that several CTAs share go through records in the
+// workspace; the last CTA to arrive merges them in CTA order (the same bits
+// every time) and resets the counter.  Nothing waits for another CTA.
 #include <math.h>
 
 #include "kv_layout.cuh"
+#include "tcgen05.cuh"
 
 NVFP4_DEFINE_ERROR_READER(nvfp4_internal_read_error_kv_attention)
 
 namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxCtas = 640;
+constexpr int kMaxSplits = 64;          // CTAs that share a segment: more cost more to merge than they read faster
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnArgs {
   const void* q;
@@ -18,89 +52,665 @@ struct AttnArgs {
   const int32_t *table, *kv_lens, *cu_q;
   uint16_t* out;
   float* lse;
+  unsigned int* counters;               // [kMaxCtas], zero between calls
+  float* records;                       // [2 kMaxCtas][rows][D + 2]
   int tokens, heads, kv_heads, group, page_size, num_pages, width, batch, window;
   float scale;
 };
 
-NVFP4_DEVINL float e2m1_to_f32(uint32_t c) {
-  return __uint_as_float(__float_as_uint(__fmul_rn(__uint_as_float((c & 7u) << 22), 0x1p126f)) | ((c & 8u) << 28));
+// ---- instructions ------------------------------------------------------------
+NVFP4_DEVINL float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+
+// Four code bytes (two E2M1 codes each) -> four FP16 pairs.
+NVFP4_DEVINL void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// Two E4M3 scale bytes -> an FP16 pair.
+NVFP4_DEVINL uint32_t e4m3x2_to_f16(uint32_t s) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)s));
+  return h;
+}
+
+NVFP4_DEVINL uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+NVFP4_DEVINL uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+NVFP4_DEVINL uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+NVFP4_DEVINL void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+NVFP4_DEVINL uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+NVFP4_DEVINL uint2 lds64(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
 
 NVFP4_DEVINL float load_q(const float* p) { return __bfloat162float(__float2bfloat16_rn(*p)); }
 NVFP4_DEVINL float load_q(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 
-// One warp per (row, head); a lane holds D / 32 elements.
-template <int D, class T>
-__global__ void __launch_bounds__(128) kv_attention_kernel(const AttnArgs a) {
-  using L = KvLayout<D>;
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (item >= (long long)a.tokens * a.heads) return;
-  const int row = (int)(item / a.heads), h = (int)(item % a.heads), kvh = h / a.group;
-  int b = row, first = row, last = row + 1;
+// ---- shapes --------------------------------------------------------------------
+template <int D, int NT>
+struct Shape {
+  static constexpr int kRows = 8 * NT;                     // query rows of a tile
+  static constexpr int kUnitGroups = 256 / D;              // 32 tokens at D = 128, 64 at D = 64: 4608 bytes
+  static constexpr int kUnitTokens = kKvGroup * kUnitGroups;
+  static constexpr int kUnitBytes = kUnitGroups * KvLayout<D>::kGroupBytes;
+  static constexpr int kStages = 3;
+  static constexpr int kMergeStride = D + 4;               // floats a row in the merge buffer (bank spread)
+  static constexpr int kRecord = kRows * (D + 2);          // floats of a record: O, then M, then L
+  // shared memory
+  static constexpr int kOffRing = 0;
+  static constexpr int kOffQ = kWarps * kStages * kUnitBytes;             // FP16 query operands
+  static constexpr int kOffMerge = kOffQ + kRows * D * 2;                 // [kWarps][8][kMergeStride] floats
+  static constexpr int kOffML = kOffMerge + kWarps * 8 * kMergeStride * 4;  // [kWarps][kRows] maxima, then sums
+  static constexpr int kOffF = kOffML + 2 * kWarps * kRows * 4;           // [kRows] score factors
+  static constexpr int kOffBar = kOffF + kRows * 4;                       // [kWarps][kStages] barriers
+  static constexpr int kOffValid = kOffBar + kWarps * kStages * 8;        // [kWarps][kStages] groups present
+  static constexpr int kOffScan = kOffValid + kWarps * kStages * 4;       // 32 words for the split
+  static constexpr int kSmem = (kOffScan + 32 * 8 + 15) / 16 * 16;
+};
+
+// ---- requests --------------------------------------------------------------------
+struct Request {
+  int first, rows, len;                 // query rows [first, first + rows), keys [0, len)
+  int begin;                            // first key that any row sees
+};
+
+NVFP4_DEVINL Request get_request(const AttnArgs& a, int b, bool report) {
+  Request r;
+  r.first = b;
+  r.rows = 1;
+  bool bad = false;
   if (a.cu_q) {
-    int lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.cu_q[mid] <= row) lo = mid; else hi = mid;
-    }
-    b = lo;
-    first = a.cu_q[b];
-    last = a.cu_q[b + 1];
-    if (row < first || row >= last) return;       // a row of no request
+    r.first = a.cu_q[b];
+    const int last = a.cu_q[b + 1];
+    bad = r.first < 0 || last < r.first || last > a.tokens;
+    r.rows = bad ? 0 : last - r.first;
   }
-  int len = max(a.kv_lens[b], 0);
-  if (len > (long long)a.width * a.page_size) {
-    len = a.width * a.page_size;
-    atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
+  r.len = max(a.kv_lens[b], 0);
+  const long long most = (long long)a.width * a.page_size;
+  if (r.len > most) {
+    r.len = (int)most;
+    bad = true;
   }
-  const int p = len - (last - first) + (row - first);
-  const int j_end = min(p + 1, len);
-  const int j_begin = a.window > 0 ? max(p - a.window + 1, 0) : 0;
-  const int blk = lane / (32 / L::kBlocks), e0 = (lane % (32 / L::kBlocks)) * E;   // first element in its block
-  float q[E], o[E];
-  const float qs = a.scale * *a.k_global;
+  if (bad && report) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
+  r.begin = a.window > 0 ? (int)max((long long)r.len - r.rows - a.window + 1, 0ll) : 0;
+  return r;
+}
+
+// Units of a segment (one row tile of one kv head); at least one, so that rows without keys are written too.
+template <class S>
+NVFP4_DEVINL int segment_units(const Request& r) {
+  const int n = (r.len + S::kUnitTokens - 1) / S::kUnitTokens - r.begin / S::kUnitTokens;
+  return n > 0 ? n : 1;
+}
+template <class S>
+NVFP4_DEVINL int request_tiles(const AttnArgs& a, const Request& r) {
+  return (int)(((long long)r.rows * a.group + S::kRows - 1) / S::kRows);
+}
+template <class S>
+NVFP4_DEVINL long long request_units(const AttnArgs& a, const Request& r) {
+  return (long long)segment_units<S>(r) * request_tiles<S>(a, r) * a.kv_heads;
+}
+
+// ---- one unit of keys ---------------------------------------------------------------
+// Scores, weights and output of one 16-token group.  `masked`: rows see part of it only.
+template <int D, int NT>
+struct WarpState {
+  float o[D / 16][NT][4];               // [row tile][column tile]: elements (2i, 2i + 1 of the lane's) x rows 2c, 2c + 1
+  float m[NT][2], l[NT][2];             // running maximum (log2 units), the lane's part of the sum
+};
+
+template <int D, int NT>
+NVFP4_DEVINL void scores(const uint8_t* g, int lane, const uint32_t (*qreg)[2], const uint8_t* sq, float (&s)[NT][4]) {
+  using L = KvLayout<D>;
+  constexpr int W = D / 32;             // code words of the lane's D/4 elements of a row
+  uint32_t raw[2][W];
+  const int r = lane >> 2, c = lane & 3;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = load_q(static_cast<const T*>(a.q) + row * a.q_ts + h * a.q_hs + blk * 16 + e0 + i) * qs;
-    o[i] = 0.0f;
+  for (int i = 0; i < 2; ++i) {
+    const uint8_t* p = g + (8 * i + r) * (D / 2) + c * (D / 8);
+    if constexpr (D == 128) {
+      const uint4 v = lds128(p);
+      raw[i][0] = v.x, raw[i][1] = v.y, raw[i][2] = v.z, raw[i][3] = v.w;
+    } else {
+      const uint2 v = lds64(p);
+      raw[i][0] = v.x, raw[i][1] = v.y;
+    }
   }
-  float m = -INFINITY, l = 0.0f;
-  for (int j = j_begin; j < j_end; ++j) {
-    const int page = a.table[(size_t)b * a.width + j / a.page_size];
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
+  uint32_t sc[2][D / 64];               // FP16 pairs of the lane's block scales
+  if constexpr (D == 128) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(g + L::kOffKScale + lane * 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t h = e4m3x2_to_f16(w >> (16 * i));
+      sc[i][0] = __byte_perm(h, h, 0x1010);
+      sc[i][1] = __byte_perm(h, h, 0x3232);
+    }
+  } else {
+    const uint32_t h = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(g + L::kOffKScale + lane * 2));
+    sc[0][0] = __byte_perm(h, h, 0x1010);
+    sc[1][0] = __byte_perm(h, h, 0x3232);
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[t][i] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {         // a word: 8 elements, two contraction steps
+    uint32_t h[2][4];
+    e2m1x8_to_f16(raw[0][w], h[0]);
+    e2m1x8_to_f16(raw[1][w], h[1]);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t a[4] = {hmul2(h[0][2 * u], sc[0][w / 2]), hmul2(h[1][2 * u], sc[1][w / 2]),
+                             hmul2(h[0][2 * u + 1], sc[0][w / 2]), hmul2(h[1][2 * u + 1], sc[1][w / 2])};
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if constexpr (NT <= 2) {
+          mma16816(s[t], a, qreg[t * (D / 16) + 2 * w + u][0], qreg[t * (D / 16) + 2 * w + u][1]);
+        } else {
+          const uint2 b = lds64(sq + ((t * (D / 16) + 2 * w + u) * 32 + lane) * 8);
+          mma16816(s[t], a, b.x, b.y);
+        }
+      }
+    }
+  }
+}
+
+// O += V^T P for one group; p[t]: FP16 weights as B operands; live: how many of the lane's four tokens exist.
+template <int D, int NT>
+NVFP4_DEVINL void weigh(const uint8_t* g, int lane, const uint32_t (&p)[NT][2], int live, WarpState<D, NT>& st) {
+  using L = KvLayout<D>;
+  const int r = lane >> 2, c = lane & 3;
+  uint32_t sw = *reinterpret_cast<const uint32_t*>(g + L::kOffVScale + (D == 128 ? r : r >> 1) * 16 + 4 * c);
+  if (live < 4) sw &= live > 0 ? (1u << (8 * live)) - 1u : 0u;      // what lies behind the last key may be NaN
+  const uint32_t s01 = e4m3x2_to_f16(sw), s23 = e4m3x2_to_f16(sw >> 16);
+  constexpr int W = D / 64;             // code words of a token: the lane's D/8 elements
+  uint32_t x[4][W];                     // [token]
+  if constexpr (D == 128) {
+    const uint8_t* q = g + L::kOffV + (r >> 1) * 256 + (r & 1) * 64 + c * 16;
+    const uint4 v0 = lds128(q), v1 = lds128(q + 128);
+    x[0][0] = v0.x, x[0][1] = v0.y, x[1][0] = v0.z, x[1][1] = v0.w;
+    x[2][0] = v1.x, x[2][1] = v1.y, x[3][0] = v1.z, x[3][1] = v1.w;
+  } else {
+    const uint4 v = lds128(g + L::kOffV + r * 64 + c * 16);
+    x[0][0] = v.x, x[1][0] = v.y, x[2][0] = v.z, x[3][0] = v.w;
+  }
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    // even and odd elements of two tokens side by side in a byte
+    uint32_t h[4][4];
+    constexpr uint32_t kLo = 0x0F0F0F0Fu;
+    e2m1x8_to_f16((x[0][w] & kLo) | ((x[1][w] << 4) & ~kLo), h[0]);
+    e2m1x8_to_f16(((x[0][w] >> 4) & kLo) | (x[1][w] & ~kLo), h[1]);
+    e2m1x8_to_f16((x[2][w] & kLo) | ((x[3][w] << 4) & ~kLo), h[2]);
+    e2m1x8_to_f16(((x[2][w] >> 4) & kLo) | (x[3][w] & ~kLo), h[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a[4] = {hmul2(h[0][i], s01), hmul2(h[1][i], s01), hmul2(h[2][i], s23), hmul2(h[3][i], s23)};
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mma16816(st.o[4 * w + i][t], a, p[t][0], p[t][1]);
+    }
+  }
+}
+
+// ---- the kernel -----------------------------------------------------------------------
+template <int D, int NT, class T>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_attention_kernel(const AttnArgs a) {
+  using S = Shape<D, NT>;
+  using L = KvLayout<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar) + warp * S::kStages;
+  volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + S::kOffValid) + warp * S::kStages;
+  uint8_t* ring = smem + S::kOffRing + warp * S::kStages * S::kUnitBytes;
+  float* s_f = reinterpret_cast<float*>(smem + S::kOffF);
+  float* s_m = reinterpret_cast<float*>(smem + S::kOffML);
+  float* s_l = s_m + kWarps * S::kRows;
+  float* s_merge = reinterpret_cast<float*>(smem + S::kOffMerge);
+  if (lane == 0)
+    for (int i = 0; i < S::kStages; ++i) mbar_init(&bars[i], 1);
+  fence_mbar_init();
+  griddep_launch_dependents();
+  griddep_wait();
+
+  // ---- the split: all units, this CTA's range, the request it starts in
+  long long* s_scan = reinterpret_cast<long long*>(smem + S::kOffScan);
+  const int b0 = (int)((long long)a.batch * tid / kThreads), b1 = (int)((long long)a.batch * (tid + 1) / kThreads);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += request_units<S>(a, get_request(a, b, blockIdx.x == 0));
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) s_scan[warp] = inc;
+  __syncthreads();
+  long long U = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_scan[w];
+    U += s_scan[w];
+  }
+  if (U == 0) return;
+  const long long excl = before + inc - mine;
+  // few units: fewer CTAs, one unit a warp; and no more of them than a merge is worth (an estimate: segments are
+  // at least batch * kv_heads when every request has rows)
+  const long long most = (long long)kMaxSplits * a.batch * a.kv_heads;
+  long long G = (U + kWarps - 1) / kWarps;
+  if (G > most) G = most;
+  if (G > gridDim.x) G = gridDim.x;
+  const long long cta = blockIdx.x;
+  if (cta >= G) return;
+  long long u = unit_start(cta, U, G);
+  const long long u_end = unit_start(cta + 1, U, G);
+  if (mine > 0 && excl <= u && u < excl + mine) {
+    long long at = excl;
+    for (int b = b0; b < b1; ++b) {
+      const long long n = request_units<S>(a, get_request(a, b, false));
+      if (u < at + n) {
+        s_scan[8] = b;
+        s_scan[9] = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  int b = (int)s_scan[8];
+  long long base = s_scan[9];
+
+  const float kg = *a.k_global, vg = *a.v_global;
+  uint32_t uses = 0;                                    // copies this warp has waited for: slot and parity
+  bool gave_up = false;
+  while (u < u_end) {
+    const Request rq = get_request(a, b, false);
+    const long long n_req = request_units<S>(a, rq);
+    if (u >= base + n_req) {
+      base += n_req;
+      ++b;
       continue;
     }
-    const uint8_t* g = a.pages + kv_group_offset<D>(page * a.page_size + j % a.page_size, kvh, a.page_size, a.kv_heads);
-    const int t = j % kKvGroup;
-    const float ks = e4m3_to_f32(g[L::k_scale(t, blk)]), vs = e4m3_to_f32(g[L::v_scale(t, blk)]);
-    float s = 0.0f;
+    const int n_seg = segment_units<S>(rq), tiles = request_tiles<S>(a, rq);
+    const long long seg = (u - base) / n_seg;
+    const long long seg0 = base + seg * n_seg;
+    const int s0 = (int)(u - seg0), s1 = (int)min((long long)n_seg, u_end - seg0);
+    const int tile = (int)(seg % tiles), kvh = (int)(seg / tiles);
+    const int row0 = tile * S::kRows;                   // row = query row * group + query head of the kv head
+    const int n_rows = min(S::kRows, rq.rows * a.group - row0);
+    // positions of the tile's first and last row: every row sees [lo_all, hi_all], some row [lo_any, hi_any]
+    const int hi_all = rq.len - rq.rows + row0 / a.group;
+    const int hi_any = rq.len - rq.rows + (row0 + n_rows - 1) / a.group;
+    const int lo_any = a.window > 0 ? max(hi_all - a.window + 1, 0) : 0;
+    const int lo_all = a.window > 0 ? max(hi_any - a.window + 1, 0) : 0;
+
+    // ---- queries: FP16 of q / 2^e in operand order, and the factors of the scores
+    for (int row = warp; row < S::kRows; row += kWarps) {
+      constexpr int E = D / 32;
+      float v[E];
+      float big = 0.0f;
+      if (row < n_rows) {
+        const int rr = row0 + row, tok = rq.first + rr / a.group, h = kvh * a.group + rr % a.group;
+        const T* q = static_cast<const T*>(a.q) + tok * a.q_ts + h * a.q_hs + lane * E;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int e = e0 + i;
-      const uint32_t byte = g[L::k_codes(t, blk) + e / 2];
-      s = fmaf(q[i], e2m1_to_f32(byte >> (4 * (e & 1))) * ks, s);
+        for (int i = 0; i < E; ++i) {
+          v[i] = load_q(q + i);
+          big = fmaxf(big, fabsf(v[i]));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = 0.0f;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      int e = (int)(__float_as_uint(big) >> 23) - 127;
+      e = big > 0.0f ? min(max(e, -126), 126) : 0;
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+      uint8_t* sq = smem + S::kOffQ;
+      if constexpr (D == 128) {
+        const int cq = lane >> 3, j = lane & 7;
+        *reinterpret_cast<uint2*>(sq + (((row >> 3) * 8 + j) * 32 + (row & 7) * 4 + cq) * 8) =
+            make_uint2(pack_f16(v[0] * down, v[1] * down), pack_f16(v[2] * down, v[3] * down));
+      } else {
+        const int cq = lane >> 3, j = (lane & 7) >> 1;
+        *reinterpret_cast<uint32_t*>(sq + (((row >> 3) * 4 + j) * 32 + (row & 7) * 4 + cq) * 8 + (lane & 1) * 4) =
+            pack_f16(v[0] * down, v[1] * down);
+      }
+      // never 0: a hidden score, -inf, times it has to stay -inf
+      if (lane == 0) s_f[row] = fmaxf(a.scale * kLog2e * kg * up, 1.2e-38f);
     }
+    __syncthreads();
+
+    // ---- this warp's units
+    WarpState<D, NT> st;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const float mn = fmaxf(m, s);
-    const float f = expf(m - mn), w = expf(s - mn);
-    m = mn;
-    l = fmaf(l, f, w);
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int e = e0 + i;
-      const uint32_t byte = g[L::v_codes(t, blk, e / 8) + e % 8 / 2];
-      o[i] = fmaf(o[i], f, w * (e2m1_to_f32(byte >> (4 * (e & 1))) * vs));
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) st.o[i][t][k] = 0.0f;
+      st.m[t][0] = st.m[t][1] = -INFINITY;
+      st.l[t][0] = st.l[t][1] = 0.0f;
     }
+    uint32_t qreg[NT <= 2 ? NT * (D / 16) : 1][2];
+    if constexpr (NT <= 2) {
+#pragma unroll
+      for (int i = 0; i < NT * (D / 16); ++i) {
+        const uint2 v = lds64(smem + S::kOffQ + (i * 32 + lane) * 8);
+        qreg[i][0] = v.x, qreg[i][1] = v.y;
+      }
+    }
+    float f[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      f[t][0] = s_f[t * 8 + (lane & 3) * 2];
+      f[t][1] = s_f[t * 8 + (lane & 3) * 2 + 1];
+    }
+    const int unit0 = rq.begin / S::kUnitTokens;        // the segment's first unit
+    const int u_lo = max(s0, lo_any / S::kUnitTokens - unit0);
+    const int u_hi = hi_any < 0 ? u_lo : min(s1, hi_any / S::kUnitTokens + 1 - unit0);
+    const int my_n = u_lo + warp < u_hi ? (u_hi - u_lo - warp + kWarps - 1) / kWarps : 0;
+    const int32_t* trow = a.table + (size_t)b * a.width;
+    const bool whole = a.page_size % S::kUnitTokens == 0;   // a unit lies in one page
+    // The page of lane's group of unit k (-1: not there, or not to be read); lanes 0 .. kUnitGroups - 1.
+    auto page_of = [&](int k) {
+      const int t0 = (unit0 + u_lo + warp + k * kWarps) * S::kUnitTokens + lane * kKvGroup;
+      if (k >= my_n || lane >= S::kUnitGroups || t0 > hi_any || t0 + kKvGroup <= lo_any) return -1;
+      const int p = trow[t0 / a.page_size];
+      if (p >= 0 && p < a.num_pages) return p;
+      atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
+      return -1;
+    };
+    auto issue = [&](int k, int page, uint32_t slot) {
+      const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+      if (lane == 0) {
+        valid[slot] = have;
+        mbar_arrive_expect_tx(&bars[slot], __popc(have) * L::kGroupBytes);
+      }
+      __syncwarp();
+      uint8_t* dst = ring + slot * S::kUnitBytes;
+      const int t0 = (unit0 + u_lo + warp + k * kWarps) * S::kUnitTokens + lane * kKvGroup;
+      if (whole && have == (1u << S::kUnitGroups) - 1u) {
+        if (lane == 0)
+          bulk_g2s(dst, a.pages + kv_group_offset<D>(page, t0 % a.page_size, kvh, a.page_size, a.kv_heads),
+                   S::kUnitBytes, &bars[slot]);
+      } else if (page >= 0) {
+        bulk_g2s(dst + lane * L::kGroupBytes,
+                 a.pages + kv_group_offset<D>(page, t0 % a.page_size, kvh, a.page_size, a.kv_heads), L::kGroupBytes,
+                 &bars[slot]);
+      }
+    };
+    int next = page_of(0);
+    for (int k = 0; k < S::kStages && k < my_n; ++k) {
+      const int now = next;
+      next = page_of(k + 1);
+      issue(k, now, (uses + k) % S::kStages);
+    }
+    for (int k = 0; k < my_n; ++k) {
+      const uint32_t slot = uses % S::kStages;
+      gave_up = !mbar_wait(&bars[slot], (uses / S::kStages) & 1) || gave_up;
+      ++uses;
+      const uint32_t have = valid[slot];
+      const uint8_t* unit = ring + slot * S::kUnitBytes;
+      const int t_unit = (unit0 + u_lo + warp + k * kWarps) * S::kUnitTokens;
+#pragma unroll 2
+      for (int gi = 0; gi < S::kUnitGroups; ++gi) {
+        if (!((have >> gi) & 1u)) continue;
+        const uint8_t* g = unit + gi * L::kGroupBytes;
+        const int t0 = t_unit + gi * kKvGroup;
+        float s[NT][4];
+        scores<D, NT>(g, lane, qreg, smem + S::kOffQ, s);
+        int live = 4;
+        if (t0 + kKvGroup - 1 > hi_all || t0 < lo_all) {
+          // token of score row pos = r + 8 i: 4 (r / 2) + 2 i + r % 2
+          live = min(max(rq.len - t0 - 4 * (lane & 3), 0), 4);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int tok = t0 + 4 * (lane >> 3) + 2 * (i >> 1) + ((lane >> 2) & 1);
+              const int rr = t * 8 + (lane & 3) * 2 + (i & 1);
+              const int hi = rq.len - rq.rows + (row0 + rr) / a.group;
+              if (tok > hi || (a.window > 0 && tok <= hi - a.window)) s[t][i] = -INFINITY;
+            }
+        }
+        // a larger score than any before moves the maximum and rescales what has been summed
+        bool grew = false;
+        float top[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k2 = 0; k2 < 2; ++k2) {
+            top[t][k2] = fmaxf(s[t][k2], s[t][k2 + 2]) * f[t][k2];
+            grew = grew || top[t][k2] > st.m[t][k2];
+          }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2) {
+              float mx = fmaxf(st.m[t][k2], top[t][k2]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              const float back = mx == -INFINITY ? 1.0f : ex2(st.m[t][k2] - mx);
+              st.m[t][k2] = mx;
+              st.l[t][k2] *= back;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                st.o[i][t][k2] *= back;
+                st.o[i][t][k2 + 2] *= back;
+              }
+            }
+        }
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float ref = st.m[t][i & 1] == -INFINITY ? 0.0f : st.m[t][i & 1];
+            w[i] = ex2(fmaf(s[t][i], f[t][i & 1], -ref));
+            st.l[t][i & 1] += w[i];
+          }
+          p[t][0] = transpose8x8(pack_f16(w[0], w[1]));
+          p[t][1] = transpose8x8(pack_f16(w[2], w[3]));
+        }
+        weigh<D, NT>(g, lane, p, live, st);
+      }
+      __syncwarp();                                     // the slot has been read
+      if (k + S::kStages < my_n && !gave_up) {
+        const int now = next;
+        next = page_of(k + S::kStages + 1);
+        issue(k + S::kStages, now, slot);
+      }
+      if (gave_up) {
+        // wait for the copies still in flight, then leave the units that are not loaded
+        for (int j = 1; j < S::kStages && k + j < my_n; ++j) {
+          mbar_wait(&bars[uses % S::kStages], (uses / S::kStages) & 1);
+          ++uses;
+        }
+        break;
+      }
+    }
+
+    // ---- the four warps together
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int k2 = 0; k2 < 2; ++k2) {
+        float l = st.l[t][k2];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane < 4) {
+          s_m[warp * S::kRows + t * 8 + lane * 2 + k2] = st.m[t][k2];
+          s_l[warp * S::kRows + t * 8 + lane * 2 + k2] = l;
+        }
+      }
+    __syncthreads();
+    const bool all = s0 == 0 && s1 == n_seg;
+    const long long c_first = cta_of_unit(seg0, U, G), c_last = cta_of_unit(seg0 + n_seg - 1, U, G);
+    float* rec = a.records + (size_t)(2 * cta + (cta == c_first ? 1 : 0)) * S::kRecord;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int k2 = 0; k2 < 2; ++k2) {
+        const int row = t * 8 + (lane & 3) * 2 + k2;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w * S::kRows + row]);
+        const float fw = st.m[t][k2] == -INFINITY ? 0.0f : ex2(st.m[t][k2] - mx);
+        float* dst = s_merge + (warp * 8 + (lane & 3) * 2 + k2) * S::kMergeStride + (lane >> 2) * (D / 8);
+#pragma unroll
+        for (int i = 0; i < D / 16; i += 2)
+          *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(st.o[i][t][k2] * fw, st.o[i][t][k2 + 2] * fw,
+                                                                st.o[i + 1][t][k2] * fw, st.o[i + 1][t][k2 + 2] * fw);
+      }
+      __syncthreads();
+      for (int e = tid; e < 8 * D / 4; e += kThreads) {
+        const int row = e / (D / 4), d = e % (D / 4) * 4;
+        if (t * 8 + row >= n_rows) continue;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        float mx = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(s_merge + (w * 8 + row) * S::kMergeStride + d);
+          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+          mx = fmaxf(mx, s_m[w * S::kRows + t * 8 + row]);
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float mw = s_m[w * S::kRows + t * 8 + row];
+          if (mw != -INFINITY) l += s_l[w * S::kRows + t * 8 + row] * ex2(mw - mx);
+        }
+        if (all) {
+          const int rr = row0 + t * 8 + row, tok = rq.first + rr / a.group, h = kvh * a.group + rr % a.group;
+          const float inv = l > 0.0f ? vg / l : 0.0f;
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x * inv, x.y * inv), hi = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+          *reinterpret_cast<uint2*>(a.out + ((size_t)tok * a.heads + h) * D + d) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          if (a.lse && d == 0) a.lse[(size_t)tok * a.heads + h] = l > 0.0f ? (mx + log2f(l)) / kLog2e : -INFINITY;
+        } else {
+          __stcg(reinterpret_cast<float4*>(rec + (t * 8 + row) * D + d), x);
+          if (d == 0) {
+            __stcg(rec + S::kRows * D + t * 8 + row, mx);
+            __stcg(rec + S::kRows * (D + 1) + t * 8 + row, l);
+          }
+        }
+      }
+      __syncthreads();
+    }
+
+    // ---- a segment that several CTAs share: the last one to arrive merges the records
+    if (!all) {
+      __threadfence();
+      __syncthreads();
+      unsigned int* flag = reinterpret_cast<unsigned int*>(smem + S::kOffScan + 128);
+      if (tid == 0) *flag = atomicAdd(&a.counters[c_first], 1u);
+      __syncthreads();
+      if (*flag == (unsigned)(c_last - c_first)) {
+        __threadfence();
+        for (int e = tid; e < n_rows * (D / 4); e += kThreads) {
+          const int row = e / (D / 4), d = e % (D / 4) * 4;
+          float mx = -INFINITY;
+          for (long long q = c_first; q <= c_last; ++q) {
+            const float* r = a.records + (size_t)(2 * q + (q == c_first ? 1 : 0)) * S::kRecord;
+            mx = fmaxf(mx, __ldcg(r + S::kRows * D + row));
+          }
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          float l = 0.0f;
+#pragma unroll 4
+          for (long long q = c_first; q <= c_last; ++q) {
+            const float* r = a.records + (size_t)(2 * q + (q == c_first ? 1 : 0)) * S::kRecord;
+            const float m = __ldcg(r + S::kRows * D + row), lq = __ldcg(r + S::kRows * (D + 1) + row);
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(r + row * D + d));
+            const float w = m == -INFINITY ? 0.0f : ex2(m - mx);
+            l = fmaf(lq, w, l);
+            x.x = fmaf(y.x, w, x.x), x.y = fmaf(y.y, w, x.y), x.z = fmaf(y.z, w, x.z), x.w = fmaf(y.w, w, x.w);
+          }
+          const int rr = row0 + row, tok = rq.first + rr / a.group, h = kvh * a.group + rr % a.group;
+          const float inv = l > 0.0f ? vg / l : 0.0f;
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x * inv, x.y * inv), hi = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+          *reinterpret_cast<uint2*>(a.out + ((size_t)tok * a.heads + h) * D + d) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          if (a.lse && d == 0) a.lse[(size_t)tok * a.heads + h] = l > 0.0f ? (mx + log2f(l)) / kLog2e : -INFINITY;
+        }
+        if (tid == 0) a.counters[c_first] = 0u;
+      }
+      __syncthreads();
+    }
+    u = seg0 + s1;
   }
-  const float inv = l > 0.0f ? *a.v_global / l : 0.0f;
-#pragma unroll
-  for (int i = 0; i < E; ++i)
-    a.out[((size_t)row * a.heads + h) * D + blk * 16 + e0 + i] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
-  if (a.lse && lane == 0) a.lse[(size_t)row * a.heads + h] = l > 0.0f ? m + logf(l) : -INFINITY;
+}
+
+constexpr size_t kCounterBytes = (kMaxCtas * 4 + 255) / 256 * 256;
+
+// CTAs of a variant: as many as are resident at once.
+template <int D, int NT, class T>
+cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
+  using S = Shape<D, NT>;
+  static PerDeviceInt grid_cache;
+  cudaError_t err = cudaSuccess;
+  const int grid = grid_cache.get([](int dev, cudaError_t* e_out) -> int {
+    int sms = 0, per = 0;
+    cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kv_attention_kernel<D, NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kv_attention_kernel<D, NT, T>, kThreads, S::kSmem);
+    if (e != cudaSuccess) {
+      *e_out = e;
+      return 0;
+    }
+    const int g = sms * (per > 0 ? per : 1);
+    return g < kMaxCtas ? g : kMaxCtas;
+  }, &err);
+  if (grid == 0) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, NT, T>, a);
+}
+
+template <int D, class T>
+cudaError_t dispatch(const AttnArgs& a, int rows, cudaStream_t stream) {
+  if (rows <= 8) return launch<D, 1, T>(a, stream);
+  if (rows <= 16) return launch<D, 2, T>(a, stream);
+  return launch<D, 4, T>(a, stream);
 }
 
 }  // namespace
@@ -112,7 +722,7 @@ nvfp4_status nvfp4_internal_check_device();
 extern "C" size_t nvfp4_kv_attention_workspace_bytes(int batch, int tokens, int heads, int kv_heads, int head_dim) {
   if (batch < 1 || tokens < 0 || nvfp4_kv_page_bytes(16, kv_heads, head_dim) == 0) return 0;
   if (heads < kv_heads || heads % kv_heads != 0 || heads / kv_heads > 64) return 0;
-  return 256;
+  return kCounterBytes + (size_t)2 * kMaxCtas * Shape<128, 4>::kRecord * sizeof(float);
 }
 
 extern "C" nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens, int64_t q_token_stride,
@@ -127,7 +737,9 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens,
   if (!(scale > 0.0f) || isinf(scale) || window < 0 || max_q < 1) return NVFP4_ERR_RANGE;
   if (tokens < 0 || batch < 0 || table_width < 1 || (!cu_q && tokens != batch)) return NVFP4_ERR_SHAPE;
   if (heads < cache->kv_heads || heads % cache->kv_heads != 0 || heads / cache->kv_heads > 64) return NVFP4_ERR_SHAPE;
-  if ((long long)batch * table_width > 0x7FFFFFFFll) return NVFP4_ERR_SHAPE;
+  if ((long long)batch * table_width > 0x7FFFFFFFll || (long long)tokens * heads > 0x7FFFFFFFll ||
+      (long long)table_width * cache->page_size > 0x7FFFFFFFll)
+    return NVFP4_ERR_SHAPE;
   if (tokens == 0 || batch == 0) return NVFP4_OK;
   if (!q || !block_table || !kv_lens || !out || !workspace) return NVFP4_ERR_NULL;
   const int per = dtype == NVFP4_DTYPE_F32 ? 4 : 8;
@@ -140,16 +752,17 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens,
     return NVFP4_ERR_SHAPE;
   const nvfp4_status ds = nvfp4_internal_check_device();
   if (ds != NVFP4_OK) return ds;
+  const int group = heads / cache->kv_heads;
+  if (window >= table_width * cache->page_size) window = 0;   // no request is longer: nothing to hide
   const AttnArgs a = {q, q_token_stride, q_head_stride, cache->pages, cache->k_global, cache->v_global,
-                      block_table, kv_lens, cu_q, out, lse, tokens, heads, cache->kv_heads,
-                      heads / cache->kv_heads, cache->page_size, cache->num_pages, table_width, batch, window, scale};
-  const unsigned grid = (unsigned)(((long long)tokens * heads + 3) / 4);
-  if (cache->head_dim == 128) {
-    if (dtype == NVFP4_DTYPE_F32) kv_attention_kernel<128, float><<<grid, 128, 0, stream>>>(a);
-    else kv_attention_kernel<128, uint16_t><<<grid, 128, 0, stream>>>(a);
-  } else {
-    if (dtype == NVFP4_DTYPE_F32) kv_attention_kernel<64, float><<<grid, 128, 0, stream>>>(a);
-    else kv_attention_kernel<64, uint16_t><<<grid, 128, 0, stream>>>(a);
-  }
-  return nvfp4_internal_cuda_status(cudaGetLastError());
+                      block_table, kv_lens, cu_q, out, lse, static_cast<unsigned int*>(workspace),
+                      reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes), tokens, heads,
+                      cache->kv_heads, group, cache->page_size, cache->num_pages, table_width, batch, window, scale};
+  const int rows = cu_q ? (int)((long long)max_q * group < 1 << 20 ? max_q * group : 1 << 20) : group;
+  cudaError_t e;
+  if (cache->head_dim == 128)
+    e = dtype == NVFP4_DTYPE_F32 ? dispatch<128, float>(a, rows, stream) : dispatch<128, uint16_t>(a, rows, stream);
+  else
+    e = dtype == NVFP4_DTYPE_F32 ? dispatch<64, float>(a, rows, stream) : dispatch<64, uint16_t>(a, rows, stream);
+  return nvfp4_internal_cuda_status(e);
 }

@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
     load16(static_cast<const T*>(a.x[which]) + token * a.ts[which] + head * a.hs[which] + b * 16, v);
     uint2 codes;
     const uint32_t s = quant_block(v, block_absmax(v), __ldg(a.glob[which]), codes);
-    uint8_t* g = a.pages + kv_group_offset<D>(slot, head, a.page_size, a.heads);
+    uint8_t* g = a.pages + kv_group_offset<D>(slot / a.page_size, slot % a.page_size, head, a.page_size, a.heads);
     const int t = slot % kKvGroup;
     if (which == 0) {
       *reinterpret_cast<uint2*>(g + L::k_codes(t, b)) = codes;
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadArgs a) {
     const int slot = a.slots[token];
     uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
     if (slot >= 0 && slot < a.num_slots) {
-      const uint8_t* g = a.pages + kv_group_offset<D>(slot, head, a.page_size, a.heads);
+      const uint8_t* g = a.pages + kv_group_offset<D>(slot / a.page_size, slot % a.page_size, head, a.page_size, a.heads);
       const int t = slot % kKvGroup;
       uint2 c;
       uint32_t s;

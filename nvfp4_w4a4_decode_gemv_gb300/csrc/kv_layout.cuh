@@ -41,10 +41,9 @@ struct KvLayout {
   static NVFP4_DEVINL int v_scale(int t, int b) { return kOffVScale + b * 16 + t; }
 };
 
-// Byte offset of the group that holds slot `slot` for kv head `head`.
+// Byte offset of the group that holds token `in` of page `page` for kv head `head`.
 template <int D>
-NVFP4_DEVINL size_t kv_group_offset(int slot, int head, int page_size, int kv_heads) {
-  const int page = slot / page_size, in = slot - page * page_size;
+NVFP4_DEVINL size_t kv_group_offset(int page, int in, int head, int page_size, int kv_heads) {
   return (((size_t)page * kv_heads + head) * (page_size / kKvGroup) + in / kKvGroup) * KvLayout<D>::kGroupBytes;
 }
 
