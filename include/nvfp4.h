@@ -505,9 +505,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int32_t* slots, in
  *                not the result)
  *   out          device, [tokens, heads, head_dim] BF16, 16-byte aligned (written; rows of no request are left)
  *   lse          device, [tokens, heads] FP32, or NULL
- *   workspace    device scratch of nvfp4_kv_attention_workspace_bytes bytes, 256-byte aligned,
- *                ZEROED ONCE before its first use; every call leaves it ready for the next one of any
- *                shape that fits.  Calls that overlap on the GPU need different workspaces.
+ *   workspace    device scratch of nvfp4_kv_attention_workspace_bytes bytes, 256-byte aligned, its first
+ *                4096 bytes ZEROED ONCE before its first use; every call leaves it ready for the next one of
+ *                any shape that fits.  Calls that overlap on the GPU need different workspaces.
  */
 size_t nvfp4_kv_attention_workspace_bytes(int batch, int tokens, int heads, int kv_heads, int head_dim);
 

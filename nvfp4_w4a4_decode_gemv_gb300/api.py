@@ -334,6 +334,8 @@ def nvfp4_f32_to_bf16(x: torch.Tensor, y: torch.Tensor | None = None, stream=Non
 # Device error bit of a KV cache kernel that met a slot, page, length or row range outside its cache or
 # tables and skipped it (nvfp4_device_status).
 DEVERR_KV_RANGE = 8
+# Bytes at the start of an nvfp4_kv_attention workspace that are zeroed before its first use.
+ATTENTION_WS_ZEROED = 4096
 
 
 def _need(t, dtype, name, dim=None):
@@ -484,6 +486,25 @@ def nvfp4_kv_attention_workspace_bytes(batch: int, tokens: int, heads: int, kv_h
 _attention_ws: dict = {}
 
 
+def _new_attention_workspace(need: int, device) -> torch.Tensor:
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    ws[:ATTENTION_WS_ZEROED].zero_()
+    return ws
+
+
+def _attention_workspace(need: int, device, stream) -> torch.Tensor:
+    """A workspace of the stream's own (calls on different streams may overlap).  A captured call gets one of its
+    graph's memory, cleared by each replay."""
+    if torch.cuda.is_current_stream_capturing():
+        return _new_attention_workspace(need, device)
+    key = (device, stream_handle(stream))
+    ws = _attention_ws.get(key)
+    if ws is None or ws.numel() < need:
+        with torch.cuda.stream(stream):                  # None: the current stream
+            ws = _attention_ws[key] = _new_attention_workspace(need, device)
+    return ws
+
+
 def nvfp4_kv_attention(q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
                        cu_q: torch.Tensor | None = None, max_q: int | None = None, scale: float | None = None,
                        window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
@@ -517,15 +538,8 @@ def nvfp4_kv_attention(q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.
         if lse.shape != shape[:2]:
             raise ValueError(f"lse must have shape {shape[:2]}")
     if workspace is None:
-        key = (q.device, stream_handle(stream))          # calls on different streams may overlap
-        workspace = _attention_ws.get(key)
-        need = nvfp4_kv_attention_workspace_bytes(batch, tokens, heads, cache.kv_heads, cache.head_dim)
-        if workspace is None or workspace.numel() < need:
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("nvfp4_kv_attention: pass a workspace to a call that is captured first")
-            workspace = _attention_ws[key] = torch.zeros(need, dtype=torch.uint8, device=q.device)
-            if stream is not None:                       # zeroed on the current stream
-                stream.wait_stream(torch.cuda.current_stream())
+        workspace = _attention_workspace(
+            nvfp4_kv_attention_workspace_bytes(batch, tokens, heads, cache.kv_heads, cache.head_dim), q.device, stream)
     qs = q.stride()
     check(lib().nvfp4_kv_attention(ptr(q), code, tokens, qs[0], qs[1], heads, cache.desc_ptr, ptr(block_table), width,
                                    ptr(kv_lens), ptr(cu_q), batch,

@@ -41,7 +41,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 640;
-constexpr int kMaxSplits = 64;          // CTAs that share a segment: more cost more to merge than they read faster
+constexpr int kMaxSplits = 32;          // pieces of a segment when there are few: more cost more to merge than they save
+constexpr int kMaxShares = 64;          // the same bound where there are many
+constexpr int kSegmentCost = 12;        // units that the fixed cost of a segment (queries, first copies, merge) stands for
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnArgs {
@@ -174,10 +176,13 @@ template <class S>
 NVFP4_DEVINL int request_tiles(const AttnArgs& a, const Request& r) {
   return (int)(((long long)r.rows * a.group + S::kRows - 1) / S::kRows);
 }
-template <class S>
-NVFP4_DEVINL long long request_units(const AttnArgs& a, const Request& r) {
-  return (long long)segment_units<S>(r) * request_tiles<S>(a, r) * a.kv_heads;
-}
+
+// How the segments are laid end to end for the split: each stands for `head` units of overhead, its own units,
+// and padding to a multiple of `align`.
+struct Split {
+  int head, align;
+  NVFP4_DEVINL int length(int n) const { return head + (n + align - 1) / align * align; }
+};
 
 // ---- one unit of keys ---------------------------------------------------------------
 // Scores, weights and output of one 16-token group.  `masked`: rows see part of it only.
@@ -301,68 +306,102 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_at
   griddep_launch_dependents();
   griddep_wait();
 
-  // ---- the split: all units, this CTA's range, the request it starts in
+  // ---- the split: this CTA's range and the request it starts in
   long long* s_scan = reinterpret_cast<long long*>(smem + S::kOffScan);
   const int b0 = (int)((long long)a.batch * tid / kThreads), b1 = (int)((long long)a.batch * (tid + 1) / kThreads);
+  long long units4 = 0;                                 // units, each segment's padded to one for every warp
+  long long n_segs = 0;
+  int longest = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = get_request(a, b, blockIdx.x == 0);
+    const long long segs = (long long)request_tiles<S>(a, r) * a.kv_heads;
+    const int n = segment_units<S>(r);
+    units4 += segs * ((n + kWarps - 1) / kWarps);
+    n_segs += segs;
+    if (segs > 0) longest = max(longest, n);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    units4 += __shfl_xor_sync(0xffffffffu, units4, o);
+    n_segs += __shfl_xor_sync(0xffffffffu, n_segs, o);
+    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  }
+  if (lane == 0) {
+    s_scan[warp] = units4;
+    s_scan[4 + warp] = longest;
+    s_scan[8 + warp] = n_segs;
+  }
+  __syncthreads();
+  units4 = s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
+  longest = (int)max(max(s_scan[4], s_scan[5]), max(s_scan[6], s_scan[7]));
+  n_segs = s_scan[8] + s_scan[9] + s_scan[10] + s_scan[11];
+  if (units4 == 0) return;
+  // Few units: every CTA a piece of one segment, one unit a warp or as many as keep a segment's pieces under
+  // kMaxSplits.  Many: equal ranges, where a segment's fixed cost counts as kSegmentCost units, and at most
+  // kMaxShares of them a segment.
+  const bool few = units4 <= gridDim.x;
+  const int piece = kWarps * max(1, (longest + kWarps * kMaxSplits - 1) / (kWarps * kMaxSplits));
+  const Split split = few ? Split{0, piece} : Split{kSegmentCost, 1};
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += request_units<S>(a, get_request(a, b, blockIdx.x == 0));
+  for (int b = b0; b < b1; ++b) {
+    const Request r = get_request(a, b, false);
+    mine += (long long)split.length(segment_units<S>(r)) * request_tiles<S>(a, r) * a.kv_heads;
+  }
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
-  if (lane == 31) s_scan[warp] = inc;
+  if (lane == 31) s_scan[12 + warp] = inc;
   __syncthreads();
   long long U = 0, before = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_scan[w];
-    U += s_scan[w];
+    if (w < warp) before += s_scan[12 + w];
+    U += s_scan[12 + w];
   }
-  if (U == 0) return;
   const long long excl = before + inc - mine;
-  // few units: fewer CTAs, one unit a warp; and no more of them than a merge is worth (an estimate: segments are
-  // at least batch * kv_heads when every request has rows)
-  const long long most = (long long)kMaxSplits * a.batch * a.kv_heads;
-  long long G = (U + kWarps - 1) / kWarps;
-  if (G > most) G = most;
-  if (G > gridDim.x) G = gridDim.x;
+  const long long G = few ? min((long long)gridDim.x, U / piece) : min((long long)gridDim.x, kMaxShares * n_segs);
   const long long cta = blockIdx.x;
   if (cta >= G) return;
   long long u = unit_start(cta, U, G);
   const long long u_end = unit_start(cta + 1, U, G);
-  if (mine > 0 && excl <= u && u < excl + mine) {
+  if (excl <= u && u < excl + mine) {
     long long at = excl;
     for (int b = b0; b < b1; ++b) {
-      const long long n = request_units<S>(a, get_request(a, b, false));
+      const Request r = get_request(a, b, false);
+      const long long n = (long long)split.length(segment_units<S>(r)) * request_tiles<S>(a, r) * a.kv_heads;
       if (u < at + n) {
-        s_scan[8] = b;
-        s_scan[9] = at;
+        s_scan[16] = b;
+        s_scan[17] = at;
         break;
       }
       at += n;
     }
   }
   __syncthreads();
-  int b = (int)s_scan[8];
-  long long base = s_scan[9];
+  int b = (int)s_scan[16];
+  long long base = s_scan[17];
 
   const float kg = *a.k_global, vg = *a.v_global;
   uint32_t uses = 0;                                    // copies this warp has waited for: slot and parity
   bool gave_up = false;
   while (u < u_end) {
     const Request rq = get_request(a, b, false);
-    const long long n_req = request_units<S>(a, rq);
+    const int n_seg = segment_units<S>(rq), tiles = request_tiles<S>(a, rq), len_seg = split.length(n_seg);
+    const long long n_req = (long long)len_seg * tiles * a.kv_heads;
     if (u >= base + n_req) {
       base += n_req;
       ++b;
       continue;
     }
-    const int n_seg = segment_units<S>(rq), tiles = request_tiles<S>(a, rq);
-    const long long seg = (u - base) / n_seg;
-    const long long seg0 = base + seg * n_seg;
-    const int s0 = (int)(u - seg0), s1 = (int)min((long long)n_seg, u_end - seg0);
+    const long long seg = (u - base) / len_seg;
+    const long long seg0 = base + seg * len_seg;        // where it stands; its own units from seg0 + head on
+    const int s0 = max((int)(u - seg0) - split.head, 0);
+    const int s1 = min((int)min((long long)len_seg, u_end - seg0) - split.head, n_seg);
+    u = min(seg0 + len_seg, u_end);
+    if (s1 <= s0) continue;                             // overhead or padding only
     const int tile = (int)(seg % tiles), kvh = (int)(seg / tiles);
     const int row0 = tile * S::kRows;                   // row = query row * group + query head of the kv head
     const int n_rows = min(S::kRows, rq.rows * a.group - row0);
@@ -372,68 +411,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_at
     const int lo_any = a.window > 0 ? max(hi_all - a.window + 1, 0) : 0;
     const int lo_all = a.window > 0 ? max(hi_any - a.window + 1, 0) : 0;
 
-    // ---- queries: FP16 of q / 2^e in operand order, and the factors of the scores
-    for (int row = warp; row < S::kRows; row += kWarps) {
-      constexpr int E = D / 32;
-      float v[E];
-      float big = 0.0f;
-      if (row < n_rows) {
-        const int rr = row0 + row, tok = rq.first + rr / a.group, h = kvh * a.group + rr % a.group;
-        const T* q = static_cast<const T*>(a.q) + tok * a.q_ts + h * a.q_hs + lane * E;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          v[i] = load_q(q + i);
-          big = fmaxf(big, fabsf(v[i]));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = 0.0f;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-      int e = (int)(__float_as_uint(big) >> 23) - 127;
-      e = big > 0.0f ? min(max(e, -126), 126) : 0;
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
-      uint8_t* sq = smem + S::kOffQ;
-      if constexpr (D == 128) {
-        const int cq = lane >> 3, j = lane & 7;
-        *reinterpret_cast<uint2*>(sq + (((row >> 3) * 8 + j) * 32 + (row & 7) * 4 + cq) * 8) =
-            make_uint2(pack_f16(v[0] * down, v[1] * down), pack_f16(v[2] * down, v[3] * down));
-      } else {
-        const int cq = lane >> 3, j = (lane & 7) >> 1;
-        *reinterpret_cast<uint32_t*>(sq + (((row >> 3) * 4 + j) * 32 + (row & 7) * 4 + cq) * 8 + (lane & 1) * 4) =
-            pack_f16(v[0] * down, v[1] * down);
-      }
-      // never 0: a hidden score, -inf, times it has to stay -inf
-      if (lane == 0) s_f[row] = fmaxf(a.scale * kLog2e * kg * up, 1.2e-38f);
-    }
-    __syncthreads();
-
-    // ---- this warp's units
-    WarpState<D, NT> st;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) st.o[i][t][k] = 0.0f;
-      st.m[t][0] = st.m[t][1] = -INFINITY;
-      st.l[t][0] = st.l[t][1] = 0.0f;
-    }
-    uint32_t qreg[NT <= 2 ? NT * (D / 16) : 1][2];
-    if constexpr (NT <= 2) {
-#pragma unroll
-      for (int i = 0; i < NT * (D / 16); ++i) {
-        const uint2 v = lds64(smem + S::kOffQ + (i * 32 + lane) * 8);
-        qreg[i][0] = v.x, qreg[i][1] = v.y;
-      }
-    }
-    float f[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      f[t][0] = s_f[t * 8 + (lane & 3) * 2];
-      f[t][1] = s_f[t * 8 + (lane & 3) * 2 + 1];
-    }
+    // ---- this warp's units, and its first copies
     const int unit0 = rq.begin / S::kUnitTokens;        // the segment's first unit
     const int u_lo = max(s0, lo_any / S::kUnitTokens - unit0);
     const int u_hi = hi_any < 0 ? u_lo : min(s1, hi_any / S::kUnitTokens + 1 - unit0);
@@ -473,6 +451,67 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_at
       const int now = next;
       next = page_of(k + 1);
       issue(k, now, (uses + k) % S::kStages);
+    }
+
+    // ---- queries (while the first copies fly): FP16 of q / 2^e in operand order, and the factors of the scores
+    constexpr int E = D / 32;
+    float v[S::kRows / kWarps][E];
+#pragma unroll
+    for (int i = 0; i < S::kRows / kWarps; ++i) {
+      const int row = warp + i * kWarps;
+      const int rr = row0 + min(row, n_rows - 1), tok = rq.first + rr / a.group, h = kvh * a.group + rr % a.group;
+      const T* q = static_cast<const T*>(a.q) + tok * a.q_ts + h * a.q_hs + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[i][e] = row < n_rows ? load_q(q + e) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < S::kRows / kWarps; ++i) {
+      const int row = warp + i * kWarps;
+      float big = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(v[i][e]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      int e = (int)(__float_as_uint(big) >> 23) - 127;
+      e = big > 0.0f ? min(max(e, -126), 126) : 0;
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+      uint8_t* sq = smem + S::kOffQ;
+      const int cq = lane >> 3;
+      if constexpr (D == 128) {
+        *reinterpret_cast<uint2*>(sq + (((row >> 3) * 8 + (lane & 7)) * 32 + (row & 7) * 4 + cq) * 8) =
+            make_uint2(pack_f16(v[i][0] * down, v[i][1] * down), pack_f16(v[i][2] * down, v[i][3] * down));
+      } else {
+        *reinterpret_cast<uint32_t*>(sq + (((row >> 3) * 4 + ((lane & 7) >> 1)) * 32 + (row & 7) * 4 + cq) * 8 +
+                                     (lane & 1) * 4) = pack_f16(v[i][0] * down, v[i][1] * down);
+      }
+      // never 0: a hidden score, -inf, times it has to stay -inf
+      if (lane == 0) s_f[row] = fmaxf(a.scale * kLog2e * kg * up, 1.2e-38f);
+    }
+    __syncthreads();
+
+    WarpState<D, NT> st;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) st.o[i][t][k] = 0.0f;
+      st.m[t][0] = st.m[t][1] = -INFINITY;
+      st.l[t][0] = st.l[t][1] = 0.0f;
+    }
+    uint32_t qreg[NT <= 2 ? NT * (D / 16) : 1][2];
+    if constexpr (NT <= 2) {
+#pragma unroll
+      for (int i = 0; i < NT * (D / 16); ++i) {
+        const uint2 v = lds64(smem + S::kOffQ + (i * 32 + lane) * 8);
+        qreg[i][0] = v.x, qreg[i][1] = v.y;
+      }
+    }
+    float f[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      f[t][0] = s_f[t * 8 + (lane & 3) * 2];
+      f[t][1] = s_f[t * 8 + (lane & 3) * 2 + 1];
     }
     for (int k = 0; k < my_n; ++k) {
       const uint32_t slot = uses % S::kStages;
@@ -576,7 +615,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_at
       }
     __syncthreads();
     const bool all = s0 == 0 && s1 == n_seg;
-    const long long c_first = cta_of_unit(seg0, U, G), c_last = cta_of_unit(seg0 + n_seg - 1, U, G);
+    const long long c_first = cta_of_unit(seg0 + split.head, U, G);
+    const long long c_last = cta_of_unit(seg0 + split.head + n_seg - 1, U, G);
     float* rec = a.records + (size_t)(2 * cta + (cta == c_first ? 1 : 0)) * S::kRecord;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -632,28 +672,36 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_at
     if (!all) {
       __threadfence();
       __syncthreads();
-      unsigned int* flag = reinterpret_cast<unsigned int*>(smem + S::kOffScan + 128);
+      unsigned int* flag = reinterpret_cast<unsigned int*>(smem + S::kOffScan + 248);
       if (tid == 0) *flag = atomicAdd(&a.counters[c_first], 1u);
       __syncthreads();
       if (*flag == (unsigned)(c_last - c_first)) {
         __threadfence();
         for (int e = tid; e < n_rows * (D / 4); e += kThreads) {
           const int row = e / (D / 4), d = e % (D / 4) * 4;
-          float mx = -INFINITY;
-          for (long long q = c_first; q <= c_last; ++q) {
-            const float* r = a.records + (size_t)(2 * q + (q == c_first ? 1 : 0)) * S::kRecord;
-            mx = fmaxf(mx, __ldcg(r + S::kRows * D + row));
-          }
+          float mx = -INFINITY, l = 0.0f;
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          float l = 0.0f;
-#pragma unroll 4
-          for (long long q = c_first; q <= c_last; ++q) {
-            const float* r = a.records + (size_t)(2 * q + (q == c_first ? 1 : 0)) * S::kRecord;
-            const float m = __ldcg(r + S::kRows * D + row), lq = __ldcg(r + S::kRows * (D + 1) + row);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(r + row * D + d));
-            const float w = m == -INFINITY ? 0.0f : ex2(m - mx);
-            l = fmaf(lq, w, l);
-            x.x = fmaf(y.x, w, x.x), x.y = fmaf(y.y, w, x.y), x.z = fmaf(y.z, w, x.z), x.w = fmaf(y.w, w, x.w);
+          constexpr int kBatch = 8;                     // records whose loads are in flight together
+          for (long long q0 = c_first; q0 <= c_last; q0 += kBatch) {
+            float m[kBatch], lq[kBatch];
+            float4 y[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+              const long long q = min(q0 + j, c_last);
+              const float* r = a.records + (size_t)(2 * q + (q == c_first ? 1 : 0)) * S::kRecord;
+              m[j] = __ldcg(r + S::kRows * D + row);
+              lq[j] = __ldcg(r + S::kRows * (D + 1) + row);
+              y[j] = __ldcg(reinterpret_cast<const float4*>(r + row * D + d));
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+              if (q0 + j > c_last || m[j] == -INFINITY) continue;
+              const float mn = fmaxf(mx, m[j]), back = ex2(mx - mn), w = ex2(m[j] - mn);
+              mx = mn;
+              l = fmaf(lq[j], w, l * back);
+              x.x = fmaf(y[j].x, w, x.x * back), x.y = fmaf(y[j].y, w, x.y * back);
+              x.z = fmaf(y[j].z, w, x.z * back), x.w = fmaf(y[j].w, w, x.w * back);
+            }
           }
           const int rr = row0 + row, tok = rq.first + rr / a.group, h = kvh * a.group + rr % a.group;
           const float inv = l > 0.0f ? vg / l : 0.0f;
@@ -666,11 +714,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_at
       }
       __syncthreads();
     }
-    u = seg0 + s1;
   }
 }
 
-constexpr size_t kCounterBytes = (kMaxCtas * 4 + 255) / 256 * 256;
+constexpr size_t kCounterBytes = 4096;  // what a caller zeroes
+static_assert(kMaxCtas * 4 <= kCounterBytes, "the counters");
 
 // CTAs of a variant: as many as are resident at once.
 template <int D, int NT, class T>
