@@ -123,14 +123,16 @@ struct Shape {
   static constexpr int kUnitGroups = 256 / D;              // 32 tokens at D = 128, 64 at D = 64: 4608 bytes
   static constexpr int kUnitTokens = kKvGroup * kUnitGroups;
   static constexpr int kUnitBytes = kUnitGroups * KvLayout<D>::kGroupBytes;
-  static constexpr int kStages = 3;
+  static constexpr int kPair = NT <= 2 ? 2 : 1;            // groups whose scores are formed together (latency)
+  static constexpr int kStages = NT == 1 ? 2 : 3;
   static constexpr int kMergeStride = D + 4;               // floats a row in the merge buffer (bank spread)
   static constexpr int kRecord = kRows * (D + 2);          // floats of a record: O, then M, then L
   // shared memory
   static constexpr int kOffRing = 0;
   static constexpr int kOffQ = kWarps * kStages * kUnitBytes;             // FP16 query operands
-  static constexpr int kOffMerge = kOffQ + kRows * D * 2;                 // [kWarps][8][kMergeStride] floats
-  static constexpr int kOffML = kOffMerge + kWarps * 8 * kMergeStride * 4;  // [kWarps][kRows] maxima, then sums
+  static constexpr int kOffMerge = 0;                      // [kWarps][8][kMergeStride] floats, in the ring: idle then
+  static_assert(kWarps * 8 * kMergeStride * 4 <= kOffQ, "the merge buffer");
+  static constexpr int kOffML = kOffQ + kRows * D * 2;                    // [kWarps][kRows] maxima, then sums
   static constexpr int kOffF = kOffML + 2 * kWarps * kRows * 4;           // [kRows] score factors
   static constexpr int kOffBar = kOffF + kRows * 4;                       // [kWarps][kStages] barriers
   static constexpr int kOffValid = kOffBar + kWarps * kStages * 8;        // [kWarps][kStages] groups present
@@ -288,7 +290,7 @@ NVFP4_DEVINL void weigh(const uint8_t* g, int lane, const uint32_t (&p)[NT][2], 
 
 // ---- the kernel -----------------------------------------------------------------------
 template <int D, int NT, class T>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_attention_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel(const AttnArgs a) {
   using S = Shape<D, NT>;
   using L = KvLayout<D>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -446,6 +448,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_at
                  &bars[slot]);
       }
     };
+    // the ring held the last segment's merge: order those writes before the copies
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     int next = page_of(0);
     for (int k = 0; k < S::kStages && k < my_n; ++k) {
       const int now = next;
@@ -507,9 +511,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_at
         qreg[i][0] = v.x, qreg[i][1] = v.y;
       }
     }
-    float f[NT][2];
+    float f[NT][2], neg_m[NT][2];                       // factors; minus the maximum, 0 while there is none
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+      neg_m[t][0] = neg_m[t][1] = 0.0f;
       f[t][0] = s_f[t * 8 + (lane & 3) * 2];
       f[t][1] = s_f[t * 8 + (lane & 3) * 2 + 1];
     }
@@ -520,26 +525,34 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_at
       const uint32_t have = valid[slot];
       const uint8_t* unit = ring + slot * S::kUnitBytes;
       const int t_unit = (unit0 + u_lo + warp + k * kWarps) * S::kUnitTokens;
-#pragma unroll 2
-      for (int gi = 0; gi < S::kUnitGroups; ++gi) {
-        if (!((have >> gi) & 1u)) continue;
+      for (int gi = 0; gi < S::kUnitGroups; gi += S::kPair) {
+        const uint32_t there = (have >> gi) & ((1u << S::kPair) - 1u);
+        if (there == 0u) continue;
         const uint8_t* g = unit + gi * L::kGroupBytes;
         const int t0 = t_unit + gi * kKvGroup;
-        float s[NT][4];
-        scores<D, NT>(g, lane, qreg, smem + S::kOffQ, s);
-        int live = 4;
-        if (t0 + kKvGroup - 1 > hi_all || t0 < lo_all) {
-          // token of score row pos = r + 8 i: 4 (r / 2) + 2 i + r % 2
-          live = min(max(rq.len - t0 - 4 * (lane & 3), 0), 4);
+        float s[S::kPair][NT][4];
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+        for (int h = 0; h < S::kPair; ++h) scores<D, NT>(g + h * L::kGroupBytes, lane, qreg, smem + S::kOffQ, s[h]);
+        int live[S::kPair];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int tok = t0 + 4 * (lane >> 3) + 2 * (i >> 1) + ((lane >> 2) & 1);
-              const int rr = t * 8 + (lane & 3) * 2 + (i & 1);
-              const int hi = rq.len - rq.rows + (row0 + rr) / a.group;
-              if (tok > hi || (a.window > 0 && tok <= hi - a.window)) s[t][i] = -INFINITY;
-            }
+        for (int h = 0; h < S::kPair; ++h) live[h] = 4;
+        if (t0 + S::kPair * kKvGroup - 1 > hi_all || t0 < lo_all || there != (1u << S::kPair) - 1u) {
+#pragma unroll
+          for (int h = 0; h < S::kPair; ++h) {
+            // token of score row pos = r + 8 i: 4 (r / 2) + 2 i + r % 2; a group that is not there is hidden too
+            const int th = t0 + h * kKvGroup;
+            const bool gone = !((there >> h) & 1u);
+            live[h] = gone ? 0 : min(max(rq.len - th - 4 * (lane & 3), 0), 4);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int tok = th + 4 * (lane >> 3) + 2 * (i >> 1) + ((lane >> 2) & 1);
+                const int rr = t * 8 + (lane & 3) * 2 + (i & 1);
+                const int hi = rq.len - rq.rows + (row0 + rr) / a.group;
+                if (gone || tok > hi || (a.window > 0 && tok <= hi - a.window)) s[h][t][i] = -INFINITY;
+              }
+          }
         }
         // a larger score than any before moves the maximum and rescales what has been summed
         bool grew = false;
@@ -548,7 +561,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_at
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int k2 = 0; k2 < 2; ++k2) {
-            top[t][k2] = fmaxf(s[t][k2], s[t][k2 + 2]) * f[t][k2];
+            float x = fmaxf(s[0][t][k2], s[0][t][k2 + 2]);
+            if (S::kPair == 2) x = fmaxf(x, fmaxf(s[S::kPair - 1][t][k2], s[S::kPair - 1][t][k2 + 2]));
+            top[t][k2] = x * f[t][k2];
             grew = grew || top[t][k2] > st.m[t][k2];
           }
         if (__any_sync(0xffffffffu, grew)) {
@@ -561,6 +576,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_at
               for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
               const float back = mx == -INFINITY ? 1.0f : ex2(st.m[t][k2] - mx);
               st.m[t][k2] = mx;
+              neg_m[t][k2] = mx == -INFINITY ? 0.0f : -mx;
               st.l[t][k2] *= back;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
@@ -569,20 +585,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 2) kv_at
               }
             }
         }
-        uint32_t p[NT][2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float w[4];
+        for (int h = 0; h < S::kPair; ++h) {
+          uint32_t p[NT][2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float ref = st.m[t][i & 1] == -INFINITY ? 0.0f : st.m[t][i & 1];
-            w[i] = ex2(fmaf(s[t][i], f[t][i & 1], -ref));
-            st.l[t][i & 1] += w[i];
+          for (int t = 0; t < NT; ++t) {
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = ex2(fmaf(s[h][t][i], f[t][i & 1], neg_m[t][i & 1]));
+            st.l[t][0] += w[0] + w[2];
+            st.l[t][1] += w[1] + w[3];
+            p[t][0] = transpose8x8(pack_f16(w[0], w[1]));
+            p[t][1] = transpose8x8(pack_f16(w[2], w[3]));
           }
-          p[t][0] = transpose8x8(pack_f16(w[0], w[1]));
-          p[t][1] = transpose8x8(pack_f16(w[2], w[3]));
+          weigh<D, NT>(g + h * L::kGroupBytes, lane, p, live[h], st);
         }
-        weigh<D, NT>(g, lane, p, live, st);
       }
       __syncwarp();                                     // the slot has been read
       if (k + S::kStages < my_n && !gave_up) {
