@@ -135,8 +135,7 @@ struct Shape {
   static constexpr int kOffML = kOffQ + kRows * D * 2;                    // [kWarps][kRows] maxima, then sums
   static constexpr int kOffF = kOffML + 2 * kWarps * kRows * 4;           // [kRows] score factors
   static constexpr int kOffBar = kOffF + kRows * 4;                       // [kWarps][kStages] barriers
-  static constexpr int kOffValid = kOffBar + kWarps * kStages * 8;        // [kWarps][kStages] groups present
-  static constexpr int kOffScan = kOffValid + kWarps * kStages * 4;       // 32 words for the split
+  static constexpr int kOffScan = kOffBar + kWarps * kStages * 8;         // 32 words for the split
   static constexpr int kSmem = (kOffScan + 32 * 8 + 15) / 16 * 16;
 };
 
@@ -296,7 +295,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar) + warp * S::kStages;
-  volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + S::kOffValid) + warp * S::kStages;
   uint8_t* ring = smem + S::kOffRing + warp * S::kStages * S::kUnitBytes;
   float* s_f = reinterpret_cast<float*>(smem + S::kOffF);
   float* s_m = reinterpret_cast<float*>(smem + S::kOffML);
@@ -387,7 +385,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
   long long base = s_scan[17];
 
   const float kg = *a.k_global, vg = *a.v_global;
-  uint32_t uses = 0;                                    // copies this warp has waited for: slot and parity
+  uint32_t slot = 0, phase = 0;                         // of the next copy that this warp waits for
+  auto advance = [&]() {
+    if (++slot == S::kStages) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  };
   bool gave_up = false;
   while (u < u_end) {
     const Request rq = get_request(a, b, false);
@@ -420,41 +424,58 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
     const int my_n = u_lo + warp < u_hi ? (u_hi - u_lo - warp + kWarps - 1) / kWarps : 0;
     const int32_t* trow = a.table + (size_t)b * a.width;
     const bool whole = a.page_size % S::kUnitTokens == 0;   // a unit lies in one page
-    // The page of lane's group of unit k (-1: not there, or not to be read); lanes 0 .. kUnitGroups - 1.
-    auto page_of = [&](int k) {
-      const int t0 = (unit0 + u_lo + warp + k * kWarps) * S::kUnitTokens + lane * kKvGroup;
-      if (k >= my_n || lane >= S::kUnitGroups || t0 > hi_any || t0 + kKvGroup <= lo_any) return -1;
-      const int p = trow[t0 / a.page_size];
-      if (p >= 0 && p < a.num_pages) return p;
-      atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
-      return -1;
-    };
-    auto issue = [&](int k, int page, uint32_t slot) {
-      const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
-      if (lane == 0) {
-        valid[slot] = have;
-        mbar_arrive_expect_tx(&bars[slot], __popc(have) * L::kGroupBytes);
+    // Lane g < kUnitGroups looks after group g of the warp's units: where it starts, its place in the page table
+    // and in its page, all advanced by kWarps units at a time without a division.
+    const int t_first = (unit0 + u_lo + warp) * S::kUnitTokens;
+    constexpr int kStep = kWarps * S::kUnitTokens;
+    int g_tok = t_first + lane * kKvGroup, g_page = g_tok / a.page_size, g_off = g_tok - g_page * a.page_size;
+    int left = lane < S::kUnitGroups ? my_n : 0;
+    const int step_pages = kStep / a.page_size, step_off = kStep - step_pages * a.page_size;
+    const uint8_t* src_head = a.pages + (size_t)kvh * (a.page_size / kKvGroup) * L::kGroupBytes;
+    const size_t page_bytes = (size_t)a.kv_heads * (a.page_size / kKvGroup) * L::kGroupBytes;
+    int nx_page = -1, nx_off = 0;                       // the next unit's page (-1: not there, or not to be read)
+    auto look_up = [&]() {
+      nx_page = -1;
+      nx_off = g_off;
+      if (left > 0 && g_tok <= hi_any && g_tok + kKvGroup > lo_any) {
+        nx_page = trow[g_page];
+        if (nx_page < 0 || nx_page >= a.num_pages) {
+          nx_page = -1;
+          atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
+        }
       }
+      --left;
+      g_tok += kStep;
+      g_page += step_pages;
+      g_off += step_off;
+      if (g_off >= a.page_size) {
+        g_off -= a.page_size;
+        ++g_page;
+      }
+    };
+    // Starts the copies of the unit looked up last into ring slot `slot`; returns which of its groups come.
+    auto issue = [&](uint32_t slot) -> uint32_t {
+      const uint32_t have = __ballot_sync(0xffffffffu, nx_page >= 0);
+      const bool one = whole && have == (1u << S::kUnitGroups) - 1u;
+      if (lane == 0) mbar_arrive_expect_tx(&bars[slot], __popc(have) * L::kGroupBytes);
       __syncwarp();
-      uint8_t* dst = ring + slot * S::kUnitBytes;
-      const int t0 = (unit0 + u_lo + warp + k * kWarps) * S::kUnitTokens + lane * kKvGroup;
-      if (whole && have == (1u << S::kUnitGroups) - 1u) {
-        if (lane == 0)
-          bulk_g2s(dst, a.pages + kv_group_offset<D>(page, t0 % a.page_size, kvh, a.page_size, a.kv_heads),
-                   S::kUnitBytes, &bars[slot]);
-      } else if (page >= 0) {
-        bulk_g2s(dst + lane * L::kGroupBytes,
-                 a.pages + kv_group_offset<D>(page, t0 % a.page_size, kvh, a.page_size, a.kv_heads), L::kGroupBytes,
-                 &bars[slot]);
-      }
+      if (nx_page >= 0 && (lane == 0 || !one))
+        bulk_g2s(ring + slot * S::kUnitBytes + lane * L::kGroupBytes,
+                 src_head + nx_page * page_bytes + (nx_off / kKvGroup) * L::kGroupBytes,
+                 one ? S::kUnitBytes : L::kGroupBytes, &bars[slot]);
+      return have;
     };
-    // the ring held the last segment's merge: order those writes before the copies
+    // the ring held the last segment's merge: order those accesses before the copies
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    int next = page_of(0);
-    for (int k = 0; k < S::kStages && k < my_n; ++k) {
-      const int now = next;
-      next = page_of(k + 1);
-      issue(k, now, (uses + k) % S::kStages);
+    uint32_t coming[S::kStages];                        // groups of the units in flight, oldest first
+    look_up();
+#pragma unroll
+    for (int k = 0; k < S::kStages; ++k) {
+      coming[k] = 0;
+      if (k < my_n) {
+        coming[k] = issue(slot + k < S::kStages ? slot + k : slot + k - S::kStages);
+        look_up();
+      }
     }
 
     // ---- queries (while the first copies fly): FP16 of q / 2^e in operand order, and the factors of the scores
@@ -518,13 +539,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
       f[t][0] = s_f[t * 8 + (lane & 3) * 2];
       f[t][1] = s_f[t * 8 + (lane & 3) * 2 + 1];
     }
-    for (int k = 0; k < my_n; ++k) {
-      const uint32_t slot = uses % S::kStages;
-      gave_up = !mbar_wait(&bars[slot], (uses / S::kStages) & 1) || gave_up;
-      ++uses;
-      const uint32_t have = valid[slot];
+    int t_unit = t_first;
+    for (int k = 0; k < my_n; ++k, t_unit += kStep) {
+      gave_up = !mbar_wait(&bars[slot], phase) || gave_up;
+      const uint32_t have = coming[0];
       const uint8_t* unit = ring + slot * S::kUnitBytes;
-      const int t_unit = (unit0 + u_lo + warp + k * kWarps) * S::kUnitTokens;
       for (int gi = 0; gi < S::kUnitGroups; gi += S::kPair) {
         const uint32_t there = (have >> gi) & ((1u << S::kPair) - 1u);
         if (there == 0u) continue;
@@ -602,16 +621,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
         }
       }
       __syncwarp();                                     // the slot has been read
+#pragma unroll
+      for (int i = 0; i + 1 < S::kStages; ++i) coming[i] = coming[i + 1];
+      coming[S::kStages - 1] = 0;
       if (k + S::kStages < my_n && !gave_up) {
-        const int now = next;
-        next = page_of(k + S::kStages + 1);
-        issue(k + S::kStages, now, slot);
+        coming[S::kStages - 1] = issue(slot);
+        look_up();
       }
+      advance();
       if (gave_up) {
         // wait for the copies still in flight, then leave the units that are not loaded
         for (int j = 1; j < S::kStages && k + j < my_n; ++j) {
-          mbar_wait(&bars[uses % S::kStages], (uses / S::kStages) & 1);
-          ++uses;
+          mbar_wait(&bars[slot], phase);
+          advance();
         }
         break;
       }
