@@ -2,18 +2,21 @@
 // occurred, biases and grammar masks, in one pass.
 //
 // A row's counts, its bias entries and its mask all belong to token ids, so the
-// vocabulary is cut into chunks: a CTA counts the row's tokens that fall into its
-// chunk in shared memory (integer atomics: any order gives the same counts),
-// marks the last bias entry of each id (an integer maximum), and then streams its
-// logits through once.  Bound by HBM for large batches (4 bytes in, 4 out a
-// logit), by latency for small ones.
+// vocabulary is cut into chunks, one CTA each.  A CTA asks for its logits first
+// (16 or 4 a thread, in registers), counts the row's tokens that fall into its
+// chunk in shared memory while they come (integer atomics: any order gives the
+// same counts), applies the penalties, marks the last bias entry of each id in the
+// same memory (an integer maximum), and writes each logit once.  Bound by HBM for
+// large batches (4 bytes in, 4 out a logit), by latency for small ones.  Every
+// CTA of a row reads the row's whole history (from L2): 16 KB against the 64 KB of
+// logits of an 8192-token chunk at 4096 tokens; counting through a cluster's
+// distributed shared memory would read it once, at the price of a cluster barrier.
 #include <math.h>
 
 #include "common.cuh"
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr uint32_t kPrompt = 0x80000000u;   // the token stands in the prompt; the other bits count the output
 
 struct LogitArgs {
@@ -27,67 +30,167 @@ struct LogitArgs {
   const uint32_t* mask;
   const int32_t* mask_rows;
   float fill;
-  int V, history, n_bias, mask_count, chunk;
+  int V, history, n_bias, mask_count;
+  int vec_in, vec_out, vec_tok;             // rows can be read / written / scanned in whole 4-element pieces
 };
 
 NVFP4_DEVINL float load1(const float* p) { return *p; }
 NVFP4_DEVINL float load1(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+NVFP4_DEVINL float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+NVFP4_DEVINL float4 load4(const uint16_t* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+}
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) process_logits_kernel(const LogitArgs a) {
-  extern __shared__ uint32_t smem[];
-  uint32_t* count = smem;                   // [chunk]
-  uint32_t* bias = smem + a.chunk;          // [chunk], only with biases: 1 + the last entry of the id, 0 none
+// PIECES pieces of 4 logits a thread: a chunk of 4 * PIECES * THREADS.
+template <class T, int THREADS, int PIECES>
+__global__ void __launch_bounds__(THREADS) process_logits_kernel(const LogitArgs a) {
+  constexpr int kChunk = 4 * PIECES * THREADS;
+  __shared__ __align__(16) uint32_t s_tab[kChunk];
   griddep_launch_dependents();
-  griddep_wait();
   const int r = blockIdx.y, tid = threadIdx.x;
-  const int v0 = blockIdx.x * a.chunk;
-  const int n = min(a.chunk, a.V - v0);
-  const bool has_tokens = a.history > 0, has_bias = a.n_bias > 0;
-  for (int i = tid; i < (has_bias ? 2 : 1) * a.chunk; i += kThreads) smem[i] = 0u;
-  __syncthreads();
-  if (has_tokens) {
-    const int used = min(max(a.n_tokens[r], 0), a.history);
-    const int prompt = a.n_prompt ? min(max(a.n_prompt[r], 0), used) : 0;
-    const int32_t* tok = a.tokens + (size_t)r * a.history;
-    for (int i = tid; i < used; i += kThreads) {
-      const uint32_t v = (uint32_t)tok[i] - (uint32_t)v0;
-      if (v < (uint32_t)n) {
-        if (i < prompt) atomicOr(&count[v], kPrompt);
-        else atomicAdd(&count[v], 1u);
-      }
+  const int v0 = blockIdx.x * kChunk;
+  const int n = min(kChunk, a.V - v0);
+#pragma unroll
+  for (int k = 0; k < PIECES; ++k) *reinterpret_cast<uint4*>(&s_tab[4 * (tid + k * THREADS)]) = make_uint4(0u, 0u, 0u, 0u);
+  griddep_wait();
+  const T* in = static_cast<const T*>(a.logits) + (size_t)r * a.ld + v0;
+  float x[PIECES][4];
+#pragma unroll
+  for (int k = 0; k < PIECES; ++k) {
+    const int i = 4 * (tid + k * THREADS);
+    if (a.vec_in && i + 4 <= n) {
+      const float4 f = load4(in + i);
+      x[k][0] = f.x, x[k][1] = f.y, x[k][2] = f.z, x[k][3] = f.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[k][j] = i + j < n ? load1(in + i + j) : 0.0f;
     }
   }
-  if (has_bias) {
-    const int32_t* ids = a.bias_ids + (size_t)r * a.n_bias;
-    for (int i = tid; i < a.n_bias; i += kThreads) {
-      const uint32_t v = (uint32_t)ids[i] - (uint32_t)v0;
-      if (v < (uint32_t)n) atomicMax(&bias[v], (uint32_t)i + 1u);
-    }
-  }
-  __syncthreads();
-  const float rep = a.repetition ? a.repetition[r] : 1.0f;
-  const float pres = a.presence ? a.presence[r] : 0.0f;
-  const float freq = a.frequency ? a.frequency[r] : 0.0f;
   const uint32_t* mask = nullptr;
   if (a.mask) {
     const int m = a.mask_rows ? a.mask_rows[r] : r;
     if (m >= 0 && m < a.mask_count) mask = a.mask + (size_t)m * ((a.V + 31) / 32);
   }
-  const T* in = static_cast<const T*>(a.logits) + (size_t)r * a.ld + v0;
-  float* out = a.out + (size_t)r * a.V + v0;
-  for (int i = tid; i < n; i += kThreads) {
-    float x = load1(in + i);
-    const uint32_t c = count[i];
-    if (c) {
-      x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-      const uint32_t k = c & ~kPrompt;
-      if (k) x = __fsub_rn(__fsub_rn(x, __fmul_rn(freq, (float)k)), pres);
-    }
-    if (has_bias && bias[i]) x = __fadd_rn(x, a.bias_values[(size_t)r * a.n_bias + bias[i] - 1u]);
-    if (mask && !((mask[(v0 + i) >> 5] >> ((v0 + i) & 31)) & 1u)) x = a.fill;
-    out[i] = x;
+  uint32_t allowed[PIECES];                 // 4 bits a piece (a piece lies in one word: v0 and i are multiples of 4)
+#pragma unroll
+  for (int k = 0; k < PIECES; ++k) {
+    const int i = 4 * (tid + k * THREADS);
+    allowed[k] = mask && i < n ? mask[(v0 + i) >> 5] >> ((v0 + i) & 31) : ~0u;
   }
+  __syncthreads();
+  if (a.history > 0) {
+    const int used = min(max(a.n_tokens[r], 0), a.history);
+    const int prompt = a.n_prompt ? min(max(a.n_prompt[r], 0), used) : 0;
+    const int32_t* tok = a.tokens + (size_t)r * a.history;
+    auto count = [&](int32_t id, int i) {
+      const uint32_t v = (uint32_t)id - (uint32_t)v0;
+      if (v < (uint32_t)n) {
+        if (i < prompt) atomicOr(&s_tab[v], kPrompt);
+        else atomicAdd(&s_tab[v], 1u);
+      }
+    };
+    int i = 0;
+    if (a.vec_tok) {
+      constexpr int kBatch = 4;             // pieces in flight
+      const int pieces = used / 4;
+      for (int p = tid; p < pieces; p += kBatch * THREADS) {
+        int4 q[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          q[j] = p + j * THREADS < pieces ? __ldg(reinterpret_cast<const int4*>(tok) + p + j * THREADS)
+                                          : make_int4(-1, -1, -1, -1);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int at = 4 * (p + j * THREADS);
+          count(q[j].x, at);
+          count(q[j].y, at + 1);
+          count(q[j].z, at + 2);
+          count(q[j].w, at + 3);
+        }
+      }
+      i = 4 * pieces;
+    }
+    for (i += tid; i < used; i += THREADS) count(__ldg(tok + i), i);
+    __syncthreads();
+    const float rep = a.repetition ? a.repetition[r] : 1.0f;
+    const float pres = a.presence ? a.presence[r] : 0.0f;
+    const float freq = a.frequency ? a.frequency[r] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k) {
+      const uint4 c4 = *reinterpret_cast<const uint4*>(&s_tab[4 * (tid + k * THREADS)]);
+      if (!(c4.x | c4.y | c4.z | c4.w)) continue;
+      const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c[j]) {
+          const uint32_t times = c[j] & ~kPrompt;
+          x[k][j] = x[k][j] > 0.0f ? __fdiv_rn(x[k][j], rep) : __fmul_rn(x[k][j], rep);
+          if (times) x[k][j] = __fsub_rn(__fsub_rn(x[k][j], __fmul_rn(freq, (float)times)), pres);
+        }
+    }
+  }
+  if (a.n_bias > 0) {
+    // the same memory: 1 + the last bias entry of each id, 0 none (a thread clears what it alone has read)
+    if (a.history > 0) {
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k)
+        *reinterpret_cast<uint4*>(&s_tab[4 * (tid + k * THREADS)]) = make_uint4(0u, 0u, 0u, 0u);
+      __syncthreads();
+    }
+    const int32_t* ids = a.bias_ids + (size_t)r * a.n_bias;
+    const float* values = a.bias_values + (size_t)r * a.n_bias;
+    for (int i = tid; i < a.n_bias; i += THREADS) {
+      const uint32_t v = (uint32_t)ids[i] - (uint32_t)v0;
+      if (v < (uint32_t)n) atomicMax(&s_tab[v], (uint32_t)i + 1u);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k) {
+      const uint4 c4 = *reinterpret_cast<const uint4*>(&s_tab[4 * (tid + k * THREADS)]);
+      const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c[j]) x[k][j] = __fadd_rn(x[k][j], values[c[j] - 1u]);
+    }
+  }
+  float* out = a.out + (size_t)r * a.V + v0;
+#pragma unroll
+  for (int k = 0; k < PIECES; ++k) {
+    const int i = 4 * (tid + k * THREADS);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (!((allowed[k] >> j) & 1u)) x[k][j] = a.fill;
+    if (a.vec_out && i + 4 <= n) {
+      *reinterpret_cast<float4*>(out + i) = make_float4(x[k][0], x[k][1], x[k][2], x[k][3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < n) out[i + j] = x[k][j];
+    }
+  }
+}
+
+template <class T, int THREADS, int PIECES>
+cudaError_t launch(const LogitArgs& a, int rows, cudaStream_t stream) {
+  constexpr int kChunk = 4 * PIECES * THREADS;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.V + kChunk - 1) / kChunk), (unsigned)rows);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, process_logits_kernel<T, THREADS, PIECES>, a);
+}
+
+template <class T>
+cudaError_t dispatch(const LogitArgs& a, int rows, cudaStream_t stream) {
+  // large chunks once they fill the GPU twice: less history read over
+  if ((long long)rows * ((a.V + 8191) / 8192) >= 304) return launch<T, 512, 4>(a, rows, stream);
+  return launch<T, 256, 1>(a, rows, stream);
 }
 
 }  // namespace
@@ -118,21 +221,11 @@ extern "C" nvfp4_status nvfp4_process_logits(const void* logits, int dtype, int 
   const nvfp4_status ds = nvfp4_internal_check_device();
   if (ds != NVFP4_OK) return ds;
   LogitArgs a = {logits, ld, out, tokens, n_tokens, n_prompt, repetition, presence, frequency, bias_ids, bias_values,
-                 mask, mask_rows, fill, V, history, n_bias, mask_count, 0};
-  a.chunk = 4096;
-  const dim3 grid((unsigned)((V + a.chunk - 1) / a.chunk), (unsigned)rows);
-  const size_t smem = (size_t)a.chunk * 4 * (n_bias > 0 ? 2 : 1);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return nvfp4_internal_cuda_status(dtype == NVFP4_DTYPE_F32
-                                        ? cudaLaunchKernelEx(&cfg, process_logits_kernel<float>, a)
-                                        : cudaLaunchKernelEx(&cfg, process_logits_kernel<uint16_t>, a));
+                 mask, mask_rows, fill, V, history, n_bias, mask_count, 0, 0, 0};
+  const size_t piece_in = dtype == NVFP4_DTYPE_F32 ? 16 : 8;       // bytes of 4 logits
+  a.vec_in = nvfp4_internal_aligned(logits, piece_in) && (rows == 1 || ld % 4 == 0);
+  a.vec_out = nvfp4_internal_aligned(out, 16) && (rows == 1 || V % 4 == 0);
+  a.vec_tok = history > 0 && nvfp4_internal_aligned(tokens, 16) && (rows == 1 || history % 4 == 0);
+  return nvfp4_internal_cuda_status(dtype == NVFP4_DTYPE_F32 ? dispatch<float>(a, rows, stream)
+                                                             : dispatch<uint16_t>(a, rows, stream));
 }
