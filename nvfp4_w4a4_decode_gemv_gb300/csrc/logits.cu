@@ -67,22 +67,43 @@ __global__ void __launch_bounds__(THREADS) process_logits_kernel(const LogitArgs
       for (int j = 0; j < 4; ++j) x[k][j] = i + j < n ? load1(in + i + j) : 0.0f;
     }
   }
+  // everything that waits for no other load is asked for before anything is used: the row's parameters, the first
+  // pieces of its history (all of the row's `history` entries exist, however many are in use), its first bias entry
+  const int32_t* tok = a.tokens + (size_t)r * a.history;
+  constexpr int kBatch = 4;                 // pieces of history in flight
+  int4 q[kBatch];
+  if (a.vec_tok) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (tid + j * THREADS < a.history / 4) q[j] = __ldg(reinterpret_cast<const int4*>(tok) + tid + j * THREADS);
+  }
+  int used = 0, prompt = 0;
+  float rep = 1.0f, pres = 0.0f, freq = 0.0f;
+  if (a.history > 0) {
+    used = a.n_tokens[r];
+    if (a.n_prompt) prompt = a.n_prompt[r];
+    if (a.repetition) rep = a.repetition[r];
+    if (a.presence) pres = a.presence[r];
+    if (a.frequency) freq = a.frequency[r];
+  }
+  const int32_t* ids = a.bias_ids + (size_t)r * a.n_bias;
+  const float* values = a.bias_values + (size_t)r * a.n_bias;
+  const int32_t id0 = tid < a.n_bias ? ids[tid] : -1;
   const uint32_t* mask = nullptr;
   if (a.mask) {
     const int m = a.mask_rows ? a.mask_rows[r] : r;
     if (m >= 0 && m < a.mask_count) mask = a.mask + (size_t)m * ((a.V + 31) / 32);
   }
-  uint32_t allowed[PIECES];                 // 4 bits a piece (a piece lies in one word: v0 and i are multiples of 4)
+  uint32_t allowed[PIECES];                 // a piece lies in one word: v0 and i are multiples of 4
 #pragma unroll
   for (int k = 0; k < PIECES; ++k) {
     const int i = 4 * (tid + k * THREADS);
-    allowed[k] = mask && i < n ? mask[(v0 + i) >> 5] >> ((v0 + i) & 31) : ~0u;
+    allowed[k] = mask && i < n ? mask[(v0 + i) >> 5] : ~0u;
   }
+  used = min(max(used, 0), a.history);
+  prompt = min(max(prompt, 0), used);
   __syncthreads();
   if (a.history > 0) {
-    const int used = min(max(a.n_tokens[r], 0), a.history);
-    const int prompt = a.n_prompt ? min(max(a.n_prompt[r], 0), used) : 0;
-    const int32_t* tok = a.tokens + (size_t)r * a.history;
     auto count = [&](int32_t id, int i) {
       const uint32_t v = (uint32_t)id - (uint32_t)v0;
       if (v < (uint32_t)n) {
@@ -92,30 +113,27 @@ __global__ void __launch_bounds__(THREADS) process_logits_kernel(const LogitArgs
     };
     int i = 0;
     if (a.vec_tok) {
-      constexpr int kBatch = 4;             // pieces in flight
       const int pieces = used / 4;
       for (int p = tid; p < pieces; p += kBatch * THREADS) {
-        int4 q[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          q[j] = p + j * THREADS < pieces ? __ldg(reinterpret_cast<const int4*>(tok) + p + j * THREADS)
-                                          : make_int4(-1, -1, -1, -1);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
           const int at = 4 * (p + j * THREADS);
-          count(q[j].x, at);
-          count(q[j].y, at + 1);
-          count(q[j].z, at + 2);
-          count(q[j].w, at + 3);
+          if (at < 4 * pieces) {
+            count(q[j].x, at);
+            count(q[j].y, at + 1);
+            count(q[j].z, at + 2);
+            count(q[j].w, at + 3);
+          }
         }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (p + (kBatch + j) * THREADS < pieces)
+            q[j] = __ldg(reinterpret_cast<const int4*>(tok) + p + (kBatch + j) * THREADS);
       }
       i = 4 * pieces;
     }
     for (i += tid; i < used; i += THREADS) count(__ldg(tok + i), i);
     __syncthreads();
-    const float rep = a.repetition ? a.repetition[r] : 1.0f;
-    const float pres = a.presence ? a.presence[r] : 0.0f;
-    const float freq = a.frequency ? a.frequency[r] : 0.0f;
 #pragma unroll
     for (int k = 0; k < PIECES; ++k) {
       const uint4 c4 = *reinterpret_cast<const uint4*>(&s_tab[4 * (tid + k * THREADS)]);
@@ -138,10 +156,8 @@ __global__ void __launch_bounds__(THREADS) process_logits_kernel(const LogitArgs
         *reinterpret_cast<uint4*>(&s_tab[4 * (tid + k * THREADS)]) = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
     }
-    const int32_t* ids = a.bias_ids + (size_t)r * a.n_bias;
-    const float* values = a.bias_values + (size_t)r * a.n_bias;
     for (int i = tid; i < a.n_bias; i += THREADS) {
-      const uint32_t v = (uint32_t)ids[i] - (uint32_t)v0;
+      const uint32_t v = (uint32_t)(i == tid ? id0 : ids[i]) - (uint32_t)v0;
       if (v < (uint32_t)n) atomicMax(&s_tab[v], (uint32_t)i + 1u);
     }
     __syncthreads();
@@ -160,7 +176,7 @@ __global__ void __launch_bounds__(THREADS) process_logits_kernel(const LogitArgs
     const int i = 4 * (tid + k * THREADS);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (!((allowed[k] >> j) & 1u)) x[k][j] = a.fill;
+      if (!((allowed[k] >> ((v0 + i + j) & 31)) & 1u)) x[k][j] = a.fill;
     if (a.vec_out && i + 4 <= n) {
       *reinterpret_cast<float4*>(out + i) = make_float4(x[k][0], x[k][1], x[k][2], x[k][3]);
     } else {
