@@ -463,8 +463,8 @@ nvfp4_status nvfp4_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int
  * global scales: s = E4M3(max|x_block| / (6 * global)), code = E2M1(x /
  * (e4m3(s) * global)).  FP32 rows are first rounded to BF16 (RNE).
  * A slot of -1 skips its row (padding); a slot outside the cache skips it and
- * records device error bit 3.  Two rows of one call with the same slot give
- * either row's bytes (per 16 elements).
+ * records device error bit 3.  No two rows of a call may have the same slot
+ * (their bytes would mix).
  *   k, v     device, 16-byte aligned, strides multiples of 16 bytes
  *   dtype    NVFP4_DTYPE_*;  tokens >= 0
  */

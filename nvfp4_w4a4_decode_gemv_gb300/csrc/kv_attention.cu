@@ -67,18 +67,6 @@ NVFP4_DEVINL float ex2(float x) {
   return y;
 }
 
-// Four code bytes (two E2M1 codes each) -> four FP16 pairs.
-NVFP4_DEVINL void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-
 // Two E4M3 scale bytes -> an FP16 pair.
 NVFP4_DEVINL uint32_t e4m3x2_to_f16(uint32_t s) {
   uint32_t h;

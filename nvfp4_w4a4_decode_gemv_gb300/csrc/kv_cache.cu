@@ -1,10 +1,19 @@
 // Rows of K and V into the NVFP4 KV cache and back.
 //
-// Append: one thread per 16-element block (the unit of the format): 32 bytes
-// of BF16 in, 8 code bytes and a scale byte out, by the quantizer's own recipe
-// (quant_block), so a cached row has the codes nvfp4_quantize_act would give it
-// under the cache's global scale.  Bound by HBM: 2 bytes an element in, 9/16 out.
-// Read: the reverse, 8.5 bytes in, 32 bytes out a thread.
+// A 16-element block is the unit of work: 32 bytes of BF16, 8 code bytes and a
+// scale byte, by the quantizer's own recipe (quant_block), so a cached row has the
+// codes nvfp4_quantize_act would give it under the cache's global scale.  Bound by
+// HBM: 2 bytes an element on one side, 9/16 on the other.
+//
+// The cache's order scatters a token's bytes over its 16-token group, and writes
+// of 1, 4 and 8 bytes cost L2 a 32-byte sector each (one thread a block, every
+// block on its own: 12.3 M sectors for 16384 tokens of 8 heads, 50 us).  So a CTA
+// looks at a window of 16 tokens, and where a whole group's 16 tokens follow one
+// another (prompts), a warp takes the group's K or V half: it quantizes into
+// shared memory and moves the half in 16-byte pieces.  Other tokens (single new
+// tokens, the ragged ends of prompts) go block by block.
+#include <cuda_fp16.h>
+
 #include "kv_layout.cuh"
 #include "quant_block.cuh"
 
@@ -15,140 +24,334 @@ namespace {
 constexpr int kThreads = 256;
 
 struct AppendArgs {
-  const void* x[2];             // K, V
-  int64_t ts[2], hs[2];         // token and head strides in elements
+  const void *k, *v;
+  int64_t k_ts, k_hs, v_ts, v_hs;   // token and head strides in elements
   const int32_t* slots;
   uint8_t* pages;
-  const float* glob[2];
-  int tokens, heads, page_size;
+  const float *k_global, *v_global;
+  int tokens, heads, page_size, heads_per_cta;
   long long num_slots;
 };
 
-NVFP4_DEVINL void load16(const float* p, float (&v)[16]) {
+// Raw words of a block: 16 FP32 or BF16 elements.
+template <class T>
+struct Raw {
+  static constexpr int kPieces = sizeof(T) == 4 ? 4 : 2;
+  uint4 w[kPieces];
+  NVFP4_DEVINL void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 f = __ldcg(reinterpret_cast<const float4*>(p) + i);
-    const float r[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[4 * i + j] = __bfloat162float(__float2bfloat16_rn(r[j]));
+    for (int i = 0; i < kPieces; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];   // L1 keeps the sectors' other halves
   }
-}
-
-NVFP4_DEVINL void load16(const uint16_t* p, float (&v)[16]) {
+  NVFP4_DEVINL void values(float (&v)[16]) const {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[8 * i + 2 * j] = bf16_lo(w[j]);
-      v[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) {
+          v[4 * i + j] = __bfloat162float(__float2bfloat16_rn(__uint_as_float(u[j])));
+        } else {
+          v[8 * i + 2 * j] = bf16_lo(u[j]);
+          v[8 * i + 2 * j + 1] = bf16_hi(u[j]);
+        }
+      }
     }
   }
+};
+
+// quant_block's recipe, the same bits: s = E4M3(bm / (6 g)), S = dec(s) g, code = E2M1(RN(x / S)).  The quotient is
+// the correctly rounded one by Markstein's theorem (P. Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990): with y = RN(1/S) and p = RN(x y), RN(p + y RN(x - p S)) = RN(x / S) while
+// nothing underflows.  quant_block divides where x y is too close to a decision point to tell; with a global scale
+// that is a power of two BF16 values meet those points exactly, in some lane of nearly every warp.
+NVFP4_DEVINL uint32_t kv_quant_block(float (&v)[16], float g, uint2& codes) {
+  const float bm = block_absmax(v);
+  const float d = __fmul_rn(6.0f, g);
+  const float t = d > 0.0f ? __fdiv_rn(bm, d) : 0.0f;
+  const uint32_t s = f32x2_to_e4m3x2(0.0f, t) & 0xFFu;
+  float S = __fmul_rn(e4m3_to_f32(s), g);
+  if (!(S > 0x1p-80f && S < 0x1p80f)) {
+    // far out: the quotient of x f and S f, f a power of two, is the same (what x f loses below 2^-149 is far
+    // below the first decision point).  S = 0 gives f = 0: zeros
+    const float f = S == 0.0f ? 0.0f : S < 1.0f ? 0x1p100f : 0x1p-100f;
+    S *= f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= f;
+  }
+  const float y = S != 0.0f ? __frcp_rn(S) : 0.0f;
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = v[8 * h + i], p = __fmul_rn(x, y);
+      q[i] = copysignf(__fmaf_rn(__fmaf_rn(-p, S, x), y, p), x);   // a zero keeps its sign
+    }
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w[h])
+        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  }
+  codes = make_uint2(w[0], w[1]);
+  return s;
 }
 
-// Item = ((token * heads + head) * 2 + {K, V}) * (D / 16) + block.
-template <int D, class T>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a) {
+// ---- a window of 16 tokens --------------------------------------------------------
+enum : uint8_t { kAlone, kLeads, kCovered, kNothing };   // by itself; first of a whole group; in one; padding or bad
+
+struct Window {
+  int slot[48];                 // of tokens i0 - 16 .. i0 + 31
+  uint8_t kind[16];             // of tokens i0 .. i0 + 15
+};
+
+// Fills `w` (a barrier inside, one after it is the caller's).
+NVFP4_DEVINL void look_at_window(Window& w, const int32_t* slots, int tokens, long long i0, long long num_slots, bool report) {
+  const int tid = threadIdx.x;
+  if (tid < 48) {
+    const long long i = i0 - 16 + tid;
+    w.slot[tid] = i >= 0 && i < tokens ? slots[i] : -1;
+  }
+  __syncthreads();
+  if (tid < 16) {
+    const int s = w.slot[16 + tid];
+    uint8_t kind = kAlone;
+    if (s < 0 || s >= num_slots) {
+      kind = kNothing;
+      if (s != -1 && report) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
+    } else {
+      const int t = s % kKvGroup;
+      bool whole = true;
+#pragma unroll
+      for (int j = 0; j < kKvGroup; ++j) whole = whole && w.slot[16 + tid - t + j] == s - t + j;
+      if (whole) kind = t == 0 ? kLeads : kCovered;
+    }
+    w.kind[tid] = kind;
+  }
+}
+
+template <int D>
+struct Map {
   using L = KvLayout<D>;
+  static constexpr int kHalf = 9 * D;                     // bytes of a group's K or V half
+  static constexpr int kPerPass = 32 / L::kBlocks;        // tokens a warp has a block each of
+  static constexpr int kPasses = kKvGroup / kPerPass;
+  // offsets in the half
+  static NVFP4_DEVINL int codes(int which, int t, int b, int h) {
+    return which == 0 ? L::k_codes(t, b) + 4 * h : L::v_codes(t, b, h) - kHalf;
+  }
+  static NVFP4_DEVINL int scale(int which, int t, int b) { return which == 0 ? L::k_scale(t, b) : L::v_scale(t, b) - kHalf; }
+};
+
+// One block of a token on its own.
+template <int D, class T>
+NVFP4_DEVINL void append_block(const AppendArgs& a, long long token, int slot, int head, int which, int b) {
+  using M = Map<D>;
+  Raw<T> raw;
+  raw.load(which == 0 ? static_cast<const T*>(a.k) + token * a.k_ts + head * a.k_hs + b * 16
+                      : static_cast<const T*>(a.v) + token * a.v_ts + head * a.v_hs + b * 16);
+  const int page = slot / a.page_size, in = slot - page * a.page_size, t = slot % kKvGroup;
+  float v[16];
+  raw.values(v);
+  uint2 c;
+  const uint32_t s = kv_quant_block(v, __ldg(which == 0 ? a.k_global : a.v_global), c);
+  uint8_t* g = a.pages + kv_group_offset<D>(page, in, head, a.page_size, a.heads) + which * M::kHalf;
+  *reinterpret_cast<uint32_t*>(g + M::codes(which, t, b, 0)) = c.x;
+  *reinterpret_cast<uint32_t*>(g + M::codes(which, t, b, 1)) = c.y;
+  g[M::scale(which, t, b)] = (uint8_t)s;
+}
+
+constexpr int kWarps = kThreads / 32;
+
+// grid: (windows, head groups of a.heads_per_cta)
+template <int D, class T>
+__global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const AppendArgs a) {
+  using M = Map<D>;
+  __shared__ Window w;
+  __shared__ __align__(16) uint8_t s_half[kWarps][M::kHalf];
   griddep_launch_dependents();
   griddep_wait();
-  const long long items = (long long)a.tokens * a.heads * 2 * L::kBlocks;
-  for (long long it = (long long)blockIdx.x * kThreads + threadIdx.x; it < items; it += (long long)gridDim.x * kThreads) {
-    const int b = (int)(it % L::kBlocks);
-    const int which = (int)(it / L::kBlocks & 1);
-    const long long th = it / (2 * L::kBlocks);
-    const int token = (int)(th / a.heads), head = (int)(th - (long long)token * a.heads);
-    const int slot = a.slots[token];
-    if (slot == -1) continue;
-    if (slot < 0 || slot >= a.num_slots) {
-      atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
-      continue;
-    }
-    float v[16];
-    load16(static_cast<const T*>(a.x[which]) + token * a.ts[which] + head * a.hs[which] + b * 16, v);
-    uint2 codes;
-    const uint32_t s = quant_block(v, block_absmax(v), __ldg(a.glob[which]), codes);
-    uint8_t* g = a.pages + kv_group_offset<D>(slot / a.page_size, slot % a.page_size, head, a.page_size, a.heads);
-    const int t = slot % kKvGroup;
-    if (which == 0) {
-      *reinterpret_cast<uint2*>(g + L::k_codes(t, b)) = codes;
-      g[L::k_scale(t, b)] = (uint8_t)s;
-    } else {
-      *reinterpret_cast<uint32_t*>(g + L::v_codes(t, b, 0)) = codes.x;
-      *reinterpret_cast<uint32_t*>(g + L::v_codes(t, b, 1)) = codes.y;
-      g[L::v_scale(t, b)] = (uint8_t)s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long i0 = (long long)blockIdx.x * kKvGroup;
+  const int h0 = blockIdx.y * a.heads_per_cta, nh = min(a.heads_per_cta, a.heads - h0);
+  look_at_window(w, a.slots, a.tokens, i0, a.num_slots, blockIdx.y == 0);
+  __syncthreads();
+  const float k_glob = __ldg(a.k_global), v_glob = __ldg(a.v_global);
+  const uint8_t kind = w.kind[lane & 15];
+  const uint32_t alone = __ballot_sync(0xffffffffu, kind == kAlone);
+  for (uint32_t lead = __ballot_sync(0xffffffffu, lane < 16 && kind == kLeads); lead != 0u; lead &= lead - 1u) {
+    const int k = __ffs(lead) - 1;
+    const long long token = i0 + k;
+    const int slot = w.slot[16 + k], page = slot / a.page_size, in = slot - page * a.page_size;
+    for (int task = warp; task < 2 * nh; task += kWarps) {
+      const int which = task & 1, head = h0 + (task >> 1);
+      const int b = lane % KvLayout<D>::kBlocks, t_lane = lane / KvLayout<D>::kBlocks;
+      const int64_t ts = which == 0 ? a.k_ts : a.v_ts;
+      const T* x = (which == 0 ? static_cast<const T*>(a.k) + head * a.k_hs : static_cast<const T*>(a.v) + head * a.v_hs) +
+                   token * ts + b * 16;
+      Raw<T> raw[M::kPasses];
+#pragma unroll
+      for (int p = 0; p < M::kPasses; ++p) raw[p].load(x + (p * M::kPerPass + t_lane) * ts);
+#pragma unroll
+      for (int p = 0; p < M::kPasses; ++p) {
+        const int t = p * M::kPerPass + t_lane;
+        float v[16];
+        raw[p].values(v);
+        uint2 c;
+        const uint32_t s = kv_quant_block(v, which == 0 ? k_glob : v_glob, c);
+        *reinterpret_cast<uint32_t*>(&s_half[warp][M::codes(which, t, b, 0)]) = c.x;
+        *reinterpret_cast<uint32_t*>(&s_half[warp][M::codes(which, t, b, 1)]) = c.y;
+        s_half[warp][M::scale(which, t, b)] = (uint8_t)s;
+      }
+      __syncwarp();
+      uint8_t* g = a.pages + kv_group_offset<D>(page, in, head, a.page_size, a.heads) + which * M::kHalf;
+      for (int i = lane; i < M::kHalf / 16; i += 32)
+        reinterpret_cast<uint4*>(g)[i] = reinterpret_cast<const uint4*>(s_half[warp])[i];
+      __syncwarp();
     }
   }
+  if (alone == 0u) return;
+  // the other tokens, block by block
+  const int items = kKvGroup * nh * 2 * KvLayout<D>::kBlocks;
+  for (int it = threadIdx.x; it < items; it += kThreads) {
+    const int b = it % KvLayout<D>::kBlocks, which = it / KvLayout<D>::kBlocks & 1, th = it / (2 * KvLayout<D>::kBlocks);
+    const int k = th % kKvGroup;
+    if (w.kind[k] == kAlone) append_block<D, T>(a, i0 + k, w.slot[16 + k], h0 + th / kKvGroup, which, b);
+  }
+}
+
+// Few tokens: a thread for every block, no look at the neighbours.  grid.y: tokens.
+template <int D, class T>
+__global__ void __launch_bounds__(kThreads) kv_append_few_kernel(const AppendArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int it = blockIdx.x * kThreads + threadIdx.x;
+  const int b = it % KvLayout<D>::kBlocks, which = it / KvLayout<D>::kBlocks & 1, head = it / (2 * KvLayout<D>::kBlocks);
+  if (head >= a.heads) return;
+  const int slot = a.slots[blockIdx.y];
+  if (slot >= 0 && slot < a.num_slots) append_block<D, T>(a, blockIdx.y, slot, head, which, b);
+  else if (slot != -1) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
 }
 
 struct ReadArgs {
   const uint8_t* pages;
   const int32_t* slots;
-  const float* glob[2];
-  uint16_t* out[2];
-  int tokens, heads, page_size;
+  const float *k_global, *v_global;
+  uint16_t *k_out, *v_out;
+  int tokens, heads, page_size, heads_per_cta;
   long long num_slots;
 };
 
-// E2M1 code (4 bits) -> float: the three low bits at FP32 bits 24..22 are 2^-126 times the magnitude, exactly
-// (also for the subnormal code 1); the multiply by 2^126 is exact.
-NVFP4_DEVINL float e2m1_to_f32(uint32_t c) {
-  return __uint_as_float(__float_as_uint(__fmul_rn(__uint_as_float((c & 7u) << 22), 0x1p126f)) | ((c & 8u) << 28));
+// 4 code bytes times S -> 8 BF16 values, 16 bytes.
+NVFP4_DEVINL uint4 half_block(uint32_t c, float S) {
+  uint32_t f[4], w[4];
+  e2m1x8_to_f16(c, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f[i]));
+    const __nv_bfloat162 p = __floats2bfloat162_rn(__fmul_rn(x.x, S), __fmul_rn(x.y, S));
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Half a block (h 0, 1) of a token on its own; slot -1: zeros.
+template <int D>
+NVFP4_DEVINL void read_half(const ReadArgs& a, long long token, int slot, int head, int which, int b, int h) {
+  using M = Map<D>;
+  uint32_t c = 0u;
+  float S = 0.0f;
+  if (slot >= 0) {
+    const int page = slot / a.page_size, in = slot - page * a.page_size, t = slot % kKvGroup;
+    const uint8_t* g = a.pages + kv_group_offset<D>(page, in, head, a.page_size, a.heads) + which * M::kHalf;
+    c = __ldcg(reinterpret_cast<const uint32_t*>(g + M::codes(which, t, b, h)));
+    S = __fmul_rn(e4m3_to_f32(__ldcg(g + M::scale(which, t, b))), __ldg(which == 0 ? a.k_global : a.v_global));
+  }
+  *reinterpret_cast<uint4*>((which == 0 ? a.k_out : a.v_out) + (token * a.heads + head) * D + b * 16 + h * 8) =
+      half_block(c, S);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadArgs a) {
-  using L = KvLayout<D>;
+__global__ void __launch_bounds__(kThreads, 4) kv_read_kernel(const ReadArgs a) {
+  using M = Map<D>;
+  __shared__ Window w;
+  __shared__ __align__(16) uint8_t s_half[kWarps][M::kHalf];
   griddep_launch_dependents();
   griddep_wait();
-  const long long items = (long long)a.tokens * a.heads * 2 * L::kBlocks;
-  for (long long it = (long long)blockIdx.x * kThreads + threadIdx.x; it < items; it += (long long)gridDim.x * kThreads) {
-    const int b = (int)(it % L::kBlocks);
-    const int which = (int)(it / L::kBlocks & 1);
-    const long long th = it / (2 * L::kBlocks);
-    const int token = (int)(th / a.heads), head = (int)(th - (long long)token * a.heads);
-    const int slot = a.slots[token];
-    uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-    if (slot >= 0 && slot < a.num_slots) {
-      const uint8_t* g = a.pages + kv_group_offset<D>(slot / a.page_size, slot % a.page_size, head, a.page_size, a.heads);
-      const int t = slot % kKvGroup;
-      uint2 c;
-      uint32_t s;
-      if (which == 0) {
-        c = __ldcg(reinterpret_cast<const uint2*>(g + L::k_codes(t, b)));
-        s = __ldcg(g + L::k_scale(t, b));
-      } else {
-        c.x = __ldcg(reinterpret_cast<const uint32_t*>(g + L::v_codes(t, b, 0)));
-        c.y = __ldcg(reinterpret_cast<const uint32_t*>(g + L::v_codes(t, b, 1)));
-        s = __ldcg(g + L::v_scale(t, b));
-      }
-      const float S = __fmul_rn(e4m3_to_f32(s), __ldg(a.glob[which]));
-      uint32_t w[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long i0 = (long long)blockIdx.x * kKvGroup;
+  const int h0 = blockIdx.y * a.heads_per_cta, nh = min(a.heads_per_cta, a.heads - h0);
+  look_at_window(w, a.slots, a.tokens, i0, a.num_slots, blockIdx.y == 0);
+  __syncthreads();
+  const float k_glob = __ldg(a.k_global), v_glob = __ldg(a.v_global);
+  const uint8_t kind = w.kind[lane & 15];
+  // tokens outside whole groups, padding among them (zeros)
+  const uint32_t other = __ballot_sync(0xffffffffu, i0 + (lane & 15) < a.tokens && (kind == kAlone || kind == kNothing));
+  for (uint32_t lead = __ballot_sync(0xffffffffu, lane < 16 && kind == kLeads); lead != 0u; lead &= lead - 1u) {
+    const int k = __ffs(lead) - 1;
+    const int slot = w.slot[16 + k], page = slot / a.page_size, in = slot - page * a.page_size;
+    for (int task = warp; task < 2 * nh; task += kWarps) {
+      const int which = task & 1, head = h0 + (task >> 1);
+      const uint8_t* g = a.pages + kv_group_offset<D>(page, in, head, a.page_size, a.heads) + which * M::kHalf;
+      for (int i = lane; i < M::kHalf / 16; i += 32)
+        reinterpret_cast<uint4*>(s_half[warp])[i] = __ldcg(reinterpret_cast<const uint4*>(g) + i);
+      __syncwarp();
+      // a lane takes half a block, so that a store of the warp is whole rows
+      constexpr int kHalves = 2 * KvLayout<D>::kBlocks, kTokens = 32 / kHalves;
+      const int hb = lane % kHalves, b = hb >> 1, h = hb & 1;
+      uint16_t* out = (which == 0 ? a.k_out : a.v_out) + ((i0 + k) * a.heads + head) * D + hb * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t byte = ((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xFFu;
-        const __nv_bfloat162 p = __floats2bfloat162_rn(__fmul_rn(e2m1_to_f32(byte & 15u), S),
-                                                       __fmul_rn(e2m1_to_f32(byte >> 4), S));
-        w[i] = *reinterpret_cast<const uint32_t*>(&p);
+      for (int p = 0; p < kKvGroup / kTokens; ++p) {
+        const int t = p * kTokens + lane / kHalves;
+        const uint32_t c = *reinterpret_cast<const uint32_t*>(&s_half[warp][M::codes(which, t, b, h)]);
+        const float S = __fmul_rn(e4m3_to_f32(s_half[warp][M::scale(which, t, b)]), which == 0 ? k_glob : v_glob);
+        *reinterpret_cast<uint4*>(out + (long long)t * a.heads * D) = half_block(c, S);
       }
-      o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      o[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else if (slot != -1) {
-      atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
+      __syncwarp();
     }
-    uint4* out = reinterpret_cast<uint4*>(a.out[which] + th * D + b * 16);
-    out[0] = o[0];
-    out[1] = o[1];
+  }
+  if (other == 0u) return;
+  const int items = kKvGroup * nh * 4 * KvLayout<D>::kBlocks;
+  for (int it = threadIdx.x; it < items; it += kThreads) {
+    const int hb = it % (2 * KvLayout<D>::kBlocks), which = it / (2 * KvLayout<D>::kBlocks) & 1;
+    const int th = it / (4 * KvLayout<D>::kBlocks), k = th % kKvGroup;
+    if (i0 + k < a.tokens && (w.kind[k] == kAlone || w.kind[k] == kNothing))
+      read_half<D>(a, i0 + k, w.kind[k] == kAlone ? w.slot[16 + k] : -1, h0 + th / kKvGroup, which, hb >> 1, hb & 1);
   }
 }
 
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv_read_few_kernel(const ReadArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int it = blockIdx.x * kThreads + threadIdx.x;
+  const int hb = it % (2 * KvLayout<D>::kBlocks), which = it / (2 * KvLayout<D>::kBlocks) & 1;
+  const int head = it / (4 * KvLayout<D>::kBlocks);
+  if (head >= a.heads) return;
+  int slot = a.slots[blockIdx.y];
+  if (slot < 0 || slot >= a.num_slots) {
+    if (slot != -1) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
+    slot = -1;
+  }
+  read_half<D>(a, blockIdx.y, slot, head, which, hb >> 1, hb & 1);
+}
+
+// Up to kFew threads every (half) block gets its own at once, and the shorter chain of loads wins.  per_token: the
+// (half) blocks of a token.
+constexpr long long kFew = 1 << 16;
+
 template <class Args>
-cudaError_t launch(void (*kern)(Args), long long items, const Args& a, cudaStream_t stream) {
-  long long grid = (items + kThreads - 1) / kThreads;
-  if (grid > 1 << 20) grid = 1 << 20;
+cudaError_t launch(void (*window)(Args), void (*few)(Args), Args a, int per_token, cudaStream_t stream) {
+  const int windows = (a.tokens + kKvGroup - 1) / kKvGroup;
+  const bool is_few = (long long)a.tokens * per_token <= kFew && a.tokens <= 65535;
+  a.heads_per_cta = 4;                    // a warp for each half
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = is_few ? dim3((unsigned)((per_token + kThreads - 1) / kThreads), (unsigned)a.tokens)
+                       : dim3((unsigned)windows, (unsigned)((a.heads + 3) / 4));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -156,7 +359,7 @@ cudaError_t launch(void (*kern)(Args), long long items, const Args& a, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return cudaLaunchKernelEx(&cfg, is_few ? few : window, a);
 }
 
 }  // namespace
@@ -198,22 +401,21 @@ extern "C" nvfp4_status nvfp4_kv_append(const void* k, const void* v, int dtype,
   const nvfp4_status ds = nvfp4_internal_check_device();
   if (ds != NVFP4_OK) return ds;
   AppendArgs a = {};
-  a.x[0] = k, a.x[1] = v;
-  a.ts[0] = k_token_stride, a.ts[1] = v_token_stride;
-  a.hs[0] = k_head_stride, a.hs[1] = v_head_stride;
+  a.k = k, a.v = v;
+  a.k_ts = k_token_stride, a.k_hs = k_head_stride;
+  a.v_ts = v_token_stride, a.v_hs = v_head_stride;
   a.slots = slots;
   a.pages = cache->pages;
-  a.glob[0] = cache->k_global, a.glob[1] = cache->v_global;
+  a.k_global = cache->k_global, a.v_global = cache->v_global;
   a.tokens = tokens, a.heads = cache->kv_heads, a.page_size = cache->page_size;
   a.num_slots = (long long)cache->num_pages * cache->page_size;
-  const long long items = (long long)tokens * a.heads * 2 * (cache->head_dim / 16);
   cudaError_t e;
   if (cache->head_dim == 128)
-    e = dtype == NVFP4_DTYPE_F32 ? launch(kv_append_kernel<128, float>, items, a, stream)
-                                 : launch(kv_append_kernel<128, uint16_t>, items, a, stream);
+    e = dtype == NVFP4_DTYPE_F32 ? launch(kv_append_kernel<128, float>, kv_append_few_kernel<128, float>, a, a.heads * 128 / 8, stream)
+                                 : launch(kv_append_kernel<128, uint16_t>, kv_append_few_kernel<128, uint16_t>, a, a.heads * 128 / 8, stream);
   else
-    e = dtype == NVFP4_DTYPE_F32 ? launch(kv_append_kernel<64, float>, items, a, stream)
-                                 : launch(kv_append_kernel<64, uint16_t>, items, a, stream);
+    e = dtype == NVFP4_DTYPE_F32 ? launch(kv_append_kernel<64, float>, kv_append_few_kernel<64, float>, a, a.heads * 64 / 8, stream)
+                                 : launch(kv_append_kernel<64, uint16_t>, kv_append_few_kernel<64, uint16_t>, a, a.heads * 64 / 8, stream);
   return nvfp4_internal_cuda_status(e);
 }
 
@@ -231,12 +433,11 @@ extern "C" nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int32_t
   ReadArgs a = {};
   a.pages = cache->pages;
   a.slots = slots;
-  a.glob[0] = cache->k_global, a.glob[1] = cache->v_global;
-  a.out[0] = k_out, a.out[1] = v_out;
+  a.k_global = cache->k_global, a.v_global = cache->v_global;
+  a.k_out = k_out, a.v_out = v_out;
   a.tokens = tokens, a.heads = cache->kv_heads, a.page_size = cache->page_size;
   a.num_slots = (long long)cache->num_pages * cache->page_size;
-  const long long items = (long long)tokens * a.heads * 2 * (cache->head_dim / 16);
-  const cudaError_t e = cache->head_dim == 128 ? launch(kv_read_kernel<128>, items, a, stream)
-                                               : launch(kv_read_kernel<64>, items, a, stream);
+  const cudaError_t e = cache->head_dim == 128 ? launch(kv_read_kernel<128>, kv_read_few_kernel<128>, a, a.heads * 128 / 4, stream)
+                                               : launch(kv_read_kernel<64>, kv_read_few_kernel<64>, a, a.heads * 64 / 4, stream);
   return nvfp4_internal_cuda_status(e);
 }

@@ -47,5 +47,17 @@ NVFP4_DEVINL size_t kv_group_offset(int page, int in, int head, int page_size, i
   return (((size_t)page * kv_heads + head) * (page_size / kKvGroup) + in / kKvGroup) * KvLayout<D>::kGroupBytes;
 }
 
+// Four code bytes (two E2M1 codes each) -> four FP16 pairs.
+NVFP4_DEVINL void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
 // Host: the checks of an nvfp4_kv_cache descriptor that every entry point makes.
 nvfp4_status nvfp4_internal_check_kv_cache(const nvfp4_kv_cache* c);
