@@ -9,6 +9,7 @@ cudaError_t nvfp4_internal_read_error_reset(unsigned int* out);
 cudaError_t nvfp4_internal_read_error_gemm(unsigned int* out);
 cudaError_t nvfp4_internal_read_error_kv_cache(unsigned int* out);
 cudaError_t nvfp4_internal_read_error_kv_attention(unsigned int* out);
+cudaError_t nvfp4_internal_read_error_kv_attention_tc(unsigned int* out);
 
 namespace {
 thread_local char g_last_cuda_error[256] = "no CUDA error";
@@ -67,5 +68,6 @@ extern "C" nvfp4_status nvfp4_device_status(unsigned int* code) {
   if (e == cudaSuccess) e = nvfp4_internal_read_error_gemm(code);
   if (e == cudaSuccess) e = nvfp4_internal_read_error_kv_cache(code);
   if (e == cudaSuccess) e = nvfp4_internal_read_error_kv_attention(code);
+  if (e == cudaSuccess) e = nvfp4_internal_read_error_kv_attention_tc(code);
   return nvfp4_internal_cuda_status(e);
 }

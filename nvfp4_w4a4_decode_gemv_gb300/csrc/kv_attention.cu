@@ -31,7 +31,7 @@
 // every time) and resets the counter.  Nothing waits for another CTA.
 #include <math.h>
 
-#include "kv_layout.cuh"
+#include "kv_attention.cuh"
 #include "tcgen05.cuh"
 
 NVFP4_DEFINE_ERROR_READER(nvfp4_internal_read_error_kv_attention)
@@ -40,51 +40,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxCtas = 640;
 constexpr int kMaxSplits = 32;          // pieces of a segment when there are few: more cost more to merge than they save
 constexpr int kMaxShares = 64;          // the same bound where there are many
+constexpr int kTcRows = 64;             // more query rows of a kv head than this take the other kernel (kv_attention_tc.cu)
 constexpr int kSegmentCost = 12;        // units that the fixed cost of a segment (queries, first copies, merge) stands for
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct AttnArgs {
-  const void* q;
-  int64_t q_ts, q_hs;
-  const uint8_t* pages;
-  const float *k_global, *v_global;
-  const int32_t *table, *kv_lens, *cu_q;
-  uint16_t* out;
-  float* lse;
-  unsigned int* counters;               // [kMaxCtas], zero between calls
-  float* records;                       // [2 kMaxCtas][rows][D + 2]
-  int tokens, heads, kv_heads, group, page_size, num_pages, width, batch, window;
-  float scale;
-};
-
-// ---- instructions ------------------------------------------------------------
-NVFP4_DEVINL float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Two E4M3 scale bytes -> an FP16 pair.
-NVFP4_DEVINL uint32_t e4m3x2_to_f16(uint32_t s) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)s));
-  return h;
-}
-
-NVFP4_DEVINL uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-NVFP4_DEVINL uint32_t pack_f16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 
 NVFP4_DEVINL uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
@@ -97,12 +56,6 @@ NVFP4_DEVINL void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
-NVFP4_DEVINL uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
-NVFP4_DEVINL uint2 lds64(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
-
-NVFP4_DEVINL float load_q(const float* p) { return __bfloat162float(__float2bfloat16_rn(*p)); }
-NVFP4_DEVINL float load_q(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 
 // ---- shapes --------------------------------------------------------------------
 template <int D, int NT>
@@ -126,34 +79,6 @@ struct Shape {
   static constexpr int kOffScan = kOffBar + kWarps * kStages * 8;         // 32 words for the split
   static constexpr int kSmem = (kOffScan + 32 * 8 + 15) / 16 * 16;
 };
-
-// ---- requests --------------------------------------------------------------------
-struct Request {
-  int first, rows, len;                 // query rows [first, first + rows), keys [0, len)
-  int begin;                            // first key that any row sees
-};
-
-NVFP4_DEVINL Request get_request(const AttnArgs& a, int b, bool report) {
-  Request r;
-  r.first = b;
-  r.rows = 1;
-  bool bad = false;
-  if (a.cu_q) {
-    r.first = a.cu_q[b];
-    const int last = a.cu_q[b + 1];
-    bad = r.first < 0 || last < r.first || last > a.tokens;
-    r.rows = bad ? 0 : last - r.first;
-  }
-  r.len = max(a.kv_lens[b], 0);
-  const long long most = (long long)a.width * a.page_size;
-  if (r.len > most) {
-    r.len = (int)most;
-    bad = true;
-  }
-  if (bad && report) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
-  r.begin = a.window > 0 ? (int)max((long long)r.len - r.rows - a.window + 1, 0ll) : 0;
-  return r;
-}
 
 // Units of a segment (one row tile of one kv head); at least one, so that rows without keys are written too.
 template <class S>
@@ -485,9 +410,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
       for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(v[i][e]));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-      int e = (int)(__float_as_uint(big) >> 23) - 127;
-      e = big > 0.0f ? min(max(e, -126), 126) : 0;
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+      float down, up;
+      power_of_two(big, down, up);
       uint8_t* sq = smem + S::kOffQ;
       const int cq = lane >> 3;
       if constexpr (D == 128) {
@@ -497,8 +421,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
         *reinterpret_cast<uint32_t*>(sq + (((row >> 3) * 4 + ((lane & 7) >> 1)) * 32 + (row & 7) * 4 + cq) * 8 +
                                      (lane & 1) * 4) = pack_f16(v[i][0] * down, v[i][1] * down);
       }
-      // never 0: a hidden score, -inf, times it has to stay -inf
-      if (lane == 0) s_f[row] = fmaxf(a.scale * kLog2e * kg * up, 1.2e-38f);
+      if (lane == 0) s_f[row] = score_factor(a.scale * kLog2e * kg * up);
     }
     __syncthreads();
 
@@ -744,8 +667,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
   }
 }
 
-constexpr size_t kCounterBytes = 4096;  // what a caller zeroes
-static_assert(kMaxCtas * 4 <= kCounterBytes, "the counters");
 
 // CTAs of a variant: as many as are resident at once.
 template <int D, int NT, class T>
@@ -835,7 +756,9 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens,
                       cache->kv_heads, group, cache->page_size, cache->num_pages, table_width, batch, window, scale};
   const int rows = cu_q ? (int)((long long)max_q * group < 1 << 20 ? max_q * group : 1 << 20) : group;
   cudaError_t e;
-  if (cache->head_dim == 128)
+  if (rows > kTcRows)
+    e = nvfp4_internal_kv_attention_tc(a, cache->head_dim, dtype, stream);
+  else if (cache->head_dim == 128)
     e = dtype == NVFP4_DTYPE_F32 ? dispatch<128, float>(a, rows, stream) : dispatch<128, uint16_t>(a, rows, stream);
   else
     e = dtype == NVFP4_DTYPE_F32 ? dispatch<64, float>(a, rows, stream) : dispatch<64, uint16_t>(a, rows, stream);

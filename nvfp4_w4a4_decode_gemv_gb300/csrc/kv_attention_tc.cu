@@ -1,0 +1,600 @@
+// Attention over the NVFP4 KV cache for many query rows a request (prompt
+// chunks), on the 5th-generation tensor cores:
+//   S = Q K^T,  P = 2^(f S - m),  O += P V,  out = O / sum P
+// for tiles of 128 query rows of one (request, kv head), 64 keys at a time.
+//
+// With R query rows a kv head a key costs 4 R D operations and 18 D / 16 bytes:
+// bound by the matrix units, by 128 x 64 exponentials a tile, and by shared memory
+// (128 bytes a cycle), which feeds them.  So only the dequantized keys and values
+// pass through shared memory; the queries (FP16 of q / 2^e, as in the decode
+// kernel) and the weights are operands in TMEM, where the scores and the output
+// are too:
+//   columns  S [0, 64), FP32; P over it in [0, 32), FP16;  O [64, 64 + D);  Q from 192.
+// K is stored as [token][D] (K-major operand), V as [token][D] too (an operand whose
+// rows are contiguous: no transposition on the way), both in 128-byte swizzled
+// panels of 64 elements.  256 TMEM columns and 92 KB of shared memory a CTA: two
+// CTAs an SM, one's exponentials under the other's products.
+//
+// Warps: 0-3 softmax (a thread a row), 4-7 dequantize (a 16-token group each),
+// 8 copies the cache's groups in, 9 issues the products.  The maximum that the
+// weights refer to moves only when a row's scores exceed it by 2^8 (then O is
+// rescaled in TMEM); up to there FP16 holds the weights as exactly as below 1.
+// Every wait is bounded and an abort flag ends the others (mbar_wait).
+// Tiles are handed out from a counter, the longest of a request first.
+#include <math.h>
+
+#include "kv_attention.cuh"
+#include "tcgen05.cuh"
+
+NVFP4_DEFINE_ERROR_READER(nvfp4_internal_read_error_kv_attention_tc)
+
+namespace {
+
+constexpr int kRows = 128;              // query rows of a tile
+constexpr int kKeys = 64;               // keys of a step
+constexpr int kGroups = kKeys / kKvGroup;
+constexpr int kRing = 3;                // raw steps in flight
+constexpr int kThreads = 320;
+constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kColS = 0, kColO = 64, kColQ = 192;
+constexpr uint32_t kSpinLimit = 1u << 22;  // polls of a wait (each suspends for a while): far beyond any step
+constexpr float kSlack = 8.0f;          // log2 units a score may exceed the maximum in use
+
+template <int D>
+struct Shape {
+  static constexpr int kRaw = kGroups * KvLayout<D>::kGroupBytes;
+  static constexpr int kPanel = kKeys * 128;              // 64 tokens x 64 elements
+  static constexpr int kTile = kKeys * D * 2;             // K or V of a step, FP16
+  static constexpr int kOffK = 0;                         // [2] steps
+  static constexpr int kOffV = 2 * kTile;                 // [2]
+  static constexpr int kOffRaw = 4 * kTile;               // [kRing]
+  static constexpr int kOffBar = kOffRaw + kRing * kRaw;
+  static constexpr int kBars = 2 * kRing + 2 + 2 + 3;
+  static constexpr int kOffWords = kOffBar + kBars * 8;   // TMEM address, abort flag, tile (4), groups present (kRing + 2)
+  static constexpr int kSmem = kOffWords + 16 * 4 + 1024; // + alignment of the swizzled panels
+  // instruction descriptors: FP32 accumulator, FP16 operands, M = 128; N = keys, and N = D with B's rows contiguous
+  static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+  static constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+};
+
+// D (+)= A . B^T with A in TMEM (two FP16 of the contraction to a column).
+NVFP4_DEVINL void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t db, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(db), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Operand whose rows (N) are contiguous, 128-byte swizzle: 64-element panels `panel` bytes apart, groups of 8
+// contraction indices 1024 bytes apart.
+NVFP4_DEVINL uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t panel) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+#define R4(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3])
+#define W4(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3])
+// 32 columns of this warp's lane quadrant; the loaded values may be used after tmem_wait_ld.
+NVFP4_DEVINL void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : R4(r, 0), R4(r, 4), R4(r, 8), R4(r, 12), R4(r, 16), R4(r, 20), R4(r, 24), R4(r, 28)
+      : "r"(taddr));
+}
+NVFP4_DEVINL void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::W4(r, 0),
+      W4(r, 4), W4(r, 8), W4(r, 12), W4(r, 16), W4(r, 20), W4(r, 24), W4(r, 28), "r"(taddr)
+      : "memory");
+}
+NVFP4_DEVINL void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::W4(r, 0),
+      W4(r, 4), W4(r, 8), W4(r, 12), "r"(taddr)
+      : "memory");
+}
+#undef R4
+#undef W4
+// The values pass through the wait, so that nothing uses them before it.
+NVFP4_DEVINL void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+NVFP4_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Waits for the phase of `bar` with this parity: bounded; false, and the abort flag up, when it gives up, or when
+// another wait has.
+NVFP4_DEVINL bool wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  for (uint32_t i = 0; i < kSpinLimit; ++i) {
+    if (mbar_try_wait(bar, parity & 1u)) return true;
+    if ((i & 1023u) == 1023u && *abort_flag) return false;
+  }
+  atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MBAR_TIMEOUT);
+  *abort_flag = 1u;
+  return false;
+}
+
+struct Tile {
+  int b, kvh, row0;
+};
+
+// Tile number t -> request, kv head and first row (b = -1: there is no such tile).  One warp; the requests are
+// summed 32 at a time.  The last rows of a request, which see most keys, come first.
+NVFP4_DEVINL Tile find_tile(const AttnArgs& a, long long t, int lane) {
+  long long before = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    int tiles = 0;
+    if (b0 + lane < a.batch) {
+      const Request r = get_request(a, b0 + lane, t == 0);
+      tiles = (int)(((long long)r.rows * a.group + kRows - 1) / kRows);
+    }
+    long long inc = (long long)tiles * a.kv_heads;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + inc > t);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      const int n = __shfl_sync(0xffffffffu, tiles, l);
+      const int i = (int)(t - before - (__shfl_sync(0xffffffffu, inc, l) - (long long)n * a.kv_heads));
+      return Tile{b0 + l, i % a.kv_heads, (n - 1 - i / a.kv_heads) * kRows};
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return Tile{-1, 0, 0};
+}
+
+// Dequantizes one 16-token group into rows [16 g, 16 g + 16) of the K and V tiles.  live: tokens that exist.
+template <int D>
+NVFP4_DEVINL void dequantize(const uint8_t* raw, uint8_t* k_tile, uint8_t* v_tile, int g, int live, int lane) {
+  using L = KvLayout<D>;
+  const int r = lane >> 2, c = lane & 3;
+  constexpr int kPanel = kKeys * 128;
+  // ---- K: lane (r, c) has D/4 elements of the tokens at pos r and r + 8
+  uint32_t sc[2][D / 64];
+  if constexpr (D == 128) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(raw + L::kOffKScale + lane * 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t h = e4m3x2_to_f16(w >> (16 * i));
+      sc[i][0] = __byte_perm(h, h, 0x1010);
+      sc[i][1] = __byte_perm(h, h, 0x3232);
+    }
+  } else {
+    const uint32_t h = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(raw + L::kOffKScale + lane * 2));
+    sc[0][0] = __byte_perm(h, h, 0x1010);
+    sc[1][0] = __byte_perm(h, h, 0x3232);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = g * kKvGroup + 4 * (r >> 1) + 2 * i + (r & 1);
+    const uint8_t* p = raw + (8 * i + r) * (D / 2) + c * (D / 8);
+    if constexpr (D == 128) {
+      // a word is an 8-element piece; lanes with c >= 2 (the second panel) take theirs in another order, so that
+      // the pieces a quarter warp stores together lie in different banks
+      uint4 v = lds128(p);
+      const bool swap = c >= 2;
+      const uint32_t w[4] = {swap ? v.z : v.x, swap ? v.w : v.y, swap ? v.x : v.z, swap ? v.y : v.w};
+      const uint32_t s_lo = swap ? sc[i][1] : sc[i][0], s_hi = swap ? sc[i][0] : sc[i][1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t h[4];
+        e2m1x8_to_f16(w[j], h);
+        const uint32_t s = j < 2 ? s_lo : s_hi;
+        const int piece = ((c & 1) * 4 + (j ^ (swap ? 2 : 0))) ^ (row & 7);
+        *reinterpret_cast<uint4*>(k_tile + (c >> 1) * kPanel + row * 128 + piece * 16) =
+            make_uint4(hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
+      }
+    } else {
+      const uint2 v = lds64(p);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t h[4];
+        e2m1x8_to_f16(j == 0 ? v.x : v.y, h);
+        const int piece = (2 * c + j) ^ (row & 7);
+        *reinterpret_cast<uint4*>(k_tile + row * 128 + piece * 16) =
+            make_uint4(hmul2(h[0], sc[i][0]), hmul2(h[1], sc[i][0]), hmul2(h[2], sc[i][0]), hmul2(h[3], sc[i][0]));
+      }
+    }
+  }
+  // ---- V: lane (r, c) has D/8 elements of tokens 4 c .. 4 c + 3
+  uint32_t sw = *reinterpret_cast<const uint32_t*>(raw + L::kOffVScale + (D == 128 ? r : r >> 1) * 16 + 4 * c);
+  const int mine = live - 4 * c;
+  if (mine < 4) sw &= mine > 0 ? (1u << (8 * mine)) - 1u : 0u;      // what lies behind the last key may be NaN
+  const uint32_t s01 = e4m3x2_to_f16(sw), s23 = e4m3x2_to_f16(sw >> 16);
+  const uint32_t vs[4] = {__byte_perm(s01, s01, 0x1010), __byte_perm(s01, s01, 0x3232), __byte_perm(s23, s23, 0x1010),
+                          __byte_perm(s23, s23, 0x3232)};
+  uint32_t x[4][D / 64];
+  if constexpr (D == 128) {
+    const uint8_t* q = raw + L::kOffV + (r >> 1) * 256 + (r & 1) * 64 + c * 16;
+    const uint4 v0 = lds128(q), v1 = lds128(q + 128);
+    const bool swap = c >= 2;             // as above
+    x[0][0] = swap ? v0.y : v0.x, x[0][1] = swap ? v0.x : v0.y, x[1][0] = swap ? v0.w : v0.z, x[1][1] = swap ? v0.z : v0.w;
+    x[2][0] = swap ? v1.y : v1.x, x[2][1] = swap ? v1.x : v1.y, x[3][0] = swap ? v1.w : v1.z, x[3][1] = swap ? v1.z : v1.w;
+  } else {
+    const uint4 v = lds128(raw + L::kOffV + r * 64 + c * 16);
+    x[0][0] = v.x, x[1][0] = v.y, x[2][0] = v.z, x[3][0] = v.w;
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int row = g * kKvGroup + 4 * c + t;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      uint32_t h[4];
+      e2m1x8_to_f16(x[t][j], h);
+      const int piece = D == 128 ? (((r & 3) * 2 + (j ^ (c >> 1))) ^ (row & 7)) : (r ^ (row & 7));
+      *reinterpret_cast<uint4*>(v_tile + (D == 128 ? (r >> 2) * kPanel : 0) + row * 128 + piece * 16) =
+          make_uint4(hmul2(h[0], vs[t]), hmul2(h[1], vs[t]), hmul2(h[2], vs[t]), hmul2(h[3], vs[t]));
+    }
+  }
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(kThreads, 2) kv_attention_tc_kernel(const AttnArgs a) {
+  using S = Shape<D>;
+  using L = KvLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
+  uint64_t *raw_full = bars, *raw_free = bars + kRing, *kv_full = bars + 2 * kRing, *kv_free = kv_full + 2;
+  uint64_t *s_full = kv_free + 2, *p_full = s_full + 1, *q_full = s_full + 2;
+  volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(smem + S::kOffWords);
+  volatile uint32_t* abort_flag = words + 1;
+  volatile int* s_tile = reinterpret_cast<volatile int*>(words + 2);
+  volatile uint32_t* raw_have = words + 6;              // [kRing] groups that a raw step brings
+  volatile uint32_t* kv_have = words + 6 + kRing;       // [2]
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_free[i], kGroups);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&kv_full[i], kGroups);
+      mbar_init(&kv_free[i], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 4);
+    mbar_init(q_full, 4);
+    *abort_flag = 0u;
+  }
+  fence_mbar_init();
+  griddep_wait();
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(const_cast<uint32_t*>(words))),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = words[0];
+  // only now: a dependent kernel that came first to the TMEM would wait for this one, and this one for it
+  griddep_launch_dependents();
+  const float kg = *a.k_global, vg = *a.v_global;
+  // steps of this CTA so far (they give ring slot, operand buffer and the parities of their barriers), tiles, and
+  // phases of s_full: a step's scores each, and a tile's output
+  uint32_t step = 0, tiles = 0, scores = 0;
+  uint32_t copied = 0;                                  // steps whose copies this warp has started
+
+  for (;;) {
+    if (warp == 0) {
+      long long t = 0;
+      if (lane == 0) t = atomicAdd(&a.counters[kTileCounter], 1u);
+      t = __shfl_sync(0xffffffffu, t, 0);
+      const Tile tile = find_tile(a, t, lane);
+      if (lane == 0) {
+        s_tile[0] = tile.b;
+        s_tile[1] = tile.kvh;
+        s_tile[2] = tile.row0;
+      }
+    }
+    __syncthreads();
+    const int b = s_tile[0], kvh = s_tile[1], row0 = s_tile[2];
+    if (b < 0) break;
+    const Request rq = get_request(a, b, false);
+    const int n_rows = (int)min((long long)kRows, (long long)rq.rows * a.group - row0);
+    const int hi_all = rq.len - rq.rows + row0 / a.group;       // as in the decode kernel
+    const int hi_any = rq.len - rq.rows + (row0 + n_rows - 1) / a.group;
+    const int lo_any = a.window > 0 ? max(hi_all - a.window + 1, 0) : 0;
+    const int lo_all = a.window > 0 ? max(hi_any - a.window + 1, 0) : 0;
+    const int step0 = lo_any / kKeys;
+    const int n = hi_any < 0 ? 0 : hi_any / kKeys + 1 - step0;  // steps of this tile
+
+    if (warp < 4) {
+      // ================ softmax: a thread a row ================
+      const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+      const int row = row0 + tid;
+      const bool mine = tid < n_rows;
+      const int tok = rq.first + row / a.group, head = kvh * a.group + row % a.group;
+      float f;
+      {
+        const T* q = static_cast<const T*>(a.q) + (mine ? tok * a.q_ts + head * a.q_hs : 0);
+        float big = 0.0f;
+        if (mine) {
+#pragma unroll 8
+          for (int i = 0; i < D; i += 4) {
+            float v[4];
+            load4(q + i, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) big = fmaxf(big, fabsf(v[j]));
+          }
+        }
+        float down, up;
+        power_of_two(big, down, up);
+        f = score_factor(a.scale * kLog2e * kg * up);
+#pragma unroll
+        for (int i = 0; i < D; i += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (mine) load4(q + i + j, v);
+            w[j / 2] = pack_f16(v[0] * down, v[1] * down);
+            w[j / 2 + 1] = pack_f16(v[2] * down, v[3] * down);
+          }
+          tmem_st16(tmem + kColQ + lanes + i / 2, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
+      const int pos = rq.len - rq.rows + row / a.group, low = a.window > 0 ? pos - a.window : -1;
+      float m = -INFINITY, l = 0.0f;
+      bool ok = true;
+      for (int k = 0; k < n && ok; ++k) {
+        ok = wait(s_full, scores + k, abort_flag);
+        tc_fence_after();
+        // the scores are read twice, 32 columns at a time: for the maximum, and for the weights (fewer registers)
+        const int t0 = (step0 + k) * kKeys;
+        const uint32_t have = kv_have[(step + k) & 1u];
+        const bool some = t0 + kKeys - 1 > hi_all || t0 < lo_all || have != (1u << kGroups) - 1u;
+        uint32_t s[32];
+        auto load_scores = [&](int h) {
+          tmem_ld32(tmem + kColS + lanes + 32 * h, s);
+          tmem_wait_ld(s);
+          if (some) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int t = t0 + 32 * h + j;
+              if (t > pos || t <= low || !((have >> ((32 * h + j) / kKvGroup)) & 1u)) s[j] = 0xFF800000u;   // -inf
+            }
+          }
+        };
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          load_scores(h);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(s[j]));
+        }
+        const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
+        float back = 1.0f;
+        if (mt > m + kSlack) {                          // (also the first finite one)
+          back = ex2(m - mt);
+          m = mt;
+          l *= back;
+        }
+        const float neg_m = m == -INFINITY ? 0.0f : -m;
+        float sum[2] = {0.0f, 0.0f};
+        uint32_t p[2][16];
+        auto weights = [&](int h) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float w0 = ex2(fmaf(__uint_as_float(s[j]), f, neg_m));
+            const float w1 = ex2(fmaf(__uint_as_float(s[j + 1]), f, neg_m));
+            sum[0] += w0;
+            sum[1] += w1;
+            p[h][j / 2] = pack_f16(w0, w1);
+          }
+        };
+        weights(1);                                     // still in registers
+        load_scores(0);
+        tmem_st16(tmem + kColS + lanes + 16, p[1]);     // over scores 16 .. 31, which are in registers now
+        weights(0);
+        tmem_st16(tmem + kColS + lanes, p[0]);
+        if (k > 0 && __any_sync(0xffffffffu, back != 1.0f)) {
+#pragma unroll 1
+          for (int i = 0; i < D; i += 32) {
+            uint32_t o[32];
+            tmem_ld32(tmem + kColO + lanes + i, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * back);
+            tmem_st32(tmem + kColO + lanes + i, o);
+          }
+        }
+        l += sum[0] + sum[1];
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+      }
+      // ---- the tile's output (its last product's commit is one more phase of s_full)
+      if (n > 0 && ok) wait(s_full, scores + n, abort_flag);
+      tc_fence_after();
+      const float inv = l > 0.0f ? vg / l : 0.0f;
+      uint16_t* out = a.out + ((size_t)tok * a.heads + head) * D;
+#pragma unroll 1
+      for (int i = 0; i < D; i += 32) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32(tmem + kColO + lanes + i, o);
+          tmem_wait_ld(o);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0u;
+        }
+        if (mine) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // a row without keys has sums of zeros, or of what other rows' keys left: its weights were 0
+              const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(o[j + 2 * e]) * inv,
+                                                             __uint_as_float(o[j + 2 * e + 1]) * inv);
+              w[e] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            *reinterpret_cast<uint4*>(out + i + j) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (mine && a.lse) a.lse[(size_t)tok * a.heads + head] = l > 0.0f ? (m + log2f(l)) / kLog2e : -INFINITY;
+      tc_fence_before();
+    } else if (warp < 8) {
+      // ================ dequantize: a group a warp ================
+      const int g = warp - 4;
+      bool ok = true;
+      for (int k = 0; k < n && ok; ++k) {
+        const uint32_t i = step + k, slot = i % kRing, buf = i & 1u;
+        ok = wait(&raw_full[slot], i / kRing, abort_flag);
+        const uint32_t have = raw_have[slot];
+        // the operand buffer's previous step has been multiplied
+        if (i >= 2) ok = wait(&kv_free[buf], i / 2 - 1, abort_flag) && ok;
+        const int t0 = (step0 + k) * kKeys + g * kKvGroup;
+        const int live = ((have >> g) & 1u) ? min(max(rq.len - t0, 0), kKvGroup) : 0;
+        dequantize<D>(smem + S::kOffRaw + slot * S::kRaw + g * L::kGroupBytes, smem + S::kOffK + buf * S::kTile,
+                      smem + S::kOffV + buf * S::kTile, g, live, lane);
+        if (g == 0 && lane == 0) kv_have[buf] = have;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_free[slot]);
+          mbar_arrive(&kv_full[buf]);
+        }
+      }
+    } else if (warp == 8) {
+      // ================ copies ================
+      const int32_t* trow = a.table + (size_t)b * a.width;
+      const uint8_t* src_head = a.pages + (size_t)kvh * (a.page_size / kKvGroup) * L::kGroupBytes;
+      const size_t page_bytes = (size_t)a.kv_heads * (a.page_size / kKvGroup) * L::kGroupBytes;
+      bool ok = true;
+      for (int k = 0; k < n && ok; ++k) {
+        const uint32_t i = step + k, slot = i % kRing;
+        // lane g < kGroups: the page of group g (-1: not there, or not to be read)
+        const int t0 = (step0 + k) * kKeys + lane * kKvGroup;
+        int page = -1;
+        if (lane < kGroups && t0 <= hi_any && t0 + kKvGroup > lo_any) {
+          page = trow[t0 / a.page_size];
+          if (page < 0 || page >= a.num_pages) {
+            page = -1;
+            atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
+          }
+        }
+        if (i >= kRing) ok = wait(&raw_free[slot], i / kRing - 1, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+        if (lane == 0) {
+          raw_have[slot] = have;
+          mbar_arrive_expect_tx(&raw_full[slot], __popc(have) * L::kGroupBytes);
+        }
+        __syncwarp();
+        if (page >= 0)
+          bulk_g2s(smem + S::kOffRaw + slot * S::kRaw + lane * L::kGroupBytes,
+                   src_head + page * page_bytes + (t0 % a.page_size / kKvGroup) * L::kGroupBytes, L::kGroupBytes,
+                   &raw_full[slot]);
+        copied = i + 1;
+      }
+    } else if (lane == 0) {
+      // ================ products ================
+      bool ok = wait(q_full, tiles, abort_flag);
+      tc_fence_after();
+      for (int k = 0; k < n && ok; ++k) {
+        const uint32_t i = step + k, buf = i & 1u;
+        ok = wait(&kv_full[buf], i / 2, abort_flag);
+        // the last step's output product reads its weights where this step's scores will stand
+        if (k > 0) ok = wait(&kv_free[(i - 1) & 1u], (i - 1) / 2, abort_flag) && ok;
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t kt = smem_u32(smem + S::kOffK + buf * S::kTile), vt = smem_u32(smem + S::kOffV + buf * S::kTile);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+          mma_f16_ta(tmem + kColS, tmem + kColQ + 8 * j, smem_desc_sw128(kt + (j >> 2) * S::kPanel + (j & 3) * 32), S::kIdescS,
+                     j > 0 ? 1u : 0u);
+        mma_commit(s_full);
+        ok = wait(p_full, i, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < kKeys / 16; ++j)
+          mma_f16_ta(tmem + kColO, tmem + kColS + 8 * j, smem_desc_mn_sw128(vt + j * 2048, S::kPanel), S::kIdescO,
+                     (k > 0 || j > 0) ? 1u : 0u);
+        mma_commit(&kv_free[buf]);
+        if (k == n - 1) mma_commit(s_full);
+      }
+    }
+    step += (uint32_t)n;
+    scores += n > 0 ? (uint32_t)n + 1u : 0u;
+    ++tiles;
+    __syncthreads();                                    // the tile's numbers and the TMEM are free again
+    if (*abort_flag) break;
+  }
+  if (*abort_flag && warp == 8) {
+    // copies may still be in flight after a wait has given up: let every started one land (bounded)
+    for (uint32_t i = copied > kRing ? copied - kRing : 0u; i < copied; ++i)
+      for (uint32_t j = 0; j < (1u << 16); ++j)
+        if (mbar_try_wait(&raw_full[i % kRing], (i / kRing) & 1u)) break;
+  }
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+  }
+  // the last CTA to leave resets the tile counter
+  if (tid == 0) {
+    __threadfence();
+    if (atomicAdd(&a.counters[kTileCounter + 1], 1u) == gridDim.x - 1u) {
+      a.counters[kTileCounter] = 0u;
+      a.counters[kTileCounter + 1] = 0u;
+    }
+  }
+}
+
+template <int D, class T>
+cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
+  using S = Shape<D>;
+  static PerDeviceInt grid_cache;
+  cudaError_t err = cudaSuccess;
+  const int grid = grid_cache.get([](int dev, cudaError_t* e_out) -> int {
+    int sms = 0;
+    cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kv_attention_tc_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) {
+      *e_out = e;
+      return 0;
+    }
+    return 2 * (sms > 0 ? sms : 1);
+  }, &err);
+  if (grid == 0) return err;
+  const long long most = ((long long)a.tokens * a.group / kRows + a.batch) * a.kv_heads;   // tiles there can be
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(most < grid ? most : grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_attention_tc_kernel<D, T>, a);
+}
+
+}  // namespace
+
+cudaError_t nvfp4_internal_kv_attention_tc(const AttnArgs& a, int head_dim, int dtype, cudaStream_t stream) {
+  if (head_dim == 128)
+    return dtype == NVFP4_DTYPE_F32 ? launch<128, float>(a, stream) : launch<128, uint16_t>(a, stream);
+  return dtype == NVFP4_DTYPE_F32 ? launch<64, float>(a, stream) : launch<64, uint16_t>(a, stream);
+}
