@@ -1,25 +1,27 @@
 // Attention over the NVFP4 KV cache for many query rows a request (prompt
 // chunks), on the 5th-generation tensor cores:
 //   S = Q K^T,  P = 2^(f S - m),  O += P V,  out = O / sum P
-// for tiles of 128 query rows of one (request, kv head), 64 keys at a time.
+// for tiles of 2 x 128 query rows of one (request, kv head), 128 keys a step.
 //
 // With R query rows a kv head a key costs 4 R D operations and 18 D / 16 bytes:
-// bound by the matrix units, by 128 x 64 exponentials a tile, and by shared memory
-// (128 bytes a cycle), which feeds them.  So only the dequantized keys and values
-// pass through shared memory; the queries (FP16 of q / 2^e, as in the decode
-// kernel) and the weights are operands in TMEM, where the scores and the output
-// are too:
-//   columns  S [0, 64), FP32; P over it in [0, 32), FP16;  O [64, 64 + D);  Q from 192.
-// K is stored as [token][D] (K-major operand), V as [token][D] too (an operand whose
-// rows are contiguous: no transposition on the way), both in 128-byte swizzled
-// panels of 64 elements.  256 TMEM columns and 92 KB of shared memory a CTA: two
-// CTAs an SM, one's exponentials under the other's products.
+// bound by the matrix units (2048 cycles a step of 256 rows at D = 128), close
+// behind by shared memory, which feeds them 128 bytes a cycle (about 2300 cycles),
+// and by the exponentials (32768 a step).  An instruction with 128 rows takes 64
+// cycles or more whatever its N, so a step has 128 keys: both products have N = 128.
+// The weights are an operand in TMEM (no trip through shared memory), the queries
+// (FP16 of q / 2^e, as in the decode kernel) one in shared memory, because scores
+// and output of both halves fill the TMEM:
+//   half h: S at columns 256 h [128, FP32], P over it [64, FP16], O at 256 h + 128 [D].
+// K and V are dequantized once a step for both halves, as [token][element] in
+// 128-byte swizzled panels of 64 elements: K is then a K-major operand, V one whose
+// rows are contiguous (no transposition on the way).
 //
-// Warps: 0-3 softmax (a thread a row), 4-7 dequantize (a 16-token group each),
-// 8 copies the cache's groups in, 9 issues the products.  The maximum that the
+// Warps: 0-3 and 4-7 softmax of the two halves (a thread a row), 8-11 dequantize (two
+// 16-token groups each), 12 copies the cache's groups in, 13 issues the products; one
+// half's softmax runs under the other's products.  The maximum that the
 // weights refer to moves only when a row's scores exceed it by 2^8 (then O is
 // rescaled in TMEM); up to there FP16 holds the weights as exactly as below 1.
-// Every wait is bounded and an abort flag ends the others (mbar_wait).
+// Every wait is bounded and an abort flag ends the others.
 // Tiles are handed out from a counter, the longest of a request first.
 #include <math.h>
 
@@ -30,31 +32,36 @@ NVFP4_DEFINE_ERROR_READER(nvfp4_internal_read_error_kv_attention_tc)
 
 namespace {
 
-constexpr int kRows = 128;              // query rows of a tile
-constexpr int kKeys = 64;               // keys of a step
+constexpr int kHalfRows = 128;          // query rows of a half: a thread each
+constexpr int kRows = 2 * kHalfRows;    // of a tile
+constexpr int kKeys = 128;              // keys of a step
 constexpr int kGroups = kKeys / kKvGroup;
 constexpr int kRing = 3;                // raw steps in flight
-constexpr int kThreads = 320;
-constexpr uint32_t kTmemCols = 256;
-constexpr uint32_t kColS = 0, kColO = 64, kColQ = 192;
+constexpr int kDequantWarps = 4;        // each takes kGroups / kDequantWarps groups
+constexpr int kThreads = (8 + kDequantWarps + 2) * 32;
+constexpr int kCopyWarp = 8 + kDequantWarps, kMmaWarp = kCopyWarp + 1;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColHalf = 256, kColO = 128;
 constexpr uint32_t kSpinLimit = 1u << 22;  // polls of a wait (each suspends for a while): far beyond any step
 constexpr float kSlack = 8.0f;          // log2 units a score may exceed the maximum in use
 
 template <int D>
 struct Shape {
   static constexpr int kRaw = kGroups * KvLayout<D>::kGroupBytes;
-  static constexpr int kPanel = kKeys * 128;              // 64 tokens x 64 elements
-  static constexpr int kTile = kKeys * D * 2;             // K or V of a step, FP16
-  static constexpr int kOffK = 0;                         // [2] steps
-  static constexpr int kOffV = 2 * kTile;                 // [2]
-  static constexpr int kOffRaw = 4 * kTile;               // [kRing]
+  static constexpr int kPanel = kKeys * 128;              // 128 rows x 64 elements
+  static constexpr int kTile = kKeys * D * 2;             // Q of a half, K or V of a step, FP16
+  static constexpr int kOffQ = 0;                         // [2] halves
+  static constexpr int kOffK = 2 * kTile;
+  static constexpr int kOffV = 3 * kTile;                 // [2] steps
+  static constexpr int kOffRaw = 5 * kTile;               // [kRing]
   static constexpr int kOffBar = kOffRaw + kRing * kRaw;
-  static constexpr int kBars = 2 * kRing + 2 + 2 + 3;
+  static constexpr int kBars = 2 * kRing + 2 + 4 + 6 + 1;
   static constexpr int kOffWords = kOffBar + kBars * 8;   // TMEM address, abort flag, tile (4), groups present (kRing + 2)
   static constexpr int kSmem = kOffWords + 16 * 4 + 1024; // + alignment of the swizzled panels
   // instruction descriptors: FP32 accumulator, FP16 operands, M = 128; N = keys, and N = D with B's rows contiguous
-  static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
-  static constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+  static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kHalfRows >> 4) << 24);
+  static constexpr uint32_t kIdescO =
+      (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kHalfRows >> 4) << 24);
 };
 
 // D (+)= A . B^T with A in TMEM (two FP16 of the contraction to a column).
@@ -150,13 +157,13 @@ NVFP4_DEVINL Tile find_tile(const AttnArgs& a, long long t, int lane) {
   return Tile{-1, 0, 0};
 }
 
-// Dequantizes one 16-token group into rows [16 g, 16 g + 16) of the K and V tiles.  live: tokens that exist.
+// Dequantizes the keys of one 16-token group into rows [16 g, 16 g + 16) of the K tile.
 template <int D>
-NVFP4_DEVINL void dequantize(const uint8_t* raw, uint8_t* k_tile, uint8_t* v_tile, int g, int live, int lane) {
+NVFP4_DEVINL void dequantize_keys(const uint8_t* raw, uint8_t* k_tile, int g, int lane) {
   using L = KvLayout<D>;
   const int r = lane >> 2, c = lane & 3;
   constexpr int kPanel = kKeys * 128;
-  // ---- K: lane (r, c) has D/4 elements of the tokens at pos r and r + 8
+  // lane (r, c) has D/4 elements of the tokens at pos r and r + 8
   uint32_t sc[2][D / 64];
   if constexpr (D == 128) {
     const uint32_t w = *reinterpret_cast<const uint32_t*>(raw + L::kOffKScale + lane * 4);
@@ -203,7 +210,15 @@ NVFP4_DEVINL void dequantize(const uint8_t* raw, uint8_t* k_tile, uint8_t* v_til
       }
     }
   }
-  // ---- V: lane (r, c) has D/8 elements of tokens 4 c .. 4 c + 3
+}
+
+// And its values into the V tile.  live: tokens that exist.
+template <int D>
+NVFP4_DEVINL void dequantize_values(const uint8_t* raw, uint8_t* v_tile, int g, int live, int lane) {
+  using L = KvLayout<D>;
+  const int r = lane >> 2, c = lane & 3;
+  constexpr int kPanel = kKeys * 128;
+  // lane (r, c) has D/8 elements of tokens 4 c .. 4 c + 3
   uint32_t sw = *reinterpret_cast<const uint32_t*>(raw + L::kOffVScale + (D == 128 ? r : r >> 1) * 16 + 4 * c);
   const int mine = live - 4 * c;
   if (mine < 4) sw &= mine > 0 ? (1u << (8 * mine)) - 1u : 0u;      // what lies behind the last key may be NaN
@@ -236,15 +251,16 @@ NVFP4_DEVINL void dequantize(const uint8_t* raw, uint8_t* k_tile, uint8_t* v_til
 }
 
 template <int D, class T>
-__global__ void __launch_bounds__(kThreads, 2) kv_attention_tc_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const AttnArgs a) {
   using S = Shape<D>;
   using L = KvLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
-  uint64_t *raw_full = bars, *raw_free = bars + kRing, *kv_full = bars + 2 * kRing, *kv_free = kv_full + 2;
-  uint64_t *s_full = kv_free + 2, *p_full = s_full + 1, *q_full = s_full + 2;
+  uint64_t *raw_full = bars, *raw_free = raw_full + kRing, *k_full = raw_free + kRing, *k_free = k_full + 1;
+  uint64_t *v_full = k_free + 1, *v_free = v_full + 2;                  // [2] steps
+  uint64_t *s_full = v_free + 2, *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2;   // [2] halves
   volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(smem + S::kOffWords);
   volatile uint32_t* abort_flag = words + 1;
   volatile int* s_tile = reinterpret_cast<volatile int*>(words + 2);
@@ -253,20 +269,23 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_tc_kernel(const Attn
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_free[i], kGroups);
+      mbar_init(&raw_free[i], kDequantWarps);
     }
+    mbar_init(k_full, kDequantWarps);
+    mbar_init(k_free, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&kv_full[i], kGroups);
-      mbar_init(&kv_free[i], 1);
+      mbar_init(&v_full[i], kDequantWarps);
+      mbar_init(&v_free[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(p_full, 4);
-    mbar_init(q_full, 4);
+    mbar_init(q_full, 8);
     *abort_flag = 0u;
   }
   fence_mbar_init();
   griddep_wait();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(const_cast<uint32_t*>(words))),
                  "r"(kTmemCols));
@@ -279,9 +298,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_tc_kernel(const Attn
   // only now: a dependent kernel that came first to the TMEM would wait for this one, and this one for it
   griddep_launch_dependents();
   const float kg = *a.k_global, vg = *a.v_global;
-  // steps of this CTA so far (they give ring slot, operand buffer and the parities of their barriers), tiles, and
-  // phases of s_full: a step's scores each, and a tile's output
-  uint32_t step = 0, tiles = 0, scores = 0;
+  // steps of this CTA so far (they give ring slot, operand buffer and the parities of their barriers), those of the
+  // second half (a tile may have one half only), tiles
+  uint32_t step = 0, step_b = 0, tiles = 0;
   uint32_t copied = 0;                                  // steps whose copies this warp has started
 
   for (;;) {
@@ -301,21 +320,24 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_tc_kernel(const Attn
     if (b < 0) break;
     const Request rq = get_request(a, b, false);
     const int n_rows = (int)min((long long)kRows, (long long)rq.rows * a.group - row0);
-    const int hi_all = rq.len - rq.rows + row0 / a.group;       // as in the decode kernel
-    const int hi_any = rq.len - rq.rows + (row0 + n_rows - 1) / a.group;
-    const int lo_any = a.window > 0 ? max(hi_all - a.window + 1, 0) : 0;
-    const int lo_all = a.window > 0 ? max(hi_any - a.window + 1, 0) : 0;
-    const int step0 = lo_any / kKeys;
-    const int n = hi_any < 0 ? 0 : hi_any / kKeys + 1 - step0;  // steps of this tile
+    const bool both = n_rows > kHalfRows;
+    // keys that some row of the tile sees: [lo, hi]
+    const int p_first = rq.len - rq.rows + row0 / a.group;
+    const int hi = rq.len - rq.rows + (row0 + n_rows - 1) / a.group;
+    const int lo = a.window > 0 ? max(p_first - a.window + 1, 0) : 0;
+    const int step0 = lo / kKeys;
+    const int n = hi < 0 ? 0 : hi / kKeys + 1 - step0;  // steps of this tile
 
-    if (warp < 4) {
-      // ================ softmax: a thread a row ================
-      const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-      const int row = row0 + tid;
-      const bool mine = tid < n_rows;
+    if (warp < 8) {
+      // ================ softmax of a half: a thread a row ================
+      const int half = warp >> 2, r = tid & (kHalfRows - 1), row_h = half * kHalfRows;
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t col_s = tmem + kColHalf * half + lanes, col_o = col_s + kColO;
+      const int row = row0 + row_h + r;
+      const bool mine = row_h + r < n_rows;
       const int tok = rq.first + row / a.group, head = kvh * a.group + row % a.group;
-      float f;
-      {
+      float f = 1.0f;
+      if (half == 0 || both) {
         const T* q = static_cast<const T*>(a.q) + (mine ? tok * a.q_ts + head * a.q_hs : 0);
         float big = 0.0f;
         if (mine) {
@@ -330,51 +352,59 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_tc_kernel(const Attn
         float down, up;
         power_of_two(big, down, up);
         f = score_factor(a.scale * kLog2e * kg * up);
+        uint8_t* sq = smem + S::kOffQ + half * S::kTile + r * 128;
+#pragma unroll 4
+        for (int i = 0; i < D; i += 8) {
+          float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+          if (mine) {
+            float x[4], y[4];
+            load4(q + i, x);
+            load4(q + i + 4, y);
 #pragma unroll
-        for (int i = 0; i < D; i += 32) {
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (mine) load4(q + i + j, v);
-            w[j / 2] = pack_f16(v[0] * down, v[1] * down);
-            w[j / 2 + 1] = pack_f16(v[2] * down, v[3] * down);
+            for (int j = 0; j < 4; ++j) v[j] = x[j] * down, v[4 + j] = y[j] * down;
           }
-          tmem_st16(tmem + kColQ + lanes + i / 2, w);
+          *reinterpret_cast<uint4*>(sq + (i / 64) * S::kPanel + (((i / 8) & 7) ^ (r & 7)) * 16) =
+              make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      const int nh = half == 0 || both ? n : 0;
+      const uint32_t first = half == 0 ? step : step_b;
+      // every row of the half sees [lo_all, hi_all]
+      const int hi_all = rq.len - rq.rows + (row0 + row_h) / a.group;
+      const int hi_any = rq.len - rq.rows + (row0 + min(row_h + kHalfRows, n_rows) - 1) / a.group;
+      const int lo_all = a.window > 0 ? max(hi_any - a.window + 1, 0) : 0;
       const int pos = rq.len - rq.rows + row / a.group, low = a.window > 0 ? pos - a.window : -1;
       float m = -INFINITY, l = 0.0f;
       bool ok = true;
-      for (int k = 0; k < n && ok; ++k) {
-        ok = wait(s_full, scores + k, abort_flag);
+      for (int k = 0; k < nh && ok; ++k) {
+        ok = wait(&s_full[half], first + k, abort_flag);
         tc_fence_after();
-        // the scores are read twice, 32 columns at a time: for the maximum, and for the weights (fewer registers)
         const int t0 = (step0 + k) * kKeys;
         const uint32_t have = kv_have[(step + k) & 1u];
         const bool some = t0 + kKeys - 1 > hi_all || t0 < lo_all || have != (1u << kGroups) - 1u;
-        uint32_t s[32];
-        auto load_scores = [&](int h) {
-          tmem_ld32(tmem + kColS + lanes + 32 * h, s);
-          tmem_wait_ld(s);
+        auto hide = [&](uint32_t (&s)[32], int c) {
           if (some) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const int t = t0 + 32 * h + j;
-              if (t > pos || t <= low || !((have >> ((32 * h + j) / kKvGroup)) & 1u)) s[j] = 0xFF800000u;   // -inf
+              const int t = t0 + 32 * c + j;
+              if (t > pos || t <= low || !((have >> (2 * c + j / kKvGroup)) & 1u)) s[j] = 0xFF800000u;   // -inf
             }
           }
         };
+        // the scores are read twice, 32 columns at a time: for the maximum, and for the weights
+        uint32_t s[2][32];
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        tmem_ld32(col_s, s[0]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          load_scores(h);
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld(s[c & 1]);
+          tmem_ld32(col_s + 32 * ((c + 1) & 3), s[(c + 1) & 1]);   // the last one is the first of the second pass
+          hide(s[c & 1], c);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(s[j]));
+          for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(s[c & 1][j]));
         }
         const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
         float back = 1.0f;
@@ -384,112 +414,126 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_tc_kernel(const Attn
           l *= back;
         }
         const float neg_m = m == -INFINITY ? 0.0f : -m;
-        float sum[2] = {0.0f, 0.0f};
-        uint32_t p[2][16];
-        auto weights = [&](int h) {
+        const float2 f2 = make_float2(f, f), neg_m2 = make_float2(neg_m, neg_m);
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld(s[c & 1]);
+          if (c < 3) tmem_ld32(col_s + 32 * (c + 1), s[(c + 1) & 1]);
+          hide(s[c & 1], c);
+          uint32_t p[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            const float w0 = ex2(fmaf(__uint_as_float(s[j]), f, neg_m));
-            const float w1 = ex2(fmaf(__uint_as_float(s[j + 1]), f, neg_m));
-            sum[0] += w0;
-            sum[1] += w1;
-            p[h][j / 2] = pack_f16(w0, w1);
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c & 1][j]), __uint_as_float(s[c & 1][j + 1])), f2,
+                                        neg_m2);
+            const float2 w = make_float2(ex2(x.x), ex2(x.y));
+            sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], w);
+            p[j / 2] = pack_f16(w.x, w.y);
           }
-        };
-        weights(1);                                     // still in registers
-        load_scores(0);
-        tmem_st16(tmem + kColS + lanes + 16, p[1]);     // over scores 16 .. 31, which are in registers now
-        weights(0);
-        tmem_st16(tmem + kColS + lanes, p[0]);
+          tmem_st16(col_s + 16 * c, p);                 // over scores that have been read
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if (k > 0 && __any_sync(0xffffffffu, back != 1.0f)) {
+          ok = wait(&pv_done[half], first + k - 1, abort_flag) && ok;   // O is at rest until these weights are multiplied
+          tc_fence_after();
 #pragma unroll 1
           for (int i = 0; i < D; i += 32) {
-            uint32_t o[32];
-            tmem_ld32(tmem + kColO + lanes + i, o);
-            tmem_wait_ld(o);
+            tmem_ld32(col_o + i, s[0]);
+            tmem_wait_ld(s[0]);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * back);
-            tmem_st32(tmem + kColO + lanes + i, o);
+            for (int j = 0; j < 32; ++j) s[0][j] = __float_as_uint(__uint_as_float(s[0][j]) * back);
+            tmem_st32(col_o + i, s[0]);
           }
         }
-        l += sum[0] + sum[1];
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+        if (lane == 0) mbar_arrive(&p_full[half]);
       }
-      // ---- the tile's output (its last product's commit is one more phase of s_full)
-      if (n > 0 && ok) wait(s_full, scores + n, abort_flag);
+      // ---- the half's output
+      if (nh > 0 && ok) wait(&pv_done[half], first + nh - 1, abort_flag);
       tc_fence_after();
       const float inv = l > 0.0f ? vg / l : 0.0f;
       uint16_t* out = a.out + ((size_t)tok * a.heads + head) * D;
+      if (half == 0 || both) {
 #pragma unroll 1
-      for (int i = 0; i < D; i += 32) {
-        uint32_t o[32];
-        if (n > 0) {
-          tmem_ld32(tmem + kColO + lanes + i, o);
-          tmem_wait_ld(o);
-        } else {
+        for (int i = 0; i < D; i += 32) {
+          uint32_t o[32];
+          if (nh > 0) {
+            tmem_ld32(col_o + i, o);
+            tmem_wait_ld(o);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0u;
-        }
-        if (mine) {
+            for (int j = 0; j < 32; ++j) o[j] = 0u;
+          }
+          if (mine) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            uint32_t w[4];
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // a row without keys has sums of zeros, or of what other rows' keys left: its weights were 0
-              const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(o[j + 2 * e]) * inv,
-                                                             __uint_as_float(o[j + 2 * e + 1]) * inv);
-              w[e] = *reinterpret_cast<const uint32_t*>(&x);
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(o[j + 2 * e]) * inv,
+                                                               __uint_as_float(o[j + 2 * e + 1]) * inv);
+                w[e] = *reinterpret_cast<const uint32_t*>(&x);
+              }
+              *reinterpret_cast<uint4*>(out + i + j) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            *reinterpret_cast<uint4*>(out + i + j) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
+        if (mine && a.lse) a.lse[(size_t)tok * a.heads + head] = l > 0.0f ? (m + log2f(l)) / kLog2e : -INFINITY;
       }
-      if (mine && a.lse) a.lse[(size_t)tok * a.heads + head] = l > 0.0f ? (m + log2f(l)) / kLog2e : -INFINITY;
       tc_fence_before();
-    } else if (warp < 8) {
-      // ================ dequantize: a group a warp ================
-      const int g = warp - 4;
+    } else if (warp < kCopyWarp) {
+      // ================ dequantize ================
+      constexpr int kMine = kGroups / kDequantWarps;
+      const int g0 = (warp - 8) * kMine;
       bool ok = true;
       for (int k = 0; k < n && ok; ++k) {
         const uint32_t i = step + k, slot = i % kRing, buf = i & 1u;
         ok = wait(&raw_full[slot], i / kRing, abort_flag);
         const uint32_t have = raw_have[slot];
-        // the operand buffer's previous step has been multiplied
-        if (i >= 2) ok = wait(&kv_free[buf], i / 2 - 1, abort_flag) && ok;
-        const int t0 = (step0 + k) * kKeys + g * kKvGroup;
-        const int live = ((have >> g) & 1u) ? min(max(rq.len - t0, 0), kKvGroup) : 0;
-        dequantize<D>(smem + S::kOffRaw + slot * S::kRaw + g * L::kGroupBytes, smem + S::kOffK + buf * S::kTile,
-                      smem + S::kOffV + buf * S::kTile, g, live, lane);
-        if (g == 0 && lane == 0) kv_have[buf] = have;
+        const uint8_t* raw = smem + S::kOffRaw + slot * S::kRaw;
+        if (i >= 1) ok = wait(k_free, i - 1, abort_flag) && ok;          // the last step's keys have been multiplied
+#pragma unroll
+        for (int g = g0; g < g0 + kMine; ++g) dequantize_keys<D>(raw + g * L::kGroupBytes, smem + S::kOffK, g, lane);
+        if (g0 == 0 && lane == 0) kv_have[buf] = have;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full);
+        if (i >= 2) ok = wait(&v_free[buf], i / 2 - 1, abort_flag) && ok;
+#pragma unroll
+        for (int g = g0; g < g0 + kMine; ++g) {
+          const int t0 = (step0 + k) * kKeys + g * kKvGroup;
+          const int live = ((have >> g) & 1u) ? min(max(rq.len - t0, 0), kKvGroup) : 0;
+          dequantize_values<D>(raw + g * L::kGroupBytes, smem + S::kOffV + buf * S::kTile, g, live, lane);
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&raw_free[slot]);
-          mbar_arrive(&kv_full[buf]);
+          mbar_arrive(&v_full[buf]);
         }
       }
-    } else if (warp == 8) {
+    } else if (warp == kCopyWarp) {
       // ================ copies ================
       const int32_t* trow = a.table + (size_t)b * a.width;
       const uint8_t* src_head = a.pages + (size_t)kvh * (a.page_size / kKvGroup) * L::kGroupBytes;
       const size_t page_bytes = (size_t)a.kv_heads * (a.page_size / kKvGroup) * L::kGroupBytes;
+      // lane g < kGroups: the page of group g of step k (-1: not there, or not to be read)
+      auto look_up = [&](int k) {
+        const int t0 = (step0 + k) * kKeys + lane * kKvGroup;
+        if (k >= n || lane >= kGroups || t0 > hi || t0 + kKvGroup <= lo) return -1;
+        const int page = trow[t0 / a.page_size];
+        if (page >= 0 && page < a.num_pages) return page;
+        atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
+        return -1;
+      };
       bool ok = true;
+      int next = look_up(0);
       for (int k = 0; k < n && ok; ++k) {
         const uint32_t i = step + k, slot = i % kRing;
-        // lane g < kGroups: the page of group g (-1: not there, or not to be read)
-        const int t0 = (step0 + k) * kKeys + lane * kKvGroup;
-        int page = -1;
-        if (lane < kGroups && t0 <= hi_any && t0 + kKvGroup > lo_any) {
-          page = trow[t0 / a.page_size];
-          if (page < 0 || page >= a.num_pages) {
-            page = -1;
-            atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
-          }
-        }
+        const int page = next;
+        next = look_up(k + 1);
         if (i >= kRing) ok = wait(&raw_free[slot], i / kRing - 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -499,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_tc_kernel(const Attn
           mbar_arrive_expect_tx(&raw_full[slot], __popc(have) * L::kGroupBytes);
         }
         __syncwarp();
+        const int t0 = (step0 + k) * kKeys + lane * kKvGroup;
         if (page >= 0)
           bulk_g2s(smem + S::kOffRaw + slot * S::kRaw + lane * L::kGroupBytes,
                    src_head + page * page_bytes + (t0 % a.page_size / kKvGroup) * L::kGroupBytes, L::kGroupBytes,
@@ -508,45 +553,59 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_tc_kernel(const Attn
     } else if (lane == 0) {
       // ================ products ================
       bool ok = wait(q_full, tiles, abort_flag);
-      tc_fence_after();
-      for (int k = 0; k < n && ok; ++k) {
-        const uint32_t i = step + k, buf = i & 1u;
-        ok = wait(&kv_full[buf], i / 2, abort_flag);
-        // the last step's output product reads its weights where this step's scores will stand
-        if (k > 0) ok = wait(&kv_free[(i - 1) & 1u], (i - 1) / 2, abort_flag) && ok;
-        if (!ok) break;
+      const int halves = both ? 2 : 1;
+      auto multiply_scores = [&](int h) {
         tc_fence_after();
-        const uint32_t kt = smem_u32(smem + S::kOffK + buf * S::kTile), vt = smem_u32(smem + S::kOffV + buf * S::kTile);
+        const uint32_t qt = smem_u32(smem + S::kOffQ + h * S::kTile), kt = smem_u32(smem + S::kOffK);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
-          mma_f16_ta(tmem + kColS, tmem + kColQ + 8 * j, smem_desc_sw128(kt + (j >> 2) * S::kPanel + (j & 3) * 32), S::kIdescS,
-                     j > 0 ? 1u : 0u);
-        mma_commit(s_full);
-        ok = wait(p_full, i, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
+          mma_f16(tmem + kColHalf * h, smem_desc_sw128(qt + (j >> 2) * S::kPanel + (j & 3) * 32),
+                  smem_desc_sw128(kt + (j >> 2) * S::kPanel + (j & 3) * 32), S::kIdescS, j > 0 ? 1u : 0u);
+        mma_commit(&s_full[h]);
+        if (h == halves - 1) mma_commit(k_free);
+      };
+      if (n > 0) {
+        ok = wait(k_full, step, abort_flag) && ok;
+        for (int h = 0; h < halves; ++h) multiply_scores(h);
+      }
+      for (int k = 0; k < n && ok; ++k) {
+        const uint32_t i = step + k, buf = i & 1u;
+        const uint32_t vt = smem_u32(smem + S::kOffV + buf * S::kTile);
+        ok = wait(&v_full[buf], i / 2, abort_flag);
+        for (int h = 0; h < halves && ok; ++h) {
+          const uint32_t u = (h == 0 ? step : step_b) + k;
+          ok = wait(&p_full[h], u, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t col = tmem + kColHalf * h;
 #pragma unroll
-        for (int j = 0; j < kKeys / 16; ++j)
-          mma_f16_ta(tmem + kColO, tmem + kColS + 8 * j, smem_desc_mn_sw128(vt + j * 2048, S::kPanel), S::kIdescO,
-                     (k > 0 || j > 0) ? 1u : 0u);
-        mma_commit(&kv_free[buf]);
-        if (k == n - 1) mma_commit(s_full);
+          for (int j = 0; j < kKeys / 16; ++j)
+            mma_f16_ta(col + kColO, col + 8 * j, smem_desc_mn_sw128(vt + j * 2048, S::kPanel), S::kIdescO,
+                       (k > 0 || j > 0) ? 1u : 0u);
+          mma_commit(&pv_done[h]);
+          if (h == halves - 1) mma_commit(&v_free[buf]);
+          if (k + 1 < n) {
+            if (h == 0) ok = wait(k_full, i + 1, abort_flag);
+            ok = wait(&pv_done[h], u, abort_flag) && ok;   // the next scores stand where these weights are
+            if (ok) multiply_scores(h);
+          }
+        }
       }
     }
     step += (uint32_t)n;
-    scores += n > 0 ? (uint32_t)n + 1u : 0u;
+    step_b += both ? (uint32_t)n : 0u;
     ++tiles;
     __syncthreads();                                    // the tile's numbers and the TMEM are free again
     if (*abort_flag) break;
   }
-  if (*abort_flag && warp == 8) {
+  if (*abort_flag && warp == kCopyWarp) {
     // copies may still be in flight after a wait has given up: let every started one land (bounded)
     for (uint32_t i = copied > kRing ? copied - kRing : 0u; i < copied; ++i)
       for (uint32_t j = 0; j < (1u << 16); ++j)
         if (mbar_try_wait(&raw_full[i % kRing], (i / kRing) & 1u)) break;
   }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
   }
@@ -574,7 +633,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
       *e_out = e;
       return 0;
     }
-    return 2 * (sms > 0 ? sms : 1);
+    return sms > 0 ? sms : 1;
   }, &err);
   if (grid == 0) return err;
   const long long most = ((long long)a.tokens * a.group / kRows + a.batch) * a.kv_heads;   // tiles there can be
