@@ -64,13 +64,35 @@ struct Shape {
       (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kHalfRows >> 4) << 24);
 };
 
-// D (+)= A . B^T with A in TMEM (two FP16 of the contraction to a column).
-NVFP4_DEVINL void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t db, uint32_t idesc, uint32_t acc) {
+// The products are issued by one lane of a warp that stays together: what the instructions take is then uniform
+// over the warp and is kept in uniform registers (issued from a branch of one lane, 32 of them took 3700 cycles).
+// D (+)= A . B^T, A in shared memory.
+NVFP4_DEVINL void mma_f16_ss(uint32_t lead, uint32_t d_tmem, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(db), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(da), "l"(db), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
+}
+// A in TMEM (two FP16 of the contraction to a column).
+NVFP4_DEVINL void mma_f16_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t db, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(db), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+NVFP4_DEVINL void commit(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+NVFP4_DEVINL uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
 }
 
 // Operand whose rows (N) are contiguous, 128-byte swizzle: 64-element panels `panel` bytes apart, groups of 8
@@ -550,19 +572,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
                    &raw_full[slot]);
         copied = i + 1;
       }
-    } else if (lane == 0) {
+    } else {
       // ================ products ================
+      const uint32_t lead = elect_one();
       bool ok = wait(q_full, tiles, abort_flag);
       const int halves = both ? 2 : 1;
+      // descriptors of the operands' starts; everything else is an addition to their address field
+      const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + S::kOffQ)), k_desc = smem_desc_sw128(smem_u32(smem + S::kOffK));
+      const uint64_t v_desc = smem_desc_mn_sw128(smem_u32(smem + S::kOffV), S::kPanel);
       auto multiply_scores = [&](int h) {
         tc_fence_after();
-        const uint32_t qt = smem_u32(smem + S::kOffQ + h * S::kTile), kt = smem_u32(smem + S::kOffK);
+        const uint64_t dq = q_desc + (uint64_t)(h * (S::kTile >> 4));
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-          mma_f16(tmem + kColHalf * h, smem_desc_sw128(qt + (j >> 2) * S::kPanel + (j & 3) * 32),
-                  smem_desc_sw128(kt + (j >> 2) * S::kPanel + (j & 3) * 32), S::kIdescS, j > 0 ? 1u : 0u);
-        mma_commit(&s_full[h]);
-        if (h == halves - 1) mma_commit(k_free);
+        for (int j = 0; j < D / 16; ++j) {
+          constexpr int kPanel16 = S::kPanel >> 4;
+          const uint64_t at = (uint64_t)((j >> 2) * kPanel16 + (j & 3) * 2);
+          mma_f16_ss(lead, tmem + kColHalf * h, dq + at, k_desc + at, S::kIdescS, j > 0 ? 1u : 0u);
+        }
+        commit(lead, &s_full[h]);
+        if (h == halves - 1) commit(lead, k_free);
       };
       if (n > 0) {
         ok = wait(k_full, step, abort_flag) && ok;
@@ -570,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
       }
       for (int k = 0; k < n && ok; ++k) {
         const uint32_t i = step + k, buf = i & 1u;
-        const uint32_t vt = smem_u32(smem + S::kOffV + buf * S::kTile);
+        const uint64_t dv = v_desc + (uint64_t)(buf * (S::kTile >> 4));
         ok = wait(&v_full[buf], i / 2, abort_flag);
         for (int h = 0; h < halves && ok; ++h) {
           const uint32_t u = (h == 0 ? step : step_b) + k;
@@ -580,10 +608,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
           const uint32_t col = tmem + kColHalf * h;
 #pragma unroll
           for (int j = 0; j < kKeys / 16; ++j)
-            mma_f16_ta(col + kColO, col + 8 * j, smem_desc_mn_sw128(vt + j * 2048, S::kPanel), S::kIdescO,
+            mma_f16_ts(lead, col + kColO, col + 8 * j, dv + (uint64_t)(j * (2048 >> 4)), S::kIdescO,
                        (k > 0 || j > 0) ? 1u : 0u);
-          mma_commit(&pv_done[h]);
-          if (h == halves - 1) mma_commit(&v_free[buf]);
+          commit(lead, &pv_done[h]);
+          if (h == halves - 1) commit(lead, &v_free[buf]);
           if (k + 1 < n) {
             if (h == 0) ok = wait(k_full, i + 1, abort_flag);
             ok = wait(&pv_done[h], u, abort_flag) && ok;   // the next scores stand where these weights are
