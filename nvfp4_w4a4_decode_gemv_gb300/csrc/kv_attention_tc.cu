@@ -11,14 +11,16 @@
 // The weights are an operand in TMEM (no trip through shared memory), the queries
 // (FP16 of q / 2^e, as in the decode kernel) one in shared memory, because scores
 // and output of both halves fill the TMEM:
-//   half h: S at columns 256 h [128, FP32], P over it [64, FP16], O at 256 h + 128 [D].
+//   half h: S at columns 256 h [128, FP32], O at 256 h + 128 [D], P [FP16] over each thread's own scores: keys 0-63
+//   at 256 h [32], keys 64-127 at 256 h + 64 [32].
 // K and V are dequantized once a step for both halves, as [token][element] in
 // 128-byte swizzled panels of 64 elements: K is then a K-major operand, V one whose
 // rows are contiguous (no transposition on the way).
 //
-// Warps: 0-3 and 4-7 softmax of the two halves (a thread a row), 8-11 dequantize (two
-// 16-token groups each), 12 copies the cache's groups in, 13 issues the products; one
-// half's softmax runs under the other's products.  The maximum that the
+// Warps: 0-7 and 8-15 softmax of the two halves (two threads a row, 64 keys each: one thread
+// for all 128 took 2900 cycles, more than the products under which it should hide), 16-19
+// dequantize (two 16-token groups each), 20 copies the cache's groups in, 21 issues the
+// products; one half's softmax runs under the other's products.  The maximum that the
 // weights refer to moves only when a row's scores exceed it by 2^8 (then O is
 // rescaled in TMEM); up to there FP16 holds the weights as exactly as below 1.
 // Every wait is bounded and an abort flag ends the others.
@@ -38,8 +40,9 @@ constexpr int kKeys = 128;              // keys of a step
 constexpr int kGroups = kKeys / kKvGroup;
 constexpr int kRing = 3;                // raw steps in flight
 constexpr int kDequantWarps = 4;        // each takes kGroups / kDequantWarps groups
-constexpr int kThreads = (8 + kDequantWarps + 2) * 32;
-constexpr int kCopyWarp = 8 + kDequantWarps, kMmaWarp = kCopyWarp + 1;
+constexpr int kSoftWarps = 16;
+constexpr int kThreads = (kSoftWarps + kDequantWarps + 2) * 32;
+constexpr int kCopyWarp = kSoftWarps + kDequantWarps, kMmaWarp = kCopyWarp + 1;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColHalf = 256, kColO = 128;
 constexpr uint32_t kSpinLimit = 1u << 22;  // polls of a wait (each suspends for a while): far beyond any step
@@ -56,8 +59,10 @@ struct Shape {
   static constexpr int kOffRaw = 5 * kTile;               // [kRing]
   static constexpr int kOffBar = kOffRaw + kRing * kRaw;
   static constexpr int kBars = 2 * kRing + 2 + 4 + 6 + 1;
-  static constexpr int kOffWords = kOffBar + kBars * 8;   // TMEM address, abort flag, tile (4), groups present (kRing + 2)
-  static constexpr int kSmem = kOffWords + 16 * 4 + 1024; // + alignment of the swizzled panels
+  static constexpr int kOffWords = kOffBar + kBars * 8;   // TMEM address, abort flag, two tiles, groups present (kRing + 2)
+  static constexpr int kOffMax = kOffWords + 16 * 4;      // [2 steps][2 halves][2 threads][kHalfRows] maxima, then sums
+  static constexpr int kOffF = kOffMax + 8 * kHalfRows * 4;   // [2][kHalfRows] score factors
+  static constexpr int kSmem = kOffF + kRows * 4 + 1024; // + alignment of the swizzled panels
   // instruction descriptors: FP32 accumulator, FP16 operands, M = 128; N = keys, and N = D with B's rows contiguous
   static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kHalfRows >> 4) << 24);
   static constexpr uint32_t kIdescO =
@@ -286,8 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
   volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(smem + S::kOffWords);
   volatile uint32_t* abort_flag = words + 1;
   volatile int* s_tile = reinterpret_cast<volatile int*>(words + 2);
-  volatile uint32_t* raw_have = words + 6;              // [kRing] groups that a raw step brings
-  volatile uint32_t* kv_have = words + 6 + kRing;       // [2]
+  volatile uint32_t* raw_have = words + 8;              // [kRing] groups that a raw step brings
+  volatile uint32_t* kv_have = words + 8 + kRing;       // [2]
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -299,10 +304,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
       mbar_init(&v_full[i], kDequantWarps);
       mbar_init(&v_free[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], kSoftWarps / 2);
       mbar_init(&pv_done[i], 1);
     }
-    mbar_init(q_full, 8);
+    mbar_init(q_full, kSoftWarps);
     *abort_flag = 0u;
   }
   fence_mbar_init();
@@ -325,20 +330,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
   uint32_t step = 0, step_b = 0, tiles = 0;
   uint32_t copied = 0;                                  // steps whose copies this warp has started
 
-  for (;;) {
-    if (warp == 0) {
-      long long t = 0;
-      if (lane == 0) t = atomicAdd(&a.counters[kTileCounter], 1u);
-      t = __shfl_sync(0xffffffffu, t, 0);
-      const Tile tile = find_tile(a, t, lane);
-      if (lane == 0) {
-        s_tile[0] = tile.b;
-        s_tile[1] = tile.kvh;
-        s_tile[2] = tile.row0;
-      }
+  // the copy warp takes the tiles from the counter, each while the one before it is worked on
+  auto take_tile = [&](uint32_t n) {
+    long long t = 0;
+    if (lane == 0) t = atomicAdd(&a.counters[kTileCounter], 1u);
+    t = __shfl_sync(0xffffffffu, t, 0);
+    const Tile tile = find_tile(a, t, lane);
+    if (lane == 0) {
+      volatile int* to = s_tile + 3 * (n & 1u);
+      to[0] = tile.b, to[1] = tile.kvh, to[2] = tile.row0;
     }
-    __syncthreads();
-    const int b = s_tile[0], kvh = s_tile[1], row0 = s_tile[2];
+  };
+  if (warp == kCopyWarp) take_tile(0);
+  __syncthreads();
+  for (;;) {
+    const volatile int* from = s_tile + 3 * (tiles & 1u);
+    const int b = from[0], kvh = from[1], row0 = from[2];
     if (b < 0) break;
     const Request rq = get_request(a, b, false);
     const int n_rows = (int)min((long long)kRows, (long long)rq.rows * a.group - row0);
@@ -350,63 +357,79 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
     const int step0 = lo / kKeys;
     const int n = hi < 0 ? 0 : hi / kKeys + 1 - step0;  // steps of this tile
 
-    if (warp < 8) {
-      // ================ softmax of a half: a thread a row ================
-      const int half = warp >> 2, r = tid & (kHalfRows - 1), row_h = half * kHalfRows;
+    if (warp < kSoftWarps) {
+      // ================ softmax of a half: two threads a row, `part` 0 and 1 ================
+      const int half = warp >> 3, part = (warp >> 2) & 1, r = (warp & 3) * 32 + lane, row_h = half * kHalfRows;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t col_s = tmem + kColHalf * half + lanes, col_o = col_s + kColO;
+      const uint32_t col_s = tmem + kColHalf * half + 64 * part + lanes, col_o = tmem + kColHalf * half + kColO + lanes;
       const int row = row0 + row_h + r;
-      const bool mine = row_h + r < n_rows;
+      const bool used = half == 0 || both, mine = row_h + r < n_rows;
       const int tok = rq.first + row / a.group, head = kvh * a.group + row % a.group;
-      float f = 1.0f;
-      if (half == 0 || both) {
-        const T* q = static_cast<const T*>(a.q) + (mine ? tok * a.q_ts + head * a.q_hs : 0);
-        float big = 0.0f;
-        if (mine) {
-#pragma unroll 8
-          for (int i = 0; i < D; i += 4) {
-            float v[4];
-            load4(q + i, v);
+      float* s_max = reinterpret_cast<float*>(smem + S::kOffMax) + half * 2 * kHalfRows + r;   // + part, + step
+      constexpr int kStepMax = 4 * kHalfRows;
+      auto meet = [&]() {                               // the half's 8 warps
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "r"(kSoftWarps / 2 * 32) : "memory");
+      };
+      // queries: a warp a row at a time (whole rows a load), eight in flight
+      float* s_f = reinterpret_cast<float*>(smem + S::kOffF) + half * kHalfRows;
+      if (used) {
+        constexpr int E = D / 32, kBatch = 8, kWarpRows = kHalfRows / (kSoftWarps / 2);
+        const int w = warp & 7;
+#pragma unroll 1
+        for (int j0 = 0; j0 < kWarpRows; j0 += kBatch) {
+          float v[kBatch][E];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) big = fmaxf(big, fabsf(v[j]));
-          }
-        }
-        float down, up;
-        power_of_two(big, down, up);
-        f = score_factor(a.scale * kLog2e * kg * up);
-        uint8_t* sq = smem + S::kOffQ + half * S::kTile + r * 128;
-#pragma unroll 4
-        for (int i = 0; i < D; i += 8) {
-          float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-          if (mine) {
-            float x[4], y[4];
-            load4(q + i, x);
-            load4(q + i + 4, y);
+          for (int j = 0; j < kBatch; ++j) {
+            const int rh = w * kWarpRows + j0 + j, rr = row0 + row_h + rh;
+            const bool there = row_h + rh < n_rows;
+            const T* q = static_cast<const T*>(a.q) +
+                         (there ? (rq.first + rr / a.group) * a.q_ts + (kvh * a.group + rr % a.group) * a.q_hs : 0) + lane * E;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = x[j] * down, v[4 + j] = y[j] * down;
+            for (int e = 0; e < E; ++e) v[j][e] = there ? load_q(q + e) : 0.0f;
           }
-          *reinterpret_cast<uint4*>(sq + (i / 64) * S::kPanel + (((i / 8) & 7) ^ (r & 7)) * 16) =
-              make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int rh = w * kWarpRows + j0 + j;
+            float big = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(v[j][e]));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+            float down, up;
+            power_of_two(big, down, up);
+            if (lane == 0) s_f[rh] = score_factor(a.scale * kLog2e * kg * up);
+            // element lane * E: panel, 16-byte piece, place in it
+            const int e0 = lane * E;
+            uint8_t* sq = smem + S::kOffQ + half * S::kTile + (e0 / 64) * S::kPanel + rh * 128 +
+                          (((e0 / 8) & 7) ^ (rh & 7)) * 16 + (e0 & 7) * 2;
+            if constexpr (E == 4)
+              *reinterpret_cast<uint2*>(sq) = make_uint2(pack_f16(v[j][0] * down, v[j][1] * down),
+                                                         pack_f16(v[j][2] * down, v[j][3] * down));
+            else
+              *reinterpret_cast<uint32_t*>(sq) = pack_f16(v[j][0] * down, v[j][1] * down);
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        meet();                                         // the factors are there
       }
+      const float f = used ? s_f[r] : 1.0f;
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
-      const int nh = half == 0 || both ? n : 0;
+      const int nh = used ? n : 0;
       const uint32_t first = half == 0 ? step : step_b;
       // every row of the half sees [lo_all, hi_all]
       const int hi_all = rq.len - rq.rows + (row0 + row_h) / a.group;
       const int hi_any = rq.len - rq.rows + (row0 + min(row_h + kHalfRows, n_rows) - 1) / a.group;
       const int lo_all = a.window > 0 ? max(hi_any - a.window + 1, 0) : 0;
       const int pos = rq.len - rq.rows + row / a.group, low = a.window > 0 ? pos - a.window : -1;
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY, l = 0.0f;                    // the same m in both threads of a row
       bool ok = true;
-      for (int k = 0; k < nh && ok; ++k) {
-        ok = wait(&s_full[half], first + k, abort_flag);
+      for (int k = 0; k < nh; ++k) {                    // (an abort ends the waits, not the meetings)
+        ok = ok && wait(&s_full[half], first + k, abort_flag);
         tc_fence_after();
-        const int t0 = (step0 + k) * kKeys;
-        const uint32_t have = kv_have[(step + k) & 1u];
-        const bool some = t0 + kKeys - 1 > hi_all || t0 < lo_all || have != (1u << kGroups) - 1u;
+        const int t0 = (step0 + k) * kKeys + 64 * part;
+        const uint32_t have = (kv_have[(step + k) & 1u] >> (4 * part)) & 15u;
+        const bool some = t0 + 63 > hi_all || t0 < lo_all || have != 15u;
         auto hide = [&](uint32_t (&s)[32], int c) {
           if (some) {
 #pragma unroll
@@ -417,18 +440,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
           }
         };
         // the scores are read twice, 32 columns at a time: for the maximum, and for the weights
-        uint32_t s[2][32];
+        uint32_t s[32];
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        tmem_ld32(col_s, s[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_wait_ld(s[c & 1]);
-          tmem_ld32(col_s + 32 * ((c + 1) & 3), s[(c + 1) & 1]);   // the last one is the first of the second pass
-          hide(s[c & 1], c);
+        for (int c = 0; c < 2; ++c) {
+          tmem_ld32(col_s + 32 * c, s);
+          tmem_wait_ld(s);
+          hide(s, c);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(s[c & 1][j]));
+          for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(s[j]));
         }
-        const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
+        const float mine_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        float* at = s_max + (k & 1) * kStepMax;
+        at[part * kHalfRows] = mine_top;
+        meet();
+        const float mt = fmaxf(mine_top, at[(part ^ 1) * kHalfRows]) * f;
         float back = 1.0f;
         if (mt > m + kSlack) {                          // (also the first finite one)
           back = ex2(m - mt);
@@ -438,33 +464,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
         const float neg_m = m == -INFINITY ? 0.0f : -m;
         const float2 f2 = make_float2(f, f), neg_m2 = make_float2(neg_m, neg_m);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        uint32_t keep[16];                              // weights of the second 32 keys, whose scores are still here:
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_wait_ld(s[c & 1]);
-          if (c < 3) tmem_ld32(col_s + 32 * (c + 1), s[(c + 1) & 1]);
-          hide(s[c & 1], c);
+        for (int cc = 0; cc < 2; ++cc) {                // they would stand over the first 32's, to be read again
+          if (cc == 1) {
+            tmem_ld32(col_s, s);
+            tmem_wait_ld(s);
+            hide(s, 0);
+          }
           uint32_t p[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c & 1][j]), __uint_as_float(s[c & 1][j + 1])), f2,
-                                        neg_m2);
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f2, neg_m2);
             const float2 w = make_float2(ex2(x.x), ex2(x.y));
             sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], w);
             p[j / 2] = pack_f16(w.x, w.y);
           }
-          tmem_st16(col_s + 16 * c, p);                 // over scores that have been read
+          if (cc == 0) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) keep[j] = p[j];
+          } else {
+            tmem_st16(col_s, p);
+            tmem_st16(col_s + 16, keep);
+          }
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         if (k > 0 && __any_sync(0xffffffffu, back != 1.0f)) {
-          ok = wait(&pv_done[half], first + k - 1, abort_flag) && ok;   // O is at rest until these weights are multiplied
+          ok = ok && wait(&pv_done[half], first + k - 1, abort_flag);   // O is at rest until these weights are multiplied
           tc_fence_after();
 #pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
-            tmem_ld32(col_o + i, s[0]);
-            tmem_wait_ld(s[0]);
+          for (int i = part * (D / 2); i < (part + 1) * (D / 2); i += 32) {
+            tmem_ld32(col_o + i, s);
+            tmem_wait_ld(s);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[0][j] = __float_as_uint(__uint_as_float(s[0][j]) * back);
-            tmem_st32(col_o + i, s[0]);
+            for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * back);
+            tmem_st32(col_o + i, s);
           }
         }
         tmem_wait_st();
@@ -472,14 +506,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[half]);
       }
-      // ---- the half's output
-      if (nh > 0 && ok) wait(&pv_done[half], first + nh - 1, abort_flag);
-      tc_fence_after();
-      const float inv = l > 0.0f ? vg / l : 0.0f;
-      uint16_t* out = a.out + ((size_t)tok * a.heads + head) * D;
-      if (half == 0 || both) {
+      // ---- the half's output: each thread one half of its row's elements
+      if (used) {
+        float* at = s_max + (nh & 1) * kStepMax;        // not the last step's
+        at[part * kHalfRows] = l;
+        meet();
+        l += at[(part ^ 1) * kHalfRows];
+        if (nh > 0 && ok) wait(&pv_done[half], first + nh - 1, abort_flag);
+        tc_fence_after();
+        const float inv = l > 0.0f ? vg / l : 0.0f;
+        uint16_t* out = a.out + ((size_t)tok * a.heads + head) * D;
 #pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
+        for (int i = part * (D / 2); i < (part + 1) * (D / 2); i += 32) {
           uint32_t o[32];
           if (nh > 0) {
             tmem_ld32(col_o + i, o);
@@ -502,13 +540,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
             }
           }
         }
-        if (mine && a.lse) a.lse[(size_t)tok * a.heads + head] = l > 0.0f ? (m + log2f(l)) / kLog2e : -INFINITY;
+        if (mine && part == 0 && a.lse)
+          a.lse[(size_t)tok * a.heads + head] = l > 0.0f ? (m + log2f(l)) / kLog2e : -INFINITY;
       }
       tc_fence_before();
     } else if (warp < kCopyWarp) {
       // ================ dequantize ================
       constexpr int kMine = kGroups / kDequantWarps;
-      const int g0 = (warp - 8) * kMine;
+      const int g0 = (warp - kSoftWarps) * kMine;
       bool ok = true;
       for (int k = 0; k < n && ok; ++k) {
         const uint32_t i = step + k, slot = i % kRing, buf = i & 1u;
@@ -552,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
       };
       bool ok = true;
       int next = look_up(0);
+      bool taken = false;
       for (int k = 0; k < n && ok; ++k) {
         const uint32_t i = step + k, slot = i % kRing;
         const int page = next;
@@ -571,7 +611,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
                    src_head + page * page_bytes + (t0 % a.page_size / kKvGroup) * L::kGroupBytes, L::kGroupBytes,
                    &raw_full[slot]);
         copied = i + 1;
+        if (k == kRing - 1) {                           // the ring is full: time for the next tile
+          take_tile(tiles + 1);
+          taken = true;
+        }
       }
+      if (!taken) take_tile(tiles + 1);
     } else {
       // ================ products ================
       const uint32_t lead = elect_one();
@@ -608,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
           const uint32_t col = tmem + kColHalf * h;
 #pragma unroll
           for (int j = 0; j < kKeys / 16; ++j)
-            mma_f16_ts(lead, col + kColO, col + 8 * j, dv + (uint64_t)(j * (2048 >> 4)), S::kIdescO,
+            mma_f16_ts(lead, col + kColO, col + (j >> 2) * 64 + 8 * (j & 3), dv + (uint64_t)(j * (2048 >> 4)), S::kIdescO,
                        (k > 0 || j > 0) ? 1u : 0u);
           commit(lead, &pv_done[h]);
           if (h == halves - 1) commit(lead, &v_free[buf]);
@@ -624,7 +669,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
     step_b += both ? (uint32_t)n : 0u;
     ++tiles;
     __syncthreads();                                    // the tile's numbers and the TMEM are free again
-    if (*abort_flag) break;
+    const bool aborted = *abort_flag != 0u;
+    __syncthreads();
+    if (aborted) break;
   }
   if (*abort_flag && warp == kCopyWarp) {
     // copies may still be in flight after a wait has given up: let every started one land (bounded)
