@@ -21,7 +21,7 @@
 // for all 128 took 2900 cycles, more than the products under which it should hide), 16-19
 // dequantize (two 16-token groups each), 20 copies the cache's groups in, 21 issues the
 // products; one half's softmax runs under the other's products.  The maximum that the
-// weights refer to moves only when a row's scores exceed it by 2^8 (then O is
+// weights refer to moves only when a row's scores exceed it by 2^13 (then O is
 // rescaled in TMEM); up to there FP16 holds the weights as exactly as below 1.
 // Every wait is bounded and an abort flag ends the others.
 // Tiles are handed out from a counter, the longest of a request first.
@@ -46,7 +46,7 @@ constexpr int kCopyWarp = kSoftWarps + kDequantWarps, kMmaWarp = kCopyWarp + 1;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColHalf = 256, kColO = 128;
 constexpr uint32_t kSpinLimit = 1u << 22;  // polls of a wait (each suspends for a while): far beyond any step
-constexpr float kSlack = 8.0f;          // log2 units a score may exceed the maximum in use
+constexpr float kSlack = 13.0f;         // log2 units a score may exceed the maximum in use (FP16 holds 2^15)
 
 template <int D>
 struct Shape {
