@@ -32,7 +32,6 @@
 #include <math.h>
 
 #include "kv_attention.cuh"
-#include "tcgen05.cuh"
 
 NVFP4_DEFINE_ERROR_READER(nvfp4_internal_read_error_kv_attention)
 
@@ -51,6 +50,12 @@ NVFP4_DEVINL uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
+// d = a b, and d += a b.
+NVFP4_DEVINL void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
 NVFP4_DEVINL void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -77,7 +82,7 @@ struct Shape {
   static constexpr int kOffF = kOffML + 2 * kWarps * kRows * 4;           // [kRows] score factors
   static constexpr int kOffBar = kOffF + kRows * 4;                       // [kWarps][kStages] barriers
   static constexpr int kOffScan = kOffBar + kWarps * kStages * 8;         // 32 words for the split
-  static constexpr int kSmem = (kOffScan + 32 * 8 + 15) / 16 * 16;
+  static constexpr int kSmem = (kOffScan + 32 * 4 + 15) / 16 * 16;
 };
 
 // Units of a segment (one row tile of one kv head); at least one, so that rows without keys are written too.
@@ -88,7 +93,7 @@ NVFP4_DEVINL int segment_units(const Request& r) {
 }
 template <class S>
 NVFP4_DEVINL int request_tiles(const AttnArgs& a, const Request& r) {
-  return (int)(((long long)r.rows * a.group + S::kRows - 1) / S::kRows);
+  return (r.rows * a.group + S::kRows - 1) / S::kRows;
 }
 
 // How the segments are laid end to end for the split: each stands for `head` units of overhead, its own units,
@@ -96,6 +101,17 @@ NVFP4_DEVINL int request_tiles(const AttnArgs& a, const Request& r) {
 struct Split {
   int head, align;
   NVFP4_DEVINL int length(int n) const { return head + (n + align - 1) / align * align; }
+};
+
+// G equal shares of U units, the first U % G one longer.
+struct Shares {
+  int size, longer;
+  NVFP4_DEVINL Shares(int U, int G) : size(U / G), longer(U - size * G) {}
+  NVFP4_DEVINL int start(int q) const { return q * size + min(q, longer); }
+  NVFP4_DEVINL int owner(int x) const {
+    const int head = longer * (size + 1);
+    return x < head ? x / (size + 1) : longer + (x - head) / size;
+  }
 };
 
 // ---- one unit of keys ---------------------------------------------------------------
@@ -138,10 +154,6 @@ NVFP4_DEVINL void scores(const uint8_t* g, int lane, const uint32_t (*qreg)[2], 
     sc[1][0] = __byte_perm(h, h, 0x3232);
   }
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[t][i] = 0.0f;
-#pragma unroll
   for (int w = 0; w < W; ++w) {         // a word: 8 elements, two contraction steps
     uint32_t h[2][4];
     e2m1x8_to_f16(raw[0][w], h[0]);
@@ -152,12 +164,11 @@ NVFP4_DEVINL void scores(const uint8_t* g, int lane, const uint32_t (*qreg)[2], 
                              hmul2(h[0][2 * u + 1], sc[0][w / 2]), hmul2(h[1][2 * u + 1], sc[1][w / 2])};
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        if constexpr (NT <= 2) {
-          mma16816(s[t], a, qreg[t * (D / 16) + 2 * w + u][0], qreg[t * (D / 16) + 2 * w + u][1]);
-        } else {
-          const uint2 b = lds64(sq + ((t * (D / 16) + 2 * w + u) * 32 + lane) * 8);
-          mma16816(s[t], a, b.x, b.y);
-        }
+        uint2 b;
+        if constexpr (NT <= 2) b = make_uint2(qreg[t * (D / 16) + 2 * w + u][0], qreg[t * (D / 16) + 2 * w + u][1]);
+        else b = lds64(sq + ((t * (D / 16) + 2 * w + u) * 32 + lane) * 8);
+        if (w == 0 && u == 0) mma16816_first(s[t], a, b.x, b.y);
+        else mma16816(s[t], a, b.x, b.y);
       }
     }
   }
@@ -219,26 +230,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
   griddep_launch_dependents();
   griddep_wait();
 
-  // ---- the split: this CTA's range and the request it starts in
-  long long* s_scan = reinterpret_cast<long long*>(smem + S::kOffScan);
-  const int b0 = (int)((long long)a.batch * tid / kThreads), b1 = (int)((long long)a.batch * (tid + 1) / kThreads);
-  long long units4 = 0;                                 // units, each segment's padded to one for every warp
-  long long n_segs = 0;
-  int longest = 0;
+  // ---- the split: this CTA's range and the request it starts in (all counts fit 31 bits: the host checks)
+  int* s_scan = reinterpret_cast<int*>(smem + S::kOffScan);
+  const int per = (a.batch + kThreads - 1) / kThreads, b0 = min(per * tid, a.batch), b1 = min(b0 + per, a.batch);
+  int units4 = 0, n_segs = 0, longest = 0;              // units4: units, each segment's padded to one for every warp
+  Request own = {};                                     // the thread's request, where it has one only
   for (int b = b0; b < b1; ++b) {
-    const Request r = get_request(a, b, blockIdx.x == 0);
-    const long long segs = (long long)request_tiles<S>(a, r) * a.kv_heads;
-    const int n = segment_units<S>(r);
+    own = get_request(a, b, blockIdx.x == 0);
+    const int segs = request_tiles<S>(a, own) * a.kv_heads, n = segment_units<S>(own);
     units4 += segs * ((n + kWarps - 1) / kWarps);
     n_segs += segs;
     if (segs > 0) longest = max(longest, n);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    units4 += __shfl_xor_sync(0xffffffffu, units4, o);
-    n_segs += __shfl_xor_sync(0xffffffffu, n_segs, o);
-    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-  }
+  units4 = __reduce_add_sync(0xffffffffu, units4);
+  n_segs = __reduce_add_sync(0xffffffffu, n_segs);
+  longest = __reduce_max_sync(0xffffffffu, longest);
   if (lane == 0) {
     s_scan[warp] = units4;
     s_scan[4 + warp] = longest;
@@ -246,45 +252,46 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
   }
   __syncthreads();
   units4 = s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
-  longest = (int)max(max(s_scan[4], s_scan[5]), max(s_scan[6], s_scan[7]));
+  longest = max(max(s_scan[4], s_scan[5]), max(s_scan[6], s_scan[7]));
   n_segs = s_scan[8] + s_scan[9] + s_scan[10] + s_scan[11];
   if (units4 == 0) return;
   // Few units: every CTA a piece of one segment, one unit a warp or as many as keep a segment's pieces under
   // kMaxSplits.  Many: equal ranges, where a segment's fixed cost counts as kSegmentCost units, and at most
   // kMaxShares of them a segment.
-  const bool few = units4 <= gridDim.x;
+  const bool few = units4 <= (int)gridDim.x;
   const int piece = kWarps * max(1, (longest + kWarps * kMaxSplits - 1) / (kWarps * kMaxSplits));
   const Split split = few ? Split{0, piece} : Split{kSegmentCost, 1};
-  long long mine = 0;
+  int mine = 0;
   for (int b = b0; b < b1; ++b) {
-    const Request r = get_request(a, b, false);
-    mine += (long long)split.length(segment_units<S>(r)) * request_tiles<S>(a, r) * a.kv_heads;
+    const Request r = per == 1 ? own : get_request(a, b, false);
+    mine += split.length(segment_units<S>(r)) * request_tiles<S>(a, r) * a.kv_heads;
   }
-  long long inc = mine;
+  int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
   if (lane == 31) s_scan[12 + warp] = inc;
   __syncthreads();
-  long long U = 0, before = 0;
+  int U = 0, before = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += s_scan[12 + w];
     U += s_scan[12 + w];
   }
-  const long long excl = before + inc - mine;
-  const long long G = few ? min((long long)gridDim.x, U / piece) : min((long long)gridDim.x, kMaxShares * n_segs);
-  const long long cta = blockIdx.x;
+  const int excl = before + inc - mine;
+  const int G = few ? min((int)gridDim.x, U / piece) : (int)min((long long)gridDim.x, (long long)kMaxShares * n_segs);
+  const int cta = blockIdx.x;
   if (cta >= G) return;
-  long long u = unit_start(cta, U, G);
-  const long long u_end = unit_start(cta + 1, U, G);
+  const Shares shares(U, G);
+  int u = shares.start(cta);
+  const int u_end = shares.start(cta + 1);
   if (excl <= u && u < excl + mine) {
-    long long at = excl;
+    int at = excl;
     for (int b = b0; b < b1; ++b) {
-      const Request r = get_request(a, b, false);
-      const long long n = (long long)split.length(segment_units<S>(r)) * request_tiles<S>(a, r) * a.kv_heads;
+      const Request r = per == 1 ? own : get_request(a, b, false);
+      const int n = split.length(segment_units<S>(r)) * request_tiles<S>(a, r) * a.kv_heads;
       if (u < at + n) {
         s_scan[16] = b;
         s_scan[17] = at;
@@ -294,8 +301,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
     }
   }
   __syncthreads();
-  int b = (int)s_scan[16];
-  long long base = s_scan[17];
+  int b = s_scan[16], base = s_scan[17];
 
   const float kg = *a.k_global, vg = *a.v_global;
   uint32_t slot = 0, phase = 0;                         // of the next copy that this warp waits for
@@ -309,19 +315,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
   while (u < u_end) {
     const Request rq = get_request(a, b, false);
     const int n_seg = segment_units<S>(rq), tiles = request_tiles<S>(a, rq), len_seg = split.length(n_seg);
-    const long long n_req = (long long)len_seg * tiles * a.kv_heads;
+    const int n_req = len_seg * tiles * a.kv_heads;
     if (u >= base + n_req) {
       base += n_req;
       ++b;
       continue;
     }
-    const long long seg = (u - base) / len_seg;
-    const long long seg0 = base + seg * len_seg;        // where it stands; its own units from seg0 + head on
-    const int s0 = max((int)(u - seg0) - split.head, 0);
-    const int s1 = min((int)min((long long)len_seg, u_end - seg0) - split.head, n_seg);
+    const int seg = (u - base) / len_seg;
+    const int seg0 = base + seg * len_seg;              // where it stands; its own units from seg0 + head on
+    const int s0 = max(u - seg0 - split.head, 0);
+    const int s1 = min(min(len_seg, u_end - seg0) - split.head, n_seg);
     u = min(seg0 + len_seg, u_end);
     if (s1 <= s0) continue;                             // overhead or padding only
-    const int tile = (int)(seg % tiles), kvh = (int)(seg / tiles);
+    const int kvh = seg / tiles, tile = seg - kvh * tiles;
     const int row0 = tile * S::kRows;                   // row = query row * group + query head of the kv head
     const int n_rows = min(S::kRows, rq.rows * a.group - row0);
     // positions of the tile's first and last row: every row sees [lo_all, hi_all], some row [lo_any, hi_any]
@@ -565,8 +571,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
       }
     __syncthreads();
     const bool all = s0 == 0 && s1 == n_seg;
-    const long long c_first = cta_of_unit(seg0 + split.head, U, G);
-    const long long c_last = cta_of_unit(seg0 + split.head + n_seg - 1, U, G);
+    const int c_first = shares.owner(seg0 + split.head), c_last = shares.owner(seg0 + split.head + n_seg - 1);
     float* rec = a.records + (size_t)(2 * cta + (cta == c_first ? 1 : 0)) * S::kRecord;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -622,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
     if (!all) {
       __threadfence();
       __syncthreads();
-      unsigned int* flag = reinterpret_cast<unsigned int*>(smem + S::kOffScan + 248);
+      unsigned int* flag = reinterpret_cast<unsigned int*>(smem + S::kOffScan + 124);
       if (tid == 0) *flag = atomicAdd(&a.counters[c_first], 1u);
       __syncthreads();
       if (*flag == (unsigned)(c_last - c_first)) {
@@ -632,12 +637,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel
           float mx = -INFINITY, l = 0.0f;
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
           constexpr int kBatch = 8;                     // records whose loads are in flight together
-          for (long long q0 = c_first; q0 <= c_last; q0 += kBatch) {
+          for (int q0 = c_first; q0 <= c_last; q0 += kBatch) {
             float m[kBatch], lq[kBatch];
             float4 y[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-              const long long q = min(q0 + j, c_last);
+              const int q = min(q0 + j, c_last);
               const float* r = a.records + (size_t)(2 * q + (q == c_first ? 1 : 0)) * S::kRecord;
               m[j] = __ldcg(r + S::kRows * D + row);
               lq[j] = __ldcg(r + S::kRows * (D + 1) + row);
@@ -755,8 +760,12 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens,
                       reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes), tokens, heads,
                       cache->kv_heads, group, cache->page_size, cache->num_pages, table_width, batch, window, scale};
   const int rows = cu_q ? (int)((long long)max_q * group < 1 << 20 ? max_q * group : 1 << 20) : group;
+  // the decode kernel counts its units (32 keys of a row tile, with their overhead) in 31 bits; this is the most there
+  // can be, whatever cu_q and kv_lens hold
+  const long long most_units = ((long long)tokens * group / 8 + batch) * cache->kv_heads *
+                               ((long long)table_width * cache->page_size / 32 + 2 + kSegmentCost + kWarps);
   cudaError_t e;
-  if (rows > kTcRows)
+  if (rows > kTcRows || most_units > 0x7FFFFFFFll)
     e = nvfp4_internal_kv_attention_tc(a, cache->head_dim, dtype, stream);
   else if (cache->head_dim == 128)
     e = dtype == NVFP4_DTYPE_F32 ? dispatch<128, float>(a, rows, stream) : dispatch<128, uint16_t>(a, rows, stream);
