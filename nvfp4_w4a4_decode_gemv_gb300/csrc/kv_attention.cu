@@ -66,11 +66,11 @@ NVFP4_DEVINL void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, u
 template <int D, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;                     // query rows of a tile
-  static constexpr int kUnitGroups = 256 / D;              // 32 tokens at D = 128, 64 at D = 64: 4608 bytes
+  static constexpr int kUnitGroups = 512 / D;              // 64 tokens at D = 128, 128 at D = 64: 9216 bytes
   static constexpr int kUnitTokens = kKvGroup * kUnitGroups;
   static constexpr int kUnitBytes = kUnitGroups * KvLayout<D>::kGroupBytes;
   static constexpr int kPair = NT <= 2 ? 2 : 1;            // groups whose scores are formed together (latency)
-  static constexpr int kStages = NT == 1 ? 2 : 3;
+  static constexpr int kStages = 2;
   static constexpr int kMergeStride = D + 4;               // floats a row in the merge buffer (bank spread)
   static constexpr int kRecord = kRows * (D + 2);          // floats of a record: O, then M, then L
   // shared memory
@@ -213,7 +213,7 @@ NVFP4_DEVINL void weigh(const uint8_t* g, int lane, const uint32_t (&p)[NT][2], 
 
 // ---- the kernel -----------------------------------------------------------------------
 template <int D, int NT, class T>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv_attention_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel(const AttnArgs a) {
   using S = Shape<D, NT>;
   using L = KvLayout<D>;
   extern __shared__ __align__(128) uint8_t smem[];
