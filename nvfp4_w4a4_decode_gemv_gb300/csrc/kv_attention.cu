@@ -106,6 +106,7 @@ struct Split {
 // G equal shares of U units, the first U % G one longer.
 struct Shares {
   int size, longer;
+  Shares() = default;
   NVFP4_DEVINL Shares(int U, int G) : size(U / G), longer(U - size * G) {}
   NVFP4_DEVINL int start(int q) const { return q * size + min(q, longer); }
   NVFP4_DEVINL int owner(int x) const {
@@ -230,78 +231,99 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
   griddep_launch_dependents();
   griddep_wait();
 
-  // ---- the split: this CTA's range and the request it starts in (all counts fit 31 bits: the host checks)
-  int* s_scan = reinterpret_cast<int*>(smem + S::kOffScan);
-  const int per = (a.batch + kThreads - 1) / kThreads, b0 = min(per * tid, a.batch), b1 = min(b0 + per, a.batch);
-  int units4 = 0, n_segs = 0, longest = 0;              // units4: units, each segment's padded to one for every warp
-  Request own = {};                                     // the thread's request, where it has one only
-  for (int b = b0; b < b1; ++b) {
-    own = get_request(a, b, blockIdx.x == 0);
-    const int segs = request_tiles<S>(a, own) * a.kv_heads, n = segment_units<S>(own);
-    units4 += segs * ((n + kWarps - 1) / kWarps);
-    n_segs += segs;
-    if (segs > 0) longest = max(longest, n);
-  }
-  units4 = __reduce_add_sync(0xffffffffu, units4);
-  n_segs = __reduce_add_sync(0xffffffffu, n_segs);
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 0) {
-    s_scan[warp] = units4;
-    s_scan[4 + warp] = longest;
-    s_scan[8 + warp] = n_segs;
-  }
-  __syncthreads();
-  units4 = s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
-  longest = max(max(s_scan[4], s_scan[5]), max(s_scan[6], s_scan[7]));
-  n_segs = s_scan[8] + s_scan[9] + s_scan[10] + s_scan[11];
-  if (units4 == 0) return;
-  // Few units: every CTA a piece of one segment, one unit a warp or as many as keep a segment's pieces under
-  // kMaxSplits.  Many: equal ranges, where a segment's fixed cost counts as kSegmentCost units, and at most
-  // kMaxShares of them a segment.
-  const bool few = units4 <= (int)gridDim.x;
-  const int piece = kWarps * max(1, (longest + kWarps * kMaxSplits - 1) / (kWarps * kMaxSplits));
-  const Split split = few ? Split{0, piece} : Split{kSegmentCost, 1};
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const Request r = per == 1 ? own : get_request(a, b, false);
-    mine += split.length(segment_units<S>(r)) * request_tiles<S>(a, r) * a.kv_heads;
-  }
-  int inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) s_scan[12 + warp] = inc;
-  __syncthreads();
-  int U = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_scan[12 + w];
-    U += s_scan[12 + w];
-  }
-  const int excl = before + inc - mine;
-  const int G = few ? min((int)gridDim.x, U / piece) : (int)min((long long)gridDim.x, (long long)kMaxShares * n_segs);
-  const int cta = blockIdx.x;
-  if (cta >= G) return;
-  const Shares shares(U, G);
-  int u = shares.start(cta);
-  const int u_end = shares.start(cta + 1);
-  if (excl <= u && u < excl + mine) {
-    int at = excl;
-    for (int b = b0; b < b1; ++b) {
-      const Request r = per == 1 ? own : get_request(a, b, false);
-      const int n = split.length(segment_units<S>(r)) * request_tiles<S>(a, r) * a.kv_heads;
-      if (u < at + n) {
-        s_scan[16] = b;
-        s_scan[17] = at;
-        break;
+  // ---- the split: this CTA's range and the request it starts in (all counts fit 31 bits: the host checks).
+  // Up to 32 requests every warp works it out by itself, a request a lane; more are shared by the CTA's threads.
+  int b, base, u, u_end, n_ctas;
+  Split split;
+  Shares shares;
+  {
+    const bool small = a.batch <= 32;
+    int* s_scan = reinterpret_cast<int*>(smem + S::kOffScan);
+    const int per = small ? 1 : (a.batch + kThreads - 1) / kThreads, me = small ? lane : tid;
+    const int b0 = min(per * me, a.batch), b1 = min(b0 + per, a.batch);
+    int units4 = 0, n_segs = 0, longest = 0;            // units4: units, each segment's padded to one for every warp
+    Request own = {};                                   // the thread's request, where it has one only
+    for (int i = b0; i < b1; ++i) {
+      own = get_request(a, i, blockIdx.x == 0);
+      const int segs = request_tiles<S>(a, own) * a.kv_heads, n = segment_units<S>(own);
+      units4 += segs * ((n + kWarps - 1) / kWarps);
+      n_segs += segs;
+      if (segs > 0) longest = max(longest, n);
+    }
+    units4 = __reduce_add_sync(0xffffffffu, units4);
+    n_segs = __reduce_add_sync(0xffffffffu, n_segs);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (!small) {
+      if (lane == 0) {
+        s_scan[warp] = units4;
+        s_scan[4 + warp] = longest;
+        s_scan[8 + warp] = n_segs;
       }
-      at += n;
+      __syncthreads();
+      units4 = s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
+      longest = max(max(s_scan[4], s_scan[5]), max(s_scan[6], s_scan[7]));
+      n_segs = s_scan[8] + s_scan[9] + s_scan[10] + s_scan[11];
+    }
+    if (units4 == 0) return;
+    // Few units: every CTA a piece of one segment, one unit a warp or as many as keep a segment's pieces under
+    // kMaxSplits.  Many: equal ranges, where a segment's fixed cost counts as kSegmentCost units, and at most
+    // kMaxShares of them a segment.
+    const bool few = units4 <= (int)gridDim.x;
+    const int piece = kWarps * max(1, (longest + kWarps * kMaxSplits - 1) / (kWarps * kMaxSplits));
+    split = few ? Split{0, piece} : Split{kSegmentCost, 1};
+    int mine = 0;
+    for (int i = b0; i < b1; ++i) {
+      const Request r = per == 1 ? own : get_request(a, i, false);
+      mine += split.length(segment_units<S>(r)) * request_tiles<S>(a, r) * a.kv_heads;
+    }
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    int U = __shfl_sync(0xffffffffu, inc, 31);
+    if (!small) {
+      if (lane == 31) s_scan[12 + warp] = inc;
+      __syncthreads();
+      U = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) inc += s_scan[12 + w];
+        U += s_scan[12 + w];
+      }
+    }
+    const int excl = inc - mine;
+    n_ctas = few ? min((int)gridDim.x, U / piece) : (int)min((long long)gridDim.x, (long long)kMaxShares * n_segs);
+    if ((int)blockIdx.x >= n_ctas) return;
+    shares = Shares(U, n_ctas);
+    u = shares.start(blockIdx.x);
+    u_end = shares.start(blockIdx.x + 1);
+    const bool here = excl <= u && u < excl + mine;
+    if (small) {
+      const int l = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+      b = l;
+      base = __shfl_sync(0xffffffffu, excl, l);
+    } else {
+      if (here) {
+        int at = excl;
+        for (int i = b0; i < b1; ++i) {
+          const Request r = per == 1 ? own : get_request(a, i, false);
+          const int n = split.length(segment_units<S>(r)) * request_tiles<S>(a, r) * a.kv_heads;
+          if (u < at + n) {
+            s_scan[16] = i;
+            s_scan[17] = at;
+            break;
+          }
+          at += n;
+        }
+      }
+      __syncthreads();
+      b = s_scan[16];
+      base = s_scan[17];
     }
   }
-  __syncthreads();
-  int b = s_scan[16], base = s_scan[17];
+  const int cta = blockIdx.x;
 
   const float kg = *a.k_global, vg = *a.v_global;
   uint32_t slot = 0, phase = 0;                         // of the next copy that this warp waits for
@@ -336,68 +358,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
     const int lo_any = a.window > 0 ? max(hi_all - a.window + 1, 0) : 0;
     const int lo_all = a.window > 0 ? max(hi_any - a.window + 1, 0) : 0;
 
-    // ---- this warp's units, and its first copies
-    const int unit0 = rq.begin / S::kUnitTokens;        // the segment's first unit
-    const int u_lo = max(s0, lo_any / S::kUnitTokens - unit0);
-    const int u_hi = hi_any < 0 ? u_lo : min(s1, hi_any / S::kUnitTokens + 1 - unit0);
-    const int my_n = u_lo + warp < u_hi ? (u_hi - u_lo - warp + kWarps - 1) / kWarps : 0;
-    const int32_t* trow = a.table + (size_t)b * a.width;
-    const bool whole = a.page_size % S::kUnitTokens == 0;   // a unit lies in one page
-    // Lane g < kUnitGroups looks after group g of the warp's units: where it starts, its place in the page table
-    // and in its page, all advanced by kWarps units at a time without a division.
-    const int t_first = (unit0 + u_lo + warp) * S::kUnitTokens;
-    constexpr int kStep = kWarps * S::kUnitTokens;
-    int g_tok = t_first + lane * kKvGroup, g_page = g_tok / a.page_size, g_off = g_tok - g_page * a.page_size;
-    int left = lane < S::kUnitGroups ? my_n : 0;
-    const int step_pages = kStep / a.page_size, step_off = kStep - step_pages * a.page_size;
-    const uint8_t* src_head = a.pages + (size_t)kvh * (a.page_size / kKvGroup) * L::kGroupBytes;
-    const size_t page_bytes = (size_t)a.kv_heads * (a.page_size / kKvGroup) * L::kGroupBytes;
-    int nx_page = -1, nx_off = 0;                       // the next unit's page (-1: not there, or not to be read)
-    auto look_up = [&]() {
-      nx_page = -1;
-      nx_off = g_off;
-      if (left > 0 && g_tok <= hi_any && g_tok + kKvGroup > lo_any) {
-        nx_page = trow[g_page];
-        if (nx_page < 0 || nx_page >= a.num_pages) {
-          nx_page = -1;
-          atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
-        }
-      }
-      --left;
-      g_tok += kStep;
-      g_page += step_pages;
-      g_off += step_off;
-      if (g_off >= a.page_size) {
-        g_off -= a.page_size;
-        ++g_page;
-      }
-    };
-    // Starts the copies of the unit looked up last into ring slot `slot`; returns which of its groups come.
-    auto issue = [&](uint32_t slot) -> uint32_t {
-      const uint32_t have = __ballot_sync(0xffffffffu, nx_page >= 0);
-      const bool one = whole && have == (1u << S::kUnitGroups) - 1u;
-      if (lane == 0) mbar_arrive_expect_tx(&bars[slot], __popc(have) * L::kGroupBytes);
-      __syncwarp();
-      if (nx_page >= 0 && (lane == 0 || !one))
-        bulk_g2s(ring + slot * S::kUnitBytes + lane * L::kGroupBytes,
-                 src_head + nx_page * page_bytes + (nx_off / kKvGroup) * L::kGroupBytes,
-                 one ? S::kUnitBytes : L::kGroupBytes, &bars[slot]);
-      return have;
-    };
-    // the ring held the last segment's merge: order those accesses before the copies
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    uint32_t coming[S::kStages];                        // groups of the units in flight, oldest first
-    look_up();
-#pragma unroll
-    for (int k = 0; k < S::kStages; ++k) {
-      coming[k] = 0;
-      if (k < my_n) {
-        coming[k] = issue(slot + k < S::kStages ? slot + k : slot + k - S::kStages);
-        look_up();
-      }
-    }
-
-    // ---- queries (while the first copies fly): FP16 of q / 2^e in operand order, and the factors of the scores
+    // ---- the queries' loads first: they and the page table's are in flight together
     constexpr int E = D / 32;
     float v[S::kRows / kWarps][E];
 #pragma unroll
@@ -408,6 +369,67 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
 #pragma unroll
       for (int e = 0; e < E; ++e) v[i][e] = row < n_rows ? load_q(q + e) : 0.0f;
     }
+
+    // ---- this warp's units, and its first copies
+    const int unit0 = rq.begin / S::kUnitTokens;        // the segment's first unit
+    const int u_lo = max(s0, lo_any / S::kUnitTokens - unit0);
+    const int u_hi = hi_any < 0 ? u_lo : min(s1, hi_any / S::kUnitTokens + 1 - unit0);
+    const int my_n = u_lo + warp < u_hi ? (u_hi - u_lo - warp + kWarps - 1) / kWarps : 0;
+    const int32_t* trow = a.table + (size_t)b * a.width;
+    const bool whole = a.page_size % S::kUnitTokens == 0;   // a unit lies in one page
+    const int t_first = (unit0 + u_lo + warp) * S::kUnitTokens;
+    constexpr int kStep = kWarps * S::kUnitTokens;
+    const uint8_t* src_head = a.pages + (size_t)kvh * (a.page_size / kKvGroup) * L::kGroupBytes;
+    const size_t page_bytes = (size_t)a.kv_heads * (a.page_size / kKvGroup) * L::kGroupBytes;
+    // The pages of the groups of kAhead units are looked up with one load, a lane a group (-1: not there, or not to be
+    // read), kAhead units before the first of them is needed.
+    constexpr int kAhead = 32 / S::kUnitGroups;
+    const int my_group = lane % S::kUnitGroups;
+    auto look_up = [&](int k0) -> int {
+      const int k = k0 + lane / S::kUnitGroups, t = t_first + k * kStep + my_group * kKvGroup;
+      if (k >= my_n || t > hi_any || t + kKvGroup <= lo_any) return -1;
+      const int page = trow[t / a.page_size];
+      if (page >= 0 && page < a.num_pages) return page;
+      atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
+      return -1;
+    };
+    int pages_now = look_up(0), pages_next = look_up(kAhead);
+    int issued = 0;                                     // units whose copies have been started
+    // where the lane's group of the next unit lies in its page, advanced without a division
+    int g_off = (t_first + my_group * kKvGroup) % a.page_size;
+    const int step_off = kStep % a.page_size;
+    // Starts the copies of the next unit into ring slot `to`; returns which of its groups come.
+    auto issue = [&](uint32_t to) -> uint32_t {
+      const int at = issued % kAhead;
+      int page = __shfl_sync(0xffffffffu, pages_now, at * S::kUnitGroups + my_group);
+      if (lane >= S::kUnitGroups) page = -1;
+      const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+      const bool one = whole && have == (1u << S::kUnitGroups) - 1u;
+      if (lane == 0) mbar_arrive_expect_tx(&bars[to], __popc(have) * L::kGroupBytes);
+      __syncwarp();
+      if (page >= 0 && (lane == 0 || !one))
+        bulk_g2s(ring + to * S::kUnitBytes + lane * L::kGroupBytes,
+                 src_head + page * page_bytes + (g_off / kKvGroup) * L::kGroupBytes, one ? S::kUnitBytes : L::kGroupBytes,
+                 &bars[to]);
+      ++issued;
+      if (at == kAhead - 1) {
+        pages_now = pages_next;
+        pages_next = look_up(issued + kAhead);
+      }
+      g_off += step_off;
+      if (g_off >= a.page_size) g_off -= a.page_size;
+      return have;
+    };
+    // the ring held the last segment's merge: order those accesses before the copies
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    uint32_t coming[S::kStages];                        // groups of the units in flight, oldest first
+#pragma unroll
+    for (int k = 0; k < S::kStages; ++k) {
+      coming[k] = 0;
+      if (k < my_n) coming[k] = issue(slot + k < S::kStages ? slot + k : slot + k - S::kStages);
+    }
+
+    // ---- the queries (while the first copies fly): FP16 of q / 2^e in operand order, and the factors of the scores
 #pragma unroll
     for (int i = 0; i < S::kRows / kWarps; ++i) {
       const int row = warp + i * kWarps;
@@ -543,7 +565,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
       coming[S::kStages - 1] = 0;
       if (k + S::kStages < my_n && !gave_up) {
         coming[S::kStages - 1] = issue(slot);
-        look_up();
       }
       advance();
       if (gave_up) {
