@@ -20,7 +20,7 @@
 // exact for BF16 queries down to 2^-14 of it.  Weights are rounded to FP16 for
 // the product with V (2^-11 of each); their sum is FP32.
 //
-// Work split: units of kUnitTokens tokens of one (request, kv head, row tile),
+// Work split: units of 64 or 32 tokens (D = 64: 128 or 64) of one (request, kv head, row tile),
 // Stream-K over all of them, so that any mix of lengths fills the GPU; the split
 // is made on the GPU from the lengths (a captured call follows them).  A CTA of
 // four warps takes a contiguous range; its warps take every fourth unit of a
@@ -42,7 +42,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxSplits = 32;          // pieces of a segment when there are few: more cost more to merge than they save
 constexpr int kMaxShares = 64;          // the same bound where there are many
 constexpr int kTcRows = 64;             // more query rows of a kv head than this take the other kernel (kv_attention_tc.cu)
-constexpr int kSegmentCost = 12;        // units that the fixed cost of a segment (queries, first copies, merge) stands for
+constexpr int kSegmentCost = 512;       // keys that the fixed cost of a segment (queries, first copies, merge) stands for
+constexpr int kShortUnits = 8;
 
 NVFP4_DEVINL uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
@@ -66,8 +67,8 @@ NVFP4_DEVINL void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, u
 template <int D, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;                     // query rows of a tile
-  static constexpr int kUnitGroups = 512 / D;              // 64 tokens at D = 128, 128 at D = 64: 9216 bytes
-  static constexpr int kUnitTokens = kKvGroup * kUnitGroups;
+  static constexpr int kUnitGroups = 512 / D;              // most groups of a unit: 64 tokens at D = 128, 128 at D = 64
+  static constexpr int kUnitLog = D == 128 ? 6 : 7;        // log2 of its tokens; short work has units of half of that
   static constexpr int kUnitBytes = kUnitGroups * KvLayout<D>::kGroupBytes;
   static constexpr int kPair = NT <= 2 ? 2 : 1;            // groups whose scores are formed together (latency)
   static constexpr int kStages = 2;
@@ -86,9 +87,8 @@ struct Shape {
 };
 
 // Units of a segment (one row tile of one kv head); at least one, so that rows without keys are written too.
-template <class S>
-NVFP4_DEVINL int segment_units(const Request& r) {
-  const int n = (r.len + S::kUnitTokens - 1) / S::kUnitTokens - r.begin / S::kUnitTokens;
+NVFP4_DEVINL int segment_units(const Request& r, int unit_log) {
+  const int n = ((r.len + (1 << unit_log) - 1) >> unit_log) - (r.begin >> unit_log);
   return n > 0 ? n : 1;
 }
 template <class S>
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
 
   // ---- the split: this CTA's range and the request it starts in (all counts fit 31 bits: the host checks).
   // Up to 32 requests every warp works it out by itself, a request a lane; more are shared by the CTA's threads.
-  int b, base, u, u_end, n_ctas;
+  int b, base, u, u_end, n_ctas, unit_log;
   Split split;
   Shares shares;
   {
@@ -241,16 +241,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
     int* s_scan = reinterpret_cast<int*>(smem + S::kOffScan);
     const int per = small ? 1 : (a.batch + kThreads - 1) / kThreads, me = small ? lane : tid;
     const int b0 = min(per * me, a.batch), b1 = min(b0 + per, a.batch);
-    int units4 = 0, n_segs = 0, longest = 0;            // units4: units, each segment's padded to one for every warp
+    // units of the two sizes, each segment's padded to one for every warp
+    int units4 = 0, units4_half = 0, n_segs = 0, longest = 0;
     Request own = {};                                   // the thread's request, where it has one only
     for (int i = b0; i < b1; ++i) {
       own = get_request(a, i, blockIdx.x == 0);
-      const int segs = request_tiles<S>(a, own) * a.kv_heads, n = segment_units<S>(own);
-      units4 += segs * ((n + kWarps - 1) / kWarps);
+      const int segs = request_tiles<S>(a, own) * a.kv_heads, n = segment_units(own, S::kUnitLog - 1);
+      units4 += segs * ((segment_units(own, S::kUnitLog) + kWarps - 1) / kWarps);
+      units4_half += segs * ((n + kWarps - 1) / kWarps);
       n_segs += segs;
-      if (segs > 0) longest = max(longest, n);
+      if (segs > 0) longest = max(longest, n);          // in halves
     }
     units4 = __reduce_add_sync(0xffffffffu, units4);
+    units4_half = __reduce_add_sync(0xffffffffu, units4_half);
     n_segs = __reduce_add_sync(0xffffffffu, n_segs);
     longest = __reduce_max_sync(0xffffffffu, longest);
     if (!small) {
@@ -258,23 +261,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
         s_scan[warp] = units4;
         s_scan[4 + warp] = longest;
         s_scan[8 + warp] = n_segs;
+        s_scan[20 + warp] = units4_half;
       }
       __syncthreads();
       units4 = s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
       longest = max(max(s_scan[4], s_scan[5]), max(s_scan[6], s_scan[7]));
       n_segs = s_scan[8] + s_scan[9] + s_scan[10] + s_scan[11];
+      units4_half = s_scan[20] + s_scan[21] + s_scan[22] + s_scan[23];
     }
     if (units4 == 0) return;
+    // less than kShortUnits rounds for a warp: halves of units divide more evenly, and their latency is shorter
+    unit_log = units4 < kShortUnits * (int)gridDim.x ? S::kUnitLog - 1 : S::kUnitLog;
+    if (unit_log != S::kUnitLog) units4 = units4_half;
+    else longest = (longest + 1) / 2;
     // Few units: every CTA a piece of one segment, one unit a warp or as many as keep a segment's pieces under
-    // kMaxSplits.  Many: equal ranges, where a segment's fixed cost counts as kSegmentCost units, and at most
+    // kMaxSplits.  Many: equal ranges, where a segment's fixed cost counts as kSegmentCost keys, and at most
     // kMaxShares of them a segment.
     const bool few = units4 <= (int)gridDim.x;
     const int piece = kWarps * max(1, (longest + kWarps * kMaxSplits - 1) / (kWarps * kMaxSplits));
-    split = few ? Split{0, piece} : Split{kSegmentCost, 1};
+    split = few ? Split{0, piece} : Split{kSegmentCost >> unit_log, 1};
     int mine = 0;
     for (int i = b0; i < b1; ++i) {
       const Request r = per == 1 ? own : get_request(a, i, false);
-      mine += split.length(segment_units<S>(r)) * request_tiles<S>(a, r) * a.kv_heads;
+      mine += split.length(segment_units(r, unit_log)) * request_tiles<S>(a, r) * a.kv_heads;
     }
     int inc = mine;
 #pragma unroll
@@ -309,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
         int at = excl;
         for (int i = b0; i < b1; ++i) {
           const Request r = per == 1 ? own : get_request(a, i, false);
-          const int n = split.length(segment_units<S>(r)) * request_tiles<S>(a, r) * a.kv_heads;
+          const int n = split.length(segment_units(r, unit_log)) * request_tiles<S>(a, r) * a.kv_heads;
           if (u < at + n) {
             s_scan[16] = i;
             s_scan[17] = at;
@@ -336,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
   bool gave_up = false;
   while (u < u_end) {
     const Request rq = get_request(a, b, false);
-    const int n_seg = segment_units<S>(rq), tiles = request_tiles<S>(a, rq), len_seg = split.length(n_seg);
+    const int n_seg = segment_units(rq, unit_log), tiles = request_tiles<S>(a, rq), len_seg = split.length(n_seg);
     const int n_req = len_seg * tiles * a.kv_heads;
     if (u >= base + n_req) {
       base += n_req;
@@ -371,50 +380,50 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
     }
 
     // ---- this warp's units, and its first copies
-    const int unit0 = rq.begin / S::kUnitTokens;        // the segment's first unit
-    const int u_lo = max(s0, lo_any / S::kUnitTokens - unit0);
-    const int u_hi = hi_any < 0 ? u_lo : min(s1, hi_any / S::kUnitTokens + 1 - unit0);
+    const int unit0 = rq.begin >> unit_log;             // the segment's first unit
+    const int u_lo = max(s0, (lo_any >> unit_log) - unit0);
+    const int u_hi = hi_any < 0 ? u_lo : min(s1, (hi_any >> unit_log) + 1 - unit0);
     const int my_n = u_lo + warp < u_hi ? (u_hi - u_lo - warp + kWarps - 1) / kWarps : 0;
     const int32_t* trow = a.table + (size_t)b * a.width;
-    const bool whole = a.page_size % S::kUnitTokens == 0;   // a unit lies in one page
-    const int t_first = (unit0 + u_lo + warp) * S::kUnitTokens;
-    constexpr int kStep = kWarps * S::kUnitTokens;
+    const int u_groups = 1 << (unit_log - 4), u_all = (1 << u_groups) - 1;
+    const bool whole = (a.page_size & ((1 << unit_log) - 1)) == 0;   // a unit lies in one page
+    const int t_first = (unit0 + u_lo + warp) << unit_log, t_step = kWarps << unit_log;
     const uint8_t* src_head = a.pages + (size_t)kvh * (a.page_size / kKvGroup) * L::kGroupBytes;
     const size_t page_bytes = (size_t)a.kv_heads * (a.page_size / kKvGroup) * L::kGroupBytes;
-    // The pages of the groups of kAhead units are looked up with one load, a lane a group (-1: not there, or not to be
-    // read), kAhead units before the first of them is needed.
-    constexpr int kAhead = 32 / S::kUnitGroups;
-    const int my_group = lane % S::kUnitGroups;
+    // The pages of the groups of `ahead` units are looked up with one load, a lane a group (-1: not there, or not to be
+    // read), `ahead` units before the first of them is needed.
+    const int ahead = 32 >> (unit_log - 4);
+    const int my_group = lane & (u_groups - 1);
     auto look_up = [&](int k0) -> int {
-      const int k = k0 + lane / S::kUnitGroups, t = t_first + k * kStep + my_group * kKvGroup;
+      const int k = k0 + (lane >> (unit_log - 4)), t = t_first + k * t_step + my_group * kKvGroup;
       if (k >= my_n || t > hi_any || t + kKvGroup <= lo_any) return -1;
       const int page = trow[t / a.page_size];
       if (page >= 0 && page < a.num_pages) return page;
       atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
       return -1;
     };
-    int pages_now = look_up(0), pages_next = look_up(kAhead);
+    int pages_now = look_up(0), pages_next = look_up(ahead);
     int issued = 0;                                     // units whose copies have been started
     // where the lane's group of the next unit lies in its page, advanced without a division
     int g_off = (t_first + my_group * kKvGroup) % a.page_size;
-    const int step_off = kStep % a.page_size;
+    const int step_off = t_step % a.page_size;
     // Starts the copies of the next unit into ring slot `to`; returns which of its groups come.
     auto issue = [&](uint32_t to) -> uint32_t {
-      const int at = issued % kAhead;
-      int page = __shfl_sync(0xffffffffu, pages_now, at * S::kUnitGroups + my_group);
-      if (lane >= S::kUnitGroups) page = -1;
+      const int at = issued & (ahead - 1);
+      int page = __shfl_sync(0xffffffffu, pages_now, (at << (unit_log - 4)) + my_group);
+      if (lane >= u_groups) page = -1;
       const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
-      const bool one = whole && have == (1u << S::kUnitGroups) - 1u;
+      const bool one = whole && have == (uint32_t)u_all;
       if (lane == 0) mbar_arrive_expect_tx(&bars[to], __popc(have) * L::kGroupBytes);
       __syncwarp();
       if (page >= 0 && (lane == 0 || !one))
         bulk_g2s(ring + to * S::kUnitBytes + lane * L::kGroupBytes,
-                 src_head + page * page_bytes + (g_off / kKvGroup) * L::kGroupBytes, one ? S::kUnitBytes : L::kGroupBytes,
+                 src_head + page * page_bytes + (g_off / kKvGroup) * L::kGroupBytes, one ? u_groups * L::kGroupBytes : L::kGroupBytes,
                  &bars[to]);
       ++issued;
-      if (at == kAhead - 1) {
+      if (at == ahead - 1) {
         pages_now = pages_next;
-        pages_next = look_up(issued + kAhead);
+        pages_next = look_up(issued + ahead);
       }
       g_off += step_off;
       if (g_off >= a.page_size) g_off -= a.page_size;
@@ -479,11 +488,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
       f[t][1] = s_f[t * 8 + (lane & 3) * 2 + 1];
     }
     int t_unit = t_first;
-    for (int k = 0; k < my_n; ++k, t_unit += kStep) {
+    for (int k = 0; k < my_n; ++k, t_unit += t_step) {
       gave_up = !mbar_wait(&bars[slot], phase) || gave_up;
       const uint32_t have = coming[0];
       const uint8_t* unit = ring + slot * S::kUnitBytes;
-      for (int gi = 0; gi < S::kUnitGroups; gi += S::kPair) {
+      for (int gi = 0; gi < u_groups; gi += S::kPair) {
         const uint32_t there = (have >> gi) & ((1u << S::kPair) - 1u);
         if (there == 0u) continue;
         const uint8_t* g = unit + gi * L::kGroupBytes;
@@ -784,7 +793,7 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens,
   // the decode kernel counts its units (32 keys of a row tile, with their overhead) in 31 bits; this is the most there
   // can be, whatever cu_q and kv_lens hold
   const long long most_units = ((long long)tokens * group / 8 + batch) * cache->kv_heads *
-                               ((long long)table_width * cache->page_size / 32 + 2 + kSegmentCost + kWarps);
+                               ((long long)table_width * cache->page_size / 32 + 2 + kSegmentCost / 32 + kWarps);
   cudaError_t e;
   if (rows > kTcRows || most_units > 0x7FFFFFFFll)
     e = nvfp4_internal_kv_attention_tc(a, cache->head_dim, dtype, stream);
