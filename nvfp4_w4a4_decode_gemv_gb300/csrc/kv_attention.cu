@@ -744,6 +744,9 @@ cudaError_t dispatch(const AttnArgs& a, int rows, cudaStream_t stream) {
   return launch<D, 4, T>(a, stream);
 }
 
+// Whether a workspace has the many-row kernel's records: calls of fewer rows hardly reach it.
+bool room_for_pieces(int tokens, int group) { return (long long)tokens * group > kTcRows; }
+
 }  // namespace
 
 nvfp4_status nvfp4_internal_cuda_status(cudaError_t e);
@@ -753,7 +756,8 @@ nvfp4_status nvfp4_internal_check_device();
 extern "C" size_t nvfp4_kv_attention_workspace_bytes(int batch, int tokens, int heads, int kv_heads, int head_dim) {
   if (batch < 1 || tokens < 0 || nvfp4_kv_page_bytes(16, kv_heads, head_dim) == 0) return 0;
   if (heads < kv_heads || heads % kv_heads != 0 || heads / kv_heads > 64) return 0;
-  return kCounterBytes + (size_t)2 * kMaxCtas * Shape<128, 4>::kRecord * sizeof(float);
+  const size_t decode = (size_t)2 * kMaxCtas * Shape<128, 4>::kRecord, many = (size_t)kTcPieces * kTcRecord;
+  return kCounterBytes + (room_for_pieces(tokens, heads / kv_heads) && many > decode ? many : decode) * sizeof(float);
 }
 
 extern "C" nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens, int64_t q_token_stride,
@@ -788,7 +792,8 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens,
   const AttnArgs a = {q, q_token_stride, q_head_stride, cache->pages, cache->k_global, cache->v_global,
                       block_table, kv_lens, cu_q, out, lse, static_cast<unsigned int*>(workspace),
                       reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes), tokens, heads,
-                      cache->kv_heads, group, cache->page_size, cache->num_pages, table_width, batch, window, scale};
+                      cache->kv_heads, group, cache->page_size, cache->num_pages, table_width, batch, window,
+                      room_for_pieces(tokens, group) ? kTcPieces : 0, scale};
   const int rows = cu_q ? (int)((long long)max_q * group < 1 << 20 ? max_q * group : 1 << 20) : group;
   // the decode kernel counts its units (32 keys of a row tile, with their overhead) in 31 bits; this is the most there
   // can be, whatever cu_q and kv_lens hold

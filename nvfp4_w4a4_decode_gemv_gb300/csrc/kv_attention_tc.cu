@@ -24,7 +24,10 @@
 // weights refer to moves only when a row's scores exceed it by 2^13 (then O is
 // rescaled in TMEM); up to there FP16 holds the weights as exactly as below 1.
 // Every wait is bounded and an abort flag ends the others.
-// Tiles are handed out from a counter, the longest of a request first.
+// Tiles are handed out from a counter, the longest of a request first.  Where there are fewer tiles than SMs, the
+// keys of each are cut into pieces of kMinSteps steps or more, which go through records in the workspace (128 KB
+// each), and a second launch merges them, all SMs at work on it (merged by the last piece to arrive instead, one
+// CTA read up to 32 records: 115 us for 128 rows over 16000 keys, 64/8 heads).
 #include <math.h>
 
 #include "kv_attention.cuh"
@@ -59,9 +62,12 @@ struct Shape {
   static constexpr int kOffRaw = 5 * kTile;               // [kRing]
   static constexpr int kOffBar = kOffRaw + kRing * kRaw;
   static constexpr int kBars = 2 * kRing + 2 + 4 + 6 + 1;
-  static constexpr int kOffWords = kOffBar + kBars * 8;   // TMEM address, abort flag, two tiles, groups present (kRing + 2)
-  static constexpr int kOffMax = kOffWords + 16 * 4;      // [2 steps][2 halves][2 threads][kHalfRows] maxima, then sums
+  static constexpr int kOffWords = kOffBar + kBars * 8;   // TMEM address, abort flag, two tiles (5 each), groups
+                                                          // present (kRing + 2), pieces
+  static constexpr int kOffMax = kOffWords + 32 * 4;      // [2 steps][2 halves][2 threads][kHalfRows] maxima, then sums
   static constexpr int kOffF = kOffMax + 8 * kHalfRows * 4;   // [2][kHalfRows] score factors
+  static constexpr int kRecord = kRows * (D + 2);         // floats of a piece's record: O, then the maxima in use, then the sums
+  static_assert(kRecord <= kTcRecord, "the workspace");
   static constexpr int kSmem = kOffF + kRows * 4 + 1024; // + alignment of the swizzled panels
   // instruction descriptors: FP32 accumulator, FP16 operands, M = 128; N = keys, and N = D with B's rows contiguous
   static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | ((uint32_t)(kHalfRows >> 4) << 24);
@@ -152,8 +158,41 @@ NVFP4_DEVINL bool wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_
   return false;
 }
 
+constexpr int kMinSteps = 4;            // below this a record costs more than the piece saves
+
 struct Tile {
   int b, kvh, row0;
+};
+
+// Row tiles of a request.
+NVFP4_DEVINL int request_tiles(const AttnArgs& a, const Request& r) {
+  return (int)(((long long)r.rows * a.group + kRows - 1) / kRows);
+}
+
+// Tiles there are, and the pieces each is cut into at most: the SMs once over, or twice where that leaves much less
+// of a last round idle.  One warp.
+NVFP4_DEVINL int count_pieces(const AttnArgs& a, int sms, int lane, bool report, long long& tiles) {
+  long long n = 0;
+  for (int b = lane; b < a.batch; b += 32) n += (long long)request_tiles(a, get_request(a, b, report)) * a.kv_heads;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  tiles = n;
+  if (n == 0 || n > a.pieces) return 1;
+  const int t = (int)n, once = max(min(sms, a.pieces) / t, 1), twice = min(2 * sms, a.pieces) / t;
+  return 5 * once < 2 * twice ? twice : once;             // 2 / twice < 0.8 / once
+}
+
+// The steps of a tile and how many of them a piece has.
+struct Steps {
+  int lo, hi, first, all, piece;                          // keys [lo, hi]; first step, steps, steps of a piece
+  NVFP4_DEVINL Steps(const AttnArgs& a, const Request& rq, int row0, int n_rows, int pieces) {
+    const int p_first = rq.len - rq.rows + row0 / a.group;
+    hi = rq.len - rq.rows + (row0 + n_rows - 1) / a.group;
+    lo = a.window > 0 ? max(p_first - a.window + 1, 0) : 0;
+    first = lo / kKeys;
+    all = hi < 0 ? 0 : hi / kKeys + 1 - first;
+    piece = max(kMinSteps, (all + pieces - 1) / pieces);
+  }
 };
 
 // Tile number t -> request, kv head and first row (b = -1: there is no such tile).  One warp; the requests are
@@ -162,10 +201,7 @@ NVFP4_DEVINL Tile find_tile(const AttnArgs& a, long long t, int lane) {
   long long before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     int tiles = 0;
-    if (b0 + lane < a.batch) {
-      const Request r = get_request(a, b0 + lane, t == 0);
-      tiles = (int)(((long long)r.rows * a.group + kRows - 1) / kRows);
-    }
+    if (b0 + lane < a.batch) tiles = request_tiles(a, get_request(a, b0 + lane, false));
     long long inc = (long long)tiles * a.kv_heads;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -291,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
   volatile uint32_t* words = reinterpret_cast<volatile uint32_t*>(smem + S::kOffWords);
   volatile uint32_t* abort_flag = words + 1;
   volatile int* s_tile = reinterpret_cast<volatile int*>(words + 2);
-  volatile uint32_t* raw_have = words + 8;              // [kRing] groups that a raw step brings
-  volatile uint32_t* kv_have = words + 8 + kRing;       // [2]
+  volatile uint32_t* raw_have = words + 12;              // [kRing] groups that a raw step brings
+  volatile uint32_t* kv_have = words + 12 + kRing;       // [2]
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -330,32 +366,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
   uint32_t step = 0, step_b = 0, tiles = 0;
   uint32_t copied = 0;                                  // steps whose copies this warp has started
 
-  // the copy warp takes the tiles from the counter, each while the one before it is worked on
+  volatile uint32_t* s_pieces = words + 12 + kRing + 2; // pieces a tile is cut into, at most
+  // the copy warp takes the pieces of tiles from the counter, each while the one before it is worked on
   auto take_tile = [&](uint32_t n) {
-    long long t = 0;
+    uint32_t t = 0;
     if (lane == 0) t = atomicAdd(&a.counters[kTileCounter], 1u);
     t = __shfl_sync(0xffffffffu, t, 0);
-    const Tile tile = find_tile(a, t, lane);
+    const uint32_t pieces = *s_pieces;
+    const Tile tile = find_tile(a, t / pieces, lane);
     if (lane == 0) {
-      volatile int* to = s_tile + 3 * (n & 1u);
-      to[0] = tile.b, to[1] = tile.kvh, to[2] = tile.row0;
+      volatile int* to = s_tile + 5 * (n & 1u);
+      to[0] = tile.b, to[1] = tile.kvh, to[2] = tile.row0, to[3] = (int)(t % pieces), to[4] = (int)(t / pieces);
     }
   };
-  if (warp == kCopyWarp) take_tile(0);
+  if (warp == kCopyWarp) {
+    long long total;
+    const int pieces = count_pieces(a, gridDim.x, lane, blockIdx.x == 0, total);
+    if (lane == 0) *s_pieces = (uint32_t)pieces;
+    __syncwarp();
+    take_tile(0);
+  }
   __syncthreads();
+  const int pieces = (int)*s_pieces;
   for (;;) {
-    const volatile int* from = s_tile + 3 * (tiles & 1u);
-    const int b = from[0], kvh = from[1], row0 = from[2];
+    const volatile int* from = s_tile + 5 * (tiles & 1u);
+    const int b = from[0], kvh = from[1], row0 = from[2], piece = from[3], tile_no = from[4];
     if (b < 0) break;
     const Request rq = get_request(a, b, false);
     const int n_rows = (int)min((long long)kRows, (long long)rq.rows * a.group - row0);
     const bool both = n_rows > kHalfRows;
-    // keys that some row of the tile sees: [lo, hi]
-    const int p_first = rq.len - rq.rows + row0 / a.group;
-    const int hi = rq.len - rq.rows + (row0 + n_rows - 1) / a.group;
-    const int lo = a.window > 0 ? max(p_first - a.window + 1, 0) : 0;
-    const int step0 = lo / kKeys;
-    const int n = hi < 0 ? 0 : hi / kKeys + 1 - step0;  // steps of this tile
+    // a tile of one piece (also one without keys) is written at once
+    const Steps steps(a, rq, row0, n_rows, pieces);
+    const int lo = steps.lo, hi = steps.hi;               // keys that some row of the tile sees
+    const bool whole = steps.all <= steps.piece, idle = piece > 0 && piece * steps.piece >= steps.all;
+    const int step0 = steps.first + piece * steps.piece;
+    const int n = idle ? 0 : min(steps.piece, steps.all - piece * steps.piece);
+    const int record = tile_no * pieces;                // of the tile's first piece
 
     if (warp < kSoftWarps) {
       // ================ softmax of a half: two threads a row, `part` 0 and 1 ================
@@ -363,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t col_s = tmem + kColHalf * half + 64 * part + lanes, col_o = tmem + kColHalf * half + kColO + lanes;
       const int row = row0 + row_h + r;
-      const bool used = half == 0 || both, mine = row_h + r < n_rows;
+      const bool used = (half == 0 || both) && !idle, mine = row_h + r < n_rows;
       const int tok = rq.first + row / a.group, head = kvh * a.group + row % a.group;
       float* s_max = reinterpret_cast<float*>(smem + S::kOffMax) + half * 2 * kHalfRows + r;   // + part, + step
       constexpr int kStepMax = 4 * kHalfRows;
@@ -516,6 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
         tc_fence_after();
         const float inv = l > 0.0f ? vg / l : 0.0f;
         uint16_t* out = a.out + ((size_t)tok * a.heads + head) * D;
+        float* rec = a.records + (size_t)(record + piece) * S::kRecord;
+        const int rt = row_h + r;                       // row in the tile
 #pragma unroll 1
         for (int i = part * (D / 2); i < (part + 1) * (D / 2); i += 32) {
           uint32_t o[32];
@@ -526,7 +574,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = 0u;
           }
-          if (mine) {
+          if (mine && !whole) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              __stcg(reinterpret_cast<float4*>(rec + (size_t)rt * D + i + j),
+                     make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]), __uint_as_float(o[j + 2]),
+                                 __uint_as_float(o[j + 3])));
+          } else if (mine) {
 #pragma unroll
             for (int j = 0; j < 32; j += 8) {
               uint32_t w[4];
@@ -540,8 +594,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
             }
           }
         }
-        if (mine && part == 0 && a.lse)
+        if (mine && part == 0 && whole && a.lse)
           a.lse[(size_t)tok * a.heads + head] = l > 0.0f ? (m + log2f(l)) / kLog2e : -INFINITY;
+        if (mine && part == 0 && !whole) {
+          __stcg(rec + kRows * D + rt, m);
+          __stcg(rec + kRows * (D + 1) + rt, l);
+        }
       }
       tc_fence_before();
     } else if (warp < kCopyWarp) {
@@ -694,6 +752,62 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
   }
 }
 
+// Merges the records of tiles that were cut, kMergeRows rows of a tile at a time.
+constexpr int kMergeRows = 32, kMergeThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) kv_attention_merge_kernel(const AttnArgs a, int sms) {
+  using S = Shape<D>;
+  __shared__ int s_info[6];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, lane = tid & 31;
+  long long tiles = 0;
+  const int pieces = count_pieces(a, sms, lane, false, tiles);
+  if (pieces <= 1) return;
+  constexpr int kParts = kRows / kMergeRows;
+  const float vg = *a.v_global;
+  for (int item = blockIdx.x; item < (int)tiles * kParts; item += gridDim.x) {
+    const int tile_no = item / kParts, r0 = item % kParts * kMergeRows;
+    __syncthreads();
+    if (tid < 32) {
+      const Tile tile = find_tile(a, tile_no, lane);
+      if (lane == 0) s_info[0] = tile.b, s_info[1] = tile.kvh, s_info[2] = tile.row0;
+    }
+    __syncthreads();
+    const int b = s_info[0], kvh = s_info[1], row0 = s_info[2];
+    const Request rq = get_request(a, b, false);
+    const int n_rows = (int)min((long long)kRows, (long long)rq.rows * a.group - row0);
+    const Steps steps(a, rq, row0, n_rows, pieces);
+    if (steps.all <= steps.piece) continue;
+    const int n_rec = (steps.all + steps.piece - 1) / steps.piece;
+    for (int e = tid; e < kMergeRows * (D / 4); e += kMergeThreads) {
+      const int rt = r0 + e / (D / 4), d = e % (D / 4) * 4;
+      if (rt >= n_rows) break;
+      const float* rec = a.records + (size_t)tile_no * pieces * S::kRecord;
+      float mx = -INFINITY, l = 0.0f;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int q = 0; q < n_rec; ++q, rec += S::kRecord) {
+        const float m = __ldcg(rec + kRows * D + rt), lq = __ldcg(rec + kRows * (D + 1) + rt);
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(rec + (size_t)rt * D + d));
+        if (m == -INFINITY) continue;
+        const float mn = fmaxf(mx, m), back = ex2(mx - mn), w = ex2(m - mn);
+        mx = mn;
+        l = fmaf(lq, w, l * back);
+        x.x = fmaf(y.x, w, x.x * back), x.y = fmaf(y.y, w, x.y * back);
+        x.z = fmaf(y.z, w, x.z * back), x.w = fmaf(y.w, w, x.w * back);
+      }
+      const int row = row0 + rt, tok = rq.first + row / a.group, head = kvh * a.group + row % a.group;
+      const float inv = l > 0.0f ? vg / l : 0.0f;
+      const __nv_bfloat162 x0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), x1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
+      *reinterpret_cast<uint2*>(a.out + ((size_t)tok * a.heads + head) * D + d) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1));
+      if (a.lse && d == 0) a.lse[(size_t)tok * a.heads + head] = l > 0.0f ? (mx + log2f(l)) / kLog2e : -INFINITY;
+    }
+  }
+}
+
 template <int D, class T>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   using S = Shape<D>;
@@ -711,9 +825,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     return sms > 0 ? sms : 1;
   }, &err);
   if (grid == 0) return err;
-  const long long most = ((long long)a.tokens * a.group / kRows + a.batch) * a.kv_heads;   // tiles there can be
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(most < grid ? most : grid));
+  cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = stream;
@@ -722,7 +835,13 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_attention_tc_kernel<D, T>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_tc_kernel<D, T>, a);
+  if (e != cudaSuccess || a.pieces == 0) return e;
+  // whether anything was cut only the GPU knows: the launch ends at once if not
+  cfg.gridDim = dim3((unsigned)(4 * grid));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, kv_attention_merge_kernel<D>, a, grid);
 }
 
 }  // namespace
