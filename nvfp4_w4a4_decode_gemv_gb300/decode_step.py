@@ -84,7 +84,7 @@ class DecodeStep:
         w = self.weights[layer]
         api.nvfp4_rms_norm_quantize(h_in, eps=self.eps, out=self.xq, r_out=self.r_out(trace), stream=stream)
         api.nvfp4_gemv_smallm_packed(self.xq, w["qkv"], y=self.y_qkv, workspace=self.ws, stream=stream)
-        api.nvfp4_quantize_f32(self.y_qkv, K=self.k_o, out=self.xq_o, stream=stream)
+        self._attend(layer, stream)
         api.nvfp4_gemv_smallm_packed(self.xq_o, w["o"], y=self.y_o, workspace=self.ws, stream=stream)
         if trace is not None:
             nv = lambda t: (t.codes.clone(), t.scales.clone(), t.global_scale.clone())
@@ -99,6 +99,10 @@ class DecodeStep:
                               "xq_d": (self.xq_d.codes.clone(), self.xq_d.scales.clone(),
                                        self.xq_d.global_scale.clone()),
                               "h_out": self.h.clone()})
+
+    def _attend(self, layer: int, stream):
+        """From the qkv output to the o projection's NVFP4 input: here the query part alone (no attention)."""
+        api.nvfp4_quantize_f32(self.y_qkv, K=self.k_o, out=self.xq_o, stream=stream)
 
     def r_out(self, trace):
         """Where the fused normalize+quantize launches put their BF16 rows: only
@@ -117,6 +121,9 @@ class DecodeStep:
         api.nvfp4_bf16_gemv_tc(self.r, self.lm_head, y=self.logits, workspace=self.ws, stream=stream)
         if trace is not None:
             trace.append({"h_final": h_in.clone(), "r_final": self.r.clone(), "logits": self.logits.clone()})
+        return self._sample(stream)
+
+    def _sample(self, stream):
         return self.sampler(self.logits, self.step_start, self.u, stream=stream)
 
     def capture(self):

@@ -1,0 +1,107 @@
+"""A decode step as a server runs it: the synthetic Qwen3-shaped step with its
+KV cache, attention and logit rules.
+
+    plan   page for each request's new token          nvfp4_kv_plan
+    per layer, between the qkv and o projections:
+        K, V columns of qkv -> the 4-bit cache        nvfp4_kv_append
+        q columns over it -> BF16                     nvfp4_kv_attention
+        -> NVFP4                                      nvfp4_quantize_act
+    logits -> penalties, biases, grammar masks        nvfp4_process_logits (in place)
+    -> ReSET sampler; the token joins its request's history
+
+Every layer has a cache of its own; one page table serves them all (a page has
+the same number in each).  Requests come with `start` (prompts, whose K and V
+rows the caller gives) and go with `end`, whose pages the next requests get.
+No rotary positions: the step is synthetic, and `plan.positions` is where a
+model takes them from.  The step itself (`run`, `capture`) reads lengths, tables
+and histories on the device only, so one captured graph follows any requests.
+"""
+import torch
+
+from . import api
+from .decode_step import DecodeStep
+
+
+class ServingStep(DecodeStep):
+    def __init__(self, M: int, layers: int, heads: int, kv_heads: int, head_dim: int = 128, page_size: int = 64,
+                 num_pages: int = 1024, max_len: int = 32768, k_global: float = 1.0, v_global: float = 1.0, **kw):
+        super().__init__(M, layers, **kw)
+        if self.k_o != heads * head_dim or self.n_qkv != (heads + 2 * kv_heads) * head_dim:
+            raise ValueError("the qkv and o shapes do not fit the heads")
+        dev, i32 = self.device, dict(dtype=torch.int32, device=self.device)
+        self.heads, self.kv_heads, self.head_dim, self.page_size, self.max_len = heads, kv_heads, head_dim, page_size, max_len
+        self.caches = [api.NVFP4KVCache.empty(num_pages, page_size, kv_heads, head_dim, k_global, v_global, dev)
+                       for _ in range(layers)]
+        # requests: keys held, page table, stack of free pages
+        self.lens = torch.zeros(M, **i32)
+        self.ones = torch.ones(M, **i32)
+        self.table = torch.full((M, -(-max_len // page_size)), -1, **i32)
+        self.free_pages = torch.arange(num_pages, **i32)
+        self.free_count = torch.full((1,), num_pages, **i32)
+        self.plan = api.KVPlan.empty(M, M, dev, free_count=self.free_count)
+        # token histories and rules
+        self.tokens = torch.zeros((M, max_len), **i32)
+        self.n_tokens, self.n_prompt = torch.zeros(M, **i32), torch.zeros(M, **i32)
+        self.rows = torch.arange(M, device=dev)
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.repetition, self.presence, self.frequency = torch.ones(M, **f32), torch.zeros(M, **f32), torch.zeros(M, **f32)
+        self.bias_ids = self.bias_values = self.mask = self.mask_rows = None
+        # views and buffers of the attention
+        cut = heads * head_dim
+        self.q = self.y_qkv[:, :cut].unflatten(-1, (heads, head_dim))
+        self.k = self.y_qkv[:, cut:cut + kv_heads * head_dim].unflatten(-1, (kv_heads, head_dim))
+        self.v = self.y_qkv[:, cut + kv_heads * head_dim:].unflatten(-1, (kv_heads, head_dim))
+        self.attn = torch.empty((M, heads, head_dim), dtype=torch.bfloat16, device=dev)
+        need = api.nvfp4_kv_attention_workspace_bytes(M, M, heads, kv_heads, head_dim)
+        self.attn_ws = torch.zeros(need, dtype=torch.uint8, device=dev)
+
+    # ---- requests -----------------------------------------------------------------
+    def start(self, prompts: dict, keys, values):
+        """New requests: {row: prompt tokens (1-D int32 on the device)}; keys[layer], values[layer]: their K and V
+        rows [total, kv_heads, head_dim], packed in row order.  Returns the plan (its info: refused, tokens)."""
+        new = torch.zeros(self.M, dtype=torch.int32)
+        for row, ids in prompts.items():
+            new[row] = ids.numel()
+        plan = api.KVPlan.empty(self.M, int(new.sum()), self.device, free_count=self.free_count)
+        api.nvfp4_kv_plan(self.lens, new.to(self.device), self.table, self.free_pages, self.free_count, self.page_size,
+                          out=plan)
+        for cache, k, v in zip(self.caches, keys, values):
+            api.nvfp4_kv_append(k, v, plan.slots, cache)
+        self.lens.copy_(plan.kv_lens)
+        for row, ids in prompts.items():
+            self.tokens[row, :ids.numel()] = ids
+            self.n_tokens[row] = self.n_prompt[row] = ids.numel()
+        return plan
+
+    def end(self, ended: torch.Tensor):
+        """Requests with ended[row] != 0 (uint8 [M]) leave; their pages are free again."""
+        api.nvfp4_kv_release(self.lens, ended, self.table, self.free_pages, self.free_count, self.page_size)
+        stay = (ended == 0).to(torch.int32)
+        for t in (self.lens, self.n_tokens, self.n_prompt):
+            t.mul_(stay)
+
+    # ---- the step -----------------------------------------------------------------
+    def _attend(self, layer: int, stream):
+        cache = self.caches[layer]
+        api.nvfp4_kv_append(self.k, self.v, self.plan.slots, cache, stream=stream)
+        api.nvfp4_kv_attention(self.q, cache, self.table, self.plan.kv_lens, out=self.attn, workspace=self.attn_ws,
+                               stream=stream)
+        api.nvfp4_quantize_act(self.attn.view(self.M, self.k_o), out=self.xq_o, stream=stream)
+
+    def _sample(self, stream):
+        api.nvfp4_process_logits(self.logits, self.tokens, self.n_tokens, self.n_prompt, self.repetition, self.presence,
+                                 self.frequency, self.bias_ids, self.bias_values, self.mask, self.mask_rows,
+                                 out=self.logits, stream=stream)
+        return super()._sample(stream)
+
+    def run(self, stream=None, trace=None):
+        """One decode step of every request: h_in, u, step_start -> sampler.token; lengths and histories move on."""
+        with torch.cuda.stream(stream):
+            api.nvfp4_kv_plan(self.lens, self.ones, self.table, self.free_pages, self.free_count, self.page_size,
+                              out=self.plan, stream=stream)
+            out = super().run(stream, trace)
+            self.lens.copy_(self.plan.kv_lens)
+            at = self.n_tokens.clamp(max=self.max_len - 1).long()
+            self.tokens[self.rows, at] = self.sampler.token
+            self.n_tokens.add_(1).clamp_(max=self.max_len)
+        return out
