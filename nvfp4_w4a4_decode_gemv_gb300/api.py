@@ -340,8 +340,15 @@ ATTENTION_WS_ZEROED = 4096
 
 def _need(t, dtype, name, dim=None):
     """A contiguous CUDA tensor of one type (and rank), or ValueError."""
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or (dim is not None and t.dim() != dim):
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or (dim is not None and t.dim() != dim):
         raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}" + (f" with {dim} dimensions" if dim else ""))
+
+
+def _need_all(dtype, dim, names, *ts):
+    """_need of several tensors (None is left out); a name is looked up for the message only."""
+    for i, t in enumerate(ts):
+        if t is not None and (t.dtype is not dtype or t.dim() != dim or not t.is_cuda or not t.is_contiguous()):
+            _need(t, dtype, names.split()[i], dim)
 
 
 def nvfp4_kv_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
@@ -398,18 +405,17 @@ def nvfp4_kv_release(lens: torch.Tensor, ended: torch.Tensor, block_table: torch
                      stream=None) -> torch.Tensor:
     """Pushes the pages of the requests with ended[b] != 0 (lens[b] tokens each) onto the free stack; returns the
     new count (in place unless free_count_out is given)."""
-    for t, n, d in ((lens, "lens", 1), (block_table, "block_table", 2), (free_pages, "free_pages", 1),
-                    (free_count, "free_count", 1)):
-        _need(t, torch.int32, n, d)
-    _need(ended, torch.uint8, "ended", 1)
     out = free_count if free_count_out is None else free_count_out
-    _need(out, torch.int32, "free_count_out", 1)
+    i32 = torch.int32
+    _need_all(i32, 1, "lens free_pages free_count free_count_out", lens, free_pages, free_count, out)
+    _need(block_table, i32, "block_table", 2)
+    _need(ended, torch.uint8, "ended", 1)
     batch, width = block_table.shape
     if lens.numel() != batch or ended.numel() != batch or free_count.numel() != 1 or out.numel() != 1:
         raise ValueError("lens and ended need one entry a row of block_table, the counts one entry")
-    check(lib().nvfp4_kv_release(ptr(lens), ptr(ended), batch, page_size, ptr(block_table), width, ptr(free_pages),
-                                 free_pages.numel(), ptr(free_count), ptr(out), stream_handle(stream)),
-          "nvfp4_kv_release")
+    check(lib().nvfp4_kv_release(lens.data_ptr(), ended.data_ptr(), batch, page_size, block_table.data_ptr(), width,
+                                 free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), out.data_ptr(),
+                                 stream_handle(stream)), "nvfp4_kv_release")
     return out
 
 
@@ -419,23 +425,24 @@ def nvfp4_kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     """Takes pages for new_lens[b] tokens behind ctx_lens[b] (block_table updated in place) and maps every new token
     to its slot.  Without `out`, the outputs are new tensors for max_tokens tokens and free_count is updated in
     place; out.free_count may be free_count."""
-    for t, n, d in ((ctx_lens, "ctx_lens", 1), (new_lens, "new_lens", 1), (block_table, "block_table", 2),
-                    (free_pages, "free_pages", 1), (free_count, "free_count", 1)):
-        _need(t, torch.int32, n, d)
+    i32 = torch.int32
+    _need(block_table, i32, "block_table", 2)
+    _need_all(i32, 1, "ctx_lens new_lens free_pages free_count", ctx_lens, new_lens, free_pages, free_count)
     batch, width = block_table.shape
     if out is None:
         if max_tokens is None:
             raise ValueError("max_tokens is needed to allocate the outputs")
         out = KVPlan.empty(batch, max_tokens, ctx_lens.device, free_count)
-    for n in KVPlan.__slots__:
-        _need(getattr(out, n), torch.int32, n, 1)
+    _need_all(i32, 1, "slots positions cu_q kv_lens free_count info", out.slots, out.positions, out.cu_q, out.kv_lens,
+              out.free_count, out.info)
     if (ctx_lens.numel() != batch or new_lens.numel() != batch or out.kv_lens.numel() != batch
             or out.cu_q.numel() != batch + 1 or out.positions.numel() != out.slots.numel()
             or free_count.numel() != 1 or out.free_count.numel() != 1 or out.info.numel() != 2):
         raise ValueError("the lengths and outputs do not fit a batch of the block_table's rows")
-    check(lib().nvfp4_kv_plan(ptr(ctx_lens), ptr(new_lens), batch, page_size, ptr(block_table), width, ptr(free_pages),
-                              free_pages.numel(), ptr(free_count), ptr(out.free_count), ptr(out.kv_lens), ptr(out.cu_q),
-                              ptr(out.slots), ptr(out.positions), out.slots.numel(), ptr(out.info),
+    check(lib().nvfp4_kv_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), batch, page_size, block_table.data_ptr(), width,
+                              free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(),
+                              out.free_count.data_ptr(), out.kv_lens.data_ptr(), out.cu_q.data_ptr(),
+                              out.slots.data_ptr(), out.positions.data_ptr(), out.slots.numel(), out.info.data_ptr(),
                               stream_handle(stream)), "nvfp4_kv_plan")
     return out
 
@@ -459,8 +466,8 @@ def nvfp4_kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache
     if slots.numel() != tokens:
         raise ValueError("slots needs one entry a token")
     ks, vs = k.stride(), v.stride()
-    check(lib().nvfp4_kv_append(ptr(k), ptr(v), code, tokens, ks[0], ks[1], vs[0], vs[1], ptr(slots), cache.desc_ptr,
-                                stream_handle(stream)), "nvfp4_kv_append")
+    check(lib().nvfp4_kv_append(k.data_ptr(), v.data_ptr(), code, tokens, ks[0], ks[1], vs[0], vs[1], slots.data_ptr(),
+                                cache.desc_ptr, stream_handle(stream)), "nvfp4_kv_append")
 
 
 def nvfp4_kv_read(cache: NVFP4KVCache, slots: torch.Tensor, k_out: torch.Tensor | None = None,
@@ -474,8 +481,8 @@ def nvfp4_kv_read(cache: NVFP4KVCache, slots: torch.Tensor, k_out: torch.Tensor 
         _need(t, torch.bfloat16, n)
         if t.shape != shape:
             raise ValueError(f"{n} must have shape {shape}")
-    check(lib().nvfp4_kv_read(cache.desc_ptr, ptr(slots), shape[0], ptr(k_out), ptr(v_out), stream_handle(stream)),
-          "nvfp4_kv_read")
+    check(lib().nvfp4_kv_read(cache.desc_ptr, slots.data_ptr(), shape[0], k_out.data_ptr(), v_out.data_ptr(),
+                              stream_handle(stream)), "nvfp4_kv_read")
     return k_out, v_out
 
 
@@ -541,11 +548,13 @@ def nvfp4_kv_attention(q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.
         workspace = _attention_workspace(
             nvfp4_kv_attention_workspace_bytes(batch, tokens, heads, cache.kv_heads, cache.head_dim), q.device, stream)
     qs = q.stride()
-    check(lib().nvfp4_kv_attention(ptr(q), code, tokens, qs[0], qs[1], heads, cache.desc_ptr, ptr(block_table), width,
-                                   ptr(kv_lens), ptr(cu_q), batch,
-                                   max_q if max_q is not None else 1 if cu_q is None else max(1, tokens),
-                                   scale if scale is not None else cache.head_dim ** -0.5, window, ptr(out), ptr(lse),
-                                   ptr(workspace), workspace.numel(), stream_handle(stream)), "nvfp4_kv_attention")
+    if max_q is None:
+        max_q = 1 if cu_q is None else max(1, tokens)
+    check(lib().nvfp4_kv_attention(q.data_ptr(), code, tokens, qs[0], qs[1], heads, cache.desc_ptr,
+                                   block_table.data_ptr(), width, kv_lens.data_ptr(), ptr(cu_q), batch, max_q,
+                                   scale if scale is not None else cache.head_dim ** -0.5, window, out.data_ptr(),
+                                   ptr(lse), workspace.data_ptr(), workspace.numel(), stream_handle(stream)),
+          "nvfp4_kv_attention")
     return out
 
 
@@ -563,15 +572,14 @@ def nvfp4_process_logits(logits: torch.Tensor, tokens: torch.Tensor | None = Non
     if code is None or not logits.is_cuda or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be a CUDA tensor [rows, V] of float32 or bfloat16 with adjacent elements")
     rows, V = logits.shape
-    for t, n, dt, d in ((tokens, "tokens", torch.int32, 2), (n_tokens, "n_tokens", torch.int32, 1),
-                        (n_prompt, "n_prompt", torch.int32, 1), (repetition, "repetition", torch.float32, 1),
-                        (presence, "presence", torch.float32, 1), (frequency, "frequency", torch.float32, 1),
-                        (bias_ids, "bias_ids", torch.int32, 2), (bias_values, "bias_values", torch.float32, 2),
-                        (mask_rows, "mask_rows", torch.int32, 1)):
-        if t is not None:
-            _need(t, dt, n, d)
-            if t.shape[0] != rows:
-                raise ValueError(f"{n} needs one entry a row of logits")
+    i32, f32 = torch.int32, torch.float32
+    _need_all(i32, 1, "n_tokens n_prompt mask_rows", n_tokens, n_prompt, mask_rows)
+    _need_all(f32, 1, "repetition presence frequency", repetition, presence, frequency)
+    _need_all(i32, 2, "tokens bias_ids", tokens, bias_ids)
+    _need_all(f32, 2, "bias_values", bias_values)
+    for t in (tokens, n_tokens, n_prompt, repetition, presence, frequency, bias_ids, bias_values, mask_rows):
+        if t is not None and t.shape[0] != rows:
+            raise ValueError("tokens, biases and the rows' parameters need one entry a row of logits")
     if (tokens is None) != (n_tokens is None) or (bias_ids is None) != (bias_values is None):
         raise ValueError("tokens and n_tokens, bias_ids and bias_values go together")
     if bias_ids is not None and bias_ids.shape != bias_values.shape:
@@ -587,10 +595,10 @@ def nvfp4_process_logits(logits: torch.Tensor, tokens: torch.Tensor | None = Non
         if out.shape != logits.shape:
             raise ValueError("out must have the shape of logits")
     check(lib().nvfp4_process_logits(
-        ptr(logits), code, rows, V, logits.stride(0) if rows > 1 else V, ptr(tokens),
+        logits.data_ptr(), code, rows, V, logits.stride(0) if rows > 1 else V, ptr(tokens),
         tokens.shape[1] if tokens is not None else 0, ptr(n_tokens), ptr(n_prompt), ptr(repetition), ptr(presence),
         ptr(frequency), ptr(bias_ids), ptr(bias_values), bias_ids.shape[1] if bias_ids is not None else 0, ptr(mask),
-        mask.shape[0] if mask is not None else 0, ptr(mask_rows), fill, ptr(out), stream_handle(stream)),
+        mask.shape[0] if mask is not None else 0, ptr(mask_rows), fill, out.data_ptr(), stream_handle(stream)),
         "nvfp4_process_logits")
     return out
 
