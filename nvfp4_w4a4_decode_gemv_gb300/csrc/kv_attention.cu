@@ -230,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
   fence_mbar_init();
   griddep_launch_dependents();
   griddep_wait();
+  fence_proxy_async_global();
 
   // ---- the split: this CTA's range and the request it starts in (all counts fit 31 bits: the host checks).
   // Up to 32 requests every warp works it out by itself, a request a lane; more are shared by the CTA's threads.

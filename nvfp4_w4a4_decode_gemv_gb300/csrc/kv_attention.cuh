@@ -27,6 +27,9 @@ struct AttnArgs {
   float scale;
 };
 
+// The cache's rows may come from the preceding kernel's ordinary stores: order them before this thread's bulk copies.
+NVFP4_DEVINL void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
 // ---- instructions ------------------------------------------------------------
 NVFP4_DEVINL float ex2(float x) {
   float y;

@@ -190,7 +190,7 @@ struct Steps {
     hi = rq.len - rq.rows + (row0 + n_rows - 1) / a.group;
     lo = a.window > 0 ? max(p_first - a.window + 1, 0) : 0;
     first = lo / kKeys;
-    all = hi < 0 ? 0 : hi / kKeys + 1 - first;
+    all = hi < 0 ? 0 : max(hi / kKeys + 1 - first, 0);
     piece = max(kMinSteps, (all + pieces - 1) / pieces);
   }
 };
@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
   }
   fence_mbar_init();
   griddep_wait();
+  fence_proxy_async_global();
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(const_cast<uint32_t*>(words))),

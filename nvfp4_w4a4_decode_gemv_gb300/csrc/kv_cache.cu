@@ -158,7 +158,7 @@ NVFP4_DEVINL void append_block(const AppendArgs& a, long long token, int slot, i
   float v[16];
   raw.values(v);
   uint2 c;
-  const uint32_t s = kv_quant_block(v, __ldg(which == 0 ? a.k_global : a.v_global), c);
+  const uint32_t s = kv_quant_block(v, *(which == 0 ? a.k_global : a.v_global), c);
   uint8_t* g = a.pages + kv_group_offset<D>(page, in, head, a.page_size, a.heads) + which * M::kHalf;
   *reinterpret_cast<uint32_t*>(g + M::codes(which, t, b, 0)) = c.x;
   *reinterpret_cast<uint32_t*>(g + M::codes(which, t, b, 1)) = c.y;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const AppendArgs
   const int h0 = blockIdx.y * a.heads_per_cta, nh = min(a.heads_per_cta, a.heads - h0);
   look_at_window(w, a.slots, a.tokens, i0, a.num_slots, blockIdx.y == 0);
   __syncthreads();
-  const float k_glob = __ldg(a.k_global), v_glob = __ldg(a.v_global);
+  const float k_glob = *a.k_global, v_glob = *a.v_global;
   const uint8_t kind = w.kind[lane & 15];
   const uint32_t alone = __ballot_sync(0xffffffffu, kind == kAlone);
   for (uint32_t lead = __ballot_sync(0xffffffffu, lane < 16 && kind == kLeads); lead != 0u; lead &= lead - 1u) {
@@ -269,7 +269,7 @@ NVFP4_DEVINL void read_half(const ReadArgs& a, long long token, int slot, int he
     const int page = slot / a.page_size, in = slot - page * a.page_size, t = slot % kKvGroup;
     const uint8_t* g = a.pages + kv_group_offset<D>(page, in, head, a.page_size, a.heads) + which * M::kHalf;
     c = __ldcg(reinterpret_cast<const uint32_t*>(g + M::codes(which, t, b, h)));
-    S = __fmul_rn(e4m3_to_f32(__ldcg(g + M::scale(which, t, b))), __ldg(which == 0 ? a.k_global : a.v_global));
+    S = __fmul_rn(e4m3_to_f32(__ldcg(g + M::scale(which, t, b))), *(which == 0 ? a.k_global : a.v_global));
   }
   *reinterpret_cast<uint4*>((which == 0 ? a.k_out : a.v_out) + (token * a.heads + head) * D + b * 16 + h * 8) =
       half_block(c, S);
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv_read_kernel(const ReadArgs a) 
   const int h0 = blockIdx.y * a.heads_per_cta, nh = min(a.heads_per_cta, a.heads - h0);
   look_at_window(w, a.slots, a.tokens, i0, a.num_slots, blockIdx.y == 0);
   __syncthreads();
-  const float k_glob = __ldg(a.k_global), v_glob = __ldg(a.v_global);
+  const float k_glob = *a.k_global, v_glob = *a.v_global;
   const uint8_t kind = w.kind[lane & 15];
   // tokens outside whole groups, padding among them (zeros)
   const uint32_t other = __ballot_sync(0xffffffffu, i0 + (lane & 15) < a.tokens && (kind == kAlone || kind == kNothing));

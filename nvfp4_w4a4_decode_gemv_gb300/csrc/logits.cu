@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(THREADS) process_logits_kernel(const LogitArgs
   if (a.vec_tok) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j)
-      if (tid + j * THREADS < a.history / 4) q[j] = __ldg(reinterpret_cast<const int4*>(tok) + tid + j * THREADS);
+      if (tid + j * THREADS < a.history / 4) q[j] = __ldcg(reinterpret_cast<const int4*>(tok) + tid + j * THREADS);
   }
   int used = 0, prompt = 0;
   float rep = 1.0f, pres = 0.0f, freq = 0.0f;
@@ -128,11 +128,11 @@ __global__ void __launch_bounds__(THREADS) process_logits_kernel(const LogitArgs
 #pragma unroll
         for (int j = 0; j < kBatch; ++j)
           if (p + (kBatch + j) * THREADS < pieces)
-            q[j] = __ldg(reinterpret_cast<const int4*>(tok) + p + (kBatch + j) * THREADS);
+            q[j] = __ldcg(reinterpret_cast<const int4*>(tok) + p + (kBatch + j) * THREADS);
       }
       i = 4 * pieces;
     }
-    for (i += tid; i < used; i += THREADS) count(__ldg(tok + i), i);
+    for (i += tid; i < used; i += THREADS) count(__ldcg(tok + i), i);
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < PIECES; ++k) {

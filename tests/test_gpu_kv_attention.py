@@ -328,3 +328,54 @@ def test_repeat_streams_and_graph():
         assert torch.equal(got, api.nvfp4_kv_attention(q, c, t, kv))
     assert torch.equal(first, out)
     assert api.device_status() == api.DEVERR_KV_RANGE      # request 1 has no pages for the 640 keys of the second replay
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_growing_scores_of_many_rows(D):
+    """Scores that rise along the keys by far more than FP16 holds, and fall again, for prompt rows: the maximum that
+    the weights refer to has to move again and again, and to stay."""
+    rng = np.random.default_rng(8)
+    page, n, m, H = 64, 900, 70, 4
+    c, k, v, pages = _cache(rng, 15, page, 1, D)
+    codes, scales = np.full((n, 1, D), 2, np.uint8), np.zeros((n, 1, D // 16), np.uint8)
+    ramp = np.concatenate([np.arange(600), 600 - 2 * np.arange(300)])
+    scales[:] = np.clip(8 + ramp // 6, 0, 118)[:, None, None]
+    _, _, vc, vs = S.read_slots(pages, np.arange(n), page, D)
+    S.write_slots(pages, np.arange(n), page, D, codes, scales, vc, vs)
+    c.pages.copy_(torch.from_numpy(pages))
+    k[:n] = S.dequantize_rows(codes, scales, 0.25)
+    t = torch.arange(15, dtype=torch.int32).cuda()[None]
+    q, _ = _queries(rng, m, H, D, torch.bfloat16, 0.02)
+    q = q * torch.tensor([1.0, -1.0, 30.0, 0.0], dtype=torch.bfloat16)[None, :, None]
+    q[:, :3] = torch.abs(q[:, :3]) * torch.sign(q[:, :3, :1])
+    q64 = Q.bf16_bits_to_f32(bits(q)).astype(np.float64)
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    cu = torch.tensor([0, m], dtype=torch.int32).cuda()
+    for max_q in (1, m):                                # both kernels
+        lse = torch.empty((m, H), device="cuda")
+        out = api.nvfp4_kv_attention(q.cuda(), c, t, lens, cu, max_q=max_q, lse=lse)
+        _check(out, lse, 0, q64, k[:n], v[:n], D ** -0.5, 0)
+    assert api.device_status() == 0
+
+
+def test_many_rows_few_tiles_are_cut_and_merged():
+    """Prompt rows of few tiles over many keys (pieces merged by a second launch), with a window, rows of the second
+    half missing, and lse; the same bits on repeat calls."""
+    for seed, lens, rows, heads, kvh, D, window in ((31, [3000], [40], 8, 2, 128, 0), (32, [2500, 1900], [33, 70], 4, 2, 64, 0),
+                                                   (33, [4000], [300], 2, 1, 64, 1500), (34, [1700], [90], 3, 1, 128, 700)):
+        _run(seed, lens, rows, heads, kvh, D, 64, window=window, max_q=1000)
+    rng = np.random.default_rng(35)
+    c, k, v, _ = _cache(rng, 50, 64, 2, 128)
+    t = torch.from_numpy(_table(rng, [3100], 64, 50)).cuda()
+    q, _ = _queries(rng, 64, 8, 128, torch.bfloat16, 1.0)
+    args = (q.cuda(), c, t, torch.tensor([3100], dtype=torch.int32).cuda(), torch.tensor([0, 64], dtype=torch.int32).cuda())
+    a = api.nvfp4_kv_attention(*args, max_q=64)
+    for _ in range(3):
+        assert torch.equal(a, api.nvfp4_kv_attention(*args, max_q=64))
+
+
+@pytest.mark.parametrize("batch", [33, 200])
+def test_prompt_rows_of_many_requests(batch):
+    """More requests than a warp counts at once, prompt chunks among single rows and empty requests."""
+    rows = [0 if i % 7 == 3 else 70 if i % 11 == 0 else 1 for i in range(batch)]
+    _run(batch, [max(r, (37 * i) % 200) for i, r in enumerate(rows)], rows, 4, 1, 64, 16, max_q=70)
