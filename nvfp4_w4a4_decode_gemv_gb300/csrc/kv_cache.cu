@@ -7,11 +7,13 @@
 //
 // The cache's order scatters a token's bytes over its 16-token group, and writes
 // of 1, 4 and 8 bytes cost L2 a 32-byte sector each (one thread a block, every
-// block on its own: 12.3 M sectors for 16384 tokens of 8 heads, 50 us).  So a CTA
-// looks at a window of 16 tokens, and where a whole group's 16 tokens follow one
-// another (prompts), a warp takes the group's K or V half: it quantizes into
-// shared memory and moves the half in 16-byte pieces.  Other tokens (single new
-// tokens, the ragged ends of prompts) go block by block.
+// block on its own: 12.3 M sectors for 16384 tokens of 8 heads, 50 us).  So a warp
+// takes the K or V rows of one head for a window of 16 tokens.  Where the 16 tokens
+// of a whole group follow one another (prompts) and the first of them is in the
+// window, it quantizes the group's half into shared memory and moves it in 16-byte
+// pieces.  Other tokens (single new tokens, the ragged ends of prompts) go block by
+// block.  A warp finds out by itself, with ballots: with a CTA looking together, its
+// barriers took a third of the time.
 #include <cuda_fp16.h>
 
 #include "kv_layout.cuh"
@@ -29,7 +31,7 @@ struct AppendArgs {
   const int32_t* slots;
   uint8_t* pages;
   const float *k_global, *v_global;
-  int tokens, heads, page_size, heads_per_cta;
+  int tokens, heads, page_size;
   long long num_slots;
 };
 
@@ -102,36 +104,32 @@ NVFP4_DEVINL uint32_t kv_quant_block(float (&v)[16], float g, uint2& codes) {
 }
 
 // ---- a window of 16 tokens --------------------------------------------------------
-enum : uint8_t { kAlone, kLeads, kCovered, kNothing };   // by itself; first of a whole group; in one; padding or bad
-
 struct Window {
-  int slot[48];                 // of tokens i0 - 16 .. i0 + 31
-  uint8_t kind[16];             // of tokens i0 .. i0 + 15
+  int slot;                     // lane 16 + k: the slot of the window's token k
+  uint32_t leads, alone, rest;  // bit k: token k is the first of a whole group, by itself, padding or bad
 };
 
-// Fills `w` (a barrier inside, one after it is the caller's).
-NVFP4_DEVINL void look_at_window(Window& w, const int32_t* slots, int tokens, long long i0, long long num_slots, bool report) {
-  const int tid = threadIdx.x;
-  if (tid < 48) {
-    const long long i = i0 - 16 + tid;
-    w.slot[tid] = i >= 0 && i < tokens ? slots[i] : -1;
-  }
-  __syncthreads();
-  if (tid < 16) {
-    const int s = w.slot[16 + tid];
-    uint8_t kind = kAlone;
-    if (s < 0 || s >= num_slots) {
-      kind = kNothing;
-      if (s != -1 && report) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
-    } else {
-      const int t = s % kKvGroup;
-      bool whole = true;
-#pragma unroll
-      for (int j = 0; j < kKvGroup; ++j) whole = whole && w.slot[16 + tid - t + j] == s - t + j;
-      if (whole) kind = t == 0 ? kLeads : kCovered;
-    }
-    w.kind[tid] = kind;
-  }
+// One warp looks at tokens i0 .. i0 + 15 and their neighbours.
+NVFP4_DEVINL Window look_at_window(const int32_t* slots, int tokens, long long i0, long long num_slots, int lane, bool report) {
+  const long long i = i0 - 16 + lane;
+  const int s = i >= 0 && i < tokens ? slots[i] : -1;
+  const int after = i + 32 < tokens ? slots[i + 32] : -1;
+  // bit j: token i0 - 16 + j's slot is followed by the next one
+  int next = __shfl_down_sync(0xffffffffu, s, 1);
+  const int first_after = __shfl_sync(0xffffffffu, after, 0), next_after = __shfl_down_sync(0xffffffffu, after, 1);
+  if (lane == 31) next = first_after;
+  const uint64_t run = (uint64_t)__ballot_sync(0xffffffffu, (uint32_t)next == (uint32_t)s + 1u) |
+                       (uint64_t)__ballot_sync(0xffffffffu, lane < 31 && (uint32_t)next_after == (uint32_t)after + 1u) << 32;
+  const bool in_window = lane >= 16 && i < tokens, valid = in_window && s >= 0 && s < num_slots;
+  const int t = s & (kKvGroup - 1);
+  const bool whole = valid && ((run >> (lane - t)) & 0x7FFFu) == 0x7FFFu;
+  if (in_window && !valid && s != -1 && report) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
+  Window w;
+  w.slot = s;
+  w.leads = __ballot_sync(0xffffffffu, whole && t == 0) >> 16;
+  w.alone = __ballot_sync(0xffffffffu, valid && !whole) >> 16;
+  w.rest = __ballot_sync(0xffffffffu, in_window && !valid) >> 16;
+  return w;
 }
 
 template <int D>
@@ -167,60 +165,67 @@ NVFP4_DEVINL void append_block(const AppendArgs& a, long long token, int slot, i
 
 constexpr int kWarps = kThreads / 32;
 
-// grid: (windows, head groups of a.heads_per_cta)
+// A warp's task: window, head, K or V, in this order.
+struct Task {
+  long long i0;
+  int head, which;
+  bool there;
+  NVFP4_DEVINL Task(int tokens, int heads) {
+    const long long n = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5), per = 2 * heads;
+    const long long window = n / per;
+    const int rest = (int)(n - window * per);
+    i0 = window * kKvGroup;
+    head = rest >> 1;
+    which = rest & 1;
+    there = i0 < tokens;
+  }
+};
+
 template <int D, class T>
 __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const AppendArgs a) {
   using M = Map<D>;
-  __shared__ Window w;
   __shared__ __align__(16) uint8_t s_half[kWarps][M::kHalf];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long i0 = (long long)blockIdx.x * kKvGroup;
-  const int h0 = blockIdx.y * a.heads_per_cta, nh = min(a.heads_per_cta, a.heads - h0);
-  look_at_window(w, a.slots, a.tokens, i0, a.num_slots, blockIdx.y == 0);
-  __syncthreads();
-  const float k_glob = *a.k_global, v_glob = *a.v_global;
-  const uint8_t kind = w.kind[lane & 15];
-  const uint32_t alone = __ballot_sync(0xffffffffu, kind == kAlone);
-  for (uint32_t lead = __ballot_sync(0xffffffffu, lane < 16 && kind == kLeads); lead != 0u; lead &= lead - 1u) {
-    const int k = __ffs(lead) - 1;
-    const long long token = i0 + k;
-    const int slot = w.slot[16 + k], page = slot / a.page_size, in = slot - page * a.page_size;
-    for (int task = warp; task < 2 * nh; task += kWarps) {
-      const int which = task & 1, head = h0 + (task >> 1);
-      const int b = lane % KvLayout<D>::kBlocks, t_lane = lane / KvLayout<D>::kBlocks;
-      const int64_t ts = which == 0 ? a.k_ts : a.v_ts;
-      const T* x = (which == 0 ? static_cast<const T*>(a.k) + head * a.k_hs : static_cast<const T*>(a.v) + head * a.v_hs) +
-                   token * ts + b * 16;
-      Raw<T> raw[M::kPasses];
+  const Task k(a.tokens, a.heads);
+  if (!k.there) return;
+  const Window w = look_at_window(a.slots, a.tokens, k.i0, a.num_slots, lane, k.head == 0 && k.which == 0);
+  const float glob = *(k.which == 0 ? a.k_global : a.v_global);
+  const int64_t ts = k.which == 0 ? a.k_ts : a.v_ts;
+  const T* rows = (k.which == 0 ? static_cast<const T*>(a.k) + k.head * a.k_hs : static_cast<const T*>(a.v) + k.head * a.v_hs) +
+                  k.i0 * ts;
+  const int b = lane % KvLayout<D>::kBlocks, t_lane = lane / KvLayout<D>::kBlocks;
+  for (uint32_t lead = w.leads; lead != 0u; lead &= lead - 1u) {
+    const int first = __ffs(lead) - 1;
+    Raw<T> raw[M::kPasses];
 #pragma unroll
-      for (int p = 0; p < M::kPasses; ++p) raw[p].load(x + (p * M::kPerPass + t_lane) * ts);
+    for (int p = 0; p < M::kPasses; ++p) raw[p].load(rows + (first + p * M::kPerPass + t_lane) * ts + b * 16);
+    const int slot = __shfl_sync(0xffffffffu, w.slot, 16 + first), page = slot / a.page_size, in = slot - page * a.page_size;
 #pragma unroll
-      for (int p = 0; p < M::kPasses; ++p) {
-        const int t = p * M::kPerPass + t_lane;
-        float v[16];
-        raw[p].values(v);
-        uint2 c;
-        const uint32_t s = kv_quant_block(v, which == 0 ? k_glob : v_glob, c);
-        *reinterpret_cast<uint32_t*>(&s_half[warp][M::codes(which, t, b, 0)]) = c.x;
-        *reinterpret_cast<uint32_t*>(&s_half[warp][M::codes(which, t, b, 1)]) = c.y;
-        s_half[warp][M::scale(which, t, b)] = (uint8_t)s;
-      }
-      __syncwarp();
-      uint8_t* g = a.pages + kv_group_offset<D>(page, in, head, a.page_size, a.heads) + which * M::kHalf;
-      for (int i = lane; i < M::kHalf / 16; i += 32)
-        reinterpret_cast<uint4*>(g)[i] = reinterpret_cast<const uint4*>(s_half[warp])[i];
-      __syncwarp();
+    for (int p = 0; p < M::kPasses; ++p) {
+      const int t = p * M::kPerPass + t_lane;
+      float v[16];
+      raw[p].values(v);
+      uint2 c;
+      const uint32_t s = kv_quant_block(v, glob, c);
+      *reinterpret_cast<uint32_t*>(&s_half[warp][M::codes(k.which, t, b, 0)]) = c.x;
+      *reinterpret_cast<uint32_t*>(&s_half[warp][M::codes(k.which, t, b, 1)]) = c.y;
+      s_half[warp][M::scale(k.which, t, b)] = (uint8_t)s;
     }
+    __syncwarp();
+    uint8_t* g = a.pages + kv_group_offset<D>(page, in, k.head, a.page_size, a.heads) + k.which * M::kHalf;
+    for (int i = lane; i < M::kHalf / 16; i += 32)
+      reinterpret_cast<uint4*>(g)[i] = reinterpret_cast<const uint4*>(s_half[warp])[i];
+    __syncwarp();
   }
-  if (alone == 0u) return;
+  if (w.alone == 0u) return;
   // the other tokens, block by block
-  const int items = kKvGroup * nh * 2 * KvLayout<D>::kBlocks;
-  for (int it = threadIdx.x; it < items; it += kThreads) {
-    const int b = it % KvLayout<D>::kBlocks, which = it / KvLayout<D>::kBlocks & 1, th = it / (2 * KvLayout<D>::kBlocks);
-    const int k = th % kKvGroup;
-    if (w.kind[k] == kAlone) append_block<D, T>(a, i0 + k, w.slot[16 + k], h0 + th / kKvGroup, which, b);
+#pragma unroll 1
+  for (int p = 0; p < M::kPasses; ++p) {
+    const int t = p * M::kPerPass + t_lane;
+    const int slot = __shfl_sync(0xffffffffu, w.slot, 16 + t);
+    if ((w.alone >> t) & 1u) append_block<D, T>(a, k.i0 + t, slot, k.head, k.which, b);
   }
 }
 
@@ -242,7 +247,7 @@ struct ReadArgs {
   const int32_t* slots;
   const float *k_global, *v_global;
   uint16_t *k_out, *v_out;
-  int tokens, heads, page_size, heads_per_cta;
+  int tokens, heads, page_size;
   long long num_slots;
 };
 
@@ -276,51 +281,44 @@ NVFP4_DEVINL void read_half(const ReadArgs& a, long long token, int slot, int he
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 4) kv_read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) kv_read_kernel(const ReadArgs a) {
   using M = Map<D>;
-  __shared__ Window w;
   __shared__ __align__(16) uint8_t s_half[kWarps][M::kHalf];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long i0 = (long long)blockIdx.x * kKvGroup;
-  const int h0 = blockIdx.y * a.heads_per_cta, nh = min(a.heads_per_cta, a.heads - h0);
-  look_at_window(w, a.slots, a.tokens, i0, a.num_slots, blockIdx.y == 0);
-  __syncthreads();
-  const float k_glob = *a.k_global, v_glob = *a.v_global;
-  const uint8_t kind = w.kind[lane & 15];
-  // tokens outside whole groups, padding among them (zeros)
-  const uint32_t other = __ballot_sync(0xffffffffu, i0 + (lane & 15) < a.tokens && (kind == kAlone || kind == kNothing));
-  for (uint32_t lead = __ballot_sync(0xffffffffu, lane < 16 && kind == kLeads); lead != 0u; lead &= lead - 1u) {
-    const int k = __ffs(lead) - 1;
-    const int slot = w.slot[16 + k], page = slot / a.page_size, in = slot - page * a.page_size;
-    for (int task = warp; task < 2 * nh; task += kWarps) {
-      const int which = task & 1, head = h0 + (task >> 1);
-      const uint8_t* g = a.pages + kv_group_offset<D>(page, in, head, a.page_size, a.heads) + which * M::kHalf;
-      for (int i = lane; i < M::kHalf / 16; i += 32)
-        reinterpret_cast<uint4*>(s_half[warp])[i] = __ldcg(reinterpret_cast<const uint4*>(g) + i);
-      __syncwarp();
-      // a lane takes half a block, so that a store of the warp is whole rows
-      constexpr int kHalves = 2 * KvLayout<D>::kBlocks, kTokens = 32 / kHalves;
-      const int hb = lane % kHalves, b = hb >> 1, h = hb & 1;
-      uint16_t* out = (which == 0 ? a.k_out : a.v_out) + ((i0 + k) * a.heads + head) * D + hb * 8;
+  const Task k(a.tokens, a.heads);
+  if (!k.there) return;
+  const Window w = look_at_window(a.slots, a.tokens, k.i0, a.num_slots, lane, k.head == 0 && k.which == 0);
+  const float glob = *(k.which == 0 ? a.k_global : a.v_global);
+  // a lane takes half a block, so that a store of the warp is whole rows
+  constexpr int kHalves = 2 * KvLayout<D>::kBlocks, kTokens = 32 / kHalves;
+  const int hb = lane % kHalves, b = hb >> 1, h = hb & 1;
+  uint16_t* rows = (k.which == 0 ? a.k_out : a.v_out) + (k.i0 * a.heads + k.head) * D + hb * 8;
+  for (uint32_t lead = w.leads; lead != 0u; lead &= lead - 1u) {
+    const int first = __ffs(lead) - 1;
+    const int slot = __shfl_sync(0xffffffffu, w.slot, 16 + first), page = slot / a.page_size, in = slot - page * a.page_size;
+    const uint8_t* g = a.pages + kv_group_offset<D>(page, in, k.head, a.page_size, a.heads) + k.which * M::kHalf;
+    for (int i = lane; i < M::kHalf / 16; i += 32)
+      reinterpret_cast<uint4*>(s_half[warp])[i] = __ldcg(reinterpret_cast<const uint4*>(g) + i);
+    __syncwarp();
 #pragma unroll
-      for (int p = 0; p < kKvGroup / kTokens; ++p) {
-        const int t = p * kTokens + lane / kHalves;
-        const uint32_t c = *reinterpret_cast<const uint32_t*>(&s_half[warp][M::codes(which, t, b, h)]);
-        const float S = __fmul_rn(e4m3_to_f32(s_half[warp][M::scale(which, t, b)]), which == 0 ? k_glob : v_glob);
-        *reinterpret_cast<uint4*>(out + (long long)t * a.heads * D) = half_block(c, S);
-      }
-      __syncwarp();
+    for (int p = 0; p < kKvGroup / kTokens; ++p) {
+      const int t = p * kTokens + lane / kHalves;
+      const uint32_t c = *reinterpret_cast<const uint32_t*>(&s_half[warp][M::codes(k.which, t, b, h)]);
+      const float S = __fmul_rn(e4m3_to_f32(s_half[warp][M::scale(k.which, t, b)]), glob);
+      *reinterpret_cast<uint4*>(rows + (long long)(first + t) * a.heads * D) = half_block(c, S);
     }
+    __syncwarp();
   }
-  if (other == 0u) return;
-  const int items = kKvGroup * nh * 4 * KvLayout<D>::kBlocks;
-  for (int it = threadIdx.x; it < items; it += kThreads) {
-    const int hb = it % (2 * KvLayout<D>::kBlocks), which = it / (2 * KvLayout<D>::kBlocks) & 1;
-    const int th = it / (4 * KvLayout<D>::kBlocks), k = th % kKvGroup;
-    if (i0 + k < a.tokens && (w.kind[k] == kAlone || w.kind[k] == kNothing))
-      read_half<D>(a, i0 + k, w.kind[k] == kAlone ? w.slot[16 + k] : -1, h0 + th / kKvGroup, which, hb >> 1, hb & 1);
+  // tokens outside whole groups, padding among them (zeros)
+  if ((w.alone | w.rest) == 0u) return;
+#pragma unroll 1
+  for (int p = 0; p < kKvGroup / kTokens; ++p) {
+    const int t = p * kTokens + lane / kHalves;
+    const int slot = __shfl_sync(0xffffffffu, w.slot, 16 + t);
+    if (((w.alone | w.rest) >> t) & 1u)
+      read_half<D>(a, k.i0 + t, ((w.alone >> t) & 1u) ? slot : -1, k.head, k.which, b, h);
   }
 }
 
@@ -346,12 +344,11 @@ constexpr long long kFew = 1 << 16;
 
 template <class Args>
 cudaError_t launch(void (*window)(Args), void (*few)(Args), Args a, int per_token, cudaStream_t stream) {
-  const int windows = (a.tokens + kKvGroup - 1) / kKvGroup;
+  const long long tasks = (a.tokens + (long long)kKvGroup - 1) / kKvGroup * a.heads * 2;
   const bool is_few = (long long)a.tokens * per_token <= kFew && a.tokens <= 65535;
-  a.heads_per_cta = 4;                    // a warp for each half
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = is_few ? dim3((unsigned)((per_token + kThreads - 1) / kThreads), (unsigned)a.tokens)
-                       : dim3((unsigned)windows, (unsigned)((a.heads + 3) / 4));
+                       : dim3((unsigned)((tasks + kWarps - 1) / kWarps));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
