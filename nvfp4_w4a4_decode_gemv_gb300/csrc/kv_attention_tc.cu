@@ -20,7 +20,10 @@
 // Warps: 0-7 and 8-15 softmax of the two halves (two threads a row, 64 keys each: one thread
 // for all 128 took 2900 cycles, more than the products under which it should hide), 16-19
 // dequantize (two 16-token groups each), 20 copies the cache's groups in, 21 issues the
-// products; one half's softmax runs under the other's products.  The maximum that the
+// products; one half's softmax runs under the other's products.  A tile of 128 rows
+// or fewer stands in both halves, which take every second step and are put together at
+// the end (with one half at work alone, its softmax and its products in turn, 64 rows
+// over 4 x 8000 keys took 52 us instead of 44).  The maximum that the
 // weights refer to moves only when a row's scores exceed it by 2^13 (then O is
 // rescaled in TMEM); up to there FP16 holds the weights as exactly as below 1.
 // Every wait is bounded and an abort flag ends the others.
@@ -63,7 +66,7 @@ struct Shape {
   static constexpr int kOffBar = kOffRaw + kRing * kRaw;
   static constexpr int kBars = 2 * kRing + 2 + 4 + 6 + 1;
   static constexpr int kOffWords = kOffBar + kBars * 8;   // TMEM address, abort flag, two tiles (5 each), groups
-                                                          // present (kRing + 2), pieces
+                                                          // present (kRing + 4), pieces
   static constexpr int kOffMax = kOffWords + 32 * 4;      // [2 steps][2 halves][2 threads][kHalfRows] maxima, then sums
   static constexpr int kOffF = kOffMax + 8 * kHalfRows * 4;   // [2][kHalfRows] score factors
   static constexpr int kRecord = kRows * (D + 2);         // floats of a piece's record: O, then the maxima in use, then the sums
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
   volatile uint32_t* abort_flag = words + 1;
   volatile int* s_tile = reinterpret_cast<volatile int*>(words + 2);
   volatile uint32_t* raw_have = words + 12;              // [kRing] groups that a raw step brings
-  volatile uint32_t* kv_have = words + 12 + kRing;       // [2]
+  volatile uint32_t* kv_have = words + 12 + kRing;       // [4] steps
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -363,11 +366,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
   griddep_launch_dependents();
   const float kg = *a.k_global, vg = *a.v_global;
   // steps of this CTA so far (they give ring slot, operand buffer and the parities of their barriers), those of the
-  // second half (a tile may have one half only), tiles
-  uint32_t step = 0, step_b = 0, tiles = 0;
+  // two halves, tiles
+  uint32_t step = 0, step_a = 0, step_b = 0, tiles = 0;
   uint32_t copied = 0;                                  // steps whose copies this warp has started
 
-  volatile uint32_t* s_pieces = words + 12 + kRing + 2; // pieces a tile is cut into, at most
+  volatile uint32_t* s_pieces = words + 12 + kRing + 4; // pieces a tile is cut into, at most
   // the copy warp takes the pieces of tiles from the counter, each while the one before it is worked on
   auto take_tile = [&](uint32_t n) {
     uint32_t t = 0;
@@ -406,29 +409,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
 
     if (warp < kSoftWarps) {
       // ================ softmax of a half: two threads a row, `part` 0 and 1 ================
-      const int half = warp >> 3, part = (warp >> 2) & 1, r = (warp & 3) * 32 + lane, row_h = half * kHalfRows;
+      const int half = warp >> 3, part = (warp >> 2) & 1, r = (warp & 3) * 32 + lane, row_h = both ? half * kHalfRows : 0;
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t col_s = tmem + kColHalf * half + 64 * part + lanes, col_o = tmem + kColHalf * half + kColO + lanes;
       const int row = row0 + row_h + r;
-      const bool used = (half == 0 || both) && !idle, mine = row_h + r < n_rows;
+      const bool mine = row_h + r < n_rows;
       const int tok = rq.first + row / a.group, head = kvh * a.group + row % a.group;
       float* s_max = reinterpret_cast<float*>(smem + S::kOffMax) + half * 2 * kHalfRows + r;   // + part, + step
       constexpr int kStepMax = 4 * kHalfRows;
       auto meet = [&]() {                               // the half's 8 warps
         asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "r"(kSoftWarps / 2 * 32) : "memory");
       };
+      auto meet_all = [&]() {                           // both halves
+        asm volatile("bar.sync 3, %0;" ::"r"(kSoftWarps * 32) : "memory");
+      };
       // queries: a warp a row at a time (whole rows a load), eight in flight
-      float* s_f = reinterpret_cast<float*>(smem + S::kOffF) + half * kHalfRows;
-      if (used) {
-        constexpr int E = D / 32, kBatch = 8, kWarpRows = kHalfRows / (kSoftWarps / 2);
-        const int w = warp & 7;
+      float* s_f = reinterpret_cast<float*>(smem + S::kOffF);
+      if (!idle) {
+        constexpr int E = D / 32, kBatch = 8;
+        const int warp_rows = (both ? kRows : kHalfRows) / kSoftWarps;
 #pragma unroll 1
-        for (int j0 = 0; j0 < kWarpRows; j0 += kBatch) {
+        for (int j0 = 0; j0 < warp_rows; j0 += kBatch) {
           float v[kBatch][E];
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
-            const int rh = w * kWarpRows + j0 + j, rr = row0 + row_h + rh;
-            const bool there = row_h + rh < n_rows;
+            const int rt = warp * warp_rows + j0 + j, rr = row0 + rt;
+            const bool there = rt < n_rows;
             const T* q = static_cast<const T*>(a.q) +
                          (there ? (rq.first + rr / a.group) * a.q_ts + (kvh * a.group + rr % a.group) * a.q_hs : 0) + lane * E;
 #pragma unroll
@@ -436,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
           }
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
-            const int rh = w * kWarpRows + j0 + j;
+            const int rt = warp * warp_rows + j0 + j, rh = rt % kHalfRows;
             float big = 0.0f;
 #pragma unroll
             for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(v[j][e]));
@@ -444,10 +450,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
             for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
             float down, up;
             power_of_two(big, down, up);
-            if (lane == 0) s_f[rh] = score_factor(a.scale * kLog2e * kg * up);
+            if (lane == 0) s_f[rt] = score_factor(a.scale * kLog2e * kg * up);
             // element lane * E: panel, 16-byte piece, place in it
             const int e0 = lane * E;
-            uint8_t* sq = smem + S::kOffQ + half * S::kTile + (e0 / 64) * S::kPanel + rh * 128 +
+            uint8_t* sq = smem + S::kOffQ + rt / kHalfRows * S::kTile + (e0 / 64) * S::kPanel + rh * 128 +
                           (((e0 / 8) & 7) ^ (rh & 7)) * 16 + (e0 & 7) * 2;
             if constexpr (E == 4)
               *reinterpret_cast<uint2*>(sq) = make_uint2(pack_f16(v[j][0] * down, v[j][1] * down),
@@ -457,13 +463,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        meet();                                         // the factors are there
+        if (both) meet();                               // the factors are there
+        else meet_all();
       }
-      const float f = used ? s_f[r] : 1.0f;
+      const float f = idle ? 1.0f : s_f[row_h + r];
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
-      const int nh = used ? n : 0;
-      const uint32_t first = half == 0 ? step : step_b;
+      const int nh = both ? n : (n + 1 - half) / 2;     // steps of the half
+      const uint32_t first = half == 0 ? step_a : step_b;
       // every row of the half sees [lo_all, hi_all]
       const int hi_all = rq.len - rq.rows + (row0 + row_h) / a.group;
       const int hi_any = rq.len - rq.rows + (row0 + min(row_h + kHalfRows, n_rows) - 1) / a.group;
@@ -474,8 +481,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
       for (int k = 0; k < nh; ++k) {                    // (an abort ends the waits, not the meetings)
         ok = ok && wait(&s_full[half], first + k, abort_flag);
         tc_fence_after();
-        const int t0 = (step0 + k) * kKeys + 64 * part;
-        const uint32_t have = (kv_have[(step + k) & 1u] >> (4 * part)) & 15u;
+        const int i = both ? k : 2 * k + half;
+        const int t0 = (step0 + i) * kKeys + 64 * part;
+        const uint32_t have = (kv_have[(step + i) & 3u] >> (4 * part)) & 15u;
         const bool some = t0 + 63 > hi_all || t0 < lo_all || have != 15u;
         auto hide = [&](uint32_t (&s)[32], int c) {
           if (some) {
@@ -553,20 +561,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[half]);
       }
-      // ---- the half's output: each thread one half of its row's elements
-      if (used) {
+      // ---- output: each thread of a row its share of the elements, 32 at a time
+      if (!idle) {
         float* at = s_max + (nh & 1) * kStepMax;        // not the last step's
         at[part * kHalfRows] = l;
         meet();
         l += at[(part ^ 1) * kHalfRows];
-        if (nh > 0 && ok) wait(&pv_done[half], first + nh - 1, abort_flag);
+        if (nh > 0 && ok) ok = wait(&pv_done[half], first + nh - 1, abort_flag);
+        float back = 1.0f, back_o = 0.0f;               // factors of this half's O and, of the same rows, the other's
+        const int nh_o = both ? 0 : (n + half) / 2;
+        if (!both) {
+          // (the buffer of this half's last step, whose maxima have been read)
+          at = s_max + ((nh + 1) & 1) * kStepMax;
+          if (part == 0) {
+            at[0] = m;
+            at[kHalfRows] = l;
+          }
+          meet_all();
+          at = s_max + (1 - 2 * half) * 2 * kHalfRows + ((nh_o + 1) & 1) * kStepMax;
+          const float m_o = at[0], l_o = at[kHalfRows], top = fmaxf(m, m_o);
+          back = m == -INFINITY ? 0.0f : ex2(m - top);
+          back_o = m_o == -INFINITY ? 0.0f : ex2(m_o - top);
+          const float mine_l = l * back, others = l_o * back_o;
+          l = __fadd_rn(mine_l, others);
+          m = top;
+          if (nh_o > 0 && ok) wait(&pv_done[half ^ 1], (half == 0 ? step_b : step_a) + nh_o - 1, abort_flag);
+        }
         tc_fence_after();
         const float inv = l > 0.0f ? vg / l : 0.0f;
         uint16_t* out = a.out + ((size_t)tok * a.heads + head) * D;
         float* rec = a.records + (size_t)(record + piece) * S::kRecord;
         const int rt = row_h + r;                       // row in the tile
+        // columns of a thread: half a row's, or a quarter (D = 64: half of them of every second thread)
+        const int i0 = both ? part * (D / 2) : D == 128 ? (2 * half + part) * 32 : half * 32;
+        const int i1 = both ? i0 + D / 2 : D == 128 || part == 0 ? i0 + 32 : i0;
 #pragma unroll 1
-        for (int i = part * (D / 2); i < (part + 1) * (D / 2); i += 32) {
+        for (int i = i0; i < i1; i += 32) {
           uint32_t o[32];
           if (nh > 0) {
             tmem_ld32(col_o + i, o);
@@ -574,6 +604,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = 0u;
+          }
+          if (!both) {
+            uint32_t x[32];
+            if (nh_o > 0) {
+              tmem_ld32(col_o + (half == 0 ? kColHalf : -kColHalf) + i, x);
+              tmem_wait_ld(x);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              o[j] = __float_as_uint(__fadd_rn(__uint_as_float(o[j]) * back, __uint_as_float(x[j]) * back_o));
           }
           if (mine && !whole) {
 #pragma unroll
@@ -595,9 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
             }
           }
         }
-        if (mine && part == 0 && whole && a.lse)
+        const bool says = mine && part == 0 && (both || half == 0);
+        if (says && whole && a.lse)
           a.lse[(size_t)tok * a.heads + head] = l > 0.0f ? (m + log2f(l)) / kLog2e : -INFINITY;
-        if (mine && part == 0 && !whole) {
+        if (says && !whole) {
           __stcg(rec + kRows * D + rt, m);
           __stcg(rec + kRows * (D + 1) + rt, l);
         }
@@ -616,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
         if (i >= 1) ok = wait(k_free, i - 1, abort_flag) && ok;          // the last step's keys have been multiplied
 #pragma unroll
         for (int g = g0; g < g0 + kMine; ++g) dequantize_keys<D>(raw + g * L::kGroupBytes, smem + S::kOffK, g, lane);
-        if (g0 == 0 && lane == 0) kv_have[buf] = have;
+        if (g0 == 0 && lane == 0) kv_have[i & 3u] = have;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(k_full);
@@ -680,13 +724,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
       // ================ products ================
       const uint32_t lead = elect_one();
       bool ok = wait(q_full, tiles, abort_flag);
-      const int halves = both ? 2 : 1;
       // descriptors of the operands' starts; everything else is an addition to their address field
       const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + S::kOffQ)), k_desc = smem_desc_sw128(smem_u32(smem + S::kOffK));
       const uint64_t v_desc = smem_desc_mn_sw128(smem_u32(smem + S::kOffV), S::kPanel);
-      auto multiply_scores = [&](int h) {
+      // item j: half j % 2's next step, which is step j / 2 where the halves have their own rows, and step j where they
+      // share the rows
+      const int items = both ? 2 * n : n;
+      auto step_of = [&](int j) { return both ? j >> 1 : j; };
+      auto multiply_scores = [&](int item) {
+        const int h = item & 1;
+        if (!both || h == 0) ok = wait(k_full, step + step_of(item), abort_flag) && ok;
+        if (!ok) return;
         tc_fence_after();
-        const uint64_t dq = q_desc + (uint64_t)(h * (S::kTile >> 4));
+        const uint64_t dq = q_desc + (uint64_t)(both ? h * (S::kTile >> 4) : 0);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
           constexpr int kPanel16 = S::kPanel >> 4;
@@ -694,38 +744,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
           mma_f16_ss(lead, tmem + kColHalf * h, dq + at, k_desc + at, S::kIdescS, j > 0 ? 1u : 0u);
         }
         commit(lead, &s_full[h]);
-        if (h == halves - 1) commit(lead, k_free);
+        if (!both || h == 1) commit(lead, k_free);
       };
-      if (n > 0) {
-        ok = wait(k_full, step, abort_flag) && ok;
-        for (int h = 0; h < halves; ++h) multiply_scores(h);
-      }
-      for (int k = 0; k < n && ok; ++k) {
-        const uint32_t i = step + k, buf = i & 1u;
+      for (int item = 0; item < min(items, 2); ++item) multiply_scores(item);
+      for (int item = 0; item < items && ok; ++item) {
+        const int h = item & 1;
+        const uint32_t i = step + step_of(item), buf = i & 1u, u = (h == 0 ? step_a : step_b) + (item >> 1);
         const uint64_t dv = v_desc + (uint64_t)(buf * (S::kTile >> 4));
-        ok = wait(&v_full[buf], i / 2, abort_flag);
-        for (int h = 0; h < halves && ok; ++h) {
-          const uint32_t u = (h == 0 ? step : step_b) + k;
-          ok = wait(&p_full[h], u, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t col = tmem + kColHalf * h;
+        if (!both || h == 0) ok = wait(&v_full[buf], i / 2, abort_flag);
+        ok = ok && wait(&p_full[h], u, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t col = tmem + kColHalf * h;
 #pragma unroll
-          for (int j = 0; j < kKeys / 16; ++j)
-            mma_f16_ts(lead, col + kColO, col + (j >> 2) * 64 + 8 * (j & 3), dv + (uint64_t)(j * (2048 >> 4)), S::kIdescO,
-                       (k > 0 || j > 0) ? 1u : 0u);
-          commit(lead, &pv_done[h]);
-          if (h == halves - 1) commit(lead, &v_free[buf]);
-          if (k + 1 < n) {
-            if (h == 0) ok = wait(k_full, i + 1, abort_flag);
-            ok = wait(&pv_done[h], u, abort_flag) && ok;   // the next scores stand where these weights are
-            if (ok) multiply_scores(h);
-          }
+        for (int j = 0; j < kKeys / 16; ++j)
+          mma_f16_ts(lead, col + kColO, col + (j >> 2) * 64 + 8 * (j & 3), dv + (uint64_t)(j * (2048 >> 4)), S::kIdescO,
+                     (item > 1 || j > 0) ? 1u : 0u);
+        commit(lead, &pv_done[h]);
+        if (!both || h == 1) commit(lead, &v_free[buf]);
+        if (item + 2 < items) {
+          ok = wait(&pv_done[h], u, abort_flag);        // the next scores stand where these weights are
+          multiply_scores(item + 2);
         }
       }
     }
     step += (uint32_t)n;
-    step_b += both ? (uint32_t)n : 0u;
+    step_a += (uint32_t)(both ? n : (n + 1) / 2);
+    step_b += (uint32_t)(both ? n : n / 2);
     ++tiles;
     __syncthreads();                                    // the tile's numbers and the TMEM are free again
     const bool aborted = *abort_flag != 0u;
