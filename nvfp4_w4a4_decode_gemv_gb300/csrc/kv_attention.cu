@@ -41,7 +41,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxSplits = 32;          // pieces of a segment when there are few: more cost more to merge than they save
 constexpr int kMaxShares = 64;          // the same bound where there are many
-constexpr int kTcRows = 64;             // more query rows of a kv head than this take the other kernel (kv_attention_tc.cu)
+// More query rows of a kv head than this take the other kernel (kv_attention_tc.cu).  Here / there, D = 128, us:
+// 32 rows: 42 / 44 (4 requests of 8000 keys, 8 kv heads), 55 / 58 (16 of 4000), 89 / 135 (16 of 500 to 16384);
+// 64 rows: 50 / 45, 82 / 60, 139 / 137;  128 rows: 79 / 48, 141 / 62, 256 / 142.
+constexpr int kTcRows = 48;
 constexpr int kSegmentCost = 512;       // keys that the fixed cost of a segment (queries, first copies, merge) stands for
 constexpr int kShortUnits = 8;
 

@@ -6,8 +6,8 @@
 
 constexpr int kMaxCtas = 640;           // most CTAs of a launch
 constexpr size_t kCounterBytes = 4096;  // start of a workspace: counters, zero between calls (what a caller zeroes)
-constexpr int kTileCounter = kMaxCtas;  // counters behind those of the segments: next tile, CTAs done
-static_assert((kTileCounter + 2) * 4 <= kCounterBytes, "the counters");
+constexpr int kTileCounter = kMaxCtas;  // counters behind those of the segments: next piece, CTAs done; steps of a piece
+static_assert((kTileCounter + 3) * 4 <= kCounterBytes, "the counters");
 constexpr int kTcPieces = 304;          // records of the many-row kernel: two a SM
 constexpr int kTcRecord = 256 * 130;    // floats of one
 constexpr float kLog2e = 1.4426950408889634f;

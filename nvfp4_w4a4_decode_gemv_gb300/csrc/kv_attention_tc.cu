@@ -27,10 +27,13 @@
 // weights refer to moves only when a row's scores exceed it by 2^13 (then O is
 // rescaled in TMEM); up to there FP16 holds the weights as exactly as below 1.
 // Every wait is bounded and an abort flag ends the others.
-// Tiles are handed out from a counter, the longest of a request first.  Where there are fewer tiles than SMs, the
-// keys of each are cut into pieces of kMinSteps steps or more, which go through records in the workspace (128 KB
-// each), and a second launch merges them, all SMs at work on it (merged by the last piece to arrive instead, one
-// CTA read up to 32 records: 115 us for 128 rows over 16000 keys, 64/8 heads).
+// Tiles are handed out from a counter, the longest of a request first.  Where they are fewer than fill the SMs, or
+// their lengths differ, their keys are cut into pieces of one size, kMinSteps steps or more, which go through records
+// in the workspace (128 KB each), and a second launch merges them, all SMs at work on it (merged by the last piece to
+// arrive instead, one CTA read up to 32 records: 115 us for 128 rows over 16000 keys, 64/8 heads, now 52).  With as
+// many pieces for every tile instead of one size, 64 rows over 16 requests of 500 to 16384 keys took 179 us, not 137.
+// 2 x 1024 prompt tokens over 4096 and 8192 keys (64/8 heads, D = 128: 377 GFLOP): 422 us, 890 TFLOP/s, a step of 256
+// rows in 4400 cycles, of which a half's softmax has 1800 and the products 2050.
 #include <math.h>
 
 #include "kv_attention.cuh"
@@ -164,7 +167,7 @@ NVFP4_DEVINL bool wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_
 constexpr int kMinSteps = 4;            // below this a record costs more than the piece saves
 
 struct Tile {
-  int b, kvh, row0;
+  int b, kvh, row0, piece, number;
 };
 
 // Row tiles of a request.
@@ -172,55 +175,132 @@ NVFP4_DEVINL int request_tiles(const AttnArgs& a, const Request& r) {
   return (int)(((long long)r.rows * a.group + kRows - 1) / kRows);
 }
 
-// Tiles there are, and the pieces each is cut into at most: the SMs once over, or twice where that leaves much less
-// of a last round idle.  One warp.
-NVFP4_DEVINL int count_pieces(const AttnArgs& a, int sms, int lane, bool report, long long& tiles) {
-  long long n = 0;
-  for (int b = lane; b < a.batch; b += 32) n += (long long)request_tiles(a, get_request(a, b, report)) * a.kv_heads;
+// Steps of a request's tiles, at most.
+NVFP4_DEVINL int request_steps(const AttnArgs& a, const Request& r) {
+  const int all = (r.len + kKeys - 1) / kKeys;
+  // the keys that the rows of a tile see: a window's and one more for each of its further tokens
+  const long long seen = (long long)a.window + min(kRows / a.group + 1, r.rows);
+  return a.window > 0 ? (int)min((long long)all, seen / kKeys + 2) : all;
+}
+
+// Pieces of a tile of a request, at most, for pieces of about `size` steps (0: not cut).
+NVFP4_DEVINL int request_pieces(const AttnArgs& a, const Request& r, int size) {
+  return size > 0 ? max((request_steps(a, r) + size - 1) / size, 1) : 1;
+}
+
+// The steps of a piece, 0 if no tile is cut: the smallest size with as many pieces as SMs, or twice as many where that
+// is much shorter, so that lengths that differ fill the SMs too.  One warp.
+NVFP4_DEVINL int piece_size(const AttnArgs& a, int sms, int lane, bool report) {
+  long long tiles_all = 0;
+  float sum = 0.0f;                                       // (an estimate is enough)
+  int longest = 0, n0 = 0, s0 = 0;                        // tiles and steps of request `lane`
+  for (int b = lane; b < a.batch; b += 32) {
+    const Request r = get_request(a, b, report);
+    const long long n = (long long)request_tiles(a, r) * a.kv_heads;
+    if (n == 0) continue;
+    const int s = request_steps(a, r);
+    tiles_all += n;
+    sum += (float)n * (float)s;
+    longest = max(longest, s);
+    if (b == lane) n0 = (int)min(n, (long long)kTcPieces), s0 = s;
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  tiles = n;
-  if (n == 0 || n > a.pieces) return 1;
-  const int t = (int)n, once = max(min(sms, a.pieces) / t, 1), twice = min(2 * sms, a.pieces) / t;
-  return 5 * once < 2 * twice ? twice : once;             // 2 / twice < 0.8 / once
+  for (int o = 16; o > 0; o >>= 1) {
+    tiles_all += __shfl_xor_sync(0xffffffffu, tiles_all, o);
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (tiles_all >= a.pieces || longest <= kMinSteps) return 0;
+  // sum / target will do where the tiles' last pieces are whole, sum / (target - tiles) always, and often one between
+  const int tiles = (int)tiles_all;
+  int best = 0, best_cost = (tiles + sms - 1) / sms * longest;
+#pragma unroll 1
+  for (int rounds = 1; rounds <= 2; ++rounds) {
+    const int target = min(rounds * sms, a.pieces);
+    if (tiles >= target) continue;
+#pragma unroll 1
+    for (int j = 0; j <= 4; ++j) {
+      const int parts = target - tiles * j / 4;
+      const int size = max((int)min(ceilf(__fdividef(sum, (float)parts)), 1e9f), kMinSteps);
+      int pieces = 0, most = 0;                           // of all; steps of the longest one
+      auto add = [&](int n, int s) {
+        const int p = (s + size - 1) / size;
+        pieces = min(pieces + n * min(p, kTcPieces + 1), kTcPieces + 1);
+        most = max(most, (s + p - 1) / p);
+      };
+      if (n0 > 0 && s0 > 0) add(n0, s0);
+      else pieces = n0;
+      for (int b = lane + 32; b < a.batch; b += 32) {
+        const Request r = get_request(a, b, false);
+        const int n = request_tiles(a, r) * a.kv_heads, s = request_steps(a, r);
+        if (n > 0 && s > 0) add(n, s);
+        else pieces = min(pieces + n, kTcPieces + 1);
+      }
+      pieces = (int)__reduce_add_sync(0xffffffffu, (uint32_t)pieces);
+      if (pieces > target) continue;
+      const int cost = rounds * max((int)__reduce_max_sync(0xffffffffu, (uint32_t)most), kMinSteps);
+      // a second round has to gain a fifth: its pieces have queries to load and records to write, too
+      if (rounds == 1 ? cost < best_cost : 5ll * cost < 4ll * best_cost) {
+        best = size;
+        best_cost = cost;
+      }
+      break;
+    }
+  }
+  return best;
 }
 
 // The steps of a tile and how many of them a piece has.
 struct Steps {
   int lo, hi, first, all, piece;                          // keys [lo, hi]; first step, steps, steps of a piece
-  NVFP4_DEVINL Steps(const AttnArgs& a, const Request& rq, int row0, int n_rows, int pieces) {
+  NVFP4_DEVINL Steps(const AttnArgs& a, const Request& rq, int row0, int n_rows, int size) {
     const int p_first = rq.len - rq.rows + row0 / a.group;
     hi = rq.len - rq.rows + (row0 + n_rows - 1) / a.group;
     lo = a.window > 0 ? max(p_first - a.window + 1, 0) : 0;
     first = lo / kKeys;
     all = hi < 0 ? 0 : max(hi / kKeys + 1 - first, 0);
-    piece = max(kMinSteps, (all + pieces - 1) / pieces);
+    // (the same for every tile of the request, so that none has more pieces than are counted for it)
+    const int pieces = request_pieces(a, rq, size);
+    piece = size > 0 ? max(kMinSteps, (request_steps(a, rq) + pieces - 1) / pieces) : all;
   }
 };
 
-// Tile number t -> request, kv head and first row (b = -1: there is no such tile).  One warp; the requests are
-// summed 32 at a time.  The last rows of a request, which see most keys, come first.
-NVFP4_DEVINL Tile find_tile(const AttnArgs& a, long long t, int lane) {
-  long long before = 0;
+// Piece number t, or the first piece of tile number t, -> request, kv head, first row, piece of the tile and its number
+// (b = -1: there is no such piece).  One warp; the requests are summed 32 at a time.  The last rows of a request, which
+// see most keys, come first.
+template <bool TILES>
+NVFP4_DEVINL Tile find(const AttnArgs& a, int t, int size, int lane) {
+  long long before = 0, numbers = 0;                      // tiles are few where TILES: some are cut
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    int tiles = 0;
-    if (b0 + lane < a.batch) tiles = request_tiles(a, get_request(a, b0 + lane, false));
-    long long inc = (long long)tiles * a.kv_heads;
+    int tiles = 0, pieces = 1;
+    if (b0 + lane < a.batch) {
+      const Request r = get_request(a, b0 + lane, false);
+      tiles = request_tiles(a, r);
+      if (size > 0 && tiles > 0) pieces = request_pieces(a, r, size);
+    }
+    const int each = TILES ? 1 : pieces;
+    long long inc = (long long)tiles * a.kv_heads * each;
+    int inc_n = TILES ? (int)inc * pieces : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+      const int w = TILES ? __shfl_up_sync(0xffffffffu, inc_n, o) : 0;
+      if (lane >= o) inc += v, inc_n += w;
     }
     const uint32_t past = __ballot_sync(0xffffffffu, before + inc > t);
     if (past) {
       const int l = __ffs(past) - 1;
-      const int n = __shfl_sync(0xffffffffu, tiles, l);
-      const int i = (int)(t - before - (__shfl_sync(0xffffffffu, inc, l) - (long long)n * a.kv_heads));
-      return Tile{b0 + l, i % a.kv_heads, (n - 1 - i / a.kv_heads) * kRows};
+      const int n = __shfl_sync(0xffffffffu, tiles, l), p = __shfl_sync(0xffffffffu, pieces, l);
+      const int per = TILES ? 1 : p;
+      const int i = (int)(t - before - (__shfl_sync(0xffffffffu, inc, l) - (long long)n * a.kv_heads * per));
+      const int tile = per > 1 ? i / per : i, piece = i - tile * per;
+      const int number = TILES ? (int)numbers + __shfl_sync(0xffffffffu, inc_n, l) - n * a.kv_heads * p + tile * p : t;
+      return Tile{b0 + l, tile % a.kv_heads, (n - 1 - tile / a.kv_heads) * kRows, piece, number};
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
+    if (TILES) numbers += __shfl_sync(0xffffffffu, inc_n, 31);
   }
-  return Tile{-1, 0, 0};
+  return Tile{-1, 0, 0, 0, 0};
 }
 
 // Dequantizes the keys of one 16-token group into rows [16 g, 16 g + 16) of the K tile.
@@ -370,42 +450,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
   uint32_t step = 0, step_a = 0, step_b = 0, tiles = 0;
   uint32_t copied = 0;                                  // steps whose copies this warp has started
 
-  volatile uint32_t* s_pieces = words + 12 + kRing + 4; // pieces a tile is cut into, at most
+  volatile uint32_t* s_size = words + 12 + kRing + 4;   // steps of a piece, 0 if no tile is cut
   // the copy warp takes the pieces of tiles from the counter, each while the one before it is worked on
   auto take_tile = [&](uint32_t n) {
     uint32_t t = 0;
     if (lane == 0) t = atomicAdd(&a.counters[kTileCounter], 1u);
     t = __shfl_sync(0xffffffffu, t, 0);
-    const uint32_t pieces = *s_pieces;
-    const Tile tile = find_tile(a, t / pieces, lane);
+    const Tile tile = find<false>(a, (int)t, (int)*s_size, lane);
     if (lane == 0) {
       volatile int* to = s_tile + 5 * (n & 1u);
-      to[0] = tile.b, to[1] = tile.kvh, to[2] = tile.row0, to[3] = (int)(t % pieces), to[4] = (int)(t / pieces);
+      to[0] = tile.b, to[1] = tile.kvh, to[2] = tile.row0, to[3] = tile.piece, to[4] = (int)t;
     }
   };
   if (warp == kCopyWarp) {
-    long long total;
-    const int pieces = count_pieces(a, gridDim.x, lane, blockIdx.x == 0, total);
-    if (lane == 0) *s_pieces = (uint32_t)pieces;
+    const int size = piece_size(a, gridDim.x, lane, blockIdx.x == 0);
+    if (lane == 0) {
+      *s_size = (uint32_t)size;
+      if (blockIdx.x == 0) a.counters[kTileCounter + 2] = (uint32_t)size;   // for the merge
+    }
     __syncwarp();
     take_tile(0);
   }
   __syncthreads();
-  const int pieces = (int)*s_pieces;
+  const int size = (int)*s_size;
   for (;;) {
     const volatile int* from = s_tile + 5 * (tiles & 1u);
-    const int b = from[0], kvh = from[1], row0 = from[2], piece = from[3], tile_no = from[4];
+    const int b = from[0], kvh = from[1], row0 = from[2], piece = from[3], record = from[4];
     if (b < 0) break;
     const Request rq = get_request(a, b, false);
     const int n_rows = (int)min((long long)kRows, (long long)rq.rows * a.group - row0);
     const bool both = n_rows > kHalfRows;
     // a tile of one piece (also one without keys) is written at once
-    const Steps steps(a, rq, row0, n_rows, pieces);
+    const Steps steps(a, rq, row0, n_rows, size);
     const int lo = steps.lo, hi = steps.hi;               // keys that some row of the tile sees
     const bool whole = steps.all <= steps.piece, idle = piece > 0 && piece * steps.piece >= steps.all;
     const int step0 = steps.first + piece * steps.piece;
     const int n = idle ? 0 : min(steps.piece, steps.all - piece * steps.piece);
-    const int record = tile_no * pieces;                // of the tile's first piece
 
     if (warp < kSoftWarps) {
       // ================ softmax of a half: two threads a row, `part` 0 and 1 ================
@@ -590,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
         tc_fence_after();
         const float inv = l > 0.0f ? vg / l : 0.0f;
         uint16_t* out = a.out + ((size_t)tok * a.heads + head) * D;
-        float* rec = a.records + (size_t)(record + piece) * S::kRecord;
+        float* rec = a.records + (size_t)record * S::kRecord;
         const int rt = row_h + r;                       // row in the tile
         // columns of a thread: half a row's, or a quarter (D = 64: half of them of every second thread)
         const int i0 = both ? part * (D / 2) : D == 128 ? (2 * half + part) * 32 : half * 32;
@@ -802,35 +882,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
 constexpr int kMergeRows = 32, kMergeThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) kv_attention_merge_kernel(const AttnArgs a, int sms) {
+__global__ void __launch_bounds__(kMergeThreads) kv_attention_merge_kernel(const AttnArgs a) {
   using S = Shape<D>;
-  __shared__ int s_info[6];
+  __shared__ int s_info[4];
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31;
-  long long tiles = 0;
-  const int pieces = count_pieces(a, sms, lane, false, tiles);
-  if (pieces <= 1) return;
+  const int size = (int)__ldcg(&a.counters[kTileCounter + 2]);
+  if (size == 0) return;
   constexpr int kParts = kRows / kMergeRows;
   const float vg = *a.v_global;
-  for (int item = blockIdx.x; item < (int)tiles * kParts; item += gridDim.x) {
-    const int tile_no = item / kParts, r0 = item % kParts * kMergeRows;
+  for (int item = blockIdx.x; ; item += gridDim.x) {
+    const int r0 = item % kParts * kMergeRows;
     __syncthreads();
     if (tid < 32) {
-      const Tile tile = find_tile(a, tile_no, lane);
-      if (lane == 0) s_info[0] = tile.b, s_info[1] = tile.kvh, s_info[2] = tile.row0;
+      const Tile tile = find<true>(a, item / kParts, size, lane);
+      if (lane == 0) s_info[0] = tile.b, s_info[1] = tile.kvh, s_info[2] = tile.row0, s_info[3] = tile.number;
     }
     __syncthreads();
-    const int b = s_info[0], kvh = s_info[1], row0 = s_info[2];
+    const int b = s_info[0], kvh = s_info[1], row0 = s_info[2], number = s_info[3];
+    if (b < 0) break;
     const Request rq = get_request(a, b, false);
     const int n_rows = (int)min((long long)kRows, (long long)rq.rows * a.group - row0);
-    const Steps steps(a, rq, row0, n_rows, pieces);
+    const Steps steps(a, rq, row0, n_rows, size);
     if (steps.all <= steps.piece) continue;
     const int n_rec = (steps.all + steps.piece - 1) / steps.piece;
     for (int e = tid; e < kMergeRows * (D / 4); e += kMergeThreads) {
       const int rt = r0 + e / (D / 4), d = e % (D / 4) * 4;
       if (rt >= n_rows) break;
-      const float* rec = a.records + (size_t)tile_no * pieces * S::kRecord;
+      const float* rec = a.records + (size_t)number * S::kRecord;
       float mx = -INFINITY, l = 0.0f;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -887,7 +967,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   cfg.gridDim = dim3((unsigned)(4 * grid));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv_attention_merge_kernel<D>, a, grid);
+  return cudaLaunchKernelEx(&cfg, kv_attention_merge_kernel<D>, a);
 }
 
 }  // namespace
