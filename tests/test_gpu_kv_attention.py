@@ -379,3 +379,17 @@ def test_prompt_rows_of_many_requests(batch):
     """More requests than a warp counts at once, prompt chunks among single rows and empty requests."""
     rows = [0 if i % 7 == 3 else 70 if i % 11 == 0 else 1 for i in range(batch)]
     _run(batch, [max(r, (37 * i) % 200) for i, r in enumerate(rows)], rows, 4, 1, 64, 16, max_q=70)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 700])
+def test_many_rows_of_unequal_lengths(D, window):
+    """Requests whose tiles are cut into different numbers of pieces, tiles in one half, in both, and of each with an
+    odd number of steps."""
+    _run(90 + window, [4100, 90, 0, 2500, 1300, 129], [8, 9, 20, 40, 7, 16], 16, 2, D, 64, window=window)
+
+
+def test_many_rows_of_more_requests_than_a_warp_has_lanes():
+    """Pieces are found across groups of 32 requests, some of them empty."""
+    lens = [(i * 531) % 3001 for i in range(45)]
+    _run(93, lens, [min(7 + i % 3, n) if i % 7 else 0 for i, n in enumerate(lens)], 8, 1, 128, 32)
