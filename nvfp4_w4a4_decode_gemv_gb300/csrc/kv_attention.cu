@@ -41,10 +41,12 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxSplits = 32;          // pieces of a segment when there are few: more cost more to merge than they save
 constexpr int kMaxShares = 64;          // the same bound where there are many
-// More query rows of a kv head than this take the other kernel (kv_attention_tc.cu).  Here / there, D = 128, us:
-// 32 rows: 42 / 44 (4 requests of 8000 keys, 8 kv heads), 55 / 58 (16 of 4000), 89 / 135 (16 of 500 to 16384);
-// 64 rows: 50 / 45, 82 / 60, 139 / 137;  128 rows: 79 / 48, 141 / 62, 256 / 142.
+// More query rows of a kv head than this, and more rows x keys (kv heads x keys there is room for), take the other
+// kernel (kv_attention_tc.cu).  Here / there, D = 128, 8 kv heads, us:  32 rows: 36 / 44 (4 requests of 8000 keys),
+// 53 / 58 (16 of 4000), 93 / 135 (16 of 500 to 16384);  64 rows: 15 / 28 (one of 2000), 35 / 48 (one of 16000),
+// 49 / 45, 77 / 60, 142 / 137;  128 rows: 19 / 31, 59 / 52, 96 / 48, 145 / 62, 275 / 142.
 constexpr int kTcRows = 48;
+constexpr long long kTcProducts = 1 << 24;
 constexpr int kSegmentCost = 512;       // keys that the fixed cost of a segment (queries, first copies, merge) stands for
 constexpr int kShortUnits = 8;
 
@@ -73,7 +75,7 @@ struct Shape {
   static constexpr int kUnitGroups = 512 / D;              // most groups of a unit: 64 tokens at D = 128, 128 at D = 64
   static constexpr int kUnitLog = D == 128 ? 6 : 7;        // log2 of its tokens; short work has units of half of that
   static constexpr int kUnitBytes = kUnitGroups * KvLayout<D>::kGroupBytes;
-  static constexpr int kPair = NT <= 2 ? 2 : 1;            // groups whose scores are formed together (latency)
+  static constexpr int kPair = 2;                          // groups whose scores are formed together (latency)
   static constexpr int kStages = 2;
   static constexpr int kMergeStride = D + 4;               // floats a row in the merge buffer (bank spread)
   static constexpr int kRecord = kRows * (D + 2);          // floats of a record: O, then M, then L
@@ -127,7 +129,7 @@ struct WarpState {
 };
 
 template <int D, int NT>
-NVFP4_DEVINL void scores(const uint8_t* g, int lane, const uint32_t (*qreg)[2], const uint8_t* sq, float (&s)[NT][4]) {
+NVFP4_DEVINL void scores(const uint8_t* g, int lane, const uint32_t (&qreg)[NT * (D / 16)][2], float (&s)[NT][4]) {
   using L = KvLayout<D>;
   constexpr int W = D / 32;             // code words of the lane's D/4 elements of a row
   uint32_t raw[2][W];
@@ -168,11 +170,9 @@ NVFP4_DEVINL void scores(const uint8_t* g, int lane, const uint32_t (*qreg)[2], 
                              hmul2(h[0][2 * u + 1], sc[0][w / 2]), hmul2(h[1][2 * u + 1], sc[1][w / 2])};
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        uint2 b;
-        if constexpr (NT <= 2) b = make_uint2(qreg[t * (D / 16) + 2 * w + u][0], qreg[t * (D / 16) + 2 * w + u][1]);
-        else b = lds64(sq + ((t * (D / 16) + 2 * w + u) * 32 + lane) * 8);
-        if (w == 0 && u == 0) mma16816_first(s[t], a, b.x, b.y);
-        else mma16816(s[t], a, b.x, b.y);
+        const uint32_t(&b)[2] = qreg[t * (D / 16) + 2 * w + u];
+        if (w == 0 && u == 0) mma16816_first(s[t], a, b[0], b[1]);
+        else mma16816(s[t], a, b[0], b[1]);
       }
     }
   }
@@ -476,13 +476,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
       st.m[t][0] = st.m[t][1] = -INFINITY;
       st.l[t][0] = st.l[t][1] = 0.0f;
     }
-    uint32_t qreg[NT <= 2 ? NT * (D / 16) : 1][2];
-    if constexpr (NT <= 2) {
+    uint32_t qreg[NT * (D / 16)][2];
 #pragma unroll
-      for (int i = 0; i < NT * (D / 16); ++i) {
-        const uint2 v = lds64(smem + S::kOffQ + (i * 32 + lane) * 8);
-        qreg[i][0] = v.x, qreg[i][1] = v.y;
-      }
+    for (int i = 0; i < NT * (D / 16); ++i) {
+      const uint2 v = lds64(smem + S::kOffQ + (i * 32 + lane) * 8);
+      qreg[i][0] = v.x, qreg[i][1] = v.y;
     }
     float f[NT][2], neg_m[NT][2];                       // factors; minus the maximum, 0 while there is none
 #pragma unroll
@@ -503,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
         const int t0 = t_unit + gi * kKvGroup;
         float s[S::kPair][NT][4];
 #pragma unroll
-        for (int h = 0; h < S::kPair; ++h) scores<D, NT>(g + h * L::kGroupBytes, lane, qreg, smem + S::kOffQ, s[h]);
+        for (int h = 0; h < S::kPair; ++h) scores<D, NT>(g + h * L::kGroupBytes, lane, qreg, s[h]);
         int live[S::kPair];
 #pragma unroll
         for (int h = 0; h < S::kPair; ++h) live[h] = 4;
@@ -533,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
 #pragma unroll
           for (int k2 = 0; k2 < 2; ++k2) {
             float x = fmaxf(s[0][t][k2], s[0][t][k2 + 2]);
-            if (S::kPair == 2) x = fmaxf(x, fmaxf(s[S::kPair - 1][t][k2], s[S::kPair - 1][t][k2 + 2]));
+            x = fmaxf(x, fmaxf(s[S::kPair - 1][t][k2], s[S::kPair - 1][t][k2 + 2]));
             top[t][k2] = x * f[t][k2];
             grew = grew || top[t][k2] > st.m[t][k2];
           }
@@ -741,11 +739,16 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, NT, T>, a);
 }
 
+// Tiles of 8 query rows or of 16 (`keys`: kv heads x keys there is room for).  More rows share a dequantized key, but a
+// tile has fewer CTAs at work at a time (two an SM instead of three) and takes longer to set up and merge: with D = 128
+// and 8 kv heads, us with 8 / 16:  16 rows: 13 / 16 (2000 keys), 50 / 53 (16 requests of 8000);  32 rows: 14 / 17,
+// 20 / 25 (8000 keys), 36 / 34 (4 of 8000), 110 / 88 (16 of 8000);  48 rows: 22 / 24, 39 / 37, 123 / 106.  Tiles of 32
+// rows gained 3 % at the largest of these and took up to twice as long at the others.
+constexpr long long kSmallKeys = 1 << 18;
+
 template <int D, class T>
-cudaError_t dispatch(const AttnArgs& a, int rows, cudaStream_t stream) {
-  if (rows <= 8) return launch<D, 1, T>(a, stream);
-  if (rows <= 16) return launch<D, 2, T>(a, stream);
-  return launch<D, 4, T>(a, stream);
+cudaError_t dispatch(const AttnArgs& a, int rows, long long keys, cudaStream_t stream) {
+  return rows <= 16 || keys <= kSmallKeys ? launch<D, 1, T>(a, stream) : launch<D, 2, T>(a, stream);
 }
 
 // Whether a workspace has the many-row kernel's records: calls of fewer rows hardly reach it.
@@ -760,7 +763,7 @@ nvfp4_status nvfp4_internal_check_device();
 extern "C" size_t nvfp4_kv_attention_workspace_bytes(int batch, int tokens, int heads, int kv_heads, int head_dim) {
   if (batch < 1 || tokens < 0 || nvfp4_kv_page_bytes(16, kv_heads, head_dim) == 0) return 0;
   if (heads < kv_heads || heads % kv_heads != 0 || heads / kv_heads > 64) return 0;
-  const size_t decode = (size_t)2 * kMaxCtas * Shape<128, 4>::kRecord, many = (size_t)kTcPieces * kTcRecord;
+  const size_t decode = (size_t)2 * kMaxCtas * Shape<128, 2>::kRecord, many = (size_t)kTcPieces * kTcRecord;
   return kCounterBytes + (room_for_pieces(tokens, heads / kv_heads) && many > decode ? many : decode) * sizeof(float);
 }
 
@@ -801,14 +804,15 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens,
   const int rows = cu_q ? (int)((long long)max_q * group < 1 << 20 ? max_q * group : 1 << 20) : group;
   // the decode kernel counts its units (32 keys of a row tile, with their overhead) in 31 bits; this is the most there
   // can be, whatever cu_q and kv_lens hold
+  const long long keys = (long long)batch * cache->kv_heads * table_width * cache->page_size;
   const long long most_units = ((long long)tokens * group / 8 + batch) * cache->kv_heads *
                                ((long long)table_width * cache->page_size / 32 + 2 + kSegmentCost / 32 + kWarps);
   cudaError_t e;
-  if (rows > kTcRows || most_units > 0x7FFFFFFFll)
+  if ((rows > kTcRows && rows * keys > kTcProducts) || most_units > 0x7FFFFFFFll)
     e = nvfp4_internal_kv_attention_tc(a, cache->head_dim, dtype, stream);
   else if (cache->head_dim == 128)
-    e = dtype == NVFP4_DTYPE_F32 ? dispatch<128, float>(a, rows, stream) : dispatch<128, uint16_t>(a, rows, stream);
+    e = dtype == NVFP4_DTYPE_F32 ? dispatch<128, float>(a, rows, keys, stream) : dispatch<128, uint16_t>(a, rows, keys, stream);
   else
-    e = dtype == NVFP4_DTYPE_F32 ? dispatch<64, float>(a, rows, stream) : dispatch<64, uint16_t>(a, rows, stream);
+    e = dtype == NVFP4_DTYPE_F32 ? dispatch<64, float>(a, rows, keys, stream) : dispatch<64, uint16_t>(a, rows, keys, stream);
   return nvfp4_internal_cuda_status(e);
 }

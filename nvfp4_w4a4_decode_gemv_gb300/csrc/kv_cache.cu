@@ -33,6 +33,7 @@ struct AppendArgs {
   const float *k_global, *v_global;
   int tokens, heads, page_size;
   long long num_slots;
+  uint64_t inv_heads;               // 2^32 / heads, rounded up: a quotient where it times heads is below 2^32
 };
 
 // Raw words of a block: 16 FP32 or BF16 elements.
@@ -229,16 +230,17 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const AppendArgs
   }
 }
 
-// Few tokens: a thread for every block, no look at the neighbours.  grid.y: tokens.
+// Few tokens: a thread for every block, no look at the neighbours.
 template <int D, class T>
 __global__ void __launch_bounds__(kThreads) kv_append_few_kernel(const AppendArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   const int it = blockIdx.x * kThreads + threadIdx.x;
-  const int b = it % KvLayout<D>::kBlocks, which = it / KvLayout<D>::kBlocks & 1, head = it / (2 * KvLayout<D>::kBlocks);
-  if (head >= a.heads) return;
-  const int slot = a.slots[blockIdx.y];
-  if (slot >= 0 && slot < a.num_slots) append_block<D, T>(a, blockIdx.y, slot, head, which, b);
+  const int b = it % KvLayout<D>::kBlocks, which = it / KvLayout<D>::kBlocks & 1, at = it / (2 * KvLayout<D>::kBlocks);
+  const int token = (int)((uint64_t)at * a.inv_heads >> 32), head = at - token * a.heads;
+  if (token >= a.tokens) return;
+  const int slot = a.slots[token];
+  if (slot >= 0 && slot < a.num_slots) append_block<D, T>(a, token, slot, head, which, b);
   else if (slot != -1) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
 }
 
@@ -249,6 +251,7 @@ struct ReadArgs {
   uint16_t *k_out, *v_out;
   int tokens, heads, page_size;
   long long num_slots;
+  uint64_t inv_heads;               // 2^32 / heads, rounded up: a quotient where it times heads is below 2^32
 };
 
 // 4 code bytes times S -> 8 BF16 values, 16 bytes.
@@ -328,27 +331,31 @@ __global__ void __launch_bounds__(kThreads) kv_read_few_kernel(const ReadArgs a)
   griddep_wait();
   const int it = blockIdx.x * kThreads + threadIdx.x;
   const int hb = it % (2 * KvLayout<D>::kBlocks), which = it / (2 * KvLayout<D>::kBlocks) & 1;
-  const int head = it / (4 * KvLayout<D>::kBlocks);
-  if (head >= a.heads) return;
-  int slot = a.slots[blockIdx.y];
+  const int at = it / (4 * KvLayout<D>::kBlocks), token = (int)((uint64_t)at * a.inv_heads >> 32);
+  const int head = at - token * a.heads;
+  if (token >= a.tokens) return;
+  int slot = a.slots[token];
   if (slot < 0 || slot >= a.num_slots) {
     if (slot != -1) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
     slot = -1;
   }
-  read_half<D>(a, blockIdx.y, slot, head, which, hb >> 1, hb & 1);
+  read_half<D>(a, token, slot, head, which, hb >> 1, hb & 1);
 }
 
-// Up to kFew threads every (half) block gets its own at once, and the shorter chain of loads wins.  per_token: the
-// (half) blocks of a token.
-constexpr long long kFew = 1 << 16;
+// Up to so many elements of K every (half) block gets a thread of its own at once, and the shorter chain of loads wins.
+// Own threads / windows, BF16, 8 heads of 128, us:  append 2.2 / 3.0 (256 tokens), 4.5 / 4.9 (2048), 7.3 / 6.6 (4096);
+// read 2.1 / 2.6, 4.7 / 4.5, 8.0 / 5.6.  One head: append 1.9 / 2.9, 2.1 / 3.0, 3.0 / 3.2.
+constexpr long long kFew = 1 << 21;
 
-template <class Args>
-cudaError_t launch(void (*window)(Args), void (*few)(Args), Args a, int per_token, cudaStream_t stream) {
+// per_thread: elements of K or V that a thread of `few` has, twice over.
+template <int D, class Args>
+cudaError_t launch(void (*window)(Args), void (*few)(Args), Args a, int per_thread, cudaStream_t stream) {
   const long long tasks = (a.tokens + (long long)kKvGroup - 1) / kKvGroup * a.heads * 2;
-  const bool is_few = (long long)a.tokens * per_token <= kFew && a.tokens <= 65535;
+  const bool is_few = (long long)a.tokens * a.heads * D <= kFew;   // (heads <= 1024)
+  a.inv_heads = ((1ull << 32) + a.heads - 1) / a.heads;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = is_few ? dim3((unsigned)((per_token + kThreads - 1) / kThreads), (unsigned)a.tokens)
-                       : dim3((unsigned)((tasks + kWarps - 1) / kWarps));
+  cfg.gridDim = dim3((unsigned)(is_few ? ((long long)a.tokens * a.heads * (D / per_thread) + kThreads - 1) / kThreads
+                                       : (tasks + kWarps - 1) / kWarps));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -408,11 +415,11 @@ extern "C" nvfp4_status nvfp4_kv_append(const void* k, const void* v, int dtype,
   a.num_slots = (long long)cache->num_pages * cache->page_size;
   cudaError_t e;
   if (cache->head_dim == 128)
-    e = dtype == NVFP4_DTYPE_F32 ? launch(kv_append_kernel<128, float>, kv_append_few_kernel<128, float>, a, a.heads * 128 / 8, stream)
-                                 : launch(kv_append_kernel<128, uint16_t>, kv_append_few_kernel<128, uint16_t>, a, a.heads * 128 / 8, stream);
+    e = dtype == NVFP4_DTYPE_F32 ? launch<128>(kv_append_kernel<128, float>, kv_append_few_kernel<128, float>, a, 8, stream)
+                                 : launch<128>(kv_append_kernel<128, uint16_t>, kv_append_few_kernel<128, uint16_t>, a, 8, stream);
   else
-    e = dtype == NVFP4_DTYPE_F32 ? launch(kv_append_kernel<64, float>, kv_append_few_kernel<64, float>, a, a.heads * 64 / 8, stream)
-                                 : launch(kv_append_kernel<64, uint16_t>, kv_append_few_kernel<64, uint16_t>, a, a.heads * 64 / 8, stream);
+    e = dtype == NVFP4_DTYPE_F32 ? launch<64>(kv_append_kernel<64, float>, kv_append_few_kernel<64, float>, a, 8, stream)
+                                 : launch<64>(kv_append_kernel<64, uint16_t>, kv_append_few_kernel<64, uint16_t>, a, 8, stream);
   return nvfp4_internal_cuda_status(e);
 }
 
@@ -434,7 +441,7 @@ extern "C" nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int32_t
   a.k_out = k_out, a.v_out = v_out;
   a.tokens = tokens, a.heads = cache->kv_heads, a.page_size = cache->page_size;
   a.num_slots = (long long)cache->num_pages * cache->page_size;
-  const cudaError_t e = cache->head_dim == 128 ? launch(kv_read_kernel<128>, kv_read_few_kernel<128>, a, a.heads * 128 / 4, stream)
-                                               : launch(kv_read_kernel<64>, kv_read_few_kernel<64>, a, a.heads * 64 / 4, stream);
+  const cudaError_t e = cache->head_dim == 128 ? launch<128>(kv_read_kernel<128>, kv_read_few_kernel<128>, a, 4, stream)
+                                               : launch<64>(kv_read_kernel<64>, kv_read_few_kernel<64>, a, 4, stream);
   return nvfp4_internal_cuda_status(e);
 }
