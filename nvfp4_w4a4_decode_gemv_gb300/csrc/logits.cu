@@ -9,8 +9,10 @@
 // same memory (an integer maximum), and writes each logit once.  Bound by HBM for
 // large batches (4 bytes in, 4 out a logit), by latency for small ones.  Every
 // CTA of a row reads the row's whole history (from L2): 16 KB against the 64 KB of
-// logits of an 8192-token chunk at 4096 tokens; counting through a cluster's
-// distributed shared memory would read it once, at the price of a cluster barrier.
+// logits of an 8192-token chunk at 4096 tokens.  64 rows of 151936 logits: 18 us without
+// a history (12.2 at the copy rate), 32 with 16384 tokens a row: the rest is issue slots
+// of the looks at tokens.  Counted once a cluster of 7 CTAs, through their distributed
+// shared memory, it took 50 us (30 instead of 20 with 256 tokens a row).
 #include <math.h>
 
 #include "common.cuh"
