@@ -12,8 +12,8 @@ KV cache, attention and logit rules.
 Every layer has a cache of its own; one page table serves them all (a page has
 the same number in each).  Requests come with `start` (prompts, whose K and V
 rows the caller gives) and go with `end`, whose pages the next requests get.
-No rotary positions: the step is synthetic, and `plan.positions` is where a
-model takes them from.  The step itself (`run`, `capture`) reads lengths, tables
+No rotary positions: the step is synthetic, and `plan.positions` (of the rows
+with a request, one behind the other) is where a model takes them from.  The step itself (`run`, `capture`) reads lengths, tables
 and histories on the device only, so one captured graph follows any requests.
 """
 import torch
@@ -34,7 +34,8 @@ class ServingStep(DecodeStep):
                        for _ in range(layers)]
         # requests: keys held, page table, stack of free pages
         self.lens = torch.zeros(M, **i32)
-        self.ones = torch.ones(M, **i32)
+        self.active = torch.zeros(M, **i32)              # 1: the row has a request
+        self.slots = torch.full((M,), -1, **i32)         # of each row's new token, -1: none, or no page for it
         self.table = torch.full((M, -(-max_len // page_size)), -1, **i32)
         self.free_pages = torch.arange(num_pages, **i32)
         self.free_count = torch.full((1,), num_pages, **i32)
@@ -71,19 +72,20 @@ class ServingStep(DecodeStep):
         for row, ids in prompts.items():
             self.tokens[row, :ids.numel()] = ids
             self.n_tokens[row] = self.n_prompt[row] = ids.numel()
+            self.active[row] = 1
         return plan
 
     def end(self, ended: torch.Tensor):
         """Requests with ended[row] != 0 (uint8 [M]) leave; their pages are free again."""
         api.nvfp4_kv_release(self.lens, ended, self.table, self.free_pages, self.free_count, self.page_size)
         stay = (ended == 0).to(torch.int32)
-        for t in (self.lens, self.n_tokens, self.n_prompt):
+        for t in (self.lens, self.n_tokens, self.n_prompt, self.active):
             t.mul_(stay)
 
     # ---- the step -----------------------------------------------------------------
     def _attend(self, layer: int, stream):
         cache = self.caches[layer]
-        api.nvfp4_kv_append(self.k, self.v, self.plan.slots, cache, stream=stream)
+        api.nvfp4_kv_append(self.k, self.v, self.slots, cache, stream=stream)
         api.nvfp4_kv_attention(self.q, cache, self.table, self.plan.kv_lens, out=self.attn, workspace=self.attn_ws,
                                stream=stream)
         api.nvfp4_quantize_act(self.attn.view(self.M, self.k_o), out=self.xq_o, stream=stream)
@@ -95,13 +97,18 @@ class ServingStep(DecodeStep):
         return super()._sample(stream)
 
     def run(self, stream=None, trace=None):
-        """One decode step of every request: h_in, u, step_start -> sampler.token; lengths and histories move on."""
+        """One decode step of every request: h_in, u, step_start -> sampler.token; lengths and histories move on, but
+        not those of a request for whose token there is no page.  Rows without a request compute, and change nothing."""
         with torch.cuda.stream(stream):
-            api.nvfp4_kv_plan(self.lens, self.ones, self.table, self.free_pages, self.free_count, self.page_size,
+            api.nvfp4_kv_plan(self.lens, self.active, self.table, self.free_pages, self.free_count, self.page_size,
                               out=self.plan, stream=stream)
+            # the plan's tokens are those of the rows with a request, one behind the other
+            packed = self.plan.slots[self.plan.cu_q[:-1].clamp(max=self.M - 1).long()]
+            self.slots.copy_(torch.where(self.active > 0, packed, -1))
             out = super().run(stream, trace)
             self.lens.copy_(self.plan.kv_lens)
             at = self.n_tokens.clamp(max=self.max_len - 1).long()
-            self.tokens[self.rows, at] = self.sampler.token
-            self.n_tokens.add_(1).clamp_(max=self.max_len)
+            moved = self.slots >= 0
+            self.tokens[self.rows, at] = torch.where(moved, self.sampler.token, self.tokens[self.rows, at])
+            self.n_tokens.add_(moved.to(torch.int32)).clamp_(max=self.max_len)
         return out

@@ -145,3 +145,38 @@ def test_full_pool_refuses_and_other_requests_go_on():
     assert to_np(st.plan.info).tolist() == [2, M] and to_np(st.lens).tolist() == [16, 16, 21]
     assert to_np(st.plan.slots)[:2].tolist() == [-1, -1]
     assert api.device_status() == 0
+
+
+def test_rows_without_a_request_stay_empty():
+    """An ended row takes no page and no token until a request starts in it, and the others' rows stay their own."""
+    rng = np.random.default_rng(4)
+    st = _step()
+    _start(st, rng, {0: 20, 1: 31, 2: 5})
+    st.end(torch.tensor([1, 0, 0], dtype=torch.uint8, device="cuda"))
+    free = int(st.free_count)
+    for i in range(2):
+        _feed(st, rng)
+        y = []
+        real = st._attend
+
+        def spy(layer, stream):
+            y.append(st.y_qkv.clone())
+            real(layer, stream)
+        st._attend = spy
+        st.run()
+        st._attend = real
+        assert to_np(st.lens).tolist() == [0, 32 + i, 6 + i] and to_np(st.n_tokens).tolist() == [0, 32 + i, 6 + i]
+        assert to_np(st.slots)[0] == -1 and to_np(st.plan.info).tolist() == [0, 2]
+        cut = HEADS * D
+        for layer in range(LAYERS):
+            yq = Q.bf16_bits_to_f32(Q.f32_to_bf16_bits(to_np(y[layer])))
+            for r in (1, 2):
+                slot = _slots(st, r, int(st.lens[r]))[-1:]
+                kc, ks, _, _ = S.read_slots(to_np(st.caches[layer].pages), slot, PAGE, D)
+                want = S.quantize_rows(yq[r, cut:cut + KVH * D].reshape(1, KVH, D), 0.5)
+                assert np.array_equal(kc, want[0]) and np.array_equal(ks, want[1])
+    assert int(st.free_count) == free - 1                     # row 1's third page
+    _start(st, rng, {0: 18})
+    _feed(st, rng)
+    st.run()
+    assert to_np(st.lens).tolist() == [19, 34, 8] and api.device_status() == 0
