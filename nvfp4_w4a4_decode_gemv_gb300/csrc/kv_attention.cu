@@ -42,15 +42,23 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxSplits = 32;          // pieces of a segment when there are few: more cost more to merge than they save
+// Pieces of a segment when there are few: more cost more to merge than they save.  8 query heads on each of 1 / 8 kv
+// heads, one request of 4000 keys, us with 4, 8, 16, 32 pieces:  16.1, 12.8, 12.4, 15.3 / 16.3, 12.8, 13.8, 17.6;
+// 16000 keys on one kv head: 37, 23, 17.9, 17.9.
+constexpr int kMaxSplits = 16;
 constexpr int kMaxShares = 64;          // the same bound where there are many
-// More query rows of a kv head than this, and more rows x keys (kv heads x keys there is room for), take the other
-// kernel (kv_attention_tc.cu).  Here / there, D = 128, 8 kv heads, us:  32 rows: 36 / 44 (4 requests of 8000 keys),
-// 53 / 58 (16 of 4000), 93 / 135 (16 of 500 to 16384);  64 rows: 15 / 28 (one of 2000), 35 / 48 (one of 16000),
-// 49 / 45, 77 / 60, 142 / 137;  128 rows: 19 / 31, 59 / 52, 96 / 48, 145 / 62, 275 / 142.
+// More query rows of a kv head than this, and more rows x keys (kv heads x keys there is room for, and what segments
+// cost besides), take the other kernel (kv_attention_tc.cu).  Here / there, D = 128, 8 kv heads, us:  32 rows: 36 / 44
+// (4 requests of 8000 keys), 53 / 58 (16 of 4000), 93 / 135 (16 of 500 to 16384);  64 rows: 15 / 28 (one of 2000),
+// 35 / 48 (one of 16000), 49 / 45, 77 / 60, 142 / 137;  128 rows: 19 / 31, 59 / 52, 96 / 48, 145 / 62, 275 / 142;
+// prompts of 200 and 400 tokens, 4 query heads a kv head:  19 / 24, 35 / 26.
 constexpr int kTcRows = 48;
-constexpr long long kTcProducts = 1 << 24;
-constexpr int kSegmentCost = 512;       // keys that the fixed cost of a segment (queries, first copies, merge) stands for
+constexpr long long kTcProducts = 10 << 20;
+// Keys that the fixed cost of a segment (queries, first copies, merge) stands for in the split.  With 256, 512, 1024:
+// 64 requests x 16 heads with a window of 1024 keys 33.6, 30.1, 30.1 us; 16 requests of 500 to 16384 keys, 32 rows 93,
+// 84.6, 86.5 us.
+constexpr int kSegmentCost = 512;
+// Rounds for a warp below which units are halved; the same cases with 4, 8, 32: 30.9, 30.1, 30.1 and 84.7, 84.6, 94 us.
 constexpr int kShortUnits = 8;
 
 NVFP4_DEVINL uint32_t transpose8x8(uint32_t a) {
@@ -811,7 +819,8 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens,
   const long long most_units = ((long long)tokens * group / 8 + batch) * cache->kv_heads *
                                ((long long)table_width * cache->page_size / 32 + 2 + kSegmentCost / 32 + kWarps);
   cudaError_t e;
-  if ((rows > kTcRows && rows * keys > kTcProducts) || most_units > 0x7FFFFFFFll)
+  const long long segment_keys = (long long)batch * cache->kv_heads * kSegmentCost;
+  if ((rows > kTcRows && rows * (keys + segment_keys) > kTcProducts) || most_units > 0x7FFFFFFFll)
     e = nvfp4_internal_kv_attention_tc(a, cache->head_dim, dtype, stream);
   else if (cache->head_dim == 128)
     e = dtype == NVFP4_DTYPE_F32 ? dispatch<128, float>(a, rows, keys, stream) : dispatch<128, uint16_t>(a, rows, keys, stream);
