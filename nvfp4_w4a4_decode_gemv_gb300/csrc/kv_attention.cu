@@ -46,7 +46,11 @@ constexpr int kThreads = 32 * kWarps;
 // heads, one request of 4000 keys, us with 4, 8, 16, 32 pieces:  16.1, 12.8, 12.4, 15.3 / 16.3, 12.8, 13.8, 17.6;
 // 16000 keys on one kv head: 37, 23, 17.9, 17.9.
 constexpr int kMaxSplits = 16;
-constexpr int kMaxShares = 64;          // the same bound where there are many
+// Where there are many: a piece of K / s keys and a merge of s pieces take time a K / s + b s, least at s = sqrt(a K / b).
+// One request, 64/8 heads, us with 16, 24, 32, 48, 64 pieces:  8000 keys 16.0, 16.5, 18.3, 23.3, 23.2;  16000 keys 20.8,
+// 20.1, 21.5, 24.3, 25.8;  64000 keys 48, 37, 40, 35, 35;  131000 keys 74, 59, 62, 53, 50.
+constexpr int kMaxShares = 64;
+constexpr float kShareRate = 1.0f / 6.0f;   // s / sqrt(K)
 // More query rows of a kv head than this, and more rows x keys (kv heads x keys there is room for, and what segments
 // cost besides), take the other kernel (kv_attention_tc.cu).  Here / there, D = 128, 8 kv heads, us:  32 rows: 36 / 44
 // (4 requests of 8000 keys), 53 / 58 (16 of 4000), 93 / 135 (16 of 500 to 16384);  64 rows: 15 / 28 (one of 2000),
@@ -60,6 +64,10 @@ constexpr long long kTcProducts = 10 << 20;
 constexpr int kSegmentCost = 512;
 // Rounds for a warp below which units are halved; the same cases with 4, 8, 32: 30.9, 30.1, 30.1 and 84.7, 84.6, 94 us.
 constexpr int kShortUnits = 8;
+
+NVFP4_DEVINL int shares_of(int keys) {
+  return min(max((int)(sqrtf((float)keys) * kShareRate), kMaxSplits), kMaxShares);
+}
 
 NVFP4_DEVINL uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
     else longest = (longest + 1) / 2;
     // Few units: every CTA a piece of one segment, one unit a warp or as many as keep a segment's pieces under
     // kMaxSplits.  Many: equal ranges, where a segment's fixed cost counts as kSegmentCost keys, and at most
-    // kMaxShares of them a segment.
+    // shares_of its keys of them a segment.
     const bool few = units4 <= (int)gridDim.x;
     const int piece = kWarps * max(1, (longest + kWarps * kMaxSplits - 1) / (kWarps * kMaxSplits));
     split = few ? Split{0, piece} : Split{kSegmentCost >> unit_log, 1};
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
       }
     }
     const int excl = inc - mine;
-    n_ctas = few ? min((int)gridDim.x, U / piece) : (int)min((long long)gridDim.x, (long long)kMaxShares * n_segs);
+    n_ctas = few ? min((int)gridDim.x, U / piece) : (int)min((long long)gridDim.x, (long long)shares_of(longest << unit_log) * n_segs);
     if ((int)blockIdx.x >= n_ctas) return;
     shares = Shares(U, n_ctas);
     u = shares.start(blockIdx.x);
