@@ -608,7 +608,8 @@ size_t reset_workspace_bytes(int M, int V);
  * four launches and computes in integer masses, exp((l - max l)/T) scaled by
  * 2^(62 - ceil(log2 V)) and rounded: deterministic, accurate to ~1e-7 of Z.
  *
- *   logits     device, [M, V] FP32, 16-byte aligned, finite
+ *   logits     device, [M, V] FP32, 16-byte aligned, finite or -inf (probability 0, e.g. a token that a grammar
+ *              forbids), with at least one finite logit a row
  *   M          1..64;  V 1 .. 2^24
  *   step_start device, [M] uint8 (may be NULL: no step boundaries)
  *   u          device, [M] FP32 uniforms in [0, 1)

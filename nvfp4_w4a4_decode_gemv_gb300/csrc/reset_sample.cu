@@ -160,13 +160,14 @@ __global__ void __launch_bounds__(kThreads) reset_sample_kernel(const float* __r
   }
   __syncthreads();
   const float cm = s_rowmax;
+  const float mb = (cm == -INFINITY) ? 0.0f : cm;   // a chunk of -inf logits sums zeros
   const float inv_tl = 1.0f / p.t_low, inv_th = 1.0f / p.t_high;   // same expressions as below
   float n0 = 0.f, z1 = 0.f, a1 = 0.f, zl = 0.f, zh = 0.f;
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
     const int i = lo + threadIdx.x + k * kThreads;
     if (i < hi) {
-      const float s = v[k] - cm;
+      const float s = v[k] - mb;
       if (s == 0.0f) {
         n0 += 1.0f;                      // e^0 = 1, counted exactly
       } else {
@@ -233,6 +234,7 @@ __global__ void __launch_bounds__(kThreads) reset_sample_kernel(const float* __r
     gmax = warp_max(gmax);
     double Z = 0.0, A = 0.0;
     auto add = [&](const float4& p0, const float4& p1) {
+      if (p0.x == -INFINITY) return;                    // a chunk of only -inf logits has no mass
       const float d = p0.x - gmax;                      // <= 0
       const double r1 = (double)expf(d);
       Z += r1 * ((double)p1.y + (double)p0.y);
