@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads) reset_sample_kernel(const float* __r
   __syncthreads();
   if (warp == 0) {
     // The first chunk whose cumulative Z_T passes the target (the last chunk
-    // if rounding leaves the target at or past the total).  Lane L owns the
+    // with mass if rounding leaves the target at or past the total).  Lane L owns the
     // consecutive chunks [L per, (L+1) per): per-lane sums, an inclusive scan
     // across the warp, and the first lane whose running sum passes the target
     // walks its own chunks (a serial loop over all chunks cost 6 us in FP64).
@@ -344,23 +344,24 @@ __global__ void __launch_bounds__(kThreads) reset_sample_kernel(const float* __r
     }
     const double total = __shfl_sync(0xffffffffu, incl, 31);
     const double target = s_target * total;     // s_target holds u until here
-    const unsigned hit = __ballot_sync(0xffffffffu, q0 < q1 && incl > target);
-    const int owner = hit ? __ffs(hit) - 1 : (NC - 1) / per;
+    const unsigned pos = __ballot_sync(0xffffffffu, mine > 0.0);
+    const unsigned hit = __ballot_sync(0xffffffffu, incl > target) & pos;
+    const int owner = hit ? __ffs(hit) - 1 : (pos ? 31 - __clz(pos) : 0);
     if (lane == owner) {
-      // The owner's last chunk is the fallback: the walk re-adds in its own
-      // order, so it may stop short of a target that `incl` passed by a
-      // rounding; for the last lane this is the "last chunk" case.
-      double before = incl - mine;
-      int cstar = q1 - 1;
-      for (int q = q0; q < q1 - 1; ++q) {
-        if (before + s_zt[q] > target) {
-          cstar = q;
-          break;
-        }
+      // The owner's last chunk with mass is the fallback: the walk re-adds in
+      // its own order, so it may stop short of a target that `incl` passed by
+      // a rounding.
+      double before = incl - mine, at = before;
+      int cstar = q0;
+      for (int q = q0; q < q1; ++q) {
+        if (!(s_zt[q] > 0.0)) continue;
+        cstar = q;
+        at = before;
+        if (before + s_zt[q] > target) break;
         before += s_zt[q];
       }
       s_chunk = cstar;
-      s_target = target - before;
+      s_target = target - at;
       s_tok = 0x7fffffff;
     }
   }
@@ -389,8 +390,9 @@ __global__ void __launch_bounds__(kThreads) reset_sample_kernel(const float* __r
     }
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
-      fsum += (i0 + k < chi) ? expf((lv[k] - gmax) * invT) : 0.0f;
-      pre[k] = fsum;
+      const float e = (i0 + k < chi) ? expf((lv[k] - gmax) * invT) : 0.0f;
+      fsum += e;
+      pre[k] = e > 0.0f ? fsum : -INFINITY;           // (one without mass is never the sample)
     }
   }
   const double tsum = (double)fsum;
@@ -415,10 +417,23 @@ __global__ void __launch_bounds__(kThreads) reset_sample_kernel(const float* __r
   }
   if (cand != 0x7fffffff) atomicMin(&s_tok, cand);
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (s_tok == 0x7fffffff) {
     // Rounding can leave the target just past the chunk's last partial sum:
-    // the sample then is the chunk's last logit.
-    token[row] = (s_tok != 0x7fffffff) ? s_tok : (chi - 1);
+    // the sample then is the chunk's last logit with mass.
+    __syncthreads();                              // everyone has looked
+    if (threadIdx.x == 0) s_tok = -1;
+    __syncthreads();
+#pragma unroll
+    for (int k = kPerThread - 1; k >= 0; --k) {
+      if (pre[k] >= 0.0f) {
+        atomicMax(&s_tok, clo + threadIdx.x * kPerThread + k);
+        break;
+      }
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    token[row] = s_tok;
     counters[row] = 0u;
   }
 }
@@ -1422,8 +1437,8 @@ __global__ void __launch_bounds__(kCThreads, 1) reset_cluster_kernel(const float
       const float n = __shfl_up_sync(0xffffffffu, zi, o);
       if (lane >= o) zi += n;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, has && zi > target);
     const unsigned pos = __ballot_sync(0xffffffffu, zr > 0.0f);
+    const unsigned hit = __ballot_sync(0xffffffffu, zi > target) & pos;
     const int rstar = hit ? __ffs(hit) - 1 : (pos ? 31 - __clz(pos) : 0);
     const float before = __shfl_sync(0xffffffffu, zi - zr, rstar);
     const float fsel = __shfl_sync(0xffffffffu, low ? fl : fh, rstar);
@@ -1459,10 +1474,10 @@ __global__ void __launch_bounds__(kCThreads, 1) reset_cluster_kernel(const float
       if (lane >= o) wi += n;
     }
     // The first warp whose running total passes the target; else the last
-    // warp that holds logits of this CTA.
-    const unsigned hit = __ballot_sync(0xffffffffu, wi > tl);
-    const int nlive = (hi - lo + 32 * PER - 1) / (32 * PER);
-    const int wsel = hit ? __ffs(hit) - 1 : nlive - 1;
+    // warp with mass (the logits behind it may be masked: -inf).
+    const unsigned pos = __ballot_sync(0xffffffffu, wt > 0.0f);
+    const unsigned hit = __ballot_sync(0xffffffffu, wi > tl) & pos;   // (tl may be a rounding below 0)
+    const int wsel = hit ? __ffs(hit) - 1 : (pos ? 31 - __clz(pos) : 0);
     const float wb = __shfl_sync(0xffffffffu, wi - wt, wsel);
     if (lane == 0) {
       s_warp = wsel;
@@ -1479,24 +1494,29 @@ __global__ void __launch_bounds__(kCThreads, 1) reset_cluster_kernel(const float
       const float n = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += n;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, incl > tl);
-    const int lsel = hit ? __ffs(hit) - 1 : 31;
+    const unsigned pos = __ballot_sync(0xffffffffu, mine > 0.0f);
+    const unsigned hit = __ballot_sync(0xffffffffu, incl > tl) & pos;
+    const int lsel = hit ? __ffs(hit) - 1 : (pos ? 31 - __clz(pos) : 0);
     if (lane == lsel) {
       const float cT = (zi == 3) ? cl : ch;
       float run = incl - mine;
-      int tok = -1, last = -1;
+      const float past = fmaxf(tl, run);              // (a sum that starts past the target by a rounding has to grow)
+      int tok = -1;
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
         if (i0 + k < hi) {
           run += exp2f((v[k] - mb) * cT);
-          last = i0 + k;
-          if (run > tl && tok < 0) tok = i0 + k;
+          if (run > past && tok < 0) tok = i0 + k;
         }
       }
-      // Rounding can leave the target just past the lane's last partial sum
-      // (or the lane may hold no logit): the sample is then the last logit of
-      // the warp's range that exists.
-      token[row] = tok >= 0 ? tok : (last >= 0 ? last : min(hi, lo + (warp + 1) * 32 * PER) - 1);
+      if (tok < 0) {
+        // Rounding can leave the target just past the lane's last partial sum:
+        // the sample is then its last logit with mass.
+#pragma unroll 1
+        for (int i = i0; i < min(i0 + PER, hi); ++i)  // (rare: read again, in few instructions)
+          if (exp2f((__ldg(base + i) - mb) * cT) > 0.0f) tok = i;
+      }
+      token[row] = tok;
     }
   }
 }

@@ -46,3 +46,21 @@ def test_masked_chunks_have_no_mass(V, top_p):
             assert R.temperature_is_ambiguous(res, p) or T[r] == np.float32(res.T)
             assert np.isfinite(ln[tok[r]]) and _token_ok(ln, float(T[r]), float(np.float32(u)), int(tok[r]), p.top_p)
     assert api.device_status() == 0
+
+
+@pytest.mark.parametrize("V", [1000, 30011, 151936, LONG])
+def test_uniforms_next_to_one_never_give_a_masked_token(V):
+    """u = 1 - 2^-24: u Z rounds past the last partial sums now and then; the token is then the last one with mass."""
+    M = 64 if V < 10 ** 5 else 16
+    s = api.ResetSampler(M, V)
+    u = torch.full((M,), 1 - 2.0 ** -24, device="cuda")
+    rng = np.random.default_rng(V)
+    for i in range(40):
+        x = _logits(V, M, 1000 * V + i).cuda()
+        cut = torch.from_numpy(rng.integers(1, V, M)).cuda()
+        x[torch.arange(V, device="cuda")[None] >= cut[:, None]] = -np.inf
+        x[:, 3::7] = -np.inf
+        x[:, 0] = 0.0
+        tok, _, _ = s(x, None, u)
+        assert torch.isfinite(x.gather(1, tok.long()[:, None])).all(), i
+    assert api.device_status() == 0
