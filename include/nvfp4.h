@@ -72,7 +72,8 @@ int nvfp4_version(void);
  *              error the GEMV workspace may hold a partial sum published after
  *              the wait gave up: zero the workspace again before its next use;
  *   bit 3 (8)  a KV cache kernel met a slot or a page outside the cache, or a
- *              length or row range outside its table, and skipped it.
+ *              length or row range outside its table, and skipped it;
+ *   bit 4 (16) reset_sample met a row that it can sample no token of.
  * Synchronous (it copies a few bytes from the device); not for use inside
  * stream capture.
  */
@@ -609,7 +610,8 @@ size_t reset_workspace_bytes(int M, int V);
  * 2^(62 - ceil(log2 V)) and rounded: deterministic, accurate to ~1e-7 of Z.
  *
  *   logits     device, [M, V] FP32, 16-byte aligned, finite or -inf (probability 0, e.g. a token that a grammar
- *              forbids), with at least one finite logit a row
+ *              forbids).  A row of -inf alone, or with a NaN or +inf, has no distribution: its token is -1, its
+ *              H 0 and its T t_high, its state stays as it is, and device error bit 4 is recorded
  *   M          1..64;  V 1 .. 2^24
  *   step_start device, [M] uint8 (may be NULL: no step boundaries)
  *   u          device, [M] FP32 uniforms in [0, 1)

@@ -23,7 +23,7 @@ __all__ = [
     "NVFP4Tensor", "ResetSampler",
     "NVFP4KVCache", "KVPlan", "nvfp4_kv_page_bytes", "nvfp4_kv_release", "nvfp4_kv_plan", "nvfp4_kv_append",
     "nvfp4_kv_read", "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_bytes", "nvfp4_process_logits",
-    "DEVERR_KV_RANGE",
+    "DEVERR_KV_RANGE", "DEVERR_NO_TOKEN",
 ]
 
 
@@ -334,6 +334,8 @@ def nvfp4_f32_to_bf16(x: torch.Tensor, y: torch.Tensor | None = None, stream=Non
 # Device error bit of a KV cache kernel that met a slot, page, length or row range outside its cache or
 # tables and skipped it (nvfp4_device_status).
 DEVERR_KV_RANGE = 8
+# Device error bit of a reset_sample row without a distribution (all -inf, a NaN, +inf): its token is -1.
+DEVERR_NO_TOKEN = 16
 # Bytes at the start of an nvfp4_kv_attention workspace that are zeroed before its first use.
 ATTENTION_WS_ZEROED = 4096
 

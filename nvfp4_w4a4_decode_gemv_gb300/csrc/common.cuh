@@ -65,6 +65,7 @@ enum : unsigned int {
   NVFP4_DEVERR_STATE_W = 2,        // reset_sample called with a window larger than the state's
   NVFP4_DEVERR_FLAG_TIMEOUT = 4,   // a wait for another CTA's partial sum exceeded its iteration limit
   NVFP4_DEVERR_KV_RANGE = 8,       // a slot, page, length or row range outside a KV cache or its tables
+  NVFP4_DEVERR_NO_TOKEN = 16,      // a row of logits without a finite entropy: nothing to sample
 };
 
 // Relaxed GPU-scope word store / load: single-copy atomic, no ordering.

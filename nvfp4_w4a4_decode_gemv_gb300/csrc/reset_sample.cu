@@ -71,7 +71,7 @@ constexpr int kHistBins = 2048;   // per-row histogram of one radix level
 struct NucRow {
   float gmax, T;                   // row maximum and chosen temperature (first launch)
   unsigned int prefix;             // key bits chosen so far; the boundary key after level 2
-  unsigned int pad;
+  unsigned int none;               // the row has nothing to sample (first launch)
   unsigned long long below;        // kept mass of the keys before the current prefix's range
   unsigned long long target;       // ceil(top_p * Z), Z the row's total integer mass
   unsigned long long zk;           // the nucleus's integer mass
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) reset_sample_kernel(const float* __r
   __shared__ double s_zt[1024];          // per-chunk Z_T (rescaled to the row max); NC <= 1024
   __shared__ double s_target;
   __shared__ float s_T, s_rowmax;
-  __shared__ int s_chunk;
+  __shared__ int s_chunk, s_none;
   __shared__ int s_tok;
 
   const int row = blockIdx.x / NC, c = blockIdx.x % NC;
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) reset_sample_kernel(const float* __r
     gmax = warp_max(gmax);
     double Z = 0.0, A = 0.0;
     auto add = [&](const float4& p0, const float4& p1) {
-      if (p0.x == -INFINITY) return;                    // a chunk of only -inf logits has no mass
+      if (p0.x == -INFINITY && p0.y == 0.0f) return;    // a chunk of only -inf logits has no mass
       const float d = p0.x - gmax;                      // <= 0
       const double r1 = (double)expf(d);
       Z += r1 * ((double)p1.y + (double)p0.y);
@@ -261,8 +261,12 @@ __global__ void __launch_bounds__(kThreads) reset_sample_kernel(const float* __r
       // the state was initialised with is an error: recorded, and the row is
       // sampled at T_high without touching its state.
       const int w = p.w;
-      const bool state_ok = (st->w == w);
-      if (!state_ok) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_STATE_W);
+      // A row without a distribution (all -inf, a NaN, +inf) gives no token
+      // and leaves its state alone, too.
+      const bool none = !isfinite(H);
+      const bool state_ok = (st->w == w) && !none;
+      if (none) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_NO_TOKEN);
+      else if (!state_ok) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_STATE_W);
       double Hs = 0.0, Hbar = 0.0, Hwin = 0.0;
       int t1 = 0, j = 0;
       if (state_ok) {
@@ -295,8 +299,9 @@ __global__ void __launch_bounds__(kThreads) reset_sample_kernel(const float* __r
         st->t = t1;
         st->j = j + 1;
       }
-      if (H_out) H_out[row] = (float)H;
+      if (H_out) H_out[row] = none ? 0.0f : (float)H;
       if (T_out) T_out[row] = T;
+      s_none = none;
       s_T = T;
       s_rowmax = gmax;
       s_target = (double)__ldg(u + row);      // scaled by Z_T below
@@ -312,7 +317,15 @@ __global__ void __launch_bounds__(kThreads) reset_sample_kernel(const float* __r
       NucRow nr = {};
       nr.gmax = gmax;
       nr.T = T;
+      nr.none = (unsigned int)s_none;
       nrows[row] = nr;
+      counters[row] = 0u;
+    }
+    return;
+  }
+  if (s_none) {
+    if (threadIdx.x == 0) {
+      token[row] = -1;
       counters[row] = 0u;
     }
     return;
@@ -1227,7 +1240,7 @@ __global__ void __launch_bounds__(kCThreads, 1) reset_cluster_kernel(const float
   __shared__ double s_ring_rest;                    // the window's other w - 1 entropies
   __shared__ RowState s_st;
   __shared__ float s_T, s_gm;
-  __shared__ int s_warp, s_rstar, s_zi;
+  __shared__ int s_warp, s_rstar, s_zi, s_none;
   __shared__ float s_tl;
 
   const uint32_t rank = cluster_ctarank();
@@ -1371,16 +1384,20 @@ __global__ void __launch_bounds__(kCThreads, 1) reset_cluster_kernel(const float
         c_A = f * (a1r + d * zr);
       }
     }
+    if (has && isnan(s_peer[lane][2])) c_rest = NAN;  // (also of a NaN among -inf alone)
     const float zlr = live ? fl * s_peer[lane][4] : 0.0f, zhr = live ? fh * s_peer[lane][5] : 0.0f;
     const float cnt = warp_sum(c_cnt), rest = warp_sum(c_rest), A = warp_sum(c_A);
     const float ztl = warp_sum(zlr), zth = warp_sum(zhr);
-    int low = 0;
+    int low = 0, none = 0;
     if (lane == 0) {
       const float zm1 = (cnt - 1.0f) + rest;
       const double H = (double)(log1pf(zm1) - A / (1.0f + zm1));
+      // A row without a distribution (all -inf, a NaN, +inf) gives no token
+      // and leaves its state alone.
+      none = !isfinite(H);
       RowState ns = s_st;
       const int w = p.w;
-      const bool state_ok = (ns.w == w);
+      const bool state_ok = (ns.w == w) && !none;
       int t1 = 0, j = 0;
       if (state_ok) {
         if (ns.t == 0 || (step_start && step_start[row])) {
@@ -1411,7 +1428,7 @@ __global__ void __launch_bounds__(kCThreads, 1) reset_cluster_kernel(const float
       }
       const float T = low ? p.t_low : p.t_high;
       if (rank == 0) {
-        if (!state_ok) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_STATE_W);
+        if (!state_ok) atomicOr(&g_nvfp4_device_error, none ? NVFP4_DEVERR_NO_TOKEN : NVFP4_DEVERR_STATE_W);
         if (state_ok) {
           RowState* stw = reinterpret_cast<RowState*>(state + (size_t)row * stride);
           reinterpret_cast<double*>(stw + 1)[ns.t % w] = H;
@@ -1420,7 +1437,7 @@ __global__ void __launch_bounds__(kCThreads, 1) reset_cluster_kernel(const float
           stw->t = t1;
           stw->j = j + 1;
         }
-        if (H_out) H_out[row] = (float)H;
+        if (H_out) H_out[row] = none ? 0.0f : (float)H;
         if (T_out) T_out[row] = T;
       }
     }
@@ -1447,11 +1464,16 @@ __global__ void __launch_bounds__(kCThreads, 1) reset_cluster_kernel(const float
       s_T = low ? p.t_low : p.t_high;
       s_rstar = rstar;
       s_zi = low ? 3 : 4;
+      s_none = none;
       s_tl = fsel > 0.0f ? (target - before) / fsel : 0.0f;   // the target within CTA rstar
     }
   }
   __syncthreads();
   const float gm = s_gm;
+  if (s_none) {                                     // (every CTA of the row)
+    if (rank == 0 && threadIdx.x == 0) token[row] = -1;
+    return;
+  }
   if constexpr (NUC) {                              // top-p (NUC is set iff 0 < top_p < 1)
     const float cT = (s_T == p.t_low) ? cl : ch;
     const int tok =
@@ -1563,6 +1585,7 @@ __global__ void __launch_bounds__(kThreads) nucleus_level_kernel(const float* __
   const float* base = logits + (size_t)row * V;
   const int lo = c * kChunk, hi = min(V, lo + kChunk);
   NucRow* nr = nrows + row;
+  if (__ldcg(&nr->none)) return;
   const float gmax = __ldcg(&nr->gmax), T = __ldcg(&nr->T);
   const float invT = 1.0f / T;
   const unsigned int prefix = __ldcg(&nr->prefix);
@@ -1684,6 +1707,10 @@ __global__ void __launch_bounds__(kThreads) nucleus_sample_kernel(const float* _
   const int lo = c * kChunk, hi = min(V, lo + kChunk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const NucRow* nr = nrows + row;
+  if (__ldcg(&nr->none)) {
+    if (c == 0 && threadIdx.x == 0) token[row] = -1;
+    return;
+  }
   const float gmax = __ldcg(&nr->gmax), T = __ldcg(&nr->T);
   const float invT = 1.0f / T;
   const unsigned int kstar = __ldcg(&nr->prefix);

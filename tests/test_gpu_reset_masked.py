@@ -64,3 +64,47 @@ def test_uniforms_next_to_one_never_give_a_masked_token(V):
         tok, _, _ = s(x, None, u)
         assert torch.isfinite(x.gather(1, tok.long()[:, None])).all(), i
     assert api.device_status() == 0
+
+
+@pytest.mark.parametrize("V", [1000, 151936, LONG])
+@pytest.mark.parametrize("top_p", [1.0, 0.9])
+def test_rows_without_a_distribution_give_no_token_and_keep_their_state(V, top_p):
+    """A row of -inf alone, one with NaN, one with +inf: token -1, reported, and the row goes on afterwards as if the
+    call had not been; the other rows do not notice."""
+    M = 4
+    a, b = api.ResetSampler(M, V, top_p=top_p), api.ResetSampler(M, V, top_p=top_p)
+    u = torch.tensor([0.1, 0.5, 0.9, 0.3], device="cuda")
+    good = _logits(V, M, 5).cuda()
+    for s in (a, b):
+        s(good, None, u)
+    bad = _logits(V, M, 6).cuda()
+    bad[0] = -np.inf
+    bad[1, V // 2] = np.nan
+    bad[3, V - 1] = np.inf
+    before = a.state.clone()
+    assert api.device_status() == 0
+    tok, H, T = (to_np(t).copy() for t in a(bad, None, u))
+    assert tok[[0, 1, 3]].tolist() == [-1, -1, -1] and tok[2] >= 0
+    assert np.all(H[[0, 1, 3]] == 0) and np.all(T[[0, 1, 3]] == np.float32(a.params.t_high))
+    assert api.device_status() == api.DEVERR_NO_TOKEN
+    stride = a.state.numel() // M
+    same = (a.state == before).view(M, stride).all(1).cpu().tolist()
+    assert same == [True, True, False, True]
+    other = bad.clone()
+    other[[0, 1, 3]] = good[[0, 1, 3]]
+    tb, Hb, Tb = (to_np(t) for t in b(other, None, u))
+    assert tb[2] == tok[2] and Hb[2] == H[2] and Tb[2] == T[2]
+    b.state.view(M, stride)[[0, 1, 3]] = before.view(M, stride)[[0, 1, 3]]
+    after = _logits(V, M, 7).cuda()
+    for x, y in zip(a(after, None, u), b(after, None, u)):
+        assert torch.equal(x, y)
+    assert api.device_status() == 0
+
+
+def test_no_alloc_rows_without_a_distribution():
+    V, M = LONG, 2
+    s = api.ResetSampler(M, V)
+    x = _logits(V, M, 8).cuda()
+    x[1] = -np.inf
+    api.reset_sample_noalloc(x, None, torch.tensor([0.5, 0.5], device="cuda"), s.state, s.params, s.token, s.H, s.T)
+    assert to_np(s.token)[0] >= 0 and to_np(s.token)[1] == -1 and api.device_status() == api.DEVERR_NO_TOKEN
