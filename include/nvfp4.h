@@ -585,6 +585,9 @@ size_t reset_state_bytes(int M, int w);
 /* Puts every row of `state` at sequence position 0 (asynchronous). */
 nvfp4_status reset_state_init(void* state, int M, int w, cudaStream_t stream);
 
+/* The same for the rows r with rows[r] != 0 alone (device, [M] uint8), e.g. where a new request takes a row. */
+nvfp4_status reset_state_init_rows(void* state, int M, int w, const uint8_t* rows, cudaStream_t stream);
+
 /* Scratch needed by reset_sample for M rows of V logits. */
 size_t reset_workspace_bytes(int M, int V);
 
@@ -629,6 +632,16 @@ nvfp4_status reset_sample(const float* logits, int M, int V, const uint8_t* step
                           const float* u, void* state, const reset_params* p, int32_t* token,
                           float* H_out, float* T_out, void* workspace, size_t workspace_bytes,
                           cudaStream_t stream);
+
+/*
+ * reset_sample for the rows r with rows[r] != 0 alone (device, [M] uint8): the
+ * others' logits are not read, their state and their entries of token, H_out
+ * and T_out stay as they are.  For batches with rows that hold no request.
+ */
+nvfp4_status reset_sample_rows(const float* logits, int M, int V, const uint8_t* step_start, const float* u,
+                               const uint8_t* rows, void* state, const reset_params* p, int32_t* token,
+                               float* H_out, float* T_out, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
 
 /*
  * reset_sample without a workspace argument: same inputs, outputs and rule as

@@ -87,9 +87,12 @@ SIGNATURES = {
                                     _c_p, _c_i, _c_p, _c_i, _c_p, _c_f, _c_p, _c_p]),
     "reset_state_bytes": (_c_sz, [_c_i, _c_i]),
     "reset_state_init": (_c_i, [_c_p, _c_i, _c_i, _c_p]),
+    "reset_state_init_rows": (_c_i, [_c_p, _c_i, _c_i, _c_p, _c_p]),
     "reset_workspace_bytes": (_c_sz, [_c_i, _c_i]),
     "reset_sample": (_c_i, [_c_p, _c_i, _c_i, _c_p, _c_p, _c_p, ctypes.POINTER(ResetParams), _c_p, _c_p, _c_p,
                             _c_p, _c_sz, _c_p]),
+    "reset_sample_rows": (_c_i, [_c_p, _c_i, _c_i, _c_p, _c_p, _c_p, _c_p, ctypes.POINTER(ResetParams), _c_p, _c_p,
+                                 _c_p, _c_p, _c_sz, _c_p]),
     "reset_sample_noalloc": (_c_i, [_c_p, _c_i, _c_i, _c_p, _c_p, _c_p, ctypes.POINTER(ResetParams), _c_p, _c_p,
                                     _c_p, _c_p]),
 }

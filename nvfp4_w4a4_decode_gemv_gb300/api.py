@@ -613,12 +613,30 @@ def reset_workspace_bytes(M: int, V: int) -> int:
     return int(lib().reset_workspace_bytes(M, V))
 
 
-def reset_state_init(state: torch.Tensor, M: int, w: int, stream=None) -> None:
-    check(lib().reset_state_init(ptr(state), M, w, stream_handle(stream)), "reset_state_init")
+def reset_state_init(state: torch.Tensor, M: int, w: int, stream=None, rows: torch.Tensor | None = None) -> None:
+    """Every row at sequence position 0; with `rows` (uint8 or bool [M]) those rows alone."""
+    if rows is None:
+        check(lib().reset_state_init(ptr(state), M, w, stream_handle(stream)), "reset_state_init")
+    else:
+        _need_row_mask(rows, M)
+        check(lib().reset_state_init_rows(ptr(state), M, w, ptr(rows), stream_handle(stream)), "reset_state_init_rows")
 
 
-def reset_sample(logits, step_start, u, state, params: ResetParams, token, H_out, T_out, workspace, stream=None):
+def _need_row_mask(rows: torch.Tensor, M: int) -> None:
+    if rows.dtype not in (torch.uint8, torch.bool) or not rows.is_cuda or not rows.is_contiguous() or rows.shape != (M,):
+        raise ValueError(f"rows must be a contiguous CUDA tensor [{M}] of uint8 or bool")
+
+
+def reset_sample(logits, step_start, u, state, params: ResetParams, token, H_out, T_out, workspace, stream=None, rows=None):
+    """One position of every row; with `rows` (uint8 or bool [M]) of those rows alone, the others' state and outputs
+    stay as they are."""
     M, V = logits.shape
+    if rows is not None:
+        _need_row_mask(rows, M)
+        check(lib().reset_sample_rows(ptr(logits), M, V, ptr(step_start), ptr(u), ptr(rows), ptr(state),
+                                      ctypes.byref(params), ptr(token), ptr(H_out), ptr(T_out), ptr(workspace),
+                                      workspace.numel(), stream_handle(stream)), "reset_sample_rows")
+        return
     check(lib().reset_sample(ptr(logits), M, V, ptr(step_start), ptr(u), ptr(state), ctypes.byref(params),
                              ptr(token), ptr(H_out), ptr(T_out), ptr(workspace), workspace.numel(),
                              stream_handle(stream)), "reset_sample")
@@ -654,10 +672,14 @@ class ResetSampler:
         self.T = torch.zeros(M, dtype=torch.float32, device=device)
         reset_state_init(self.state, M, w)
 
-    def __call__(self, logits, step_start, u, stream=None):
+    def __call__(self, logits, step_start, u, stream=None, rows=None):
         reset_sample(logits, step_start, u, self.state, self.params, self.token, self.H, self.T, self.workspace,
-                     stream)
+                     stream, rows)
         return self.token, self.H, self.T
+
+    def restart(self, rows: torch.Tensor, stream=None):
+        """The rows with rows[r] != 0 (uint8 or bool [M]) get new sequences."""
+        reset_state_init(self.state, self.M, self.params.w, stream, rows)
 
 
 def device_status() -> int:

@@ -57,7 +57,7 @@ extern "C" const char* nvfp4_status_str(nvfp4_status s) {
 
 extern "C" const char* nvfp4_last_cuda_error(void) { return g_last_cuda_error; }
 
-extern "C" int nvfp4_version(void) { return (1 << 16) | 1; }
+extern "C" int nvfp4_version(void) { return (1 << 16) | 2; }
 
 extern "C" nvfp4_status nvfp4_device_status(unsigned int* code) {
   if (!code) return NVFP4_ERR_NULL;

@@ -122,7 +122,8 @@ struct Part {
 
 __global__ void __launch_bounds__(kThreads) reset_sample_kernel(const float* __restrict__ logits, int M, int V, int NC,
                                                                const uint8_t* __restrict__ step_start,
-                                                               const float* __restrict__ u, uint8_t* state,
+                                                               const float* __restrict__ u,
+                                                               const uint8_t* __restrict__ rows, uint8_t* state,
                                                                int stride, Params p, int32_t* token, float* H_out,
                                                                float* T_out, Part* parts, unsigned int* counters,
                                                                NucRow* nrows, unsigned long long* hist) {
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(kThreads) reset_sample_kernel(const float* __r
   __shared__ int s_tok;
 
   const int row = blockIdx.x / NC, c = blockIdx.x % NC;
+  if (rows && !rows[row]) return;
   const float* base = logits + (size_t)row * V;
   const int lo = c * kChunk;
   const int hi = min(V, lo + kChunk);
@@ -1226,7 +1228,8 @@ __device__ __forceinline__ int cluster_nucleus(const float* s_v, int i0, int hi,
 template <int PER, bool NUC>
 __global__ void __launch_bounds__(kCThreads, 1) reset_cluster_kernel(const float* __restrict__ logits, int V, int CS,
                                                                       const uint8_t* __restrict__ step_start,
-                                                                      const float* __restrict__ u, uint8_t* state,
+                                                                      const float* __restrict__ u,
+                                                                      const uint8_t* __restrict__ rows, uint8_t* state,
                                                                       int stride, Params p, int32_t* token,
                                                                       float* H_out, float* T_out) {
   constexpr int kCover = kCThreads * PER;
@@ -1245,6 +1248,7 @@ __global__ void __launch_bounds__(kCThreads, 1) reset_cluster_kernel(const float
 
   const uint32_t rank = cluster_ctarank();
   const int row = blockIdx.x / CS;
+  if (rows && !rows[row]) return;                   // (the whole cluster)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float* base = logits + (size_t)row * V;
   const int lo = (int)rank * kCover;
@@ -1576,12 +1580,14 @@ __device__ __forceinline__ unsigned long long block_excl_scan_u64(unsigned long 
 // the last CTA of the row picks the digit, records it and clears the histogram.
 template <int level>
 __global__ void __launch_bounds__(kThreads) nucleus_level_kernel(const float* __restrict__ logits, int V, int NC,
-                                                                float top_p, float mscale, NucRow* nrows,
+                                                                float top_p, float mscale,
+                                                                const uint8_t* __restrict__ rows, NucRow* nrows,
                                                                 unsigned long long* hist, unsigned int* counters) {
   __shared__ unsigned long long s_h[kHistBins];
   __shared__ unsigned long long s_w[kThreads / 32];
   __shared__ int s_last, s_b;
   const int row = blockIdx.x / NC, c = blockIdx.x % NC;
+  if (rows && !rows[row]) return;
   const float* base = logits + (size_t)row * V;
   const int lo = c * kChunk, hi = min(V, lo + kChunk);
   NucRow* nr = nrows + row;
@@ -1697,12 +1703,13 @@ __global__ void __launch_bounds__(kThreads) nucleus_level_kernel(const float* __
 // prefix scan of that one chunk -- all in exact integers.
 __global__ void __launch_bounds__(kThreads) nucleus_sample_kernel(const float* __restrict__ logits, int V, int NC,
                                                                  const float* __restrict__ u, float mscale,
-                                                                 const NucRow* nrows, unsigned long long* csum,
+                                                                 const uint8_t* __restrict__ rows, const NucRow* nrows, unsigned long long* csum,
                                                                  unsigned int* counters, int32_t* token) {
   __shared__ unsigned long long s_w[kThreads / 32];
   __shared__ unsigned long long s_target;
   __shared__ int s_last, s_chunk, s_tok;
   const int row = blockIdx.x / NC, c = blockIdx.x % NC;
+  if (rows && !rows[row]) return;
   const float* base = logits + (size_t)row * V;
   const int lo = c * kChunk, hi = min(V, lo + kChunk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1810,9 +1817,9 @@ __global__ void __launch_bounds__(kThreads) nucleus_sample_kernel(const float* _
   }
 }
 
-__global__ void reset_state_init_kernel(uint8_t* state, int M, int w, int stride) {
+__global__ void reset_state_init_kernel(uint8_t* state, int M, int w, int stride, const uint8_t* rows) {
   const int r = blockIdx.x * blockDim.x + threadIdx.x;
-  if (r >= M) return;
+  if (r >= M || (rows && !rows[r])) return;
   RowState* st = reinterpret_cast<RowState*>(state + (size_t)r * stride);
   st->t = 0;
   st->j = 0;
@@ -1875,7 +1882,7 @@ nvfp4_status check_params(const reset_params* p) {
 // path then serves).
 template <int PER, bool NUC>
 nvfp4_status launch_cluster_per(const float* logits, int M, int V, int CS, const uint8_t* step_start, const float* u,
-                                void* state, const Params& prm, int32_t* token, float* H_out, float* T_out,
+                                const uint8_t* rows, void* state, const Params& prm, int32_t* token, float* H_out, float* T_out,
                                 cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(M * CS));
@@ -1903,25 +1910,25 @@ nvfp4_status launch_cluster_per(const float* logits, int M, int V, int CS, const
     if (err != cudaSuccess) return nvfp4_internal_cuda_status(err);
     cfg.dynamicSmemBytes = (size_t)bytes;
   }
-  return nvfp4_internal_cuda_status(cudaLaunchKernelEx(&cfg, reset_cluster_kernel<PER, NUC>, logits, V, CS, step_start, u,
+  return nvfp4_internal_cuda_status(cudaLaunchKernelEx(&cfg, reset_cluster_kernel<PER, NUC>, logits, V, CS, step_start, u, rows,
                                                        static_cast<uint8_t*>(state), (int)state_stride(prm.w), prm,
                                                        token, H_out, T_out));
 }
 
 template <bool NUC>
-bool launch_cluster_nuc(const float* logits, int M, int V, const uint8_t* step_start, const float* u, void* state,
-                        const Params& prm, int32_t* token, float* H_out, float* T_out, cudaStream_t stream,
+bool launch_cluster_nuc(const float* logits, int M, int V, const uint8_t* step_start, const float* u,
+                        const uint8_t* rows, void* state, const Params& prm, int32_t* token, float* H_out, float* T_out, cudaStream_t stream,
                         nvfp4_status* st) {
   const long long per_cta12 = (long long)kCThreads * 12, per_cta20 = (long long)kCThreads * 20,
                   per_cta32 = (long long)kCThreads * 32;
   if (V <= kMaxClusterCtas * per_cta12) {
-    *st = launch_cluster_per<12, NUC>(logits, M, V, (int)((V + per_cta12 - 1) / per_cta12), step_start, u, state,
+    *st = launch_cluster_per<12, NUC>(logits, M, V, (int)((V + per_cta12 - 1) / per_cta12), step_start, u, rows, state,
                                       prm, token, H_out, T_out, stream);
   } else if (V <= kMaxClusterCtas * per_cta20) {
-    *st = launch_cluster_per<20, NUC>(logits, M, V, (int)((V + per_cta20 - 1) / per_cta20), step_start, u, state,
+    *st = launch_cluster_per<20, NUC>(logits, M, V, (int)((V + per_cta20 - 1) / per_cta20), step_start, u, rows, state,
                                       prm, token, H_out, T_out, stream);
   } else if (V <= kMaxClusterCtas * per_cta32) {
-    *st = launch_cluster_per<32, NUC>(logits, M, V, (int)((V + per_cta32 - 1) / per_cta32), step_start, u, state,
+    *st = launch_cluster_per<32, NUC>(logits, M, V, (int)((V + per_cta32 - 1) / per_cta32), step_start, u, rows, state,
                                       prm, token, H_out, T_out, stream);
   } else {
     return false;
@@ -1931,17 +1938,17 @@ bool launch_cluster_nuc(const float* logits, int M, int V, const uint8_t* step_s
 
 // The cluster sampler when the row fits one cluster (V <= 8 x 1024 x 32);
 // false otherwise (the multi-launch path then serves).
-bool launch_cluster(const float* logits, int M, int V, const uint8_t* step_start, const float* u, void* state,
-                    const Params& prm, int32_t* token, float* H_out, float* T_out, cudaStream_t stream,
+bool launch_cluster(const float* logits, int M, int V, const uint8_t* step_start, const float* u, const uint8_t* rows,
+                    void* state, const Params& prm, int32_t* token, float* H_out, float* T_out, cudaStream_t stream,
                     nvfp4_status* st) {
   const bool nuc = prm.top_p > 0.0f && prm.top_p < 1.0f;
-  return nuc ? launch_cluster_nuc<true>(logits, M, V, step_start, u, state, prm, token, H_out, T_out, stream, st)
-             : launch_cluster_nuc<false>(logits, M, V, step_start, u, state, prm, token, H_out, T_out, stream, st);
+  return nuc ? launch_cluster_nuc<true>(logits, M, V, step_start, u, rows, state, prm, token, H_out, T_out, stream, st)
+             : launch_cluster_nuc<false>(logits, M, V, step_start, u, rows, state, prm, token, H_out, T_out, stream, st);
 }
 
 // The sampler's launches for M rows in `scratch` (laid out by sample_layout).
 nvfp4_status launch_sample(const float* logits, int M, int V, int NC, const uint8_t* step_start, const float* u,
-                           void* state, const reset_params* p, int32_t* token, float* H_out, float* T_out,
+                           const uint8_t* rows, void* state, const reset_params* p, int32_t* token, float* H_out, float* T_out,
                            uint8_t* scratch, cudaStream_t stream) {
   const SampleLayout L = sample_layout(M, NC);
   unsigned int* counters = reinterpret_cast<unsigned int*>(scratch);
@@ -1953,20 +1960,20 @@ nvfp4_status launch_sample(const float* logits, int M, int V, int NC, const uint
   Params prm{p->tau0, p->t_low, p->t_high, p->w, p->threshold, p->top_p, mass_scale(V)};
   {
     nvfp4_status cst = NVFP4_OK;
-    if (launch_cluster(logits, M, V, step_start, u, state, prm, token, H_out, T_out, stream, &cst)) return cst;
+    if (launch_cluster(logits, M, V, step_start, u, rows, state, prm, token, H_out, T_out, stream, &cst)) return cst;
   }
-  reset_sample_kernel<<<M * NC, kThreads, 0, stream>>>(logits, M, V, NC, step_start, u, static_cast<uint8_t*>(state),
-                                                        (int)state_stride(p->w), prm, token, H_out, T_out, parts,
+  reset_sample_kernel<<<M * NC, kThreads, 0, stream>>>(logits, M, V, NC, step_start, u, rows,
+                                                        static_cast<uint8_t*>(state), (int)state_stride(p->w), prm, token, H_out, T_out, parts,
                                                         counters, nucleus ? nrows : nullptr, hist);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !nucleus) return nvfp4_internal_cuda_status(e);
   const float mscale = mass_scale(V);
-  nucleus_level_kernel<0><<<M * NC, kThreads, 0, stream>>>(logits, V, NC, p->top_p, mscale, nrows, hist, counters);
-  nucleus_level_kernel<1><<<M * NC, kThreads, 0, stream>>>(logits, V, NC, p->top_p, mscale, nrows, hist, counters);
-  nucleus_level_kernel<2><<<M * NC, kThreads, 0, stream>>>(logits, V, NC, p->top_p, mscale, nrows, hist, counters);
+  nucleus_level_kernel<0><<<M * NC, kThreads, 0, stream>>>(logits, V, NC, p->top_p, mscale, rows, nrows, hist, counters);
+  nucleus_level_kernel<1><<<M * NC, kThreads, 0, stream>>>(logits, V, NC, p->top_p, mscale, rows, nrows, hist, counters);
+  nucleus_level_kernel<2><<<M * NC, kThreads, 0, stream>>>(logits, V, NC, p->top_p, mscale, rows, nrows, hist, counters);
   e = cudaGetLastError();
   if (e != cudaSuccess) return nvfp4_internal_cuda_status(e);
-  nucleus_sample_kernel<<<M * NC, kThreads, 0, stream>>>(logits, V, NC, u, mscale, nrows, csum, counters, token);
+  nucleus_sample_kernel<<<M * NC, kThreads, 0, stream>>>(logits, V, NC, u, mscale, rows, nrows, csum, counters, token);
   return nvfp4_internal_cuda_status(cudaGetLastError());
 }
 
@@ -1977,12 +1984,21 @@ extern "C" size_t reset_state_bytes(int M, int w) {
   return (size_t)M * state_stride(w);
 }
 
-extern "C" nvfp4_status reset_state_init(void* state, int M, int w, cudaStream_t stream) {
+static nvfp4_status state_init(void* state, int M, int w, const uint8_t* rows, cudaStream_t stream) {
   if (!state) return NVFP4_ERR_NULL;
   if (M < 1 || M > kMaxRows || w < 1 || w > kMaxW) return NVFP4_ERR_RANGE;
   if (!nvfp4_internal_aligned(state, 16)) return NVFP4_ERR_ALIGN;
-  reset_state_init_kernel<<<1, kMaxRows, 0, stream>>>(static_cast<uint8_t*>(state), M, w, (int)state_stride(w));
+  reset_state_init_kernel<<<1, kMaxRows, 0, stream>>>(static_cast<uint8_t*>(state), M, w, (int)state_stride(w),
+                                                      rows);
   return nvfp4_internal_cuda_status(cudaGetLastError());
+}
+
+extern "C" nvfp4_status reset_state_init(void* state, int M, int w, cudaStream_t stream) {
+  return state_init(state, M, w, nullptr, stream);
+}
+
+extern "C" nvfp4_status reset_state_init_rows(void* state, int M, int w, const uint8_t* rows, cudaStream_t stream) {
+  return rows ? state_init(state, M, w, rows, stream) : NVFP4_ERR_NULL;
 }
 
 extern "C" size_t reset_workspace_bytes(int M, int V) {
@@ -1991,9 +2007,9 @@ extern "C" size_t reset_workspace_bytes(int M, int V) {
   return sample_layout(M, NC).total;
 }
 
-extern "C" nvfp4_status reset_sample(const float* logits, int M, int V, const uint8_t* step_start, const float* u,
-                                     void* state, const reset_params* p, int32_t* token, float* H_out, float* T_out,
-                                     void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+static nvfp4_status sample(const float* logits, int M, int V, const uint8_t* step_start, const float* u,
+                           const uint8_t* rows, void* state, const reset_params* p, int32_t* token, float* H_out,
+                           float* T_out, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   if (!logits || !u || !state || !p || !token || !workspace) return NVFP4_ERR_NULL;
   if (M < 1 || M > kMaxRows) return NVFP4_ERR_RANGE;
   if (V < 1 || V > (1 << 24)) return NVFP4_ERR_SHAPE;
@@ -2007,8 +2023,22 @@ extern "C" nvfp4_status reset_sample(const float* logits, int M, int V, const ui
   if (workspace_bytes < reset_workspace_bytes(M, V)) return NVFP4_ERR_SHAPE;
   nvfp4_status ds = nvfp4_internal_check_device();
   if (ds != NVFP4_OK) return ds;
-  return launch_sample(logits, M, V, NC, step_start, u, state, p, token, H_out, T_out,
+  return launch_sample(logits, M, V, NC, step_start, u, rows, state, p, token, H_out, T_out,
                        static_cast<uint8_t*>(workspace), stream);
+}
+
+extern "C" nvfp4_status reset_sample(const float* logits, int M, int V, const uint8_t* step_start, const float* u,
+                                     void* state, const reset_params* p, int32_t* token, float* H_out, float* T_out,
+                                     void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return sample(logits, M, V, step_start, u, nullptr, state, p, token, H_out, T_out, workspace, workspace_bytes, stream);
+}
+
+extern "C" nvfp4_status reset_sample_rows(const float* logits, int M, int V, const uint8_t* step_start, const float* u,
+                                          const uint8_t* rows, void* state, const reset_params* p, int32_t* token,
+                                          float* H_out, float* T_out, void* workspace, size_t workspace_bytes,
+                                          cudaStream_t stream) {
+  if (!rows) return NVFP4_ERR_NULL;
+  return sample(logits, M, V, step_start, u, rows, state, p, token, H_out, T_out, workspace, workspace_bytes, stream);
 }
 
 // ---- allocation-free variant ------------------------------------------------------
@@ -2076,5 +2106,5 @@ extern "C" nvfp4_status reset_sample_noalloc(const float* logits, int M, int V, 
     e = cudaMemsetAsync(scratch, 0, kCounterBytes, stream);
     if (e != cudaSuccess) return nvfp4_internal_cuda_status(e);
   }
-  return launch_sample(logits, M, V, NC, step_start, u, state, p, token, H_out, T_out, scratch, stream);
+  return launch_sample(logits, M, V, NC, step_start, u, nullptr, state, p, token, H_out, T_out, scratch, stream);
 }

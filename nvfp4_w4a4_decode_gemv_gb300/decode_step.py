@@ -100,6 +100,10 @@ class DecodeStep:
                                        self.xq_d.global_scale.clone()),
                               "h_out": self.h.clone()})
 
+    def _input(self):
+        """The hidden state that the first layer reads."""
+        return self.h_in
+
     def _attend(self, layer: int, stream):
         """From the qkv output to the o projection's NVFP4 input: here the query part alone (no attention)."""
         api.nvfp4_quantize_f32(self.y_qkv, K=self.k_o, out=self.xq_o, stream=stream)
@@ -113,7 +117,7 @@ class DecodeStep:
         """Issue one decode step on `stream` (the current stream by default):
         h_in, step_start, u -> sampler.token / .H / .T.  With a list `trace`,
         the intermediates of every layer are appended to it (eager runs only)."""
-        h_in = self.h_in
+        h_in = self._input()
         for layer in range(self.layers):
             self._layer(layer, h_in, stream, trace)
             h_in = self.h

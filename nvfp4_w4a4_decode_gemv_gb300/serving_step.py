@@ -7,7 +7,7 @@ KV cache, attention and logit rules.
         q columns over it -> BF16                     nvfp4_kv_attention
         -> NVFP4                                      nvfp4_quantize_act
     logits -> penalties, biases, grammar masks        nvfp4_process_logits (in place)
-    -> ReSET sampler; the token joins its request's history
+    -> ReSET sampler of the rows with a request; the token joins its request's history
 
 Every layer has a cache of its own; one page table serves them all (a page has
 the same number in each).  Requests come with `start` (prompts, whose K and V
@@ -36,6 +36,10 @@ class ServingStep(DecodeStep):
         self.lens = torch.zeros(M, **i32)
         self.active = torch.zeros(M, **i32)              # 1: the row has a request
         self.slots = torch.full((M,), -1, **i32)         # of each row's new token, -1: none, or no page for it
+        self.live = torch.zeros(M, dtype=torch.bool, device=dev)   # rows with a slot: the step is theirs
+        self.attn_lens = torch.zeros(M, **i32)           # keys that a live row sees, 0 for the others
+        self.h_live = torch.zeros_like(self.h_in)        # h_in of the live rows, 0 for the others
+        self.none, self.zero = torch.zeros((), **i32), torch.zeros((), device=dev)
         self.table = torch.full((M, -(-max_len // page_size)), -1, **i32)
         self.free_pages = torch.arange(num_pages, **i32)
         self.free_count = torch.full((1,), num_pages, **i32)
@@ -69,6 +73,7 @@ class ServingStep(DecodeStep):
         for cache, k, v in zip(self.caches, keys, values):
             api.nvfp4_kv_append(k, v, plan.slots, cache)
         self.lens.copy_(plan.kv_lens)
+        self.sampler.restart(torch.tensor([row in prompts for row in range(self.M)], device=self.device))
         for row, ids in prompts.items():
             self.tokens[row, :ids.numel()] = ids
             self.n_tokens[row] = self.n_prompt[row] = ids.numel()
@@ -83,10 +88,13 @@ class ServingStep(DecodeStep):
             t.mul_(stay)
 
     # ---- the step -----------------------------------------------------------------
+    def _input(self):
+        return self.h_live
+
     def _attend(self, layer: int, stream):
         cache = self.caches[layer]
         api.nvfp4_kv_append(self.k, self.v, self.slots, cache, stream=stream)
-        api.nvfp4_kv_attention(self.q, cache, self.table, self.plan.kv_lens, out=self.attn, workspace=self.attn_ws,
+        api.nvfp4_kv_attention(self.q, cache, self.table, self.attn_lens, out=self.attn, workspace=self.attn_ws,
                                stream=stream)
         api.nvfp4_quantize_act(self.attn.view(self.M, self.k_o), out=self.xq_o, stream=stream)
 
@@ -94,21 +102,25 @@ class ServingStep(DecodeStep):
         api.nvfp4_process_logits(self.logits, self.tokens, self.n_tokens, self.n_prompt, self.repetition, self.presence,
                                  self.frequency, self.bias_ids, self.bias_values, self.mask, self.mask_rows,
                                  out=self.logits, stream=stream)
-        return super()._sample(stream)
+        return self.sampler(self.logits, self.step_start, self.u, stream=stream, rows=self.live)
 
     def run(self, stream=None, trace=None):
         """One decode step of every request: h_in, u, step_start -> sampler.token; lengths and histories move on, but
-        not those of a request for whose token there is no page.  Rows without a request compute, and change nothing."""
+        not those of a request for whose token there is no page.  Such rows, and those without a request, are zero
+        throughout: they change no result of the others (whose activations they share a scale with), no state and no
+        output."""
         with torch.cuda.stream(stream):
             api.nvfp4_kv_plan(self.lens, self.active, self.table, self.free_pages, self.free_count, self.page_size,
                               out=self.plan, stream=stream)
             # the plan's tokens are those of the rows with a request, one behind the other
             packed = self.plan.slots[self.plan.cu_q[:-1].clamp(max=self.M - 1).long()]
             self.slots.copy_(torch.where(self.active > 0, packed, -1))
+            torch.ge(self.slots, 0, out=self.live)
+            torch.where(self.live, self.plan.kv_lens, self.none, out=self.attn_lens)
+            torch.where(self.live[:, None], self.h_in, self.zero, out=self.h_live)
             out = super().run(stream, trace)
             self.lens.copy_(self.plan.kv_lens)
             at = self.n_tokens.clamp(max=self.max_len - 1).long()
-            moved = self.slots >= 0
-            self.tokens[self.rows, at] = torch.where(moved, self.sampler.token, self.tokens[self.rows, at])
-            self.n_tokens.add_(moved.to(torch.int32)).clamp_(max=self.max_len)
+            self.tokens[self.rows, at] = torch.where(self.live, self.sampler.token, self.tokens[self.rows, at])
+            self.n_tokens.add_(self.live.to(torch.int32)).clamp_(max=self.max_len)
         return out

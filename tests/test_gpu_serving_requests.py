@@ -123,64 +123,3 @@ def test_captured_step_with_empty_and_reused_rows():
         return out
     for x, y in zip(play(False), play(True)):
         _same(x, y)
-
-
-def test_a_refused_prompt_leaves_its_row_empty():
-    """A pool too small for the second of three prompts: its row has no request, takes no page when one comes free,
-    and can be started again."""
-    big, small, other = Request(60, 40), Request(61, 5), Request(62, 16)
-    st = _step(num_pages=3)
-    plan = _start(st, {0: small, 1: big, 2: other})                  # 1 + 3 + 1 pages of 3: rows 1 and 2 (behind it) refused
-    assert to_np(plan.info).tolist()[0] == 2 and to_np(plan.kv_lens).tolist() == [5, 0, 0]
-    assert to_np(st.lens).tolist() == [5, 0, 0] and to_np(st.active).tolist() == [1, 0, 0]
-    assert to_np(st.n_tokens).tolist() == [5, 0, 0] and to_np(st.n_prompt).tolist() == [5, 0, 0]
-    _run(st, {0: small.feeds[0]})
-    _end(st, 0)
-    assert int(st.free_count) == 3
-    st.run()
-    assert int(st.free_count) == 3 and to_np(st.lens).tolist() == [0, 0, 0] and not to_np(st.n_tokens).any()
-    _start(st, {1: big})
-    ref = _step()
-    _start(ref, {1: Request(60, 40)})
-    for i in range(3):
-        _same(_run(st, {1: big.feeds[i]})[1], _run(ref, {1: big.feeds[i]})[1])
-    assert api.device_status() == 0
-
-
-def test_prompts_that_do_not_fit_a_row_are_refused_before_anything_is_taken():
-    st = _step()
-    held = [t.clone() for t in (st.lens, st.n_tokens, st.active, st.free_count, st.table, st.tokens)]
-    too_long, fine = Request(70, 201), Request(71, 200)              # max_len 200, pages for 208
-    with pytest.raises(ValueError, match="max_len"):
-        _start(st, {0: Request(72, 3), 2: too_long})
-    with pytest.raises(ValueError, match="row"):
-        _start(st, {M: Request(72, 3)})
-    with pytest.raises(ValueError, match="row"):
-        _start(st, {-1: Request(72, 3)})
-    for t, x in zip((st.lens, st.n_tokens, st.active, st.free_count, st.table, st.tokens), held):
-        assert torch.equal(t, x)
-    _start(st, {2: fine})
-    assert to_np(st.lens).tolist() == [0, 0, 200]
-
-
-def test_a_row_with_a_request_takes_no_other():
-    st = _step()
-    _start(st, {0: Request(80, 20)})
-    free, lens = int(st.free_count), to_np(st.lens).copy()
-    with pytest.raises(ValueError, match="has a request"):
-        _start(st, {0: Request(81, 4), 1: Request(82, 4)})
-    assert int(st.free_count) == free and np.array_equal(to_np(st.lens), lens) and to_np(st.active).tolist() == [1, 0, 0]
-
-
-def test_a_full_history_ends_the_row():
-    """max_len tokens: no page, no key and no token more, though the last page has room; the history stays."""
-    st = _step()
-    _start(st, {0: Request(90, 199), 1: Request(91, 10)})
-    req = Request(92, 1)
-    _run(st, {0: req.feeds[0], 1: req.feeds[1]})
-    assert to_np(st.n_tokens).tolist() == [200, 11, 0] and to_np(st.lens).tolist() == [200, 11, 0]
-    history, state = to_np(st.tokens)[0].copy(), st.sampler.state.view(M, -1)[0].clone()
-    for i in range(2):
-        _run(st, {0: req.feeds[2 + i], 1: req.feeds[4 + i]})
-    assert to_np(st.n_tokens).tolist() == [200, 13, 0] and to_np(st.lens).tolist() == [200, 13, 0]
-    assert np.array_equal(to_np(st.tokens)[0], history) and torch.equal(st.sampler.state.view(M, -1)[0], state)
