@@ -63,21 +63,24 @@ class ServingStep(DecodeStep):
     # ---- requests -----------------------------------------------------------------
     def start(self, prompts: dict, keys, values):
         """New requests: {row: prompt tokens (1-D int32 on the device)}; keys[layer], values[layer]: their K and V
-        rows [total, kv_heads, head_dim], packed in row order.  Returns the plan (its info: refused, tokens)."""
+        rows [total, kv_heads, head_dim], packed in row order.  Returns the plan (its info: refused, tokens): a prompt
+        without room has kv_lens[row] = 0 there, and its row stays without a request."""
         new = torch.zeros(self.M, dtype=torch.int32)
         for row, ids in prompts.items():
             new[row] = ids.numel()
         plan = api.KVPlan.empty(self.M, int(new.sum()), self.device, free_count=self.free_count)
-        api.nvfp4_kv_plan(self.lens, new.to(self.device), self.table, self.free_pages, self.free_count, self.page_size,
-                          out=plan)
+        new = new.to(self.device)
+        api.nvfp4_kv_plan(self.lens, new, self.table, self.free_pages, self.free_count, self.page_size, out=plan)
+        given = torch.tensor([row in prompts for row in range(self.M)], device=self.device)
+        taken = given & (plan.kv_lens == self.lens + new)
         for cache, k, v in zip(self.caches, keys, values):
             api.nvfp4_kv_append(k, v, plan.slots, cache)
         self.lens.copy_(plan.kv_lens)
-        self.sampler.restart(torch.tensor([row in prompts for row in range(self.M)], device=self.device))
+        self.sampler.restart(taken)
         for row, ids in prompts.items():
-            self.tokens[row, :ids.numel()] = ids
-            self.n_tokens[row] = self.n_prompt[row] = ids.numel()
-            self.active[row] = 1
+            self.tokens[row, :ids.numel()] = ids         # (of no meaning while n_tokens is 0)
+        for t, value in ((self.n_tokens, new), (self.n_prompt, new), (self.active, 1)):
+            t.copy_(torch.where(taken, value, t))
         return plan
 
     def end(self, ended: torch.Tensor):

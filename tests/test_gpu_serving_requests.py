@@ -123,3 +123,25 @@ def test_captured_step_with_empty_and_reused_rows():
         return out
     for x, y in zip(play(False), play(True)):
         _same(x, y)
+
+
+def test_a_refused_prompt_leaves_its_row_empty():
+    """A pool too small for the second of three prompts: its row has no request, takes no page when one comes free,
+    and can be started again."""
+    big, small, other = Request(60, 40), Request(61, 5), Request(62, 16)
+    st = _step(num_pages=3)
+    plan = _start(st, {0: small, 1: big, 2: other})                  # 1 + 3 + 1 pages of 3: rows 1 and 2 (behind it) refused
+    assert to_np(plan.info).tolist()[0] == 2 and to_np(plan.kv_lens).tolist() == [5, 0, 0]
+    assert to_np(st.lens).tolist() == [5, 0, 0] and to_np(st.active).tolist() == [1, 0, 0]
+    assert to_np(st.n_tokens).tolist() == [5, 0, 0] and to_np(st.n_prompt).tolist() == [5, 0, 0]
+    _run(st, {0: small.feeds[0]})
+    _end(st, 0)
+    assert int(st.free_count) == 3
+    st.run()
+    assert int(st.free_count) == 3 and to_np(st.lens).tolist() == [0, 0, 0] and not to_np(st.n_tokens).any()
+    _start(st, {1: big})
+    ref = _step()
+    _start(ref, {1: Request(60, 40)})
+    for i in range(3):
+        _same(_run(st, {1: big.feeds[i]})[1], _run(ref, {1: big.feeds[i]})[1])
+    assert api.device_status() == 0
