@@ -67,6 +67,10 @@ class ServingStep(DecodeStep):
         without room has kv_lens[row] = 0 there, and its row stays without a request."""
         new = torch.zeros(self.M, dtype=torch.int32)
         for row, ids in prompts.items():
+            if not 0 <= row < self.M:
+                raise ValueError(f"there is no row {row}")
+            if ids.numel() > self.max_len:
+                raise ValueError(f"the prompt of row {row} is longer than max_len")
             new[row] = ids.numel()
         plan = api.KVPlan.empty(self.M, int(new.sum()), self.device, free_count=self.free_count)
         new = new.to(self.device)

@@ -145,3 +145,19 @@ def test_a_refused_prompt_leaves_its_row_empty():
     for i in range(3):
         _same(_run(st, {1: big.feeds[i]})[1], _run(ref, {1: big.feeds[i]})[1])
     assert api.device_status() == 0
+
+
+def test_prompts_that_do_not_fit_a_row_are_refused_before_anything_is_taken():
+    st = _step()
+    held = [t.clone() for t in (st.lens, st.n_tokens, st.active, st.free_count, st.table, st.tokens)]
+    too_long, fine = Request(70, 201), Request(71, 200)              # max_len 200, pages for 208
+    with pytest.raises(ValueError, match="max_len"):
+        _start(st, {0: Request(72, 3), 2: too_long})
+    with pytest.raises(ValueError, match="row"):
+        _start(st, {M: Request(72, 3)})
+    with pytest.raises(ValueError, match="row"):
+        _start(st, {-1: Request(72, 3)})
+    for t, x in zip((st.lens, st.n_tokens, st.active, st.free_count, st.table, st.tokens), held):
+        assert torch.equal(t, x)
+    _start(st, {2: fine})
+    assert to_np(st.lens).tolist() == [0, 0, 200]
