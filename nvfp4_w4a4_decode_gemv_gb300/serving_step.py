@@ -72,6 +72,10 @@ class ServingStep(DecodeStep):
             if ids.numel() > self.max_len:
                 raise ValueError(f"the prompt of row {row} is longer than max_len")
             new[row] = ids.numel()
+        held = self.active.tolist()
+        for row in prompts:
+            if held[row]:
+                raise ValueError(f"row {row} has a request")
         plan = api.KVPlan.empty(self.M, int(new.sum()), self.device, free_count=self.free_count)
         new = new.to(self.device)
         api.nvfp4_kv_plan(self.lens, new, self.table, self.free_pages, self.free_count, self.page_size, out=plan)

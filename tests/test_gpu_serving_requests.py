@@ -161,3 +161,12 @@ def test_prompts_that_do_not_fit_a_row_are_refused_before_anything_is_taken():
         assert torch.equal(t, x)
     _start(st, {2: fine})
     assert to_np(st.lens).tolist() == [0, 0, 200]
+
+
+def test_a_row_with_a_request_takes_no_other():
+    st = _step()
+    _start(st, {0: Request(80, 20)})
+    free, lens = int(st.free_count), to_np(st.lens).copy()
+    with pytest.raises(ValueError, match="has a request"):
+        _start(st, {0: Request(81, 4), 1: Request(82, 4)})
+    assert int(st.free_count) == free and np.array_equal(to_np(st.lens), lens) and to_np(st.active).tolist() == [1, 0, 0]
