@@ -13,7 +13,7 @@ Every layer has a cache of its own; one page table serves them all (a page has
 the same number in each).  Requests come with `start` (prompts, whose K and V
 rows the caller gives) and go with `end`, whose pages the next requests get.
 No rotary positions: the step is synthetic, and `plan.positions` (of the rows
-with a request, one behind the other) is where a model takes them from.  The step itself (`run`, `capture`) reads lengths, tables
+that get a token, one behind the other) is where a model takes them from.  The step itself (`run`, `capture`) reads lengths, tables
 and histories on the device only, so one captured graph follows any requests.
 """
 import torch
@@ -35,6 +35,7 @@ class ServingStep(DecodeStep):
         # requests: keys held, page table, stack of free pages
         self.lens = torch.zeros(M, **i32)
         self.active = torch.zeros(M, **i32)              # 1: the row has a request
+        self.wanted = torch.zeros(M, **i32)              # 1: and its history has room for a token
         self.slots = torch.full((M,), -1, **i32)         # of each row's new token, -1: none, or no page for it
         self.live = torch.zeros(M, dtype=torch.bool, device=dev)   # rows with a slot: the step is theirs
         self.attn_lens = torch.zeros(M, **i32)           # keys that a live row sees, 0 for the others
@@ -117,15 +118,17 @@ class ServingStep(DecodeStep):
 
     def run(self, stream=None, trace=None):
         """One decode step of every request: h_in, u, step_start -> sampler.token; lengths and histories move on, but
-        not those of a request for whose token there is no page.  Such rows, and those without a request, are zero
-        throughout: they change no result of the others (whose activations they share a scale with), no state and no
-        output."""
+        not those of a request for whose token there is no page, or whose history is full (max_len tokens).  Such rows,
+        and those without a request, are zero throughout: they change no result of the others (whose activations they
+        share a scale with), no state and no output."""
         with torch.cuda.stream(stream):
-            api.nvfp4_kv_plan(self.lens, self.active, self.table, self.free_pages, self.free_count, self.page_size,
+            # a row with a request and room in its history gets a token
+            torch.mul(self.active, self.n_tokens < self.max_len, out=self.wanted)
+            api.nvfp4_kv_plan(self.lens, self.wanted, self.table, self.free_pages, self.free_count, self.page_size,
                               out=self.plan, stream=stream)
-            # the plan's tokens are those of the rows with a request, one behind the other
+            # the plan's tokens are those of the wanted rows, one behind the other
             packed = self.plan.slots[self.plan.cu_q[:-1].clamp(max=self.M - 1).long()]
-            self.slots.copy_(torch.where(self.active > 0, packed, -1))
+            self.slots.copy_(torch.where(self.wanted > 0, packed, -1))
             torch.ge(self.slots, 0, out=self.live)
             torch.where(self.live, self.plan.kv_lens, self.none, out=self.attn_lens)
             torch.where(self.live[:, None], self.h_in, self.zero, out=self.h_live)
@@ -133,5 +136,5 @@ class ServingStep(DecodeStep):
             self.lens.copy_(self.plan.kv_lens)
             at = self.n_tokens.clamp(max=self.max_len - 1).long()
             self.tokens[self.rows, at] = torch.where(self.live, self.sampler.token, self.tokens[self.rows, at])
-            self.n_tokens.add_(self.live.to(torch.int32)).clamp_(max=self.max_len)
+            self.n_tokens.add_(self.live.to(torch.int32))
         return out

@@ -170,3 +170,17 @@ def test_a_row_with_a_request_takes_no_other():
     with pytest.raises(ValueError, match="has a request"):
         _start(st, {0: Request(81, 4), 1: Request(82, 4)})
     assert int(st.free_count) == free and np.array_equal(to_np(st.lens), lens) and to_np(st.active).tolist() == [1, 0, 0]
+
+
+def test_a_full_history_ends_the_row():
+    """max_len tokens: no page, no key and no token more, though the last page has room; the history stays."""
+    st = _step()
+    _start(st, {0: Request(90, 199), 1: Request(91, 10)})
+    req = Request(92, 1)
+    _run(st, {0: req.feeds[0], 1: req.feeds[1]})
+    assert to_np(st.n_tokens).tolist() == [200, 11, 0] and to_np(st.lens).tolist() == [200, 11, 0]
+    history, state = to_np(st.tokens)[0].copy(), st.sampler.state.view(M, -1)[0].clone()
+    for i in range(2):
+        _run(st, {0: req.feeds[2 + i], 1: req.feeds[4 + i]})
+    assert to_np(st.n_tokens).tolist() == [200, 13, 0] and to_np(st.lens).tolist() == [200, 13, 0]
+    assert np.array_equal(to_np(st.tokens)[0], history) and torch.equal(st.sampler.state.view(M, -1)[0], state)
