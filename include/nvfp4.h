@@ -490,7 +490,8 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int32_t* slots, in
  * kv head h / (heads / kv_heads):
  *   out[r, h, :] = sum_j softmax_j(scale * q[r, h] . K[j]) V[j]      (BF16)
  *   lse[r, h]    = log sum_j exp(scale * q[r, h] . K[j])             (FP32, natural log)
- * A row that sees no key gives out = 0, lse = -inf.  The keys' dequantized
+ * A row that sees no key gives out = 0, lse = -inf; so does one all of whose scores are -inf.  A row with a NaN score,
+ * or one of +inf, gives NaN.  The keys' dequantized
  * values are exact; scores, their maxima and sums and the accumulators are FP32;
  * FP32 queries are first rounded to BF16 (RNE).
  *   q            device, [tokens, heads, head_dim] at q + r * q_token_stride + h * q_head_stride

@@ -654,15 +654,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float mw = s_m[w * S::kRows + t * 8 + row];
-          if (mw != -INFINITY) l += s_l[w * S::kRows + t * 8 + row] * ex2(mw - mx);
+          l += s_l[w * S::kRows + t * 8 + row] * (mw == -INFINITY ? 1.0f : ex2(mw - mx));   // (0 or NaN without a maximum)
         }
         if (all) {
           const int rr = row0 + t * 8 + row, tok = rq.first + rr / a.group, h = kvh * a.group + rr % a.group;
-          const float inv = l > 0.0f ? vg / l : 0.0f;
+          const float inv = l == 0.0f ? 0.0f : vg / l;
           const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x * inv, x.y * inv), hi = __floats2bfloat162_rn(x.z * inv, x.w * inv);
           *reinterpret_cast<uint2*>(a.out + ((size_t)tok * a.heads + h) * D + d) =
               make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-          if (a.lse && d == 0) a.lse[(size_t)tok * a.heads + h] = l > 0.0f ? (mx + log2f(l)) / kLog2e : -INFINITY;
+          if (a.lse && d == 0) a.lse[(size_t)tok * a.heads + h] = l == 0.0f ? -INFINITY : (mx + log2f(l)) / kLog2e;
         } else {
           __stcg(reinterpret_cast<float4*>(rec + (t * 8 + row) * D + d), x);
           if (d == 0) {
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
             }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-              if (q0 + j > c_last || m[j] == -INFINITY) continue;
+              if (q0 + j > c_last || no_keys(m[j], lq[j])) continue;
               const float mn = fmaxf(mx, m[j]), back = ex2(mx - mn), w = ex2(m[j] - mn);
               mx = mn;
               l = fmaf(lq[j], w, l * back);
@@ -710,11 +710,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
             }
           }
           const int rr = row0 + row, tok = rq.first + rr / a.group, h = kvh * a.group + rr % a.group;
-          const float inv = l > 0.0f ? vg / l : 0.0f;
+          const float inv = l == 0.0f ? 0.0f : vg / l;
           const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x * inv, x.y * inv), hi = __floats2bfloat162_rn(x.z * inv, x.w * inv);
           *reinterpret_cast<uint2*>(a.out + ((size_t)tok * a.heads + h) * D + d) =
               make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-          if (a.lse && d == 0) a.lse[(size_t)tok * a.heads + h] = l > 0.0f ? (mx + log2f(l)) / kLog2e : -INFINITY;
+          if (a.lse && d == 0) a.lse[(size_t)tok * a.heads + h] = l == 0.0f ? -INFINITY : (mx + log2f(l)) / kLog2e;
         }
         if (tid == 0) a.counters[c_first] = 0u;
       }

@@ -2,6 +2,8 @@
 // a call, conversions, and a request's rows and keys.
 #pragma once
 
+#include <math.h>
+
 #include "kv_layout.cuh"
 
 constexpr int kMaxCtas = 640;           // most CTAs of a launch
@@ -102,6 +104,10 @@ NVFP4_DEVINL Request get_request(const AttnArgs& a, int b, bool report) {
 
 // A score's factor is never 0: a hidden score, -inf, times it has to stay -inf.
 NVFP4_DEVINL float score_factor(float f) { return fmaxf(f, 1.2e-38f); }
+
+// Whether a partial sum l with maximum m counts nothing.  A row of NaN scores has no maximum either; its NaN sum is
+// carried on, so that the row's output is NaN however its keys are cut.
+NVFP4_DEVINL bool no_keys(float m, float l) { return m == -INFINITY && l == 0.0f; }
 
 // 2^-e and 2^e of the power of two at `big` (1 for 0), within FP32's normal range.
 NVFP4_DEVINL void power_of_two(float big, float& down, float& up) {

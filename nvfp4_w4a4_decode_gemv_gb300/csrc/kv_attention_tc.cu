@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
           if (nh_o > 0 && ok) wait(&pv_done[half ^ 1], (half == 0 ? step_b : step_a) + nh_o - 1, abort_flag);
         }
         tc_fence_after();
-        const float inv = l > 0.0f ? vg / l : 0.0f;
+        const float inv = l == 0.0f ? 0.0f : vg / l;
         uint16_t* out = a.out + ((size_t)tok * a.heads + head) * D;
         float* rec = a.records + (size_t)record * S::kRecord;
         const int rt = row_h + r;                       // row in the tile
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tc_kernel(const Attn
         }
         const bool says = mine && part == 0 && (both || half == 0);
         if (says && whole && a.lse)
-          a.lse[(size_t)tok * a.heads + head] = l > 0.0f ? (m + log2f(l)) / kLog2e : -INFINITY;
+          a.lse[(size_t)tok * a.heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) / kLog2e;
         if (says && !whole) {
           __stcg(rec + kRows * D + rt, m);
           __stcg(rec + kRows * (D + 1) + rt, l);
@@ -917,7 +917,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv_attention_merge_kernel(const
       for (int q = 0; q < n_rec; ++q, rec += S::kRecord) {
         const float m = __ldcg(rec + kRows * D + rt), lq = __ldcg(rec + kRows * (D + 1) + rt);
         const float4 y = __ldcg(reinterpret_cast<const float4*>(rec + (size_t)rt * D + d));
-        if (m == -INFINITY) continue;
+        if (no_keys(m, lq)) continue;
         const float mn = fmaxf(mx, m), back = ex2(mx - mn), w = ex2(m - mn);
         mx = mn;
         l = fmaf(lq, w, l * back);
@@ -925,11 +925,11 @@ __global__ void __launch_bounds__(kMergeThreads) kv_attention_merge_kernel(const
         x.z = fmaf(y.z, w, x.z * back), x.w = fmaf(y.w, w, x.w * back);
       }
       const int row = row0 + rt, tok = rq.first + row / a.group, head = kvh * a.group + row % a.group;
-      const float inv = l > 0.0f ? vg / l : 0.0f;
+      const float inv = l == 0.0f ? 0.0f : vg / l;
       const __nv_bfloat162 x0 = __floats2bfloat162_rn(x.x * inv, x.y * inv), x1 = __floats2bfloat162_rn(x.z * inv, x.w * inv);
       *reinterpret_cast<uint2*>(a.out + ((size_t)tok * a.heads + head) * D + d) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1));
-      if (a.lse && d == 0) a.lse[(size_t)tok * a.heads + head] = l > 0.0f ? (mx + log2f(l)) / kLog2e : -INFINITY;
+      if (a.lse && d == 0) a.lse[(size_t)tok * a.heads + head] = l == 0.0f ? -INFINITY : (mx + log2f(l)) / kLog2e;
     }
   }
 }
