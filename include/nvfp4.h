@@ -450,7 +450,8 @@ nvfp4_status nvfp4_kv_release(const int32_t* lens, const uint8_t* ended, int bat
  * as no token.  Entries of slots and positions past the last token are -1 and 0.
  *   batch >= 1; max_tokens >= 0: entries of slots and positions; tokens beyond are not written
  *   info  device, two int32: requests refused, tokens planned (cu_q[batch])
- *   free_count, free_count_out may be the same address; all other outputs are distinct
+ *   free_count_out may be free_count and kv_lens may be ctx_lens; outputs that overlap anything else are refused
+ *   (NVFP4_ERR_SHAPE)
  */
 nvfp4_status nvfp4_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int batch, int page_size,
                            int32_t* block_table, int table_width, const int32_t* free_pages, int free_capacity,

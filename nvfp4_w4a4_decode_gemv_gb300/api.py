@@ -426,7 +426,7 @@ def nvfp4_kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
                   out: KVPlan | None = None, stream=None) -> KVPlan:
     """Takes pages for new_lens[b] tokens behind ctx_lens[b] (block_table updated in place) and maps every new token
     to its slot.  Without `out`, the outputs are new tensors for max_tokens tokens and free_count is updated in
-    place; out.free_count may be free_count."""
+    place; out.free_count may be free_count, out.kv_lens may be ctx_lens."""
     i32 = torch.int32
     _need(block_table, i32, "block_table", 2)
     _need_all(i32, 1, "ctx_lens new_lens free_pages free_count", ctx_lens, new_lens, free_pages, free_count)

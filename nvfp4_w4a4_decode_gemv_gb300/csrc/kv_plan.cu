@@ -67,7 +67,7 @@ struct PlanArgs {
   const int32_t *stack, *count;
   int32_t *count_out, *kv_lens, *cu_q, *slots, *positions, *info;
   int batch, page, width, capacity, max_tokens;
-  int count_only;                        // write count_out and nothing else
+  int count_only;                        // write count_out and kv_lens (where they are not NULL) and nothing else
 };
 
 template <int THREADS>
@@ -105,9 +105,9 @@ __global__ void __launch_bounds__(THREADS) kv_plan_kernel(const PlanArgs a) {
     refused += __syncthreads_count(refuse && b < a.batch);
     const int tok_end = tok0 + tot.x;
     const int n = min(THREADS, a.batch - b0);
+    if (a.kv_lens && blockIdx.x == 0 && b < a.batch) a.kv_lens[b] = refuse ? c : c + q;
     if (!a.count_only) {
       if (blockIdx.x == 0 && b < a.batch) {
-        a.kv_lens[b] = refuse ? c : c + q;
         a.cu_q[b] = s_tok[tid];
         if (b == a.batch - 1) a.cu_q[a.batch] = tok_end;
       }
@@ -222,9 +222,9 @@ cudaError_t launch(void (*kern)(Args), int grid, int threads, const Args& a, cud
 
 // CTAs that may start after others have ended must not read a count that those
 // have written: with several CTAs and one address for both counts, the count
-// is written by a second launch of one CTA.
-template <class Args>
-cudaError_t launch_counted(void (*kern)(Args), int grid, int threads, Args a, cudaStream_t stream) {
+// is written by a second launch of one CTA.  So are the new lengths of a plan
+// that lie over the old ones.
+cudaError_t launch_counted(void (*kern)(ReleaseArgs), int grid, int threads, ReleaseArgs a, cudaStream_t stream) {
   const bool split = grid > 1 && a.count_out == a.count;
   int32_t* out = a.count_out;
   if (split) a.count_out = nullptr;
@@ -235,6 +235,26 @@ cudaError_t launch_counted(void (*kern)(Args), int grid, int threads, Args a, cu
     e = launch(kern, 1, threads, a, stream);
   }
   return e;
+}
+cudaError_t launch_counted(void (*kern)(PlanArgs), int grid, int threads, PlanArgs a, cudaStream_t stream) {
+  PlanArgs later = a;
+  later.count_only = 1;
+  if (grid == 1 || a.count_out != a.count) later.count_out = nullptr;
+  else a.count_out = nullptr;
+  if (grid == 1 || a.kv_lens != a.ctx) later.kv_lens = nullptr;
+  else a.kv_lens = nullptr;
+  cudaError_t e = launch(kern, grid, threads, a, stream);
+  if (e == cudaSuccess && (later.count_out || later.kv_lens)) e = launch(kern, 1, threads, later, stream);
+  return e;
+}
+
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return x < y + b.bytes && y < x + a.bytes;
 }
 
 bool page_ok(int page_size) { return page_size >= 16 && page_size <= 1024 && page_size % 16 == 0; }
@@ -282,6 +302,17 @@ extern "C" nvfp4_status nvfp4_kv_plan(const int32_t* ctx_lens, const int32_t* ne
                         (const void*)kv_lens, (const void*)cu_q, (const void*)slots, (const void*)positions,
                         (const void*)info})
     if (!nvfp4_internal_aligned(p, 4)) return NVFP4_ERR_ALIGN;
+  {
+    // what is written, then what is read only; kv_lens over ctx_lens and free_count_out over free_count are allowed
+    const size_t n = (size_t)batch * 4, t = (size_t)max_tokens * 4;
+    const Range r[] = {{kv_lens, n}, {free_count_out, 4}, {block_table, n * table_width}, {cu_q, n + 4}, {slots, t},
+                       {positions, t}, {info, 8}, {ctx_lens, n}, {free_count, 4}, {new_lens, n},
+                       {free_pages, (size_t)free_capacity * 4}};
+    for (int i = 0; i < 7; ++i)
+      for (int j = i + 1; j < 11; ++j)
+        if (r[i].bytes && r[j].bytes && overlap(r[i], r[j]) && !(j == i + 7 && i < 2 && r[i].p == r[j].p))
+          return NVFP4_ERR_SHAPE;
+  }
   const nvfp4_status ds = nvfp4_internal_check_device();
   if (ds != NVFP4_OK) return ds;
   const PlanArgs a = {ctx_lens, new_lens, block_table, free_pages, free_count, free_count_out, kv_lens, cu_q, slots,
