@@ -521,7 +521,8 @@ def nvfp4_kv_attention(q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.
     """softmax(scale q K^T) V of packed query rows q [tokens, heads, head_dim] over the cache, causal from the
     bottom right (BF16).  kv_lens [batch]: keys of each request, its new tokens among them; cu_q [batch + 1]: first
     row of each request, None: one row each; max_q: most rows of a request; scale: 1 / sqrt(head_dim) by default;
-    window: a row sees its last `window` keys only (0: all); lse [tokens, heads] FP32 receives log sum exp."""
+    window: a row sees its last `window` keys only (0: all); lse [tokens, heads] FP32 receives log sum exp; workspace:
+    uint8, its first ATTENTION_WS_ZEROED bytes zeroed once (the stream's own by default)."""
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, head_dim]")
     tokens, heads = q.shape[0], q.shape[1]
@@ -549,6 +550,8 @@ def nvfp4_kv_attention(q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.
     if workspace is None:
         workspace = _attention_workspace(
             nvfp4_kv_attention_workspace_bytes(batch, tokens, heads, cache.kv_heads, cache.head_dim), q.device, stream)
+    else:
+        _need(workspace, torch.uint8, "workspace")
     qs = q.stride()
     if max_q is None:
         max_q = 1 if cu_q is None else max(1, tokens)
