@@ -502,15 +502,17 @@ def _new_attention_workspace(need: int, device) -> torch.Tensor:
 
 
 def _attention_workspace(need: int, device, stream) -> torch.Tensor:
-    """A workspace of the stream's own (calls on different streams may overlap).  A captured call gets one of its
-    graph's memory, cleared by each replay."""
+    """A workspace of the stream's own (calls on different streams may overlap), cleared on that stream.  A captured
+    call gets one of its graph's memory, cleared by each replay."""
+    if stream is not None:
+        with torch.cuda.stream(stream):                  # its memory, its order, and whether it is being captured
+            return _attention_workspace(need, device, None)
     if torch.cuda.is_current_stream_capturing():
         return _new_attention_workspace(need, device)
-    key = (device, stream_handle(stream))
+    key = (device, stream_handle())
     ws = _attention_ws.get(key)
     if ws is None or ws.numel() < need:
-        with torch.cuda.stream(stream):                  # None: the current stream
-            ws = _attention_ws[key] = _new_attention_workspace(need, device)
+        ws = _attention_ws[key] = _new_attention_workspace(need, device)
     return ws
 
 

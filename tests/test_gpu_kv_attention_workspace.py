@@ -28,3 +28,53 @@ def test_a_callers_workspace_is_checked():
     with pytest.raises(RuntimeError, match="SHAPE"):
         api.nvfp4_kv_attention(*args, workspace=zeros(need - 1))
     assert torch.equal(want, api.nvfp4_kv_attention(*args, workspace=zeros(need)))
+
+
+def test_a_captured_call_on_a_side_stream_clears_its_workspace_there():
+    """The capturing stream is busy with other work and memory when the side stream's call starts."""
+    args = _call(np.random.default_rng(2), batch=3, n=6000)
+    want = api.nvfp4_kv_attention(*args)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    out = torch.empty_like(want)
+    x = torch.randn((4096, 4096), device="cuda")
+    y = torch.empty_like(x)
+    torch.mm(x, x, out=y)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        side.wait_stream(main)
+        for _ in range(3):
+            torch.mm(x, x, out=y)
+        api.nvfp4_kv_attention(*args, out=out, stream=side)
+        junk = [torch.full((20 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        main.wait_stream(side)
+        del junk
+    for _ in range(5):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert api.device_status() == 0
+
+
+def test_the_workspace_of_a_capturing_side_stream_is_the_graphs_own(monkeypatch):
+    """Host side alone: where the workspace of a call comes from, and on which stream it is cleared."""
+    seen = []
+    real = api._new_attention_workspace
+
+    def spy(need, device):
+        seen.append((torch.cuda.current_stream().cuda_stream, torch.cuda.is_current_stream_capturing()))
+        return real(need, device)
+    monkeypatch.setattr(api, "_new_attention_workspace", spy)
+    args = _call(np.random.default_rng(3))
+    out = torch.empty_like(args[0])
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    api.nvfp4_kv_attention(*args, out=out, stream=side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        side.wait_stream(main)
+        api.nvfp4_kv_attention(*args, out=out, stream=side)
+        main.wait_stream(side)
+    assert seen == [(side.cuda_stream, False), (side.cuda_stream, True)]
