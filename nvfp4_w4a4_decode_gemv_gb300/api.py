@@ -353,6 +353,18 @@ def _need_all(dtype, dim, names, *ts):
             _need(t, dtype, names.split()[i], dim)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output of a call on `stream` (None: the current one): that stream's memory, so that nothing else is at work
+    in it, given back when the current stream, on which the caller holds it, has come so far, too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 def nvfp4_kv_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
     return int(lib().nvfp4_kv_page_bytes(page_size, kv_heads, head_dim))
 
@@ -396,8 +408,8 @@ class KVPlan:
         self.kv_lens, self.free_count, self.info = kv_lens, free_count, info
 
     @classmethod
-    def empty(cls, batch: int, max_tokens: int, device="cuda", free_count: torch.Tensor | None = None):
-        i32 = lambda n: torch.empty(n, dtype=torch.int32, device=device)
+    def empty(cls, batch: int, max_tokens: int, device="cuda", free_count: torch.Tensor | None = None, stream=None):
+        i32 = lambda n: _empty(n, torch.int32, device, stream)
         return cls(i32(max_tokens), i32(max_tokens), i32(batch + 1), i32(batch),
                    i32(1) if free_count is None else free_count, i32(2))
 
@@ -434,7 +446,7 @@ def nvfp4_kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     if out is None:
         if max_tokens is None:
             raise ValueError("max_tokens is needed to allocate the outputs")
-        out = KVPlan.empty(batch, max_tokens, ctx_lens.device, free_count)
+        out = KVPlan.empty(batch, max_tokens, ctx_lens.device, free_count, stream)
     _need_all(i32, 1, "slots positions cu_q kv_lens free_count info", out.slots, out.positions, out.cu_q, out.kv_lens,
               out.free_count, out.info)
     if (ctx_lens.numel() != batch or new_lens.numel() != batch or out.kv_lens.numel() != batch
@@ -477,8 +489,8 @@ def nvfp4_kv_read(cache: NVFP4KVCache, slots: torch.Tensor, k_out: torch.Tensor 
     """The cached rows of the slots as BF16 [tokens, kv_heads, head_dim] (k, v); zeros where a slot is -1."""
     _need(slots, torch.int32, "slots", 1)
     shape = (slots.numel(), cache.kv_heads, cache.head_dim)
-    k_out = k_out if k_out is not None else torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
-    v_out = v_out if v_out is not None else torch.empty(shape, dtype=torch.bfloat16, device=slots.device)
+    k_out = k_out if k_out is not None else _empty(shape, torch.bfloat16, slots.device, stream)
+    v_out = v_out if v_out is not None else _empty(shape, torch.bfloat16, slots.device, stream)
     for t, n in ((k_out, "k_out"), (v_out, "v_out")):
         _need(t, torch.bfloat16, n)
         if t.shape != shape:
@@ -540,7 +552,7 @@ def nvfp4_kv_attention(q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.
             raise ValueError("cu_q needs batch + 1 entries")
     shape = (tokens, heads, cache.head_dim)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = _empty(shape, torch.bfloat16, q.device, stream)
     else:
         _need(out, torch.bfloat16, "out")
         if out.shape != shape:
@@ -596,7 +608,7 @@ def nvfp4_process_logits(logits: torch.Tensor, tokens: torch.Tensor | None = Non
         if mask.shape[1] != (V + 31) // 32 or (mask_rows is None and mask.shape[0] < rows):
             raise ValueError("mask needs ceil(V / 32) words a row, and a row for each row of logits without mask_rows")
     if out is None:
-        out = torch.empty((rows, V), dtype=torch.float32, device=logits.device)
+        out = _empty((rows, V), torch.float32, logits.device, stream)
     else:
         _need(out, torch.float32, "out", 2)
         if out.shape != logits.shape:
