@@ -467,7 +467,7 @@ nvfp4_status nvfp4_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int
  * A slot of -1 skips its row (padding); a slot outside the cache skips it and
  * records device error bit 3.  No two rows of a call may have the same slot
  * (their bytes would mix).
- *   k, v     device, 16-byte aligned, strides multiples of 16 bytes
+ *   k, v     device, 16-byte aligned, strides multiples of 16 bytes (any where there is one token, or one head)
  *   dtype    NVFP4_DTYPE_*;  tokens >= 0
  */
 nvfp4_status nvfp4_kv_append(const void* k, const void* v, int dtype, int tokens, int64_t k_token_stride,
@@ -496,7 +496,7 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int32_t* slots, in
  * values are exact; scores, their maxima and sums and the accumulators are FP32;
  * FP32 queries are first rounded to BF16 (RNE).
  *   q            device, [tokens, heads, head_dim] at q + r * q_token_stride + h * q_head_stride
- *                (elements; 16-byte aligned, strides multiples of 16 bytes)
+ *                (elements; 16-byte aligned, strides multiples of 16 bytes, as of k and v above)
  *   heads        a multiple of kv_heads, at most 64 times it
  *   block_table  device, [batch, table_width] int32: page of tokens j * page_size ..
  *                Only entries of pages that some row sees are read; a page outside the cache is

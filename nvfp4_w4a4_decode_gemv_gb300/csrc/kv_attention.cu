@@ -804,7 +804,7 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens,
   if (tokens == 0 || batch == 0) return NVFP4_OK;
   if (!q || !block_table || !kv_lens || !out || !workspace) return NVFP4_ERR_NULL;
   const int per = dtype == NVFP4_DTYPE_F32 ? 4 : 8;
-  if (q_token_stride % per || q_head_stride % per) return NVFP4_ERR_ALIGN;
+  if ((tokens > 1 && q_token_stride % per) || (heads > 1 && q_head_stride % per)) return NVFP4_ERR_ALIGN;
   if (!nvfp4_internal_aligned(q, 16) || !nvfp4_internal_aligned(out, 16) || !nvfp4_internal_aligned(workspace, 256))
     return NVFP4_ERR_ALIGN;
   for (const void* p : {(const void*)block_table, (const void*)kv_lens, (const void*)cu_q, (const void*)lse})

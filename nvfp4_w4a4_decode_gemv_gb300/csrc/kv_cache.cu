@@ -409,8 +409,9 @@ extern "C" nvfp4_status nvfp4_kv_append(const void* k, const void* v, int dtype,
   if (tokens == 0) return NVFP4_OK;
   if (!k || !v || !slots) return NVFP4_ERR_NULL;
   const int per = dtype == NVFP4_DTYPE_F32 ? 4 : 8;          // elements of 16 bytes
-  if (k_token_stride % per || k_head_stride % per || v_token_stride % per || v_head_stride % per)
-    return NVFP4_ERR_ALIGN;
+  // (the stride of a single token or head is used in no address)
+  if (tokens > 1 && (k_token_stride % per || v_token_stride % per)) return NVFP4_ERR_ALIGN;
+  if (cache->kv_heads > 1 && (k_head_stride % per || v_head_stride % per)) return NVFP4_ERR_ALIGN;
   if (!nvfp4_internal_aligned(k, 16) || !nvfp4_internal_aligned(v, 16) || !nvfp4_internal_aligned(slots, 4))
     return NVFP4_ERR_ALIGN;
   const nvfp4_status ds = nvfp4_internal_check_device();
