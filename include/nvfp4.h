@@ -501,7 +501,8 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int32_t* slots, in
  *   block_table  device, [batch, table_width] int32: page of tokens j * page_size ..
  *                Only entries of pages that some row sees are read; a page outside the cache is
  *                skipped (its keys count as unseen) and records device error bit 3, and so does a
- *                kv_lens beyond table_width * page_size (cut there) or a row range outside [0, tokens).
+ *                kv_lens beyond table_width * page_size (cut there) or a row range outside [0, tokens).  Where
+ *                cu_q falls and ranges overlap, the call may compute nothing.
  *   kv_lens      device, [batch] int32
  *   cu_q         device, [batch + 1] int32, or NULL: one row a request (tokens == batch)
  *   max_q        >= 1: most rows of a request, as far as the caller knows (it chooses the kernel,

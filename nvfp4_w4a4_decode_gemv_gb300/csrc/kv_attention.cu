@@ -267,8 +267,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
     // units of the two sizes, each segment's padded to one for every warp
     int units4 = 0, units4_half = 0, n_segs = 0, longest = 0;
     Request own = {};                                   // the thread's request, where it has one only
+    bool bad = false;
     for (int i = b0; i < b1; ++i) {
       own = get_request(a, i, blockIdx.x == 0);
+      bad = bad || own.bad;
       const int segs = request_tiles<S>(a, own) * a.kv_heads, n = segment_units(own, S::kUnitLog - 1);
       units4 += segs * ((segment_units(own, S::kUnitLog) + kWarps - 1) / kWarps);
       units4_half += segs * ((n + kWarps - 1) / kWarps);
@@ -286,11 +288,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv_attention_kernel
         s_scan[8 + warp] = n_segs;
         s_scan[20 + warp] = units4_half;
       }
-      __syncthreads();
+      bad = __syncthreads_or(bad);
       units4 = s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
       longest = max(max(s_scan[4], s_scan[5]), max(s_scan[6], s_scan[7]));
       n_segs = s_scan[8] + s_scan[9] + s_scan[10] + s_scan[11];
       units4_half = s_scan[20] + s_scan[21] + s_scan[22] + s_scan[23];
+    }
+    // Ranges that never fall add up to no more than the rows there are, and the host's bound on the units holds.
+    // Where one falls, the others may overlap: the call is given up if they do.
+    if (small ? __any_sync(0xffffffffu, bad) : bad) {
+      float rows = 0.0f;
+      for (int i = b0; i < b1; ++i) rows += (float)get_request(a, i, false).rows;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, o);
+      if (!small) {
+        if (lane == 0) s_scan[24 + warp] = __float_as_int(rows);
+        __syncthreads();
+        rows = __int_as_float(s_scan[24]) + __int_as_float(s_scan[25]) + __int_as_float(s_scan[26]) + __int_as_float(s_scan[27]);
+      }
+      if (rows > 1.001f * (float)a.tokens) return;
     }
     if (units4 == 0) return;
     // less than kShortUnits rounds for a warp: halves of units divide more evenly, and their latency is shorter
@@ -822,13 +838,13 @@ extern "C" nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens,
                       room_for_pieces(tokens, group) ? kTcPieces : 0, scale};
   const int rows = cu_q ? (int)((long long)max_q * group < 1 << 20 ? max_q * group : 1 << 20) : group;
   // the decode kernel counts its units (32 keys of a row tile, with their overhead) in 31 bits; this is the most there
-  // can be, whatever cu_q and kv_lens hold
+  // can be, whatever kv_lens hold, with row ranges that do not overlap (the kernel looks)
   const long long keys = (long long)batch * cache->kv_heads * table_width * cache->page_size;
   const long long most_units = ((long long)tokens * group / 8 + batch) * cache->kv_heads *
                                ((long long)table_width * cache->page_size / 32 + 2 + kSegmentCost / 32 + kWarps);
   cudaError_t e;
   const long long segment_keys = (long long)batch * cache->kv_heads * kSegmentCost;
-  if ((rows > kTcRows && rows * (keys + segment_keys) > kTcProducts) || most_units > 0x7FFFFFFFll)
+  if ((rows > kTcRows && rows * (keys + segment_keys) > kTcProducts) || most_units > 0x7F000000ll)
     e = nvfp4_internal_kv_attention_tc(a, cache->head_dim, dtype, stream);
   else if (cache->head_dim == 128)
     e = dtype == NVFP4_DTYPE_F32 ? dispatch<128, float>(a, rows, keys, stream) : dispatch<128, uint16_t>(a, rows, keys, stream);

@@ -78,18 +78,21 @@ NVFP4_DEVINL void load4(const uint16_t* p, float (&v)[4]) {
 struct Request {
   int first, rows, len;                 // query rows [first, first + rows), keys [0, len)
   int begin;                            // first key that any row sees
+  bool bad;                             // its row range is none
 };
 
 NVFP4_DEVINL Request get_request(const AttnArgs& a, int b, bool report) {
   Request r;
   r.first = b;
   r.rows = 1;
+  r.bad = false;
   bool bad = false;
   if (a.cu_q) {
     r.first = a.cu_q[b];
     const int last = a.cu_q[b + 1];
     bad = r.first < 0 || last < r.first || last > a.tokens;
     r.rows = bad ? 0 : last - r.first;
+    r.bad = bad;
   }
   r.len = max(a.kv_lens[b], 0);
   const long long most = (long long)a.width * a.page_size;
