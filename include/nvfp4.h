@@ -491,10 +491,14 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int32_t* slots, in
  * kv head h / (heads / kv_heads):
  *   out[r, h, :] = sum_j softmax_j(scale * q[r, h] . K[j]) V[j]      (BF16)
  *   lse[r, h]    = log sum_j exp(scale * q[r, h] . K[j])             (FP32, natural log)
- * A row that sees no key gives out = 0, lse = -inf; so does one all of whose scores are -inf.  A row with a NaN score,
- * or one of +inf, gives NaN.  The keys' dequantized
- * values are exact; scores, their maxima and sums and the accumulators are FP32;
- * FP32 queries are first rounded to BF16 (RNE).
+ * A row that sees no key gives out = 0, lse = -inf; so does one all of whose scores are -inf.  A row with a NaN
+ * score, or one of +inf, gives NaN.
+ * Precision: the keys' and values' dequantized values are exact.  FP32 queries are first rounded to BF16 (RNE); a
+ * query enters the products as FP16 of q / 2^e, 2^e the power of two at its row's maximum (exact down to 2^-14 of
+ * it).  Scores, their maxima, the sums and the accumulators are FP32.  The weights that multiply V are rounded to
+ * FP16 (2^-11 of each, and those under 2^-25 of the maximum in use become 0), the weights that are summed are not.
+ * The kernel for many rows moves its maximum only when a score exceeds it by a factor of 2^13, so its largest weight
+ * need not be 1.  The result is rounded to BF16.
  *   q            device, [tokens, heads, head_dim] at q + r * q_token_stride + h * q_head_stride
  *                (elements; 16-byte aligned, strides multiples of 16 bytes, as of k and v above)
  *   heads        a multiple of kv_heads, at most 64 times it
@@ -547,7 +551,8 @@ nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens, int64_t q_
  *   mask      device, bit v % 32 of word v / 32 set: v is allowed; [mask_count, ceil(V/32)] uint32, or NULL
  *   mask_rows device, [rows] int32: the mask row of each row, -1 (or any outside [0, mask_count)): none;
  *             NULL: row r has mask row r (mask_count >= rows)
- *   fill      what forbidden logits become, e.g. -inf (a row whose mask allows nothing is all fill)
+ *   fill      what forbidden logits become, e.g. -inf (a row whose mask allows nothing is all fill; reset_sample gives
+ *             no token for a row of -inf)
  *   out       device, [rows, V] FP32, 16-byte aligned when V % 4 == 0 is to be fast (written); for FP32 logits with
  *             ld == V it may be the logits themselves
  */

@@ -18,7 +18,9 @@
 //    16-byte pieces without bank conflicts.
 // Queries enter as FP16 of q / 2^e, 2^e the power of two at the row's maximum:
 // exact for BF16 queries down to 2^-14 of it.  Weights are rounded to FP16 for
-// the product with V (2^-11 of each); their sum is FP32.
+// the product with V (2^-11 of each, 0 below 2^-25 of the maximum); their sum is of
+// the FP32 weights, so up to n 2^-25 of it may have no part in the product: less than
+// what n additions in FP32 may lose.
 //
 // Work split: units of 64 or 32 tokens (D = 64: 128 or 64) of one (request, kv head, row tile),
 // Stream-K over all of them, so that any mix of lengths fills the GPU; the split

@@ -67,8 +67,9 @@ struct Raw {
 // The quotient is the correctly rounded one by Markstein's theorem (P. Markstein, "Computation of elementary functions
 // on the IBM RISC System/6000 processor", 1990): with y = RN(1/S) and p = RN(x y), RN(p + y RN(x - p S)) = RN(x / S)
 // while nothing underflows or overflows; NaN passes through bm and t into the branch, which costs no look of its own
-// then (a cut of every quotient: 23.4 us for 16384 tokens of 8 heads instead of 21.1).  quant_block divides where x y is too close to a decision point to tell; with a global scale
-// that is a power of two BF16 values meet those points exactly, in some lane of nearly every warp.
+// then (a cut of every quotient: 23.4 us for 16384 tokens of 8 heads instead of 21.1).  quant_block divides where x y
+// is too close to a decision point to tell; with a global scale that is a power of two BF16 values meet those points
+// exactly, in some lane of nearly every warp.
 NVFP4_DEVINL uint32_t kv_quant_block(float (&v)[16], float g, uint2& codes) {
   float bm = 0.0f;
 #pragma unroll

@@ -120,7 +120,8 @@ class ServingStep(DecodeStep):
         """One decode step of every request: h_in, u, step_start -> sampler.token; lengths and histories move on, but
         not those of a request for whose token there is no page, or whose history is full (max_len tokens).  Such rows,
         and those without a request, are zero throughout: they change no result of the others (whose activations they
-        share a scale with), no state and no output."""
+        share a scale with), no state and no output.  A row whose rules leave no token gets -1, which its history
+        holds but does not count (device error bit 4)."""
         with torch.cuda.stream(stream):
             # a row with a request and room in its history gets a token
             torch.mul(self.active, self.n_tokens < self.max_len, out=self.wanted)
