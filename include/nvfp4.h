@@ -73,7 +73,10 @@ int nvfp4_version(void);
  *              the wait gave up: zero the workspace again before its next use;
  *   bit 3 (8)  a KV cache kernel met a slot or a page outside the cache, or a
  *              length or row range outside its table, and skipped it;
- *   bit 4 (16) reset_sample met a row that it can sample no token of.
+ *   bit 4 (16) reset_sample met a row that it can sample no token of;
+ *   bit 5 (32) nvfp4_moe_route met a token whose logits give no choice;
+ *   bit 6 (64) an expert kernel met an expert, offset, pair or place outside
+ *              its tables and skipped it.
  * Synchronous (it copies a few bytes from the device); not for use inside
  * stream capture.
  */
@@ -524,6 +527,119 @@ nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens, int64_t q_
                                 const int32_t* kv_lens, const int32_t* cu_q, int batch, int max_q, float scale,
                                 int window, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
                                 cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Experts: routing, and the chosen experts' NVFP4 products                    */
+/* ------------------------------------------------------------------------ */
+/*
+ * A layer with experts sends each token to top_k of them.  A PAIR is a token t
+ * and its j-th expert, number t * top_k + j.  A PLAN of the pairs is
+ *   offsets  [experts + 1]        the pairs of expert e stand at places
+ *                                 offsets[e] .. offsets[e+1];
+ *   pairs    [tokens * top_k]     the pair at each place, those of an expert
+ *                                 in the order of their numbers; -1 behind
+ *                                 offsets[experts];
+ *   places   [tokens * top_k]     the place of each pair, -1: it has none.
+ * The ReSET pages describe dense layers only; this part has no counterpart
+ * there.  experts 1 .. 512, top_k 1 .. 32, tokens * top_k < 2^31.
+ */
+enum { NVFP4_MOE_SOFTMAX = 0, NVFP4_MOE_SIGMOID = 1 };
+
+typedef struct nvfp4_moe_router {
+  int top_k;        /* experts of a token, 1 .. 32                                            */
+  int score;        /* NVFP4_MOE_*: softmax over all experts, or a sigmoid of each            */
+  int groups;       /* experts e / (experts / groups) form a group; 1 .. 32, divides experts  */
+  int top_groups;   /* groups a token may choose from, 1 .. groups                            */
+  int group_best;   /* 1 or 2: a group's rank is by the sum of its so many largest values     */
+  int renormalize;  /* non-zero: the weights of a token's experts are divided by their sum    */
+  float scale;      /* and multiplied by this, finite                                         */
+} nvfp4_moe_router;
+
+/* Scratch of nvfp4_moe_route and nvfp4_moe_plan; 0 for calls that need none.  No state: nothing is kept in it. */
+size_t nvfp4_moe_route_workspace_bytes(int tokens, int experts);
+
+/*
+ * Scores, choice, weights and plan from router logits x[t, e]:
+ *   s[t, e] = softmax_e(x[t, :]) or 1 / (1 + exp(-x[t, e]))
+ *   v[t, e] = s[t, e] + bias[e]          (what the choice goes by; without a bias the order of x)
+ *   with top_groups < groups: the top_groups groups with the largest sums of their group_best largest v stay
+ *   ids[t, :]     = the top_k experts with the largest v, in that order
+ *   weights[t, j] = s[t, ids[t, j]], divided by the row's sum if renormalize, times scale          (FP32)
+ * Equal values go to the lowest expert (or group).  Values are told apart as 64-bit arithmetic tells them: where FP32
+ * cannot settle the order, the token is chosen again in FP64.  Renormalized weights do not underflow with their sum.
+ * A token with a NaN among its logits (or biases), and with softmax one with a logit of +inf or with -inf alone, gives
+ * no choice: ids -1, weights 0, no pair; device error bit 5 is recorded.  Logits of -inf are experts of score 0.
+ *   logits   device, [tokens, experts] of dtype NVFP4_DTYPE_*, row t at logits + t * ld (elements)
+ *   bias     device, [experts] FP32, or NULL
+ *   rows     device, [tokens] uint8, or NULL: tokens with rows[t] == 0 are not read and get ids -1, weights 0, no pair
+ *   ids, weights   device, [tokens, top_k] int32 / FP32 (written)
+ *   offsets, pairs, places   the plan (written)
+ *   workspace      device scratch, 4-byte aligned; may be NULL where the size is 0
+ */
+nvfp4_status nvfp4_moe_route(const void* logits, int dtype, int tokens, int experts, int64_t ld,
+                             const nvfp4_moe_router* router, const float* bias, const uint8_t* rows, int32_t* ids,
+                             float* weights, int32_t* offsets, int32_t* pairs, int32_t* places, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The plan of a choice made elsewhere: ids [tokens, top_k] int32, -1 for no expert; ids outside [0, experts) are no
+ * pair either and record device error bit 6.  An expert may stand twice in a row.
+ */
+nvfp4_status nvfp4_moe_plan(const int32_t* ids, int tokens, int top_k, int experts, int32_t* offsets, int32_t* pairs,
+                            int32_t* places, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Packed expert weights.  nvfp4_moe_pack_weights rewrites the row-major NVFP4 matrices of all experts, wq
+ * [experts, N, K/2] and ws [experts, N, K/16], into blocks of 18432 bytes, one per (expert, tile of 128 rows, 256 of K),
+ * in this order, K fastest:
+ *   bytes [0, 16384)      the 16-byte piece j (0..7) of the codes of tile row r at r*128 + ((j XOR (r mod 8)) * 16)
+ *   bytes [16384, 18432)  scales of 16-element blocks 4q .. 4q+3 (q 0..3) of tile row r at
+ *                         16384 + q*512 + (r mod 32)*16 + (r/32)*4
+ * With gated != 0 the matrix is gate and up, N = 2 I, gate rows [0, I), up rows [I, 2I), I a multiple of 64, and their
+ * rows alternate in the tiles: row 2i is gate row i, row 2i+1 up row i.  Rows beyond N and elements beyond K are zero.
+ *   nvfp4_moe_packed_weight_bytes = experts * ceil(N/128) * ceil(K/256) * 18432, or 0 for an invalid shape:
+ *   experts 1 .. 512, N 1 .. 2^20, K a multiple of 64, 64 .. 2^20
+ *   wq, packed 16-byte aligned, ws 4-byte aligned; packed must not overlap wq or ws
+ */
+size_t nvfp4_moe_packed_weight_bytes(int experts, int N, int K, int gated);
+
+nvfp4_status nvfp4_moe_pack_weights(const uint8_t* wq, const uint8_t* ws, int experts, int N, int K, int gated,
+                                    uint8_t* packed, size_t packed_bytes, cudaStream_t stream);
+
+/*
+ * Gate and up products of the chosen experts, and SiLU(gate) * up, in one pass over their weights: with pair p at place q
+ * (p = pairs[q]), token t = p / top_k and expert e (offsets[e] <= q < offsets[e+1]),
+ *   g = xg wg[e] sum_k x[t, k] w[e, i, k],  u = the same with w[e, inter + i, k]       (FP32)
+ *   h[q, i] = BF16(g / (1 + exp(-g)) * u)
+ * Rows of h behind offsets[experts] are zero, so that nvfp4_quantize_act may take all of h.
+ *   xq, xs, xg   activations in NVFP4 layout, [tokens, K/2] 16-byte, [tokens, K/16] 4-byte aligned, one float
+ *   wpacked, wg  packed with gated != 0 (N = 2 inter), 16-byte aligned; [experts] FP32 global scales
+ *   inter        a multiple of 64;  K a multiple of 64
+ *   h            device, [tokens * top_k, inter] BF16, 16-byte aligned (written)
+ * Only the weights of experts that have pairs are read.  Sums of a product are FP32 in an order that the shape and the
+ * plan fix: the same inputs give the same bits.  Offsets, pairs and places outside their tables are taken into them or
+ * skipped and record device error bit 6 (the rows concerned mean nothing).
+ */
+nvfp4_status nvfp4_moe_gate_up(const uint8_t* xq, const uint8_t* xs, const float* xg, int tokens, int top_k,
+                               const int32_t* offsets, const int32_t* pairs, const uint8_t* wpacked, const float* wg,
+                               int experts, int inter, int K, uint16_t* h, cudaStream_t stream);
+
+/*
+ * Down products of the chosen experts, summed over a token's experts:
+ *   y[t, n] = sum_j weights[t, j] hg wg[e] sum_k h[place(t, j), k] w[e, n, k]          (FP32)
+ * over the pairs of t that have a place (none: 0).  No product is rounded on the way.
+ *   hq, hs, hg   NVFP4 rows by place, [tokens * top_k, K/2] 16-byte, [.., K/16] 4-byte aligned, one float
+ *   wpacked, wg  packed with gated == 0 ([experts, N, K]), [experts] FP32
+ *   weights      device, [tokens, top_k] FP32;  places: the plan's
+ *   y            device, [tokens, N] FP32, 16-byte aligned (written)
+ *   workspace    device scratch of nvfp4_moe_down_workspace_bytes bytes (0 up to 64 tokens), 16-byte aligned; no state
+ */
+size_t nvfp4_moe_down_workspace_bytes(int tokens, int top_k, int N);
+
+nvfp4_status nvfp4_moe_down(const uint8_t* hq, const uint8_t* hs, const float* hg, int tokens, int top_k,
+                            const int32_t* offsets, const int32_t* pairs, const int32_t* places, const float* weights,
+                            const uint8_t* wpacked, const float* wg, int experts, int N, int K, float* y, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Rules on the logits                                                        */

@@ -42,6 +42,15 @@ class KVCacheDesc(ctypes.Structure):
                 ("head_dim", ctypes.c_int)]
 
 
+class MoERouter(ctypes.Structure):
+    """nvfp4_moe_router."""
+    _fields_ = [("top_k", ctypes.c_int), ("score", ctypes.c_int), ("groups", ctypes.c_int), ("top_groups", ctypes.c_int),
+                ("group_best", ctypes.c_int), ("renormalize", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+# NVFP4_MOE_* of nvfp4.h
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+
 # NVFP4_DTYPE_* of nvfp4.h
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
@@ -85,6 +94,16 @@ SIGNATURES = {
                                   _c_f, _c_i, _c_p, _c_p, _c_p, _c_sz, _c_p]),
     "nvfp4_process_logits": (_c_i, [_c_p, _c_i, _c_i, _c_i, _c_i64, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
                                     _c_p, _c_i, _c_p, _c_i, _c_p, _c_f, _c_p, _c_p]),
+    "nvfp4_moe_route_workspace_bytes": (_c_sz, [_c_i, _c_i]),
+    "nvfp4_moe_route": (_c_i, [_c_p, _c_i, _c_i, _c_i, _c_i64, ctypes.POINTER(MoERouter), _c_p, _c_p, _c_p, _c_p, _c_p,
+                               _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "nvfp4_moe_plan": (_c_i, [_c_p, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "nvfp4_moe_packed_weight_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i]),
+    "nvfp4_moe_pack_weights": (_c_i, [_c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p, _c_sz, _c_p]),
+    "nvfp4_moe_gate_up": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_p, _c_p]),
+    "nvfp4_moe_down_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i]),
+    "nvfp4_moe_down": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_p,
+                              _c_p, _c_sz, _c_p]),
     "reset_state_bytes": (_c_sz, [_c_i, _c_i]),
     "reset_state_init": (_c_i, [_c_p, _c_i, _c_i, _c_p]),
     "reset_state_init_rows": (_c_i, [_c_p, _c_i, _c_i, _c_p, _c_p]),

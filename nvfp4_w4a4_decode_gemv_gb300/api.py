@@ -8,8 +8,8 @@ import weakref
 
 import torch
 
-from ._lib import (DTYPES, THRESHOLD_FIXED, THRESHOLD_RESET, THRESHOLD_WINDOW, KVCacheDesc, ResetParams, check, lib,
-                   ptr, stream_handle)
+from ._lib import (DTYPES, MOE_SCORES, THRESHOLD_FIXED, THRESHOLD_RESET, THRESHOLD_WINDOW, KVCacheDesc, MoERouter,
+                   ResetParams, check, lib, ptr, stream_handle)
 
 __all__ = [
     "nvfp4_quantize_act", "nvfp4_quantize_f32", "nvfp4_silu_mul_quantize", "nvfp4_gemv_smallm",
@@ -24,6 +24,8 @@ __all__ = [
     "NVFP4KVCache", "KVPlan", "nvfp4_kv_page_bytes", "nvfp4_kv_release", "nvfp4_kv_plan", "nvfp4_kv_append",
     "nvfp4_kv_read", "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_bytes", "nvfp4_process_logits",
     "DEVERR_KV_RANGE", "DEVERR_NO_TOKEN",
+    "MoERouting", "NVFP4MoEWeight", "nvfp4_moe_route", "nvfp4_moe_plan", "nvfp4_moe_packed_weight_bytes",
+    "nvfp4_moe_pack_weights", "nvfp4_moe_gate_up", "nvfp4_moe_down", "DEVERR_NO_EXPERT", "DEVERR_MOE_RANGE",
 ]
 
 
@@ -575,6 +577,192 @@ def nvfp4_kv_attention(q: torch.Tensor, cache: NVFP4KVCache, block_table: torch.
                                    ptr(lse), workspace.data_ptr(), workspace.numel(), stream_handle(stream)),
           "nvfp4_kv_attention")
     return out
+
+
+# Device error bit of a token whose router logits give no choice (a NaN; with softmax +inf, or -inf alone): its ids are -1.
+DEVERR_NO_EXPERT = 32
+# Device error bit of an expert kernel that met an expert, offset, pair or place outside its tables and skipped it.
+DEVERR_MOE_RANGE = 64
+
+
+class MoERouting:
+    """Which experts take which tokens, on the device: ids int32 and weights float32 [tokens, top_k] (weights may be
+    None), and the plan of the pairs (token t's j-th expert is pair t top_k + j): offsets int32 [experts + 1] (where an
+    expert's pairs begin), pairs int32 [tokens * top_k] (the pair at each place, -1 behind the last) and places int32
+    [tokens, top_k] (where each pair stands, -1: nowhere)."""
+
+    __slots__ = ("ids", "weights", "offsets", "pairs", "places", "tokens", "top_k", "experts")
+
+    def __init__(self, ids, weights, offsets, pairs, places):
+        i32 = torch.int32
+        _need_all(i32, 2, "ids places", ids, places)
+        _need_all(i32, 1, "offsets pairs", offsets, pairs)
+        _need_all(torch.float32, 2, "weights", weights)
+        if (places.shape != ids.shape or pairs.numel() != ids.numel() or offsets.numel() < 2
+                or (weights is not None and weights.shape != ids.shape)):
+            raise ValueError("weights and places have the shape of ids [tokens, top_k], pairs its entries, offsets an "
+                             "entry an expert and one more")
+        self.ids, self.weights, self.offsets, self.pairs, self.places = ids, weights, offsets, pairs, places
+        (self.tokens, self.top_k), self.experts = ids.shape, offsets.numel() - 1
+
+    @classmethod
+    def empty(cls, tokens: int, top_k: int, experts: int, device="cuda", stream=None):
+        i32 = torch.int32
+        return cls(_empty((tokens, top_k), i32, device, stream), _empty((tokens, top_k), torch.float32, device, stream),
+                   _empty(experts + 1, i32, device, stream), _empty(tokens * top_k, i32, device, stream),
+                   _empty((tokens, top_k), i32, device, stream))
+
+
+def _scratch(need: int, device, stream) -> torch.Tensor | None:
+    """Workspace of a call that keeps no state: memory of its stream, or none."""
+    return _empty(need, torch.uint8, device, stream) if need else None
+
+
+def nvfp4_moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None,
+                    groups: int = 1, top_groups: int = 1, group_best: int = 1, renormalize: bool = True,
+                    scale: float = 1.0, rows: torch.Tensor | None = None, out: MoERouting | None = None,
+                    stream=None) -> MoERouting:
+    """Router logits [tokens, experts] (float32 or bfloat16, adjacent elements in a row) -> the top_k experts of each
+    token, their weights and the plan by expert.  score: "softmax" or "sigmoid"; bias [experts] float32: added to the
+    scores for the choice alone; groups: only the top_groups groups of experts with the largest sums of their group_best
+    (1 or 2) best values stay; renormalize: a token's weights sum to `scale`, else they are its scores times `scale`; rows
+    (uint8 or bool [tokens]): tokens with 0 get no expert (ids -1)."""
+    code = DTYPES.get(logits.dtype)
+    if code is None or not logits.is_cuda or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a CUDA tensor [tokens, experts] of float32 or bfloat16 with adjacent elements")
+    tokens, experts = logits.shape
+    if score not in MOE_SCORES:
+        raise ValueError(f"score must be one of {sorted(MOE_SCORES)}")
+    if bias is not None:
+        _need(bias, torch.float32, "bias", 1)
+        if bias.numel() != experts:
+            raise ValueError("bias needs one entry an expert")
+    if rows is not None:
+        _need_row_mask(rows, tokens)
+    if out is None:
+        if experts < 1 or top_k < 1:
+            raise ValueError("experts and top_k must be positive")
+        out = MoERouting.empty(tokens, top_k, experts, logits.device, stream)
+    elif out.tokens != tokens or out.top_k != top_k or out.experts != experts or out.weights is None:
+        raise ValueError("out does not fit the tokens, experts and top_k")
+    router = MoERouter(top_k, MOE_SCORES[score], groups, top_groups, group_best, renormalize, scale)
+    ws = _scratch(int(lib().nvfp4_moe_route_workspace_bytes(tokens, experts)), logits.device, stream)
+    check(lib().nvfp4_moe_route(logits.data_ptr(), code, tokens, experts, logits.stride(0) if tokens > 1 else experts,
+                                ctypes.byref(router), ptr(bias), ptr(rows), out.ids.data_ptr(), out.weights.data_ptr(),
+                                out.offsets.data_ptr(), out.pairs.data_ptr(), out.places.data_ptr(), ptr(ws),
+                                ws.numel() if ws is not None else 0, stream_handle(stream)), "nvfp4_moe_route")
+    return out
+
+
+def nvfp4_moe_plan(ids: torch.Tensor, experts: int, weights: torch.Tensor | None = None, stream=None) -> MoERouting:
+    """The plan of a choice made elsewhere: ids int32 [tokens, top_k] (-1: no expert), with its weights."""
+    _need(ids, torch.int32, "ids", 2)
+    if experts < 1:
+        raise ValueError("experts must be positive")
+    i32, dev = torch.int32, ids.device
+    out = MoERouting(ids, weights, _empty(experts + 1, i32, dev, stream), _empty(ids.numel(), i32, dev, stream),
+                     _empty(tuple(ids.shape), i32, dev, stream))
+    ws = _scratch(int(lib().nvfp4_moe_route_workspace_bytes(out.tokens, experts)), dev, stream)
+    check(lib().nvfp4_moe_plan(ids.data_ptr(), out.tokens, out.top_k, experts, out.offsets.data_ptr(),
+                               out.pairs.data_ptr(), out.places.data_ptr(), ptr(ws), ws.numel() if ws is not None else 0,
+                               stream_handle(stream)), "nvfp4_moe_plan")
+    return out
+
+
+def nvfp4_moe_packed_weight_bytes(experts: int, N: int, K: int, gated: bool) -> int:
+    return int(lib().nvfp4_moe_packed_weight_bytes(experts, N, K, int(gated)))
+
+
+class NVFP4MoEWeight:
+    """The NVFP4 weights [experts, N, K] of all experts in the packed layout of nvfp4_moe_pack_weights: packed uint8
+    [bytes], global_scale float32 [experts].  gated: gate and up in one, N = 2 * inter."""
+
+    def __init__(self, packed, global_scale, experts: int, N: int, K: int, gated: bool):
+        _need(packed, torch.uint8, "packed", 1)
+        _need(global_scale, torch.float32, "global_scale", 1)
+        need = nvfp4_moe_packed_weight_bytes(experts, N, K, gated)
+        if need == 0 or packed.numel() < need or global_scale.numel() != experts:
+            raise ValueError(f"unsupported expert weights: experts {experts}, N {N}, K {K}, {packed.numel()} bytes")
+        self.packed, self.global_scale = packed, global_scale
+        self.experts, self.N, self.K, self.gated = experts, N, K, bool(gated)
+
+
+def nvfp4_moe_pack_weights(codes: torch.Tensor, scales: torch.Tensor, global_scale: torch.Tensor, gated: bool,
+                           out: torch.Tensor | None = None, stream=None) -> NVFP4MoEWeight:
+    """Row-major NVFP4 codes [experts, N, K/2], scales [experts, N, K/16] and global scales [experts] -> packed.  gated:
+    rows [0, N/2) are the gate's, [N/2, N) the up's."""
+    _need(codes, torch.uint8, "codes", 3)
+    _need(scales, torch.uint8, "scales", 3)
+    experts, N, half = codes.shape
+    if scales.shape != (experts, N, half // 8) or half % 8:
+        raise ValueError("codes and scales disagree on their shapes")
+    need = nvfp4_moe_packed_weight_bytes(experts, N, 2 * half, gated)
+    if need == 0:
+        raise ValueError(f"unsupported expert weights: experts {experts}, N {N}, K {2 * half}, gated {bool(gated)}")
+    if out is None:
+        out = _empty(need, torch.uint8, codes.device, stream)
+    w = NVFP4MoEWeight(out, global_scale, experts, N, 2 * half, gated)
+    check(lib().nvfp4_moe_pack_weights(codes.data_ptr(), scales.data_ptr(), experts, N, 2 * half, int(gated),
+                                       out.data_ptr(), out.numel(), stream_handle(stream)), "nvfp4_moe_pack_weights")
+    return w
+
+
+def _need_nvfp4(x: NVFP4Tensor, rows: int, K: int, name: str):
+    for t in (x.codes, x.scales):
+        _need(t, torch.uint8, name, 2)
+    _need(x.global_scale, torch.float32, name)
+    if x.codes.shape != (rows, K // 2) or x.scales.shape != (rows, K // 16) or x.global_scale.numel() != 1:
+        raise ValueError(f"{name} must have {rows} rows of {K}")
+
+
+def nvfp4_moe_gate_up(x: NVFP4Tensor, w: NVFP4MoEWeight, routing: MoERouting, out: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """BF16(SiLU(gate) * up) of the chosen experts on x [tokens, K]: rows by place [tokens * top_k, inter], zero behind
+    the last pair."""
+    r = routing
+    if not w.gated or r.experts != w.experts:
+        raise ValueError("w must hold gate and up of the routing's experts")
+    _need_nvfp4(x, r.tokens, w.K, "x")
+    shape = (r.tokens * r.top_k, w.N // 2)
+    if out is None:
+        out = _empty(shape, torch.bfloat16, x.codes.device, stream)
+    else:
+        _need(out, torch.bfloat16, "out")
+        if out.shape != shape:
+            raise ValueError(f"out must have shape {shape}")
+    check(lib().nvfp4_moe_gate_up(x.codes.data_ptr(), x.scales.data_ptr(), x.global_scale.data_ptr(), r.tokens, r.top_k,
+                                  r.offsets.data_ptr(), r.pairs.data_ptr(), w.packed.data_ptr(),
+                                  w.global_scale.data_ptr(), w.experts, w.N // 2, w.K, out.data_ptr(),
+                                  stream_handle(stream)), "nvfp4_moe_gate_up")
+    return out
+
+
+def nvfp4_moe_down(h: NVFP4Tensor, w: NVFP4MoEWeight, routing: MoERouting, y: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y[tokens, N] FP32 = sum over a token's experts of weight * dequant(h) @ dequant(w)^T, h [tokens * top_k, K] by
+    place.  `workspace`: a uint8 tensor of at least nvfp4_moe_down_workspace_bytes bytes (the stream's memory by
+    default)."""
+    r = routing
+    if w.gated or r.experts != w.experts or r.weights is None:
+        raise ValueError("w must hold plain matrices of the routing's experts, and the routing weights")
+    _need_nvfp4(h, r.tokens * r.top_k, w.K, "h")
+    shape, dev = (r.tokens, w.N), h.codes.device
+    if y is None:
+        y = _empty(shape, torch.float32, dev, stream)
+    else:
+        _need(y, torch.float32, "y")
+        if y.shape != shape:
+            raise ValueError(f"y must have shape {shape}")
+    if workspace is None:
+        workspace = _scratch(int(lib().nvfp4_moe_down_workspace_bytes(r.tokens, r.top_k, w.N)), dev, stream)
+    else:
+        _need(workspace, torch.uint8, "workspace")
+    check(lib().nvfp4_moe_down(h.codes.data_ptr(), h.scales.data_ptr(), h.global_scale.data_ptr(), r.tokens, r.top_k,
+                               r.offsets.data_ptr(), r.pairs.data_ptr(), r.places.data_ptr(), r.weights.data_ptr(),
+                               w.packed.data_ptr(), w.global_scale.data_ptr(), w.experts, w.N, w.K, y.data_ptr(),
+                               ptr(workspace), workspace.numel() if workspace is not None else 0, stream_handle(stream)),
+          "nvfp4_moe_down")
+    return y
 
 
 def nvfp4_process_logits(logits: torch.Tensor, tokens: torch.Tensor | None = None, n_tokens: torch.Tensor | None = None,

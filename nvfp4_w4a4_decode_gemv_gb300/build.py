@@ -18,7 +18,7 @@ LIB_NAME = "libnvfp4_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["abi.cu", "quantize.cu", "gemv.cu", "gemv_tc.cu", "gemm_tc.cu", "reset_sample.cu", "glue.cu",
            "kv_plan.cu", "kv_cache.cu", "kv_attention.cu", "kv_attention_tc.cu",
-           "logits.cu"]
+           "logits.cu", "moe_route.cu", "moe_experts.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "-I" + os.path.join(ROOT, "include")]

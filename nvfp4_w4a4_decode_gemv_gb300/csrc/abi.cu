@@ -10,6 +10,8 @@ cudaError_t nvfp4_internal_read_error_gemm(unsigned int* out);
 cudaError_t nvfp4_internal_read_error_kv_cache(unsigned int* out);
 cudaError_t nvfp4_internal_read_error_kv_attention(unsigned int* out);
 cudaError_t nvfp4_internal_read_error_kv_attention_tc(unsigned int* out);
+cudaError_t nvfp4_internal_read_error_moe_route(unsigned int* out);
+cudaError_t nvfp4_internal_read_error_moe_experts(unsigned int* out);
 
 namespace {
 thread_local char g_last_cuda_error[256] = "no CUDA error";
@@ -57,7 +59,7 @@ extern "C" const char* nvfp4_status_str(nvfp4_status s) {
 
 extern "C" const char* nvfp4_last_cuda_error(void) { return g_last_cuda_error; }
 
-extern "C" int nvfp4_version(void) { return (1 << 16) | 2; }
+extern "C" int nvfp4_version(void) { return (1 << 16) | 3; }
 
 extern "C" nvfp4_status nvfp4_device_status(unsigned int* code) {
   if (!code) return NVFP4_ERR_NULL;
@@ -69,5 +71,7 @@ extern "C" nvfp4_status nvfp4_device_status(unsigned int* code) {
   if (e == cudaSuccess) e = nvfp4_internal_read_error_kv_cache(code);
   if (e == cudaSuccess) e = nvfp4_internal_read_error_kv_attention(code);
   if (e == cudaSuccess) e = nvfp4_internal_read_error_kv_attention_tc(code);
+  if (e == cudaSuccess) e = nvfp4_internal_read_error_moe_route(code);
+  if (e == cudaSuccess) e = nvfp4_internal_read_error_moe_experts(code);
   return nvfp4_internal_cuda_status(e);
 }

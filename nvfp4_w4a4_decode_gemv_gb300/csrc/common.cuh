@@ -66,6 +66,8 @@ enum : unsigned int {
   NVFP4_DEVERR_FLAG_TIMEOUT = 4,   // a wait for another CTA's partial sum exceeded its iteration limit
   NVFP4_DEVERR_KV_RANGE = 8,       // a slot, page, length or row range outside a KV cache or its tables
   NVFP4_DEVERR_NO_TOKEN = 16,      // a row of logits without a finite entropy: nothing to sample
+  NVFP4_DEVERR_NO_EXPERT = 32,     // a token whose router logits have no order or no scores
+  NVFP4_DEVERR_MOE_RANGE = 64,     // an expert, offset, pair or place outside a plan's tables
 };
 
 // Relaxed GPU-scope word store / load: single-copy atomic, no ordering.

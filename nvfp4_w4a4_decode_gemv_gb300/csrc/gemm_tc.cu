@@ -77,19 +77,6 @@ NVFP4_DEVINL unsigned int* record(const GemmArgs& a, long long q, int m, int row
   return a.records + ((size_t)q * a.M + m) * kTR + row;
 }
 
-// Reads accumulator columns [col, col + 16) of this warp's lane quadrant.
-NVFP4_DEVINL void read16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 // Adds, in CTA order, the partial sums of contributors q0 .. q1 (at most
 // kBatch of them) for tokens [m0, m0 + 16) of weight row `row` to v, once every
 // word is written (bounded wait, device error bit 2 when it gives up); the live

@@ -106,11 +106,6 @@ NVFP4_DEVINL void commit(uint32_t lead, uint64_t* bar) {
       "r"(lead)
       : "memory");
 }
-NVFP4_DEVINL uint32_t elect_one() {
-  uint32_t e;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-  return e;
-}
 
 // Operand whose rows (N) are contiguous, 128-byte swizzle: 64-element panels `panel` bytes apart, groups of 8
 // contraction indices 1024 bytes apart.

@@ -1,0 +1,585 @@
+// Routing of tokens to experts: scores, the choice of the best, their weights,
+// and the plan of the (token, expert) pairs by expert that the experts'
+// products read.
+//
+// A warp takes a token; a lane holds experts lane, lane + 32, ...  The choice is
+// top_k rounds of a warp maximum over order-preserving integer keys (equal keys:
+// the lowest expert).  Without a bias the keys are the logits themselves, since
+// both scores grow with them: exact.  With a bias, or with groups ranked by the
+// sum of two scores, the values are FP32 with a bound on their error; a token
+// whose order that bound does not settle is chosen again from 64-bit values
+// (one in some hundreds of tokens), so that the result is the one of the
+// formulas in 64 bits.
+//
+// The plan is a stable counting sort: counts of a CTA's tokens by expert, sums
+// over the CTAs before it, then ranks in the CTA by warp matches.  Every sum is of
+// integers: no order of atomics shows.  Few tokens take one launch of one CTA;
+// else the counts of a launch are what the second one begins with.
+#include <math.h>
+
+#include "common.cuh"
+
+NVFP4_DEFINE_ERROR_READER(nvfp4_internal_read_error_moe_route)
+
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxExperts = 512;
+constexpr int kMaxTop = 32;
+constexpr int kMaxGroups = 32;
+constexpr int kMaxCtas = 152;             // of a call: bounds the workspace; one CTA an SM
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+struct PlanArgs {
+  int32_t *ids, *offsets, *pairs, *places;
+  int32_t* counts;                        // [CTAs][experts], or NULL: one CTA does everything
+  long long n_pairs;
+  int experts, top, per;                  // per: tokens of a CTA
+};
+
+struct RouteArgs {
+  PlanArgs plan;
+  const void* logits;
+  int64_t ld;
+  const float* bias;
+  const uint8_t* rows;
+  float* weights;
+  int tokens, groups, each, top_groups, group_best;
+  uint32_t inv_each;                      // 2^20 / each, rounded up: expert * inv_each >> 20 is its group (expert < 512)
+  int sigmoid, renormalize;
+  float scale;
+};
+
+NVFP4_DEVINL float load1(const float* p) { return *p; }
+NVFP4_DEVINL float load1(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+
+// Keys: unsigned integers in the order of the values; 0 is below every value's key.
+NVFP4_DEVINL uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+NVFP4_DEVINL float value_of(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
+NVFP4_DEVINL unsigned long long key_of(double v) {
+  const unsigned long long b = (unsigned long long)__double_as_longlong(v);
+  return b ^ ((b >> 63) ? ~0ull : 1ull << 63);
+}
+NVFP4_DEVINL double value_of(unsigned long long k) {
+  return __longlong_as_double((long long)(k ^ ((k >> 63) ? 1ull << 63 : ~0ull)));
+}
+NVFP4_DEVINL uint32_t warp_max(uint32_t k) { return __reduce_max_sync(kAll, k); }
+NVFP4_DEVINL unsigned long long warp_max(unsigned long long k) {
+  const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(k >> 32));
+  const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+  return (unsigned long long)hi << 32 | lo;
+}
+template <class F> struct KeyOf;
+template <> struct KeyOf<float> { using T = uint32_t; };
+template <> struct KeyOf<double> { using T = unsigned long long; };
+
+NVFP4_DEVINL float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+NVFP4_DEVINL double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+// The largest key of the warp and the lowest index that has it (index < 2^16); best and at: the lane's own.
+template <class K>
+NVFP4_DEVINL K warp_best(K best, int at, int& winner) {
+  const K m = warp_max(best);
+  winner = (int)__reduce_min_sync(kAll, best == m ? (uint32_t)at : 0xFFFFu);
+  return m;
+}
+
+// The groups that stay, as a mask: the top_groups best by the sum of their group_best (1 or 2) largest values.  unsure:
+// the first group left out is within 2 err of the last one kept.
+template <class F, int NV>
+NVFP4_DEVINL uint32_t best_groups(const RouteArgs& a, const F (&v)[NV], int lane, F err, bool& unsure) {
+  using K = typename KeyOf<F>::T;
+  K mine = 0;                                             // lane g: the key of group g's score
+  for (int g = 0; g < a.groups; ++g) {
+    K first = 0, second = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = i * 32 + lane;
+      if (e < a.plan.experts && (int)(((uint32_t)e * a.inv_each) >> 20) == g) {
+        const K k = key_of(v[i]);
+        if (k > first) {
+          second = first;
+          first = k;
+        } else if (k > second) {
+          second = k;
+        }
+      }
+    }
+    int owner;
+    const K m1 = warp_best(first, lane, owner);
+    K score = m1;
+    if (a.group_best == 2 && a.each > 1) score = key_of(value_of(m1) + value_of(warp_max(lane == owner ? second : first)));
+    if (lane == g) mine = score;
+  }
+  uint32_t kept = 0u;
+  K last = 0;
+  for (int j = 0; j <= a.top_groups && j < a.groups; ++j) {
+    int g;
+    const K m = warp_best(mine, lane, g);
+    if (j == a.top_groups) {
+      if (!(value_of(last) - value_of(m) > 2 * err)) unsure = true;
+      break;
+    }
+    kept |= 1u << g;
+    if (lane == g) mine = 0;
+    last = m;
+  }
+  return kept;
+}
+
+// Lane j's choice j (j < top_k).  c: what the choice goes by, v: what the groups go by.  unsure: two neighbours in the
+// order, the first left out among them, are within 2 err.
+template <class F, int NV>
+NVFP4_DEVINL int pick(const RouteArgs& a, const F (&c)[NV], const F (&v)[NV], int lane, F c_err, F v_err, bool& unsure) {
+  using K = typename KeyOf<F>::T;
+  unsure = false;
+  uint32_t kept = kAll;
+  if (a.top_groups < a.groups) kept = best_groups<F, NV>(a, v, lane, v_err, unsure);
+  K key[NV];
+  K best = 0;
+  int at = lane;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = i * 32 + lane;
+    key[i] = e < a.plan.experts && (a.groups == 1 || (kept >> (((uint32_t)e * a.inv_each) >> 20) & 1u)) ? key_of(c[i]) : 0;
+    if (key[i] > best) {
+      best = key[i];
+      at = e;
+    }
+  }
+  int mine = -1;
+  K last = 0;
+  const int rounds = a.plan.top + (c_err > 0 ? 1 : 0);    // one more looks at the first that is left out
+  for (int j = 0; j < rounds; ++j) {
+    int e;
+    const K m = warp_best(best, at, e);
+    if (m == 0) break;                                    // nothing is left out
+    if (j > 0 && c_err > 0 && !(value_of(last) - value_of(m) > 2 * c_err)) unsure = true;
+    last = m;
+    if (lane == j) mine = e;
+    if (lane == (e & 31)) {
+      best = 0;
+      at = lane;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (i * 32 + lane == e) key[i] = 0;
+        if (key[i] > best) {
+          best = key[i];
+          at = i * 32 + lane;
+        }
+      }
+    }
+  }
+  return mine;
+}
+
+// The choice from 64-bit values.
+template <int NV, class T>
+__device__ __noinline__ int pick_exact(const RouteArgs& a, const T* row, int lane) {
+  double x[NV], v[NV];
+  double m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = i * 32 + lane;
+    x[i] = e < a.plan.experts ? (double)load1(row + e) + 0.0 : -INFINITY;
+    m = fmax(m, x[i]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kAll, m, o));
+  double z = 0.0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    v[i] = a.sigmoid ? 1.0 / (1.0 + exp(-x[i])) : exp(x[i] - m);
+    z += v[i];
+  }
+  z = a.sigmoid ? 1.0 : warp_sum(z);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = i * 32 + lane;
+    v[i] = v[i] / z + (a.bias && e < a.plan.experts ? (double)a.bias[e] : 0.0);
+    if (a.bias) x[i] = v[i];
+  }
+  bool unsure;
+  return pick<double, NV>(a, x, v, lane, 0.0, 0.0, unsure);
+}
+
+// One token by one warp: lane j < top_k returns its expert (-1: none) and writes it with its weight.
+template <int NV, class T>
+NVFP4_DEVINL int route_row(const RouteArgs& a, int token, int lane) {
+  const int E = a.plan.experts, top = a.plan.top;
+  int id = -1;
+  float w = 0.0f;
+  if (!a.rows || a.rows[token] != 0) {
+    const T* row = static_cast<const T*>(a.logits) + (size_t)token * a.ld;
+    float x[NV], v[NV];
+    float m = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = i * 32 + lane;
+      x[i] = e < E ? load1(row + e) + 0.0f : -INFINITY;   // (+ 0: both zeros are one value)
+      bad = bad || isnan(x[i]);
+      m = fmaxf(m, x[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+    if (!a.sigmoid) bad = bad || isinf(m);
+    float z = 1.0f, c_err = 0.0f, v_err = 0.0f;
+    const bool sums = a.top_groups < a.groups && a.group_best == 2;
+    if (a.bias || sums || (!a.sigmoid && !a.renormalize)) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        v[i] = a.sigmoid ? __fdiv_rn(1.0f, 1.0f + expf(-x[i])) : expf(x[i] - m);
+        sum += v[i];
+      }
+      if (!a.sigmoid) z = warp_sum(sum);
+      float most = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int e = i * 32 + lane;
+        if (!a.sigmoid) v[i] = __fdiv_rn(v[i], z);
+        if (a.bias && e < E) {
+          v[i] += a.bias[e];
+          bad = bad || isnan(v[i]);
+        }
+        // (an infinite value settles nothing: the error is then infinite too)
+        if (e < E) most = fmaxf(most, fabsf(v[i]));
+      }
+      most = __uint_as_float(warp_max(__float_as_uint(most)));
+      // |v - exact| is below this.  Sigmoid: 2 ulp of expf, half a one each of sum, quotient and bias.  Softmax, each score
+      // at most 1 / z: x - m loses 2^-24 |x - m|, which e^(x - m) makes 2^-25.4 of 1 at most; expf 2^-22 of each term and
+      // of their sum; the sum of up to 512 terms 21 halves of an ulp, the quotient one: 2^-18.8 in all.  A sum of two
+      // values doubles it.
+      const float score = a.sigmoid ? 0x1p-21f : 0x1p-18f * fminf(1.0f, __fdiv_rn(1.0f, z)) + 0x1p-24f;
+      v_err = 2.0f * (score + 0x1p-23f * most);
+      if (a.bias) c_err = score + 0x1p-23f * most;
+      if (!sums && !a.bias) v_err = 0.0f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = x[i];
+    }
+    bad = __any_sync(kAll, bad);
+    if (!bad) {
+      bool unsure;
+      if (a.bias) {
+        id = pick<float, NV>(a, v, v, lane, c_err, v_err, unsure);
+      } else if (sums) {
+        id = pick<float, NV>(a, x, v, lane, 0.0f, v_err, unsure);
+      } else {
+        id = pick<float, NV>(a, x, x, lane, 0.0f, 0.0f, unsure);
+        unsure = false;                                   // logits: equal ones are equal
+      }
+      if (unsure) id = pick_exact<NV, T>(a, row, lane);
+      const bool chosen = lane < top;
+      const float xc = chosen ? load1(row + max(id, 0)) + 0.0f : -INFINITY;
+      if (a.renormalize) {
+        // exp(x) / (1 + exp(x)) and exp(x) alike, relative to the largest of the chosen: no sum underflows
+        float xm = xc;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) xm = fmaxf(xm, __shfl_xor_sync(kAll, xm, o));
+        float t = 0.0f;
+        if (chosen && xm > -INFINITY)
+          t = a.sigmoid ? __fdiv_rn(expf(fminf(xc, 0.0f) - fminf(xm, 0.0f)), 1.0f + expf(-fabsf(xc))) : expf(xc - xm);
+        const float sum = warp_sum(t);
+        w = sum > 0.0f ? __fdiv_rn(t, sum) * a.scale : 0.0f;
+      } else {
+        w = (a.sigmoid ? __fdiv_rn(1.0f, 1.0f + expf(-xc)) : __fdiv_rn(expf(xc - m), z)) * a.scale;
+      }
+    } else if (lane == 0) {
+      atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_NO_EXPERT);
+    }
+  }
+  if (lane < top) {
+    a.plan.ids[(size_t)token * top + lane] = id;
+    a.weights[(size_t)token * top + lane] = w;
+  }
+  return lane < top ? id : -1;
+}
+
+// Exclusive sums of s_tot[0, n) over the first warp, into s_first[0, n]; n <= 512.
+NVFP4_DEVINL void first_of_experts(const int* s_tot, int* s_first, int n) {
+  const int lane = threadIdx.x, per = (n + 31) / 32;
+  int sum = 0;
+  for (int i = 0; i < per; ++i) sum += lane * per + i < n ? s_tot[lane * per + i] : 0;
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kAll, inc, o);
+    if (lane >= o) inc += x;
+  }
+  int at = inc - sum;
+  for (int i = 0; i < per; ++i)
+    if (lane * per + i < n) {
+      s_first[lane * per + i] = at;
+      at += s_tot[lane * per + i];
+    }
+  if (lane == 31) s_first[n] = at;
+}
+
+// This CTA's pairs [p0, p1) to their places; s_next[e]: the next place of expert e; s_warp: kWarps * experts ints.
+NVFP4_DEVINL void place_pairs(const PlanArgs& a, long long p0, long long p1, int* s_next, int* s_warp) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = a.experts;
+  for (long long p = p0; p < p1; p += kThreads) {
+    const int warps = (int)((min(p1 - p, (long long)kThreads) + 31) / 32);   // that have pairs
+    for (int i = tid; i < warps * E; i += kThreads) s_warp[i] = 0;
+    __syncthreads();
+    const long long pair = p + tid;
+    int e = pair < p1 ? __ldcg(a.ids + pair) : -1;
+    if (e < 0 || e >= E) e = -1;
+    const uint32_t same = __match_any_sync(kAll, e);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    if (e >= 0 && rank == 0) s_warp[warp * E + e] = __popc(same);
+    __syncthreads();
+    for (int i = tid; i < E; i += kThreads) {
+      int at = s_next[i];
+      for (int w = 0; w < warps; ++w) {
+        const int n = s_warp[w * E + i];
+        s_warp[w * E + i] = at;
+        at += n;
+      }
+      s_next[i] = at;
+    }
+    __syncthreads();
+    if (pair < p1) {
+      const int at = e >= 0 ? s_warp[warp * E + e] + rank : -1;
+      a.places[pair] = at;
+      if (e >= 0) a.pairs[at] = (int)pair;
+    }
+    __syncthreads();
+  }
+}
+
+// Entries of pairs behind the last one, this CTA's share.
+NVFP4_DEVINL void fill_pairs(const PlanArgs& a, long long p0, long long p1, int total) {
+  for (long long p = max(p0, (long long)total) + threadIdx.x; p < p1; p += kThreads) a.pairs[p] = -1;
+}
+
+extern __shared__ int s_dyn[];            // kWarps * experts, where a plan is made
+
+// ids == NULL route; else (NV = 0): the ids are the caller's.
+template <int NV, class T>
+__global__ void __launch_bounds__(kThreads) moe_route_kernel(const RouteArgs a) {
+  __shared__ int s_cnt[kMaxExperts], s_first[kMaxExperts + 1];
+  const PlanArgs& pl = a.plan;
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < pl.experts; i += kThreads) s_cnt[i] = 0;
+  __syncthreads();
+  griddep_wait();
+  const int t0 = min(blockIdx.x * pl.per, a.tokens), t1 = min(t0 + pl.per, a.tokens);
+  const long long p0 = (long long)t0 * pl.top, p1 = (long long)t1 * pl.top;
+  if constexpr (NV > 0) {
+    for (int t = t0 + warp; t < t1; t += kWarps) {
+      const int id = route_row<NV, T>(a, t, lane);
+      if (id >= 0) atomicAdd(&s_cnt[id], 1);
+    }
+  } else {
+    for (long long p = p0 + tid; p < p1; p += kThreads) {
+      const int id = pl.ids[p];
+      if (id >= 0 && id < pl.experts) atomicAdd(&s_cnt[id], 1);
+      else if (id != -1) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
+    }
+  }
+  __syncthreads();                        // (and the ids are visible to the CTA)
+  if (pl.counts) {
+    for (int i = tid; i < pl.experts; i += kThreads) pl.counts[(size_t)blockIdx.x * pl.experts + i] = s_cnt[i];
+    return;
+  }
+  if (warp == 0) first_of_experts(s_cnt, s_first, pl.experts);
+  __syncthreads();
+  for (int i = tid; i <= pl.experts; i += kThreads) pl.offsets[i] = s_first[i];
+  fill_pairs(pl, 0, pl.n_pairs, s_first[pl.experts]);
+  __syncthreads();                        // s_first turns into the next places
+  place_pairs(pl, p0, p1, s_first, s_dyn);
+}
+
+__global__ void __launch_bounds__(kThreads) moe_place_kernel(const PlanArgs a) {
+  __shared__ int s_tot[kMaxExperts], s_before[kMaxExperts], s_first[kMaxExperts + 1];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, E = a.experts, G = gridDim.x;
+  for (int i = tid; i < E; i += kThreads) s_tot[i] = s_before[i] = 0;
+  __syncthreads();
+  const int parts = kThreads / E, part = tid / E, e = tid - part * E;
+  if (part < parts) {
+    int tot = 0, before = 0;
+    const int b0 = part * G / parts, b1 = (part + 1) * G / parts;
+#pragma unroll 8
+    for (int b = b0; b < b1; ++b) {
+      const int n = a.counts[(size_t)b * E + e];
+      tot += n;
+      if (b < (int)blockIdx.x) before += n;
+    }
+    atomicAdd(&s_tot[e], tot);
+    atomicAdd(&s_before[e], before);
+  }
+  __syncthreads();
+  if (tid < 32) first_of_experts(s_tot, s_first, E);
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int i = tid; i <= E; i += kThreads) a.offsets[i] = s_first[i];
+  const long long p0 = min((long long)blockIdx.x * a.per * a.top, a.n_pairs);
+  const long long p1 = min(p0 + (long long)a.per * a.top, a.n_pairs);
+  fill_pairs(a, p0, p1, s_first[E]);
+  for (int i = tid; i < E; i += kThreads) s_tot[i] = s_first[i] + s_before[i];
+  __syncthreads();
+  place_pairs(a, p0, p1, s_tot, s_dyn);
+}
+
+template <class Args>
+cudaError_t launch(void (*kern)(Args), int grid, size_t smem, const Args& a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+using RouteKernel = void (*)(RouteArgs);
+
+template <class T>
+RouteKernel kernel_for(int experts) {
+  if (experts <= 32) return moe_route_kernel<1, T>;
+  if (experts <= 64) return moe_route_kernel<2, T>;
+  if (experts <= 128) return moe_route_kernel<4, T>;
+  if (experts <= 256) return moe_route_kernel<8, T>;
+  return moe_route_kernel<16, T>;
+}
+
+// The largest dynamic shared memory that a plan takes, allowed once a device for every kernel here.
+cudaError_t allow_smem() {
+  static PerDeviceInt done;
+  cudaError_t err = cudaSuccess;
+  done.get([](int, cudaError_t* e_out) -> int {
+    const RouteKernel all[] = {moe_route_kernel<0, float>, moe_route_kernel<1, float>, moe_route_kernel<2, float>,
+                               moe_route_kernel<4, float>, moe_route_kernel<8, float>, moe_route_kernel<16, float>,
+                               moe_route_kernel<1, uint16_t>, moe_route_kernel<2, uint16_t>, moe_route_kernel<4, uint16_t>,
+                               moe_route_kernel<8, uint16_t>, moe_route_kernel<16, uint16_t>};
+    const int bytes = kWarps * kMaxExperts * (int)sizeof(int);
+    cudaError_t e = cudaFuncSetAttribute(moe_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    for (RouteKernel k : all)
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    *e_out = e;
+    return e == cudaSuccess ? 1 : 0;
+  }, &err);
+  return err;
+}
+
+// Tokens that one CTA routes and plans by itself.
+constexpr int kOneCta = 64;
+
+int ctas_for(int tokens) {
+  if (tokens <= kOneCta) return 1;
+  const int n = (tokens + kWarps - 1) / kWarps;
+  return n < kMaxCtas ? n : kMaxCtas;
+}
+
+cudaError_t run(RouteKernel kern, RouteArgs a, cudaStream_t stream) {
+  cudaError_t e = allow_smem();
+  if (e != cudaSuccess) return e;
+  const int ctas = ctas_for(a.tokens);
+  a.plan.per = (a.tokens + ctas - 1) / ctas;
+  a.plan.n_pairs = (long long)a.tokens * a.plan.top;
+  const size_t smem = (size_t)kWarps * a.plan.experts * sizeof(int);
+  if (ctas == 1) {
+    a.plan.counts = nullptr;
+    return launch(kern, 1, smem, a, stream);
+  }
+  e = launch(kern, ctas, 0, a, stream);
+  return e == cudaSuccess ? launch(moe_place_kernel, ctas, smem, a.plan, stream) : e;
+}
+
+}  // namespace
+
+nvfp4_status nvfp4_internal_cuda_status(cudaError_t e);
+bool nvfp4_internal_aligned(const void* p, size_t a);
+nvfp4_status nvfp4_internal_check_device();
+
+namespace {
+
+nvfp4_status check_plan(int tokens, int top_k, int experts, const PlanArgs& p, const void* workspace, size_t bytes) {
+  if (experts < 1 || experts > kMaxExperts || tokens < 0 || top_k < 1 || top_k > kMaxTop) return NVFP4_ERR_SHAPE;
+  if ((long long)tokens * top_k > 0x7FFFFFFFll) return NVFP4_ERR_SHAPE;
+  if (!p.offsets || (tokens > 0 && (!p.ids || !p.pairs || !p.places))) return NVFP4_ERR_NULL;
+  if (!nvfp4_internal_aligned(p.offsets, 4) || !nvfp4_internal_aligned(p.ids, 4) || !nvfp4_internal_aligned(p.pairs, 4) ||
+      !nvfp4_internal_aligned(p.places, 4) || !nvfp4_internal_aligned(workspace, 4))
+    return NVFP4_ERR_ALIGN;
+  const size_t need = nvfp4_moe_route_workspace_bytes(tokens, experts);
+  if (need > 0 && !workspace) return NVFP4_ERR_NULL;
+  if (bytes < need) return NVFP4_ERR_SHAPE;
+  return NVFP4_OK;
+}
+
+}  // namespace
+
+extern "C" size_t nvfp4_moe_route_workspace_bytes(int tokens, int experts) {
+  if (tokens < 0 || experts < 1 || experts > kMaxExperts) return 0;
+  const int ctas = ctas_for(tokens);
+  return ctas == 1 ? 0 : (size_t)ctas * experts * sizeof(int32_t);
+}
+
+extern "C" nvfp4_status nvfp4_moe_route(const void* logits, int dtype, int tokens, int experts, int64_t ld,
+                                        const nvfp4_moe_router* r, const float* bias, const uint8_t* rows, int32_t* ids,
+                                        float* weights, int32_t* offsets, int32_t* pairs, int32_t* places, void* workspace,
+                                        size_t workspace_bytes, cudaStream_t stream) {
+  if (!r) return NVFP4_ERR_NULL;
+  RouteArgs a = {};
+  a.plan.ids = ids, a.plan.offsets = offsets, a.plan.pairs = pairs, a.plan.places = places;
+  a.plan.counts = static_cast<int32_t*>(workspace);
+  const nvfp4_status cs = check_plan(tokens, r->top_k, experts, a.plan, workspace, workspace_bytes);
+  if (cs != NVFP4_OK) return cs;
+  if (r->groups < 1 || r->groups > kMaxGroups || experts % r->groups != 0 || r->top_groups < 1 ||
+      r->top_groups > r->groups || r->top_k > experts / r->groups * r->top_groups || ld < experts)
+    return NVFP4_ERR_SHAPE;
+  if (dtype != NVFP4_DTYPE_F32 && dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_RANGE;
+  if (r->score != NVFP4_MOE_SOFTMAX && r->score != NVFP4_MOE_SIGMOID) return NVFP4_ERR_RANGE;
+  if (r->group_best < 1 || r->group_best > 2 || !isfinite(r->scale)) return NVFP4_ERR_RANGE;
+  if (tokens > 0 && (!logits || !weights)) return NVFP4_ERR_NULL;
+  if (!nvfp4_internal_aligned(logits, dtype == NVFP4_DTYPE_F32 ? 4 : 2) || !nvfp4_internal_aligned(bias, 4) ||
+      !nvfp4_internal_aligned(weights, 4))
+    return NVFP4_ERR_ALIGN;
+  const nvfp4_status ds = nvfp4_internal_check_device();
+  if (ds != NVFP4_OK) return ds;
+  a.plan.experts = experts, a.plan.top = r->top_k;
+  a.logits = logits, a.ld = ld, a.bias = bias, a.rows = rows, a.weights = weights;
+  a.tokens = tokens, a.groups = r->groups, a.each = experts / r->groups, a.top_groups = r->top_groups;
+  a.group_best = r->group_best, a.sigmoid = r->score == NVFP4_MOE_SIGMOID, a.renormalize = r->renormalize != 0;
+  a.scale = r->scale;
+  a.inv_each = ((1u << 20) + a.each - 1) / a.each;
+  return nvfp4_internal_cuda_status(
+      run(dtype == NVFP4_DTYPE_F32 ? kernel_for<float>(experts) : kernel_for<uint16_t>(experts), a, stream));
+}
+
+extern "C" nvfp4_status nvfp4_moe_plan(const int32_t* ids, int tokens, int top_k, int experts, int32_t* offsets,
+                                       int32_t* pairs, int32_t* places, void* workspace, size_t workspace_bytes,
+                                       cudaStream_t stream) {
+  RouteArgs a = {};
+  a.plan.ids = const_cast<int32_t*>(ids), a.plan.offsets = offsets, a.plan.pairs = pairs, a.plan.places = places;
+  a.plan.counts = static_cast<int32_t*>(workspace);
+  const nvfp4_status cs = check_plan(tokens, top_k, experts, a.plan, workspace, workspace_bytes);
+  if (cs != NVFP4_OK) return cs;
+  const nvfp4_status ds = nvfp4_internal_check_device();
+  if (ds != NVFP4_OK) return ds;
+  a.plan.experts = experts, a.plan.top = top_k;
+  a.tokens = tokens;
+  return nvfp4_internal_cuda_status(run(moe_route_kernel<0, float>, a, stream));
+}
