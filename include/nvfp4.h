@@ -478,6 +478,30 @@ nvfp4_status nvfp4_kv_append(const void* k, const void* v, int dtype, int tokens
                              const int32_t* slots, const nvfp4_kv_cache* cache, cudaStream_t stream);
 
 /*
+ * nvfp4_kv_append with the rotation of positions on the way: q and k rows are rotated, q goes to q_out (BF16), k and v to
+ * their slots.  With (c, s) = table[positions[i], m], pair m (m < rotated / 2) of a row turns from (a, b) to
+ *   (a c - b s, b c + a s)          every product and sum rounded to FP32, the results to BF16 (RNE)
+ * where (a, b) are elements (m, m + rotated/2) with NVFP4_ROPE_HALVES and (2m, 2m + 1) with NVFP4_ROPE_PAIRS; elements from
+ * `rotated` on are rounded to BF16 alone.  K rows are quantized from their BF16 values by the recipe of nvfp4_kv_append.
+ * FP32 rows are not rounded before they are rotated; v rows are first rounded to BF16.
+ * A slot of -1 skips its row (padding: nothing of it is read, its q_out is zero).  So does, recording device error bit 3,
+ * a slot outside the cache or a position outside the table.  No two rows of a call may have the same slot.
+ *   q           device, [tokens, heads, head_dim] at q + i * q_token_stride + h * q_head_stride; heads 1 .. 65536
+ *   k, v        as in nvfp4_kv_append;  dtype of all three;  all 16-byte aligned, strides multiples of 16 bytes
+ *   positions   device, [tokens] int32
+ *   table       device, [max_positions, rotated / 2, 2] FP32: cosine and sine, 16-byte aligned
+ *   rotated     a multiple of 32, 32 .. head_dim
+ *   q_out       device, [tokens, heads, head_dim] BF16, 16-byte aligned (written); not q, k or v
+ */
+enum { NVFP4_ROPE_HALVES = 0, NVFP4_ROPE_PAIRS = 1 };
+
+nvfp4_status nvfp4_kv_append_rope(const void* q, const void* k, const void* v, int dtype, int tokens, int heads,
+                                  int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                                  int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                                  const int32_t* positions, const float* table, int max_positions, int rotated, int style,
+                                  const int32_t* slots, const nvfp4_kv_cache* cache, uint16_t* q_out, cudaStream_t stream);
+
+/*
  * Reads rows back: k_out, v_out [tokens, kv_heads, head_dim] BF16 (16-byte
  * aligned) receive BF16(e2m1(code) * (e4m3(scale) * global)) of the slots'
  * rows, products in FP32; a slot of -1 gives zeros, one outside the cache gives zeros and

@@ -51,6 +51,9 @@ class MoERouter(ctypes.Structure):
 # NVFP4_MOE_* of nvfp4.h
 MOE_SCORES = {"softmax": 0, "sigmoid": 1}
 
+# NVFP4_ROPE_* of nvfp4.h
+ROPE_STYLES = {"halves": 0, "pairs": 1}
+
 # NVFP4_DTYPE_* of nvfp4.h
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
@@ -88,6 +91,8 @@ SIGNATURES = {
     "nvfp4_kv_plan": (_c_i, [_c_p, _c_p, _c_i, _c_i, _c_p, _c_i, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i,
                              _c_p, _c_p]),
     "nvfp4_kv_append": (_c_i, [_c_p, _c_p, _c_i, _c_i, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p]),
+    "nvfp4_kv_append_rope": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64,
+                                    _c_p, _c_p, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p, _c_p]),
     "nvfp4_kv_read": (_c_i, [_c_p, _c_p, _c_i, _c_p, _c_p, _c_p]),
     "nvfp4_kv_attention_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i, _c_i]),
     "nvfp4_kv_attention": (_c_i, [_c_p, _c_i, _c_i, _c_i64, _c_i64, _c_i, _c_p, _c_p, _c_i, _c_p, _c_p, _c_i, _c_i,

@@ -8,8 +8,8 @@ import weakref
 
 import torch
 
-from ._lib import (DTYPES, MOE_SCORES, THRESHOLD_FIXED, THRESHOLD_RESET, THRESHOLD_WINDOW, KVCacheDesc, MoERouter,
-                   ResetParams, check, lib, ptr, stream_handle)
+from ._lib import (DTYPES, MOE_SCORES, ROPE_STYLES, THRESHOLD_FIXED, THRESHOLD_RESET, THRESHOLD_WINDOW, KVCacheDesc,
+                   MoERouter, ResetParams, check, lib, ptr, stream_handle)
 
 __all__ = [
     "nvfp4_quantize_act", "nvfp4_quantize_f32", "nvfp4_silu_mul_quantize", "nvfp4_gemv_smallm",
@@ -24,6 +24,7 @@ __all__ = [
     "NVFP4KVCache", "KVPlan", "nvfp4_kv_page_bytes", "nvfp4_kv_release", "nvfp4_kv_plan", "nvfp4_kv_append",
     "nvfp4_kv_read", "nvfp4_kv_attention", "nvfp4_kv_attention_workspace_bytes", "nvfp4_process_logits",
     "DEVERR_KV_RANGE", "DEVERR_NO_TOKEN",
+    "rope_table", "nvfp4_kv_append_rope",
     "MoERouting", "NVFP4MoEWeight", "nvfp4_moe_route", "nvfp4_moe_plan", "nvfp4_moe_packed_weight_bytes",
     "nvfp4_moe_pack_weights", "nvfp4_moe_gate_up", "nvfp4_moe_down", "DEVERR_NO_EXPERT", "DEVERR_MOE_RANGE",
 ]
@@ -484,6 +485,47 @@ def nvfp4_kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache
     ks, vs = k.stride(), v.stride()
     check(lib().nvfp4_kv_append(k.data_ptr(), v.data_ptr(), code, tokens, ks[0], ks[1], vs[0], vs[1], slots.data_ptr(),
                                 cache.desc_ptr, stream_handle(stream)), "nvfp4_kv_append")
+
+
+def rope_table(max_positions: int, rotated: int, base: float = 10000.0, scale: float = 1.0, device="cuda") -> torch.Tensor:
+    """Cosines and sines of position * scale * base^(-2 m / rotated), m < rotated / 2, for nvfp4_kv_append_rope: float32
+    [max_positions, rotated / 2, 2], computed in 64 bits."""
+    f64 = dict(dtype=torch.float64, device=device)
+    angle = (torch.arange(max_positions, **f64) * scale)[:, None] * base ** (torch.arange(rotated // 2, **f64) * (-2.0 / rotated))
+    return torch.stack([angle.cos(), angle.sin()], -1).float()
+
+
+def nvfp4_kv_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+                         cache: NVFP4KVCache, table: torch.Tensor, style: str = "halves",
+                         q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rows q [tokens, heads, head_dim] and k [tokens, kv_heads, head_dim] rotated by their positions (int32 [tokens]) with
+    the cosines and sines of table (float32 [max_positions, rotated / 2, 2], rope_table); k and v go quantized into the
+    cache's slots (-1: skip, q zero), q comes back in BF16.  style: the rotated part's "halves" form the pairs, or
+    neighbours do ("pairs")."""
+    if q.dim() != 3 or style not in ROPE_STYLES:
+        raise ValueError(f"q must be [tokens, heads, head_dim], style one of {sorted(ROPE_STYLES)}")
+    tokens, heads, dim = q.shape[0], q.shape[1], cache.head_dim
+    code = _need_rows(q, "q", heads, dim)
+    if (_need_rows(k, "k", cache.kv_heads, dim) != code or _need_rows(v, "v", cache.kv_heads, dim) != code
+            or k.shape[0] != tokens or v.shape[0] != tokens):
+        raise ValueError("q, k and v must have the same type and number of tokens")
+    _need_all(torch.int32, 1, "positions slots", positions, slots)
+    _need(table, torch.float32, "table", 3)
+    if positions.numel() != tokens or slots.numel() != tokens or table.shape[2] != 2:
+        raise ValueError("positions and slots need one entry a token, table two numbers a pair")
+    shape = (tokens, heads, dim)
+    if q_out is None:
+        q_out = _empty(shape, torch.bfloat16, q.device, stream)
+    else:
+        _need(q_out, torch.bfloat16, "q_out")
+        if q_out.shape != shape:
+            raise ValueError(f"q_out must have shape {shape}")
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    check(lib().nvfp4_kv_append_rope(q.data_ptr(), k.data_ptr(), v.data_ptr(), code, tokens, heads, qs[0], qs[1], ks[0],
+                                     ks[1], vs[0], vs[1], positions.data_ptr(), table.data_ptr(), table.shape[0],
+                                     2 * table.shape[1], ROPE_STYLES[style], slots.data_ptr(), cache.desc_ptr,
+                                     q_out.data_ptr(), stream_handle(stream)), "nvfp4_kv_append_rope")
+    return q_out
 
 
 def nvfp4_kv_read(cache: NVFP4KVCache, slots: torch.Tensor, k_out: torch.Tensor | None = None,

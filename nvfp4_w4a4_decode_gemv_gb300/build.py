@@ -17,7 +17,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB_NAME = "libnvfp4_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["abi.cu", "quantize.cu", "gemv.cu", "gemv_tc.cu", "gemm_tc.cu", "reset_sample.cu", "glue.cu",
-           "kv_plan.cu", "kv_cache.cu", "kv_attention.cu", "kv_attention_tc.cu",
+           "kv_plan.cu", "kv_cache.cu", "kv_rope.cu", "kv_attention.cu", "kv_attention_tc.cu",
            "logits.cu", "moe_route.cu", "moe_experts.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -10,6 +10,7 @@ cudaError_t nvfp4_internal_read_error_gemm(unsigned int* out);
 cudaError_t nvfp4_internal_read_error_kv_cache(unsigned int* out);
 cudaError_t nvfp4_internal_read_error_kv_attention(unsigned int* out);
 cudaError_t nvfp4_internal_read_error_kv_attention_tc(unsigned int* out);
+cudaError_t nvfp4_internal_read_error_kv_rope(unsigned int* out);
 cudaError_t nvfp4_internal_read_error_moe_route(unsigned int* out);
 cudaError_t nvfp4_internal_read_error_moe_experts(unsigned int* out);
 
@@ -71,6 +72,7 @@ extern "C" nvfp4_status nvfp4_device_status(unsigned int* code) {
   if (e == cudaSuccess) e = nvfp4_internal_read_error_kv_cache(code);
   if (e == cudaSuccess) e = nvfp4_internal_read_error_kv_attention(code);
   if (e == cudaSuccess) e = nvfp4_internal_read_error_kv_attention_tc(code);
+  if (e == cudaSuccess) e = nvfp4_internal_read_error_kv_rope(code);
   if (e == cudaSuccess) e = nvfp4_internal_read_error_moe_route(code);
   if (e == cudaSuccess) e = nvfp4_internal_read_error_moe_experts(code);
   return nvfp4_internal_cuda_status(e);
