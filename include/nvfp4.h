@@ -486,7 +486,8 @@ nvfp4_status nvfp4_kv_append(const void* k, const void* v, int dtype, int tokens
  * FP32 rows are not rounded before they are rotated; v rows are first rounded to BF16.
  * A slot of -1 skips its row (padding: nothing of it is read, its q_out is zero).  So does, recording device error bit 3,
  * a slot outside the cache or a position outside the table.  No two rows of a call may have the same slot.
- *   q           device, [tokens, heads, head_dim] at q + i * q_token_stride + h * q_head_stride; heads 1 .. 65536
+ *   q           device, [tokens, heads, head_dim] at q + i * q_token_stride + h * q_head_stride; heads 0 .. 65536
+ *               (0: k and v alone; q and q_out are not looked at)
  *   k, v        as in nvfp4_kv_append;  dtype of all three;  all 16-byte aligned, strides multiples of 16 bytes
  *   positions   device, [tokens] int32
  *   table       device, [max_positions, rotated / 2, 2] FP32: cosine and sine, 16-byte aligned

@@ -495,36 +495,41 @@ def rope_table(max_positions: int, rotated: int, base: float = 10000.0, scale: f
     return torch.stack([angle.cos(), angle.sin()], -1).float()
 
 
-def nvfp4_kv_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
-                         cache: NVFP4KVCache, table: torch.Tensor, style: str = "halves",
-                         q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+def nvfp4_kv_append_rope(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                         slots: torch.Tensor, cache: NVFP4KVCache, table: torch.Tensor, style: str = "halves",
+                         q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
     """Rows q [tokens, heads, head_dim] and k [tokens, kv_heads, head_dim] rotated by their positions (int32 [tokens]) with
     the cosines and sines of table (float32 [max_positions, rotated / 2, 2], rope_table); k and v go quantized into the
-    cache's slots (-1: skip, q zero), q comes back in BF16.  style: the rotated part's "halves" form the pairs, or
-    neighbours do ("pairs")."""
-    if q.dim() != 3 or style not in ROPE_STYLES:
-        raise ValueError(f"q must be [tokens, heads, head_dim], style one of {sorted(ROPE_STYLES)}")
-    tokens, heads, dim = q.shape[0], q.shape[1], cache.head_dim
-    code = _need_rows(q, "q", heads, dim)
-    if (_need_rows(k, "k", cache.kv_heads, dim) != code or _need_rows(v, "v", cache.kv_heads, dim) != code
-            or k.shape[0] != tokens or v.shape[0] != tokens):
-        raise ValueError("q, k and v must have the same type and number of tokens")
+    cache's slots (-1: skip, q zero), q comes back in BF16 (None: k and v alone).  style: the rotated part's "halves" form
+    the pairs, or neighbours do ("pairs")."""
+    if style not in ROPE_STYLES:
+        raise ValueError(f"style must be one of {sorted(ROPE_STYLES)}")
+    dim, tokens = cache.head_dim, k.shape[0]
+    code = _need_rows(k, "k", cache.kv_heads, dim)
+    if _need_rows(v, "v", cache.kv_heads, dim) != code or v.shape[0] != tokens:
+        raise ValueError("k and v must have the same type and number of tokens")
     _need_all(torch.int32, 1, "positions slots", positions, slots)
     _need(table, torch.float32, "table", 3)
     if positions.numel() != tokens or slots.numel() != tokens or table.shape[2] != 2:
         raise ValueError("positions and slots need one entry a token, table two numbers a pair")
-    shape = (tokens, heads, dim)
-    if q_out is None:
-        q_out = _empty(shape, torch.bfloat16, q.device, stream)
-    else:
-        _need(q_out, torch.bfloat16, "q_out")
-        if q_out.shape != shape:
-            raise ValueError(f"q_out must have shape {shape}")
-    qs, ks, vs = q.stride(), k.stride(), v.stride()
-    check(lib().nvfp4_kv_append_rope(q.data_ptr(), k.data_ptr(), v.data_ptr(), code, tokens, heads, qs[0], qs[1], ks[0],
-                                     ks[1], vs[0], vs[1], positions.data_ptr(), table.data_ptr(), table.shape[0],
+    heads, qs = 0, (0, 0)
+    if q is not None:
+        heads, qs = q.shape[1] if q.dim() == 3 else 0, q.stride()
+        if _need_rows(q, "q", heads, dim) != code or q.shape[0] != tokens:
+            raise ValueError("q must have the type and number of tokens of k and v")
+        if q_out is None:
+            q_out = _empty((tokens, heads, dim), torch.bfloat16, q.device, stream)
+        else:
+            _need(q_out, torch.bfloat16, "q_out")
+            if q_out.shape != q.shape:
+                raise ValueError(f"q_out must have shape {tuple(q.shape)}")
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
+    ks, vs = k.stride(), v.stride()
+    check(lib().nvfp4_kv_append_rope(ptr(q), k.data_ptr(), v.data_ptr(), code, tokens, heads, qs[0], qs[1], ks[0], ks[1],
+                                     vs[0], vs[1], positions.data_ptr(), table.data_ptr(), table.shape[0],
                                      2 * table.shape[1], ROPE_STYLES[style], slots.data_ptr(), cache.desc_ptr,
-                                     q_out.data_ptr(), stream_handle(stream)), "nvfp4_kv_append_rope")
+                                     ptr(q_out), stream_handle(stream)), "nvfp4_kv_append_rope")
     return q_out
 
 

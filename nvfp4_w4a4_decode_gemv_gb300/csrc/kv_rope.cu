@@ -203,9 +203,9 @@ __global__ void __launch_bounds__(kThreads) kv_rope_few_kernel(const RopeArgs a)
   const long long token = at / kPairs / rows;
   if (token >= a.tokens) return;
   const int slot = SlotsAndPositions{a}(token);
+  if (row == 0 && j == 0 && slot != -1 && (slot < 0 || slot >= a.num_slots))
+    atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
   if (row < a.heads) {
-    if (row == 0 && j == 0 && slot != -1 && (slot < 0 || slot >= a.num_slots))
-      atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_KV_RANGE);
     turn_q<D, T>(a, token, slot, a.positions[token], row, row + 1, j);
   } else if (slot >= 0 && slot < a.num_slots) {
     const int n = row - a.heads;
@@ -332,14 +332,15 @@ extern "C" nvfp4_status nvfp4_kv_append_rope(const void* q, const void* k, const
   if (cs != NVFP4_OK) return cs;
   if (dtype != NVFP4_DTYPE_F32 && dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_RANGE;
   if (style != NVFP4_ROPE_HALVES && style != NVFP4_ROPE_PAIRS) return NVFP4_ERR_RANGE;
-  if (tokens < 0 || heads < 1 || heads > 65536 || max_positions < 1 || rotated < 32 || rotated > cache->head_dim ||
+  if (tokens < 0 || heads < 0 || heads > 65536 || max_positions < 1 || rotated < 32 || rotated > cache->head_dim ||
       rotated % 32 != 0)
     return NVFP4_ERR_SHAPE;
   if (tokens == 0) return NVFP4_OK;
-  if (!q || !k || !v || !positions || !table || !slots || !q_out) return NVFP4_ERR_NULL;
+  if (!k || !v || !positions || !table || !slots || (heads > 0 && (!q || !q_out))) return NVFP4_ERR_NULL;
   const int per = dtype == NVFP4_DTYPE_F32 ? 4 : 8;          // elements of 16 bytes
   // (the stride of a single token or head is used in no address)
-  if (tokens > 1 && (q_token_stride % per || k_token_stride % per || v_token_stride % per)) return NVFP4_ERR_ALIGN;
+  if (tokens > 1 && ((heads > 0 && q_token_stride % per) || k_token_stride % per || v_token_stride % per))
+    return NVFP4_ERR_ALIGN;
   if (heads > 1 && q_head_stride % per) return NVFP4_ERR_ALIGN;
   if (cache->kv_heads > 1 && (k_head_stride % per || v_head_stride % per)) return NVFP4_ERR_ALIGN;
   if (!nvfp4_internal_aligned(q, 16) || !nvfp4_internal_aligned(k, 16) || !nvfp4_internal_aligned(v, 16) ||

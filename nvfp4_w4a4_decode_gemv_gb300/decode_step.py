@@ -43,10 +43,7 @@ class DecodeStep:
             for i, (name, K, N) in enumerate(shapes):
                 g = torch.Generator(device=dev)
                 g.manual_seed(seed * 100003 + layer * 16 + i)
-                wb = (torch.randn((N, K), generator=g, device=dev) * synth.W_STD).to(torch.bfloat16)
-                wq = api.nvfp4_quantize_act(wb)
-                del wb
-                packed[name] = api.nvfp4_pack_weights(wq)
+                packed[name], wq = self._make_weight(name, K, N, g)
                 if keep_rowmajor:
                     rm[name] = wq
             self.weights.append(packed)
@@ -79,6 +76,14 @@ class DecodeStep:
         self.u = torch.zeros(M, dtype=torch.float32, device=dev)
         self.graph = None
 
+    def _random_weight(self, K: int, N: int, g: torch.Generator) -> api.NVFP4Tensor:
+        return api.nvfp4_quantize_act((torch.randn((N, K), generator=g, device=self.device) * synth.W_STD).to(torch.bfloat16))
+
+    def _make_weight(self, name: str, K: int, N: int, g: torch.Generator):
+        """A layer's projection, packed and row-major."""
+        w = self._random_weight(K, N, g)
+        return api.nvfp4_pack_weights(w), w
+
     # ---- the chain ------------------------------------------------------------
     def _layer(self, layer: int, h_in: torch.Tensor, stream, trace):
         w = self.weights[layer]
@@ -90,15 +95,20 @@ class DecodeStep:
             nv = lambda t: (t.codes.clone(), t.scales.clone(), t.global_scale.clone())
             trace.append({"h_in": h_in.clone(), "r": self.r.clone(), "xq": nv(self.xq), "y_qkv": self.y_qkv.clone(),
                           "xq_o": nv(self.xq_o), "y_o": self.y_o.clone()})
-        api.nvfp4_rms_norm_quantize(self.y_o, eps=self.eps, out=self.xq_gu, r_out=self.r_out(trace), stream=stream)
-        api.nvfp4_gemv_smallm_packed(self.xq_gu, w["gate_up"], y=self.y_gu, workspace=self.ws, stream=stream)
-        api.nvfp4_silu_mul_quantize(self.y_gu, out=self.xq_d, stream=stream)
-        api.nvfp4_gemv_smallm_packed(self.xq_d, w["down"], y=self.h, workspace=self.ws, stream=stream)
+        self._mlp(layer, stream, trace)
         if trace is not None:
             trace[-1].update({"r2": self.r.clone(), "xq_gu": nv(self.xq_gu), "y_gu": self.y_gu.clone(),
                               "xq_d": (self.xq_d.codes.clone(), self.xq_d.scales.clone(),
                                        self.xq_d.global_scale.clone()),
                               "h_out": self.h.clone()})
+
+    def _mlp(self, layer: int, stream, trace):
+        """From the o projection's output to the layer's."""
+        w = self.weights[layer]
+        api.nvfp4_rms_norm_quantize(self.y_o, eps=self.eps, out=self.xq_gu, r_out=self.r_out(trace), stream=stream)
+        api.nvfp4_gemv_smallm_packed(self.xq_gu, w["gate_up"], y=self.y_gu, workspace=self.ws, stream=stream)
+        api.nvfp4_silu_mul_quantize(self.y_gu, out=self.xq_d, stream=stream)
+        api.nvfp4_gemv_smallm_packed(self.xq_d, w["down"], y=self.h, workspace=self.ws, stream=stream)
 
     def _input(self):
         """The hidden state that the first layer reads."""

@@ -3,17 +3,24 @@ KV cache, attention and logit rules.
 
     plan   page for each request's new token          nvfp4_kv_plan
     per layer, between the qkv and o projections:
-        K, V columns of qkv -> the 4-bit cache        nvfp4_kv_append
+        K, V columns of qkv -> the 4-bit cache        nvfp4_kv_append, or with positions, q and K rotated by them,
+                                                      nvfp4_kv_append_rope
         q columns over it -> BF16                     nvfp4_kv_attention
         -> NVFP4                                      nvfp4_quantize_act
+    per layer, with experts, instead of its gate_up and down projections:
+        router logits of the normalized rows          nvfp4_bf16_gemv_tc
+        -> the chosen experts and the pairs' plan     nvfp4_moe_route
+        gate and up of each, SiLU(gate) up            nvfp4_moe_gate_up
+        -> NVFP4                                      nvfp4_quantize_act
+        down, summed with the weights                 nvfp4_moe_down
     logits -> penalties, biases, grammar masks        nvfp4_process_logits (in place)
     -> ReSET sampler of the rows with a request; the token joins its request's history
 
 Every layer has a cache of its own; one page table serves them all (a page has
 the same number in each).  Requests come with `start` (prompts, whose K and V
 rows the caller gives) and go with `end`, whose pages the next requests get.
-No rotary positions: the step is synthetic, and `plan.positions` (of the rows
-that get a token, one behind the other) is where a model takes them from.  The step itself (`run`, `capture`) reads lengths, tables
+Positions are optional, as the step is synthetic (`rotary`); a token's position is its
+place in its request.  The step itself (`run`, `capture`) reads lengths, tables
 and histories on the device only, so one captured graph follows any requests.
 """
 import torch
@@ -23,8 +30,16 @@ from .decode_step import DecodeStep
 
 
 class ServingStep(DecodeStep):
+    """rotary: the base of the rotation's angles (None: no positions), of the first `rotated` elements of a head (all by
+    default), in pairs of `rope_style`.  experts: their number (0: dense layers); `shapes` then holds the gate_up and down
+    projections of one expert, and `router` what nvfp4_moe_route takes (top_k, score, groups, ...); `route_bias[layer]` may
+    be set to a float32 [experts] tensor."""
+
     def __init__(self, M: int, layers: int, heads: int, kv_heads: int, head_dim: int = 128, page_size: int = 64,
-                 num_pages: int = 1024, max_len: int = 32768, k_global: float = 1.0, v_global: float = 1.0, **kw):
+                 num_pages: int = 1024, max_len: int = 32768, k_global: float = 1.0, v_global: float = 1.0,
+                 rotary: float | None = None, rotated: int | None = None, rope_style: str = "halves", experts: int = 0,
+                 router: dict | None = None, **kw):
+        self.experts, self.router, self.routers = experts, dict(router or {"top_k": 1}), []
         super().__init__(M, layers, **kw)
         if self.k_o != heads * head_dim or self.n_qkv != (heads + 2 * kv_heads) * head_dim:
             raise ValueError("the qkv and o shapes do not fit the heads")
@@ -52,6 +67,26 @@ class ServingStep(DecodeStep):
         f32 = dict(dtype=torch.float32, device=dev)
         self.repetition, self.presence, self.frequency = torch.ones(M, **f32), torch.zeros(M, **f32), torch.zeros(M, **f32)
         self.bias_ids = self.bias_values = self.mask = self.mask_rows = None
+        self.rope, self.rope_style = None, rope_style
+        if rotary is not None:
+            self.rope = api.rope_table(max_len, rotated or head_dim, rotary, device=dev)
+            self.q_turned = torch.empty((M, heads, head_dim), dtype=torch.bfloat16, device=dev)
+        if experts:
+            shared = kw.get("share_weights")
+            g = torch.Generator(device=dev)
+            g.manual_seed(kw.get("seed", 0) * 100003 + 99989)
+            self.routers = shared.routers if shared is not None else [
+                (torch.randn((experts, self.hidden), generator=g, device=dev) / self.hidden ** 0.5).to(torch.bfloat16)
+                for _ in range(layers)]
+            self.route_bias = [None] * layers
+            top_k = self.router["top_k"]
+            self.route_logits = torch.empty((M, experts), **f32)
+            self.routing = api.MoERouting.empty(M, top_k, experts, dev)
+            self.h_mid = torch.empty((M * top_k, self.k_d), dtype=torch.bfloat16, device=dev)
+            self.xq_d = api.NVFP4Tensor.empty(M * top_k, self.k_d, dev)
+            need = api.nvfp4_bf16_gemv_workspace_bytes(M, experts, self.hidden)
+            if self.ws.numel() < need:
+                self.ws = torch.zeros(need, dtype=torch.uint8, device=dev)
         # views and buffers of the attention
         cut = heads * head_dim
         self.q = self.y_qkv[:, :cut].unflatten(-1, (heads, head_dim))
@@ -61,10 +96,17 @@ class ServingStep(DecodeStep):
         need = api.nvfp4_kv_attention_workspace_bytes(M, M, heads, kv_heads, head_dim)
         self.attn_ws = torch.zeros(need, dtype=torch.uint8, device=dev)
 
+    def _make_weight(self, name, K, N, g):
+        if not self.experts or name not in ("gate_up", "down"):
+            return super()._make_weight(name, K, N, g)
+        rows = [self._random_weight(K, N, g) for _ in range(self.experts)]
+        stack = [torch.stack([getattr(w, part) for w in rows]) for part in ("codes", "scales", "global_scale")]
+        return api.nvfp4_moe_pack_weights(stack[0], stack[1], stack[2].view(-1), gated=name == "gate_up"), rows
+
     # ---- requests -----------------------------------------------------------------
     def start(self, prompts: dict, keys, values):
         """New requests: {row: prompt tokens (1-D int32 on the device)}; keys[layer], values[layer]: their K and V
-        rows [total, kv_heads, head_dim], packed in row order.  Returns the plan (its info: refused, tokens): a prompt
+        rows [total, kv_heads, head_dim], packed in row order (K not yet rotated: positions turn it here).  Returns the plan (its info: refused, tokens): a prompt
         without room has kv_lens[row] = 0 there, and its row stays without a request."""
         new = torch.zeros(self.M, dtype=torch.int32)
         for row, ids in prompts.items():
@@ -83,7 +125,10 @@ class ServingStep(DecodeStep):
         given = torch.tensor([row in prompts for row in range(self.M)], device=self.device)
         taken = given & (plan.kv_lens == self.lens + new)
         for cache, k, v in zip(self.caches, keys, values):
-            api.nvfp4_kv_append(k, v, plan.slots, cache)
+            if self.rope is None:
+                api.nvfp4_kv_append(k, v, plan.slots, cache)
+            else:
+                api.nvfp4_kv_append_rope(None, k, v, plan.positions, plan.slots, cache, self.rope, self.rope_style)
         self.lens.copy_(plan.kv_lens)
         self.sampler.restart(taken)
         for row, ids in prompts.items():
@@ -105,10 +150,27 @@ class ServingStep(DecodeStep):
 
     def _attend(self, layer: int, stream):
         cache = self.caches[layer]
-        api.nvfp4_kv_append(self.k, self.v, self.slots, cache, stream=stream)
-        api.nvfp4_kv_attention(self.q, cache, self.table, self.attn_lens, out=self.attn, workspace=self.attn_ws,
+        q = self.q
+        if self.rope is None:
+            api.nvfp4_kv_append(self.k, self.v, self.slots, cache, stream=stream)
+        else:                                            # a live row's new token stands behind the keys it holds
+            q = api.nvfp4_kv_append_rope(q, self.k, self.v, self.lens, self.slots, cache, self.rope, self.rope_style,
+                                         q_out=self.q_turned, stream=stream)
+        api.nvfp4_kv_attention(q, cache, self.table, self.attn_lens, out=self.attn, workspace=self.attn_ws,
                                stream=stream)
         api.nvfp4_quantize_act(self.attn.view(self.M, self.k_o), out=self.xq_o, stream=stream)
+
+    def _mlp(self, layer: int, stream, trace):
+        if not self.experts:
+            return super()._mlp(layer, stream, trace)
+        w = self.weights[layer]
+        api.nvfp4_rms_norm_quantize(self.y_o, eps=self.eps, out=self.xq_gu, r_out=self.r, stream=stream)
+        api.nvfp4_bf16_gemv_tc(self.r, self.routers[layer], y=self.route_logits, workspace=self.ws, stream=stream)
+        api.nvfp4_moe_route(self.route_logits, bias=self.route_bias[layer], rows=self.live, out=self.routing, stream=stream,
+                            **self.router)
+        api.nvfp4_moe_gate_up(self.xq_gu, w["gate_up"], self.routing, out=self.h_mid, stream=stream)
+        api.nvfp4_quantize_act(self.h_mid, out=self.xq_d, stream=stream)
+        api.nvfp4_moe_down(self.xq_d, w["down"], self.routing, y=self.h, stream=stream)
 
     def _sample(self, stream):
         api.nvfp4_process_logits(self.logits, self.tokens, self.n_tokens, self.n_prompt, self.repetition, self.presence,

@@ -99,6 +99,27 @@ def test_strides_of_one_token_and_one_head():
     assert np.array_equal(Q.bf16_bits_to_f32(bits(got)), want)
 
 
+@pytest.mark.parametrize("tokens", [5, 4200])
+def test_keys_and_values_alone(tokens):
+    """The same cache as with q; bad slots are reported."""
+    rng = np.random.default_rng(4)
+    slots, positions, n_pages = _windows(tokens, 16, 3, rng)
+    s, p = (torch.from_numpy(a.astype(np.int32)).cuda() for a in (slots, positions))
+    q, k, v = torch.randn((3, tokens, 4, 128), device="cuda").bfloat16()
+    table = api.rope_table(4000, 64)
+    caches = [api.NVFP4KVCache.empty(n_pages, 16, 4, 128) for _ in range(2)]
+    for c in caches:
+        c.pages.zero_()
+    api.nvfp4_kv_append_rope(q, k, v, p, s, caches[0], table)
+    assert api.nvfp4_kv_append_rope(None, k, v, p, s, caches[1], table) is None
+    assert torch.equal(caches[0].pages, caches[1].pages) and api.device_status() == 0
+    s[1] = -5
+    api.nvfp4_kv_append_rope(None, k, v, p, s, caches[1], table)
+    assert api.device_status() == api.DEVERR_KV_RANGE
+    with pytest.raises(ValueError):
+        api.nvfp4_kv_append_rope(None, k, v, p, s, caches[1], table, q_out=q)
+
+
 @pytest.mark.parametrize("rotated,base,scale", [(64, 10000.0, 1.0), (128, 1e6, 0.25), (32, 500.0, 1.0)])
 def test_table(rotated, base, scale):
     """Off by half an FP32 step, and by what the angle (64 bits, positions up to 131072) is off: 2^-52 131072."""

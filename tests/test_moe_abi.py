@@ -101,9 +101,10 @@ def test_rotating_append_refusals(lib):  # noqa: F811
         assert call(**{null: None}) == 1, null
     for bad in ({"dtype": 2}, {"style": 2}, {"style": -1}):
         assert call(**bad) == 4, bad
-    for bad in ({"T": -1}, {"H": 0}, {"H": 65537}, {"P": 0}, {"rot": 0}, {"rot": 16}, {"rot": 48}, {"rot": 160}):
+    for bad in ({"T": -1}, {"H": -1}, {"H": 65537}, {"P": 0}, {"rot": 0}, {"rot": 16}, {"rot": 48}, {"rot": 160}):
         assert call(**bad) == 2, bad
     assert call(T=0) == 0
+    assert call(H=0, q=None, out=None, table=FAKE + 8) == 3     # k and v alone: q is not looked at
     for bad, by in (("q", 8), ("k", 8), ("v", 8), ("table", 8), ("out", 8), ("slots", 2), ("pos", 2)):
         assert call(**{bad: FAKE + by}) == 3, bad
     for i in range(6):
