@@ -641,13 +641,17 @@ nvfp4_status nvfp4_moe_pack_weights(const uint8_t* wq, const uint8_t* ws, int ex
  *   wpacked, wg  packed with gated != 0 (N = 2 inter), 16-byte aligned; [experts] FP32 global scales
  *   inter        a multiple of 64;  K a multiple of 64
  *   h            device, [tokens * top_k, inter] BF16, 16-byte aligned (written)
+ *   workspace    device scratch of nvfp4_moe_gate_up_workspace_bytes bytes (0 up to 64 tokens), 256-byte aligned; no state
  * Only the weights of experts that have pairs are read.  Sums of a product are FP32 in an order that the shape and the
  * plan fix: the same inputs give the same bits.  Offsets, pairs and places outside their tables are taken into them or
  * skipped and record device error bit 6 (the rows concerned mean nothing).
  */
+size_t nvfp4_moe_gate_up_workspace_bytes(int tokens, int top_k, int experts, int K);
+
 nvfp4_status nvfp4_moe_gate_up(const uint8_t* xq, const uint8_t* xs, const float* xg, int tokens, int top_k,
                                const int32_t* offsets, const int32_t* pairs, const uint8_t* wpacked, const float* wg,
-                               int experts, int inter, int K, uint16_t* h, cudaStream_t stream);
+                               int experts, int inter, int K, uint16_t* h, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
 
 /*
  * Down products of the chosen experts, summed over a token's experts:
@@ -657,9 +661,9 @@ nvfp4_status nvfp4_moe_gate_up(const uint8_t* xq, const uint8_t* xs, const float
  *   wpacked, wg  packed with gated == 0 ([experts, N, K]), [experts] FP32
  *   weights      device, [tokens, top_k] FP32;  places: the plan's
  *   y            device, [tokens, N] FP32, 16-byte aligned (written)
- *   workspace    device scratch of nvfp4_moe_down_workspace_bytes bytes (0 up to 64 tokens), 16-byte aligned; no state
+ *   workspace    device scratch of nvfp4_moe_down_workspace_bytes bytes (0 up to 64 tokens), 256-byte aligned; no state
  */
-size_t nvfp4_moe_down_workspace_bytes(int tokens, int top_k, int N);
+size_t nvfp4_moe_down_workspace_bytes(int tokens, int top_k, int experts, int N, int K);
 
 nvfp4_status nvfp4_moe_down(const uint8_t* hq, const uint8_t* hs, const float* hg, int tokens, int top_k,
                             const int32_t* offsets, const int32_t* pairs, const int32_t* places, const float* weights,

@@ -105,8 +105,10 @@ SIGNATURES = {
     "nvfp4_moe_plan": (_c_i, [_c_p, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
     "nvfp4_moe_packed_weight_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i]),
     "nvfp4_moe_pack_weights": (_c_i, [_c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p, _c_sz, _c_p]),
-    "nvfp4_moe_gate_up": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_p, _c_p]),
-    "nvfp4_moe_down_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i]),
+    "nvfp4_moe_gate_up_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i]),
+    "nvfp4_moe_gate_up": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_p, _c_p, _c_sz,
+                                 _c_p]),
+    "nvfp4_moe_down_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i, _c_i]),
     "nvfp4_moe_down": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_p,
                               _c_p, _c_sz, _c_p]),
     "reset_state_bytes": (_c_sz, [_c_i, _c_i]),

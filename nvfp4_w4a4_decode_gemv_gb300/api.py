@@ -26,7 +26,8 @@ __all__ = [
     "DEVERR_KV_RANGE", "DEVERR_NO_TOKEN",
     "rope_table", "nvfp4_kv_append_rope",
     "MoERouting", "NVFP4MoEWeight", "nvfp4_moe_route", "nvfp4_moe_plan", "nvfp4_moe_packed_weight_bytes",
-    "nvfp4_moe_pack_weights", "nvfp4_moe_gate_up", "nvfp4_moe_down", "DEVERR_NO_EXPERT", "DEVERR_MOE_RANGE",
+    "nvfp4_moe_pack_weights", "nvfp4_moe_gate_up", "nvfp4_moe_gate_up_workspace_bytes", "nvfp4_moe_down",
+    "nvfp4_moe_down_workspace_bytes", "DEVERR_NO_EXPERT", "DEVERR_MOE_RANGE",
 ]
 
 
@@ -762,10 +763,19 @@ def _need_nvfp4(x: NVFP4Tensor, rows: int, K: int, name: str):
         raise ValueError(f"{name} must have {rows} rows of {K}")
 
 
+def nvfp4_moe_gate_up_workspace_bytes(tokens: int, top_k: int, experts: int, K: int) -> int:
+    return int(lib().nvfp4_moe_gate_up_workspace_bytes(tokens, top_k, experts, K))
+
+
+def nvfp4_moe_down_workspace_bytes(tokens: int, top_k: int, experts: int, N: int, K: int) -> int:
+    return int(lib().nvfp4_moe_down_workspace_bytes(tokens, top_k, experts, N, K))
+
+
 def nvfp4_moe_gate_up(x: NVFP4Tensor, w: NVFP4MoEWeight, routing: MoERouting, out: torch.Tensor | None = None,
-                      stream=None) -> torch.Tensor:
+                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """BF16(SiLU(gate) * up) of the chosen experts on x [tokens, K]: rows by place [tokens * top_k, inter], zero behind
-    the last pair."""
+    the last pair.  `workspace`: a uint8 tensor of at least nvfp4_moe_gate_up_workspace_bytes bytes (the stream's memory
+    by default)."""
     r = routing
     if not w.gated or r.experts != w.experts:
         raise ValueError("w must hold gate and up of the routing's experts")
@@ -777,10 +787,15 @@ def nvfp4_moe_gate_up(x: NVFP4Tensor, w: NVFP4MoEWeight, routing: MoERouting, ou
         _need(out, torch.bfloat16, "out")
         if out.shape != shape:
             raise ValueError(f"out must have shape {shape}")
+    if workspace is None:
+        workspace = _scratch(nvfp4_moe_gate_up_workspace_bytes(r.tokens, r.top_k, w.experts, w.K), x.codes.device, stream)
+    else:
+        _need(workspace, torch.uint8, "workspace")
     check(lib().nvfp4_moe_gate_up(x.codes.data_ptr(), x.scales.data_ptr(), x.global_scale.data_ptr(), r.tokens, r.top_k,
                                   r.offsets.data_ptr(), r.pairs.data_ptr(), w.packed.data_ptr(),
-                                  w.global_scale.data_ptr(), w.experts, w.N // 2, w.K, out.data_ptr(),
-                                  stream_handle(stream)), "nvfp4_moe_gate_up")
+                                  w.global_scale.data_ptr(), w.experts, w.N // 2, w.K, out.data_ptr(), ptr(workspace),
+                                  workspace.numel() if workspace is not None else 0, stream_handle(stream)),
+          "nvfp4_moe_gate_up")
     return out
 
 
@@ -801,7 +816,7 @@ def nvfp4_moe_down(h: NVFP4Tensor, w: NVFP4MoEWeight, routing: MoERouting, y: to
         if y.shape != shape:
             raise ValueError(f"y must have shape {shape}")
     if workspace is None:
-        workspace = _scratch(int(lib().nvfp4_moe_down_workspace_bytes(r.tokens, r.top_k, w.N)), dev, stream)
+        workspace = _scratch(nvfp4_moe_down_workspace_bytes(r.tokens, r.top_k, w.experts, w.N, w.K), dev, stream)
     else:
         _need(workspace, torch.uint8, "workspace")
     check(lib().nvfp4_moe_down(h.codes.data_ptr(), h.scales.data_ptr(), h.global_scale.data_ptr(), r.tokens, r.top_k,

@@ -26,6 +26,8 @@
 //   PART  (down, many tokens) items as in UP; products go to a workspace [places, N], and a second kernel adds a
 //         token's products with its weights.
 // Nothing here waits for another CTA but at cluster barriers, and no state is left behind.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <string.h>
 
 #include "common.cuh"
@@ -39,48 +41,51 @@ constexpr int kTR = 128;                     // weight rows of a tile: MMA M
 constexpr int kChunk = 256;                  // K of a stage
 constexpr int kWCodes = kTR * 128;           // 16384
 constexpr int kBlock = kWCodes + kTR * 16;   // 18432
-constexpr int kWarps = 10;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kLoaders = 128;                // warps 2-5
-constexpr int kLag = 2;                      // stages whose row copies are in flight behind the one that is issued
+constexpr int kXBlock = 2048;                // scales of 128 places and a chunk, as tcgen05.cp takes them
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kTmemCols = 512;
 
+// The experts that have pairs, as a kernel keeps them: first places, counts, tiles of 128 places before, the offsets as
+// given, sums, experts.
+constexpr int kTableBytes = kMaxExperts * (4 * 4 + 2) + 32;
+
 enum Mode { UP, SUM, PART };
 
-template <int NT, int MODE>
+// NT places to a tile, in halves of 128 at most.  FEW: rows of x by asynchronous copies of the loader warps, and sums of y
+// in shared memory with SUM; else by TMA from rows in the order of the plan.
+template <int NT, int MODE, bool FEW>
 struct Shape {
-  static constexpr int kXCodes = NT * 128;
-  static constexpr int kHalves = NT > 128 ? 2 : 1;                    // of 128 tokens
+  static constexpr int kHalves = NT > 128 ? 2 : 1;
+  static constexpr int kHalf = NT > 128 ? 128 : NT;                   // columns of an accumulator buffer
   static constexpr int kOffX = kBlock;
-  static constexpr int kOffXS = kOffX + kXCodes;
-  static constexpr int kSlot = kOffXS + kHalves * 2048;
+  static constexpr int kOffXS = kOffX + NT * 128;
+  static constexpr int kSlot = kOffXS + kHalves * kXBlock;
   static constexpr int kSums = MODE == SUM ? NT * kTR * 4 : 0;        // y of up to NT tokens
-  static constexpr int kStages = NT == 16 ? 9 : NT == 64 ? (MODE == SUM ? 6 : 7) : NT == 128 ? 6 : 4;
-  static constexpr int kBufs = NT > 128 ? 1 : 2;
-  static constexpr uint32_t kColSF = (uint32_t)(kBufs * NT);          // first scale column
+  static constexpr int kStages = NT == 16 ? 9 : NT == 64 ? (MODE == SUM ? 6 : 7) : 4;
+  static constexpr uint32_t kColSF = 2u * kHalf;                      // first scale column, behind two buffers
   static constexpr uint32_t kSFStage = 16u + 16u * kHalves;           // weights' 4 x 4, tokens' 4 x 4 a half
   static constexpr int kOffSums = kStages * kSlot;
-  static constexpr int kOffTables = kOffSums + kSums;                 // first places, counts, experts
-  static constexpr int kOffBars = kOffTables + kMaxExperts * 10;
+  static constexpr int kOffTables = kOffSums + kSums;
+  static constexpr int kOffBars = kOffTables + kTableBytes;
   static constexpr size_t kBytes = 1024 + kOffBars + (2 * kStages + 4) * 8 + 16;
   static_assert(kColSF + kSFStage * kStages <= kTmemCols, "scale columns must fit the TMEM allocation");
   static_assert(kBytes <= 227 * 1024 && kSlot % 1024 == 0 && kOffX % 1024 == 0, "shared memory");
-  static_assert(kLag < kStages, "a stage must be handed over before the ring comes round");
 };
 
 struct ExpertArgs {
   const uint8_t *xc, *xs;                    // rows of x: codes [.., K/2], scales [.., K/16]
+  const uint8_t* x_blocks;                   // !FEW: scales in kXBlock blocks [tile of 128 places][C]
   const float* xg;
   const uint8_t* w;                          // [experts][RT][C] blocks
   const float* wg;                           // [experts]
   const int32_t *offsets, *pairs;
   const float* weights;                      // SUM
   uint16_t* h;                               // UP: [n_pairs, inter]
-  float* out;                                // SUM: y [tokens, N]; PART: [n_pairs, N]
+  float* out;                                // SUM: y [tokens, N]; PART: [n_pairs, columns of the call]
   int tokens, top, experts, N, K, C, RT;     // N: columns of y, or of h
+  int rt0, rts;                              // row tiles of the call
   int n_pairs;
   int cluster;
 };
@@ -88,15 +93,87 @@ struct ExpertArgs {
 // A stretch of K of one tile: what a pass of the ring's roles works on.
 struct Segment {
   int e, p0, n, rt, c0, nc;                  // expert, first place, places, row tile, first chunk, chunks
+  int block;                                 // first tile of 128 places
 };
 
 // The experts that have pairs, in order.
 struct Table {
-  const int *first, *count;
-  const uint16_t* expert;
-  int used;
+  int *first, *count, *blocks, *offsets;     // blocks: tiles of 128 places of the experts before
+  long long* sums;
+  uint16_t* expert;
+  int used, total;                           // entries; pairs
   long long tiles;                           // stretches of up to NT pairs
+  NVFP4_DEVINL explicit Table(uint8_t* mem) {            // kTableBytes, 16-byte aligned
+    first = reinterpret_cast<int*>(mem);
+    count = first + kMaxExperts;
+    blocks = count + kMaxExperts;
+    offsets = blocks + kMaxExperts;                      // kMaxExperts + 1
+    sums = reinterpret_cast<long long*>(offsets + kMaxExperts + 2);
+    expert = reinterpret_cast<uint16_t*>(sums + 3);
+  }
 };
+
+// Built by the whole CTA; ends with a __syncthreads.
+template <int NT>
+NVFP4_DEVINL void build_table(const ExpertArgs& a, Table& tb) {
+  for (int i = threadIdx.x; i <= a.experts; i += blockDim.x) tb.offsets[i] = __ldcg(a.offsets + i);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    // a lane looks at `per` experts that follow one another
+    const int lane = threadIdx.x, per = (a.experts + 31) / 32;
+    int used = 0, blocks = 0;
+    long long tiles = 0;
+    bool bad = false;
+    auto look = [&](auto take) {
+      for (int i = 0; i < per; ++i) {
+        const int e = lane * per + i;
+        if (e >= a.experts) break;
+        const int f = tb.offsets[e], l = tb.offsets[e + 1];
+        const int lo = min(max(f, 0), a.n_pairs), hi = min(max(l, 0), a.n_pairs);
+        bad = bad || f != lo || l != hi || hi < lo;
+        if (hi > lo) take(e, lo, hi - lo);
+      }
+    };
+    look([&](int, int, int n) {
+      ++used;
+      blocks += (n + 127) / 128;
+      tiles += (n + NT - 1) / NT;
+    });
+    int at = used, before = blocks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, at, o), y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) {
+        at += x;
+        before += y;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+    if (lane == 31) {
+      tb.sums[0] = tiles;
+      tb.sums[1] = at;
+      tb.sums[2] = min(max(tb.offsets[a.experts], 0), a.n_pairs);
+    }
+    at -= used;
+    before -= blocks;
+    look([&](int e, int lo, int n) {
+      tb.first[at] = lo;
+      tb.count[at] = n;
+      tb.blocks[at] = before;
+      tb.expert[at] = (uint16_t)e;
+      ++at;
+      before += (n + 127) / 128;
+    });
+    if (bad && blockIdx.x == 0) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  tb.tiles = tb.sums[0];
+  tb.used = (int)tb.sums[1];
+  tb.total = (int)tb.sums[2];
+}
 
 // Every role walks the CTA's segments by itself, in the same order.
 template <int NT, int MODE>
@@ -115,7 +192,7 @@ struct Walk {
       step = 0;
     } else {
       it = blockIdx.x / a.cluster;
-      end = t.tiles * a.RT;
+      end = t.tiles * a.rts;
       step = gridDim.x / a.cluster;
     }
   }
@@ -134,13 +211,14 @@ struct Walk {
       s.nc = (int)min((long long)(a.C - s.c0), end - it);
       it += s.nc;
     } else {
-      while (it >= base + (long long)(tt = (tb.count[used] + NT - 1) / NT) * a.RT) {
-        base += (long long)tt * a.RT;
+      while (it >= base + (long long)(tt = (tb.count[used] + NT - 1) / NT) * a.rts) {
+        base += (long long)tt * a.rts;
         ++used;
       }
-      const long long in = it - base;        // an expert's items: the tiles of pairs of a row tile follow one another
-      s.rt = (int)(in / tt);
-      t = (int)(in - (long long)s.rt * tt);
+      const int in = (int)(it - base);       // an expert's items: the tiles of pairs of a row tile follow one another
+      s.rt = in / tt;
+      t = in - s.rt * tt;
+      s.rt += a.rt0;
       s.c0 = a.C * rank / a.cluster;
       s.nc = a.C * (rank + 1) / a.cluster - s.c0;
       it += step;
@@ -148,7 +226,22 @@ struct Walk {
     s.e = tb.expert[used];
     s.p0 = tb.first[used] + t * NT;
     s.n = min(NT, tb.count[used] - t * NT);
+    s.block = tb.blocks[used] + t * (NT / 128);
     return true;
+  }
+};
+
+// Which of the two accumulator buffers a segment takes: one in turn, or both (more than 128 places), and how often each has
+// been taken; a role counts along.
+struct Buffers {
+  uint32_t uses0 = 0u, uses1 = 0u;
+  int turn = 0;
+  NVFP4_DEVINL int first(bool both) const { return both ? 0 : turn; }
+  NVFP4_DEVINL uint32_t uses(int buf) const { return buf ? uses1 : uses0; }
+  NVFP4_DEVINL void took(bool both) {
+    uses0 += both || turn == 0;
+    uses1 += both || turn == 1;
+    if (!both) turn ^= 1;
   }
 };
 
@@ -188,174 +281,211 @@ NVFP4_DEVINL float ld_dsmem_f32(uint32_t addr) {
 
 NVFP4_DEVINL float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-template <int NT, int MODE>
-__global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const ExpertArgs a) {
-  using S = Shape<NT, MODE>;
-  constexpr int kS = S::kStages;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float* sums = reinterpret_cast<float*>(smem + S::kOffSums);
-  int* t_first = reinterpret_cast<int*>(smem + S::kOffTables);
-  int* t_count = t_first + kMaxExperts;
-  uint16_t* t_expert = reinterpret_cast<uint16_t*>(t_count + kMaxExperts);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kOffBars);
-  uint64_t* empty = full + kS;
-  uint64_t* acc_full = empty + kS;
-  uint64_t* acc_empty = acc_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
-  __shared__ int s_used, s_total;
-  __shared__ long long s_tiles;
+// 16 columns of the accumulator, even lanes gates and odd lanes ups, to h: 16 bytes a lane, 8 values of one place.
+// Halves of what a lane holds go to the lane whose bit differs, bit by bit: first gates meet ups, then lanes 2, 4 and 8
+// apart trade places for values of h.
+NVFP4_DEVINL void store_h16(const ExpertArgs& a, const Segment& sg, int quad, int m0, const float (&v)[16], float scale) {
+  const int lane = threadIdx.x & 31;
+  const bool odd = lane & 1, b1 = lane & 2, b2 = lane & 4, b3 = lane & 8;
+  float h[8];                                // place 2 j + odd
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float a0 = v[2 * j] * scale, a1 = v[2 * j + 1] * scale;
+    const float other = __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
+    h[j] = odd ? silu_mul(other, a1) : silu_mul(a0, other);
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float keep = b1 ? h[2 * j + 1] : h[2 * j];
+    const float other = __shfl_xor_sync(0xffffffffu, b1 ? h[2 * j] : h[2 * j + 1], 2);
+    const __nv_bfloat162 p = __floats2bfloat162_rn(b1 ? other : keep, b1 ? keep : other);
+    w[j] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  uint32_t x[2][2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t keep = b2 ? w[2 * j + 1] : w[2 * j];
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, b2 ? w[2 * j] : w[2 * j + 1], 4);
+    x[j][0] = b2 ? other : keep;
+    x[j][1] = b2 ? keep : other;
+  }
+  uint32_t o[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) o[j] = __shfl_xor_sync(0xffffffffu, b3 ? x[0][j] : x[1][j], 8);
+  const uint4 out = b3 ? make_uint4(o[0], o[1], x[1][0], x[1][1]) : make_uint4(x[0][0], x[0][1], o[0], o[1]);
+  const int m = m0 + 2 * ((lane >> 1) & 7) + (lane & 1), i = sg.rt * 64 + quad * 16 + 8 * (lane >> 4);
+  if (m < sg.n) *reinterpret_cast<uint4*>(a.h + (size_t)(sg.p0 + m) * a.N + i) = out;
+}
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kS; ++s) {
-      mbar_init(&full[s], 1 + kLoaders / 32);
+// The parts of a kernel that all roles need.
+template <int NT, int MODE, bool FEW>
+struct Smem {
+  using S = Shape<NT, MODE, FEW>;
+  uint8_t* base;
+  uint64_t *full, *empty, *acc_full, *acc_empty;
+  uint32_t* tmem_slot;
+  float* sums;
+  NVFP4_DEVINL explicit Smem(uint8_t* raw) {
+    base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    sums = reinterpret_cast<float*>(base + S::kOffSums);
+    full = reinterpret_cast<uint64_t*>(base + S::kOffBars);
+    empty = full + S::kStages;
+    acc_full = empty + S::kStages;
+    acc_empty = acc_full + 2;
+    tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  }
+  NVFP4_DEVINL Table table() const { return Table(base + S::kOffTables); }
+  // By the first thread; `arrivals`: on a stage, `readers`: warps that read an accumulator.
+  NVFP4_DEVINL void init_barriers(int arrivals, int readers) const {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full[s], arrivals);
       mbar_init(&empty[s], 1);
     }
     for (int d = 0; d < 2; ++d) {
       mbar_init(&acc_full[d], 1);
-      mbar_init(&acc_empty[d], 4);
+      mbar_init(&acc_empty[d], readers);
     }
     fence_mbar_init();
   }
-  if (warp == 1) {
+  // By warp 1.
+  NVFP4_DEVINL void alloc_tmem() const {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(kTmemCols));
+                 "r"(kTmemCols)
+                 : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  static NVFP4_DEVINL void free_tmem(uint32_t tmem) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+  }
+};
+
+// The weight blocks of the CTA's segments, by one thread.
+template <int NT, int MODE, bool FEW>
+NVFP4_DEVINL void copy_weights(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, Walk<NT, MODE> walk) {
+  using S = Shape<NT, MODE, FEW>;
+  constexpr int kS = S::kStages;
+  Segment sg;
+  int s = 0, k = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  while (ok && walk.next(sg)) {
+    const uint8_t* src = a.w + (((size_t)sg.e * a.RT + sg.rt) * a.C + sg.c0) * kBlock;
+    for (int c = 0; c < sg.nc; ++c, src += kBlock) {
+      if (k >= kS && !mbar_wait(&sm.empty[s], phase ^ 1u)) {
+        ok = false;
+        break;
+      }
+      mbar_arrive_expect_tx(&sm.full[s], kBlock);
+      bulk_g2s(sm.base + s * S::kSlot, src, kBlock, &sm.full[s]);
+      ++k;
+      if (++s == kS) { s = 0; phase ^= 1u; }
+    }
+  }
+  // Not to leave with copies in flight: the last ones' waits (bounded; on the normal path long over).
+  for (int j = k > kS ? k - kS : 0; j < k; ++j) mbar_wait(&sm.full[j % kS], (j / kS) & 1);
+}
+
+// Scales to TMEM and products, by one warp.  It waits together; one lane then issues a stage's copies, products and commit
+// in one branch, with the others held at its end.  (Predicated one by one, with the other lanes free to run ahead, they
+// faulted once several stages were ready: operands are in uniform registers, which the lanes that run ahead overwrite.)
+template <int NT, int MODE, bool FEW>
+NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, Walk<NT, MODE> walk, uint32_t tmem) {
+  using S = Shape<NT, MODE, FEW>;
+  constexpr int kS = S::kStages;
+  const bool lead = elect_one() != 0u;
+  const uint32_t base = smem_u32(sm.base);
+  Segment sg;
+  Buffers bufs;
+  int s = 0, k = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  while (ok && walk.next(sg)) {
+    const bool both = S::kHalves == 2 && sg.n > 128;
+    const int buf = bufs.first(both);
+    if (bufs.uses(buf) > 0 && !mbar_wait_warp(&sm.acc_empty[buf], (bufs.uses(buf) - 1) & 1)) break;
+    if (both && bufs.uses1 > 0 && !mbar_wait_warp(&sm.acc_empty[1], (bufs.uses1 - 1) & 1)) break;
+    bufs.took(both);
+    for (int c = 0; c < sg.nc; ++c) {
+      if (!mbar_wait_warp(&sm.full[s], phase)) {
+        ok = false;
+        break;
+      }
+      if (lead) {
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf * S::kHalf), slot = base + (uint32_t)(s * S::kSlot);
+        const uint64_t da = smem_desc_sw128(slot), db = smem_desc_sw128(slot + S::kOffX);
+        const uint64_t dwa = smem_desc_rows16(slot + kWCodes), dxa = smem_desc_rows16(slot + S::kOffXS);
+        const uint32_t sfa = tmem + S::kColSF + S::kSFStage * (uint32_t)s, sfb = sfa + 16u;
+        const uint32_t idesc = idesc_for(sg.n);          // of the first 128 places; the others are another MMA's
+        const int mmas = min(4, (a.K - (sg.c0 + c) * kChunk) / 64);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < mmas) {
+            copy_scales(sfa + 4u * q, dwa + (uint64_t)(32 * q));
+            copy_scales(sfb + 4u * S::kHalves * q, dxa + (uint64_t)(32 * q));
+            if (both) copy_scales(sfb + 8u * q + 4u, dxa + (uint64_t)(128 + 32 * q));
+          }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < mmas) {
+            const uint32_t acc = c > 0 || q > 0 ? 1u : 0u;
+            mma_mxf4nvf4(d, da + 2 * q, db + 2 * q, idesc, sfa + 4u * q, sfb + 4u * S::kHalves * q, acc);
+            if (both)
+              mma_mxf4nvf4(d + 128u, da + 2 * q, db + (uint64_t)(128 * 128 / 16 + 2 * q), idesc_for(sg.n - 128),
+                           sfa + 4u * q, sfb + 8u * q + 4u, acc);
+          }
+        mma_commit(&sm.empty[s]);
+        if (c == sg.nc - 1) {
+          mma_commit(&sm.acc_full[buf]);
+          if (both) mma_commit(&sm.acc_full[1]);
+        }
+      }
+      __syncwarp();
+      ++k;
+      if (++s == kS) { s = 0; phase ^= 1u; }
+    }
+  }
+  if (k > 0) mbar_wait_warp(&sm.empty[(k - 1) % kS], ((k - 1) / kS) & 1);   // not to leave with MMAs in flight
+}
+
+extern __shared__ __align__(1024) uint8_t smem_raw[];
+
+// ---- few tokens: UP, SUM ------------------------------------------------------------
+constexpr int kFewWarps = 10;
+constexpr int kFewThreads = 32 * kFewWarps;
+constexpr int kLoaders = 128;                // warps 2-5
+constexpr int kLag = 2;                      // stages whose row copies are in flight behind the one that is issued
+
+template <int NT, int MODE>
+__global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const ExpertArgs a) {
+  using S = Shape<NT, MODE, true>;
+  constexpr int kS = S::kStages;
+  static_assert(S::kHalves == 1 && kLag < kS, "one buffer a segment; a stage is handed over before the ring comes round");
+  const Smem<NT, MODE, true> sm(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) sm.init_barriers(1 + kLoaders / 32, 4);
+  if (warp == 1) sm.alloc_tmem();
   griddep_launch_dependents();
   griddep_wait();                            // the plan comes from a preceding kernel
-  if (warp == 0) {
-    // the experts that have pairs: a lane looks at `per` experts that follow one another
-    const int per = (a.experts + 31) / 32;
-    int used = 0;
-    long long tiles = 0;
-    bool bad = false;
-    auto look = [&](auto take) {
-      for (int i = 0; i < per; ++i) {
-        const int e = lane * per + i;
-        if (e >= a.experts) break;
-        const int f = __ldcg(a.offsets + e), l = __ldcg(a.offsets + e + 1);
-        const int lo = min(max(f, 0), a.n_pairs), hi = min(max(l, 0), a.n_pairs);
-        bad = bad || f != lo || l != hi || hi < lo;
-        if (hi > lo) take(e, lo, hi - lo);
-      }
-    };
-    look([&](int, int, int n) {
-      ++used;
-      tiles += (n + NT - 1) / NT;
-    });
-    int at = used;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, at, o);
-      if (lane >= o) at += x;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-    if (lane == 31) {
-      s_used = at;
-      s_tiles = tiles;
-      s_total = min(max(__ldcg(a.offsets + a.experts), 0), a.n_pairs);
-    }
-    at -= used;
-    look([&](int e, int lo, int n) {
-      t_first[at] = lo;
-      t_count[at] = n;
-      t_expert[at] = (uint16_t)e;
-      ++at;
-    });
-    if (bad) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const Table tb = {t_first, t_count, t_expert, s_used, s_tiles};
+  Table tb = sm.table();
+  build_table<NT>(a, tb);
+  const uint32_t tmem = *sm.tmem_slot;
   Walk<NT, MODE> walk(tb, a);
   Segment sg;
 
   if (MODE == UP) {
     // rows of no pair are zero: one scale over all rows is taken of h
     const size_t per = (size_t)a.N / 8, end = (size_t)a.n_pairs * per;
-    for (size_t i = s_total * per + blockIdx.x * kThreads + threadIdx.x; i < end; i += (size_t)gridDim.x * kThreads)
+    for (size_t i = tb.total * per + blockIdx.x * kFewThreads + threadIdx.x; i < end; i += (size_t)gridDim.x * kFewThreads)
       reinterpret_cast<uint4*>(a.h)[i] = make_uint4(0u, 0u, 0u, 0u);
   }
+  __syncwarp();
 
   if (warp == 0) {
-    // ---------------- weight blocks ----------------
-    if (lane == 0) {
-      int s = 0, k = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      while (ok && walk.next(sg)) {
-        const uint8_t* src = a.w + (((size_t)sg.e * a.RT + sg.rt) * a.C + sg.c0) * kBlock;
-        for (int c = 0; c < sg.nc; ++c, src += kBlock) {
-          if (k >= kS && !mbar_wait(&empty[s], phase ^ 1u)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&full[s], kBlock);
-          bulk_g2s(smem + s * S::kSlot, src, kBlock, &full[s]);
-          ++k;
-          if (++s == kS) { s = 0; phase ^= 1u; }
-        }
-      }
-      // Not to leave with copies in flight: the last ones' waits (bounded; on the normal path long over).
-      for (int j = k > kS ? k - kS : 0; j < k; ++j) mbar_wait(&full[j % kS], (j / kS) & 1);
-    }
+    if (lane == 0) copy_weights(sm, a, walk);
   } else if (warp == 1) {
-    // ---------------- scales and products ----------------
-    // The warp waits together; one lane then issues a stage's copies, products and commit in one branch, with the others
-    // held at its end.  (Predicated one by one, with the other lanes free to run ahead, they faulted once several stages
-    // were ready: operands are in uniform registers, which the lanes that run ahead overwrite.)
-    const bool lead = elect_one() != 0u;
-    const uint32_t base = smem_u32(smem);
-    int s = 0, k = 0, seg = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    while (ok && walk.next(sg)) {
-      const int buf = seg % S::kBufs;
-      if (seg >= S::kBufs && !mbar_wait_warp(&acc_empty[buf], (seg / S::kBufs - 1) & 1)) break;
-      for (int c = 0; c < sg.nc; ++c) {
-        if (!mbar_wait_warp(&full[s], phase)) {
-          ok = false;
-          break;
-        }
-        if (lead) {
-          tc_fence_after();
-          const uint32_t d = tmem + (uint32_t)(buf * NT), slot = base + (uint32_t)(s * S::kSlot);
-          const uint64_t da = smem_desc_sw128(slot), db = smem_desc_sw128(slot + S::kOffX);
-          const uint64_t dwa = smem_desc_rows16(slot + kWCodes), dxa = smem_desc_rows16(slot + S::kOffXS);
-          const uint32_t sfa = tmem + S::kColSF + S::kSFStage * (uint32_t)s, sfb = sfa + 16u;
-          const uint32_t idesc = idesc_for(sg.n);          // of the first 128 places; the others are another MMA's
-          const int mmas = min(4, (a.K - (sg.c0 + c) * kChunk) / 64);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (q < mmas) {
-              copy_scales(sfa + 4u * q, dwa + (uint64_t)(32 * q));
-              copy_scales(sfb + 4u * S::kHalves * q, dxa + (uint64_t)(32 * q));
-              if (S::kHalves == 2 && sg.n > 128) copy_scales(sfb + 8u * q + 4u, dxa + (uint64_t)(128 + 32 * q));
-            }
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (q < mmas) {
-              const uint32_t acc = c > 0 || q > 0 ? 1u : 0u;
-              mma_mxf4nvf4(d, da + 2 * q, db + 2 * q, idesc, sfa + 4u * q, sfb + 4u * S::kHalves * q, acc);
-              if (S::kHalves == 2 && sg.n > 128)
-                mma_mxf4nvf4(d + 128u, da + 2 * q, db + (uint64_t)(128 * 128 / 16 + 2 * q), idesc_for(sg.n - 128),
-                             sfa + 4u * q, sfb + 8u * q + 4u, acc);
-            }
-          mma_commit(&empty[s]);
-          if (c == sg.nc - 1) mma_commit(&acc_full[buf]);
-        }
-        __syncwarp();
-        ++k;
-        if (++s == kS) { s = 0; phase ^= 1u; }
-      }
-      ++seg;
-    }
-    if (k > 0) mbar_wait_warp(&empty[(k - 1) % kS], ((k - 1) / kS) & 1);   // not to leave with MMAs in flight
+    multiply(sm, a, walk, tmem);
   } else if (warp < 6) {
     // ---------------- rows of x ----------------
     const int lt = threadIdx.x - 64;
@@ -367,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const ExpertAr
     auto hand_over = [&](int j) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[j % kS]);
+      if (lane == 0) mbar_arrive(&sm.full[j % kS]);
     };
     // the row of x at a place (the lowest one for a place of no pair)
     auto row_at = [&](int place) {
@@ -387,11 +517,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const ExpertAr
 #pragma unroll
       for (int i = 0; i < kRS; ++i) row_s[i] = rs + 32 * i < sg.n ? row_at(sg.p0 + rs + 32 * i) : -1;
       for (int c = sg.c0; c < sg.c0 + sg.nc; ++c) {
-        if (k >= kS && !mbar_wait_warp(&empty[s], phase ^ 1u)) {
+        if (k >= kS && !mbar_wait_warp(&sm.empty[s], phase ^ 1u)) {
           ok = false;
           break;
         }
-        const uint32_t slot = smem_u32(smem) + (uint32_t)(s * S::kSlot);
+        const uint32_t slot = smem_u32(sm.base) + (uint32_t)(s * S::kSlot);
         if (c * 128 + piece * 16 < (int)row_codes) {
           const uint32_t dst = slot + S::kOffX + rc * 128 + ((piece ^ (rc & 7)) << 4);     // (16 i does not move the swizzle)
           const uint8_t* src = a.xc + c * 128 + piece * 16;
@@ -400,11 +530,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const ExpertAr
             if (row_c[i] >= 0) async_copy16(dst + 2048 * i, src + row_c[i] * row_codes);
         }
         if (c * 16 + q * 4 < (int)row_scales) {
-          const uint32_t dst = slot + S::kOffXS + q * 512 + rs * 16;                         // row rs + 32 i: word i % 4
+          const uint32_t dst = slot + S::kOffXS + q * 512 + rs * 16;                         // row rs + 32 i: word i
           const uint8_t* src = a.xs + c * 16 + q * 4;
 #pragma unroll
           for (int i = 0; i < kRS; ++i)
-            if (row_s[i] >= 0) async_copy4(dst + (i / 4) * 2048 + (i % 4) * 4, src + row_s[i] * row_scales);
+            if (row_s[i] >= 0) async_copy4(dst + i * 4, src + row_s[i] * row_scales);
         }
         async_commit();
         if (k >= kLag) {
@@ -422,74 +552,92 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const ExpertAr
     const int p = warp & 3, row = p * 32 + lane;
     const float xg = __ldcg(a.xg);
     if (MODE == SUM)
-      for (int t = 0; t < a.tokens; ++t) sums[t * kTR + row] = 0.0f;
-    int seg = 0;
-    while (walk.next(sg)) {
-      const int buf = seg % S::kBufs;
-      const float scale = __fmul_rn(xg, __ldcg(a.wg + sg.e));
-      if (!mbar_wait_warp(&acc_full[buf], (seg / S::kBufs) & 1)) break;
+      for (int t = 0; t < a.tokens; ++t) sm.sums[t * kTR + row] = 0.0f;
+    Buffers bufs;
+    // The pairs of a segment's places lane, lane + 32 and their weights are read a segment ahead.
+    constexpr int kCols = (NT + 31) / 32;
+    auto load_pairs = [&](int (&pair)[kCols]) {
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        const int m = lane + 32 * i;
+        pair[i] = m < sg.n ? __ldcg(a.pairs + sg.p0 + m) : 0;
+        if (pair[i] < 0 || pair[i] >= a.n_pairs) {
+          if (p == 0) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
+          pair[i] = -1;
+        }
+      }
+    };
+    int pair[kCols], next_pair[kCols];
+    float wgt[kCols];
+    bool more = walk.next(sg);
+    float wg = more ? __ldcg(a.wg + sg.e) : 0.0f;
+    if (MODE == SUM && more) {
+      load_pairs(pair);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) wgt[i] = pair[i] >= 0 ? __ldcg(a.weights + pair[i]) : 0.0f;
+    }
+    while (more) {
+      const Segment cur = sg;
+      const float scale = __fmul_rn(xg, wg);
+      more = walk.next(sg);
+      if (more) wg = __ldcg(a.wg + sg.e);
+      if (MODE == SUM && more) load_pairs(next_pair);
+      const int buf = bufs.first(false);
+      if (!mbar_wait_warp(&sm.acc_full[buf], bufs.uses(buf) & 1)) break;
       tc_fence_after();
-      const uint32_t d = tmem + ((uint32_t)(p * 32) << 16) + (uint32_t)(buf * NT);
-      for (int m0 = 0; m0 < sg.n; m0 += 16) {
+      bufs.took(false);
+      const uint32_t d = tmem + ((uint32_t)(p * 32) << 16) + (uint32_t)(buf * S::kHalf);
+#pragma unroll 1
+      for (int m0 = 0; m0 < cur.n; m0 += 16) {
         float v[16];
         __syncwarp();
         read16(d + (uint32_t)m0, v);
         if (MODE == UP && a.cluster > 1) {
           // raw sums to the ring's memory (free: every MMA of the CTA's one item is done)
-          float* stage = reinterpret_cast<float*>(smem);
+          float* stage = reinterpret_cast<float*>(sm.base);
 #pragma unroll
           for (int i = 0; i < 16; ++i) stage[(m0 + i) * kTR + row] = v[i];
         } else if (MODE == UP) {
-          // even lanes hold gates, odd ones ups: an even lane takes the even places of h row `row / 2`, an odd one the others
-          const int i = sg.rt * 64 + row / 2;
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float a0 = v[j] * scale, a1 = v[j + 1] * scale;
-            const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a0 : a1, 1);
-            const float hv = lane & 1 ? silu_mul(other, a1) : silu_mul(a0, other);
-            const int m = m0 + j + (lane & 1);
-            if (m < sg.n && i < a.N)
-              a.h[(size_t)(sg.p0 + m) * a.N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(hv));
-          }
-        } else if (MODE == SUM) {
-          int pair[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) pair[i] = m0 + i < sg.n ? __ldcg(a.pairs + sg.p0 + m0 + i) : -1;
+          store_h16(a, cur, p, m0, v, scale);
+        } else {
+          const int at = m0 >> 5, l0 = m0 & 31;
+          int pr = pair[0];
+          float wt = wgt[0];
+          if (kCols > 1 && at == 1) pr = pair[kCols - 1], wt = wgt[kCols - 1];
+          const int t_lane = pr >= 0 ? pr / a.top : -1;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (m0 + i >= sg.n) continue;
-            if (pair[i] < 0 || pair[i] >= a.n_pairs) {
-              if (row == 0) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
-              continue;
+            const int t = __shfl_sync(0xffffffffu, t_lane, l0 + i);
+            const float w = __shfl_sync(0xffffffffu, wt, l0 + i);
+            if (m0 + i < cur.n && t >= 0) {
+              float* y = &sm.sums[t * kTR + row];
+              *y = fmaf(w, v[i] * scale, *y);
             }
-            float* y = &sums[pair[i] / a.top * kTR + row];
-            *y = fmaf(__ldcg(a.weights + pair[i]), v[i] * scale, *y);
-          }
-        } else {
-          const int n = sg.rt * kTR + row;
-          if (n < a.N) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (m0 + i < sg.n) a.out[(size_t)(sg.p0 + m0 + i) * a.N + n] = v[i] * scale;
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
-      ++seg;
+      if (lane == 0) mbar_arrive(&sm.acc_empty[buf]);
+      if (MODE == SUM && more) {
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+          pair[i] = next_pair[i];
+          wgt[i] = pair[i] >= 0 ? __ldcg(a.weights + pair[i]) : 0.0f;
+        }
+      }
     }
   }
 
   // ---------------- the cluster's parts ----------------
   __syncwarp();
-  if (MODE != PART && a.cluster > 1) cluster_sync();
+  if (a.cluster > 1) cluster_sync();
   if (MODE == SUM && warp >= 6) {
     const int row = (warp & 3) * 32 + lane, n = blockIdx.x / a.cluster * kTR + row;
     for (int t = walk.rank; t < a.tokens; t += a.cluster) {
       float y = 0.0f;
       for (int r = 0; r < a.cluster; ++r)                       // in the order of the ranks
-        y += r == walk.rank ? sums[t * kTR + row] : ld_dsmem_f32(dsmem_addr(&sums[t * kTR + row], (uint32_t)r));
+        y += r == walk.rank ? sm.sums[t * kTR + row] : ld_dsmem_f32(dsmem_addr(&sm.sums[t * kTR + row], (uint32_t)r));
       if (n < a.N) a.out[(size_t)t * a.N + n] = y;
     }
   }
@@ -499,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const ExpertAr
     if (again.next(sg)) {
       const int row = (warp & 3) * 32 + lane, i = sg.rt * 64 + row / 2;
       const float scale = __fmul_rn(__ldcg(a.xg), __ldcg(a.wg + sg.e));
-      const float* stage = reinterpret_cast<const float*>(smem);
+      const float* stage = reinterpret_cast<const float*>(sm.base);
       for (int m = walk.rank; m < sg.n; m += a.cluster) {
         float v = 0.0f;
         for (int r = 0; r < a.cluster; ++r) v += ld_dsmem_f32(dsmem_addr(&stage[m * kTR + row], (uint32_t)r));
@@ -512,28 +660,197 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const ExpertAr
   }
   tc_fence_before();
   __syncwarp();
-  if (MODE != PART && a.cluster > 1) cluster_sync();              // (the others have read this CTA's memory)
+  if (a.cluster > 1) cluster_sync();                              // (the others have read this CTA's memory)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    sm.free_tmem(tmem);
+  }
+}
+
+// ---- many tokens: UP, PART -----------------------------------------------------------
+constexpr int kManyWarps = 12;               // 0 weights, 1 products, 2 rows of x, 4-11 the accumulator
+constexpr int kManyThreads = 32 * kManyWarps;
+constexpr int kBoxRows = 32;                 // rows of x of a copy
+
+template <int NT, int MODE>
+__global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_constant__ CUtensorMap tm_x,
+                                                                   const ExpertArgs a) {
+  using S = Shape<NT, MODE, false>;
+  constexpr int kS = S::kStages;
+  const Smem<NT, MODE, false> sm(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tm_x);
+    sm.init_barriers(2, 8);
+  }
+  if (warp == 1) sm.alloc_tmem();
+  griddep_launch_dependents();
+  griddep_wait();
+  Table tb = sm.table();
+  build_table<NT>(a, tb);
+  const uint32_t tmem = *sm.tmem_slot;
+  Walk<NT, MODE> walk(tb, a);
+  Segment sg;
+  if (MODE == UP) {
+    const size_t per = (size_t)a.N / 8, end = (size_t)a.n_pairs * per;
+    for (size_t i = tb.total * per + blockIdx.x * kManyThreads + threadIdx.x; i < end; i += (size_t)gridDim.x * kManyThreads)
+      reinterpret_cast<uint4*>(a.h)[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __syncwarp();
+
+  if (warp == 0) {
+    if (lane == 0) copy_weights(sm, a, walk);
+  } else if (warp == 1) {
+    multiply(sm, a, walk, tmem);
+  } else if (warp == 2) {
+    // ---------------- rows of x, in the order of the plan, and their scales ----------------
+    if (lane == 0) {
+      int s = 0, k = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      while (ok && walk.next(sg)) {
+        const int boxes = (sg.n + kBoxRows - 1) / kBoxRows, halves = (sg.n + 127) / 128;
+        for (int c = 0; c < sg.nc; ++c) {
+          if (k >= kS && !mbar_wait(&sm.empty[s], phase ^ 1u)) {
+            ok = false;
+            break;
+          }
+          uint8_t* slot = sm.base + s * S::kSlot;
+          mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(boxes * kBoxRows * 128 + halves * kXBlock));
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(slot + S::kOffX + b * (kBoxRows * 128), &tm_x, (sg.c0 + c) * 128, sg.p0 + b * kBoxRows, &sm.full[s]);
+          for (int h = 0; h < halves; ++h)
+            bulk_g2s(slot + S::kOffXS + h * kXBlock, a.x_blocks + ((size_t)(sg.block + h) * a.C + sg.c0 + c) * kXBlock,
+                     kXBlock, &sm.full[s]);
+          ++k;
+          if (++s == kS) { s = 0; phase ^= 1u; }
+        }
+      }
+      for (int j = k > kS ? k - kS : 0; j < k; ++j) mbar_wait(&sm.full[j % kS], (j / kS) & 1);
+    }
+  } else if (warp >= 4) {
+    // ---------------- the accumulator: two warps a lane quadrant, 16 columns in turn ----------------
+    const int p = warp & 3, row = p * 32 + lane, part = (warp - 4) >> 2;
+    const float xg = __ldcg(a.xg);
+    Buffers bufs;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const float scale = __fmul_rn(xg, __ldcg(a.wg + sg.e));
+      const bool both = S::kHalves == 2 && sg.n > 128;
+      const int halves = both ? 2 : 1;
+#pragma unroll 1
+      for (int half = 0; half < halves; ++half) {
+        const int buf = both ? half : bufs.first(false);
+        if (!mbar_wait_warp(&sm.acc_full[buf], bufs.uses(buf) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + ((uint32_t)(p * 32) << 16) + (uint32_t)(buf * S::kHalf);
+        const int end = min(sg.n - half * 128, S::kHalf);
+#pragma unroll 1
+        for (int m0 = 16 * part; m0 < end; m0 += 32) {
+          float v[16];
+          __syncwarp();
+          read16(d + (uint32_t)m0, v);
+          if (MODE == UP) {
+            store_h16(a, sg, p, half * 128 + m0, v, scale);
+          } else {
+            const int n = (sg.rt - a.rt0) * kTR + row, m = half * 128 + m0;
+            float* dst = a.out + (size_t)(sg.p0 + m) * (a.rts * kTR) + n;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (m + i < sg.n) dst[(size_t)i * (a.rts * kTR)] = v[i] * scale;
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.acc_empty[buf]);
+      }
+      bufs.took(both);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    sm.free_tmem(tmem);
+  }
+}
+
+// Rows of x in the order of the plan, and their scales in blocks of 128 places and 256 of K: a CTA a tile of 128 places of
+// an expert and kArrangeChunks chunks.  codes NULL: the rows stand so already (down), only the scales are laid out.
+struct ArrangeArgs {
+  ExpertArgs x;
+  uint8_t *codes, *blocks;
+};
+constexpr int kArrangeThreads = 256;
+constexpr int kArrangeChunks = 4;
+
+__global__ void __launch_bounds__(kArrangeThreads) moe_arrange_kernel(const ArrangeArgs g) {
+  __shared__ __align__(16) uint8_t s_table[kTableBytes];
+  __shared__ int s_row[128];
+  griddep_launch_dependents();
+  griddep_wait();
+  const ExpertArgs& a = g.x;
+  Table tb(s_table);
+  build_table<128>(a, tb);
+  if ((long long)blockIdx.x >= tb.tiles) return;
+  int used = 0;                              // the last entry whose tiles begin at blockIdx.x or before
+  for (int hi = tb.used; hi - used > 1;) {
+    const int mid = (used + hi) >> 1;
+    if (tb.blocks[mid] <= (int)blockIdx.x) used = mid; else hi = mid;
+  }
+  const int in = blockIdx.x - tb.blocks[used], p0 = tb.first[used] + 128 * in, n = min(128, tb.count[used] - 128 * in);
+  for (int r = threadIdx.x; r < n; r += kArrangeThreads) {
+    int row = p0 + r;
+    if (g.codes) {
+      const int pair = __ldcg(a.pairs + row);
+      const bool there = pair >= 0 && pair < a.n_pairs;
+      if (!there) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
+      row = there ? pair / a.top : 0;
+    }
+    s_row[r] = row;
+  }
+  __syncthreads();
+  const int c0 = blockIdx.y * kArrangeChunks, c1 = min(a.C, c0 + kArrangeChunks);
+  const int row_codes = a.K / 2, row_scales = a.K / 16;
+  // scales: word q of chunk c of rows i, i + 32, i + 64, i + 96 in 16 bytes
+  for (int x = threadIdx.x; x < (c1 - c0) * 128; x += kArrangeThreads) {
+    const int c = c0 + (x >> 7), q = (x >> 5) & 3, i = x & 31, at = c * 16 + q * 4;
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      if (i + 32 * p < n && at < row_scales)
+        w[p] = __ldcg(reinterpret_cast<const uint32_t*>(a.xs + (size_t)s_row[i + 32 * p] * row_scales + at));
+    *reinterpret_cast<uint4*>(g.blocks + ((size_t)blockIdx.x * a.C + c) * kXBlock + q * 512 + i * 16) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (!g.codes) return;
+  const int b0 = c0 * 128, pieces = (min(row_codes, c1 * 128) - b0) / 16;
+  for (int x = threadIdx.x; x < n * pieces; x += kArrangeThreads) {
+    const int r = x / pieces, at = b0 + (x - r * pieces) * 16;
+    *reinterpret_cast<uint4*>(g.codes + (size_t)(p0 + r) * row_codes + at) =
+        __ldcg(reinterpret_cast<const uint4*>(a.xc + (size_t)s_row[r] * row_codes + at));
   }
 }
 
 // y[t, n] = sum_j weights[t, j] part[places[t, j], n], in the order of j: a thread has V columns of a token.
 struct CombineArgs {
-  const float *part, *weights;
+  const float *part, *weights;               // part: [n_pairs, ld], columns [n0, n1) of y
   const int32_t* places;
   float* y;
-  int tokens, top, N, n_pairs;
+  int tokens, top, N, n_pairs, n0, n1, ld;
 };
 
 template <int V>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  const int n = (blockIdx.x * 256 + threadIdx.x) * V;
-  if (n >= a.N) return;
+  const int n = a.n0 + (blockIdx.x * 256 + threadIdx.x) * V;
+  if (n >= a.n1) return;
   for (int t = blockIdx.y; t < a.tokens; t += gridDim.y) {
     float y[V] = {};
 #pragma unroll 4
@@ -544,7 +861,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
         continue;
       }
       const float w = __ldcg(a.weights + (size_t)t * a.top + j);
-      const float* src = a.part + (size_t)place * a.N + n;
+      const float* src = a.part + (size_t)place * a.ld + (n - a.n0);
       if constexpr (V == 4) {
         const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
         y[0] = fmaf(w, x.x, y[0]);
@@ -615,8 +932,9 @@ int device_sms() {
   return n > 0 ? n : 152;
 }
 
-template <class Args>
-cudaError_t launch(void (*kern)(Args), dim3 grid, int threads, size_t smem, int cluster, const Args& a, cudaStream_t stream) {
+template <class... Args>
+cudaError_t launch(void (*kern)(Args...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                   const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
@@ -631,53 +949,79 @@ cudaError_t launch(void (*kern)(Args), dim3 grid, int threads, size_t smem, int 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Allows a kernel its dynamic shared memory, once a device.
+template <auto KERNEL>
+cudaError_t allow_smem(size_t bytes) {
+  static PerDeviceInt done;
+  cudaError_t err = cudaSuccess;
+  done.get([bytes](int, cudaError_t* e) -> int {
+    *e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    return *e == cudaSuccess ? 1 : 0;
+  }, &err);
+  return err;
 }
 
 template <int NT, int MODE>
-cudaError_t run(int grid, const ExpertArgs& a, cudaStream_t stream) {
-  static PerDeviceInt done;
-  cudaError_t err = cudaSuccess;
-  done.get([](int, cudaError_t* e) -> int {
-    *e = cudaFuncSetAttribute(moe_experts_kernel<NT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)Shape<NT, MODE>::kBytes);
-    return *e == cudaSuccess ? 1 : 0;
-  }, &err);
-  if (err != cudaSuccess) return err;
-  return launch(moe_experts_kernel<NT, MODE>, dim3((unsigned)grid), kThreads, Shape<NT, MODE>::kBytes, a.cluster, a, stream);
+cudaError_t run_few(long long grid, const ExpertArgs& a, cudaStream_t stream) {
+  constexpr size_t bytes = Shape<NT, MODE, true>::kBytes;
+  const cudaError_t e = allow_smem<moe_few_kernel<NT, MODE>>(bytes);
+  if (e != cudaSuccess) return e;
+  return launch(moe_few_kernel<NT, MODE>, dim3((unsigned)grid), kFewThreads, bytes, a.cluster, stream, a);
 }
 
-// Tokens up to which y is summed in shared memory.
-constexpr int kSumTokens = 64;
+template <int NT, int MODE>
+cudaError_t run_many(long long grid, const CUtensorMap& map, const ExpertArgs& a, cudaStream_t stream) {
+  constexpr size_t bytes = Shape<NT, MODE, false>::kBytes;
+  const cudaError_t e = allow_smem<moe_many_kernel<NT, MODE>>(bytes);
+  if (e != cudaSuccess) return e;
+  return launch(moe_many_kernel<NT, MODE>, dim3((unsigned)grid), kManyThreads, bytes, 1, stream, map, a);
+}
+
+// Tokens up to which y is summed in shared memory and x comes by the loaders.
+constexpr int kFewTokens = 64;
+
+long long used_experts(const ExpertArgs& a) { return a.n_pairs < a.experts ? a.n_pairs : a.experts; }
 
 // Most stretches of up to nt pairs that any plan of the pairs has.
 long long most_tiles(const ExpertArgs& a, int nt) {
-  const long long used = a.n_pairs < a.experts ? a.n_pairs : a.experts;
+  const long long used = used_experts(a);
   return used + (a.n_pairs - used) / nt;
 }
 
-// Places of a tile: an expert of few tokens has few places; of many tokens, about the mean.
-int tile_for(const ExpertArgs& a) {
-  const long long used = a.n_pairs < a.experts ? a.n_pairs : a.experts;
-  const long long mean = used > 0 ? a.n_pairs / used : 0;
-  if (a.tokens <= 16) return 16;
-  if (a.tokens <= 64 || mean <= 24) return 64;
-  return mean <= 64 ? 128 : 256;
+// Places of a tile, many tokens: about the mean's double, so that most experts have one tile.
+int tile_for(const ExpertArgs& a) { return a.n_pairs <= 24 * used_experts(a) ? 64 : 256; }
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+size_t codes_bytes(const ExpertArgs& a) { return align256((size_t)a.n_pairs * a.K / 2); }
+size_t blocks_bytes(const ExpertArgs& a) { return align256((size_t)most_tiles(a, 128) * a.C * kXBlock); }
+
+}  // namespace
+
+// Defined in gemv.cu.
+bool nvfp4_internal_encode_2d(CUtensorMap* map, const void* base, uint64_t inner_bytes, uint64_t rows,
+                              uint32_t box_inner, uint32_t box_rows, bool swizzle128);
+
+namespace {
+
+// Rows of x by place (codes: where they go, NULL: they stand so) and their scales' blocks, and the map of the rows.
+cudaError_t arrange(const ExpertArgs& a, uint8_t* codes, uint8_t* blocks, CUtensorMap* map, cudaStream_t stream) {
+  memset(map, 0, sizeof(*map));
+  if (!nvfp4_internal_encode_2d(map, codes ? codes : a.xc, (uint64_t)a.K / 2, (uint64_t)a.n_pairs, 128, kBoxRows, true))
+    return cudaErrorInvalidValue;
+  ArrangeArgs g = {a, codes, blocks};
+  const dim3 grid((unsigned)most_tiles(a, 128), (unsigned)((a.C + kArrangeChunks - 1) / kArrangeChunks));
+  return launch(moe_arrange_kernel, grid, kArrangeThreads, 0, 1, stream, g);
 }
 
-cudaError_t run_items(bool up, ExpertArgs a, cudaStream_t stream) {
-  const int nt = tile_for(a), sms = device_sms();
-  const long long items = most_tiles(a, nt) * a.RT;
-  a.cluster = 1;
-  if (up)
-    while (a.cluster < kMaxCluster && items * a.cluster * 2 <= sms && a.C >= a.cluster * 2) a.cluster *= 2;
-  long long grid = items * a.cluster;
-  if (grid > sms) grid = sms;
-  if (grid < 1) grid = 1;
-  if (up) return nt == 16 ? run<16, UP>(grid, a, stream) : nt == 64 ? run<64, UP>(grid, a, stream)
-                 : nt == 128 ? run<128, UP>(grid, a, stream) : run<256, UP>(grid, a, stream);
-  return nt == 16 ? run<16, PART>(grid, a, stream) : nt == 64 ? run<64, PART>(grid, a, stream)
-         : nt == 128 ? run<128, PART>(grid, a, stream) : run<256, PART>(grid, a, stream);
+// Most bytes of products that wait for their sum: they stay in L2 (129 MB) between the two kernels.
+constexpr long long kSlabBytes = 64 << 20;
+
+int slab_tiles(const ExpertArgs& a) {
+  const long long per = (long long)a.n_pairs * kTR * 4, fit = kSlabBytes / per;
+  return (int)(fit < 1 ? 1 : fit < a.RT ? fit : a.RT);
 }
 
 bool bad_matrix(int experts, int N, int K, bool gated) {
@@ -710,7 +1054,7 @@ extern "C" nvfp4_status nvfp4_moe_pack_weights(const uint8_t* wq, const uint8_t*
   a.N = N, a.K = K, a.C = (K + kChunk - 1) / kChunk, a.RT = (N + kTR - 1) / kTR, a.gated = gated != 0;
   a.blocks = (long long)(need / kBlock);
   const long long grid = a.blocks < 65536 ? a.blocks : 65536;
-  return nvfp4_internal_cuda_status(launch(moe_pack_kernel, dim3((unsigned)grid), 256, 0, 1, a, stream));
+  return nvfp4_internal_cuda_status(launch(moe_pack_kernel, dim3((unsigned)grid), 256, 0, 1, stream, a));
 }
 
 namespace {
@@ -732,7 +1076,7 @@ ExpertArgs experts_args(const uint8_t* xq, const uint8_t* xs, const float* xg, i
   memset(&a, 0, sizeof(a));
   a.xc = xq, a.xs = xs, a.xg = xg, a.w = w, a.wg = wg, a.offsets = offsets, a.pairs = pairs;
   a.tokens = tokens, a.top = top_k, a.experts = experts, a.K = K;
-  a.C = (K + kChunk - 1) / kChunk, a.RT = (rows + kTR - 1) / kTR;
+  a.C = (K + kChunk - 1) / kChunk, a.RT = a.rts = (rows + kTR - 1) / kTR;
   a.n_pairs = tokens * top_k;                // (checked to fit by check_experts before it is used)
   a.cluster = 1;
   return a;
@@ -740,23 +1084,54 @@ ExpertArgs experts_args(const uint8_t* xq, const uint8_t* xs, const float* xg, i
 
 }  // namespace
 
+extern "C" size_t nvfp4_moe_gate_up_workspace_bytes(int tokens, int top_k, int experts, int K) {
+  if (tokens <= kFewTokens || top_k < 1 || top_k > kMaxTop || (long long)tokens * top_k > 0x7FFFFFFFll ||
+      bad_matrix(experts, 128, K, false))
+    return 0;
+  const ExpertArgs a = experts_args(nullptr, nullptr, nullptr, tokens, top_k, nullptr, nullptr, nullptr, nullptr, experts, 128, K);
+  return codes_bytes(a) + blocks_bytes(a);
+}
+
 extern "C" nvfp4_status nvfp4_moe_gate_up(const uint8_t* xq, const uint8_t* xs, const float* xg, int tokens, int top_k,
                                           const int32_t* offsets, const int32_t* pairs, const uint8_t* wpacked,
-                                          const float* wg, int experts, int inter, int K, uint16_t* h, cudaStream_t stream) {
+                                          const float* wg, int experts, int inter, int K, uint16_t* h, void* workspace,
+                                          size_t workspace_bytes, cudaStream_t stream) {
   if (inter < 64 || inter > (1 << 19) || bad_matrix(experts, 2 * inter, K, true)) return NVFP4_ERR_SHAPE;
   if (tokens < 0 || top_k < 1 || top_k > kMaxTop || (long long)tokens * top_k > 0x7FFFFFFFll) return NVFP4_ERR_SHAPE;
   ExpertArgs a = experts_args(xq, xs, xg, tokens, top_k, offsets, pairs, wpacked, wg, experts, 2 * inter, K);
   a.h = h, a.N = inter;
   const nvfp4_status cs = check_experts(xq, xs, xg, a, h);
   if (cs != NVFP4_OK || tokens == 0) return cs;
+  const size_t need = nvfp4_moe_gate_up_workspace_bytes(tokens, top_k, experts, K);
+  if (need > 0 && !workspace) return NVFP4_ERR_NULL;
+  if (!nvfp4_internal_aligned(workspace, 256)) return NVFP4_ERR_ALIGN;
+  if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
   const nvfp4_status ds = nvfp4_internal_check_device();
   if (ds != NVFP4_OK) return ds;
-  return nvfp4_internal_cuda_status(run_items(true, a, stream));
+  const int sms = device_sms();
+  if (need == 0) {
+    const int nt = tokens <= 16 ? 16 : 64;
+    const long long items = most_tiles(a, nt) * a.RT;
+    while (a.cluster < kMaxCluster && items * a.cluster * 2 <= sms && a.C >= a.cluster * 2) a.cluster *= 2;
+    const long long grid = items * a.cluster < sms ? items * a.cluster : sms;
+    return nvfp4_internal_cuda_status(nt == 16 ? run_few<16, UP>(grid, a, stream) : run_few<64, UP>(grid, a, stream));
+  }
+  uint8_t *codes = static_cast<uint8_t*>(workspace), *blocks = codes + codes_bytes(a);
+  CUtensorMap map;
+  const cudaError_t e = arrange(a, codes, blocks, &map, stream);
+  if (e != cudaSuccess) return nvfp4_internal_cuda_status(e);
+  a.x_blocks = blocks;
+  const int nt = tile_for(a);
+  const long long items = most_tiles(a, nt) * a.RT, grid = items < sms ? items : sms;
+  return nvfp4_internal_cuda_status(nt == 64 ? run_many<64, UP>(grid, map, a, stream) : run_many<256, UP>(grid, map, a, stream));
 }
 
-extern "C" size_t nvfp4_moe_down_workspace_bytes(int tokens, int top_k, int N) {
-  if (tokens <= kSumTokens || top_k < 1 || top_k > kMaxTop || N < 1 || N > (1 << 20)) return 0;
-  return (size_t)tokens * top_k * N * sizeof(float);
+extern "C" size_t nvfp4_moe_down_workspace_bytes(int tokens, int top_k, int experts, int N, int K) {
+  if (tokens <= kFewTokens || top_k < 1 || top_k > kMaxTop || (long long)tokens * top_k > 0x7FFFFFFFll ||
+      bad_matrix(experts, N, K, false))
+    return 0;
+  const ExpertArgs a = experts_args(nullptr, nullptr, nullptr, tokens, top_k, nullptr, nullptr, nullptr, nullptr, experts, N, K);
+  return blocks_bytes(a) + (size_t)a.n_pairs * slab_tiles(a) * kTR * sizeof(float);
 }
 
 extern "C" nvfp4_status nvfp4_moe_down(const uint8_t* hq, const uint8_t* hs, const float* hg, int tokens, int top_k,
@@ -770,27 +1145,39 @@ extern "C" nvfp4_status nvfp4_moe_down(const uint8_t* hq, const uint8_t* hs, con
   const nvfp4_status cs = check_experts(hq, hs, hg, a, y);
   if (cs != NVFP4_OK || tokens == 0) return cs;
   if (!places || !weights) return NVFP4_ERR_NULL;
-  const size_t need = nvfp4_moe_down_workspace_bytes(tokens, top_k, N);
+  const size_t need = nvfp4_moe_down_workspace_bytes(tokens, top_k, experts, N, K);
   if (need > 0 && !workspace) return NVFP4_ERR_NULL;
-  if (!nvfp4_internal_aligned(places, 4) || !nvfp4_internal_aligned(weights, 4) || !nvfp4_internal_aligned(workspace, 16))
+  if (!nvfp4_internal_aligned(places, 4) || !nvfp4_internal_aligned(weights, 4) || !nvfp4_internal_aligned(workspace, 256))
     return NVFP4_ERR_ALIGN;
   if (workspace_bytes < need) return NVFP4_ERR_SHAPE;
   const nvfp4_status ds = nvfp4_internal_check_device();
   if (ds != NVFP4_OK) return ds;
+  const int sms = device_sms();
   if (need == 0) {
     a.out = y;
-    const int sms = device_sms();
     while (a.cluster < kMaxCluster && a.RT * (a.cluster + 1) <= sms) ++a.cluster;
-    return nvfp4_internal_cuda_status(tokens <= 16 ? run<16, SUM>(a.RT * a.cluster, a, stream)
-                                                   : run<64, SUM>(a.RT * a.cluster, a, stream));
+    return nvfp4_internal_cuda_status(tokens <= 16 ? run_few<16, SUM>((long long)a.RT * a.cluster, a, stream)
+                                                   : run_few<64, SUM>((long long)a.RT * a.cluster, a, stream));
   }
-  a.out = static_cast<float*>(workspace);
-  cudaError_t e = run_items(false, a, stream);
+  uint8_t* blocks = static_cast<uint8_t*>(workspace);
+  CUtensorMap map;
+  cudaError_t e = arrange(a, nullptr, blocks, &map, stream);
   if (e != cudaSuccess) return nvfp4_internal_cuda_status(e);
-  CombineArgs c = {a.out, weights, places, y, tokens, top_k, N, a.n_pairs};
-  const int per = N % 4 == 0 ? 1024 : 256;
-  const dim3 grid((unsigned)((N + per - 1) / per), (unsigned)(tokens < 65535 ? tokens : 65535));
-  e = N % 4 == 0 ? launch(moe_combine_kernel<4>, grid, 256, 0, 1, c, stream)
-                 : launch(moe_combine_kernel<1>, grid, 256, 0, 1, c, stream);
+  a.x_blocks = blocks;
+  a.out = reinterpret_cast<float*>(blocks + blocks_bytes(a));
+  const int nt = tile_for(a), slab = slab_tiles(a);
+  for (a.rt0 = 0; a.rt0 < a.RT; a.rt0 += slab) {
+    a.rts = a.RT - a.rt0 < slab ? a.RT - a.rt0 : slab;
+    const long long items = most_tiles(a, nt) * a.rts, grid = items < sms ? items : sms;
+    e = nt == 64 ? run_many<64, PART>(grid, map, a, stream) : run_many<256, PART>(grid, map, a, stream);
+    if (e != cudaSuccess) break;
+    const int n0 = a.rt0 * kTR, n1 = (a.rt0 + a.rts) * kTR < N ? (a.rt0 + a.rts) * kTR : N;
+    const CombineArgs c = {a.out, weights, places, y, tokens, top_k, N, a.n_pairs, n0, n1, a.rts * kTR};
+    const int per = N % 4 == 0 ? 1024 : 256;
+    const dim3 grid2((unsigned)((n1 - n0 + per - 1) / per), (unsigned)(tokens < 65535 ? tokens : 65535));
+    e = N % 4 == 0 ? launch(moe_combine_kernel<4>, grid2, 256, 0, 1, stream, c)
+                   : launch(moe_combine_kernel<1>, grid2, 256, 0, 1, stream, c);
+    if (e != cudaSuccess) break;
+  }
   return nvfp4_internal_cuda_status(e);
 }

@@ -139,11 +139,12 @@ def test_many_experts(T):
 def test_outputs_are_all_that_is_written(T):
     c = Case(_ids(np.random.default_rng(4), T, 2, 4), 4, 320, 192, seed=5)
     h, y = Guarded((T * 2, 192), torch.bfloat16), Guarded((T, 320), torch.float32)
-    c.check_up(api.nvfp4_moe_gate_up(_tensor(c.x), c.up, c.routing, out=h.t))
-    need = T * 2 * 320 * 4 if T > 64 else 0
-    ws = Guarded((max(need, 16),), torch.uint8)
-    c.check_down(api.nvfp4_moe_down(_tensor(c.h), c.down, c.routing, y=y.t, workspace=ws.t))
-    for g, n in ((h, "h"), (y, "y"), (ws, "workspace")):
+    need = [max(16, n) for n in (api.nvfp4_moe_gate_up_workspace_bytes(T, 2, 4, 320),
+                                 api.nvfp4_moe_down_workspace_bytes(T, 2, 4, 320, 192))]
+    ws = [Guarded((n,), torch.uint8) for n in need]
+    c.check_up(api.nvfp4_moe_gate_up(_tensor(c.x), c.up, c.routing, out=h.t, workspace=ws[0].t))
+    c.check_down(api.nvfp4_moe_down(_tensor(c.h), c.down, c.routing, y=y.t, workspace=ws[1].t))
+    for g, n in ((h, "h"), (y, "y"), (ws[0], "workspace of h"), (ws[1], "workspace of y")):
         g.check(n)
 
 

@@ -65,8 +65,9 @@ def test_pack_refusals(lib):  # noqa: F811
 
 
 def test_products_refusals(lib):  # noqa: F811
-    def up(xq=FAKE, xs=FAKE, xg=FAKE, T=4, k=2, off=FAKE, pairs=FAKE, w=FAKE, wg=FAKE, E=8, I=64, K=256, h=FAKE):
-        return lib.nvfp4_moe_gate_up(xq, xs, xg, T, k, off, pairs, w, wg, E, I, K, h, None)
+    def up(xq=FAKE, xs=FAKE, xg=FAKE, T=4, k=2, off=FAKE, pairs=FAKE, w=FAKE, wg=FAKE, E=8, I=64, K=256, h=FAKE,
+           ws=None, wsb=0):
+        return lib.nvfp4_moe_gate_up(xq, xs, xg, T, k, off, pairs, w, wg, E, I, K, h, ws, wsb, None)
 
     def down(xq=FAKE, xs=FAKE, xg=FAKE, T=4, k=2, off=FAKE, pairs=FAKE, places=FAKE, wt=FAKE, w=FAKE, wg=FAKE, E=8, N=100,
              K=256, y=FAKE, ws=None, wsb=0):
@@ -82,9 +83,14 @@ def test_products_refusals(lib):  # noqa: F811
     for bad, by in (("xq", 8), ("xs", 2), ("xg", 2), ("off", 2), ("pairs", 1), ("w", 8), ("wg", 2)):
         assert up(**{bad: FAKE + by}) == 3 and down(**{bad: FAKE + by}) == 3, bad
     assert up(h=FAKE + 8) == 3 and down(y=FAKE + 8) == 3 and down(places=FAKE + 2) == 3 and down(wt=FAKE + 2) == 3
-    need = lib.nvfp4_moe_down_workspace_bytes(1000, 2, 100)
-    assert need > 0 and lib.nvfp4_moe_down_workspace_bytes(4, 2, 100) == 0
-    assert down(T=1000) == 1 and down(T=1000, ws=FAKE, wsb=need - 1) == 2 and down(T=1000, ws=FAKE + 8, wsb=need) == 3
+    for f, need in ((down, lib.nvfp4_moe_down_workspace_bytes(1000, 2, 8, 100, 256)),
+                    (up, lib.nvfp4_moe_gate_up_workspace_bytes(1000, 2, 8, 256))):
+        assert need > 0
+        assert f(T=1000) == 1 and f(T=1000, ws=FAKE, wsb=need - 1) == 2 and f(T=1000, ws=FAKE + 8, wsb=need) == 3
+    assert lib.nvfp4_moe_down_workspace_bytes(64, 2, 8, 100, 256) == 0
+    assert lib.nvfp4_moe_gate_up_workspace_bytes(64, 2, 8, 256) == 0
+    for bad in ((1000, 0, 8, 100, 256), (1000, 2, 0, 100, 256), (1000, 2, 8, 0, 256), (1000, 2, 8, 100, 32), (1 << 30, 2, 8, 100, 256)):
+        assert lib.nvfp4_moe_down_workspace_bytes(*bad) == 0, bad
 
 
 def test_rotating_append_refusals(lib):  # noqa: F811
