@@ -47,9 +47,10 @@ constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kTmemCols = 512;
 
-// The experts that have pairs, as a kernel keeps them: first places, counts, tiles of 128 places before, the offsets as
-// given, sums, experts.
-constexpr int kTableBytes = kMaxExperts * (4 * 4 + 2) + 32;
+// The experts that have pairs, as a kernel keeps them: first places, counts, tiles of NT and of 128 places before, experts;
+// sums.  The offsets as given stand elsewhere while the table is built.
+constexpr int kTableBytes = kMaxExperts * (4 * 4 + 2) + 16;
+constexpr int kOffsetsBytes = (kMaxExperts + 1) * 4;
 
 enum Mode { UP, SUM, PART };
 
@@ -98,18 +99,18 @@ struct Segment {
 
 // The experts that have pairs, in order.
 struct Table {
-  int *first, *count, *blocks, *offsets;     // blocks: tiles of 128 places of the experts before
-  long long* sums;
+  int *first, *count, *tiles_before, *blocks, *offsets;  // tiles of up to NT places, and of 128, of the experts before
+  int* sums;
   uint16_t* expert;
-  int used, total;                           // entries; pairs
-  long long tiles;                           // stretches of up to NT pairs
-  NVFP4_DEVINL explicit Table(uint8_t* mem) {            // kTableBytes, 16-byte aligned
+  int used, total, tiles;                                // entries; pairs; tiles of up to NT places
+  NVFP4_DEVINL Table(uint8_t* mem, uint8_t* scratch) {   // kTableBytes, and kOffsetsBytes until it is built; 16-byte aligned
     first = reinterpret_cast<int*>(mem);
     count = first + kMaxExperts;
-    blocks = count + kMaxExperts;
-    offsets = blocks + kMaxExperts;                      // kMaxExperts + 1
-    sums = reinterpret_cast<long long*>(offsets + kMaxExperts + 2);
-    expert = reinterpret_cast<uint16_t*>(sums + 3);
+    tiles_before = count + kMaxExperts;
+    blocks = tiles_before + kMaxExperts;
+    sums = blocks + kMaxExperts;                         // 4
+    expert = reinterpret_cast<uint16_t*>(sums + 4);
+    offsets = reinterpret_cast<int*>(scratch);
   }
 };
 
@@ -121,8 +122,7 @@ NVFP4_DEVINL void build_table(const ExpertArgs& a, Table& tb) {
   if (threadIdx.x < 32) {
     // a lane looks at `per` experts that follow one another
     const int lane = threadIdx.x, per = (a.experts + 31) / 32;
-    int used = 0, blocks = 0;
-    long long tiles = 0;
+    int used = 0, blocks = 0, tiles = 0;
     bool bad = false;
     auto look = [&](auto take) {
       for (int i = 0; i < per; ++i) {
@@ -139,56 +139,61 @@ NVFP4_DEVINL void build_table(const ExpertArgs& a, Table& tb) {
       blocks += (n + 127) / 128;
       tiles += (n + NT - 1) / NT;
     });
-    int at = used, before = blocks;
+    int at = used, before = blocks, tiles_before = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, at, o), y = __shfl_up_sync(0xffffffffu, before, o);
+      const int z = __shfl_up_sync(0xffffffffu, tiles_before, o);
       if (lane >= o) {
         at += x;
         before += y;
+        tiles_before += z;
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
     if (lane == 31) {
-      tb.sums[0] = tiles;
+      tb.sums[0] = tiles_before;
       tb.sums[1] = at;
       tb.sums[2] = min(max(tb.offsets[a.experts], 0), a.n_pairs);
     }
     at -= used;
     before -= blocks;
+    tiles_before -= tiles;
     look([&](int e, int lo, int n) {
       tb.first[at] = lo;
       tb.count[at] = n;
       tb.blocks[at] = before;
+      tb.tiles_before[at] = tiles_before;
       tb.expert[at] = (uint16_t)e;
       ++at;
       before += (n + 127) / 128;
+      tiles_before += (n + NT - 1) / NT;
     });
     if (bad && blockIdx.x == 0) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
   }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (the ring's copies may come where the offsets stood)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   tb.tiles = tb.sums[0];
-  tb.used = (int)tb.sums[1];
-  tb.total = (int)tb.sums[2];
+  tb.used = tb.sums[1];
+  tb.total = tb.sums[2];
 }
 
-// Every role walks the CTA's segments by itself, in the same order.
+// Every role's warp walks the CTA's segments by itself, in the same order; its lanes look an item up together (one by one
+// along the experts took 3700 cycles a segment, as long as 5 stages).
 template <int NT, int MODE>
 struct Walk {
   const Table& tb;
   const ExpertArgs& a;
-  long long it, end, base;                   // UP, PART: item; SUM: unit (tile of pairs, chunk)
-  int used;                                  // the table's entry that `base` belongs to
+  int it, end;                               // UP, PART: item; SUM: unit (tile of places, chunk)
+  int used, tile;                            // SUM: the entry and its tile that `it` stands in, -1: to be looked up
   int rank, step;
-  NVFP4_DEVINL Walk(const Table& t, const ExpertArgs& args) : tb(t), a(args), base(0), used(0) {
+  NVFP4_DEVINL Walk(const Table& t, const ExpertArgs& args) : tb(t), a(args), used(-1), tile(0) {
     rank = args.cluster > 1 ? (int)cluster_ctarank() : 0;
     if (MODE == SUM) {
-      const long long units = t.tiles * a.C;
-      it = units * rank / a.cluster;
-      end = units * (rank + 1) / a.cluster;
+      const long long units = (long long)t.tiles * a.C;
+      it = (int)(units * rank / a.cluster);
+      end = (int)(units * (rank + 1) / a.cluster);
       step = 0;
     } else {
       it = blockIdx.x / a.cluster;
@@ -196,27 +201,38 @@ struct Walk {
       step = gridDim.x / a.cluster;
     }
   }
+  // The last entry whose tiles, times `of`, begin at x or before.
+  NVFP4_DEVINL int entry_of(int x, int of) const {
+    const int lane = threadIdx.x & 31, per = (tb.used + 31) / 32, at = lane * per;
+    const int piece = __popc(__ballot_sync(0xffffffffu, at < tb.used && tb.tiles_before[at] * of <= x)) - 1;
+    const int i = piece * per + lane;
+    return piece * per + __popc(__ballot_sync(0xffffffffu, lane < per && i < tb.used && tb.tiles_before[i] * of <= x)) - 1;
+  }
+  // By a whole warp.
   NVFP4_DEVINL bool next(Segment& s) {
     if (it >= end) return false;
-    int tt, t;
+    int t;
     if (MODE == SUM) {
-      const long long tile = it / a.C;
-      while (tile >= base + (tt = (tb.count[used] + NT - 1) / NT)) {
-        base += tt;
-        ++used;
+      if (used < 0) {
+        const int at = it / a.C;
+        used = entry_of(at, 1);
+        tile = at - tb.tiles_before[used];
+        s.c0 = it - at * a.C;
+      } else {
+        s.c0 = 0;
+        if (++tile == (tb.count[used] + NT - 1) / NT) {
+          tile = 0;
+          ++used;
+        }
       }
-      t = (int)(tile - base);
+      t = tile;
       s.rt = blockIdx.x / a.cluster;
-      s.c0 = (int)(it - tile * a.C);
-      s.nc = (int)min((long long)(a.C - s.c0), end - it);
+      s.nc = min(a.C - s.c0, end - it);
       it += s.nc;
     } else {
-      while (it >= base + (long long)(tt = (tb.count[used] + NT - 1) / NT) * a.rts) {
-        base += (long long)tt * a.rts;
-        ++used;
-      }
-      const int in = (int)(it - base);       // an expert's items: the tiles of pairs of a row tile follow one another
-      s.rt = in / tt;
+      used = entry_of(it, a.rts);
+      const int in = it - tb.tiles_before[used] * a.rts, tt = (tb.count[used] + NT - 1) / NT;
+      s.rt = tt == 1 ? in : in / tt;         // an expert's items: the tiles of places of a row tile follow one another
       t = in - s.rt * tt;
       s.rt += a.rt0;
       s.c0 = a.C * rank / a.cluster;
@@ -335,7 +351,7 @@ struct Smem {
     acc_empty = acc_full + 2;
     tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
   }
-  NVFP4_DEVINL Table table() const { return Table(base + S::kOffTables); }
+  NVFP4_DEVINL Table table() const { return Table(base + S::kOffTables, base); }
   // By the first thread; `arrivals`: on a stage, `readers`: warps that read an accumulator.
   NVFP4_DEVINL void init_barriers(int arrivals, int readers) const {
     for (int s = 0; s < S::kStages; ++s) {
@@ -360,30 +376,40 @@ struct Smem {
   }
 };
 
-// The weight blocks of the CTA's segments, by one thread.
-template <int NT, int MODE, bool FEW>
-NVFP4_DEVINL void copy_weights(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, Walk<NT, MODE> walk) {
+// Stages of a CTA's segments that one lane of a warp fills: fill(sg, c, slot, bar) for each, once its last use is over.
+template <int NT, int MODE, bool FEW, class F>
+NVFP4_DEVINL void fill_stages(const Smem<NT, MODE, FEW>& sm, Walk<NT, MODE> walk, const F& fill) {
   using S = Shape<NT, MODE, FEW>;
   constexpr int kS = S::kStages;
   Segment sg;
-  int s = 0, k = 0;
+  int s = 0, k = 0, ok = 1;
   uint32_t phase = 0;
-  bool ok = true;
   while (ok && walk.next(sg)) {
-    const uint8_t* src = a.w + (((size_t)sg.e * a.RT + sg.rt) * a.C + sg.c0) * kBlock;
-    for (int c = 0; c < sg.nc; ++c, src += kBlock) {
-      if (k >= kS && !mbar_wait(&sm.empty[s], phase ^ 1u)) {
-        ok = false;
-        break;
+    if ((threadIdx.x & 31) == 0) {
+      for (int c = sg.c0; c < sg.c0 + sg.nc; ++c) {
+        if (k >= kS && !mbar_wait(&sm.empty[s], phase ^ 1u)) {
+          ok = 0;
+          break;
+        }
+        fill(sg, c, sm.base + s * S::kSlot, &sm.full[s]);
+        ++k;
+        if (++s == kS) { s = 0; phase ^= 1u; }
       }
-      mbar_arrive_expect_tx(&sm.full[s], kBlock);
-      bulk_g2s(sm.base + s * S::kSlot, src, kBlock, &sm.full[s]);
-      ++k;
-      if (++s == kS) { s = 0; phase ^= 1u; }
     }
+    ok = __shfl_sync(0xffffffffu, ok, 0);
   }
   // Not to leave with copies in flight: the last ones' waits (bounded; on the normal path long over).
-  for (int j = k > kS ? k - kS : 0; j < k; ++j) mbar_wait(&sm.full[j % kS], (j / kS) & 1);
+  if ((threadIdx.x & 31) == 0)
+    for (int j = k > kS ? k - kS : 0; j < k; ++j) mbar_wait(&sm.full[j % kS], (j / kS) & 1);
+  __syncwarp();
+}
+
+template <int NT, int MODE, bool FEW>
+NVFP4_DEVINL void copy_weights(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, const Walk<NT, MODE>& walk) {
+  fill_stages(sm, walk, [&](const Segment& sg, int c, uint8_t* slot, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, kBlock);
+    bulk_g2s(slot, a.w + (((size_t)sg.e * a.RT + sg.rt) * a.C + c) * kBlock, kBlock, bar);
+  });
 }
 
 // Scales to TMEM and products, by one warp.  It waits together; one lane then issues a stage's copies, products and commit
@@ -483,7 +509,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const ExpertArg
   __syncwarp();
 
   if (warp == 0) {
-    if (lane == 0) copy_weights(sm, a, walk);
+    copy_weights(sm, a, walk);
   } else if (warp == 1) {
     multiply(sm, a, walk, tmem);
   } else if (warp < 6) {
@@ -677,7 +703,6 @@ template <int NT, int MODE>
 __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_constant__ CUtensorMap tm_x,
                                                                    const ExpertArgs a) {
   using S = Shape<NT, MODE, false>;
-  constexpr int kS = S::kStages;
   const Smem<NT, MODE, false> sm(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -700,35 +725,19 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
   __syncwarp();
 
   if (warp == 0) {
-    if (lane == 0) copy_weights(sm, a, walk);
+    copy_weights(sm, a, walk);
   } else if (warp == 1) {
     multiply(sm, a, walk, tmem);
   } else if (warp == 2) {
     // ---------------- rows of x, in the order of the plan, and their scales ----------------
-    if (lane == 0) {
-      int s = 0, k = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      while (ok && walk.next(sg)) {
-        const int boxes = (sg.n + kBoxRows - 1) / kBoxRows, halves = (sg.n + 127) / 128;
-        for (int c = 0; c < sg.nc; ++c) {
-          if (k >= kS && !mbar_wait(&sm.empty[s], phase ^ 1u)) {
-            ok = false;
-            break;
-          }
-          uint8_t* slot = sm.base + s * S::kSlot;
-          mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(boxes * kBoxRows * 128 + halves * kXBlock));
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(slot + S::kOffX + b * (kBoxRows * 128), &tm_x, (sg.c0 + c) * 128, sg.p0 + b * kBoxRows, &sm.full[s]);
-          for (int h = 0; h < halves; ++h)
-            bulk_g2s(slot + S::kOffXS + h * kXBlock, a.x_blocks + ((size_t)(sg.block + h) * a.C + sg.c0 + c) * kXBlock,
-                     kXBlock, &sm.full[s]);
-          ++k;
-          if (++s == kS) { s = 0; phase ^= 1u; }
-        }
-      }
-      for (int j = k > kS ? k - kS : 0; j < k; ++j) mbar_wait(&sm.full[j % kS], (j / kS) & 1);
-    }
+    fill_stages(sm, walk, [&](const Segment& sg, int c, uint8_t* slot, uint64_t* bar) {
+      const int boxes = (sg.n + kBoxRows - 1) / kBoxRows, halves = (sg.n + 127) / 128;
+      mbar_arrive_expect_tx(bar, (uint32_t)(boxes * kBoxRows * 128 + halves * kXBlock));
+      for (int b = 0; b < boxes; ++b)
+        tma_load_2d(slot + S::kOffX + b * (kBoxRows * 128), &tm_x, c * 128, sg.p0 + b * kBoxRows, bar);
+      for (int h = 0; h < halves; ++h)
+        bulk_g2s(slot + S::kOffXS + h * kXBlock, a.x_blocks + ((size_t)(sg.block + h) * a.C + c) * kXBlock, kXBlock, bar);
+    });
   } else if (warp >= 4) {
     // ---------------- the accumulator: two warps a lane quadrant, 16 columns in turn ----------------
     const int p = warp & 3, row = p * 32 + lane, part = (warp - 4) >> 2;
@@ -790,14 +799,14 @@ constexpr int kArrangeThreads = 256;
 constexpr int kArrangeChunks = 4;
 
 __global__ void __launch_bounds__(kArrangeThreads) moe_arrange_kernel(const ArrangeArgs g) {
-  __shared__ __align__(16) uint8_t s_table[kTableBytes];
+  __shared__ __align__(16) uint8_t s_table[kTableBytes], s_offsets[kOffsetsBytes];
   __shared__ int s_row[128];
   griddep_launch_dependents();
   griddep_wait();
   const ExpertArgs& a = g.x;
-  Table tb(s_table);
+  Table tb(s_table, s_offsets);
   build_table<128>(a, tb);
-  if ((long long)blockIdx.x >= tb.tiles) return;
+  if ((int)blockIdx.x >= tb.tiles) return;
   int used = 0;                              // the last entry whose tiles begin at blockIdx.x or before
   for (int hi = tb.used; hi - used > 1;) {
     const int mid = (used + hi) >> 1;
@@ -1024,6 +1033,12 @@ int slab_tiles(const ExpertArgs& a) {
   return (int)(fit < 1 ? 1 : fit < a.RT ? fit : a.RT);
 }
 
+// Whether a call's items and units are counted in 31 bits.
+bool too_many_items(const ExpertArgs& a) {
+  const long long tiles = most_tiles(a, 16);
+  return tiles * a.RT > 0x7FFFFFFFll || tiles * a.C > 0x7FFFFFFFll;
+}
+
 bool bad_matrix(int experts, int N, int K, bool gated) {
   return experts < 1 || experts > kMaxExperts || N < 1 || N > (1 << 20) || K < 64 || K > (1 << 20) || K % 64 != 0 ||
          (gated && N % 128 != 0);
@@ -1100,6 +1115,7 @@ extern "C" nvfp4_status nvfp4_moe_gate_up(const uint8_t* xq, const uint8_t* xs, 
   if (tokens < 0 || top_k < 1 || top_k > kMaxTop || (long long)tokens * top_k > 0x7FFFFFFFll) return NVFP4_ERR_SHAPE;
   ExpertArgs a = experts_args(xq, xs, xg, tokens, top_k, offsets, pairs, wpacked, wg, experts, 2 * inter, K);
   a.h = h, a.N = inter;
+  if (too_many_items(a)) return NVFP4_ERR_SHAPE;
   const nvfp4_status cs = check_experts(xq, xs, xg, a, h);
   if (cs != NVFP4_OK || tokens == 0) return cs;
   const size_t need = nvfp4_moe_gate_up_workspace_bytes(tokens, top_k, experts, K);
@@ -1142,6 +1158,7 @@ extern "C" nvfp4_status nvfp4_moe_down(const uint8_t* hq, const uint8_t* hs, con
   if (tokens < 0 || top_k < 1 || top_k > kMaxTop || (long long)tokens * top_k > 0x7FFFFFFFll) return NVFP4_ERR_SHAPE;
   ExpertArgs a = experts_args(hq, hs, hg, tokens, top_k, offsets, pairs, wpacked, wg, experts, N, K);
   a.N = N, a.weights = weights;
+  if (too_many_items(a)) return NVFP4_ERR_SHAPE;
   const nvfp4_status cs = check_experts(hq, hs, hg, a, y);
   if (cs != NVFP4_OK || tokens == 0) return cs;
   if (!places || !weights) return NVFP4_ERR_NULL;
