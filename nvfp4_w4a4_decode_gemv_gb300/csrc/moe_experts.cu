@@ -114,15 +114,16 @@ struct Table {
   }
 };
 
-// Built by the whole CTA; ends with a __syncthreads.
-template <int NT>
+// Built by the whole CTA; ends with a __syncthreads.  HEAVY: experts of more than 128 places come first, so that items dealt
+// out in turn cost about the same (a stage of more than 128 places takes twice the MMAs).
+template <int NT, bool HEAVY>
 NVFP4_DEVINL void build_table(const ExpertArgs& a, Table& tb) {
   for (int i = threadIdx.x; i <= a.experts; i += blockDim.x) tb.offsets[i] = __ldcg(a.offsets + i);
   __syncthreads();
   if (threadIdx.x < 32) {
     // a lane looks at `per` experts that follow one another
     const int lane = threadIdx.x, per = (a.experts + 31) / 32;
-    int used = 0, blocks = 0, tiles = 0;
+    int used[2] = {0, 0}, tiles[2] = {0, 0}, blocks = 0;      // [0]: of heavy experts
     bool bad = false;
     auto look = [&](auto take) {
       for (int i = 0; i < per; ++i) {
@@ -131,42 +132,49 @@ NVFP4_DEVINL void build_table(const ExpertArgs& a, Table& tb) {
         const int f = tb.offsets[e], l = tb.offsets[e + 1];
         const int lo = min(max(f, 0), a.n_pairs), hi = min(max(l, 0), a.n_pairs);
         bad = bad || f != lo || l != hi || hi < lo;
-        if (hi > lo) take(e, lo, hi - lo);
+        if (hi > lo) take(e, lo, hi - lo, HEAVY && hi - lo <= 128);
       }
     };
-    look([&](int, int, int n) {
-      ++used;
+    look([&](int, int, int n, bool light) {
+      const int t = (n + NT - 1) / NT;
+      used[0] += light ? 0 : 1;
+      used[1] += light ? 1 : 0;
+      tiles[0] += light ? 0 : t;
+      tiles[1] += light ? t : 0;
       blocks += (n + 127) / 128;
-      tiles += (n + NT - 1) / NT;
     });
-    int at = used, before = blocks, tiles_before = tiles;
+    int at[5] = {used[0], used[1], tiles[0], tiles[1], blocks};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, at, o), y = __shfl_up_sync(0xffffffffu, before, o);
-      const int z = __shfl_up_sync(0xffffffffu, tiles_before, o);
-      if (lane >= o) {
-        at += x;
-        before += y;
-        tiles_before += z;
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        if (!HEAVY && (i == 1 || i == 3)) continue;
+        const int x = __shfl_up_sync(0xffffffffu, at[i], o);
+        if (lane >= o) at[i] += x;
       }
-    }
+    const int heavy = __shfl_sync(0xffffffffu, at[0], 31), heavy_tiles = __shfl_sync(0xffffffffu, at[2], 31);
     if (lane == 31) {
-      tb.sums[0] = tiles_before;
-      tb.sums[1] = at;
+      tb.sums[0] = heavy_tiles + at[3];
+      tb.sums[1] = heavy + at[1];
       tb.sums[2] = min(max(tb.offsets[a.experts], 0), a.n_pairs);
     }
-    at -= used;
-    before -= blocks;
-    tiles_before -= tiles;
-    look([&](int e, int lo, int n) {
-      tb.first[at] = lo;
-      tb.count[at] = n;
-      tb.blocks[at] = before;
-      tb.tiles_before[at] = tiles_before;
-      tb.expert[at] = (uint16_t)e;
-      ++at;
-      before += (n + 127) / 128;
-      tiles_before += (n + NT - 1) / NT;
+    at[0] -= used[0];
+    at[1] += heavy - used[1];
+    at[2] -= tiles[0];
+    at[3] += heavy_tiles - tiles[1];
+    at[4] -= blocks;
+    look([&](int e, int lo, int n, bool light) {
+      const int i = light ? at[1] : at[0], t = (n + NT - 1) / NT;
+      tb.first[i] = lo;
+      tb.count[i] = n;
+      tb.blocks[i] = at[4];
+      tb.tiles_before[i] = light ? at[3] : at[2];
+      tb.expert[i] = (uint16_t)e;
+      at[0] += light ? 0 : 1;
+      at[1] += light ? 1 : 0;
+      at[2] += light ? 0 : t;
+      at[3] += light ? t : 0;
+      at[4] += (n + 127) / 128;
     });
     if (bad && blockIdx.x == 0) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
   }
@@ -260,6 +268,19 @@ struct Buffers {
     if (!both) turn ^= 1;
   }
 };
+
+// One look, without waiting.
+NVFP4_DEVINL bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
 // 32 rows of 16 bytes, one behind the other, to 4 columns of every lane quadrant: word w of row i to lane i, column w.
 NVFP4_DEVINL void copy_scales(uint32_t tmem, uint64_t desc) {
@@ -415,6 +436,8 @@ NVFP4_DEVINL void copy_weights(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& 
 // Scales to TMEM and products, by one warp.  It waits together; one lane then issues a stage's copies, products and commit
 // in one branch, with the others held at its end.  (Predicated one by one, with the other lanes free to run ahead, they
 // faulted once several stages were ready: operands are in uniform registers, which the lanes that run ahead overwrite.)
+// The next stage's barrier is looked at before a stage's instructions are issued: behind them, the look would wait until
+// the tensor core has taken them (300 cycles a stage of 1000).
 template <int NT, int MODE, bool FEW>
 NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, Walk<NT, MODE> walk, uint32_t tmem) {
   using S = Shape<NT, MODE, FEW>;
@@ -425,7 +448,7 @@ NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, W
   Buffers bufs;
   int s = 0, k = 0;
   uint32_t phase = 0;
-  bool ok = true;
+  bool ok = true, ready = false;
   while (ok && walk.next(sg)) {
     const bool both = S::kHalves == 2 && sg.n > 128;
     const int buf = bufs.first(both);
@@ -433,10 +456,13 @@ NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, W
     if (both && bufs.uses1 > 0 && !mbar_wait_warp(&sm.acc_empty[1], (bufs.uses1 - 1) & 1)) break;
     bufs.took(both);
     for (int c = 0; c < sg.nc; ++c) {
-      if (!mbar_wait_warp(&sm.full[s], phase)) {
+      if (!ready && !mbar_wait_warp(&sm.full[s], phase)) {
         ok = false;
         break;
       }
+      const int next = s + 1 == kS ? 0 : s + 1;
+      const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
+      ready = __all_sync(0xffffffffu, mbar_test_wait(&sm.full[next], next_phase));
       if (lead) {
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(buf * S::kHalf), slot = base + (uint32_t)(s * S::kSlot);
@@ -469,7 +495,8 @@ NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, W
       }
       __syncwarp();
       ++k;
-      if (++s == kS) { s = 0; phase ^= 1u; }
+      s = next;
+      phase = next_phase;
     }
   }
   if (k > 0) mbar_wait_warp(&sm.empty[(k - 1) % kS], ((k - 1) / kS) & 1);   // not to leave with MMAs in flight
@@ -495,7 +522,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const ExpertArg
   griddep_launch_dependents();
   griddep_wait();                            // the plan comes from a preceding kernel
   Table tb = sm.table();
-  build_table<NT>(a, tb);
+  build_table<NT, false>(a, tb);
   const uint32_t tmem = *sm.tmem_slot;
   Walk<NT, MODE> walk(tb, a);
   Segment sg;
@@ -713,7 +740,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
   griddep_launch_dependents();
   griddep_wait();
   Table tb = sm.table();
-  build_table<NT>(a, tb);
+  build_table<NT, (NT > 128)>(a, tb);
   const uint32_t tmem = *sm.tmem_slot;
   Walk<NT, MODE> walk(tb, a);
   Segment sg;
@@ -805,7 +832,7 @@ __global__ void __launch_bounds__(kArrangeThreads) moe_arrange_kernel(const Arra
   griddep_wait();
   const ExpertArgs& a = g.x;
   Table tb(s_table, s_offsets);
-  build_table<128>(a, tb);
+  build_table<128, false>(a, tb);
   if ((int)blockIdx.x >= tb.tiles) return;
   int used = 0;                              // the last entry whose tiles begin at blockIdx.x or before
   for (int hi = tb.used; hi - used > 1;) {
@@ -839,10 +866,18 @@ __global__ void __launch_bounds__(kArrangeThreads) moe_arrange_kernel(const Arra
   }
   if (!g.codes) return;
   const int b0 = c0 * 128, pieces = (min(row_codes, c1 * 128) - b0) / 16;
-  for (int x = threadIdx.x; x < n * pieces; x += kArrangeThreads) {
-    const int r = x / pieces, at = b0 + (x - r * pieces) * 16;
-    *reinterpret_cast<uint4*>(g.codes + (size_t)(p0 + r) * row_codes + at) =
-        __ldcg(reinterpret_cast<const uint4*>(a.xc + (size_t)s_row[r] * row_codes + at));
+  for (int x = threadIdx.x; x < n * pieces; x += 4 * kArrangeThreads) {
+    uint4 v[4];
+    size_t to[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int y = x + i * kArrangeThreads, r = y / pieces, at = b0 + (y - r * pieces) * 16;
+      to[i] = (size_t)(p0 + r) * row_codes + at;
+      if (y < n * pieces) v[i] = __ldcg(reinterpret_cast<const uint4*>(a.xc + (size_t)s_row[r] * row_codes + at));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (x + i * kArrangeThreads < n * pieces) *reinterpret_cast<uint4*>(g.codes + to[i]) = v[i];
   }
 }
 
@@ -854,6 +889,8 @@ struct CombineArgs {
   int tokens, top, N, n_pairs, n0, n1, ld;
 };
 
+constexpr int kAtOnce = 8;                   // products of a token that are read together
+
 template <int V>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
   griddep_launch_dependents();
@@ -862,24 +899,35 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
   if (n >= a.n1) return;
   for (int t = blockIdx.y; t < a.tokens; t += gridDim.y) {
     float y[V] = {};
-#pragma unroll 4
-    for (int j = 0; j < a.top; ++j) {
-      const int place = __ldcg(a.places + (size_t)t * a.top + j);
-      if (place < 0 || place >= a.n_pairs) {
-        if (place != -1) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
-        continue;
+    for (int j0 = 0; j0 < a.top; j0 += kAtOnce) {
+      int place[kAtOnce];
+      float w[kAtOnce], x[kAtOnce][V];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const bool there = j0 + j < a.top;
+        place[j] = there ? __ldcg(a.places + (size_t)t * a.top + j0 + j) : -1;
+        w[j] = there ? __ldcg(a.weights + (size_t)t * a.top + j0 + j) : 0.0f;
       }
-      const float w = __ldcg(a.weights + (size_t)t * a.top + j);
-      const float* src = a.part + (size_t)place * a.ld + (n - a.n0);
-      if constexpr (V == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-        y[0] = fmaf(w, x.x, y[0]);
-        y[1] = fmaf(w, x.y, y[1]);
-        y[2] = fmaf(w, x.z, y[2]);
-        y[3] = fmaf(w, x.w, y[3]);
-      } else {
-        y[0] = fmaf(w, __ldcg(src), y[0]);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (place[j] < -1 || place[j] >= a.n_pairs) {
+          atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
+          place[j] = -1;
+        }
+        const float* src = a.part + (size_t)max(place[j], 0) * a.ld + (n - a.n0);
+        if constexpr (V == 4) {
+          const float4 v = place[j] >= 0 ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
+        } else {
+          x[j][0] = place[j] >= 0 ? __ldcg(src) : 0.0f;
+        }
       }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (place[j] >= 0) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) y[v] = fmaf(w[j], x[j][v], y[v]);
+        }
     }
     float* dst = a.y + (size_t)t * a.N + n;
     if constexpr (V == 4)
