@@ -443,7 +443,9 @@ NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, W
   using S = Shape<NT, MODE, FEW>;
   constexpr int kS = S::kStages;
   const bool lead = elect_one() != 0u;
-  const uint32_t base = smem_u32(sm.base);
+  // operands of the first stage; another stage's are an addition to the address field
+  const uint64_t da0 = smem_desc_sw128(smem_u32(sm.base)), db0 = smem_desc_sw128(smem_u32(sm.base + S::kOffX));
+  const uint64_t dwa0 = smem_desc_rows16(smem_u32(sm.base + kWCodes)), dxa0 = smem_desc_rows16(smem_u32(sm.base + S::kOffXS));
   Segment sg;
   Buffers bufs;
   int s = 0, k = 0;
@@ -465,9 +467,9 @@ NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, W
       ready = __all_sync(0xffffffffu, mbar_test_wait(&sm.full[next], next_phase));
       if (lead) {
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(buf * S::kHalf), slot = base + (uint32_t)(s * S::kSlot);
-        const uint64_t da = smem_desc_sw128(slot), db = smem_desc_sw128(slot + S::kOffX);
-        const uint64_t dwa = smem_desc_rows16(slot + kWCodes), dxa = smem_desc_rows16(slot + S::kOffXS);
+        const uint32_t d = tmem + (uint32_t)(buf * S::kHalf);
+        const uint64_t at = (uint64_t)(s * (S::kSlot >> 4));
+        const uint64_t da = da0 + at, db = db0 + at, dwa = dwa0 + at, dxa = dxa0 + at;
         const uint32_t sfa = tmem + S::kColSF + S::kSFStage * (uint32_t)s, sfb = sfa + 16u;
         const uint32_t idesc = idesc_for(sg.n);          // of the first 128 places; the others are another MMA's
         const int mmas = min(4, (a.K - (sg.c0 + c) * kChunk) / 64);
@@ -724,7 +726,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const ExpertArg
 // ---- many tokens: UP, PART -----------------------------------------------------------
 constexpr int kManyWarps = 12;               // 0 weights, 1 products, 2 rows of x, 4-11 the accumulator
 constexpr int kManyThreads = 32 * kManyWarps;
-constexpr int kBoxRows = 32;                 // rows of x of a copy
+constexpr int kBoxRows = 64;                 // rows of x of a copy (2048 tokens, up: 137 us; 32: 141)
 
 template <int NT, int MODE>
 __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_constant__ CUtensorMap tm_x,
@@ -890,6 +892,7 @@ struct CombineArgs {
 };
 
 constexpr int kAtOnce = 8;                   // products of a token that are read together
+constexpr int kCombineCtas = 16;              // CTAs an SM: each goes through several tokens
 
 template <int V>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
@@ -897,36 +900,45 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
   griddep_wait();
   const int n = a.n0 + (blockIdx.x * 256 + threadIdx.x) * V;
   if (n >= a.n1) return;
+  // places and weights are read a token ahead
+  auto look = [&](int t, int j0, int (&place)[kAtOnce], float (&w)[kAtOnce]) {
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const bool there = t < a.tokens && j0 + j < a.top;
+      place[j] = there ? __ldcg(a.places + (size_t)t * a.top + j0 + j) : -1;
+      w[j] = there ? __ldcg(a.weights + (size_t)t * a.top + j0 + j) : 0.0f;
+    }
+  };
+  int place[kAtOnce];
+  float w[kAtOnce];
+  look(blockIdx.y, 0, place, w);
   for (int t = blockIdx.y; t < a.tokens; t += gridDim.y) {
     float y[V] = {};
     for (int j0 = 0; j0 < a.top; j0 += kAtOnce) {
-      int place[kAtOnce];
-      float w[kAtOnce], x[kAtOnce][V];
+      float x[kAtOnce][V];
+      bool there[kAtOnce];
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
-        const bool there = j0 + j < a.top;
-        place[j] = there ? __ldcg(a.places + (size_t)t * a.top + j0 + j) : -1;
-        w[j] = there ? __ldcg(a.weights + (size_t)t * a.top + j0 + j) : 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        if (place[j] < -1 || place[j] >= a.n_pairs) {
-          atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
-          place[j] = -1;
-        }
-        const float* src = a.part + (size_t)max(place[j], 0) * a.ld + (n - a.n0);
+        there[j] = place[j] >= 0 && place[j] < a.n_pairs;
+        if (!there[j] && place[j] != -1) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
+        const float* src = a.part + (size_t)(there[j] ? place[j] : 0) * a.ld + (n - a.n0);
         if constexpr (V == 4) {
-          const float4 v = place[j] >= 0 ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 v = there[j] ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
           x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
         } else {
-          x[j][0] = place[j] >= 0 ? __ldcg(src) : 0.0f;
+          x[j][0] = there[j] ? __ldcg(src) : 0.0f;
         }
       }
+      float wj[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) wj[j] = w[j];
+      const bool more = j0 + kAtOnce < a.top;
+      look(more ? t : t + gridDim.y, more ? j0 + kAtOnce : 0, place, w);
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j)
-        if (place[j] >= 0) {
+        if (there[j]) {
 #pragma unroll
-          for (int v = 0; v < V; ++v) y[v] = fmaf(w[j], x[j][v], y[v]);
+          for (int v = 0; v < V; ++v) y[v] = fmaf(wj[j], x[j][v], y[v]);
         }
     }
     float* dst = a.y + (size_t)t * a.N + n;
@@ -1073,8 +1085,9 @@ cudaError_t arrange(const ExpertArgs& a, uint8_t* codes, uint8_t* blocks, CUtens
   return launch(moe_arrange_kernel, grid, kArrangeThreads, 0, 1, stream, g);
 }
 
-// Most bytes of products that wait for their sum: they stay in L2 (129 MB) between the two kernels.
-constexpr long long kSlabBytes = 64 << 20;
+// Most bytes of products that wait for their sum: above, y is done in slabs of columns.  Smaller slabs that stay in L2 (129 MB)
+// cost their launches and gained nothing (2048 tokens of 8 experts, N 4096, K 768: 32 MB 206 us, 64 184, 128 177, 512 170).
+constexpr long long kSlabBytes = 512ll << 20;
 
 int slab_tiles(const ExpertArgs& a) {
   const long long per = (long long)a.n_pairs * kTR * 4, fit = kSlabBytes / per;
@@ -1239,7 +1252,8 @@ extern "C" nvfp4_status nvfp4_moe_down(const uint8_t* hq, const uint8_t* hs, con
     const int n0 = a.rt0 * kTR, n1 = (a.rt0 + a.rts) * kTR < N ? (a.rt0 + a.rts) * kTR : N;
     const CombineArgs c = {a.out, weights, places, y, tokens, top_k, N, a.n_pairs, n0, n1, a.rts * kTR};
     const int per = N % 4 == 0 ? 1024 : 256;
-    const dim3 grid2((unsigned)((n1 - n0 + per - 1) / per), (unsigned)(tokens < 65535 ? tokens : 65535));
+    const int across = (n1 - n0 + per - 1) / per, down = (kCombineCtas * sms + across - 1) / across;
+    const dim3 grid2((unsigned)across, (unsigned)(tokens < down ? tokens : down));
     e = N % 4 == 0 ? launch(moe_combine_kernel<4>, grid2, 256, 0, 1, stream, c)
                    : launch(moe_combine_kernel<1>, grid2, 256, 0, 1, stream, c);
     if (e != cudaSuccess) break;

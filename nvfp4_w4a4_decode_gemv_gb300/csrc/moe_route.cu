@@ -2,7 +2,7 @@
 // and the plan of the (token, expert) pairs by expert that the experts'
 // products read.
 //
-// A warp takes a token; a lane holds experts lane, lane + 32, ...  The choice is
+// A warp takes a token; a lane holds NV experts that follow one another.  The choice is
 // top_k rounds of a warp maximum over order-preserving integer keys (equal keys:
 // the lowest expert).  Without a bias the keys are the logits themselves, since
 // both scores grow with them: exact.  With a bias, or with groups ranked by the
@@ -28,6 +28,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTop = 32;
 constexpr int kMaxGroups = 32;
+constexpr int kOneCta = 64;               // tokens that one CTA routes and plans by itself
 constexpr int kMaxCtas = 152;             // of a call: bounds the workspace; one CTA an SM
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
@@ -47,6 +48,8 @@ struct RouteArgs {
   float* weights;
   int tokens, groups, each, top_groups, group_best;
   uint32_t inv_each;                      // 2^20 / each, rounded up: expert * inv_each >> 20 is its group (expert < 512)
+  int lanes;                              // of a group, where groups are whole lanes and a power of two of them; else 0
+  int vector;                             // rows are read in 16-byte pieces
   int sigmoid, renormalize;
   float scale;
 };
@@ -88,53 +91,105 @@ NVFP4_DEVINL double warp_sum(double v) {
   return v;
 }
 
-// The largest key of the warp and the lowest index that has it (index < 2^16); best and at: the lane's own.
+// The largest key of the warp and the lowest lane that has it: lanes hold ascending experts.
 template <class K>
-NVFP4_DEVINL K warp_best(K best, int at, int& winner) {
+NVFP4_DEVINL K warp_best(K best, int& lane_of) {
   const K m = warp_max(best);
-  winner = (int)__reduce_min_sync(kAll, best == m ? (uint32_t)at : 0xFFFFu);
+  lane_of = __ffs(__ballot_sync(kAll, best == m)) - 1;
   return m;
 }
 
-// The groups that stay, as a mask: the top_groups best by the sum of their group_best (1 or 2) largest values.  unsure:
-// the first group left out is within 2 err of the last one kept.
-template <class F, int NV>
-NVFP4_DEVINL uint32_t best_groups(const RouteArgs& a, const F (&v)[NV], int lane, F err, bool& unsure) {
-  using K = typename KeyOf<F>::T;
-  K mine = 0;                                             // lane g: the key of group g's score
-  for (int g = 0; g < a.groups; ++g) {
-    K first = 0, second = 0;
+// A lane's largest key and the first of its experts that has it.
+template <class K, int NV>
+NVFP4_DEVINL K lane_best(const K (&key)[NV], int& at) {
+  K best = key[0];
+  at = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = i * 32 + lane;
-      if (e < a.plan.experts && (int)(((uint32_t)e * a.inv_each) >> 20) == g) {
-        const K k = key_of(v[i]);
-        if (k > first) {
-          second = first;
-          first = k;
-        } else if (k > second) {
-          second = k;
-        }
+  for (int i = 1; i < NV; ++i)
+    if (key[i] > best) {
+      best = key[i];
+      at = i;
+    }
+  return best;
+}
+
+// The two largest of (a0 >= a1) and (b0 >= b1).
+template <class K>
+NVFP4_DEVINL void merge_two(K& a0, K& a1, K b0, K b1) {
+  const K lo = a0 < b0 ? a0 : b0, second = a1 > b1 ? a1 : b1;
+  a0 = a0 > b0 ? a0 : b0;
+  a1 = lo > second ? lo : second;
+}
+NVFP4_DEVINL uint32_t shfl_xor(uint32_t k, int o) { return __shfl_xor_sync(kAll, k, o); }
+NVFP4_DEVINL unsigned long long shfl_xor(unsigned long long k, int o) { return __shfl_xor_sync(kAll, k, o); }
+
+template <class K, int NV>
+NVFP4_DEVINL void lane_two(const K (&key)[NV], K& first, K& second) {
+  first = key[0];
+  second = 0;
+#pragma unroll
+  for (int i = 1; i < NV; ++i) merge_two<K>(first, second, key[i], 0);
+}
+
+// Keys of a group's score: its largest value, or the sum of its two largest.
+template <class F, class K>
+NVFP4_DEVINL K group_score(const RouteArgs& a, K first, K second) {
+  return a.group_best == 2 && a.each > 1 ? key_of(value_of(first) + value_of(second)) : first;
+}
+
+// Bit i: the group of this lane's expert i is one of the top_groups best by the sum of their group_best (1 or 2) largest
+// values.  unsure: the first group left out is within 2 err of the last one kept.
+template <class F, int NV>
+NVFP4_DEVINL uint32_t kept_experts(const RouteArgs& a, const F (&v)[NV], int lane, F err, bool& unsure) {
+  using K = typename KeyOf<F>::T;
+  K key[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) key[i] = lane * NV + i < a.plan.experts ? key_of(v[i]) : 0;
+  K mine, last = 0;                          // the score of the lane's group, or of group `lane`
+  uint32_t kept = 0u;
+  if (a.lanes > 0) {
+    // a group is `lanes` (a power of two) whole lanes: all groups at once
+    K second;
+    lane_two<K, NV>(key, mine, second);
+    for (int o = 1; o < a.lanes; o <<= 1) merge_two<K>(mine, second, shfl_xor(mine, o), shfl_xor(second, o));
+    mine = lane * NV < a.plan.experts ? group_score<F, K>(a, mine, second) : 0;
+    for (int j = 0; j <= a.top_groups && j < a.groups; ++j) {
+      int l;
+      const K m = warp_best(mine, l);
+      if (j == a.top_groups) {
+        if (!(value_of(last) - value_of(m) > 2 * err)) unsure = true;
+        break;
+      }
+      last = m;
+      if (lane / a.lanes == l / a.lanes) {
+        kept = kAll;
+        mine = 0;
       }
     }
-    int owner;
-    const K m1 = warp_best(first, lane, owner);
-    K score = m1;
-    if (a.group_best == 2 && a.each > 1) score = key_of(value_of(m1) + value_of(warp_max(lane == owner ? second : first)));
-    if (lane == g) mine = score;
+    return kept;
   }
-  uint32_t kept = 0u;
-  K last = 0;
+  mine = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    K in[NV], first, second;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) in[i] = (int)(((uint32_t)(lane * NV + i) * a.inv_each) >> 20) == g ? key[i] : 0;
+    lane_two<K, NV>(in, first, second);
+    int owner;
+    const K m1 = warp_best(first, owner);
+    const K m2 = warp_max(lane == owner ? second : first);
+    if (lane == g) mine = group_score<F, K>(a, m1, m2);
+  }
   for (int j = 0; j <= a.top_groups && j < a.groups; ++j) {
     int g;
-    const K m = warp_best(mine, lane, g);
+    const K m = warp_best(mine, g);
     if (j == a.top_groups) {
       if (!(value_of(last) - value_of(m) > 2 * err)) unsure = true;
       break;
     }
-    kept |= 1u << g;
-    if (lane == g) mine = 0;
     last = m;
+    if (lane == g) mine = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) kept |= (int)(((uint32_t)(lane * NV + i) * a.inv_each) >> 20) == g ? 1u << i : 0u;
   }
   return kept;
 }
@@ -145,41 +200,28 @@ template <class F, int NV>
 NVFP4_DEVINL int pick(const RouteArgs& a, const F (&c)[NV], const F (&v)[NV], int lane, F c_err, F v_err, bool& unsure) {
   using K = typename KeyOf<F>::T;
   unsure = false;
-  uint32_t kept = kAll;
-  if (a.top_groups < a.groups) kept = best_groups<F, NV>(a, v, lane, v_err, unsure);
+  const uint32_t kept = a.top_groups < a.groups ? kept_experts<F, NV>(a, v, lane, v_err, unsure) : kAll;
   K key[NV];
-  K best = 0;
-  int at = lane;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = i * 32 + lane;
-    key[i] = e < a.plan.experts && (a.groups == 1 || (kept >> (((uint32_t)e * a.inv_each) >> 20) & 1u)) ? key_of(c[i]) : 0;
-    if (key[i] > best) {
-      best = key[i];
-      at = e;
-    }
-  }
+  for (int i = 0; i < NV; ++i) key[i] = lane * NV + i < a.plan.experts && (kept >> i & 1u) ? key_of(c[i]) : 0;
+  int at;
+  K best = lane_best<K, NV>(key, at);
   int mine = -1;
   K last = 0;
   const int rounds = a.plan.top + (c_err > 0 ? 1 : 0);    // one more looks at the first that is left out
   for (int j = 0; j < rounds; ++j) {
-    int e;
-    const K m = warp_best(best, at, e);
+    int owner;
+    const K m = warp_best(best, owner);
     if (m == 0) break;                                    // nothing is left out
     if (j > 0 && c_err > 0 && !(value_of(last) - value_of(m) > 2 * c_err)) unsure = true;
     last = m;
-    if (lane == j) mine = e;
-    if (lane == (e & 31)) {
-      best = 0;
-      at = lane;
+    const int i_of = __shfl_sync(kAll, at, owner);
+    if (lane == j) mine = owner * NV + i_of;
+    if (lane == owner) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (i * 32 + lane == e) key[i] = 0;
-        if (key[i] > best) {
-          best = key[i];
-          at = i * 32 + lane;
-        }
-      }
+      for (int i = 0; i < NV; ++i)
+        if (i == at) key[i] = 0;
+      best = lane_best<K, NV>(key, at);
     }
   }
   return mine;
@@ -192,7 +234,7 @@ __device__ __noinline__ int pick_exact(const RouteArgs& a, const T* row, int lan
   double m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = i * 32 + lane;
+    const int e = lane * NV + i;
     x[i] = e < a.plan.experts ? (double)load1(row + e) + 0.0 : -INFINITY;
     m = fmax(m, x[i]);
   }
@@ -207,12 +249,46 @@ __device__ __noinline__ int pick_exact(const RouteArgs& a, const T* row, int lan
   z = a.sigmoid ? 1.0 : warp_sum(z);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = i * 32 + lane;
+    const int e = lane * NV + i;
     v[i] = v[i] / z + (a.bias && e < a.plan.experts ? (double)a.bias[e] : 0.0);
     if (a.bias) x[i] = v[i];
   }
   bool unsure;
   return pick<double, NV>(a, x, v, lane, 0.0, 0.0, unsure);
+}
+
+// A lane's NV elements of a row, -inf beyond the experts; whole 16-byte pieces where the rows allow it.
+template <int NV>
+NVFP4_DEVINL void load_row(const RouteArgs& a, const float* row, int lane, float (&x)[NV]) {
+  if constexpr (NV % 4 == 0) {
+    if (a.vector && lane * NV + NV <= a.plan.experts) {
+#pragma unroll
+      for (int i = 0; i < NV / 4; ++i) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(row + lane * NV) + i);
+        x[4 * i] = u.x, x[4 * i + 1] = u.y, x[4 * i + 2] = u.z, x[4 * i + 3] = u.w;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) x[i] = lane * NV + i < a.plan.experts ? load1(row + lane * NV + i) : -INFINITY;
+}
+template <int NV>
+NVFP4_DEVINL void load_row(const RouteArgs& a, const uint16_t* row, int lane, float (&x)[NV]) {
+  if constexpr (NV % 8 == 0) {
+    if (a.vector && lane * NV + NV <= a.plan.experts) {
+#pragma unroll
+      for (int i = 0; i < NV / 8; ++i) {
+        const uint4 u = __ldcg(reinterpret_cast<const uint4*>(row + lane * NV) + i);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[8 * i + 2 * j] = bf16_lo(w[j]), x[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) x[i] = lane * NV + i < a.plan.experts ? load1(row + lane * NV + i) : -INFINITY;
 }
 
 // One token by one warp: lane j < top_k returns its expert (-1: none) and writes it with its weight.
@@ -226,31 +302,34 @@ NVFP4_DEVINL int route_row(const RouteArgs& a, int token, int lane) {
     float x[NV], v[NV];
     float m = -INFINITY;
     bool bad = false;
+    load_row<NV>(a, row, lane, x);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = i * 32 + lane;
-      x[i] = e < E ? load1(row + e) + 0.0f : -INFINITY;   // (+ 0: both zeros are one value)
+      x[i] += 0.0f;                                       // (both zeros are one value)
       bad = bad || isnan(x[i]);
       m = fmaxf(m, x[i]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-    if (!a.sigmoid) bad = bad || isinf(m);
     float z = 1.0f, c_err = 0.0f, v_err = 0.0f;
+    if (!a.sigmoid) {
+      m = value_of(warp_max(key_of(m)));
+      bad = bad || isinf(m);
+    }
     const bool sums = a.top_groups < a.groups && a.group_best == 2;
     if (a.bias || sums || (!a.sigmoid && !a.renormalize)) {
+      // For the choice alone, with approximate exponentials and quotients, since their error is bounded and the weights
+      // are computed again.
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        v[i] = a.sigmoid ? __fdiv_rn(1.0f, 1.0f + expf(-x[i])) : expf(x[i] - m);
+        v[i] = a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-x[i])) : __expf(x[i] - m);
         sum += v[i];
       }
-      if (!a.sigmoid) z = warp_sum(sum);
+      const float inv = a.sigmoid ? 1.0f : __fdividef(1.0f, warp_sum(sum));
       float most = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e = i * 32 + lane;
-        if (!a.sigmoid) v[i] = __fdiv_rn(v[i], z);
+        const int e = lane * NV + i;
+        v[i] *= inv;
         if (a.bias && e < E) {
           v[i] += a.bias[e];
           bad = bad || isnan(v[i]);
@@ -259,17 +338,23 @@ NVFP4_DEVINL int route_row(const RouteArgs& a, int token, int lane) {
         if (e < E) most = fmaxf(most, fabsf(v[i]));
       }
       most = __uint_as_float(warp_max(__float_as_uint(most)));
-      // |v - exact| is below this.  Sigmoid: 2 ulp of expf, half a one each of sum, quotient and bias.  Softmax, each score
-      // at most 1 / z: x - m loses 2^-24 |x - m|, which e^(x - m) makes 2^-25.4 of 1 at most; expf 2^-22 of each term and
-      // of their sum; the sum of up to 512 terms 21 halves of an ulp, the quotient one: 2^-18.8 in all.  A sum of two
-      // values doubles it.
-      const float score = a.sigmoid ? 0x1p-21f : 0x1p-18f * fminf(1.0f, __fdiv_rn(1.0f, z)) + 0x1p-24f;
+      // |v - exact| is below this.  __expf(t) is off by 2 + 1.173 |t| ulp, __fdividef by 2.  Sigmoid: e^-x is weighed with
+      // s (1 - s), which makes at most 0.6 ulp of it; sum, quotient and bias add 3: 2^-21.  Softmax, each score at most
+      // 1 / z = inv: (2 + 1.173 |t|) e^t is at most 2 ulp of the largest term, x - m loses half of one; z is off by 21
+      // half ulps of up to 512 terms' sum and by 2.5 ulp of its terms' mean: 2^-18.7 of inv in all.  A sum of two values
+      // doubles it.  (e^-x that overflows gives 0 and is off by 2^-126.)
+      const float score = a.sigmoid ? 0x1p-20f : 0x1p-18f * fminf(1.0f, inv) + 0x1p-24f;
       v_err = 2.0f * (score + 0x1p-23f * most);
       if (a.bias) c_err = score + 0x1p-23f * most;
-      if (!sums && !a.bias) v_err = 0.0f;
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] = x[i];
+    }
+    if (!a.sigmoid && !a.renormalize) {
+      float sum = 0.0f;                                   // for the weights
+#pragma unroll
+      for (int i = 0; i < NV; ++i) sum += expf(x[i] - m);
+      z = warp_sum(sum);
     }
     bad = __any_sync(kAll, bad);
     if (!bad) {
@@ -287,9 +372,7 @@ NVFP4_DEVINL int route_row(const RouteArgs& a, int token, int lane) {
       const float xc = chosen ? load1(row + max(id, 0)) + 0.0f : -INFINITY;
       if (a.renormalize) {
         // exp(x) / (1 + exp(x)) and exp(x) alike, relative to the largest of the chosen: no sum underflows
-        float xm = xc;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) xm = fmaxf(xm, __shfl_xor_sync(kAll, xm, o));
+        const float xm = value_of(warp_max(key_of(xc)));
         float t = 0.0f;
         if (chosen && xm > -INFINITY)
           t = a.sigmoid ? __fdiv_rn(expf(fminf(xc, 0.0f) - fminf(xm, 0.0f)), 1.0f + expf(-fabsf(xc))) : expf(xc - xm);
@@ -329,15 +412,16 @@ NVFP4_DEVINL void first_of_experts(const int* s_tot, int* s_first, int n) {
   if (lane == 31) s_first[n] = at;
 }
 
-// This CTA's pairs [p0, p1) to their places; s_next[e]: the next place of expert e; s_warp: kWarps * experts ints.
-NVFP4_DEVINL void place_pairs(const PlanArgs& a, long long p0, long long p1, int* s_next, int* s_warp) {
+// This CTA's pairs [p0, p1) to their places; ids: theirs from p0 on; s_next[e]: the next place of expert e; s_warp:
+// kWarps * experts ints.
+NVFP4_DEVINL void place_pairs(const PlanArgs& a, const int32_t* ids, long long p0, long long p1, int* s_next, int* s_warp) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = a.experts;
   for (long long p = p0; p < p1; p += kThreads) {
     const int warps = (int)((min(p1 - p, (long long)kThreads) + 31) / 32);   // that have pairs
     for (int i = tid; i < warps * E; i += kThreads) s_warp[i] = 0;
     __syncthreads();
     const long long pair = p + tid;
-    int e = pair < p1 ? __ldcg(a.ids + pair) : -1;
+    int e = pair < p1 ? ids[pair - p0] : -1;
     if (e < 0 || e >= E) e = -1;
     const uint32_t same = __match_any_sync(kAll, e);
     const int rank = __popc(same & ((1u << lane) - 1u));
@@ -373,6 +457,7 @@ extern __shared__ int s_dyn[];            // kWarps * experts, where a plan is m
 template <int NV, class T>
 __global__ void __launch_bounds__(kThreads) moe_route_kernel(const RouteArgs a) {
   __shared__ int s_cnt[kMaxExperts], s_first[kMaxExperts + 1];
+  __shared__ int32_t s_ids[kOneCta * kMaxTop];             // of the one CTA's tokens
   const PlanArgs& pl = a.plan;
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -385,15 +470,17 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(const RouteArgs a) 
     for (int t = t0 + warp; t < t1; t += kWarps) {
       const int id = route_row<NV, T>(a, t, lane);
       if (id >= 0) atomicAdd(&s_cnt[id], 1);
+      if (!pl.counts && lane < pl.top) s_ids[t * pl.top + lane] = id;
     }
   } else {
     for (long long p = p0 + tid; p < p1; p += kThreads) {
       const int id = pl.ids[p];
+      if (!pl.counts) s_ids[p] = id;
       if (id >= 0 && id < pl.experts) atomicAdd(&s_cnt[id], 1);
       else if (id != -1) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
     }
   }
-  __syncthreads();                        // (and the ids are visible to the CTA)
+  __syncthreads();
   if (pl.counts) {
     for (int i = tid; i < pl.experts; i += kThreads) pl.counts[(size_t)blockIdx.x * pl.experts + i] = s_cnt[i];
     return;
@@ -403,7 +490,7 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(const RouteArgs a) 
   for (int i = tid; i <= pl.experts; i += kThreads) pl.offsets[i] = s_first[i];
   fill_pairs(pl, 0, pl.n_pairs, s_first[pl.experts]);
   __syncthreads();                        // s_first turns into the next places
-  place_pairs(pl, p0, p1, s_first, s_dyn);
+  place_pairs(pl, s_ids, p0, p1, s_first, s_dyn);
 }
 
 __global__ void __launch_bounds__(kThreads) moe_place_kernel(const PlanArgs a) {
@@ -436,7 +523,7 @@ __global__ void __launch_bounds__(kThreads) moe_place_kernel(const PlanArgs a) {
   fill_pairs(a, p0, p1, s_first[E]);
   for (int i = tid; i < E; i += kThreads) s_tot[i] = s_first[i] + s_before[i];
   __syncthreads();
-  place_pairs(a, p0, p1, s_tot, s_dyn);
+  place_pairs(a, a.ids + p0, p0, p1, s_tot, s_dyn);
 }
 
 template <class Args>
@@ -456,13 +543,26 @@ cudaError_t launch(void (*kern)(Args), int grid, size_t smem, const Args& a, cud
 
 using RouteKernel = void (*)(RouteArgs);
 
+// Experts of a lane: the least that is built.
+constexpr int kPerLane[] = {1, 2, 4, 5, 8, 12, 16};
+
+int per_lane(int experts) {
+  for (int nv : kPerLane)
+    if (32 * nv >= experts) return nv;
+  return 16;
+}
+
 template <class T>
-RouteKernel kernel_for(int experts) {
-  if (experts <= 32) return moe_route_kernel<1, T>;
-  if (experts <= 64) return moe_route_kernel<2, T>;
-  if (experts <= 128) return moe_route_kernel<4, T>;
-  if (experts <= 256) return moe_route_kernel<8, T>;
-  return moe_route_kernel<16, T>;
+RouteKernel kernel_for(int nv) {
+  switch (nv) {
+    case 1: return moe_route_kernel<1, T>;
+    case 2: return moe_route_kernel<2, T>;
+    case 4: return moe_route_kernel<4, T>;
+    case 5: return moe_route_kernel<5, T>;
+    case 8: return moe_route_kernel<8, T>;
+    case 12: return moe_route_kernel<12, T>;
+    default: return moe_route_kernel<16, T>;
+  }
 }
 
 // The largest dynamic shared memory that a plan takes, allowed once a device for every kernel here.
@@ -470,22 +570,18 @@ cudaError_t allow_smem() {
   static PerDeviceInt done;
   cudaError_t err = cudaSuccess;
   done.get([](int, cudaError_t* e_out) -> int {
-    const RouteKernel all[] = {moe_route_kernel<0, float>, moe_route_kernel<1, float>, moe_route_kernel<2, float>,
-                               moe_route_kernel<4, float>, moe_route_kernel<8, float>, moe_route_kernel<16, float>,
-                               moe_route_kernel<1, uint16_t>, moe_route_kernel<2, uint16_t>, moe_route_kernel<4, uint16_t>,
-                               moe_route_kernel<8, uint16_t>, moe_route_kernel<16, uint16_t>};
     const int bytes = kWarps * kMaxExperts * (int)sizeof(int);
     cudaError_t e = cudaFuncSetAttribute(moe_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    for (RouteKernel k : all)
-      if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(moe_route_kernel<0, float>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    for (int nv : kPerLane)
+      for (RouteKernel k : {kernel_for<float>(nv), kernel_for<uint16_t>(nv)})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     *e_out = e;
     return e == cudaSuccess ? 1 : 0;
   }, &err);
   return err;
 }
-
-// Tokens that one CTA routes and plans by itself.
-constexpr int kOneCta = 64;
 
 int ctas_for(int tokens) {
   if (tokens <= kOneCta) return 1;
@@ -565,8 +661,11 @@ extern "C" nvfp4_status nvfp4_moe_route(const void* logits, int dtype, int token
   a.group_best = r->group_best, a.sigmoid = r->score == NVFP4_MOE_SIGMOID, a.renormalize = r->renormalize != 0;
   a.scale = r->scale;
   a.inv_each = ((1u << 20) + a.each - 1) / a.each;
-  return nvfp4_internal_cuda_status(
-      run(dtype == NVFP4_DTYPE_F32 ? kernel_for<float>(experts) : kernel_for<uint16_t>(experts), a, stream));
+  const int nv = per_lane(experts), lanes = a.each % nv == 0 ? a.each / nv : 0;
+  a.lanes = lanes > 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  const int per = dtype == NVFP4_DTYPE_F32 ? 4 : 8;          // elements of 16 bytes
+  a.vector = nvfp4_internal_aligned(logits, 16) && (tokens < 2 || ld % per == 0);
+  return nvfp4_internal_cuda_status(run(dtype == NVFP4_DTYPE_F32 ? kernel_for<float>(nv) : kernel_for<uint16_t>(nv), a, stream));
 }
 
 extern "C" nvfp4_status nvfp4_moe_plan(const int32_t* ids, int tokens, int top_k, int experts, int32_t* offsets,
