@@ -8,8 +8,8 @@
 // both scores grow with them: exact.  With a bias, or with groups ranked by the
 // sum of two scores, the values are FP32 with a bound on their error; a token
 // whose order that bound does not settle is chosen again from 64-bit values
-// (one in some hundreds of tokens), so that the result is the one of the
-// formulas in 64 bits.
+// of the experts in question (one in some hundreds of tokens), so that the result
+// is the one of the formulas in 64 bits.
 //
 // The plan is a stable counting sort: counts of a CTA's tokens by expert, sums
 // over the CTAs before it, then ranks in the CTA by warp matches.  Every sum is of
@@ -194,13 +194,11 @@ NVFP4_DEVINL uint32_t kept_experts(const RouteArgs& a, const F (&v)[NV], int lan
   return kept;
 }
 
-// Lane j's choice j (j < top_k).  c: what the choice goes by, v: what the groups go by.  unsure: two neighbours in the
-// order, the first left out among them, are within 2 err.
+// Lane j's choice j (j < top_k) of the experts kept; c: what it goes by.  unsure: two neighbours in the order, the first left
+// out among them, are within 2 err.  kth: the value of the last one chosen.
 template <class F, int NV>
-NVFP4_DEVINL int pick(const RouteArgs& a, const F (&c)[NV], const F (&v)[NV], int lane, F c_err, F v_err, bool& unsure) {
+NVFP4_DEVINL int choose(const RouteArgs& a, const F (&c)[NV], uint32_t kept, int lane, F err, bool& unsure, F& kth) {
   using K = typename KeyOf<F>::T;
-  unsure = false;
-  const uint32_t kept = a.top_groups < a.groups ? kept_experts<F, NV>(a, v, lane, v_err, unsure) : kAll;
   K key[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) key[i] = lane * NV + i < a.plan.experts && (kept >> i & 1u) ? key_of(c[i]) : 0;
@@ -208,13 +206,13 @@ NVFP4_DEVINL int pick(const RouteArgs& a, const F (&c)[NV], const F (&v)[NV], in
   K best = lane_best<K, NV>(key, at);
   int mine = -1;
   K last = 0;
-  const int rounds = a.plan.top + (c_err > 0 ? 1 : 0);    // one more looks at the first that is left out
+  const int rounds = a.plan.top + (err > 0 ? 1 : 0);      // one more looks at the first that is left out
   for (int j = 0; j < rounds; ++j) {
     int owner;
     const K m = warp_best(best, owner);
     if (m == 0) break;                                    // nothing is left out
-    if (j > 0 && c_err > 0 && !(value_of(last) - value_of(m) > 2 * c_err)) unsure = true;
-    last = m;
+    if (j > 0 && err > 0 && !(value_of(last) - value_of(m) > 2 * err)) unsure = true;
+    if (j < a.plan.top) last = m;
     const int i_of = __shfl_sync(kAll, at, owner);
     if (lane == j) mine = owner * NV + i_of;
     if (lane == owner) {
@@ -224,37 +222,118 @@ NVFP4_DEVINL int pick(const RouteArgs& a, const F (&c)[NV], const F (&v)[NV], in
       best = lane_best<K, NV>(key, at);
     }
   }
+  kth = value_of(last);
   return mine;
 }
 
-// The choice from 64-bit values.
+// ---- the choice where FP32 does not settle it ------------------------------------------
+// From 64-bit values of the experts that FP32 leaves in question, as a rule a handful.  A 64-bit exponential and quotient
+// take a warp 2 us whether one lane needs them or all do: candidates are dealt out to the lanes, 32 at a time.
+struct Scratch {                             // of a warp
+  double value[32];
+  int expert[32];
+};
+
+__device__ __noinline__ double score64(bool sigmoid, double x, double m, double z) {
+  const double e = exp(sigmoid ? -x : x - m);
+  return sigmoid ? 1.0 / (1.0 + e) : e / z;
+}
+
+// d[i] = the 64-bit value of each of this lane's experts i with bit i of `which` set.
 template <int NV, class T>
-__device__ __noinline__ int pick_exact(const RouteArgs& a, const T* row, int lane) {
-  double x[NV], v[NV];
-  double m = -INFINITY;
+NVFP4_DEVINL void exact_values(const RouteArgs& a, const T* row, Scratch& s, uint32_t which, double m, double z, int lane,
+                               double (&d)[NV]) {
+  const int n = __popc(which);
+  int first = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kAll, first, o);
+    if (lane >= o) first += x;
+  }
+  const int total = __shfl_sync(kAll, first, 31);
+  first -= n;
+#pragma unroll 1
+  for (int at = 0; at < total; at += 32) {
+    int k = first - at;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (which >> i & 1u) {
+        if (k >= 0 && k < 32) s.expert[k] = lane * NV + i;
+        ++k;
+      }
+    __syncwarp();
+    if (at + lane < total) {
+      const int e = s.expert[lane];
+      const double v = score64(a.sigmoid != 0, (double)load1(row + e), m, z);
+      s.value[lane] = a.bias ? v + (double)a.bias[e] : v;
+    }
+    __syncwarp();
+    k = first - at;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (which >> i & 1u) {
+        if (k >= 0 && k < 32) d[i] = s.value[k];
+        ++k;
+      }
+    __syncwarp();
+  }
+}
+
+// v: the FP32 values, off by err (groups: sums of two of them by v_err) at most.
+template <int NV, class T>
+__device__ __noinline__ int settle(const RouteArgs& a, const T* row, Scratch& s, const float* px, const float* pv, float m,
+                                   float err, float v_err, int lane) {
+  float x[NV], v[NV];
+  double d[NV];
+  uint32_t all = 0u;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = lane * NV + i;
-    x[i] = e < a.plan.experts ? (double)load1(row + e) + 0.0 : -INFINITY;
-    m = fmax(m, x[i]);
+    x[i] = px[i];
+    v[i] = pv[i];
+    d[i] = -INFINITY;
+    all |= lane * NV + i < a.plan.experts ? 1u << i : 0u;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kAll, m, o));
-  double z = 0.0;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    v[i] = a.sigmoid ? 1.0 / (1.0 + exp(-x[i])) : exp(x[i] - m);
-    z += v[i];
+  double z = 1.0;
+  if (!a.sigmoid && a.bias) {                // (without a bias, scores of one token may do without their sum)
+    z = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < NV; ++i)
+      if (all >> i & 1u) z += score64(false, (double)load1(row + lane * NV + i), m, 1.0);
+    z = warp_sum(z);
   }
-  z = a.sigmoid ? 1.0 : warp_sum(z);
+  uint32_t kept = kAll, known = 0u;
+  bool unused = false;
+  if (a.top_groups < a.groups) {
+    known = all;                             // groups across lanes: all of them
+    if (a.lanes > 0) {
+      // of a group, what may be one of its group_best largest
+      uint32_t key[NV], first, second;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = lane * NV + i;
-    v[i] = v[i] / z + (a.bias && e < a.plan.experts ? (double)a.bias[e] : 0.0);
-    if (a.bias) x[i] = v[i];
+      for (int i = 0; i < NV; ++i) key[i] = all >> i & 1u ? key_of(v[i]) : 0u;
+      lane_two<uint32_t, NV>(key, first, second);
+      for (int o = 1; o < a.lanes; o <<= 1) merge_two<uint32_t>(first, second, shfl_xor(first, o), shfl_xor(second, o));
+      const float least = value_of(a.group_best == 2 && a.each > 1 ? second : first);
+      known = 0u;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) known |= !(v[i] < least - 2.0f * v_err) ? 1u << i : 0u;
+      known &= all;
+    }
+    exact_values<NV>(a, row, s, known, m, z, lane, d);
+    kept = kept_experts<double, NV>(a, d, lane, 0.0, unused);
   }
-  bool unsure;
-  return pick<double, NV>(a, x, v, lane, 0.0, 0.0, unsure);
+  float kth;
+  if (!a.bias) return choose<float, NV>(a, x, kept, lane, 0.0f, unused, kth);
+  choose<float, NV>(a, v, kept, lane, 0.0f, unused, kth);
+  uint32_t close = 0u;                       // what may be one of the chosen
+#pragma unroll
+  for (int i = 0; i < NV; ++i) close |= !(v[i] < kth - 2.0f * err) ? 1u << i : 0u;
+  close &= kept & all;
+  exact_values<NV>(a, row, s, close & ~known, m, z, lane, d);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (!(close >> i & 1u)) d[i] = -INFINITY;
+  double last;
+  return choose<double, NV>(a, d, kept, lane, 0.0, unused, last);
 }
 
 // A lane's NV elements of a row, -inf beyond the experts; whole 16-byte pieces where the rows allow it.
@@ -293,7 +372,7 @@ NVFP4_DEVINL void load_row(const RouteArgs& a, const uint16_t* row, int lane, fl
 
 // One token by one warp: lane j < top_k returns its expert (-1: none) and writes it with its weight.
 template <int NV, class T>
-NVFP4_DEVINL int route_row(const RouteArgs& a, int token, int lane) {
+NVFP4_DEVINL int route_row(const RouteArgs& a, Scratch& scratch, int token, int lane) {
   const int E = a.plan.experts, top = a.plan.top;
   int id = -1;
   float w = 0.0f;
@@ -358,16 +437,21 @@ NVFP4_DEVINL int route_row(const RouteArgs& a, int token, int lane) {
     }
     bad = __any_sync(kAll, bad);
     if (!bad) {
-      bool unsure;
-      if (a.bias) {
-        id = pick<float, NV>(a, v, v, lane, c_err, v_err, unsure);
-      } else if (sums) {
-        id = pick<float, NV>(a, x, v, lane, 0.0f, v_err, unsure);
-      } else {
-        id = pick<float, NV>(a, x, x, lane, 0.0f, 0.0f, unsure);
-        unsure = false;                                   // logits: equal ones are equal
+      bool unsure = false;
+      float kth;
+      uint32_t kept = kAll;
+      const bool by_value = a.bias || sums;
+      if (a.top_groups < a.groups)
+        kept = by_value ? kept_experts<float, NV>(a, v, lane, v_err, unsure) : kept_experts<float, NV>(a, x, lane, 0.0f, unsure);
+      if (!by_value) unsure = false;                      // logits: equal ones are equal
+      id = a.bias ? choose<float, NV>(a, v, kept, lane, c_err, unsure, kth)
+                  : choose<float, NV>(a, x, kept, lane, 0.0f, unsure, kth);
+      if (unsure) {
+        float px[NV], pv[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) px[i] = x[i], pv[i] = v[i];
+        id = settle<NV, T>(a, row, scratch, px, pv, m, c_err, v_err, lane);
       }
-      if (unsure) id = pick_exact<NV, T>(a, row, lane);
       const bool chosen = lane < top;
       const float xc = chosen ? load1(row + max(id, 0)) + 0.0f : -INFINITY;
       if (a.renormalize) {
@@ -458,6 +542,7 @@ template <int NV, class T>
 __global__ void __launch_bounds__(kThreads) moe_route_kernel(const RouteArgs a) {
   __shared__ int s_cnt[kMaxExperts], s_first[kMaxExperts + 1];
   __shared__ int32_t s_ids[kOneCta * kMaxTop];             // of the one CTA's tokens
+  __shared__ Scratch s_scratch[NV > 0 ? kWarps : 1];
   const PlanArgs& pl = a.plan;
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -468,7 +553,7 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(const RouteArgs a) 
   const long long p0 = (long long)t0 * pl.top, p1 = (long long)t1 * pl.top;
   if constexpr (NV > 0) {
     for (int t = t0 + warp; t < t1; t += kWarps) {
-      const int id = route_row<NV, T>(a, t, lane);
+      const int id = route_row<NV, T>(a, s_scratch[warp], t, lane);
       if (id >= 0) atomicAdd(&s_cnt[id], 1);
       if (!pl.counts && lane < pl.top) s_ids[t * pl.top + lane] = id;
     }
