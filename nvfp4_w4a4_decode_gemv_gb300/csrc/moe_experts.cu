@@ -84,7 +84,7 @@ struct ExpertArgs {
   const int32_t *offsets, *pairs;
   const float* weights;                      // SUM
   uint16_t* h;                               // UP: [n_pairs, inter]
-  float* out;                                // SUM: y [tokens, N]; PART: [n_pairs, columns of the call]
+  float* out;                                // SUM: y [tokens, N]; PART: [rts][n_pairs][kTR]
   int tokens, top, experts, N, K, C, RT;     // N: columns of y, or of h
   int rt0, rts;                              // row tiles of the call
   int n_pairs;
@@ -187,8 +187,9 @@ NVFP4_DEVINL void build_table(const ExpertArgs& a, Table& tb) {
   tb.total = tb.sums[2];
 }
 
-// Every role's warp walks the CTA's segments by itself, in the same order; its lanes look an item up together (one by one
-// along the experts took 3700 cycles a segment, as long as 5 stages).
+// Every role's warp walks the CTA's segments by itself, in the same order.  UP, PART: its lanes look up the next 32 items, one
+// each, and hand them out one by one (looked up when they were wanted, by the warp together, each took 700 cycles, as long as
+// a stage).
 template <int NT, int MODE>
 struct Walk {
   const Table& tb;
@@ -196,7 +197,10 @@ struct Walk {
   int it, end;                               // UP, PART: item; SUM: unit (tile of places, chunk)
   int used, tile;                            // SUM: the entry and its tile that `it` stands in, -1: to be looked up
   int rank, step;
-  NVFP4_DEVINL Walk(const Table& t, const ExpertArgs& args) : tb(t), a(args), used(-1), tile(0) {
+  int c0, nc;                                // UP, PART: the rank's chunks
+  Segment mine;                              // UP, PART: the lane's of the 32 items, and how many of them are handed out
+  int handed;
+  NVFP4_DEVINL Walk(const Table& t, const ExpertArgs& args) : tb(t), a(args), used(-1), tile(0), handed(32) {
     rank = args.cluster > 1 ? (int)cluster_ctarank() : 0;
     if (MODE == SUM) {
       const long long units = (long long)t.tiles * a.C;
@@ -207,23 +211,41 @@ struct Walk {
       it = blockIdx.x / a.cluster;
       end = t.tiles * a.rts;
       step = gridDim.x / a.cluster;
+      c0 = a.C * rank / a.cluster;
+      nc = a.C * (rank + 1) / a.cluster - c0;
     }
   }
-  // The last entry whose tiles, times `of`, begin at x or before.
-  NVFP4_DEVINL int entry_of(int x, int of) const {
+  // The last entry whose tiles begin at x or before, by a whole warp.
+  NVFP4_DEVINL int entry_of(int x) const {
     const int lane = threadIdx.x & 31, per = (tb.used + 31) / 32, at = lane * per;
-    const int piece = __popc(__ballot_sync(0xffffffffu, at < tb.used && tb.tiles_before[at] * of <= x)) - 1;
+    const int piece = __popc(__ballot_sync(0xffffffffu, at < tb.used && tb.tiles_before[at] <= x)) - 1;
     const int i = piece * per + lane;
-    return piece * per + __popc(__ballot_sync(0xffffffffu, lane < per && i < tb.used && tb.tiles_before[i] * of <= x)) - 1;
+    return piece * per + __popc(__ballot_sync(0xffffffffu, lane < per && i < tb.used && tb.tiles_before[i] <= x)) - 1;
+  }
+  NVFP4_DEVINL void place(Segment& s, int u, int t) const {   // tile t of entry u
+    s.e = tb.expert[u];
+    s.p0 = tb.first[u] + t * NT;
+    s.n = min(NT, tb.count[u] - t * NT);
+    s.block = tb.blocks[u] + t * (NT / 128);
+  }
+  NVFP4_DEVINL void look_up(int item) {
+    int u = 0;                               // the last entry whose items begin at `item` or before
+    for (int hi = tb.used; hi - u > 1;) {
+      const int mid = (u + hi) >> 1;
+      if (tb.tiles_before[mid] * a.rts <= item) u = mid; else hi = mid;
+    }
+    const int in = item - tb.tiles_before[u] * a.rts, tt = (tb.count[u] + NT - 1) / NT;
+    mine.rt = tt == 1 ? in : in / tt;        // an expert's items: the tiles of places of a row tile follow one another
+    place(mine, u, in - mine.rt * tt);
+    mine.rt += a.rt0;
   }
   // By a whole warp.
   NVFP4_DEVINL bool next(Segment& s) {
     if (it >= end) return false;
-    int t;
     if (MODE == SUM) {
       if (used < 0) {
         const int at = it / a.C;
-        used = entry_of(at, 1);
+        used = entry_of(at);
         tile = at - tb.tiles_before[used];
         s.c0 = it - at * a.C;
       } else {
@@ -233,24 +255,27 @@ struct Walk {
           ++used;
         }
       }
-      t = tile;
+      place(s, used, tile);
       s.rt = blockIdx.x / a.cluster;
       s.nc = min(a.C - s.c0, end - it);
       it += s.nc;
     } else {
-      used = entry_of(it, a.rts);
-      const int in = it - tb.tiles_before[used] * a.rts, tt = (tb.count[used] + NT - 1) / NT;
-      s.rt = tt == 1 ? in : in / tt;         // an expert's items: the tiles of places of a row tile follow one another
-      t = in - s.rt * tt;
-      s.rt += a.rt0;
-      s.c0 = a.C * rank / a.cluster;
-      s.nc = a.C * (rank + 1) / a.cluster - s.c0;
-      it += step;
+      if (handed == 32) {
+        const int lane = threadIdx.x & 31;
+        if ((long long)lane * step < end - it) look_up(it + lane * step);
+        handed = 0;
+        __syncwarp();
+      }
+      s.e = __shfl_sync(0xffffffffu, mine.e, handed);
+      s.p0 = __shfl_sync(0xffffffffu, mine.p0, handed);
+      s.n = __shfl_sync(0xffffffffu, mine.n, handed);
+      s.rt = __shfl_sync(0xffffffffu, mine.rt, handed);
+      s.block = __shfl_sync(0xffffffffu, mine.block, handed);
+      s.c0 = c0;
+      s.nc = nc;
+      ++handed;
+      it = step < end - it ? it + step : end;
     }
-    s.e = tb.expert[used];
-    s.p0 = tb.first[used] + t * NT;
-    s.n = min(NT, tb.count[used] - t * NT);
-    s.block = tb.blocks[used] + t * (NT / 128);
     return true;
   }
 };
@@ -292,10 +317,10 @@ NVFP4_DEVINL uint64_t smem_desc_rows16(uint32_t saddr) {
          ((uint64_t)1 << 46);
 }
 
-// E2M1 x E2M1, UE4M3 scales, K-major operands, M = 128 and N = n rounded up to 16, 32, 64 or 128 (an MMA takes 64 cycles
-// whatever its N up to 128).
+// E2M1 x E2M1, UE4M3 scales, K-major operands, M = 128 and N = n rounded up to 16, 32, 64, 128, 192 or 256 (an MMA takes 64
+// cycles whatever its N up to 128).
 NVFP4_DEVINL uint32_t idesc_for(int n) {
-  const uint32_t eighths = n <= 16 ? 2u : n <= 32 ? 4u : n <= 64 ? 8u : 16u;
+  const uint32_t eighths = n <= 16 ? 2u : n <= 32 ? 4u : n <= 64 ? 8u : n <= 128 ? 16u : n <= 192 ? 24u : 32u;
   return (1u << 7) | (1u << 10) | (eighths << 17) | ((uint32_t)(kTR >> 4) << 24);
 }
 
@@ -471,7 +496,7 @@ NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, W
         const uint64_t at = (uint64_t)(s * (S::kSlot >> 4));
         const uint64_t da = da0 + at, db = db0 + at, dwa = dwa0 + at, dxa = dxa0 + at;
         const uint32_t sfa = tmem + S::kColSF + S::kSFStage * (uint32_t)s, sfb = sfa + 16u;
-        const uint32_t idesc = idesc_for(sg.n);          // of the first 128 places; the others are another MMA's
+        const uint32_t idesc = idesc_for(sg.n);
         const int mmas = min(4, (a.K - (sg.c0 + c) * kChunk) / 64);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -485,9 +510,6 @@ NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, W
           if (q < mmas) {
             const uint32_t acc = c > 0 || q > 0 ? 1u : 0u;
             mma_mxf4nvf4(d, da + 2 * q, db + 2 * q, idesc, sfa + 4u * q, sfb + 4u * S::kHalves * q, acc);
-            if (both)
-              mma_mxf4nvf4(d + 128u, da + 2 * q, db + (uint64_t)(128 * 128 / 16 + 2 * q), idesc_for(sg.n - 128),
-                           sfa + 4u * q, sfb + 8u * q + 4u, acc);
           }
         mma_commit(&sm.empty[s]);
         if (c == sg.nc - 1) {
@@ -724,7 +746,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const ExpertArg
 }
 
 // ---- many tokens: UP, PART -----------------------------------------------------------
-constexpr int kManyWarps = 12;               // 0 weights, 1 products, 2 rows of x, 4-11 the accumulator
+// 0 weights, 1 products, 2 rows of x, 4-19 the accumulator: with 16 of them a warp holds all its columns of a buffer in
+// registers, so that the buffer is free before they are stored (2048 tokens of 8 of 128 experts, K 4096 and 1536 rows up,
+// K 768 and 4096 rows down: 135 and 155 us; 8 warps, 16 columns at a time: 137 and 157).
+constexpr int kManyWarps = 20;
+constexpr int kReaders = kManyWarps - 4;
 constexpr int kManyThreads = 32 * kManyWarps;
 constexpr int kBoxRows = 64;                 // rows of x of a copy (2048 tokens, up: 137 us; 32: 141)
 
@@ -736,7 +762,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     prefetch_tmap(&tm_x);
-    sm.init_barriers(2, 8);
+    sm.init_barriers(2, kReaders);
   }
   if (warp == 1) sm.alloc_tmem();
   griddep_launch_dependents();
@@ -768,7 +794,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
         bulk_g2s(slot + S::kOffXS + h * kXBlock, a.x_blocks + ((size_t)(sg.block + h) * a.C + c) * kXBlock, kXBlock, bar);
     });
   } else if (warp >= 4) {
-    // ---------------- the accumulator: two warps a lane quadrant, 16 columns in turn ----------------
+    // ---------------- the accumulator: four warps a lane quadrant, 16 columns in turn ----------------
     const int p = warp & 3, row = p * 32 + lane, part = (warp - 4) >> 2;
     const float xg = __ldcg(a.xg);
     Buffers bufs;
@@ -786,25 +812,30 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
         }
         tc_fence_after();
         const uint32_t d = tmem + ((uint32_t)(p * 32) << 16) + (uint32_t)(buf * S::kHalf);
+        // All of the warp's columns to registers first, so that the buffer is free while they are stored.
+        constexpr int kGroups = (S::kHalf + 16 * (kReaders / 4) - 1) / (16 * (kReaders / 4));
         const int end = min(sg.n - half * 128, S::kHalf);
-#pragma unroll 1
-        for (int m0 = 16 * part; m0 < end; m0 += 32) {
-          float v[16];
-          __syncwarp();
-          read16(d + (uint32_t)m0, v);
-          if (MODE == UP) {
-            store_h16(a, sg, p, half * 128 + m0, v, scale);
-          } else {
-            const int n = (sg.rt - a.rt0) * kTR + row, m = half * 128 + m0;
-            float* dst = a.out + (size_t)(sg.p0 + m) * (a.rts * kTR) + n;
+        float v[kGroups][16];
+        __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (m + i < sg.n) dst[(size_t)i * (a.rts * kTR)] = v[i] * scale;
-          }
-        }
+        for (int g = 0; g < kGroups; ++g)
+          if (16 * part + 4 * kReaders * g < end) read16(d + (uint32_t)(16 * part + 4 * kReaders * g), v[g]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.acc_empty[buf]);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          const int m = half * 128 + 16 * part + 4 * kReaders * g;
+          if (m >= sg.n) break;
+          if (MODE == UP) {
+            store_h16(a, sg, p, m, v[g], scale);
+          } else {
+            float* dst = a.out + ((size_t)(sg.rt - a.rt0) * a.n_pairs + sg.p0 + m) * kTR + row;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (m + i < sg.n) dst[i * kTR] = v[g][i] * scale;
+          }
+        }
       }
       bufs.took(both);
     }
@@ -885,10 +916,10 @@ __global__ void __launch_bounds__(kArrangeThreads) moe_arrange_kernel(const Arra
 
 // y[t, n] = sum_j weights[t, j] part[places[t, j], n], in the order of j: a thread has V columns of a token.
 struct CombineArgs {
-  const float *part, *weights;               // part: [n_pairs, ld], columns [n0, n1) of y
+  const float *part, *weights;               // part: [column / 128][n_pairs][128], columns [n0, n1) of y
   const int32_t* places;
   float* y;
-  int tokens, top, N, n_pairs, n0, n1, ld;
+  int tokens, top, N, n_pairs, n0, n1;
 };
 
 constexpr int kAtOnce = 8;                   // products of a token that are read together
@@ -900,6 +931,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
   griddep_wait();
   const int n = a.n0 + (blockIdx.x * 256 + threadIdx.x) * V;
   if (n >= a.n1) return;
+  const size_t column = (size_t)((n - a.n0) / kTR) * a.n_pairs;
   // places and weights are read a token ahead
   auto look = [&](int t, int j0, int (&place)[kAtOnce], float (&w)[kAtOnce]) {
 #pragma unroll
@@ -921,7 +953,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
       for (int j = 0; j < kAtOnce; ++j) {
         there[j] = place[j] >= 0 && place[j] < a.n_pairs;
         if (!there[j] && place[j] != -1) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
-        const float* src = a.part + (size_t)(there[j] ? place[j] : 0) * a.ld + (n - a.n0);
+        const float* src = a.part + (column + (there[j] ? place[j] : 0)) * kTR + n % kTR;
         if constexpr (V == 4) {
           const float4 v = there[j] ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
           x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
@@ -1250,7 +1282,7 @@ extern "C" nvfp4_status nvfp4_moe_down(const uint8_t* hq, const uint8_t* hs, con
     e = nt == 64 ? run_many<64, PART>(grid, map, a, stream) : run_many<256, PART>(grid, map, a, stream);
     if (e != cudaSuccess) break;
     const int n0 = a.rt0 * kTR, n1 = (a.rt0 + a.rts) * kTR < N ? (a.rt0 + a.rts) * kTR : N;
-    const CombineArgs c = {a.out, weights, places, y, tokens, top_k, N, a.n_pairs, n0, n1, a.rts * kTR};
+    const CombineArgs c = {a.out, weights, places, y, tokens, top_k, N, a.n_pairs, n0, n1};
     const int per = N % 4 == 0 ? 1024 : 256;
     const int across = (n1 - n0 + per - 1) / per, down = (kCombineCtas * sms + across - 1) / across;
     const dim3 grid2((unsigned)across, (unsigned)(tokens < down ? tokens : down));
