@@ -340,6 +340,14 @@ NVFP4_DEVINL float ld_dsmem_f32(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+NVFP4_DEVINL float4 ld_dsmem_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 
 NVFP4_DEVINL float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
@@ -684,6 +692,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const ExpertArg
           const int t_lane = pr >= 0 ? pr / a.top : -1;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
+            if (i % 4 == 0 && m0 + i >= cur.n) break;         // (most segments of a decode batch have a few places)
             const int t = __shfl_sync(0xffffffffu, t_lane, l0 + i);
             const float w = __shfl_sync(0xffffffffu, wt, l0 + i);
             if (m0 + i < cur.n && t >= 0) {
@@ -708,14 +717,28 @@ __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const ExpertArg
 
   // ---------------- the cluster's parts ----------------
   __syncwarp();
-  if (a.cluster > 1) cluster_sync();
-  if (MODE == SUM && warp >= 6) {
-    const int row = (warp & 3) * 32 + lane, n = blockIdx.x / a.cluster * kTR + row;
-    for (int t = walk.rank; t < a.tokens; t += a.cluster) {
-      float y = 0.0f;
-      for (int r = 0; r < a.cluster; ++r)                       // in the order of the ranks
-        y += r == walk.rank ? sm.sums[t * kTR + row] : ld_dsmem_f32(dsmem_addr(&sm.sums[t * kTR + row], (uint32_t)r));
-      if (n < a.N) a.out[(size_t)t * a.N + n] = y;
+  if (a.cluster > 1) cluster_sync(); else __syncthreads();
+  if (MODE == SUM) {
+    // a warp a token; all ranks' parts are read together (one by one, 64 tokens of 3 ranks took 10 us) and added in their order
+    const int n = blockIdx.x / a.cluster * kTR + 4 * lane;
+    for (int t = walk.rank + a.cluster * warp; t < a.tokens; t += a.cluster * kFewWarps) {
+      float4 x[kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < a.cluster) x[r] = ld_dsmem_f32x4(dsmem_addr(&sm.sums[t * kTR + 4 * lane], (uint32_t)r));
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < a.cluster) y.x += x[r].x, y.y += x[r].y, y.z += x[r].z, y.w += x[r].w;
+      float* dst = a.out + (size_t)t * a.N + n;
+      if (a.N % 4 == 0) {
+        if (n < a.N) *reinterpret_cast<float4*>(dst) = y;
+      } else {
+        if (n < a.N) dst[0] = y.x;
+        if (n + 1 < a.N) dst[1] = y.y;
+        if (n + 2 < a.N) dst[2] = y.z;
+        if (n + 3 < a.N) dst[3] = y.w;
+      }
     }
   }
   if (MODE == UP && a.cluster > 1 && warp >= 6) {
@@ -726,8 +749,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const ExpertArg
       const float scale = __fmul_rn(__ldcg(a.xg), __ldcg(a.wg + sg.e));
       const float* stage = reinterpret_cast<const float*>(sm.base);
       for (int m = walk.rank; m < sg.n; m += a.cluster) {
-        float v = 0.0f;
-        for (int r = 0; r < a.cluster; ++r) v += ld_dsmem_f32(dsmem_addr(&stage[m * kTR + row], (uint32_t)r));
+        float x[kMaxCluster], v = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < a.cluster) x[r] = ld_dsmem_f32(dsmem_addr(&stage[m * kTR + row], (uint32_t)r));
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < a.cluster) v += x[r];
         v *= scale;
         const float other = __shfl_xor_sync(0xffffffffu, v, 1);
         if (!(lane & 1) && i < a.N)
