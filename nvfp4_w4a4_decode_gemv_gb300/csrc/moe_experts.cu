@@ -539,17 +539,17 @@ extern __shared__ __align__(1024) uint8_t smem_raw[];
 // ---- few tokens: UP, SUM ------------------------------------------------------------
 constexpr int kFewWarps = 10;
 constexpr int kFewThreads = 32 * kFewWarps;
-constexpr int kLoaders = 128;                // warps 2-5
-constexpr int kLag = 2;                      // stages whose row copies are in flight behind the one that is issued
+constexpr int kLoaders = 4;                  // warps 2-5
 
 template <int NT, int MODE>
 __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const ExpertArgs a) {
   using S = Shape<NT, MODE, true>;
   constexpr int kS = S::kStages;
-  static_assert(S::kHalves == 1 && kLag < kS, "one buffer a segment; a stage is handed over before the ring comes round");
+  static_assert(S::kHalves == 1 && kLoaders <= kS && (kLoaders & (kLoaders - 1)) == 0,
+                "one buffer a segment; a loader looks at a stage's release when those of two rounds before are over");
   const Smem<NT, MODE, true> sm(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) sm.init_barriers(1 + kLoaders / 32, 4);
+  if (threadIdx.x == 0) sm.init_barriers(2, 4);
   if (warp == 1) sm.alloc_tmem();
   griddep_launch_dependents();
   griddep_wait();                            // the plan comes from a preceding kernel
@@ -573,65 +573,64 @@ __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const ExpertArg
     multiply(sm, a, walk, tmem);
   } else if (warp < 6) {
     // ---------------- rows of x ----------------
-    const int lt = threadIdx.x - 64;
+    // A warp a stage: the fence that hands a stage over waits for all that its warp has under way, so a warp has no other
+    // (with all four on a stage, each fenced every stage: 64 tokens of 8 of 128 experts, N 5120, K 768 took 62 us).
+    const int mine = warp - 2, piece = lane & 7, q = lane & 3;
     const size_t row_codes = (size_t)a.K / 2, row_scales = (size_t)a.K / 16;
-    int s = 0, k = 0;
-    uint32_t phase = 0;
+    constexpr int kCols = (NT + 31) / 32;
+    int row[kCols];                            // rows of x of places lane, lane + 32 (the lowest one for a place of no pair)
     bool ok = true;
-    // stage j's copies of this warp are in place: the MMAs read them through the asynchronous proxy
-    auto hand_over = [&](int j) {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.full[j % kS]);
-    };
-    // the row of x at a place (the lowest one for a place of no pair)
-    auto row_at = [&](int place) {
-      if (MODE != UP) return place;
-      const int pair = __ldcg(a.pairs + place);
-      const bool in = pair >= 0 && pair < a.n_pairs;
-      if (!in) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
-      return in ? pair / a.top : 0;
-    };
-    // a thread copies piece lt % 8 of rows lt / 8 + 16 i, and scale word lt % 4 of rows lt / 4 + 32 i
-    constexpr int kRC = NT / 16, kRS = (NT + 31) / 32;
-    const int piece = lt & 7, q = lt & 3, rc = lt >> 3, rs = lt >> 2;
-    while (ok && walk.next(sg)) {
-      int row_c[kRC], row_s[kRS];
+    for (int k = 0; ok && walk.next(sg); k += sg.nc) {
+      int c = (mine - k) & (kLoaders - 1);
+      if (c >= sg.nc) continue;
 #pragma unroll
-      for (int i = 0; i < kRC; ++i) row_c[i] = rc + 16 * i < sg.n ? row_at(sg.p0 + rc + 16 * i) : -1;
-#pragma unroll
-      for (int i = 0; i < kRS; ++i) row_s[i] = rs + 32 * i < sg.n ? row_at(sg.p0 + rs + 32 * i) : -1;
-      for (int c = sg.c0; c < sg.c0 + sg.nc; ++c) {
-        if (k >= kS && !mbar_wait_warp(&sm.empty[s], phase ^ 1u)) {
+      for (int i = 0; i < kCols; ++i) {
+        const int place = lane + 32 * i;
+        row[i] = place < sg.n ? sg.p0 + place : 0;
+        if (MODE == UP && place < sg.n) {
+          const int pair = __ldcg(a.pairs + row[i]);
+          const bool in = pair >= 0 && pair < a.n_pairs;
+          if (!in) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
+          row[i] = in ? pair / a.top : 0;
+        }
+      }
+      auto row_of = [&](int r) {               // of place r < NT, by the whole warp
+        int x = __shfl_sync(0xffffffffu, row[0], r & 31);
+        if (kCols > 1) {
+          const int y = __shfl_sync(0xffffffffu, row[kCols - 1], r & 31);
+          x = r >= 32 ? y : x;
+        }
+        return x;
+      };
+      for (; c < sg.nc; c += kLoaders) {
+        const int s = (k + c) % kS, chunk = sg.c0 + c;
+        // (the release before that one, two rounds ago, is over: stages are released in order, and this warp has waited for
+        // that of kLoaders stages ago)
+        if (k + c >= kS && !mbar_wait_warp(&sm.empty[s], (uint32_t)((k + c) / kS - 1) & 1u)) {
           ok = false;
           break;
         }
         const uint32_t slot = smem_u32(sm.base) + (uint32_t)(s * S::kSlot);
-        if (c * 128 + piece * 16 < (int)row_codes) {
-          const uint32_t dst = slot + S::kOffX + rc * 128 + ((piece ^ (rc & 7)) << 4);     // (16 i does not move the swizzle)
-          const uint8_t* src = a.xc + c * 128 + piece * 16;
-#pragma unroll
-          for (int i = 0; i < kRC; ++i)
-            if (row_c[i] >= 0) async_copy16(dst + 2048 * i, src + row_c[i] * row_codes);
+        const bool in_c = chunk * 128 + piece * 16 < (int)row_codes, in_s = chunk * 16 + q * 4 < (int)row_scales;
+#pragma unroll 4
+        for (int r0 = 0; r0 < sg.n; r0 += 4) {
+          const int r = r0 + (lane >> 3), from = row_of(r);
+          if (in_c && r < sg.n)
+            async_copy16(slot + S::kOffX + r * 128 + ((piece ^ (r & 7)) << 4), a.xc + from * row_codes + chunk * 128 + piece * 16);
         }
-        if (c * 16 + q * 4 < (int)row_scales) {
-          const uint32_t dst = slot + S::kOffXS + q * 512 + rs * 16;                         // row rs + 32 i: word i
-          const uint8_t* src = a.xs + c * 16 + q * 4;
-#pragma unroll
-          for (int i = 0; i < kRS; ++i)
-            if (row_s[i] >= 0) async_copy4(dst + i * 4, src + row_s[i] * row_scales);
+#pragma unroll 2
+        for (int r0 = 0; r0 < sg.n; r0 += 8) {
+          const int r = r0 + (lane >> 2), from = row_of(r);
+          if (in_s && r < sg.n)
+            async_copy4(slot + S::kOffXS + q * 512 + (r & 31) * 16 + (r >> 5) * 4, a.xs + from * row_scales + chunk * 16 + q * 4);
         }
         async_commit();
-        if (k >= kLag) {
-          async_wait<kLag>();
-          hand_over(k - kLag);
-        }
-        ++k;
-        if (++s == kS) { s = 0; phase ^= 1u; }
+        async_wait<0>();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMAs read through the asynchronous proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.full[s]);
       }
     }
-    async_wait<0>();
-    for (int j = k > kLag ? k - kLag : 0; j < k; ++j) hand_over(j);
   } else {
     // ---------------- the accumulator ----------------
     const int p = warp & 3, row = p * 32 + lane;
