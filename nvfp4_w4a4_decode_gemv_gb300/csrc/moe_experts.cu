@@ -466,11 +466,12 @@ NVFP4_DEVINL void copy_weights(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& 
   });
 }
 
-// Scales to TMEM and products, by one warp.  It waits together; one lane then issues a stage's copies, products and commit
-// in one branch, with the others held at its end.  (Predicated one by one, with the other lanes free to run ahead, they
-// faulted once several stages were ready: operands are in uniform registers, which the lanes that run ahead overwrite.)
-// The next stage's barrier is looked at before a stage's instructions are issued: behind them, the look would wait until
-// the tensor core has taken them (300 cycles a stage of 1000).
+// Scales to TMEM and products, by one warp: it looks a segment up and waits for its accumulator together; one lane then takes
+// all of the segment's stages, with the others held until it is through.  (Instructions predicated lane by lane, with the
+// other lanes free to run ahead, faulted once several stages were ready: operands are in uniform registers, which the lanes
+// that run ahead overwrite.  A vote and a branch for each stage cost 2 % more than one for a segment.)  The next stage's
+// barrier is looked at before a stage's instructions are issued: behind them, the look would wait until the tensor core has
+// taken them (300 cycles).
 template <int NT, int MODE, bool FEW>
 NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, Walk<NT, MODE> walk, uint32_t tmem) {
   using S = Shape<NT, MODE, FEW>;
@@ -481,7 +482,7 @@ NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, W
   const uint64_t dwa0 = smem_desc_rows16(smem_u32(sm.base + kWCodes)), dxa0 = smem_desc_rows16(smem_u32(sm.base + S::kOffXS));
   Segment sg;
   Buffers bufs;
-  int s = 0, k = 0;
+  int s = 0, k = 0;                          // of the lane that issues
   uint32_t phase = 0;
   bool ok = true, ready = false;
   while (ok && walk.next(sg)) {
@@ -490,21 +491,21 @@ NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, W
     if (bufs.uses(buf) > 0 && !mbar_wait_warp(&sm.acc_empty[buf], (bufs.uses(buf) - 1) & 1)) break;
     if (both && bufs.uses1 > 0 && !mbar_wait_warp(&sm.acc_empty[1], (bufs.uses1 - 1) & 1)) break;
     bufs.took(both);
-    for (int c = 0; c < sg.nc; ++c) {
-      if (!ready && !mbar_wait_warp(&sm.full[s], phase)) {
-        ok = false;
-        break;
-      }
-      const int next = s + 1 == kS ? 0 : s + 1;
-      const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
-      ready = __all_sync(0xffffffffu, mbar_test_wait(&sm.full[next], next_phase));
-      if (lead) {
+    const uint32_t idesc = idesc_for(sg.n), d = tmem + (uint32_t)(buf * S::kHalf);
+    int good = 1;
+    if (lead) {
+      for (int c = 0; c < sg.nc; ++c) {
+        if (!ready && !mbar_wait(&sm.full[s], phase)) {
+          good = 0;
+          break;
+        }
+        const int next = s + 1 == kS ? 0 : s + 1;
+        const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
+        ready = mbar_test_wait(&sm.full[next], next_phase);
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(buf * S::kHalf);
         const uint64_t at = (uint64_t)(s * (S::kSlot >> 4));
         const uint64_t da = da0 + at, db = db0 + at, dwa = dwa0 + at, dxa = dxa0 + at;
         const uint32_t sfa = tmem + S::kColSF + S::kSFStage * (uint32_t)s, sfb = sfa + 16u;
-        const uint32_t idesc = idesc_for(sg.n);
         const int mmas = min(4, (a.K - (sg.c0 + c) * kChunk) / 64);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -524,14 +525,15 @@ NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, W
           mma_commit(&sm.acc_full[buf]);
           if (both) mma_commit(&sm.acc_full[1]);
         }
+        ++k;
+        s = next;
+        phase = next_phase;
       }
-      __syncwarp();
-      ++k;
-      s = next;
-      phase = next_phase;
     }
+    ok = __all_sync(0xffffffffu, good);
   }
-  if (k > 0) mbar_wait_warp(&sm.empty[(k - 1) % kS], ((k - 1) / kS) & 1);   // not to leave with MMAs in flight
+  if (k > 0) mbar_wait(&sm.empty[(k - 1) % kS], ((k - 1) / kS) & 1);   // not to leave with MMAs in flight
+  __syncwarp();
 }
 
 extern __shared__ __align__(1024) uint8_t smem_raw[];
