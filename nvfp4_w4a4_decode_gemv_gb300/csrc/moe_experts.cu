@@ -927,19 +927,21 @@ __global__ void __launch_bounds__(kArrangeThreads) moe_arrange_kernel(const Arra
         make_uint4(w[0], w[1], w[2], w[3]);
   }
   if (!g.codes) return;
-  const int b0 = c0 * 128, pieces = (min(row_codes, c1 * 128) - b0) / 16;
-  for (int x = threadIdx.x; x < n * pieces; x += 4 * kArrangeThreads) {
+  // a warp a row's codes of the CTA's chunks
+  constexpr int kPieces = kArrangeChunks * 8;
+  const int b0 = c0 * 128, b1 = min(row_codes, c1 * 128);
+  for (int x = threadIdx.x; x < n * kPieces; x += 4 * kArrangeThreads) {
     uint4 v[4];
-    size_t to[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int y = x + i * kArrangeThreads, r = y / pieces, at = b0 + (y - r * pieces) * 16;
-      to[i] = (size_t)(p0 + r) * row_codes + at;
-      if (y < n * pieces) v[i] = __ldcg(reinterpret_cast<const uint4*>(a.xc + (size_t)s_row[r] * row_codes + at));
+      const int y = x + i * kArrangeThreads, r = y / kPieces, at = b0 + y % kPieces * 16;
+      if (r < n && at < b1) v[i] = __ldcg(reinterpret_cast<const uint4*>(a.xc + (size_t)s_row[r] * row_codes + at));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (x + i * kArrangeThreads < n * pieces) *reinterpret_cast<uint4*>(g.codes + to[i]) = v[i];
+    for (int i = 0; i < 4; ++i) {
+      const int y = x + i * kArrangeThreads, r = y / kPieces, at = b0 + y % kPieces * 16;
+      if (r < n && at < b1) *reinterpret_cast<uint4*>(g.codes + (size_t)(p0 + r) * row_codes + at) = v[i];
+    }
   }
 }
 
