@@ -641,7 +641,7 @@ nvfp4_status nvfp4_moe_pack_weights(const uint8_t* wq, const uint8_t* ws, int ex
  *   wpacked, wg  packed with gated != 0 (N = 2 inter), 16-byte aligned; [experts] FP32 global scales
  *   inter        a multiple of 64;  K a multiple of 64
  *   h            device, [tokens * top_k, inter] BF16, 16-byte aligned (written)
- *   workspace    device scratch of nvfp4_moe_gate_up_workspace_bytes bytes (0 up to 64 tokens), 256-byte aligned; no state
+ *   workspace    device scratch of nvfp4_moe_gate_up_workspace_bytes bytes (0 for few tokens), 256-byte aligned; no state
  * Only the weights of experts that have pairs are read.  Sums of a product are FP32 in an order that the shape and the
  * plan fix: the same inputs give the same bits.  Offsets, pairs and places outside their tables are taken into them or
  * skipped and record device error bit 6 (the rows concerned mean nothing).

@@ -2,30 +2,32 @@
 //   gate_up  h[p, i] = BF16(SiLU(g) u),  g = xg wg[e] x[t(p)] . w[e, gate row i],  u the same with up row i
 //   down     y[t, n] = sum_j weight[t, j] hg wg[e] h[place(t, j)] . w[e, n]
 //
-// As in the projections, 128 weight rows are the wide side of the MMA (kind::mxf4nvf4) and an expert's rows of x its
-// narrow side, here up to NT of them, N chosen at run time: the work of a tile is the bytes of its weights
-// however few rows the expert got.  Bound by HBM (each chosen expert's weights once) until an expert has some hundreds
-// of rows.
+// As in the projections, 128 weight rows are the wide side of the MMA (kind::mxf4nvf4) and an expert's rows of x its narrow
+// side, N chosen at run time: the work of a tile is the bytes of its weights however few rows the expert got.
 //
-// Weights are packed (nvfp4_moe_pack_weights) in blocks of 128 rows x 256 K, one bulk copy each; a block's scales stand
-// as tcgen05.cp wants them, so that they go from the block to TMEM without a thread's help.  Rows of gate and up
-// alternate: a TMEM lane and its neighbour hold both halves of an h.
-//
-// Roles of a CTA (one an SM):
-//   warp 0     weight blocks into a ring of S stages
-//   warp 1     scales to TMEM, 4 MMAs of K = 64 a stage, commits
-//   warps 2-5  rows of x into the stage: 16-byte asynchronous copies of the rows that the plan names, in the order of
-//              the 128-byte swizzle; their scales in the order of tcgen05.cp
-//   warps 6-9  the accumulator (two buffers up to 128 columns) to h, or to sums of y
+// Weights are packed (nvfp4_moe_pack_weights) in blocks of 128 rows x 256 K, one bulk copy each; a block's scales stand as
+// tcgen05.cp wants them, so that they go from the block to TMEM without a thread's help.  Rows of gate and up alternate: a
+// TMEM lane and its neighbour hold both halves of an h.
 //
 // Three modes:
-//   UP    items (expert, row tile, up to NT of its pairs) dealt out to the CTAs in turn; with fewer items than SMs a
-//         cluster splits an item's K and adds the parts over distributed shared memory.
-//   SUM   (down, few tokens) a cluster takes a tile of y's columns and shares out all the experts' K for it: every
-//         token's sum over its experts stays in shared memory and meets the other CTAs' there.  No workspace, one launch.
-//   PART  (down, many tokens) items as in UP; products go to a workspace [places, N], and a second kernel adds a
-//         token's products with its weights.
-// Nothing here waits for another CTA but at cluster barriers, and no state is left behind.
+//   UP    items (expert, row tile, up to NT of its pairs) dealt out to the CTAs in turn; with fewer items than SMs a cluster
+//         splits an item's K and adds the parts over distributed shared memory.
+//   SUM   (down, few tokens) a cluster takes a tile of y's columns and shares out all the experts' K for it: every token's sum
+//         over its experts stays in shared memory and meets the other CTAs' there.  No workspace, one launch.
+//   PART  (down, many tokens) items as in UP; products go to a workspace, and a second kernel adds a token's products with
+//         its weights.
+// No CTA waits for another but at cluster barriers, and no state is left behind.
+//
+// Measured (128 experts where not said; of the copy rate, 6.76 TB/s, what the bytes that a call cannot do without take):
+//   up, few places an expert   1 token of 8, K 4096, 2048 rows: 10.5 us (8.8 in a graph; 54 %), a launch, the table of the
+//                              experts (1.7 us) and the ramp of the copies; 8 tokens, K 5120, 1536 rows: 36 us (86 %); 33 tokens
+//                              of 2 of 8 experts, K 4096, 16384 rows: 48.6 us (92 %)
+//   up, many                   2048 tokens of 8, K 4096, 1536 rows: 134 us (1.54 PFLOP/s; 53 %): 15 us of laying out, then 75 us
+//                              of scale copies and MMAs (without its loads and stores the kernel takes 88) under 73 us of copies
+//   down, few tokens           1 token of 8, K 1024, 4096 rows: 8.2 us (34 %); 64 tokens, K 768, 5120 rows: 54 us (71 %), on the
+//                              120 SMs that 40 row tiles of 3 CTAs fill
+//   down, many                 2048 tokens, K 768, 4096 rows: 154 us (26 %): FP32 products written (268 MB, 87 us with the
+//                              products themselves) and read again (54 us at 5.4 TB/s)
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <string.h>
@@ -64,7 +66,7 @@ struct Shape {
   static constexpr int kOffXS = kOffX + NT * 128;
   static constexpr int kSlot = kOffXS + kHalves * kXBlock;
   static constexpr int kSums = MODE == SUM ? NT * kTR * 4 : 0;        // y of up to NT tokens
-  static constexpr int kStages = NT == 16 ? 9 : NT == 64 ? (MODE == SUM ? 6 : 7) : 4;
+  static constexpr int kStages = FEW ? (MODE == SUM ? 6 : 7) : 4;
   static constexpr uint32_t kColSF = 2u * kHalf;                      // first scale column, behind two buffers
   static constexpr uint32_t kSFStage = 16u + 16u * kHalves;           // weights' 4 x 4, tokens' 4 x 4 a half
   static constexpr int kOffSums = kStages * kSlot;
@@ -1112,7 +1114,11 @@ cudaError_t run_many(long long grid, const CUtensorMap& map, const ExpertArgs& a
   return launch(moe_many_kernel<NT, MODE>, dim3((unsigned)grid), kManyThreads, bytes, 1, stream, map, a);
 }
 
-// Tokens up to which y is summed in shared memory and x comes by the loaders.
+// Places of a tile: with few 64 (16 places are no faster for 1, 8 or 16 tokens: a stage's time is that of its weights), with
+// many 256 (1024 tokens of 8 of 128 experts, up: 112 us, with 64 places 136; with 16 places an expert as fast).
+constexpr int kFewTile = 64, kManyTile = 256;
+
+// Tokens up to which y is summed in shared memory.
 constexpr int kFewTokens = 64;
 
 long long used_experts(const ExpertArgs& a) { return a.n_pairs < a.experts ? a.n_pairs : a.experts; }
@@ -1123,8 +1129,10 @@ long long most_tiles(const ExpertArgs& a, int nt) {
   return used + (a.n_pairs - used) / nt;
 }
 
-// Places of a tile, many tokens: about the mean's double, so that most experts have one tile.
-int tile_for(const ExpertArgs& a) { return a.n_pairs <= 24 * used_experts(a) ? 64 : 256; }
+// Whether h goes without rows laid out first: few tokens, or few places an expert (K 4096, 1536 rows, 512 tokens of 8 of 128
+// experts, 32 places each: 85 us, laid out 101; K 4096, 16384 rows, 2 of 8 experts, 32 places each: 55 and 67, 64 places: 84
+// and 76).
+bool few_places(const ExpertArgs& a) { return a.tokens <= kFewTokens || a.n_pairs <= 32 * used_experts(a); }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 size_t codes_bytes(const ExpertArgs& a) { return align256((size_t)a.n_pairs * a.K / 2); }
@@ -1159,7 +1167,7 @@ int slab_tiles(const ExpertArgs& a) {
 
 // Whether a call's items and units are counted in 31 bits.
 bool too_many_items(const ExpertArgs& a) {
-  const long long tiles = most_tiles(a, 16);
+  const long long tiles = most_tiles(a, kFewTile);
   return tiles * a.RT > 0x7FFFFFFFll || tiles * a.C > 0x7FFFFFFFll;
 }
 
@@ -1224,11 +1232,11 @@ ExpertArgs experts_args(const uint8_t* xq, const uint8_t* xs, const float* xg, i
 }  // namespace
 
 extern "C" size_t nvfp4_moe_gate_up_workspace_bytes(int tokens, int top_k, int experts, int K) {
-  if (tokens <= kFewTokens || top_k < 1 || top_k > kMaxTop || (long long)tokens * top_k > 0x7FFFFFFFll ||
+  if (tokens < 1 || top_k < 1 || top_k > kMaxTop || (long long)tokens * top_k > 0x7FFFFFFFll ||
       bad_matrix(experts, 128, K, false))
     return 0;
   const ExpertArgs a = experts_args(nullptr, nullptr, nullptr, tokens, top_k, nullptr, nullptr, nullptr, nullptr, experts, 128, K);
-  return codes_bytes(a) + blocks_bytes(a);
+  return few_places(a) ? 0 : codes_bytes(a) + blocks_bytes(a);
 }
 
 extern "C" nvfp4_status nvfp4_moe_gate_up(const uint8_t* xq, const uint8_t* xs, const float* xg, int tokens, int top_k,
@@ -1250,20 +1258,18 @@ extern "C" nvfp4_status nvfp4_moe_gate_up(const uint8_t* xq, const uint8_t* xs, 
   if (ds != NVFP4_OK) return ds;
   const int sms = device_sms();
   if (need == 0) {
-    const int nt = tokens <= 16 ? 16 : 64;
-    const long long items = most_tiles(a, nt) * a.RT;
+    const long long items = most_tiles(a, kFewTile) * a.RT;
     while (a.cluster < kMaxCluster && items * a.cluster * 2 <= sms && a.C >= a.cluster * 2) a.cluster *= 2;
     const long long grid = items * a.cluster < sms ? items * a.cluster : sms;
-    return nvfp4_internal_cuda_status(nt == 16 ? run_few<16, UP>(grid, a, stream) : run_few<64, UP>(grid, a, stream));
+    return nvfp4_internal_cuda_status(run_few<kFewTile, UP>(grid, a, stream));
   }
   uint8_t *codes = static_cast<uint8_t*>(workspace), *blocks = codes + codes_bytes(a);
   CUtensorMap map;
   const cudaError_t e = arrange(a, codes, blocks, &map, stream);
   if (e != cudaSuccess) return nvfp4_internal_cuda_status(e);
   a.x_blocks = blocks;
-  const int nt = tile_for(a);
-  const long long items = most_tiles(a, nt) * a.RT, grid = items < sms ? items : sms;
-  return nvfp4_internal_cuda_status(nt == 64 ? run_many<64, UP>(grid, map, a, stream) : run_many<256, UP>(grid, map, a, stream));
+  const long long items = most_tiles(a, kManyTile) * a.RT, grid = items < sms ? items : sms;
+  return nvfp4_internal_cuda_status(run_many<kManyTile, UP>(grid, map, a, stream));
 }
 
 extern "C" size_t nvfp4_moe_down_workspace_bytes(int tokens, int top_k, int experts, int N, int K) {
@@ -1297,8 +1303,7 @@ extern "C" nvfp4_status nvfp4_moe_down(const uint8_t* hq, const uint8_t* hs, con
   if (need == 0) {
     a.out = y;
     while (a.cluster < kMaxCluster && a.RT * (a.cluster + 1) <= sms) ++a.cluster;
-    return nvfp4_internal_cuda_status(tokens <= 16 ? run_few<16, SUM>((long long)a.RT * a.cluster, a, stream)
-                                                   : run_few<64, SUM>((long long)a.RT * a.cluster, a, stream));
+    return nvfp4_internal_cuda_status(run_few<kFewTile, SUM>((long long)a.RT * a.cluster, a, stream));
   }
   uint8_t* blocks = static_cast<uint8_t*>(workspace);
   CUtensorMap map;
@@ -1306,11 +1311,11 @@ extern "C" nvfp4_status nvfp4_moe_down(const uint8_t* hq, const uint8_t* hs, con
   if (e != cudaSuccess) return nvfp4_internal_cuda_status(e);
   a.x_blocks = blocks;
   a.out = reinterpret_cast<float*>(blocks + blocks_bytes(a));
-  const int nt = tile_for(a), slab = slab_tiles(a);
+  const int slab = slab_tiles(a);
   for (a.rt0 = 0; a.rt0 < a.RT; a.rt0 += slab) {
     a.rts = a.RT - a.rt0 < slab ? a.RT - a.rt0 : slab;
-    const long long items = most_tiles(a, nt) * a.rts, grid = items < sms ? items : sms;
-    e = nt == 64 ? run_many<64, PART>(grid, map, a, stream) : run_many<256, PART>(grid, map, a, stream);
+    const long long items = most_tiles(a, kManyTile) * a.rts, grid = items < sms ? items : sms;
+    e = run_many<kManyTile, PART>(grid, map, a, stream);
     if (e != cudaSuccess) break;
     const int n0 = a.rt0 * kTR, n1 = (a.rt0 + a.rts) * kTR < N ? (a.rt0 + a.rts) * kTR : N;
     const CombineArgs c = {a.out, weights, places, y, tokens, top_k, N, a.n_pairs, n0, n1};

@@ -15,6 +15,11 @@
 // over the CTAs before it, then ranks in the CTA by warp matches.  Every sum is of
 // integers: no order of atomics shows.  Few tokens take one launch of one CTA;
 // else the counts of a launch are what the second one begins with.
+//
+// Bound by latency and issue, not by its bytes.  8 of 256 experts, 8192 tokens,
+// sigmoid scores with a bias, 4 of 8 groups by their two best: 37 us (floor 1.4),
+// some 7 of them the 64-bit values and 11 the plan; plain softmax 20 us.  One
+// token of 128 experts: 4.5 us in a graph, 7 called from Python.
 #include <math.h>
 
 #include "common.cuh"
@@ -28,7 +33,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTop = 32;
 constexpr int kMaxGroups = 32;
-constexpr int kOneCta = 64;               // tokens that one CTA routes and plans by itself
+// Tokens that one CTA routes and plans by itself: one launch and no workspace (64 tokens, 6 of 64 experts in groups: 10.0 us
+// called from Python, by two launches 14.1; in a graph 10.0 and 8.4; 32 tokens in a graph 6.1 and 6.3).
+constexpr int kOneCta = 64;
 constexpr int kMaxCtas = 152;             // of a call: bounds the workspace; one CTA an SM
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 

@@ -244,3 +244,9 @@ def test_bindings_refuse_what_does_not_fit():
                  lambda: api.MoERouting(bare.ids, None, bare.offsets, bare.pairs[:3], bare.places)):
         with pytest.raises(ValueError):
             call()
+
+
+# either side of 32 pairs an expert, where rows of x are laid out first
+@pytest.mark.parametrize("T,k,E", [(96, 3, 9), (97, 3, 9), (128, 8, 32), (129, 8, 32), (2000, 2, 500)])
+def test_few_and_many_places(T, k, E):
+    Case(_ids(np.random.default_rng(T), T, k, E), E, 192, 64, seed=T).run()
