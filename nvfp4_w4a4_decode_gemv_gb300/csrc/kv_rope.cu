@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 4) kv_rope_kernel(const RopeArgs a) 
   }
 }
 
-// Up to so many elements of K every block gets a thread of its own (40 and 8 heads of 128, with the read back: 1024 tokens 8.3
-// us, by windows 12.1; 2048 tokens 14.3 and 13.8).
+// Up to so many elements of K every block gets a thread of its own (40 and 8 heads of 128: 1024 tokens 8.3 us, by windows
+// 12.1; 2048 tokens 14.3 and 13.8).
 constexpr long long kFew = 1 << 20;
 
 template <int D, class T>

@@ -540,7 +540,7 @@ NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, W
 
 extern __shared__ __align__(1024) uint8_t smem_raw[];
 
-// ---- few tokens: UP, SUM ------------------------------------------------------------
+// ---- few places: UP, SUM ------------------------------------------------------------
 constexpr int kFewWarps = 10;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kLoaders = 4;                  // warps 2-5
@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const ExpertArg
   }
 }
 
-// ---- many tokens: UP, PART -----------------------------------------------------------
+// ---- many places: UP, PART -----------------------------------------------------------
 // 0 weights, 1 products, 2 rows of x, 4-19 the accumulator: with 16 of them a warp holds all its columns of a buffer in
 // registers, so that the buffer is free before they are stored (2048 tokens of 8 of 128 experts, K 4096 and 1536 rows up,
 // K 768 and 4096 rows down: 135 and 155 us; 8 warps, 16 columns at a time: 137 and 157).
@@ -881,7 +881,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
 }
 
 // Rows of x in the order of the plan, and their scales in blocks of 128 places and 256 of K: a CTA a tile of 128 places of
-// an expert and kArrangeChunks chunks.  codes NULL: the rows stand so already (down), only the scales are laid out.
+// an expert and kArrangeChunks chunks.  codes NULL: the rows stand so already (down), only the scales are laid out.  Bound by
+// the latency of the table, the pairs and the rows, one behind the other: 2048 tokens of 8 of 128 experts, K 4096, 38 MB
+// written: 20 us (scales alone, K 768: 7).
 struct ArrangeArgs {
   ExpertArgs x;
   uint8_t *codes, *blocks;
@@ -947,7 +949,8 @@ __global__ void __launch_bounds__(kArrangeThreads) moe_arrange_kernel(const Arra
   }
 }
 
-// y[t, n] = sum_j weights[t, j] part[places[t, j], n], in the order of j: a thread has V columns of a token.
+// y[t, n] = sum_j weights[t, j] part[places[t, j], n], in the order of j: a thread has V columns of a token.  Bound by HBM:
+// 2048 tokens of 8, N 4096: 302 MB in 54 us (5.6 TB/s).
 struct CombineArgs {
   const float *part, *weights;               // part: [column / 128][n_pairs][128], columns [n0, n1) of y
   const int32_t* places;
@@ -956,7 +959,8 @@ struct CombineArgs {
 };
 
 constexpr int kAtOnce = 8;                   // products of a token that are read together
-constexpr int kCombineCtas = 16;              // CTAs an SM: each goes through several tokens
+constexpr int kCombineCtas = 16;             // CTAs an SM, each goes through several tokens (2048 tokens of 8, N 4096: 162 us
+                                             // with the products; 8: 163, 4: 178, 2: 233)
 
 template <int V>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
