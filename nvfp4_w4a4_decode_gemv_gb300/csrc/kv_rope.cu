@@ -7,9 +7,9 @@
 // A thread takes a 16-element block of K or V, which the quantizer wants whole, and reads the block that a block of K is
 // turned with beside it (from L1, where that block's own thread has it too).  Of q it takes 8 pairs of elements.  Bound by
 // HBM: the rows in, q and the cache out.  8192 tokens of 40 heads of q and 8 of K and V, BF16, D 128: 211 MB in 41 us
-// (5.1 TB/s); 8 tokens of 32 and 8 heads, FP32: 6.7 us, the loads' latency one after another.  That prompt, with both
-// blocks of a pair turned by one thread 60 us (its registers left too few warps to cover the loads), with q in a launch of
-// its own 59 us, with all windows before q 45 us.
+// (5.1 TB/s), 54 with their read back; 8 tokens of 32 and 8 heads, FP32: 6.7 us cold, the loads' latency one after another.
+// That prompt with the read back, with both blocks of a pair turned by one thread 60 us (its registers left too few warps to
+// cover the loads), with q in a launch of its own 70, with all windows before q 58.
 #include <cuda_fp16.h>
 
 #include "kv_rows.cuh"

@@ -18,16 +18,17 @@
 //         its weights.
 // No CTA waits for another but at cluster barriers, and no state is left behind.
 //
-// Measured (128 experts where not said; of the copy rate, 6.76 TB/s, what the bytes that a call cannot do without take):
-//   up, few places an expert   1 token of 8, K 4096, 2048 rows: 10.5 us (8.8 in a graph; 54 %), a launch, the table of the
-//                              experts (1.7 us) and the ramp of the copies; 8 tokens, K 5120, 1536 rows: 36 us (86 %); 33 tokens
-//                              of 2 of 8 experts, K 4096, 16384 rows: 48.6 us (92 %)
-//   up, many                   2048 tokens of 8, K 4096, 1536 rows: 134 us (1.54 PFLOP/s; 53 %): 15 us of laying out, then 75 us
-//                              of scale copies and MMAs (without its loads and stores the kernel takes 88) under 73 us of copies
-//   down, few tokens           1 token of 8, K 1024, 4096 rows: 8.2 us (34 %); 64 tokens, K 768, 5120 rows: 54 us (71 %), on the
-//                              120 SMs that 40 row tiles of 3 CTAs fill
-//   down, many                 2048 tokens, K 768, 4096 rows: 154 us (26 %): FP32 products written (268 MB, 87 us with the
-//                              products themselves) and read again (54 us at 5.4 TB/s)
+// Measured (128 experts where not said; in brackets the share of the time that the bytes a call cannot do without would take
+// at the copy rate, 6.76 TB/s):
+//   up, few places an expert   1 token of 8, K 4096, 2048 rows: 10.5 us, 8.9 in a graph (53 %): a launch, the experts' table
+//                              (1.7 us) and the ramp of the copies; 8 tokens of 8, K 5120, 1536 rows: 36 us (86 %);
+//                              33 tokens of 2 of 8 experts, K 4096, 16384 rows: 48.6 us (92 %)
+//   up, many                   2048 tokens of 8, K 4096, 1536 rows: 134 us (1.54 PFLOP/s; 53 %); without its loads and
+//                              stores 103: the issue of scale copies and MMAs bounds it
+//   down, few tokens           1 token of 8, K 1024, 4096 rows: 8.2 us (34 %); 64 tokens of 8, K 768, 5120 rows: 54 us
+//                              (71 %), on the 120 SMs that 40 row tiles of 3 CTAs fill
+//   down, many                 2048 tokens of 8, K 768, 4096 rows: 154 us (26 %): 268 MB of FP32 products written and read
+//                              again; without the writes 124
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <string.h>
@@ -145,6 +146,9 @@ NVFP4_DEVINL void build_table(const ExpertArgs& a, Table& tb) {
       tiles[1] += light ? t : 0;
       blocks += (n + 127) / 128;
     });
+    // Ranges that fall or leave the pairs have more tiles between them than the workspace and the grid are made for: no pairs.
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad) used[0] = used[1] = tiles[0] = tiles[1] = blocks = 0;
     int at[5] = {used[0], used[1], tiles[0], tiles[1], blocks};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
@@ -158,14 +162,14 @@ NVFP4_DEVINL void build_table(const ExpertArgs& a, Table& tb) {
     if (lane == 31) {
       tb.sums[0] = heavy_tiles + at[3];
       tb.sums[1] = heavy + at[1];
-      tb.sums[2] = min(max(tb.offsets[a.experts], 0), a.n_pairs);
+      tb.sums[2] = bad ? 0 : tb.offsets[a.experts];
     }
     at[0] -= used[0];
     at[1] += heavy - used[1];
     at[2] -= tiles[0];
     at[3] += heavy_tiles - tiles[1];
     at[4] -= blocks;
-    look([&](int e, int lo, int n, bool light) {
+    if (!bad) look([&](int e, int lo, int n, bool light) {
       const int i = light ? at[1] : at[0], t = (n + NT - 1) / NT;
       tb.first[i] = lo;
       tb.count[i] = n;
@@ -178,7 +182,7 @@ NVFP4_DEVINL void build_table(const ExpertArgs& a, Table& tb) {
       at[3] += light ? t : 0;
       at[4] += (n + 127) / 128;
     });
-    if (bad && blockIdx.x == 0) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
+    if (bad && lane == 0 && blockIdx.x == 0) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (the ring's copies may come where the offsets stood)
   tc_fence_before();

@@ -250,3 +250,22 @@ def test_bindings_refuse_what_does_not_fit():
 @pytest.mark.parametrize("T,k,E", [(96, 3, 9), (97, 3, 9), (128, 8, 32), (129, 8, 32), (2000, 2, 500)])
 def test_few_and_many_places(T, k, E):
     Case(_ids(np.random.default_rng(T), T, k, E), E, 192, 64, seed=T).run()
+
+
+@pytest.mark.parametrize("T,E", [(4, 4), (60, 300), (100, 4), (130, 512), (1000, 16)])
+def test_offsets_that_fall_are_a_plan_without_pairs(T, E):
+    """Ranges that overlap would have more tiles between them than any plan of the pairs."""
+    c = Case(_ids(np.random.default_rng(T), T, 2, E), E, 128, 64)
+    r = api.nvfp4_moe_plan(torch.from_numpy(c.ids).cuda(), E, torch.from_numpy(c.weights).cuda())
+    r.offsets[::2], r.offsets[1::2] = 0, 2 * T
+    h, y = Guarded((2 * T, 64), torch.bfloat16), Guarded((T, 128), torch.float32)
+    h.t.fill_(7.0)
+    api.nvfp4_moe_gate_up(_tensor(c.x), c.up, r, out=h.t)
+    assert api.device_status() == api.DEVERR_MOE_RANGE
+    assert not to_np(h.t.float()).any()
+    api.nvfp4_moe_down(_tensor(c.h), c.down, r, y=y.t)
+    assert api.device_status() == api.DEVERR_MOE_RANGE
+    assert T > 64 or not to_np(y.t).any()
+    h.check("h")
+    y.check("y")
+    c.run()
