@@ -1137,9 +1137,9 @@ long long most_tiles(const ExpertArgs& a, int nt) {
   return used + (a.n_pairs - used) / nt;
 }
 
-// Whether h goes without rows laid out first: few tokens, or few places an expert (K 4096, 1536 rows, 512 tokens of 8 of 128
-// experts, 32 places each: 85 us, laid out 101; K 4096, 16384 rows, 2 of 8 experts, 32 places each: 55 and 67, 64 places: 84
-// and 76).
+// Whether h goes without rows laid out first: few tokens, or few places an expert on average, which is what the host knows
+// (K 4096, 1536 rows, 512 tokens of 8 of 128 experts, 32 places each: 85 us, laid out 101; K 4096, 16384 rows, 2 of 8
+// experts, 32 places each: 55 and 67, 64 places: 84 and 76).
 bool few_places(const ExpertArgs& a) { return a.tokens <= kFewTokens || a.n_pairs <= 32 * used_experts(a); }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }

@@ -183,7 +183,7 @@ def test_broken_plans_are_reported():
         c.run()
 
 
-@pytest.mark.parametrize("T", [5, 90])
+@pytest.mark.parametrize("T", [5, 90, 200])
 def test_same_bits_again_replayed_and_on_two_streams(T):
     c = Case(_ids(np.random.default_rng(7), T, 4, 12), 12, 512, 256)
     x, h = _tensor(c.x), _tensor(c.h)
