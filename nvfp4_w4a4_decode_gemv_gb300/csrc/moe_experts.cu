@@ -545,7 +545,7 @@ NVFP4_DEVINL void multiply(const Smem<NT, MODE, FEW>& sm, const ExpertArgs& a, W
 extern __shared__ __align__(1024) uint8_t smem_raw[];
 
 // ---- few places: UP, SUM ------------------------------------------------------------
-constexpr int kFewWarps = 10;
+constexpr int kFewWarps = 10;               // 0 weights, 1 products, 2-5 rows of x, 6-9 the accumulator
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kLoaders = 4;                  // warps 2-5
 
