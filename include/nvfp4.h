@@ -657,7 +657,8 @@ nvfp4_status nvfp4_moe_gate_up(const uint8_t* xq, const uint8_t* xs, const float
 /*
  * Down products of the chosen experts, summed over a token's experts:
  *   y[t, n] = sum_j weights[t, j] hg wg[e] sum_k h[place(t, j), k] w[e, n, k]          (FP32)
- * over the pairs of t that have a place (none: 0).  No product is rounded on the way.
+ * over the pairs of t that have a place (none: 0).  No product is rounded on the way.  Up to 64 tokens the pairs are gone by,
+ * beyond them the places: one outside [0, offsets[experts]) has no product, is skipped and records device error bit 6.
  *   hq, hs, hg   NVFP4 rows by place, [tokens * top_k, K/2] 16-byte, [.., K/16] 4-byte aligned, one float
  *   wpacked, wg  packed with gated == 0 ([experts, N, K]), [experts] FP32
  *   weights      device, [tokens, top_k] FP32;  places: the plan's

@@ -891,6 +891,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
 struct ArrangeArgs {
   ExpertArgs x;
   uint8_t *codes, *blocks;
+  int* last;                                 // down: the number of pairs that get products (0: a plan that is refused); or NULL
 };
 constexpr int kArrangeThreads = 256;
 constexpr int kArrangeChunks = 4;
@@ -903,6 +904,7 @@ __global__ void __launch_bounds__(kArrangeThreads) moe_arrange_kernel(const Arra
   const ExpertArgs& a = g.x;
   Table tb(s_table, s_offsets);
   build_table<128, false>(a, tb);
+  if (g.last && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *g.last = tb.total;
   if ((int)blockIdx.x >= tb.tiles) return;
   int used = 0;                              // the last entry whose tiles begin at blockIdx.x or before
   for (int hi = tb.used; hi - used > 1;) {
@@ -957,7 +959,7 @@ __global__ void __launch_bounds__(kArrangeThreads) moe_arrange_kernel(const Arra
 // 2048 tokens of 8, N 4096: 302 MB in 54 us (5.6 TB/s).
 struct CombineArgs {
   const float *part, *weights;               // part: [column / 128][n_pairs][128], columns [n0, n1) of y
-  const int32_t* places;
+  const int32_t *places, *last;              // last: places from *last on have no product (what stands there was never written)
   float* y;
   int tokens, top, N, n_pairs, n0, n1;
 };
@@ -985,6 +987,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
   int place[kAtOnce];
   float w[kAtOnce];
   look(blockIdx.y, 0, place, w);
+  const int last = __ldcg(a.last);
   for (int t = blockIdx.y; t < a.tokens; t += gridDim.y) {
     float y[V] = {};
     for (int j0 = 0; j0 < a.top; j0 += kAtOnce) {
@@ -992,7 +995,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
       bool there[kAtOnce];
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
-        there[j] = place[j] >= 0 && place[j] < a.n_pairs;
+        there[j] = place[j] >= 0 && place[j] < last;
         if (!there[j] && place[j] != -1) atomicOr(&g_nvfp4_device_error, NVFP4_DEVERR_MOE_RANGE);
         const float* src = a.part + (column + (there[j] ? place[j] : 0)) * kTR + n % kTR;
         if constexpr (V == 4) {
@@ -1155,11 +1158,11 @@ bool nvfp4_internal_encode_2d(CUtensorMap* map, const void* base, uint64_t inner
 namespace {
 
 // Rows of x by place (codes: where they go, NULL: they stand so) and their scales' blocks, and the map of the rows.
-cudaError_t arrange(const ExpertArgs& a, uint8_t* codes, uint8_t* blocks, CUtensorMap* map, cudaStream_t stream) {
+cudaError_t arrange(const ExpertArgs& a, uint8_t* codes, uint8_t* blocks, int* last, CUtensorMap* map, cudaStream_t stream) {
   memset(map, 0, sizeof(*map));
   if (!nvfp4_internal_encode_2d(map, codes ? codes : a.xc, (uint64_t)a.K / 2, (uint64_t)a.n_pairs, 128, kBoxRows, true))
     return cudaErrorInvalidValue;
-  ArrangeArgs g = {a, codes, blocks};
+  ArrangeArgs g = {a, codes, blocks, last};
   const dim3 grid((unsigned)most_tiles(a, 128), (unsigned)((a.C + kArrangeChunks - 1) / kArrangeChunks));
   return launch(moe_arrange_kernel, grid, kArrangeThreads, 0, 1, stream, g);
 }
@@ -1168,10 +1171,14 @@ cudaError_t arrange(const ExpertArgs& a, uint8_t* codes, uint8_t* blocks, CUtens
 // cost their launches and gained nothing (2048 tokens of 8 experts, N 4096, K 768: 32 MB 206 us, 64 184, 128 177, 512 170).
 constexpr long long kSlabBytes = 512ll << 20;
 
+constexpr size_t kLastBytes = 256;           // the number of pairs that get products, behind the products
+
 int slab_tiles(const ExpertArgs& a) {
   const long long per = (long long)a.n_pairs * kTR * 4, fit = kSlabBytes / per;
   return (int)(fit < 1 ? 1 : fit < a.RT ? fit : a.RT);
 }
+
+size_t products_bytes(const ExpertArgs& a) { return (size_t)a.n_pairs * slab_tiles(a) * kTR * sizeof(float); }
 
 // Whether a call's items and units are counted in 31 bits.
 bool too_many_items(const ExpertArgs& a) {
@@ -1273,7 +1280,7 @@ extern "C" nvfp4_status nvfp4_moe_gate_up(const uint8_t* xq, const uint8_t* xs, 
   }
   uint8_t *codes = static_cast<uint8_t*>(workspace), *blocks = codes + codes_bytes(a);
   CUtensorMap map;
-  const cudaError_t e = arrange(a, codes, blocks, &map, stream);
+  const cudaError_t e = arrange(a, codes, blocks, nullptr, &map, stream);
   if (e != cudaSuccess) return nvfp4_internal_cuda_status(e);
   a.x_blocks = blocks;
   const long long items = most_tiles(a, kManyTile) * a.RT, grid = items < sms ? items : sms;
@@ -1285,7 +1292,7 @@ extern "C" size_t nvfp4_moe_down_workspace_bytes(int tokens, int top_k, int expe
       bad_matrix(experts, N, K, false))
     return 0;
   const ExpertArgs a = experts_args(nullptr, nullptr, nullptr, tokens, top_k, nullptr, nullptr, nullptr, nullptr, experts, N, K);
-  return blocks_bytes(a) + (size_t)a.n_pairs * slab_tiles(a) * kTR * sizeof(float);
+  return blocks_bytes(a) + products_bytes(a) + kLastBytes;
 }
 
 extern "C" nvfp4_status nvfp4_moe_down(const uint8_t* hq, const uint8_t* hs, const float* hg, int tokens, int top_k,
@@ -1314,11 +1321,13 @@ extern "C" nvfp4_status nvfp4_moe_down(const uint8_t* hq, const uint8_t* hs, con
     return nvfp4_internal_cuda_status(run_few<kFewTile, SUM>((long long)a.RT * a.cluster, a, stream));
   }
   uint8_t* blocks = static_cast<uint8_t*>(workspace);
+  uint8_t* products = blocks + blocks_bytes(a);
+  int* last = reinterpret_cast<int*>(products + products_bytes(a));
   CUtensorMap map;
-  cudaError_t e = arrange(a, nullptr, blocks, &map, stream);
+  cudaError_t e = arrange(a, nullptr, blocks, last, &map, stream);
   if (e != cudaSuccess) return nvfp4_internal_cuda_status(e);
   a.x_blocks = blocks;
-  a.out = reinterpret_cast<float*>(blocks + blocks_bytes(a));
+  a.out = reinterpret_cast<float*>(products);
   const int slab = slab_tiles(a);
   for (a.rt0 = 0; a.rt0 < a.RT; a.rt0 += slab) {
     a.rts = a.RT - a.rt0 < slab ? a.RT - a.rt0 : slab;
@@ -1326,7 +1335,7 @@ extern "C" nvfp4_status nvfp4_moe_down(const uint8_t* hq, const uint8_t* hs, con
     e = run_many<kManyTile, PART>(grid, map, a, stream);
     if (e != cudaSuccess) break;
     const int n0 = a.rt0 * kTR, n1 = (a.rt0 + a.rts) * kTR < N ? (a.rt0 + a.rts) * kTR : N;
-    const CombineArgs c = {a.out, weights, places, y, tokens, top_k, N, a.n_pairs, n0, n1};
+    const CombineArgs c = {a.out, weights, places, last, y, tokens, top_k, N, a.n_pairs, n0, n1};
     const int per = N % 4 == 0 ? 1024 : 256;
     const int across = (n1 - n0 + per - 1) / per, down = (kCombineCtas * sms + across - 1) / across;
     const dim3 grid2((unsigned)across, (unsigned)(tokens < down ? tokens : down));
