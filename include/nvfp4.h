@@ -644,8 +644,8 @@ nvfp4_status nvfp4_moe_pack_weights(const uint8_t* wq, const uint8_t* ws, int ex
  *   workspace    device scratch of nvfp4_moe_gate_up_workspace_bytes bytes (0 for few tokens), 256-byte aligned; no state
  * Only the weights of experts that have pairs are read.  Sums of a product are FP32 in an order that the shape and the
  * plan fix: the same inputs give the same bits.  Pairs and places outside their tables are taken into them or skipped and
- * record device error bit 6 (the rows concerned mean nothing), as do offsets that fall or lie outside [0, tokens * top_k]:
- * a plan of such is one without pairs.
+ * record device error bit 6 (the rows concerned mean nothing), as do offsets that do not begin at 0, fall or lie outside
+ * [0, tokens * top_k]: a plan of such is one without pairs.
  */
 size_t nvfp4_moe_gate_up_workspace_bytes(int tokens, int top_k, int experts, int K);
 

@@ -134,7 +134,7 @@ NVFP4_DEVINL void build_table(const ExpertArgs& a, Table& tb) {
         if (e >= a.experts) break;
         const int f = tb.offsets[e], l = tb.offsets[e + 1];
         const int lo = min(max(f, 0), a.n_pairs), hi = min(max(l, 0), a.n_pairs);
-        bad = bad || f != lo || l != hi || hi < lo;
+        bad = bad || f != lo || l != hi || hi < lo || (e == 0 && f != 0);
         if (hi > lo) take(e, lo, hi - lo, HEAVY && hi - lo <= 128);
       }
     };
@@ -147,6 +147,7 @@ NVFP4_DEVINL void build_table(const ExpertArgs& a, Table& tb) {
       blocks += (n + 127) / 128;
     });
     // Ranges that fall or leave the pairs have more tiles between them than the workspace and the grid are made for: no pairs.
+    // A first place that is no one's would be left as it is: no pairs either.
     bad = __any_sync(0xffffffffu, bad);
     if (bad) used[0] = used[1] = tiles[0] = tiles[1] = blocks = 0;
     int at[5] = {used[0], used[1], tiles[0], tiles[1], blocks};
