@@ -635,7 +635,7 @@ nvfp4_status nvfp4_moe_pack_weights(const uint8_t* wq, const uint8_t* ws, int ex
  * Gate and up products of the chosen experts, and SiLU(gate) * up, in one pass over their weights: with pair p at place q
  * (p = pairs[q]), token t = p / top_k and expert e (offsets[e] <= q < offsets[e+1]),
  *   g = xg wg[e] sum_k x[t, k] w[e, i, k],  u = the same with w[e, inter + i, k]       (FP32)
- *   h[q, i] = BF16(g / (1 + exp(-g)) * u)
+ *   h[q, i] = BF16(g / (1 + exp(-g)) * u)          (0 for g below -88.72, where FP32's exp(-g) overflows)
  * Rows of h behind offsets[experts] are zero, so that nvfp4_quantize_act may take all of h.
  *   xq, xs, xg   activations in NVFP4 layout, [tokens, K/2] 16-byte, [tokens, K/16] 4-byte aligned, one float
  *   wpacked, wg  packed with gated != 0 (N = 2 inter), 16-byte aligned; [experts] FP32 global scales

@@ -215,5 +215,12 @@ NVFP4_DEVINL uint32_t f32x2_to_e2m1x2(float hi, float lo) {
   return r;
 }
 
+// 2^x, off by 2^-22 of it.
+NVFP4_DEVINL float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 NVFP4_DEVINL float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 NVFP4_DEVINL float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }

@@ -33,12 +33,6 @@ struct AttnArgs {
 NVFP4_DEVINL void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 // ---- instructions ------------------------------------------------------------
-NVFP4_DEVINL float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Two E4M3 scale bytes -> an FP16 pair.
 NVFP4_DEVINL uint32_t e4m3x2_to_f16(uint32_t s) {
   uint32_t h;

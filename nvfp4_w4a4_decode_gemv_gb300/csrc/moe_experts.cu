@@ -356,7 +356,12 @@ NVFP4_DEVINL float4 ld_dsmem_f32x4(uint32_t addr) {
   return v;
 }
 
-NVFP4_DEVINL float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+// g / (1 + e^-g) u of g4 = g / 4.  An approximate power (off by 2^-22, its argument by 1.25 2^-24 |g|) and quotient (2^-22):
+// 2^-16 of the result, far below the 2^-8 of its BF16.  Both sides of the quotient are a quarter: __fdividef gives 0 for a
+// divisor above 2^126, which 1 + e^-g reaches at g = -87.3.  Below g = -88.72 e^-g overflows and the result is 0.
+NVFP4_DEVINL float silu_mul(float g4, float u) {
+  return __fdividef(g4, 0.25f + ex2(fmaf(g4, -5.77078016f, -2.0f))) * u;    // e^-g / 4 = 2^(-4 log2(e) g4 - 2)
+}
 
 // 16 columns of the accumulator, even lanes gates and odd lanes ups, to h: 16 bytes a lane, 8 values of one place.
 // Halves of what a lane holds go to the lane whose bit differs, bit by bit: first gates meet ups, then lanes 2, 4 and 8
@@ -364,10 +369,11 @@ NVFP4_DEVINL float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __ex
 NVFP4_DEVINL void store_h16(const ExpertArgs& a, const Segment& sg, int quad, int m0, const float (&v)[16], float scale) {
   const int lane = threadIdx.x & 31;
   const bool odd = lane & 1, b1 = lane & 2, b2 = lane & 4, b3 = lane & 8;
+  const float f = odd ? scale : 0.25f * scale;
   float h[8];                                // place 2 j + odd
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float a0 = v[2 * j] * scale, a1 = v[2 * j + 1] * scale;
+    const float a0 = v[2 * j] * f, a1 = v[2 * j + 1] * f;
     const float other = __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
     h[j] = odd ? silu_mul(other, a1) : silu_mul(a0, other);
   }
@@ -764,7 +770,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const ExpertArg
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r)
           if (r < a.cluster) v += x[r];
-        v *= scale;
+        v *= lane & 1 ? scale : 0.25f * scale;
         const float other = __shfl_xor_sync(0xffffffffu, v, 1);
         if (!(lane & 1) && i < a.N)
           a.h[(size_t)(sg.p0 + m) * a.N + i] = __bfloat16_as_ushort(__float2bfloat16_rn(silu_mul(v, other)));
