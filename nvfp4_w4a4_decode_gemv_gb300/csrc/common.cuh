@@ -155,6 +155,9 @@ NVFP4_DEVINL void fence_acq_rel_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "m
 NVFP4_DEVINL void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 NVFP4_DEVINL void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// What this thread's bulk copies read may come from the preceding kernel's ordinary stores: order them before the copies.
+NVFP4_DEVINL void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
 // Ask L2 for the line holding p.  A hint, but not an invisible one: when the
 // line is rewritten afterwards (by a kernel still running while this one
 // waits on it), a later non-coherent load (ld.global.nc) on this SM was

@@ -29,9 +29,6 @@ struct AttnArgs {
   float scale;
 };
 
-// The cache's rows may come from the preceding kernel's ordinary stores: order them before this thread's bulk copies.
-NVFP4_DEVINL void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
-
 // ---- instructions ------------------------------------------------------------
 // Two E4M3 scale bytes -> an FP16 pair.
 NVFP4_DEVINL uint32_t e4m3x2_to_f16(uint32_t s) {

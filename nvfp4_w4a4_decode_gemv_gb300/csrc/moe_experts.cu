@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) moe_few_kernel(const ExpertArg
   if (warp == 1) sm.alloc_tmem();
   griddep_launch_dependents();
   griddep_wait();                            // the plan comes from a preceding kernel
+  fence_proxy_async_global();                // (and the weights may)
   Table tb = sm.table();
   build_table<NT, false>(a, tb);
   const uint32_t tmem = *sm.tmem_slot;
@@ -809,6 +810,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) moe_many_kernel(const __grid_
   if (warp == 1) sm.alloc_tmem();
   griddep_launch_dependents();
   griddep_wait();
+  fence_proxy_async_global();                // rows and scales were laid out by a preceding kernel
   Table tb = sm.table();
   build_table<NT, (NT > 128)>(a, tb);
   const uint32_t tmem = *sm.tmem_slot;
