@@ -25,6 +25,8 @@ from ._lib import ResetParams
 
 
 class DecodeStep:
+    experts = 0                    # of a layer's MLP (0: dense)
+
     def __init__(self, M: int, layers: int, shapes=synth.QWEN3_32B, vocab: int = synth.LM_HEAD_VOCAB,
                  seed: int = 0, eps: float = 1e-6, reset: ResetParams | None = None, keep_rowmajor: bool = False,
                  device="cuda", share_weights: "DecodeStep | None" = None):
@@ -36,7 +38,9 @@ class DecodeStep:
         self.weights = []          # per layer: {name: NVFP4PackedWeight}
         self.rowmajor = []         # per layer (keep_rowmajor): {name: NVFP4Tensor}
         if share_weights is not None:  # another step's weights and lm_head (steps of other M on one model)
-            assert share_weights.layers == layers and share_weights.hidden == hidden
+            for what in ("layers", "hidden", "vocab", "n_qkv", "k_o", "n_gu", "k_d", "experts"):
+                if getattr(share_weights, what) != getattr(self, what):
+                    raise ValueError(f"share_weights: {what} is {getattr(share_weights, what)} there, {getattr(self, what)} here")
             self.weights, self.rowmajor = share_weights.weights, share_weights.rowmajor
         for layer in range(0 if share_weights is not None else layers):
             packed, rm = {}, {}
