@@ -101,7 +101,7 @@ class DecodeStep:
                           "xq_o": nv(self.xq_o), "y_o": self.y_o.clone()})
         self._mlp(layer, stream, trace)
         if trace is not None:
-            trace[-1].update({"r2": self.r.clone(), "xq_gu": nv(self.xq_gu), "y_gu": self.y_gu.clone(),
+            trace[-1].update({"r2": self.r.clone(), "xq_gu": nv(self.xq_gu),
                               "xq_d": (self.xq_d.codes.clone(), self.xq_d.scales.clone(),
                                        self.xq_d.global_scale.clone()),
                               "h_out": self.h.clone()})
@@ -111,6 +111,8 @@ class DecodeStep:
         w = self.weights[layer]
         api.nvfp4_rms_norm_quantize(self.y_o, eps=self.eps, out=self.xq_gu, r_out=self.r_out(trace), stream=stream)
         api.nvfp4_gemv_smallm_packed(self.xq_gu, w["gate_up"], y=self.y_gu, workspace=self.ws, stream=stream)
+        if trace is not None:
+            trace[-1]["y_gu"] = self.y_gu.clone()
         api.nvfp4_silu_mul_quantize(self.y_gu, out=self.xq_d, stream=stream)
         api.nvfp4_gemv_smallm_packed(self.xq_d, w["down"], y=self.h, workspace=self.ws, stream=stream)
 

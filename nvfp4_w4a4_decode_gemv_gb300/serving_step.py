@@ -169,6 +169,8 @@ class ServingStep(DecodeStep):
         api.nvfp4_moe_route(self.route_logits, bias=self.route_bias[layer], rows=self.live, out=self.routing, stream=stream,
                             **self.router)
         api.nvfp4_moe_gate_up(self.xq_gu, w["gate_up"], self.routing, out=self.h_mid, stream=stream)
+        if trace is not None:
+            trace[-1]["h_mid"] = self.h_mid.clone()
         api.nvfp4_quantize_act(self.h_mid, out=self.xq_d, stream=stream)
         api.nvfp4_moe_down(self.xq_d, w["down"], self.routing, y=self.h, stream=stream)
 
