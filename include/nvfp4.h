@@ -567,6 +567,9 @@ nvfp4_status nvfp4_kv_attention(const void* q, int dtype, int tokens, int64_t q_
  *   places   [tokens * top_k]     the place of each pair, -1: it has none.
  * The ReSET pages describe dense layers only; this part has no counterpart
  * there.  experts 1 .. 512, top_k 1 .. 32, tokens * top_k < 2^31.
+ * The activations' global scale is one for all experts, as nvfp4_quantize_act
+ * gives it: experts calibrated with an input scale each are not covered.
+ * Workspaces keep no state; calls that overlap on the GPU need different ones.
  */
 enum { NVFP4_MOE_SOFTMAX = 0, NVFP4_MOE_SIGMOID = 1 };
 
@@ -641,7 +644,8 @@ nvfp4_status nvfp4_moe_pack_weights(const uint8_t* wq, const uint8_t* ws, int ex
  *   wpacked, wg  packed with gated != 0 (N = 2 inter), 16-byte aligned; [experts] FP32 global scales
  *   inter        a multiple of 64;  K a multiple of 64
  *   h            device, [tokens * top_k, inter] BF16, 16-byte aligned (written)
- *   workspace    device scratch of nvfp4_moe_gate_up_workspace_bytes bytes (0 for few tokens), 256-byte aligned; no state
+ *   workspace    device scratch of nvfp4_moe_gate_up_workspace_bytes bytes (0 for few tokens, or few pairs an expert),
+ *                256-byte aligned; no state
  * Only the weights of experts that have pairs are read.  Sums of a product are FP32 in an order that the shape and the
  * plan fix: the same inputs give the same bits.  Pairs and places outside their tables are taken into them or skipped and
  * record device error bit 6 (the rows concerned mean nothing), as do offsets that do not begin at 0, fall or lie outside

@@ -24,9 +24,11 @@
 //                              (1.7 us) and the ramp of the copies; 8 tokens of 8, K 5120, 1536 rows: 36 us (86 %);
 //                              33 tokens of 2 of 8 experts, K 4096, 16384 rows: 48.6 us (92 %)
 //   up, many                   2048 tokens of 8, K 4096, 1536 rows: 134 us (1.54 PFLOP/s; 53 %); without its loads and
-//                              stores 103: the issue of scale copies and MMAs bounds it
+//                              stores 103, 15 to 20 of them for laying the rows out; with one MMA a stage in place of four 74.
+//                              Stages of 400 to 700 cycles add up to 35 to 65
 //   down, few tokens           1 token of 8, K 1024, 4096 rows: 8.2 us (34 %); 64 tokens of 8, K 768, 5120 rows: 54 us
-//                              (71 %), on the 120 SMs that 40 row tiles of 3 CTAs fill
+//                              (71 %), on the 120 SMs that 40 row tiles of 3 CTAs fill.  N 256, 1024, 2880, 7168, 9856: 23,
+//                              25, 33, 78, 141 us on 16, 64, 138, 112, 77 SMs
 //   down, many                 2048 tokens of 8, K 768, 4096 rows: 154 us (26 %): 268 MB of FP32 products written and read
 //                              again; without the writes 124
 #include <cuda.h>
@@ -1138,7 +1140,10 @@ cudaError_t run_many(long long grid, const CUtensorMap& map, const ExpertArgs& a
 // many 256 (1024 tokens of 8 of 128 experts, up: 112 us, with 64 places 136; with 16 places an expert as fast).
 constexpr int kFewTile = 64, kManyTile = 256;
 
-// Tokens up to which y is summed in shared memory.
+// Tokens up to which y is summed in shared memory, which holds no more.  Both sides, us: 128 experts, 8 a token, N 5120, K 768:
+// 16 tokens 40, by products and sums 49; 32 tokens 47, 57; 64 tokens 55, 64.  2 of 8 experts, N 4096, K 2048: 64 tokens 14, 20.
+// Beyond 76 row tiles a tile has one CTA and the sums lose (N 9856: 141, 109).  For h, where all places are those of few
+// experts: 64 tokens of 2 of 2, K 4096, 8192 rows 14, laid out 18.
 constexpr int kFewTokens = 64;
 
 long long used_experts(const ExpertArgs& a) { return a.n_pairs < a.experts ? a.n_pairs : a.experts; }
