@@ -428,7 +428,8 @@ NVFP4_DEVINL int route_row(const RouteArgs& a, Scratch& scratch, int token, int 
       // s (1 - s), which makes at most 0.6 ulp of it; sum, quotient and bias add 3: 2^-21.  Softmax, each score at most
       // 1 / z = inv: (2 + 1.173 |t|) e^t is at most 2 ulp of the largest term, x - m loses half of one; z is off by 21
       // half ulps of up to 512 terms' sum and by 8.5 ulp of its terms' mean at worst (511 of them near t = -4.9 beside one at
-      // 0, x - m rounded), the quotient by 2: 2^-18.4 of inv in all.  A sum of two values doubles it.  (e^-x that overflows gives 0 and is off by 2^-126.)
+      // 0, x - m rounded), the quotient by 2: 2^-18.4 of inv in all.  A sum of two values doubles it.  (e^-x that overflows
+      // gives 0 and is off by 2^-126.)
       const float score = a.sigmoid ? 0x1p-20f : 0x1p-18f * fminf(1.0f, inv) + 0x1p-24f;
       v_err = 2.0f * (score + 0x1p-23f * most);
       if (a.bias) c_err = score + 0x1p-23f * most;
